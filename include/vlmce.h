@@ -56,8 +56,21 @@ typedef enum {
     VLMCE_ERR_TOO_LARGE = 7           /* a size beyond what the kernels support      */
 } vlmce_status;
 
-/* VLMCE_F16: fp16, accepted by flce_fwd_bwd_ex and vlmce_gemm only. */
-typedef enum { VLMCE_F32 = 0, VLMCE_BF16 = 1, VLMCE_F16 = 2 } vlmce_dtype;
+/* VLMCE_F16: fp16, accepted by flce_fwd_bwd_ex, vlmce_gemm, rmsnorm_*,
+ * linear_* and glu_*.  VLMCE_E4M3: 8-bit floating point (4 exponent, 3
+ * mantissa bits, no infinities), the output of rmsnorm_fwd and the operands of
+ * linear_fwd and glu_fwd. */
+typedef enum { VLMCE_F32 = 0, VLMCE_BF16 = 1, VLMCE_F16 = 2, VLMCE_E4M3 = 3 } vlmce_dtype;
+/* Activations of linear_* and (but for NONE) glu_*: a s(a) with s(a) = 1 / (1 +
+ * e^-a); a P(a) with the normal CDF P; its tanh form a (1 + tanh(sqrt(2/pi) (a
+ * + 0.044715 a^3))) / 2; max(a, 0). */
+typedef enum {
+    VLMCE_ACT_NONE = 0,
+    VLMCE_ACT_SILU = 1,
+    VLMCE_ACT_GELU = 2,
+    VLMCE_ACT_GELU_TANH = 3,
+    VLMCE_ACT_RELU = 4
+} vlmce_act;
 /* VLMCE_NONE: per-token losses only; the gradient is not averaged (each row
  * is scaled by grad_scale, and by grad_per_token[r] where given) and
  * out_reduced[0] is the sum of the losses.  Not accepted by flce_fwd_bwd. */
@@ -285,6 +298,157 @@ vlmce_status swiglu_fwd(const void *x, int32_t dtype, int64_t T, int64_t n, int6
 vlmce_status swiglu_bwd(const void *x, int64_t x_stride, const void *dy, int64_t dy_stride,
                         void *dx, int64_t dx_stride, int32_t dtype, int64_t T, int64_t n,
                         vlmce_stream_t stream);
+
+/*
+ * rmsnorm_fwd -- root-mean-square norm of T rows of H elements, with the
+ * residual's addition:  s = x + residual,  rstd = (mean_j s_j^2 + eps)^-1/2,
+ * y = s rstd (weight + weight_offset).  Arithmetic in fp32 (y is formed from
+ * the unrounded s), each output rounded once to nearest even.
+ *
+ * x, residual     device, rows of `dtype` (VLMCE_F32, VLMCE_BF16 or VLMCE_F16)
+ *                 at the given strides (elements, >= H); residual may be NULL
+ *                 (s = x).
+ * weight          [H] of weight_dtype: `dtype` or VLMCE_F32.
+ * eps             >= 0, finite; weight_offset finite (1 for norms that store
+ *                 weight - 1).
+ * y               [T, y_stride] of y_dtype: `dtype`, or VLMCE_E4M3 with
+ *                 scale[t] = max_j |y_j| / 448 and y holding e4m3(y_j /
+ *                 scale[t]) (a row whose products s_j (weight_j + offset) are
+ *                 all below 1e-30 takes 1e-30 for their maximum).
+ * residual_out    rows of `dtype` receiving s, or NULL; it may be x or residual
+ *                 itself (same stride).
+ * rstd            [T] fp32, or NULL.
+ * scale           [T] fp32 with VLMCE_E4M3, else NULL.
+ * No other two buffers may overlap.  Every pointer is aligned to its element;
+ * 16-byte accesses are used when H, the strides and the bases allow it.
+ */
+vlmce_status rmsnorm_fwd(const void *x, int64_t x_stride, const void *residual,
+                         int64_t residual_stride, const void *weight, int32_t weight_dtype,
+                         int32_t dtype, int64_t T, int64_t H, float eps, float weight_offset,
+                         void *y, int64_t y_stride, int32_t y_dtype, void *residual_out,
+                         int64_t residual_out_stride, float *rstd, float *scale,
+                         vlmce_stream_t stream);
+
+/* Bytes of device workspace rmsnorm_bwd needs (256-byte aligned): partial sums
+ * of dweight and a value per row.  0 for sizes rmsnorm_bwd rejects. */
+size_t vlmce_rmsnorm_bwd_workspace_bytes(int64_t T, int64_t H);
+
+/*
+ * rmsnorm_bwd -- gradients of y = s rstd (weight + weight_offset) with
+ * a = dy (weight + weight_offset) and xhat = s rstd:
+ *   dx = rstd (a - xhat mean_j(a_j xhat_j)) + dresidual,  dweight = sum_t dy xhat.
+ * x holds the rows s that rmsnorm_fwd normalised (its residual_out), rstd its
+ * rstd.  dx is the gradient of s, thus of x and of residual alike; dresidual
+ * (or NULL) is the gradient that reaches s along the residual stream.
+ *
+ * dx              [T, dx_stride] of `dtype`; it may be dy or dresidual itself
+ *                 (same stride), and overlap nothing else.
+ * dweight         [H] fp32, overwritten, or added to when accumulate_dweight !=
+ *                 0; or NULL.
+ * workspace       >= vlmce_rmsnorm_bwd_workspace_bytes(T, H) bytes, 256-byte
+ *                 aligned.
+ * Deterministic: fixed-order sums, no floating-point atomics.
+ */
+vlmce_status rmsnorm_bwd(const void *dy, int64_t dy_stride, const void *x, int64_t x_stride,
+                         const void *weight, int32_t weight_dtype, const float *rstd,
+                         const void *dresidual, int64_t dresidual_stride, int32_t dtype, int64_t T,
+                         int64_t H, float weight_offset, void *dx, int64_t dx_stride,
+                         float *dweight, int32_t accumulate_dweight, void *workspace,
+                         size_t workspace_bytes, vlmce_stream_t stream);
+
+/*
+ * linear_fwd -- linear layer with its epilogue in the product:
+ *   z = x W^T + bias,  y = act(z) + residual
+ * on tcgen05 tensor cores with fp32 accumulators; the epilogue is in fp32 and
+ * each output is rounded once.
+ *
+ * x               [T, x_stride], rows of K elements of `dtype`: VLMCE_BF16,
+ *                 VLMCE_F16 or VLMCE_E4M3.
+ * weight          [N, weight_stride], rows of K elements of `dtype`.
+ *                 K and both strides are multiples of 16 bytes, both pointers
+ *                 16-byte aligned (the tensor cores' tiles are fetched in units
+ *                 of 16 bytes).
+ * x_scale,        with VLMCE_E4M3: fp32 [T] and [N], the factors of the rows
+ * weight_scale    (row t stands for x_scale[t] x[t]); else NULL.
+ * bias            [N] of out_dtype, or NULL.
+ * residual        [T, residual_stride] of out_dtype, or NULL; it may be y itself
+ *                 (same stride).
+ * out_dtype       `dtype`, or VLMCE_BF16 / VLMCE_F16 with VLMCE_E4M3.
+ * y               [T, y_stride >= N] of out_dtype.
+ * preact          [T, preact_stride >= N] of out_dtype receiving z (what
+ *                 linear_bwd needs with an activation), or NULL.
+ * dev_err         device int32, or NULL: VLMCE_DEVERR_* bits are OR-ed into it
+ *                 (the caller clears it).
+ * T >= 0, N >= 1, K >= 1.  Outputs overlap nothing but what is said above.
+ * Deterministic: the same arguments give the same bits.
+ */
+vlmce_status linear_fwd(const void *x, int64_t x_stride, const float *x_scale, const void *weight,
+                        int64_t weight_stride, const float *weight_scale, int32_t dtype,
+                        const void *bias, const void *residual, int64_t residual_stride,
+                        int32_t out_dtype, int64_t T, int64_t N, int64_t K, int32_t act, void *y,
+                        int64_t y_stride, void *preact, int64_t preact_stride, int32_t *dev_err,
+                        vlmce_stream_t stream);
+
+/* Bytes of device workspace linear_bwd / glu_bwd need (256-byte aligned): the
+ * 16-bit gradient of the pre-activations, partial sums of dbias and a tile
+ * counter.  0 for sizes they reject. */
+size_t vlmce_linear_bwd_workspace_bytes(int64_t T, int64_t N, int64_t K);
+size_t vlmce_glu_bwd_workspace_bytes(int64_t T, int64_t n, int64_t K);
+
+/*
+ * linear_bwd -- gradients of linear_fwd for 16-bit x and weight:
+ *   dz = dy act'(z),  dx = dz W,  dweight = dz^T x,  dbias = sum_t dz
+ * (the residual's gradient is dy itself).  dz is formed in fp32 and rounded
+ * once to `dtype` for the two products; dbias is summed from the fp32 values.
+ *
+ * dtype           VLMCE_BF16 or VLMCE_F16: dy, x, weight, preact, dx.
+ * dy              [T, dy_stride >= N]; preact: linear_fwd's z (not read, and may
+ *                 be NULL, without an activation).
+ * x, weight       as linear_fwd (x is read for dweight, weight for dx).
+ * dx              [T, dx_stride], 16-byte aligned, dx_stride a multiple of 8; or
+ *                 NULL.
+ * dweight         [N, K] contiguous of dweight_dtype (VLMCE_F32 or `dtype`),
+ *                 16-byte aligned, or NULL.
+ * dbias           [N] fp32, or NULL.
+ * accumulate      != 0: dweight (then fp32) and dbias are added to instead of
+ *                 overwritten.
+ * workspace       >= vlmce_linear_bwd_workspace_bytes(T, N, K) bytes, 256-byte
+ *                 aligned.
+ * At least one of dx, dweight, dbias is given (T > 0).  Outputs overlap
+ * nothing.  dev_err as linear_fwd.  Deterministic.
+ */
+vlmce_status linear_bwd(const void *dy, int64_t dy_stride, const void *x, int64_t x_stride,
+                        const void *weight, int64_t weight_stride, const void *preact,
+                        int64_t preact_stride, int32_t dtype, int64_t T, int64_t N, int64_t K,
+                        int32_t act, void *dx, int64_t dx_stride, void *dweight,
+                        int32_t dweight_dtype, float *dbias, int32_t accumulate, int32_t *dev_err,
+                        void *workspace, size_t workspace_bytes, vlmce_stream_t stream);
+
+/*
+ * glu_fwd -- gated feed-forward layer: both projections, the activation and the
+ * product in one kernel.  weight is [2n, weight_stride]: the gate's rows 0 ..
+ * n - 1, then the up projection's (the layout whose output swiglu_fwd takes):
+ *   (g | u) = x W^T,  y = act(g) u,  act other than VLMCE_ACT_NONE.
+ * y [T, y_stride >= n]; preact [T, preact_stride >= 2n] receives (g | u), what
+ * glu_bwd needs, or NULL; weight_scale [2n].  Everything else as linear_fwd.
+ */
+vlmce_status glu_fwd(const void *x, int64_t x_stride, const float *x_scale, const void *weight,
+                     int64_t weight_stride, const float *weight_scale, int32_t dtype,
+                     int32_t out_dtype, int64_t T, int64_t n, int64_t K, int32_t act, void *y,
+                     int64_t y_stride, void *preact, int64_t preact_stride, int32_t *dev_err,
+                     vlmce_stream_t stream);
+
+/*
+ * glu_bwd -- gradients of glu_fwd:  dz = (dy u act'(g) | dy act(g)),
+ * dx = dz W,  dweight = dz^T x ([2n, K]).  preact is glu_fwd's (g | u).
+ * Everything else as linear_bwd.
+ */
+vlmce_status glu_bwd(const void *dy, int64_t dy_stride, const void *x, int64_t x_stride,
+                     const void *weight, int64_t weight_stride, const void *preact,
+                     int64_t preact_stride, int32_t dtype, int64_t T, int64_t n, int64_t K,
+                     int32_t act, void *dx, int64_t dx_stride, void *dweight,
+                     int32_t dweight_dtype, int32_t accumulate, int32_t *dev_err, void *workspace,
+                     size_t workspace_bytes, vlmce_stream_t stream);
 
 /* Bytes of device workspace flce_fwd_bwd needs (256-byte aligned): per-row
  * statistics of every 256-column logits tile, two bf16 [N, 8192] gradient

@@ -1,4 +1,5 @@
-"""GB300-native (sm_103a) fused large-vocabulary LM cross-entropy.
+"""GB300-native (sm_103a) fused large-vocabulary LM cross-entropy, and the
+decoder-layer operators around it (RMS norm, linear and gated layers).
 
 The compute lives in ``lib/libvlmce.so`` (hand-written CUDA kernels behind the
 C ABI in ``include/vlmce.h``); this package holds the build script, a thin
@@ -7,3 +8,6 @@ ctypes/PyTorch binding and the seeded synthetic workloads.
 from .ce import (CEResult, ce_fwd_bwd, ce_fwd_bwd_host, describe_plan, host_workspace_bytes,  # noqa: F401
                  max_vocab, workspace_bytes)
 from .flce import FLCEResult, flce_fwd_bwd  # noqa: F401
+from .linear import (LinearGrads, LinearResult, glu_bwd, glu_fwd, linear_bwd,  # noqa: F401
+                     linear_fwd)
+from .rmsnorm import RMSNormGrads, RMSNormResult, rmsnorm_bwd, rmsnorm_fwd  # noqa: F401

@@ -24,10 +24,16 @@ ERR_TOO_LARGE = 7
 F32 = 0
 BF16 = 1
 F16 = 2
+E4M3 = 3
 NONE = 0
 MEAN = 1
 SUM = 2
 DEVERR_TIMEOUT = 1
+ACT_NONE = 0
+ACT_SILU = 1
+ACT_GELU = 2
+ACT_GELU_TANH = 3
+ACT_RELU = 4
 
 _lock = threading.Lock()
 _lib = None
@@ -79,6 +85,21 @@ SIGNATURES = {
     "vlmce_gemm_bf16": (_i32, [_vp, _i32, _vp, _i32, _vp, _i64, _i64, _i64, _i64, _i64, _i64,
                                _i32, _vp]),
     "vlmce_flce_profile_events": (None, [_vp, _vp]),
+    "rmsnorm_fwd": (_i32, [_vp, _i64, _vp, _i64, _vp, _i32, _i32, _i64, _i64, _f32, _f32, _vp, _i64,
+                           _i32, _vp, _i64, _vp, _vp, _vp]),
+    "vlmce_rmsnorm_bwd_workspace_bytes": (_sz, [_i64, _i64]),
+    "rmsnorm_bwd": (_i32, [_vp, _i64, _vp, _i64, _vp, _i32, _vp, _vp, _i64, _i32, _i64, _i64, _f32,
+                           _vp, _i64, _vp, _i32, _vp, _sz, _vp]),
+    "linear_fwd": (_i32, [_vp, _i64, _vp, _vp, _i64, _vp, _i32, _vp, _vp, _i64, _i32, _i64, _i64,
+                          _i64, _i32, _vp, _i64, _vp, _i64, _vp, _vp]),
+    "vlmce_linear_bwd_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "vlmce_glu_bwd_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "linear_bwd": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _i64, _i64, _i64, _i32,
+                          _vp, _i64, _vp, _i32, _vp, _i32, _vp, _vp, _sz, _vp]),
+    "glu_fwd": (_i32, [_vp, _i64, _vp, _vp, _i64, _vp, _i32, _i32, _i64, _i64, _i64, _i32, _vp,
+                       _i64, _vp, _i64, _vp, _vp]),
+    "glu_bwd": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _i64, _i64, _i64, _i32,
+                       _vp, _i64, _vp, _i32, _i32, _vp, _vp, _sz, _vp]),
 }
 
 

@@ -61,39 +61,12 @@
 
 #include "ce_common.cuh"
 #include "gemm_types.h"
+#include "mbar_wait.cuh"
 #include "ptx.cuh"
 #include "tcgen05.cuh"
 
 namespace vlmce {
 namespace gemm {
-
-// ------------------------------------------------------------ barriers
-template <bool CLUSTER_ACQUIRE = false>
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort,
-                                         int *err) {
-    auto try_once = [&] {
-        return CLUSTER_ACQUIRE ? ptx::mbar_try_wait_cluster(bar, parity)
-                               : ptx::mbar_try_wait(bar, parity);
-    };
-    if (try_once()) return true;
-    if (*abort) return false;
-    const unsigned long long t0 = ptx::globaltimer_ns();
-    for (;;) {
-        for (int i = 0; i < 64; ++i)
-            if (try_once()) return true;
-        if (*abort) return false;
-        if (ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
-            *abort = 1;
-            if (err) atomicOr(err, VLMCE_DEVERR_TIMEOUT);
-            return false;
-        }
-    }
-}
-// Same, but never skipped: used where copies or MMAs may still be in flight.
-__device__ __forceinline__ void drain_bar(uint32_t bar, uint32_t parity, int *err) {
-    volatile int no_abort = 0;
-    wait_bar(bar, parity, &no_abort, err);
-}
 
 // ------------------------------------------------------------ tiles
 struct Tile {

@@ -28,7 +28,6 @@ constexpr int kTileQConsumers = 11;  // leader: producer, MMA issuer, 4 epilogue
 constexpr int kBarriers = 2 * kStages + 5 + 2 * kTileQ;
 constexpr int kSmemBytes = 1024 + kStages * kStageBytes + 8 * kBarriers + 16 + 4 * kTileQ;
 constexpr int kMaxProblems = 3;
-constexpr unsigned long long kWaitLimitNs = 4000000000ull;
 
 enum Mode : int {
     kStoreF32 = 0,   // C = acc (fp32)

@@ -1,0 +1,51 @@
+// mm_types.h -- launch parameters of the matrix-product kernels of the linear
+// and gated layers (mm_large.cuh: CTA pairs on 256 x 256 tiles; mm_small.cuh:
+// single CTAs on 128 weight rows x few tokens) and their host entry points.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "vlmce.h"
+
+namespace vlmce {
+namespace mm {
+
+// What a forward epilogue does with an accumulator acc[t, n]:
+//   z = acc xs[t] ws[n] + bias[n];  preact[t, n] = z;
+//   y[t, n] = act(z) + residual[t, n]                        (linear)
+//   g, u = the two accumulators of column n, scaled likewise;
+//   preact[t, n], preact[t, n_out + n] = g, u;  y[t, n] = act(g) u   (gated)
+// in fp32, each output rounded once to 16 bits.  Null pointers leave a step out.
+struct Epi {
+    uint16_t *y;
+    int64_t y_ld;
+    uint16_t *preact;
+    int64_t preact_ld;
+    const uint16_t *bias;
+    const uint16_t *residual;
+    int64_t residual_ld;
+    const float *xs, *ws;
+    int act, f16;
+    // bytes (32, 16 or 2) that accesses of whole 32-column groups may use
+    int y_vec, preact_vec, preact_up_vec, residual_vec;
+};
+
+// One forward product: x [T, K], weight [N, K] (gated: [2N, K]).
+struct Fwd {
+    const void *x, *w;
+    int64_t x_ld, w_ld;
+    int64_t T, N, K;
+    int gated;
+    int32_t dtype;  // VLMCE_BF16, VLMCE_F16 or VLMCE_E4M3
+    Epi e;
+    int *err;
+};
+
+// Enqueue it (T, N, K >= 1); the kernel is chosen by the sizes.
+cudaError_t forward(const Fwd &f, int sm_count, cudaStream_t s);
+
+}  // namespace mm
+}  // namespace vlmce

@@ -1,0 +1,663 @@
+// rmsnorm.cu -- root-mean-square norm of rows with the residual's addition,
+// forward (output in the input type, or in e4m3 with one scale per row) and
+// backward.
+//
+//   forward   s = x + residual,  rstd = (mean_j s_j^2 + eps)^-1/2,
+//             y = s rstd (w + offset)
+//   e4m3      scale = max_j |y_j| / 448,  q = e4m3(y / scale)
+//   backward  a_j = dy_j (w_j + offset),  xhat = s rstd,
+//             dx = rstd (a - xhat mean_j(a_j xhat_j)) + dresidual
+//             dw_j = sum_t dy_j xhat_j
+//
+// All in fp32, each output rounded once; y is formed from the unrounded sum s.
+// For e4m3 the row's sum of squares and max |s (w + offset)| come from one
+// reduction: rstd cancels in y / scale = s (w + offset) 448 / max|s (w + offset)|.
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+
+#include "act.cuh"
+#include "host_util.h"
+#include "ptx.cuh"
+#include "vlmce.h"
+
+namespace vlmce {
+namespace rms {
+namespace {
+
+template <int DT>
+struct Elt {
+    static constexpr int kBytes = DT == VLMCE_F32 ? 4 : 2;
+    static constexpr int kPer16 = 16 / kBytes;
+};
+
+// E consecutive elements at element index i of a row (E = 16 bytes' worth, or 1).
+template <int DT, int E>
+__device__ __forceinline__ void load_e(const void *row, int64_t i, float (&v)[E]) {
+    if constexpr (E == 1) {
+        if constexpr (DT == VLMCE_F32)
+            v[0] = static_cast<const float *>(row)[i];
+        else
+            v[0] = act::from16(static_cast<const uint16_t *>(row)[i], DT == VLMCE_F16);
+    } else if constexpr (DT == VLMCE_F32) {
+        const float4 u = *reinterpret_cast<const float4 *>(static_cast<const float *>(row) + i);
+        v[0] = u.x;
+        v[1] = u.y;
+        v[2] = u.z;
+        v[3] = u.w;
+    } else {
+        const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(row) + i);
+        act::unpack16x2(u.x, v[0], v[1], DT == VLMCE_F16);
+        act::unpack16x2(u.y, v[2], v[3], DT == VLMCE_F16);
+        act::unpack16x2(u.z, v[4], v[5], DT == VLMCE_F16);
+        act::unpack16x2(u.w, v[6], v[7], DT == VLMCE_F16);
+    }
+}
+template <int DT, int E>
+__device__ __forceinline__ void store_e(void *row, int64_t i, const float (&v)[E]) {
+    if constexpr (E == 1) {
+        if constexpr (DT == VLMCE_F32)
+            static_cast<float *>(row)[i] = v[0];
+        else
+            static_cast<uint16_t *>(row)[i] = act::to16(v[0], DT == VLMCE_F16);
+    } else if constexpr (DT == VLMCE_F32) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(row) + i) =
+            make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+        constexpr bool f16 = DT == VLMCE_F16;
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(row) + i) =
+            make_uint4(act::pack16x2(v[0], v[1], f16), act::pack16x2(v[2], v[3], f16),
+                       act::pack16x2(v[4], v[5], f16), act::pack16x2(v[6], v[7], f16));
+    }
+}
+template <int E>
+__device__ __forceinline__ void store_e4m3(unsigned char *row, int64_t i, const float (&v)[E]) {
+    if constexpr (E == 1) {
+        row[i] = __nv_cvt_float_to_fp8(v[0], __NV_SATFINITE, __NV_E4M3);
+    } else {
+        uint32_t u[E / 4];
+#pragma unroll
+        for (int j = 0; j < E / 4; ++j)
+            u[j] = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * j], v[4 * j + 1]), __NV_SATFINITE,
+                                            __NV_E4M3) |
+                   static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(
+                       make_float2(v[4 * j + 2], v[4 * j + 3]), __NV_SATFINITE, __NV_E4M3))
+                       << 16;
+        if constexpr (E == 8)
+            *reinterpret_cast<uint2 *>(row + i) = make_uint2(u[0], u[1]);
+        else
+            *reinterpret_cast<uint32_t *>(row + i) = u[0];
+    }
+}
+// The weight has the rows' type or fp32.
+template <int DT, int E>
+__device__ __forceinline__ void load_w(const void *w, bool f32, int64_t i, float offset,
+                                       float (&v)[E]) {
+    if (DT == VLMCE_F32 || !f32) {
+        load_e<DT, E>(w, i, v);
+    } else if constexpr (E == 8) {
+        float a[4], b[4];
+        load_e<VLMCE_F32, 4>(w, i, a);
+        load_e<VLMCE_F32, 4>(w, i + 4, b);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[j] = a[j];
+            v[4 + j] = b[j];
+        }
+    } else {
+        load_e<VLMCE_F32, E>(w, i, v);
+    }
+#pragma unroll
+    for (int j = 0; j < E; ++j) v[j] += offset;
+}
+
+// Sum of a and maximum of m over the block, in every thread.  sh: [2][32].
+__device__ __forceinline__ void block_sum_max(float &a, float &m, float (*sh)[32]) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, off);
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    }
+    const int warps = blockDim.x >> 5;
+    if (warps == 1) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (lane == 0) {
+        sh[0][warp] = a;
+        sh[1][warp] = m;
+    }
+    __syncthreads();
+    a = lane < warps ? sh[0][lane] : 0.f;
+    m = lane < warps ? sh[1][lane] : 0.f;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, off);
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    }
+}
+
+// ------------------------------------------------------------ forward
+struct FwdParams {
+    const unsigned char *x, *residual;
+    const void *weight;
+    unsigned char *y, *sum;
+    float *rstd, *scale;
+    int64_t T, H;
+    int64_t x_ld, residual_ld, y_ld, sum_ld;  // bytes
+    float eps, offset;
+    int w_f32;
+};
+
+// One CTA per row; thread i holds the row's elements (i + k blockDim) E .. + E
+// for k < NG in registers (fp32 sums), so memory is read once.  NG = 0: rows
+// too wide for that; the sums are read again for the second pass.
+template <int DT, int E, int NG, bool QUANT>
+__global__ void __launch_bounds__(1024) fwd_kernel(const FwdParams p) {
+    __shared__ float sh[2][32];
+    const int64_t row = blockIdx.x;
+    const unsigned char *x = p.x + row * p.x_ld;
+    const unsigned char *res = p.residual ? p.residual + row * p.residual_ld : nullptr;
+    unsigned char *sum = p.sum ? p.sum + row * p.sum_ld : nullptr;
+    unsigned char *y = p.y + row * p.y_ld;
+    constexpr int kHold = NG > 0 ? NG : 1;
+    float v[kHold][E];
+    float ss = 0.f, mx = 0.f;
+    auto sum_at = [&](int64_t i, float (&s)[E]) {
+        load_e<DT, E>(x, i, s);
+        if (res) {
+            float r[E];
+            load_e<DT, E>(res, i, r);
+#pragma unroll
+            for (int j = 0; j < E; ++j) s[j] += r[j];
+        }
+    };
+    auto fold = [&](int64_t i, const float (&s)[E]) {
+#pragma unroll
+        for (int j = 0; j < E; ++j) ss = fmaf(s[j], s[j], ss);
+        if constexpr (QUANT) {
+            float w[E];
+            load_w<DT, E>(p.weight, p.w_f32 != 0, i, p.offset, w);
+#pragma unroll
+            for (int j = 0; j < E; ++j) mx = fmaxf(mx, fabsf(s[j] * w[j]));
+        }
+    };
+    const int64_t step = static_cast<int64_t>(blockDim.x) * E;
+    const int64_t i0 = static_cast<int64_t>(threadIdx.x) * E;
+    if constexpr (NG > 0) {
+#pragma unroll
+        for (int k = 0; k < NG; ++k)
+            if (i0 + k * step < p.H) sum_at(i0 + k * step, v[k]);
+#pragma unroll
+        for (int k = 0; k < NG; ++k)
+            if (i0 + k * step < p.H) {
+                fold(i0 + k * step, v[k]);
+                if (sum) store_e<DT, E>(sum, i0 + k * step, v[k]);
+            }
+    } else {
+        for (int64_t i = i0; i < p.H; i += step) {
+            sum_at(i, v[0]);
+            fold(i, v[0]);
+        }
+    }
+    block_sum_max(ss, mx, sh);
+    const float rstd = __frsqrt_rn(ss / static_cast<float>(p.H) + p.eps);
+    mx = fmaxf(mx, 1e-30f);
+    if (threadIdx.x == 0) {
+        if (p.rstd) p.rstd[row] = rstd;
+        if constexpr (QUANT) p.scale[row] = rstd * mx / 448.f;
+    }
+    const float mul = QUANT ? 448.f / mx : rstd;
+    auto emit = [&](int64_t i, const float (&s)[E]) {
+        float w[E], o[E];
+        load_w<DT, E>(p.weight, p.w_f32 != 0, i, p.offset, w);
+        if constexpr (QUANT) {
+#pragma unroll
+            for (int j = 0; j < E; ++j) o[j] = s[j] * w[j] * mul;
+            store_e4m3<E>(y, i, o);
+        } else {
+#pragma unroll
+            for (int j = 0; j < E; ++j) o[j] = s[j] * mul * w[j];
+            store_e<DT, E>(y, i, o);
+        }
+    };
+    if constexpr (NG > 0) {
+#pragma unroll
+        for (int k = 0; k < NG; ++k)
+            if (i0 + k * step < p.H) emit(i0 + k * step, v[k]);
+    } else {
+        for (int64_t i = i0; i < p.H; i += step) {
+            sum_at(i, v[0]);
+            if (sum) store_e<DT, E>(sum, i, v[0]);
+            emit(i, v[0]);
+        }
+    }
+}
+
+// ------------------------------------------------------------ backward
+struct BwdParams {
+    const unsigned char *dy, *x, *dres;
+    const void *weight;
+    const float *rstd;
+    unsigned char *dx;
+    float *part;       // [CTAs][H] partial dw, or null
+    float *dot;        // wide rows: [T] mean_j(a_j xhat_j)
+    int64_t T, H;
+    int64_t dy_ld, x_ld, dres_ld, dx_ld;  // bytes
+    float offset;
+    int w_f32;
+};
+
+// Each CTA takes rows blockIdx.x, + gridDim.x, ...; a thread owns the same
+// columns in all of them, so dw accumulates in registers.
+template <int DT, int E, int NG>
+__global__ void __launch_bounds__(1024) bwd_kernel(const BwdParams p) {
+    __shared__ float sh[2][2][32];
+    const int64_t step = static_cast<int64_t>(blockDim.x) * E;
+    const int64_t i0 = static_cast<int64_t>(threadIdx.x) * E;
+    float dw[NG][E];
+#pragma unroll
+    for (int k = 0; k < NG; ++k)
+#pragma unroll
+        for (int j = 0; j < E; ++j) dw[k][j] = 0.f;
+    int flip = 0;
+    for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x, flip ^= 1) {
+        const unsigned char *dy = p.dy + row * p.dy_ld, *x = p.x + row * p.x_ld;
+        const float rstd = p.rstd[row];
+        float a[NG][E], h[NG][E];
+        float c = 0.f, unused = 0.f;
+#pragma unroll
+        for (int k = 0; k < NG; ++k) {
+            const int64_t i = i0 + k * step;
+            if (i < p.H) {
+                load_e<DT, E>(dy, i, a[k]);
+                load_e<DT, E>(x, i, h[k]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < NG; ++k) {
+            const int64_t i = i0 + k * step;
+            if (i < p.H) {
+                float w[E];
+                load_w<DT, E>(p.weight, p.w_f32 != 0, i, p.offset, w);
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    h[k][j] *= rstd;
+                    dw[k][j] = fmaf(a[k][j], h[k][j], dw[k][j]);
+                    a[k][j] *= w[j];
+                    c = fmaf(a[k][j], h[k][j], c);
+                }
+            }
+        }
+        block_sum_max(c, unused, sh[flip]);  // two buffers: one barrier a row
+        c /= static_cast<float>(p.H);
+#pragma unroll
+        for (int k = 0; k < NG; ++k) {
+            const int64_t i = i0 + k * step;
+            if (i < p.H) {
+                float r[E];
+#pragma unroll
+                for (int j = 0; j < E; ++j) r[j] = 0.f;
+                if (p.dres) load_e<DT, E>(p.dres + row * p.dres_ld, i, r);
+#pragma unroll
+                for (int j = 0; j < E; ++j) r[j] = fmaf(rstd, a[k][j] - h[k][j] * c, r[j]);
+                store_e<DT, E>(p.dx + row * p.dx_ld, i, r);
+            }
+        }
+    }
+    if (p.part) {
+        float *part = p.part + static_cast<int64_t>(blockIdx.x) * p.H;
+#pragma unroll
+        for (int k = 0; k < NG; ++k)
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+                if (i0 + k * step < p.H) part[i0 + k * step + j] = dw[k][j];
+    }
+}
+
+// Rows too wide for one CTA's registers: the rows' mean(a xhat), then dx and
+// the partial dw by column segments.
+template <int DT, int E>
+__global__ void __launch_bounds__(512) dot_kernel(const BwdParams p) {
+    __shared__ float sh[2][32];
+    const int64_t row = blockIdx.x;
+    const float rstd = p.rstd[row];
+    float c = 0.f, unused = 0.f;
+    for (int64_t i = static_cast<int64_t>(threadIdx.x) * E; i < p.H;
+         i += static_cast<int64_t>(blockDim.x) * E) {
+        float d[E], h[E], w[E];
+        load_e<DT, E>(p.dy + row * p.dy_ld, i, d);
+        load_e<DT, E>(p.x + row * p.x_ld, i, h);
+        load_w<DT, E>(p.weight, p.w_f32 != 0, i, p.offset, w);
+#pragma unroll
+        for (int j = 0; j < E; ++j) c = fmaf(d[j] * w[j], h[j] * rstd, c);
+    }
+    block_sum_max(c, unused, sh);
+    if (threadIdx.x == 0) p.dot[row] = c / static_cast<float>(p.H);
+}
+template <int DT, int E>
+__global__ void __launch_bounds__(512) segment_kernel(const BwdParams p) {
+    const int64_t i = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) * E;
+    if (i >= p.H) return;
+    float dw[E], w[E];
+    load_w<DT, E>(p.weight, p.w_f32 != 0, i, p.offset, w);
+#pragma unroll
+    for (int j = 0; j < E; ++j) dw[j] = 0.f;
+    for (int64_t row = blockIdx.y; row < p.T; row += gridDim.y) {
+        const float rstd = p.rstd[row], c = p.dot[row];
+        float d[E], h[E], r[E];
+        load_e<DT, E>(p.dy + row * p.dy_ld, i, d);
+        load_e<DT, E>(p.x + row * p.x_ld, i, h);
+#pragma unroll
+        for (int j = 0; j < E; ++j) r[j] = 0.f;
+        if (p.dres) load_e<DT, E>(p.dres + row * p.dres_ld, i, r);
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            h[j] *= rstd;
+            dw[j] = fmaf(d[j], h[j], dw[j]);
+            r[j] = fmaf(rstd, d[j] * w[j] - h[j] * c, r[j]);
+        }
+        store_e<DT, E>(p.dx + row * p.dx_ld, i, r);
+    }
+    if (p.part) {
+#pragma unroll
+        for (int j = 0; j < E; ++j) p.part[blockIdx.y * p.H + i + j] = dw[j];
+    }
+}
+
+__global__ void __launch_bounds__(256) dw_kernel(const float *part, int parts, int64_t H, float *dw,
+                                                 int accumulate) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 32 + (threadIdx.x & 31);
+    __shared__ float sh[8][32];
+    const int warp = threadIdx.x >> 5;
+    float a = 0.f;
+    if (i < H)
+        for (int q = warp; q < parts; q += 8) a += part[static_cast<int64_t>(q) * H + i];
+    sh[warp][threadIdx.x & 31] = a;
+    __syncthreads();
+    if (warp == 0 && i < H) {
+        a = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) a += sh[w][threadIdx.x];
+        dw[i] = accumulate ? dw[i] + a : a;
+    }
+}
+
+// ------------------------------------------------------------ host side
+constexpr int64_t kMaxH = INT64_C(1) << 30;
+constexpr int kMaxParts = 512;  // CTAs whose partial dw the workspace holds
+
+int elt_of(int32_t dtype) { return dtype == VLMCE_F32 ? 4 : 2; }
+bool dtype_ok(int32_t d) { return d == VLMCE_F32 || d == VLMCE_BF16 || d == VLMCE_F16; }
+
+// Registers hold ng granules of E elements per thread with `threads` threads;
+// ng = 0: the row is too wide.
+struct Shape {
+    int ng, threads;
+};
+Shape shape_of(int64_t H, int E) {
+    const int64_t granules = (H + E - 1) / E;
+    const int sizes[3] = {E == 1 ? 4 : 1, E == 1 ? 8 : 2, E == 1 ? 16 : 4};
+    const int most[3] = {256, 512, 1024};
+    for (int k = 0; k < 3; ++k)
+        if (granules <= static_cast<int64_t>(sizes[k]) * most[k])
+            return {sizes[k],
+                    static_cast<int>(round_up((granules + sizes[k] - 1) / sizes[k], 32))};
+    return {0, 512};
+}
+
+using FwdKernel = void (*)(const FwdParams);
+template <int DT, bool Q>
+FwdKernel fwd_pick(bool vec, int ng) {
+    constexpr int E = Elt<DT>::kPer16;
+    if (vec) {
+        switch (ng) {
+            case 1: return fwd_kernel<DT, E, 1, Q>;
+            case 2: return fwd_kernel<DT, E, 2, Q>;
+            case 4: return fwd_kernel<DT, E, 4, Q>;
+            default: return fwd_kernel<DT, E, 0, Q>;
+        }
+    }
+    switch (ng) {
+        case 4: return fwd_kernel<DT, 1, 4, Q>;
+        case 8: return fwd_kernel<DT, 1, 8, Q>;
+        case 16: return fwd_kernel<DT, 1, 16, Q>;
+        default: return fwd_kernel<DT, 1, 0, Q>;
+    }
+}
+FwdKernel fwd_kernel_of(int32_t dtype, bool quant, bool vec, int ng) {
+    switch (dtype) {
+        case VLMCE_F32:
+            return quant ? fwd_pick<VLMCE_F32, true>(vec, ng) : fwd_pick<VLMCE_F32, false>(vec, ng);
+        case VLMCE_BF16:
+            return quant ? fwd_pick<VLMCE_BF16, true>(vec, ng)
+                         : fwd_pick<VLMCE_BF16, false>(vec, ng);
+        default:
+            return quant ? fwd_pick<VLMCE_F16, true>(vec, ng) : fwd_pick<VLMCE_F16, false>(vec, ng);
+    }
+}
+using BwdKernel = void (*)(const BwdParams);
+template <int DT>
+BwdKernel bwd_pick(bool vec, int ng) {
+    constexpr int E = Elt<DT>::kPer16;
+    if (vec) {
+        switch (ng) {
+            case 1: return bwd_kernel<DT, E, 1>;
+            case 2: return bwd_kernel<DT, E, 2>;
+            default: return bwd_kernel<DT, E, 4>;
+        }
+    }
+    switch (ng) {
+        case 4: return bwd_kernel<DT, 1, 4>;
+        case 8: return bwd_kernel<DT, 1, 8>;
+        default: return bwd_kernel<DT, 1, 16>;
+    }
+}
+BwdKernel bwd_kernel_of(int32_t dtype, bool vec, int ng) {
+    switch (dtype) {
+        case VLMCE_F32: return bwd_pick<VLMCE_F32>(vec, ng);
+        case VLMCE_BF16: return bwd_pick<VLMCE_BF16>(vec, ng);
+        default: return bwd_pick<VLMCE_F16>(vec, ng);
+    }
+}
+template <int DT>
+void wide_pick(bool vec, BwdKernel *dot, BwdKernel *seg) {
+    constexpr int E = Elt<DT>::kPer16;
+    *dot = vec ? dot_kernel<DT, E> : dot_kernel<DT, 1>;
+    *seg = vec ? segment_kernel<DT, E> : segment_kernel<DT, 1>;
+}
+
+// A [T, H] argument: stride in elements of elt bytes.
+vlmce_status check_rows(const void *p, int64_t T, int64_t H, int64_t ld, int elt) {
+    if (ld < H) return VLMCE_ERR_INVALID_ARG;
+    if (ld > (INT64_MAX / 8) / elt / std::max<int64_t>(T, 1)) return VLMCE_ERR_TOO_LARGE;
+    if (T > 0 && !p) return VLMCE_ERR_INVALID_ARG;
+    if (!aligned(p, static_cast<uintptr_t>(elt))) return VLMCE_ERR_MISALIGNED;
+    return VLMCE_OK;
+}
+bool overlap(const void *a, int64_t a_ld, int a_elt, const void *b, int64_t b_ld, int b_elt,
+             int64_t T, int64_t H) {
+    if (!a || !b || T < 1) return false;
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+    return pa < pb + static_cast<uintptr_t>(((T - 1) * b_ld + H) * b_elt) &&
+           pb < pa + static_cast<uintptr_t>(((T - 1) * a_ld + H) * a_elt);
+}
+
+}  // namespace
+}  // namespace rms
+}  // namespace vlmce
+
+extern "C" vlmce_status rmsnorm_fwd(const void *x, int64_t x_stride, const void *residual,
+                                    int64_t residual_stride, const void *weight,
+                                    int32_t weight_dtype, int32_t dtype, int64_t T, int64_t H,
+                                    float eps, float weight_offset, void *y, int64_t y_stride,
+                                    int32_t y_dtype, void *residual_out,
+                                    int64_t residual_out_stride, float *rstd, float *scale,
+                                    vlmce_stream_t stream) {
+    using namespace vlmce;
+    using namespace vlmce::rms;
+    if (!dtype_ok(dtype) || (weight_dtype != dtype && weight_dtype != VLMCE_F32) ||
+        (y_dtype != dtype && y_dtype != VLMCE_E4M3))
+        return VLMCE_ERR_UNSUPPORTED_DTYPE;
+    const bool quant = y_dtype == VLMCE_E4M3;
+    const int elt = elt_of(dtype), yelt = quant ? 1 : elt;
+    if (T < 0 || H < 1 || !(eps >= 0.f) || !std::isfinite(eps) || !std::isfinite(weight_offset) ||
+        !weight || (T > 0 && quant != (scale != nullptr)))
+        return VLMCE_ERR_INVALID_ARG;
+    if (H > kMaxH || T > INT32_MAX) return VLMCE_ERR_TOO_LARGE;
+    vlmce_status st = check_rows(x, T, H, x_stride, elt);
+    if (st == VLMCE_OK) st = check_rows(y, T, H, y_stride, yelt);
+    if (st == VLMCE_OK && residual) st = check_rows(residual, T, H, residual_stride, elt);
+    if (st == VLMCE_OK && residual_out)
+        st = check_rows(residual_out, T, H, residual_out_stride, elt);
+    if (st != VLMCE_OK) return st;
+    if (!aligned(weight, weight_dtype == VLMCE_F32 ? 4 : 2) || !aligned(rstd, 4) ||
+        !aligned(scale, 4))
+        return VLMCE_ERR_MISALIGNED;
+    auto same = [&](const void *a, int64_t a_ld, const void *b, int64_t b_ld) {
+        return a == b && (a_ld == b_ld || T <= 1);
+    };
+    if (overlap(y, y_stride, yelt, x, x_stride, elt, T, H) ||
+        overlap(y, y_stride, yelt, residual, residual_stride, elt, T, H) ||
+        overlap(y, y_stride, yelt, residual_out, residual_out_stride, elt, T, H) ||
+        (overlap(residual_out, residual_out_stride, elt, x, x_stride, elt, T, H) &&
+         !same(residual_out, residual_out_stride, x, x_stride)) ||
+        (overlap(residual_out, residual_out_stride, elt, residual, residual_stride, elt, T, H) &&
+         !same(residual_out, residual_out_stride, residual, residual_stride)))
+        return VLMCE_ERR_INVALID_ARG;
+    if (T == 0) return VLMCE_OK;
+    DeviceInfo dev;
+    st = current_device(&dev);
+    if (st != VLMCE_OK) return st;
+    const int E = 16 / elt;
+    const bool vec = H % E == 0 && x_stride % E == 0 && aligned(x, 16) && y_stride % E == 0 &&
+                     aligned(y, static_cast<uintptr_t>(E * yelt)) && aligned(weight, 16) &&
+                     (!residual || (residual_stride % E == 0 && aligned(residual, 16))) &&
+                     (!residual_out || (residual_out_stride % E == 0 && aligned(residual_out, 16)));
+    const Shape sh = shape_of(H, vec ? E : 1);
+    FwdParams p = {};
+    p.x = static_cast<const unsigned char *>(x);
+    p.residual = static_cast<const unsigned char *>(residual);
+    p.weight = weight;
+    p.y = static_cast<unsigned char *>(y);
+    p.sum = static_cast<unsigned char *>(residual_out);
+    p.rstd = rstd;
+    p.scale = scale;
+    p.T = T;
+    p.H = H;
+    p.x_ld = x_stride * elt;
+    p.residual_ld = residual_stride * elt;
+    p.y_ld = y_stride * yelt;
+    p.sum_ld = residual_out_stride * elt;
+    p.eps = eps;
+    p.offset = weight_offset;
+    p.w_f32 = weight_dtype == VLMCE_F32;
+    fwd_kernel_of(dtype, quant, vec, sh.ng)<<<static_cast<unsigned>(T), sh.threads, 0,
+                                              reinterpret_cast<cudaStream_t>(stream)>>>(p);
+    return launch_status(cudaSuccess, "rmsnorm_fwd");
+}
+
+extern "C" size_t vlmce_rmsnorm_bwd_workspace_bytes(int64_t T, int64_t H) {
+    using namespace vlmce;
+    using namespace vlmce::rms;
+    if (T < 0 || H < 1 || H > kMaxH || T > INT32_MAX) return 0;
+    return static_cast<size_t>(round_up(4 * H * std::min<int64_t>(std::max<int64_t>(T, 1), kMaxParts), 256) +
+                               round_up(4 * T, 256));
+}
+
+extern "C" vlmce_status rmsnorm_bwd(const void *dy, int64_t dy_stride, const void *x,
+                                    int64_t x_stride, const void *weight, int32_t weight_dtype,
+                                    const float *rstd, const void *dresidual,
+                                    int64_t dresidual_stride, int32_t dtype, int64_t T, int64_t H,
+                                    float weight_offset, void *dx, int64_t dx_stride,
+                                    float *dweight, int32_t accumulate_dweight, void *workspace,
+                                    size_t workspace_bytes, vlmce_stream_t stream) {
+    using namespace vlmce;
+    using namespace vlmce::rms;
+    if (!dtype_ok(dtype) || (weight_dtype != dtype && weight_dtype != VLMCE_F32))
+        return VLMCE_ERR_UNSUPPORTED_DTYPE;
+    const int elt = elt_of(dtype);
+    if (T < 0 || H < 1 || !std::isfinite(weight_offset) || !weight || (T > 0 && !rstd))
+        return VLMCE_ERR_INVALID_ARG;
+    if (H > kMaxH || T > INT32_MAX) return VLMCE_ERR_TOO_LARGE;
+    vlmce_status st = check_rows(dy, T, H, dy_stride, elt);
+    if (st == VLMCE_OK) st = check_rows(x, T, H, x_stride, elt);
+    if (st == VLMCE_OK) st = check_rows(dx, T, H, dx_stride, elt);
+    if (st == VLMCE_OK && dresidual) st = check_rows(dresidual, T, H, dresidual_stride, elt);
+    if (st != VLMCE_OK) return st;
+    if (!aligned(weight, weight_dtype == VLMCE_F32 ? 4 : 2) || !aligned(rstd, 4) ||
+        !aligned(dweight, 4))
+        return VLMCE_ERR_MISALIGNED;
+    auto clash = [&](const void *b, int64_t b_ld) {
+        return overlap(dx, dx_stride, elt, b, b_ld, elt, T, H) &&
+               !(dx == b && (dx_stride == b_ld || T <= 1));
+    };
+    if (overlap(dx, dx_stride, elt, x, x_stride, elt, T, H) || clash(dy, dy_stride) ||
+        clash(dresidual, dresidual_stride))
+        return VLMCE_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < vlmce_rmsnorm_bwd_workspace_bytes(T, H))
+        return VLMCE_ERR_WORKSPACE_TOO_SMALL;
+    if (!aligned(workspace, 256)) return VLMCE_ERR_MISALIGNED;
+    DeviceInfo dev;
+    st = current_device(&dev);
+    if (st != VLMCE_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (T == 0) {
+        cudaError_t e = cudaSuccess;
+        if (dweight && !accumulate_dweight)
+            e = cudaMemsetAsync(dweight, 0, static_cast<size_t>(4 * H), s);
+        return launch_status(e, "rmsnorm_bwd");
+    }
+    const int E = 16 / elt;
+    const bool vec = H % E == 0 && x_stride % E == 0 && aligned(x, 16) && dy_stride % E == 0 &&
+                     aligned(dy, 16) && dx_stride % E == 0 && aligned(dx, 16) &&
+                     aligned(weight, 16) &&
+                     (!dresidual || (dresidual_stride % E == 0 && aligned(dresidual, 16)));
+    const Shape sh = shape_of(H, vec ? E : 1);
+    const int64_t parts_max = std::min<int64_t>(T, kMaxParts);
+    BwdParams p = {};
+    p.dy = static_cast<const unsigned char *>(dy);
+    p.x = static_cast<const unsigned char *>(x);
+    p.dres = static_cast<const unsigned char *>(dresidual);
+    p.weight = weight;
+    p.rstd = rstd;
+    p.dx = static_cast<unsigned char *>(dx);
+    p.part = dweight ? static_cast<float *>(workspace) : nullptr;
+    p.dot = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) +
+                                      round_up(4 * H * parts_max, 256));
+    p.T = T;
+    p.H = H;
+    p.dy_ld = dy_stride * elt;
+    p.x_ld = x_stride * elt;
+    p.dres_ld = dresidual_stride * elt;
+    p.dx_ld = dx_stride * elt;
+    p.offset = weight_offset;
+    p.w_f32 = weight_dtype == VLMCE_F32;
+    int64_t parts;
+    if (sh.ng > 0) {
+        parts = std::min<int64_t>(parts_max, static_cast<int64_t>(dev.sm_count) * 2);
+        bwd_kernel_of(dtype, vec, sh.ng)<<<static_cast<unsigned>(parts), sh.threads, 0, s>>>(p);
+    } else {
+        BwdKernel dot, seg;
+        if (dtype == VLMCE_F32)
+            wide_pick<VLMCE_F32>(vec, &dot, &seg);
+        else if (dtype == VLMCE_BF16)
+            wide_pick<VLMCE_BF16>(vec, &dot, &seg);
+        else
+            wide_pick<VLMCE_F16>(vec, &dot, &seg);
+        dot<<<static_cast<unsigned>(T), 512, 0, s>>>(p);
+        st = launch_status(cudaSuccess, "rmsnorm_bwd");
+        if (st != VLMCE_OK) return st;
+        const int64_t per = 512 * (vec ? E : 1);
+        const int64_t gx = (H + per - 1) / per;
+        parts = std::min<int64_t>(parts_max,
+                                  std::max<int64_t>(1, static_cast<int64_t>(dev.sm_count) * 4 / gx));
+        seg<<<dim3(static_cast<unsigned>(gx), static_cast<unsigned>(parts), 1), 512, 0, s>>>(p);
+    }
+    st = launch_status(cudaSuccess, "rmsnorm_bwd");
+    if (st != VLMCE_OK || !dweight) return st;
+    dw_kernel<<<static_cast<unsigned>((H + 31) / 32), 256, 0, s>>>(
+        p.part, static_cast<int>(parts), H, dweight, accumulate_dweight);
+    return launch_status(cudaSuccess, "rmsnorm_bwd");
+}

@@ -1,10 +1,11 @@
-// tcgen05.cuh -- inline-PTX wrappers for the sm_100-family tensor cores,
-// in their CTA-pair form (.cta_group::2: one MMA spans the tensor cores of
-// two SMs of a cluster): tensor-memory (TMEM) allocation, tcgen05.mma with
-// bf16 operands and fp32 accumulators, commits that arrive on the mbarriers
-// of both CTAs of the pair, TMEM loads, tiled TMA loads, and the
-// shared-memory / instruction descriptors the MMA consumes.  Every tcgen05
-// instruction of a kernel must use the same .cta_group.
+// tcgen05.cuh -- inline-PTX wrappers for the sm_100-family tensor cores:
+// tensor-memory (TMEM) allocation, tcgen05.mma with 16-bit or 8-bit operands
+// and fp32 accumulators, commits that arrive on mbarriers, TMEM loads, tiled
+// TMA loads, and the shared-memory / instruction descriptors the MMA
+// consumes; in the CTA-pair form (.cta_group::2: one MMA spans the tensor
+// cores of two SMs of a cluster, commits arrive in both CTAs of the pair) and
+// the single-CTA form.  Every tcgen05 instruction of a kernel must use the
+// same .cta_group.
 #pragma once
 
 #include <cuda.h>
@@ -51,6 +52,17 @@ __device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, 
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// Same with 8-bit floating-point operands (kind::f8f6f4, K = 32 per instruction);
+// the formats are in the instruction descriptor.
+__device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
 // Once every pair MMA this thread issued so far has completed, arrive once on
 // the mbarrier at shared-memory offset `mbar` of each CTA in `cta_mask`.
 __device__ __forceinline__ void mma_commit_pair(uint32_t mbar, uint16_t cta_mask) {
@@ -61,6 +73,53 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t mbar, uint16_t cta_mask
         : "memory");
 }
 
+// ------------------------------------------------- single-CTA forms
+__device__ __forceinline__ void tmem_alloc(uint32_t dst, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst),
+                 "r"(ncols)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish() {
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                         uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                       uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t mbar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(mbar)
+        : "memory");
+}
+
+// 32 lanes x 16 consecutive fp32 columns of TMEM into 16 registers per thread.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
 // 32 lanes x 32 consecutive fp32 columns of TMEM into 32 registers per thread
 // (thread i of the warp gets lane base + i).  Complete with tmem_ld_wait().
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
@@ -92,6 +151,15 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
         "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile"
         ".mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
         "l"(tm), "r"(c0), "r"(c1), "r"(mbar_leader)
+        : "memory");
+}
+// Counted on an mbarrier of this CTA.
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *tm, int c0, int c1,
+                                            uint32_t mbar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(tm), "r"(c0), "r"(c1), "r"(mbar)
         : "memory");
 }
 __device__ __forceinline__ void prefetch_tensormap(const CUtensorMap *tm) {
