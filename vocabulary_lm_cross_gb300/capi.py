@@ -115,6 +115,8 @@ class VlmceError(RuntimeError):
 def lib():
     """The loaded library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB):

@@ -226,7 +226,10 @@ vlmce_status forward(const FwdArgs &a, const char *where) {
     const int elt = fp8 ? 1 : 2;
     if (a.T < 0 || a.N < 1 || a.K < 1 || a.K * elt % 16 != 0 || !act_ok(a.act, a.gated))
         return VLMCE_ERR_INVALID_ARG;
-    if (a.T > kMaxDim || a.N > kMaxDim / 2 || a.K > kMaxDim) return VLMCE_ERR_TOO_LARGE;
+    // the products' tiles are numbered in 32 bits
+    if (a.T > kMaxDim || a.N > kMaxDim / 2 || a.K > kMaxDim ||
+        a.T / 256 + 1 > INT32_MAX / 16 / (a.N / 128 + 1))
+        return VLMCE_ERR_TOO_LARGE;
     const int64_t rows = a.gated ? 2 * a.N : a.N;
     vlmce_status st = check_operand(a.x, a.T, a.K, a.x_stride, elt);
     if (st == VLMCE_OK) st = check_operand(a.weight, rows, a.K, a.weight_stride, elt);
@@ -279,7 +282,7 @@ vlmce_status forward(const FwdArgs &a, const char *where) {
     e.preact_vec = vec_of(a.preact, a.preact_stride);
     e.preact_up_vec = vec_of(static_cast<uint16_t *>(a.preact) + a.N, a.preact_stride);
     e.residual_vec = vec_of(a.residual, a.residual_stride);
-    return launch_status(mm::forward(f, dev.sm_count, a.stream), where);
+    return launch_status(mm::forward(f, a.stream), where);
 }
 
 // ------------------------------------------------------------ backward
@@ -313,7 +316,6 @@ constexpr int64_t kHead = 256;  // the GEMM launch's tile counter
 int64_t dz_ld_of(int64_t rows) { return round_up(rows, 8); }
 int64_t part_bytes(int64_t N) { return round_up(4 * kMaxRowChunks * N, 256); }
 bool bwd_sizes_ok(int64_t T, int64_t N, int64_t K) {
-    // the products' 256 x 256 tiles are numbered in 32 bits
     return T >= 0 && N >= 1 && K >= 1 && T <= kMaxDim && N <= kMaxDim / 2 && K <= kMaxDim &&
            (T / 256 + 1 + N / 128 + 1) <= INT32_MAX / (K / 256 + 1);
 }

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 
 #include "gemm_launch.h"
@@ -43,54 +44,186 @@ SmallKernel small_kernel(bool gated, bool fp8) {
     return fp8 ? mm_small_kernel<false, true> : mm_small_kernel<false, false>;
 }
 
-// Opt in to the kernels' dynamic shared memory (once per device) and count
-// the CTA pairs of the large kernels that fit at once.
-cudaError_t setup(int *pairs) {
+// Clusters of `csize` CTAs, launched dependent on what precedes them.
+void launch_attributes(cudaLaunchAttribute (&attr)[2], unsigned csize) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = csize;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+}
+
+// Per device: the CTA pairs of the large kernels, and the clusters of 1 ..
+// kMaxSplit small CTAs with one (or two) CTAs' shared memory per SM, that fit
+// at once (SMs of a GPC that cannot complete a cluster stay idle).
+struct Capacity {
+    int pairs = 0;
+    int small[2][kMaxSplit];
+};
+constexpr int kSmSmem = 233472;  // 228 KB
+constexpr int small_budget(int per_sm) { return kSmSmem / per_sm - kSmemReserved; }
+
+template <class Kernel>
+cudaError_t clusters_of(Kernel k, int csize, int threads, int smem, int *n) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    launch_attributes(attr, static_cast<unsigned>(csize));
+    cfg.gridDim = dim3(static_cast<unsigned>(csize), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(n, k, &cfg);
+    return e == cudaSuccess && *n < 1 ? cudaErrorInvalidConfiguration : e;
+}
+
+// Opt in to the kernels' dynamic shared memory and query the capacities, once
+// per device.
+cudaError_t setup(Capacity *out) {
     static std::mutex mu;
-    static int cached[kMaxDevices] = {};
+    static Capacity cached[kMaxDevices];
     int device = 0;
     cudaError_t e = cudaGetDevice(&device);
     if (e != cudaSuccess) return e;
     if (device < 0 || device >= kMaxDevices) return cudaErrorInvalidDevice;
     std::lock_guard<std::mutex> lock(mu);
-    if (cached[device] == 0) {
-        int least = 0;
+    if (cached[device].pairs == 0) {
+        Capacity c;
         for (int k = 0; k < 4; ++k) {
-            LargeKernel lk = large_kernel(k & 1, k & 2);
+            const LargeKernel lk = large_kernel(k & 1, k & 2);
             e = cudaFuncSetAttribute(lk, cudaFuncAttributeMaxDynamicSharedMemorySize, kLargeSmem);
-            if (e != cudaSuccess) return e;
-            e = cudaFuncSetAttribute(small_kernel(k & 1, k & 2),
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
-            if (e != cudaSuccess) return e;
-            cudaLaunchConfig_t cfg = {};
-            cudaLaunchAttribute attr[1];
-            attr[0].id = cudaLaunchAttributeClusterDimension;
-            attr[0].val.clusterDim.x = 2;
-            attr[0].val.clusterDim.y = 1;
-            attr[0].val.clusterDim.z = 1;
-            cfg.gridDim = dim3(2, 1, 1);
-            cfg.blockDim = dim3(kLargeThreads, 1, 1);
-            cfg.dynamicSmemBytes = kLargeSmem;
-            cfg.attrs = attr;
-            cfg.numAttrs = 1;
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(small_kernel(k & 1, k & 2),
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         small_budget(1));
             int n = 0;
-            e = cudaOccupancyMaxActiveClusters(&n, lk, &cfg);
+            if (e == cudaSuccess) e = clusters_of(lk, 2, kLargeThreads, kLargeSmem, &n);
             if (e != cudaSuccess) return e;
-            if (n < 1) return cudaErrorInvalidConfiguration;
-            least = k == 0 ? n : std::min(least, n);
+            c.pairs = k == 0 ? n : std::min(c.pairs, n);
         }
-        cached[device] = least;
+        for (int per_sm = 1; per_sm <= 2; ++per_sm)
+            for (int split = 1; split <= kMaxSplit; ++split) {
+                e = clusters_of(small_kernel(true, false), split, kSmallThreads,
+                                small_budget(per_sm), &c.small[per_sm - 1][split - 1]);
+                if (e != cudaSuccess) return e;
+            }
+        cached[device] = c;
     }
-    *pairs = cached[device];
+    *out = cached[device];
     return cudaSuccess;
 }
 
-}  // namespace
+// How a product is run: pair tiles, or bn tokens x 128 weight rows per CTA
+// with K split over `split` CTAs.
+struct Plan {
+    bool large;
+    int bn, split, stages, per_stage, tmem_cols, smem;
+    double clocks;  // estimate
+};
 
-cudaError_t forward_large(const Fwd &f, cudaStream_t s) {
-    int pairs = 0;
-    cudaError_t e = setup(&pairs);
-    if (e != cudaSuccess) return e;
+// Estimates in SM clocks at 1.9 GHz, fitted to a sweep on GB300 of every bn,
+// split and per_stage over 27 products (T = 1 .. 2000, K = 512 .. 16384, N =
+// 100 .. 12288, both types, linear and gated): the chosen plan is within 2 % of
+// the fastest on average, 11 % at worst.  A stage of a small CTA costs the
+// larger of its MMAs (128 x bn: bn / 2 clocks each at the tensor cores' rate,
+// or the shared-memory reads of both operands) and its way from L2, shared by
+// the CTAs of an SM; it is free again a fetch latency, a transfer and its MMAs
+// later.  The weight comes from HBM at 6.8 TB/s at best.
+constexpr double kHbmBytesPerClock = 3570., kL2BytesPerClock = 70.;
+constexpr double kFetch = 1200., kPerStage = 145., kPerCta = 6600., kSplitSync = 1750.;
+constexpr double kOut = 25., kOutSplit = 34.;   // epilogue, per token of an accumulator
+constexpr double kPairChunk = 670., kPairCta = 7200.;
+
+double hbm_clocks(const Fwd &f) {
+    return static_cast<double>(f.N) * (f.gated ? 2 : 1) * f.K *
+           (f.dtype == VLMCE_E4M3 ? 1 : 2) / kHbmBytesPerClock;
+}
+
+bool small_plan(const Fwd &f, const Capacity &cap, int64_t ty, int split, int per_stage,
+                Plan *out) {
+    const int kw = f.gated ? 2 : 1;
+    const int chunks = chunks_of(f);
+    Plan p = {};
+    p.bn = static_cast<int>(round_up((f.T + ty - 1) / ty, 16));
+    if (p.bn > 256 || split * per_stage > chunks) return false;
+    p.split = split;
+    p.per_stage = per_stage;
+    const int64_t clusters = (f.N + 127) / 128 * ((f.T + p.bn - 1) / p.bn);
+    p.tmem_cols = 32;
+    while (p.tmem_cols < kw * p.bn) p.tmem_cols *= 2;
+    const int per_sm = p.tmem_cols > 256 || clusters <= cap.small[0][split - 1] ? 1 : 2;
+    const double waves = static_cast<double>(clusters) / cap.small[per_sm - 1][split - 1];
+    const double rounds = per_sm == 1 ? std::ceil(waves) : waves > 1. ? waves + 0.3 : 1.;
+    const int stage = per_stage * (kw * kWTileBytes + p.bn * 128);
+    const int steps = ((chunks + split - 1) / split + per_stage - 1) / per_stage;
+    p.stages =
+        std::min({(small_budget(per_sm) - 1024 - kSmallTail) / stage, kMaxSmallStages, steps});
+    if (p.stages < 1) return false;
+    p.smem = std::max({1024 + p.stages * stage + kSmallTail,
+                       p.tmem_cols * kSmemPerTmemCol - kSmemReserved, kSmallSmemMin});
+    const double mma = per_stage * kw * 4 * std::max(p.bn / 2., 32. + p.bn / 4.);
+    const double load = stage / kL2BytesPerClock;
+    const double step =
+        std::max(per_sm * std::max(mma, load), (kFetch + load + mma) / p.stages) + kPerStage;
+    const double main = rounds * steps * step, hbm = hbm_clocks(f);
+    const double epilogue =
+        per_sm * kw * p.bn * (split > 1 ? kOutSplit : kOut) + (split > 1 ? kSplitSync : 0.);
+    p.clocks = std::cbrt(main * main * main + hbm * hbm * hbm) + rounds * (kPerCta + epilogue);
+    *out = p;
+    return true;
+}
+
+Plan choose(const Fwd &f, const Capacity &cap) {
+    Plan best = {};
+    best.large = true;
+    const int64_t tiles =
+        ((f.T + 255) / 256) * (f.gated ? (f.N + 127) / 128 : (f.N + 255) / 256);
+    const double main =
+        static_cast<double>((tiles + cap.pairs - 1) / cap.pairs) * chunks_of(f) * kPairChunk;
+    best.clocks = std::hypot(main, 0.4 * hbm_clocks(f)) + kPairCta;
+    const int64_t t0 = (f.T + 255) / 256;
+    if (t0 > 16) return best;  // enough tokens for the pair tiles
+    for (int64_t ty = t0; ty < t0 + 5; ++ty)
+        for (int split = 1; split <= kMaxSplit; ++split)
+            for (int per_stage = 1; per_stage <= 2; ++per_stage) {
+                Plan p;
+                if (small_plan(f, cap, ty, split, per_stage, &p) && p.clocks < best.clocks)
+                    best = p;
+            }
+    return best;
+}
+
+// choose() for the sizes a host thread met last (a decoder's few layer shapes;
+// the search takes several microseconds).
+Plan plan_of(const Fwd &f, const Capacity &cap) {
+    struct Entry {
+        int64_t T = -1, N, K;
+        int gated, pairs;
+        int32_t dtype;
+        Plan plan;
+    };
+    constexpr int kEntries = 64;
+    static thread_local Entry entries[kEntries];
+    const uint64_t h = static_cast<uint64_t>(f.T) * 0x9E3779B97F4A7C15ull ^
+                       static_cast<uint64_t>(f.N) * 0xC2B2AE3D27D4EB4Full ^
+                       static_cast<uint64_t>(f.K) * 0x165667B19E3779F9ull ^
+                       static_cast<uint64_t>(f.dtype * 2 + f.gated);
+    Entry &e = entries[(h ^ h >> 29) % kEntries];
+    if (e.T != f.T || e.N != f.N || e.K != f.K || e.gated != f.gated || e.dtype != f.dtype ||
+        e.pairs != cap.pairs) {
+        e.plan = choose(f, cap);
+        e.T = f.T;
+        e.N = f.N;
+        e.K = f.K;
+        e.gated = f.gated;
+        e.dtype = f.dtype;
+        e.pairs = cap.pairs;
+    }
+    return e.plan;
+}
+
+cudaError_t forward_large(const Fwd &f, int pairs, cudaStream_t s) {
     CUtensorMap mx, mw;
     const int64_t rows = f.gated ? 2 * f.N : f.N;
     if (!operand_map(&mx, f.x, f.dtype, f.T, f.K, f.x_ld, kHalfRows) ||
@@ -109,53 +242,36 @@ cudaError_t forward_large(const Fwd &f, cudaStream_t s) {
     p.e = f.e;
     p.err = f.err;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    launch_attributes(attr, 2);
     cfg.gridDim = dim3(2 * std::min(p.tiles, pairs), 1, 1);
     cfg.blockDim = dim3(kLargeThreads, 1, 1);
     cfg.dynamicSmemBytes = kLargeSmem;
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, large_kernel(f.gated != 0, f.dtype == VLMCE_E4M3), mx, mw,
                               static_cast<const LargeParams>(p));
 }
 
-cudaError_t forward_small(const Fwd &f, int sm_count, cudaStream_t s) {
-    int pairs = 0;
-    cudaError_t e = setup(&pairs);
-    if (e != cudaSuccess) return e;
+cudaError_t forward_small(const Fwd &f, const Plan &plan, cudaStream_t s) {
     const int kw = f.gated ? 2 : 1;
     SmallParams p = {};
     p.T = static_cast<int>(f.T);
     p.N = static_cast<int>(f.N);
     p.up_row = static_cast<int>(f.N);
     p.chunks = chunks_of(f);
-    const int64_t token_tiles = (f.T + 255) / 256;
-    p.bn = static_cast<int>(round_up((f.T + token_tiles - 1) / token_tiles, 16));
+    p.split = plan.split;
+    p.bn = plan.bn;
+    p.stages = plan.stages;
+    p.per_stage = plan.per_stage;
+    p.tmem_cols = plan.tmem_cols;
     const int64_t ty = (f.T + p.bn - 1) / p.bn;
     const int64_t mt = (f.N + 127) / 128;
-    int cols = 32;
-    while (cols < kw * p.bn) cols *= 2;
-    p.tmem_cols = cols;
-    const int per_sm = cols > 256 ? 1 : 2;
-    // K split over a cluster while the CTAs fit in one wave and each keeps
-    // several chunks of K
-    p.split = 1;
-    while (p.split < kMaxSplit && mt * ty * p.split * 2 <= static_cast<int64_t>(sm_count) * per_sm &&
-           p.chunks >= 8 * p.split)
-        p.split *= 2;
-    const int stage = kw * kWTileBytes + p.bn * 128;
-    const int budget = 233472 / per_sm - kSmemReserved;
-    const int want = (p.chunks + p.split - 1) / p.split;
-    p.stages = std::min({(budget - 1024 - kSmallTail) / stage, kMaxSmallStages, want});
-    const int ring = p.stages * stage;
-    p.red_tokens = std::min(p.bn, ring / (kw * 512) / 16 * 16);
-    int smem = 1024 + ring + kSmallTail;
-    smem = std::max({smem, cols * kSmemPerTmemCol - kSmemReserved, kSmallSmemMin});
+    const int ring = p.stages * p.per_stage * (kw * kWTileBytes + p.bn * 128);
+    p.red_tokens = p.bn;
+    while ((p.red_tokens / 4 + p.split - 1) / p.split * 4 * p.split * kw * 512 > ring)
+        p.red_tokens -= 16;
     p.e = f.e;
     p.err = f.err;
     if (ty > 65535 || mt * p.split > INT32_MAX) return cudaErrorInvalidConfiguration;
@@ -166,26 +282,26 @@ cudaError_t forward_small(const Fwd &f, int sm_count, cudaStream_t s) {
         !operand_map(&mw, f.w, f.dtype, rows, f.K, f.w_ld, 128))
         return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(p.split);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    launch_attributes(attr, static_cast<unsigned>(p.split));
     cfg.gridDim = dim3(static_cast<unsigned>(mt * p.split), static_cast<unsigned>(ty), 1);
     cfg.blockDim = dim3(kSmallThreads, 1, 1);
-    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.dynamicSmemBytes = static_cast<size_t>(plan.smem);
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, small_kernel(f.gated != 0, f.dtype == VLMCE_E4M3), mw, mx,
                               static_cast<const SmallParams>(p));
 }
 
-cudaError_t forward(const Fwd &f, int sm_count, cudaStream_t s) {
-    const int64_t tiles =
-        ((f.T + 255) / 256) * (f.gated ? (f.N + 127) / 128 : (f.N + 255) / 256);
-    if (f.T <= 256 || tiles < sm_count / 2) return forward_small(f, sm_count, s);
-    return forward_large(f, s);
+}  // namespace
+
+cudaError_t forward(const Fwd &f, cudaStream_t s) {
+    Capacity cap;
+    const cudaError_t e = setup(&cap);
+    if (e != cudaSuccess) return e;
+    const Plan plan = plan_of(f, cap);
+    return plan.large ? forward_large(f, cap.pairs, s) : forward_small(f, plan, s);
 }
 
 }  // namespace mm

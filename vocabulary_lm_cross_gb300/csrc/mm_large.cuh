@@ -40,7 +40,9 @@ constexpr int kEpiWarps = 8;
 constexpr int kLargeTmemCols = 512;
 constexpr int kGroupM = 8;
 constexpr int kLargeBars = 2 * kStages + 5;    // full, empty, tmem full x2, tmem empty x2, drain
-constexpr int kLargeSmem = 1024 + kStages * kStageBytes + 8 * kLargeBars + 16;
+constexpr int kLargeTail = 8 * kLargeBars + 16;  // barriers, TMEM slot, abort flag
+constexpr int kStageWords = 32 * 17;             // an epilogue warp's transposing buffer
+constexpr int kLargeSmem = 1024 + kStages * kStageBytes + kLargeTail + kEpiWarps * kStageWords * 4;
 
 struct LargeParams {
     int T, N;          // tokens, outputs
@@ -64,14 +66,19 @@ __device__ __forceinline__ LargeTile large_tile(const LargeParams &p, int t) {
 }
 
 // ---------------------------------------------------------- row segments
-// 32 consecutive 16-bit columns of one row; nv of them exist; vec: bytes an
-// access may use when all 32 exist (32, 16 or 2).
-__device__ __forceinline__ void store32(uint16_t *p, const float (&v)[32], int nv, int vec,
-                                        bool f16) {
-    if (nv == 32 && vec >= 16) {
-        uint32_t u[16];
+// A warp's 32 rows x 32 consecutive 16-bit columns, one row per lane, `nr`
+// rows and `nc` columns of which exist.  vec: bytes an access may use where all
+// 32 columns exist (32, 16 or 2).  Rows without 16-byte alignment, and the last
+// columns, pass through `stage` (the warp's 32 x 17 words of shared memory),
+// so that a warp's accesses still cover consecutive addresses of a row.
+__device__ __forceinline__ void store_seg(uint16_t *base, int64_t ld, const float (&v)[32], int nr,
+                                          int nc, int vec, bool f16, uint32_t *stage, int lane) {
+    uint32_t u[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) u[j] = act::pack16x2(v[2 * j], v[2 * j + 1], f16);
+    for (int j = 0; j < 16; ++j) u[j] = act::pack16x2(v[2 * j], v[2 * j + 1], f16);
+    if (nc == 32 && vec >= 16) {
+        if (lane >= nr) return;
+        uint16_t *p = base + lane * ld;
         if (vec >= 32) {
             ptx::st_global_v8(p, u[0], u[1], u[2], u[3], u[4], u[5], u[6], u[7]);
             ptx::st_global_v8(p + 16, u[8], u[9], u[10], u[11], u[12], u[13], u[14], u[15]);
@@ -81,65 +88,90 @@ __device__ __forceinline__ void store32(uint16_t *p, const float (&v)[32], int n
                 *reinterpret_cast<uint4 *>(p + 8 * j) =
                     make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
         }
-    } else {
+        return;
+    }
+    __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (j < nv) p[j] = act::to16(v[j], f16);
+    for (int j = 0; j < 16; ++j) stage[lane * 17 + j] = u[j];
+    __syncwarp();
+    const uint16_t *s16 = reinterpret_cast<const uint16_t *>(stage);
+    if (lane < nc) {
+#pragma unroll 8
+        for (int r = 0; r < nr; ++r) base[r * ld + lane] = s16[r * 34 + lane];
     }
 }
-__device__ __forceinline__ void add32(const uint16_t *p, float (&v)[32], int nv, int vec,
-                                      bool f16) {
-    if (nv == 32 && vec >= 16) {
-        uint4 u[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) u[j] = *reinterpret_cast<const uint4 *>(p + 8 * j);
+__device__ __forceinline__ void add_seg(const uint16_t *base, int64_t ld, float (&v)[32], int nr,
+                                        int nc, int vec, bool f16, uint32_t *stage, int lane) {
+    uint32_t u[16];
+    if (nc == 32 && vec >= 16) {
+        if (lane >= nr) return;
+        const uint16_t *p = base + lane * ld;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint32_t w[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float a, b;
-                act::unpack16x2(w[i], a, b, f16);
-                v[8 * j + 2 * i] += a;
-                v[8 * j + 2 * i + 1] += b;
-            }
+            const uint4 q = *reinterpret_cast<const uint4 *>(p + 8 * j);
+            u[4 * j] = q.x;
+            u[4 * j + 1] = q.y;
+            u[4 * j + 2] = q.z;
+            u[4 * j + 3] = q.w;
         }
     } else {
+        uint16_t *s16 = reinterpret_cast<uint16_t *>(stage);
+        __syncwarp();
+        if (lane < nc) {
+#pragma unroll 8
+            for (int r = 0; r < nr; ++r) s16[r * 34 + lane] = base[r * ld + lane];
+        }
+        __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (j < nv) v[j] += act::from16(p[j], f16);
+        for (int j = 0; j < 16; ++j) u[j] = stage[lane * 17 + j];
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        float a, b;
+        act::unpack16x2(u[j], a, b, f16);
+        v[2 * j] += a;
+        v[2 * j + 1] += b;
     }
 }
 
-__device__ __forceinline__ void scale32(float (&v)[32], float xs, const float *ws, int nv) {
+__device__ __forceinline__ void scale32(float (&v)[32], float xs, const float *ws, int nc) {
 #pragma unroll
     for (int j = 0; j < 32; ++j)
-        if (j < nv) v[j] *= xs * ws[j];
+        if (j < nc) v[j] *= xs * ws[j];
 }
 
-// Epilogue of 32 consecutive outputs of one token (Epi in mm_types.h).
-__device__ __forceinline__ void linear32(const LargeParams &p, const uint32_t (&r)[32], int row,
-                                         int col, int nv, float xs) {
+// Epilogue of a warp's 32 tokens from row0 x 32 outputs from col (Epi in
+// mm_types.h), one token per lane.
+__device__ __forceinline__ void linear_seg(const LargeParams &p, const uint32_t (&r)[32], int64_t row0,
+                                           int col, float xs, uint32_t *stage, int lane) {
     const Epi &e = p.e;
     const bool f16 = e.f16 != 0;
+    const int nr = static_cast<int>(min(int64_t{32}, p.T - row0)), nc = min(32, p.N - col);
     float v[32];
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-    if (e.ws) scale32(v, xs, e.ws + col, nv);
-    if (e.bias) add32(e.bias + col, v, nv, 2, f16);
+    if (e.ws) scale32(v, xs, e.ws + col, nc);
+    if (e.bias) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (j < nc) v[j] += act::from16(e.bias[col + j], f16);
+    }
     if (e.preact)
-        store32(e.preact + static_cast<int64_t>(row) * e.preact_ld + col, v, nv, e.preact_vec, f16);
+        store_seg(e.preact + row0 * e.preact_ld + col, e.preact_ld, v, nr, nc, e.preact_vec, f16,
+                  stage, lane);
     act::apply_n(v, e.act);
     if (e.residual)
-        add32(e.residual + static_cast<int64_t>(row) * e.residual_ld + col, v, nv, e.residual_vec,
-              f16);
-    store32(e.y + static_cast<int64_t>(row) * e.y_ld + col, v, nv, e.y_vec, f16);
+        add_seg(e.residual + row0 * e.residual_ld + col, e.residual_ld, v, nr, nc, e.residual_vec,
+                f16, stage, lane);
+    store_seg(e.y + row0 * e.y_ld + col, e.y_ld, v, nr, nc, e.y_vec, f16, stage, lane);
 }
-__device__ __forceinline__ void gated32(const LargeParams &p, const uint32_t (&rg)[32],
-                                        const uint32_t (&ru)[32], int row, int col, int nv,
-                                        float xs) {
+__device__ __forceinline__ void gated_seg(const LargeParams &p, const uint32_t (&rg)[32],
+                                          const uint32_t (&ru)[32], int64_t row0, int col,
+                                          float xs,
+                                          uint32_t *stage, int lane) {
     const Epi &e = p.e;
     const bool f16 = e.f16 != 0;
+    const int nr = static_cast<int>(min(int64_t{32}, p.T - row0)), nc = min(32, p.N - col);
     float g[32], u[32];
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
@@ -147,18 +179,18 @@ __device__ __forceinline__ void gated32(const LargeParams &p, const uint32_t (&r
         u[j] = __uint_as_float(ru[j]);
     }
     if (e.ws) {
-        scale32(g, xs, e.ws + col, nv);
-        scale32(u, xs, e.ws + p.up_row + col, nv);
+        scale32(g, xs, e.ws + col, nc);
+        scale32(u, xs, e.ws + p.up_row + col, nc);
     }
     if (e.preact) {
-        uint16_t *z = e.preact + static_cast<int64_t>(row) * e.preact_ld + col;
-        store32(z, g, nv, e.preact_vec, f16);
-        store32(z + p.N, u, nv, e.preact_up_vec, f16);
+        uint16_t *z = e.preact + row0 * e.preact_ld + col;
+        store_seg(z, e.preact_ld, g, nr, nc, e.preact_vec, f16, stage, lane);
+        store_seg(z + p.N, e.preact_ld, u, nr, nc, e.preact_up_vec, f16, stage, lane);
     }
     act::apply_n(g, e.act);
 #pragma unroll
     for (int j = 0; j < 32; ++j) g[j] *= u[j];
-    store32(e.y + static_cast<int64_t>(row) * e.y_ld + col, g, nv, e.y_vec, f16);
+    store_seg(e.y + row0 * e.y_ld + col, e.y_ld, g, nr, nc, e.y_vec, f16, stage, lane);
 }
 
 template <bool GATED, bool FP8>
@@ -209,6 +241,10 @@ __global__ void __launch_bounds__(kLargeThreads, 1)
     ptx::cluster_sync_any();  // barrier inits and the TMEM address visible to the cluster
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
+    // TMEM is held: the next kernel of the stream may set itself up; this one
+    // waits for its predecessor's results before it touches global memory
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
     constexpr int kElts = FP8 ? 128 : 64;  // K elements of a 128-byte chunk
 
     if (warp == 0) {
@@ -282,7 +318,8 @@ __global__ void __launch_bounds__(kLargeThreads, 1)
         }
     } else {
         const int q = warp & 3, half = (warp - 2) >> 2;
-        const int rl = static_cast<int>(prank) * kHalfRows + q * 32 + lane;
+        uint32_t *stage = reinterpret_cast<uint32_t *>(smem + kStages * kStageBytes + kLargeTail) +
+                          (warp - 2) * kStageWords;
         const uint32_t tempty_leader = ptx::mapa(tempty(0), 0);
         const Epi &e = p.e;
         int it = 0;
@@ -291,9 +328,8 @@ __global__ void __launch_bounds__(kLargeThreads, 1)
             const int b = it & 1;
             wait_bar(tfull(b), (it >> 1) & 1, abort, p.err);
             tc::fence_after_sync();
-            const int row = tl.m0 + rl;
-            const bool row_ok = row < p.T;
-            const float xs = e.xs && row_ok ? e.xs[row] : 1.f;
+            const int64_t row0 = tl.m0 + kHalfRows * static_cast<int>(prank) + q * 32;
+            const float xs = e.xs && row0 + lane < p.T ? e.xs[row0 + lane] : 1.f;
             const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * 256;
             if constexpr (GATED) {
 #pragma unroll 1
@@ -303,8 +339,8 @@ __global__ void __launch_bounds__(kLargeThreads, 1)
                     tc::tmem_ld32(tbase + 128 + 32 * c, ru);
                     tc::tmem_ld_wait();
                     const int col = tl.n0 + 32 * c;
-                    const int nv = min(32, p.N - col);
-                    if (nv > 0 && row_ok) gated32(p, rg, ru, row, col, nv, xs);
+                    if (col < p.N && row0 < p.T)
+                        gated_seg(p, rg, ru, row0, col, xs, stage, lane);
                     __syncwarp();
                 }
             } else {
@@ -314,8 +350,7 @@ __global__ void __launch_bounds__(kLargeThreads, 1)
                     tc::tmem_ld32(tbase + 32 * c, r);
                     tc::tmem_ld_wait();
                     const int col = tl.n0 + 32 * c;
-                    const int nv = min(32, p.N - col);
-                    if (nv > 0 && row_ok) linear32(p, r, row, col, nv, xs);
+                    if (col < p.N && row0 < p.T) linear_seg(p, r, row0, col, xs, stage, lane);
                     __syncwarp();
                 }
             }

@@ -9,9 +9,11 @@
 // K of the weight rows and of the tokens, 128-byte swizzle) is filled by TMA.
 //
 // Where the weight has too few row tiles to occupy every SM, `split` CTAs of
-// a cluster share a tile, each on its own part of K; their fp32 accumulators
-// meet in shared memory and are added in rank order (fixed, so the result does
-// not depend on timing).
+// a cluster share a tile, each on its own part of K.  Each CTA owns a run of
+// the tile's tokens: the others push their fp32 accumulators of those tokens
+// into its shared memory (four tokens of a row per 16-byte store; stores do
+// not wait for the other SM), and it adds them in rank order (fixed, so the
+// result does not depend on timing).
 //
 // Two CTAs of this kernel, or one and another kernel's, may share an SM.  TMEM
 // allocation blocks while columns are short, and a blocked CTA of a cluster
@@ -19,8 +21,9 @@
 // allocates TMEM takes at least the same share of the SM's shared memory
 // (kSmemPerTmemCol per column), so that TMEM never runs out first.
 //
-// CTA = 6 warps: warp 0 TMA producer, warp 1 TMEM and MMA issuer, warps 2-5
-// epilogue (one weight row per thread).
+// CTA = 10 warps: warp 0 TMA producer, warp 1 TMEM and MMA issuer, warps 2-9
+// epilogue (one weight row per thread, two threads on alternate groups of
+// tokens).
 #pragma once
 
 #include <cuda.h>
@@ -34,7 +37,7 @@
 namespace vlmce {
 namespace mm {
 
-constexpr int kSmallThreads = 192;
+constexpr int kSmallThreads = 320;
 constexpr int kWTileBytes = 128 * 128;  // 128 weight rows x 128 bytes of K
 constexpr int kMaxSmallStages = 12;
 constexpr int kMaxSplit = 8;
@@ -53,37 +56,78 @@ struct SmallParams {
     int split;        // CTAs of a cluster sharing a tile's K
     int bn;           // tokens per tile (multiple of 16)
     int stages;
+    int per_stage;    // chunks of a stage
     int tmem_cols;
     int red_tokens;   // tokens reduced at a time when split > 1 (multiple of 16)
     Epi e;
     int *err;
 };
 
-// One output: token t, column n of acc (linear) or of (g, u) (gated).
-__device__ __forceinline__ void small_linear(const SmallParams &p, float v, int t, int n) {
+// The epilogue of NJ tokens t of one weight row n (Epi in mm_types.h); tokens
+// from `count` on do not exist.  The row's factors are loaded once per thread.
+struct RowFactors {
+    float ws, ws_up, bias;
+};
+template <bool GATED>
+__device__ __forceinline__ RowFactors row_factors(const SmallParams &p, int n) {
     const Epi &e = p.e;
-    const bool f16 = e.f16 != 0;
-    if (e.ws) v *= e.xs[t] * e.ws[n];
-    if (e.bias) v += act::from16(e.bias[n], f16);
-    if (e.preact) e.preact[static_cast<int64_t>(t) * e.preact_ld + n] = act::to16(v, f16);
-    v = act::apply(v, e.act);
-    if (e.residual) v += act::from16(e.residual[static_cast<int64_t>(t) * e.residual_ld + n], f16);
-    e.y[static_cast<int64_t>(t) * e.y_ld + n] = act::to16(v, f16);
-}
-__device__ __forceinline__ void small_gated(const SmallParams &p, float g, float u, int t, int n) {
-    const Epi &e = p.e;
-    const bool f16 = e.f16 != 0;
+    RowFactors f = {1.f, 1.f, 0.f};
     if (e.ws) {
-        const float xs = e.xs[t];
-        g *= xs * e.ws[n];
-        u *= xs * e.ws[p.up_row + n];
+        f.ws = e.ws[n];
+        if constexpr (GATED) f.ws_up = e.ws[p.up_row + n];
+    }
+    if constexpr (!GATED)
+        if (e.bias) f.bias = act::from16(e.bias[n], e.f16 != 0);
+    return f;
+}
+template <bool GATED, int NJ>
+__device__ __forceinline__ void small_epilogue(const SmallParams &p, const RowFactors &f,
+                                               float (&g)[NJ], float (&u)[NJ], const int (&t)[NJ],
+                                               int count, int n) {
+    const Epi &e = p.e;
+    const bool f16 = e.f16 != 0;
+    float r[NJ];
+    if constexpr (!GATED) {
+        if (e.residual) {
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+                if (j < count)
+                    r[j] = act::from16(e.residual[t[j] * e.residual_ld + n], f16);
+        }
+    }
+    if (e.ws) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+            if (j < count) {
+                const float xs = e.xs[t[j]];
+                g[j] *= xs * f.ws;
+                if constexpr (GATED) u[j] *= xs * f.ws_up;
+            }
+    }
+    if constexpr (!GATED) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) g[j] += f.bias;
     }
     if (e.preact) {
-        uint16_t *z = e.preact + static_cast<int64_t>(t) * e.preact_ld + n;
-        z[0] = act::to16(g, f16);
-        z[p.N] = act::to16(u, f16);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+            if (j < count) {
+                uint16_t *z = e.preact + t[j] * e.preact_ld + n;
+                z[0] = act::to16(g[j], f16);
+                if constexpr (GATED) z[p.N] = act::to16(u[j], f16);
+            }
     }
-    e.y[static_cast<int64_t>(t) * e.y_ld + n] = act::to16(act::apply(g, e.act) * u, f16);
+    act::apply_n(g, e.act);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+        if constexpr (GATED)
+            g[j] *= u[j];
+        else if (e.residual)
+            g[j] += r[j];
+    }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+        if (j < count) e.y[t[j] * e.y_ld + n] = act::to16(g[j], f16);
 }
 
 template <bool GATED, bool FP8>
@@ -95,7 +139,8 @@ __global__ void __launch_bounds__(kSmallThreads)
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     constexpr int kW = GATED ? 2 : 1;
     constexpr int kElts = FP8 ? 128 : 64;
-    const int stage_bytes = kW * kWTileBytes + p.bn * 128;
+    const int chunk_bytes = kW * kWTileBytes + p.bn * 128;
+    const int stage_bytes = p.per_stage * chunk_bytes;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + p.stages * stage_bytes);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * kMaxSmallStages + 2);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -134,26 +179,42 @@ __global__ void __launch_bounds__(kSmallThreads)
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
+    // TMEM is held: the next kernel of the stream may set itself up; this one
+    // waits for its predecessor's results before it touches global memory
+    // (the weight's first tiles may already come into L2)
+    ptx::griddep_launch_dependents();
+    if (warp == 0 && lane == 0) {
+        const int ahead = min(c1, c0 + p.stages * p.per_stage);
+        for (int c = c0; c < ahead; ++c) {
+            tc::tma_prefetch_2d(&mw, c * kElts, n0);
+            if constexpr (GATED) tc::tma_prefetch_2d(&mw, c * kElts, p.up_row + n0);
+        }
+    }
+    ptx::griddep_wait();
 
     if (warp == 0) {
         if (lane == 0) {
             int s = 0;
             uint32_t ph = 0;
-            for (int c = c0; c < c1; ++c) {
+            for (int c = c0; c < c1; c += p.per_stage) {
                 wait_bar(empty(s), ph ^ 1, abort, p.err);
-                ptx::mbar_arrive_expect_tx(full(s), static_cast<uint32_t>(stage_bytes));
-                const uint32_t sa = ring + s * stage_bytes;
-                tc::tma_load_2d(sa, &mw, c * kElts, n0, full(s));
-                if constexpr (GATED)
-                    tc::tma_load_2d(sa + kWTileBytes, &mw, c * kElts, p.up_row + n0, full(s));
-                tc::tma_load_2d(sa + kW * kWTileBytes, &mx, c * kElts, t0, full(s));
+                const int n = min(p.per_stage, c1 - c);
+                ptx::mbar_arrive_expect_tx(full(s), static_cast<uint32_t>(n * chunk_bytes));
+                for (int i = 0; i < n; ++i) {
+                    const uint32_t sa = ring + s * stage_bytes + i * chunk_bytes;
+                    const int k = (c + i) * kElts;
+                    tc::tma_load_2d(sa, &mw, k, n0, full(s));
+                    if constexpr (GATED)
+                        tc::tma_load_2d(sa + kWTileBytes, &mw, k, p.up_row + n0, full(s));
+                    tc::tma_load_2d(sa + kW * kWTileBytes, &mx, k, t0, full(s));
+                }
                 if (++s == p.stages) {
                     s = 0;
                     ph ^= 1;
                 }
             }
             // every copy has landed once the last full phase of each stage completed
-            const int issued = c1 - c0;
+            const int issued = (c1 - c0 + p.per_stage - 1) / p.per_stage;
             for (int i = 0; i < p.stages && i < issued; ++i) {
                 const int k = issued - 1 - i;
                 drain_bar(full(k % p.stages), static_cast<uint32_t>((k / p.stages) & 1), p.err);
@@ -164,23 +225,27 @@ __global__ void __launch_bounds__(kSmallThreads)
             const uint32_t idesc = tc::idesc_bf16_f32(128, p.bn, false, false, FP8 || p.e.f16);
             int s = 0;
             uint32_t ph = 0;
-            for (int c = c0; c < c1; ++c) {
+            for (int c = c0; c < c1; c += p.per_stage) {
                 wait_bar(full(s), ph, abort, p.err);
                 tc::fence_after_sync();
-                const uint32_t sa = ring + s * stage_bytes;
+                const int n = min(p.per_stage, c1 - c);
+                for (int i = 0; i < n; ++i) {
+                    const uint32_t sa = ring + s * stage_bytes + i * chunk_bytes;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint64_t xd =
-                        tc::smem_desc_sw128(sa + kW * kWTileBytes + 32 * k, 16, 1024);
+                    for (int k = 0; k < 4; ++k) {
+                        const uint64_t xd =
+                            tc::smem_desc_sw128(sa + kW * kWTileBytes + 32 * k, 16, 1024);
 #pragma unroll
-                    for (int w = 0; w < kW; ++w) {
-                        const uint64_t wd =
-                            tc::smem_desc_sw128(sa + w * kWTileBytes + 32 * k, 16, 1024);
-                        const uint32_t d = tmem + static_cast<uint32_t>(w * p.bn);
-                        if constexpr (FP8)
-                            tc::mma_f8(d, wd, xd, idesc, c > c0 || k != 0);
-                        else
-                            tc::mma_bf16(d, wd, xd, idesc, c > c0 || k != 0);
+                        for (int w = 0; w < kW; ++w) {
+                            const uint64_t wd =
+                                tc::smem_desc_sw128(sa + w * kWTileBytes + 32 * k, 16, 1024);
+                            const uint32_t d = tmem + static_cast<uint32_t>(w * p.bn);
+                            const uint32_t add = c + i > c0 || k != 0;
+                            if constexpr (FP8)
+                                tc::mma_f8(d, wd, xd, idesc, add);
+                            else
+                                tc::mma_bf16(d, wd, xd, idesc, add);
+                        }
                     }
                 }
                 tc::mma_commit(empty(s));
@@ -197,76 +262,104 @@ __global__ void __launch_bounds__(kSmallThreads)
         tc::fence_after_sync();
     }
 
-    const int q = warp & 3;  // TMEM subpartition of an epilogue warp
+    const int q = warp & 3;            // TMEM subpartition of an epilogue warp
+    const int half = (warp - 2) >> 2;  // which of the subpartition's two warps
     const int row = q * 32 + lane;
+    const bool row_ok = n0 + row < p.N;
     const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    constexpr int NJ = 8;
     if (p.split == 1) {
         if (warp >= 2) {
-            const bool row_ok = n0 + row < p.N;
+            RowFactors f = {1.f, 1.f, 0.f};
+            if (row_ok) f = row_factors<GATED>(p, n0 + row);
 #pragma unroll 1
-            for (int j0 = 0; j0 < nt; j0 += 16) {
+            for (int j0 = 16 * half; j0 < nt; j0 += 32) {
                 uint32_t a[16], b[16];
                 tc::tmem_ld16(tbase + j0, a);
                 if constexpr (GATED) tc::tmem_ld16(tbase + p.bn + j0, b);
                 tc::tmem_ld_wait();
                 if (row_ok) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (j0 + j < nt) {
-                            if constexpr (GATED)
-                                small_gated(p, __uint_as_float(a[j]), __uint_as_float(b[j]),
-                                            t0 + j0 + j, n0 + row);
-                            else
-                                small_linear(p, __uint_as_float(a[j]), t0 + j0 + j, n0 + row);
+                    for (int h = 0; h < 16; h += NJ) {
+                        float g[NJ], u[NJ];
+                        int t[NJ];
+#pragma unroll
+                        for (int j = 0; j < NJ; ++j) {
+                            g[j] = __uint_as_float(a[h + j]);
+                            u[j] = GATED ? __uint_as_float(b[h + j]) : 0.f;
+                            t[j] = t0 + j0 + h + j;
                         }
+                        if (j0 + h < nt)
+                            small_epilogue<GATED, NJ>(p, f, g, u, t, nt - j0 - h, n0 + row);
+                    }
                 }
                 __syncwarp();
             }
         }
     } else {
-        // the ring is free (every copy landed, every MMA completed): it holds
-        // this CTA's accumulators as [kW][token][128 rows], red_tokens at a time
-        __syncthreads();
-        float *part = reinterpret_cast<float *>(smem);
-        const uint32_t part_s = ptx::smem_addr(part);
-        const int plane = p.red_tokens * 128;
+        // Every CTA's ring is free after the first barrier (copies landed, MMAs
+        // completed).  It then holds, for this CTA's run of `own` tokens of a block
+        // of red_tokens, the accumulators [from][kW][token / 4][128 rows][4].
+        const uint32_t part = ptx::smem_addr(smem);
+        const int own = (p.red_tokens / 4 + p.split - 1) / p.split * 4;
+        const int plane = own * 128;  // floats of one accumulator of one sender
+        RowFactors f = {1.f, 1.f, 0.f};
+        if (warp >= 2 && row_ok) f = row_factors<GATED>(p, n0 + row);
 #pragma unroll 1
         for (int jb = 0; jb < nt; jb += p.red_tokens) {
+            ptx::cluster_sync_any();
             const int je = min(p.red_tokens, nt - jb);
             if (warp >= 2) {
 #pragma unroll 1
-                for (int j0 = 0; j0 < je; j0 += 16) {
+                for (int j0 = 16 * half; j0 < je; j0 += 32) {
+                    uint32_t a[16], b[16];
+                    tc::tmem_ld16(tbase + jb + j0, a);
+                    if constexpr (GATED) tc::tmem_ld16(tbase + p.bn + jb + j0, b);
+                    tc::tmem_ld_wait();
 #pragma unroll
-                    for (int w = 0; w < kW; ++w) {
-                        uint32_t a[16];
-                        tc::tmem_ld16(tbase + w * p.bn + jb + j0, a);
-                        tc::tmem_ld_wait();
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            part[w * plane + (j0 + j) * 128 + row] = __uint_as_float(a[j]);
+                    for (int j = 0; j < 16; j += 4) {
+                        if (j0 + j < je) {
+                            const int to = (j0 + j) / own, i = (j0 + j) - to * own;
+                            const uint32_t dst = ptx::mapa(
+                                part + 4u * (rank * kW * plane + i * 128 + 4 * row), to);
+                            ptx::st_dsmem_v4(dst, make_uint4(a[j], a[j + 1], a[j + 2], a[j + 3]));
+                            if constexpr (GATED)
+                                ptx::st_dsmem_v4(dst + 4u * plane, make_uint4(b[j], b[j + 1],
+                                                                              b[j + 2], b[j + 3]));
+                        }
                     }
                 }
             }
             ptx::cluster_sync_any();
-            if (warp >= 2 && n0 + row < p.N) {
+            if (warp >= 2 && row_ok) {
+                const int mine = min(own, je - rank * own);
+                const float *src = reinterpret_cast<const float *>(smem) + 4 * row;
 #pragma unroll 1
-                for (int j = rank; j < je; j += p.split) {
-                    float v[kW];
+                for (int i0 = 4 * half; i0 < mine; i0 += 8) {
+                    float g[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
+                    int t[4];
 #pragma unroll
-                    for (int w = 0; w < kW; ++w) v[w] = 0.f;
-#pragma unroll 1
+                    for (int j = 0; j < 4; ++j) t[j] = t0 + jb + rank * own + i0 + j;
+#pragma unroll 2
                     for (int r = 0; r < p.split; ++r) {
-                        const uint32_t src = ptx::mapa(part_s + 4u * (j * 128 + row), r);
-#pragma unroll
-                        for (int w = 0; w < kW; ++w) v[w] += ptx::ld_dsmem_f32(src + 4u * w * plane);
+                        const float4 v = *reinterpret_cast<const float4 *>(
+                            src + r * kW * plane + i0 * 128);
+                        g[0] += v.x;
+                        g[1] += v.y;
+                        g[2] += v.z;
+                        g[3] += v.w;
+                        if constexpr (GATED) {
+                            const float4 w = *reinterpret_cast<const float4 *>(
+                                src + (r * kW + 1) * plane + i0 * 128);
+                            u[0] += w.x;
+                            u[1] += w.y;
+                            u[2] += w.z;
+                            u[3] += w.w;
+                        }
                     }
-                    if constexpr (GATED)
-                        small_gated(p, v[0], v[kW - 1], t0 + jb + j, n0 + row);
-                    else
-                        small_linear(p, v[0], t0 + jb + j, n0 + row);
+                    small_epilogue<GATED, 4>(p, f, g, u, t, mine - i0, n0 + row);
                 }
             }
-            ptx::cluster_sync_any();  // the peers have read this CTA's part
         }
     }
     tc::fence_before_sync();

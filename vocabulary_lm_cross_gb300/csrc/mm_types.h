@@ -45,7 +45,7 @@ struct Fwd {
 };
 
 // Enqueue it (T, N, K >= 1); the kernel is chosen by the sizes.
-cudaError_t forward(const Fwd &f, int sm_count, cudaStream_t s);
+cudaError_t forward(const Fwd &f, cudaStream_t s);
 
 }  // namespace mm
 }  // namespace vlmce

@@ -114,28 +114,30 @@ __device__ __forceinline__ void load_w(const void *w, bool f32, int64_t i, float
     for (int j = 0; j < E; ++j) v[j] += offset;
 }
 
-// Sum of a and maximum of m over the block, in every thread.  sh: [2][32].
-__device__ __forceinline__ void block_sum_max(float &a, float &m, float (*sh)[32]) {
+// Sum of a (and, with MAX, the maximum of m >= 0) over the block, in every
+// thread.  sh: [2][32].
+template <bool MAX>
+__device__ __forceinline__ void warp_sum_max(float &a, float &m) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
         a += __shfl_xor_sync(0xffffffffu, a, off);
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        if constexpr (MAX) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
     }
+}
+template <bool MAX>
+__device__ __forceinline__ void block_sum_max(float &a, float &m, float (*sh)[32]) {
+    warp_sum_max<MAX>(a, m);
     const int warps = blockDim.x >> 5;
     if (warps == 1) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (lane == 0) {
         sh[0][warp] = a;
-        sh[1][warp] = m;
+        if constexpr (MAX) sh[1][warp] = m;
     }
     __syncthreads();
     a = lane < warps ? sh[0][lane] : 0.f;
-    m = lane < warps ? sh[1][lane] : 0.f;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, off);
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    }
+    if constexpr (MAX) m = lane < warps ? sh[1][lane] : 0.f;
+    warp_sum_max<MAX>(a, m);
 }
 
 // ------------------------------------------------------------ forward
@@ -156,6 +158,8 @@ struct FwdParams {
 template <int DT, int E, int NG, bool QUANT>
 __global__ void __launch_bounds__(1024) fwd_kernel(const FwdParams p) {
     __shared__ float sh[2][32];
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
     const int64_t row = blockIdx.x;
     const unsigned char *x = p.x + row * p.x_ld;
     const unsigned char *res = p.residual ? p.residual + row * p.residual_ld : nullptr;
@@ -201,7 +205,7 @@ __global__ void __launch_bounds__(1024) fwd_kernel(const FwdParams p) {
             fold(i, v[0]);
         }
     }
-    block_sum_max(ss, mx, sh);
+    block_sum_max<QUANT>(ss, mx, sh);
     const float rstd = __frsqrt_rn(ss / static_cast<float>(p.H) + p.eps);
     mx = fmaxf(mx, 1e-30f);
     if (threadIdx.x == 0) {
@@ -235,6 +239,96 @@ __global__ void __launch_bounds__(1024) fwd_kernel(const FwdParams p) {
     }
 }
 
+// Many rows: CTAs stay and take rows blockIdx.x, + gridDim.x, ...  A thread owns
+// the same kOwn granules of every row, with their weights in registers, and
+// keeps the granules of the next kAhead - 1 rows on their way into its own slots
+// of shared memory, so loads never wait for a row's reduction and stores.  At
+// least two CTAs share an SM: one works while the other meets at its barrier.
+constexpr int kOwn = 2;
+constexpr int kRingThreads = 512;  // most threads of a CTA
+constexpr int kFwdAhead = 3, kBwdAhead = 2;
+
+template <int DT, bool QUANT>
+__global__ void __launch_bounds__(kRingThreads, 2) fwd_ring_kernel(const FwdParams p) {
+    constexpr int E = Elt<DT>::kPer16;
+    extern __shared__ __align__(16) unsigned char ring[];  // [kFwdAhead][2][kOwn][threads][16]
+    __shared__ float sh[2][2][32];
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    int64_t at[kOwn];
+    bool in[kOwn];
+    float w[kOwn][E];
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) {
+        at[k] = static_cast<int64_t>(k * blockDim.x + threadIdx.x) * E;
+        in[k] = at[k] < p.H;
+        if (in[k]) load_w<DT, E>(p.weight, p.w_f32 != 0, at[k], p.offset, w[k]);
+    }
+    auto slot = [&](int s, int which, int k) {
+        return ring + 16 * (((s * 2 + which) * kOwn + k) * blockDim.x + threadIdx.x);
+    };
+    auto fetch = [&](int64_t row, int s) {
+        if (row < p.T) {
+#pragma unroll
+            for (int k = 0; k < kOwn; ++k)
+                if (in[k]) {
+                    const int64_t off = at[k] * Elt<DT>::kBytes;
+                    ptx::cp_async16(ptx::smem_addr(slot(s, 0, k)), p.x + row * p.x_ld + off);
+                    if (p.residual)
+                        ptx::cp_async16(ptx::smem_addr(slot(s, 1, k)),
+                                        p.residual + row * p.residual_ld + off);
+                }
+        }
+        ptx::cp_async_commit();
+    };
+    const int64_t step = gridDim.x;
+    for (int n = 0; n < kFwdAhead - 1; ++n) fetch(blockIdx.x + n * step, n);
+    int s = 0, flip = 0;
+    for (int64_t row = blockIdx.x; row < p.T; row += step, flip ^= 1) {
+        fetch(row + (kFwdAhead - 1) * step, s == 0 ? kFwdAhead - 1 : s - 1);
+        ptx::cp_async_wait<kFwdAhead - 1>();
+        float v[kOwn][E];
+        float ss = 0.f, mx = 0.f;
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k)
+            if (in[k]) {
+                load_e<DT, E>(slot(s, 0, k), 0, v[k]);
+                if (p.residual) {
+                    float r[E];
+                    load_e<DT, E>(slot(s, 1, k), 0, r);
+#pragma unroll
+                    for (int j = 0; j < E; ++j) v[k][j] += r[j];
+                }
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    ss = fmaf(v[k][j], v[k][j], ss);
+                    if constexpr (QUANT) mx = fmaxf(mx, fabsf(v[k][j] * w[k][j]));
+                }
+                if (p.sum) store_e<DT, E>(p.sum + row * p.sum_ld, at[k], v[k]);
+            }
+        block_sum_max<QUANT>(ss, mx, sh[flip]);  // two buffers: one barrier a row
+        const float rstd = __frsqrt_rn(ss / static_cast<float>(p.H) + p.eps);
+        mx = fmaxf(mx, 1e-30f);
+        if (threadIdx.x == 0) {
+            if (p.rstd) p.rstd[row] = rstd;
+            if constexpr (QUANT) p.scale[row] = rstd * mx / 448.f;
+        }
+        const float mul = QUANT ? 448.f / mx : rstd;
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k)
+            if (in[k]) {
+#pragma unroll
+                for (int j = 0; j < E; ++j)
+                    v[k][j] = QUANT ? v[k][j] * w[k][j] * mul : v[k][j] * mul * w[k][j];
+                if constexpr (QUANT)
+                    store_e4m3<E>(p.y + row * p.y_ld, at[k], v[k]);
+                else
+                    store_e<DT, E>(p.y + row * p.y_ld, at[k], v[k]);
+            }
+        if (++s == kFwdAhead) s = 0;
+    }
+}
+
 // ------------------------------------------------------------ backward
 struct BwdParams {
     const unsigned char *dy, *x, *dres;
@@ -254,6 +348,8 @@ struct BwdParams {
 template <int DT, int E, int NG>
 __global__ void __launch_bounds__(1024) bwd_kernel(const BwdParams p) {
     __shared__ float sh[2][2][32];
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
     const int64_t step = static_cast<int64_t>(blockDim.x) * E;
     const int64_t i0 = static_cast<int64_t>(threadIdx.x) * E;
     float dw[NG][E];
@@ -290,7 +386,7 @@ __global__ void __launch_bounds__(1024) bwd_kernel(const BwdParams p) {
                 }
             }
         }
-        block_sum_max(c, unused, sh[flip]);  // two buffers: one barrier a row
+        block_sum_max<false>(c, unused, sh[flip]);  // two buffers: one barrier a row
         c /= static_cast<float>(p.H);
 #pragma unroll
         for (int k = 0; k < NG; ++k) {
@@ -316,11 +412,106 @@ __global__ void __launch_bounds__(1024) bwd_kernel(const BwdParams p) {
     }
 }
 
+// The same with the ring of fwd_ring_kernel, read a second time after a row's
+// reduction instead of held in registers.
+template <int DT>
+__global__ void __launch_bounds__(kRingThreads, 2) bwd_ring_kernel(const BwdParams p) {
+    constexpr int E = Elt<DT>::kPer16;
+    extern __shared__ __align__(16) unsigned char ring[];  // [kBwdAhead][3][kOwn][threads][16]
+    __shared__ float sh[2][2][32];
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    int64_t at[kOwn];
+    bool in[kOwn];
+    float w[kOwn][E], dw[kOwn][E];
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) {
+        at[k] = static_cast<int64_t>(k * blockDim.x + threadIdx.x) * E;
+        in[k] = at[k] < p.H;
+        if (in[k]) load_w<DT, E>(p.weight, p.w_f32 != 0, at[k], p.offset, w[k]);
+#pragma unroll
+        for (int j = 0; j < E; ++j) dw[k][j] = 0.f;
+    }
+    auto slot = [&](int s, int which, int k) {
+        return ring + 16 * (((s * 3 + which) * kOwn + k) * blockDim.x + threadIdx.x);
+    };
+    auto fetch = [&](int64_t row, int s) {
+        if (row < p.T) {
+#pragma unroll
+            for (int k = 0; k < kOwn; ++k)
+                if (in[k]) {
+                    const int64_t off = at[k] * Elt<DT>::kBytes;
+                    ptx::cp_async16(ptx::smem_addr(slot(s, 0, k)), p.dy + row * p.dy_ld + off);
+                    ptx::cp_async16(ptx::smem_addr(slot(s, 1, k)), p.x + row * p.x_ld + off);
+                    if (p.dres)
+                        ptx::cp_async16(ptx::smem_addr(slot(s, 2, k)),
+                                        p.dres + row * p.dres_ld + off);
+                }
+        }
+        ptx::cp_async_commit();
+    };
+    const int64_t step = gridDim.x;
+    const float inv_h = 1.f / static_cast<float>(p.H);
+    for (int n = 0; n < kBwdAhead - 1; ++n) fetch(blockIdx.x + n * step, n);
+    float rstd = 0.f, next = blockIdx.x < p.T ? p.rstd[blockIdx.x] : 0.f;
+    int s = 0, flip = 0;
+    for (int64_t row = blockIdx.x; row < p.T; row += step, flip ^= 1) {
+        rstd = next;
+        if (row + step < p.T) next = p.rstd[row + step];
+        fetch(row + (kBwdAhead - 1) * step, s == 0 ? kBwdAhead - 1 : s - 1);
+        ptx::cp_async_wait<kBwdAhead - 1>();
+        float c = 0.f, unused = 0.f;
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k)
+            if (in[k]) {
+                float d[E], h[E];
+                load_e<DT, E>(slot(s, 0, k), 0, d);
+                load_e<DT, E>(slot(s, 1, k), 0, h);
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    const float g = d[j] * (h[j] * rstd);
+                    dw[k][j] += g;
+                    c = fmaf(g, w[k][j], c);
+                }
+            }
+        block_sum_max<false>(c, unused, sh[flip]);
+        c *= inv_h;
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k)
+            if (in[k]) {
+                float d[E], h[E], r[E];
+                load_e<DT, E>(slot(s, 0, k), 0, d);
+                load_e<DT, E>(slot(s, 1, k), 0, h);
+#pragma unroll
+                for (int j = 0; j < E; ++j) r[j] = 0.f;
+                if (p.dres) load_e<DT, E>(slot(s, 2, k), 0, r);
+#pragma unroll
+                for (int j = 0; j < E; ++j)
+                    r[j] = fmaf(rstd, fmaf(d[j], w[k][j], -(h[j] * rstd) * c), r[j]);
+                store_e<DT, E>(p.dx + row * p.dx_ld, at[k], r);
+            }
+        if (++s == kBwdAhead) s = 0;
+    }
+    if (p.part) {
+        float *part = p.part + static_cast<int64_t>(blockIdx.x) * p.H;
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k)
+            if (in[k]) {
+#pragma unroll
+                for (int j = 0; j < E; j += 4)
+                    *reinterpret_cast<float4 *>(part + at[k] + j) =
+                        make_float4(dw[k][j], dw[k][j + 1], dw[k][j + 2], dw[k][j + 3]);
+            }
+    }
+}
+
 // Rows too wide for one CTA's registers: the rows' mean(a xhat), then dx and
 // the partial dw by column segments.
 template <int DT, int E>
 __global__ void __launch_bounds__(512) dot_kernel(const BwdParams p) {
     __shared__ float sh[2][32];
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
     const int64_t row = blockIdx.x;
     const float rstd = p.rstd[row];
     float c = 0.f, unused = 0.f;
@@ -333,11 +524,13 @@ __global__ void __launch_bounds__(512) dot_kernel(const BwdParams p) {
 #pragma unroll
         for (int j = 0; j < E; ++j) c = fmaf(d[j] * w[j], h[j] * rstd, c);
     }
-    block_sum_max(c, unused, sh);
+    block_sum_max<false>(c, unused, sh);
     if (threadIdx.x == 0) p.dot[row] = c / static_cast<float>(p.H);
 }
 template <int DT, int E>
 __global__ void __launch_bounds__(512) segment_kernel(const BwdParams p) {
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
     const int64_t i = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) * E;
     if (i >= p.H) return;
     float dw[E], w[E];
@@ -366,27 +559,65 @@ __global__ void __launch_bounds__(512) segment_kernel(const BwdParams p) {
     }
 }
 
-__global__ void __launch_bounds__(256) dw_kernel(const float *part, int parts, int64_t H, float *dw,
-                                                 int accumulate) {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 32 + (threadIdx.x & 31);
-    __shared__ float sh[8][32];
-    const int warp = threadIdx.x >> 5;
+constexpr int kDwWarps = 32;
+struct DwParams {
+    const float *part;
+    float *dw;
+    int64_t H;
+    int parts, accumulate;
+};
+__global__ void __launch_bounds__(32 * kDwWarps) dw_kernel(const DwParams p) {
+    __shared__ float sh[kDwWarps][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
     float a = 0.f;
-    if (i < H)
-        for (int q = warp; q < parts; q += 8) a += part[static_cast<int64_t>(q) * H + i];
-    sh[warp][threadIdx.x & 31] = a;
+    if (i < p.H) {
+#pragma unroll 8
+        for (int q = warp; q < p.parts; q += kDwWarps) a += p.part[q * p.H + i];
+    }
+    sh[warp][lane] = a;
     __syncthreads();
-    if (warp == 0 && i < H) {
+    if (warp == 0 && i < p.H) {
         a = 0.f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) a += sh[w][threadIdx.x];
-        dw[i] = accumulate ? dw[i] + a : a;
+        for (int w = 0; w < kDwWarps; ++w) a += sh[w][lane];
+        p.dw[i] = p.accumulate ? p.dw[i] + a : a;
     }
 }
 
 // ------------------------------------------------------------ host side
 constexpr int64_t kMaxH = INT64_C(1) << 30;
-constexpr int kMaxParts = 512;  // CTAs whose partial dw the workspace holds
+// CTAs whose partial dw the workspace holds (SMs x CTAs of one SM).
+int64_t max_parts(int64_t T, int64_t H) {
+    const int64_t n = 160 * std::min<int64_t>(8, std::max<int64_t>(2, 8192 / H));
+    return std::min(std::max<int64_t>(T, 1), n);
+}
+// CTAs of `threads` threads on one SM, for about 1024 threads.
+int per_sm_of(int threads) { return std::max(1, std::min(8, 1024 / threads)); }
+
+// All kernels are launched dependent on what precedes them on the stream.
+template <class Params>
+cudaError_t launch(void (*k)(Params), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                   const Params &p) {
+    if (smem > 0) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, p);
+}
 
 int elt_of(int32_t dtype) { return dtype == VLMCE_F32 ? 4 : 2; }
 bool dtype_ok(int32_t d) { return d == VLMCE_F32 || d == VLMCE_BF16 || d == VLMCE_F16; }
@@ -437,7 +668,30 @@ FwdKernel fwd_kernel_of(int32_t dtype, bool quant, bool vec, int ng) {
             return quant ? fwd_pick<VLMCE_F16, true>(vec, ng) : fwd_pick<VLMCE_F16, false>(vec, ng);
     }
 }
+// Threads of the ring kernels, kOwn granules of 16 bytes each; 0: the row is too
+// wide.
+int ring_threads(int64_t H, int32_t dtype) {
+    const int64_t granules = H * elt_of(dtype) / 16;
+    return granules <= kOwn * kRingThreads
+               ? static_cast<int>(round_up((granules + kOwn - 1) / kOwn, 32))
+               : 0;
+}
+template <bool Q>
+FwdKernel fwd_ring_of(int32_t dtype) {
+    switch (dtype) {
+        case VLMCE_F32: return fwd_ring_kernel<VLMCE_F32, Q>;
+        case VLMCE_BF16: return fwd_ring_kernel<VLMCE_BF16, Q>;
+        default: return fwd_ring_kernel<VLMCE_F16, Q>;
+    }
+}
 using BwdKernel = void (*)(const BwdParams);
+BwdKernel bwd_ring_of(int32_t dtype) {
+    switch (dtype) {
+        case VLMCE_F32: return bwd_ring_kernel<VLMCE_F32>;
+        case VLMCE_BF16: return bwd_ring_kernel<VLMCE_BF16>;
+        default: return bwd_ring_kernel<VLMCE_F16>;
+    }
+}
 template <int DT>
 BwdKernel bwd_pick(bool vec, int ng) {
     constexpr int E = Elt<DT>::kPer16;
@@ -553,17 +807,27 @@ extern "C" vlmce_status rmsnorm_fwd(const void *x, int64_t x_stride, const void 
     p.eps = eps;
     p.offset = weight_offset;
     p.w_f32 = weight_dtype == VLMCE_F32;
-    fwd_kernel_of(dtype, quant, vec, sh.ng)<<<static_cast<unsigned>(T), sh.threads, 0,
-                                              reinterpret_cast<cudaStream_t>(stream)>>>(p);
-    return launch_status(cudaSuccess, "rmsnorm_fwd");
+    cudaStream_t st_ = reinterpret_cast<cudaStream_t>(stream);
+    const int rt = vec ? ring_threads(H, dtype) : 0;
+    if (rt > 0) {
+        const int64_t ctas = static_cast<int64_t>(dev.sm_count) * per_sm_of(rt);
+        if (T >= 3 * ctas)  // rows enough to run ahead
+            return launch_status(
+                launch(quant ? fwd_ring_of<true>(dtype) : fwd_ring_of<false>(dtype),
+                       dim3(static_cast<unsigned>(ctas), 1, 1), rt,
+                       static_cast<size_t>(kFwdAhead) * 2 * kOwn * 16 * rt, st_, p),
+                "rmsnorm_fwd");
+    }
+    return launch_status(launch(fwd_kernel_of(dtype, quant, vec, sh.ng),
+                                dim3(static_cast<unsigned>(T), 1, 1), sh.threads, 0, st_, p),
+                         "rmsnorm_fwd");
 }
 
 extern "C" size_t vlmce_rmsnorm_bwd_workspace_bytes(int64_t T, int64_t H) {
     using namespace vlmce;
     using namespace vlmce::rms;
     if (T < 0 || H < 1 || H > kMaxH || T > INT32_MAX) return 0;
-    return static_cast<size_t>(round_up(4 * H * std::min<int64_t>(std::max<int64_t>(T, 1), kMaxParts), 256) +
-                               round_up(4 * T, 256));
+    return static_cast<size_t>(round_up(4 * H * max_parts(T, H), 256) + round_up(4 * T, 256));
 }
 
 extern "C" vlmce_status rmsnorm_bwd(const void *dy, int64_t dy_stride, const void *x,
@@ -615,7 +879,7 @@ extern "C" vlmce_status rmsnorm_bwd(const void *dy, int64_t dy_stride, const voi
                      aligned(weight, 16) &&
                      (!dresidual || (dresidual_stride % E == 0 && aligned(dresidual, 16)));
     const Shape sh = shape_of(H, vec ? E : 1);
-    const int64_t parts_max = std::min<int64_t>(T, kMaxParts);
+    const int64_t parts_max = max_parts(T, H);
     BwdParams p = {};
     p.dy = static_cast<const unsigned char *>(dy);
     p.x = static_cast<const unsigned char *>(x);
@@ -635,9 +899,18 @@ extern "C" vlmce_status rmsnorm_bwd(const void *dy, int64_t dy_stride, const voi
     p.offset = weight_offset;
     p.w_f32 = weight_dtype == VLMCE_F32;
     int64_t parts;
-    if (sh.ng > 0) {
-        parts = std::min<int64_t>(parts_max, static_cast<int64_t>(dev.sm_count) * 2);
-        bwd_kernel_of(dtype, vec, sh.ng)<<<static_cast<unsigned>(parts), sh.threads, 0, s>>>(p);
+    const int rt = vec ? ring_threads(H, dtype) : 0;
+    const int64_t ring_ctas = rt > 0 ? static_cast<int64_t>(dev.sm_count) * per_sm_of(rt) : 0;
+    cudaError_t e;
+    if (rt > 0 && T >= 3 * ring_ctas && ring_ctas <= parts_max) {
+        parts = ring_ctas;
+        e = launch(bwd_ring_of(dtype), dim3(static_cast<unsigned>(parts), 1, 1), rt,
+                   static_cast<size_t>(kBwdAhead) * 3 * kOwn * 16 * rt, s, p);
+    } else if (sh.ng > 0) {
+        parts = std::min<int64_t>(parts_max, static_cast<int64_t>(dev.sm_count) *
+                                                 std::max(2, per_sm_of(sh.threads)));
+        e = launch(bwd_kernel_of(dtype, vec, sh.ng), dim3(static_cast<unsigned>(parts), 1, 1),
+                   sh.threads, 0, s, p);
     } else {
         BwdKernel dot, seg;
         if (dtype == VLMCE_F32)
@@ -646,18 +919,20 @@ extern "C" vlmce_status rmsnorm_bwd(const void *dy, int64_t dy_stride, const voi
             wide_pick<VLMCE_BF16>(vec, &dot, &seg);
         else
             wide_pick<VLMCE_F16>(vec, &dot, &seg);
-        dot<<<static_cast<unsigned>(T), 512, 0, s>>>(p);
-        st = launch_status(cudaSuccess, "rmsnorm_bwd");
+        e = launch(dot, dim3(static_cast<unsigned>(T), 1, 1), 512, 0, s, p);
+        st = launch_status(e, "rmsnorm_bwd");
         if (st != VLMCE_OK) return st;
         const int64_t per = 512 * (vec ? E : 1);
         const int64_t gx = (H + per - 1) / per;
         parts = std::min<int64_t>(parts_max,
                                   std::max<int64_t>(1, static_cast<int64_t>(dev.sm_count) * 4 / gx));
-        seg<<<dim3(static_cast<unsigned>(gx), static_cast<unsigned>(parts), 1), 512, 0, s>>>(p);
+        e = launch(seg, dim3(static_cast<unsigned>(gx), static_cast<unsigned>(parts), 1), 512, 0, s,
+                   p);
     }
-    st = launch_status(cudaSuccess, "rmsnorm_bwd");
+    st = launch_status(e, "rmsnorm_bwd");
     if (st != VLMCE_OK || !dweight) return st;
-    dw_kernel<<<static_cast<unsigned>((H + 31) / 32), 256, 0, s>>>(
-        p.part, static_cast<int>(parts), H, dweight, accumulate_dweight);
-    return launch_status(cudaSuccess, "rmsnorm_bwd");
+    DwParams d = {p.part, dweight, H, static_cast<int>(parts), accumulate_dweight};
+    return launch_status(launch(dw_kernel, dim3(static_cast<unsigned>((H + 31) / 32), 1, 1),
+                                32 * kDwWarps, 0, s, d),
+                         "rmsnorm_bwd");
 }

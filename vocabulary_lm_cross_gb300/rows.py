@@ -15,7 +15,7 @@ def rows(t: torch.Tensor, name: str, shape, dtype, device) -> int:
     """The row stride of a 2-D argument, after its checks."""
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}")
@@ -43,13 +43,22 @@ def matrix(t: torch.Tensor, name: str) -> None:
         raise TypeError(f"{name} must be a CUDA tensor")
 
 
+# The handle of a device's current stream: torch.cuda.current_stream builds a
+# Stream object for it, which costs 2 us a call on the host.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+if _raw_stream is None:  # a CPU-only torch
+    def _raw_stream(index):
+        return torch.cuda.current_stream(index).cuda_stream
+
+
 def call(fn, name: str, device, *args) -> None:
     """Enqueue on the device's current stream; raises on a non-zero status."""
-    if device.index == torch.cuda.current_device():
-        st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    index = device.index
+    if index == torch.cuda.current_device():
+        st = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(device):
-            st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+        with torch.cuda.device(index):
+            st = fn(*args, _raw_stream(index))
     if st != capi.OK:
         capi.check(st, name)
 
