@@ -64,6 +64,11 @@ struct Capacity {
 constexpr int kSmSmem = 233472;  // 228 KB
 constexpr int small_budget(int per_sm) { return kSmSmem / per_sm - kSmemReserved; }
 
+// Stands for the small kernels in occupancy queries, which count a kernel that
+// allocates TMEM as one CTA per SM whatever it takes (several do share one).
+// Never launched.
+__global__ void __launch_bounds__(kSmallBound, 2) small_shape_kernel() {}
+
 template <class Kernel>
 cudaError_t clusters_of(Kernel k, int csize, int threads, int smem, int *n) {
     cudaLaunchConfig_t cfg = {};
@@ -102,9 +107,12 @@ cudaError_t setup(Capacity *out) {
             if (e != cudaSuccess) return e;
             c.pairs = k == 0 ? n : std::min(c.pairs, n);
         }
+        e = cudaFuncSetAttribute(small_shape_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 small_budget(1));
+        if (e != cudaSuccess) return e;
         for (int per_sm = 1; per_sm <= 2; ++per_sm)
             for (int split = 1; split <= kMaxSplit; ++split) {
-                e = clusters_of(small_kernel(true, false), split, kSmallThreads,
+                e = clusters_of(small_shape_kernel, split, kSmallThreads,
                                 small_budget(per_sm), &c.small[per_sm - 1][split - 1]);
                 if (e != cudaSuccess) return e;
             }
@@ -130,10 +138,10 @@ struct Plan {
 // or the shared-memory reads of both operands) and its way from L2, shared by
 // the CTAs of an SM; it is free again a fetch latency, a transfer and its MMAs
 // later.  The weight comes from HBM at 6.8 TB/s at best.
-constexpr double kHbmBytesPerClock = 3570., kL2BytesPerClock = 70.;
-constexpr double kFetch = 1200., kPerStage = 145., kPerCta = 6600., kSplitSync = 1750.;
-constexpr double kOut = 25., kOutSplit = 34.;   // epilogue, per token of an accumulator
-constexpr double kPairChunk = 670., kPairCta = 7200.;
+constexpr double kHbmBytesPerClock = 3570., kL2BytesPerClock = 76.;
+constexpr double kFetch = 900., kPerStage = 260., kPerCta = 6900., kSplitSync = 1300.;
+constexpr double kOut = 25., kOutSplit = 40.;   // epilogue, per token of an accumulator
+constexpr double kPairChunk = 640., kPairCta = 7900.;
 
 double hbm_clocks(const Fwd &f) {
     return static_cast<double>(f.N) * (f.gated ? 2 : 1) * f.K *
@@ -169,7 +177,7 @@ bool small_plan(const Fwd &f, const Capacity &cap, int64_t ty, int split, int pe
     const double main = rounds * steps * step, hbm = hbm_clocks(f);
     const double epilogue =
         per_sm * kw * p.bn * (split > 1 ? kOutSplit : kOut) + (split > 1 ? kSplitSync : 0.);
-    p.clocks = std::cbrt(main * main * main + hbm * hbm * hbm) + rounds * (kPerCta + epilogue);
+    p.clocks = std::sqrt(std::hypot(main * main, hbm * hbm)) + rounds * (kPerCta + epilogue);
     *out = p;
     return true;
 }
@@ -181,7 +189,7 @@ Plan choose(const Fwd &f, const Capacity &cap) {
         ((f.T + 255) / 256) * (f.gated ? (f.N + 127) / 128 : (f.N + 255) / 256);
     const double main =
         static_cast<double>((tiles + cap.pairs - 1) / cap.pairs) * chunks_of(f) * kPairChunk;
-    best.clocks = std::hypot(main, 0.4 * hbm_clocks(f)) + kPairCta;
+    best.clocks = std::hypot(main, 0.6 * hbm_clocks(f)) + kPairCta;
     const int64_t t0 = (f.T + 255) / 256;
     if (t0 > 16) return best;  // enough tokens for the pair tiles
     for (int64_t ty = t0; ty < t0 + 5; ++ty)

@@ -38,10 +38,14 @@ namespace vlmce {
 namespace mm {
 
 constexpr int kSmallThreads = 320;
+// An SM's four quarters hold warps w, w + 4, ... of a block: 10 warps take the
+// registers of 12 where two blocks share it.
+constexpr int kSmallBound = 384;
 constexpr int kWTileBytes = 128 * 128;  // 128 weight rows x 128 bytes of K
 constexpr int kMaxSmallStages = 12;
 constexpr int kMaxSplit = 8;
-constexpr int kSmallTail = 8 * (2 * kMaxSmallStages + 2) + 16;  // barriers, TMEM slot, abort flag
+// barriers, TMEM slot, abort flag, the tokens' factors
+constexpr int kSmallTail = 8 * (2 * kMaxSmallStages + 2) + 16 + 4 * 256;
 // Shared memory of an SM (228 KB, 1 KB of it reserved per resident CTA) over its
 // 512 TMEM columns; and a floor that does not fit beside a pair kernel, which
 // holds all 512 columns with 198 KB.
@@ -63,8 +67,10 @@ struct SmallParams {
     int *err;
 };
 
-// The epilogue of NJ tokens t of one weight row n (Epi in mm_types.h); tokens
-// from `count` on do not exist.  The row's factors are loaded once per thread.
+// What the epilogue reads besides the accumulators is fetched ahead of it, while
+// the products run: with the ring's copies in flight everywhere a load takes
+// microseconds (T = 64, K = 16384, N = 6656 in e4m3: a residual read in the
+// epilogue cost 7.5 of 32.5 us).
 struct RowFactors {
     float ws, ws_up, bias;
 };
@@ -80,41 +86,49 @@ __device__ __forceinline__ RowFactors row_factors(const SmallParams &p, int n) {
         if (e.bias) f.bias = act::from16(e.bias[n], e.f16 != 0);
     return f;
 }
+// A thread's tokens come in units of 16: token i of the unit starting at j is
+// j + i (`run` = 16), or j + i % 4 + i / 4 * 8 (`run` = 4: two threads share
+// every eight tokens).  Tokens at or after `end` do not exist.
+__device__ __forceinline__ int unit_token(int j, int i, int run) {
+    return run == 16 ? j + i : j + (i & 3) + (i >> 2) * 8;
+}
+__device__ __forceinline__ void fetch_residual(const SmallParams &p, uint16_t (&r)[16], int j,
+                                               int end, int run, int64_t t0, int n) {
+    const Epi &e = p.e;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int t = unit_token(j, i, run);
+        r[i] = t < end ? e.residual[(t0 + t) * e.residual_ld + n] : 0;
+    }
+}
+// The epilogue of NJ consecutive tokens t0 + j .. of one weight row n (Epi in
+// mm_types.h); tokens from `count` on do not exist.  xs: their factors, r: the
+// residual's values.
 template <bool GATED, int NJ>
 __device__ __forceinline__ void small_epilogue(const SmallParams &p, const RowFactors &f,
-                                               float (&g)[NJ], float (&u)[NJ], const int (&t)[NJ],
-                                               int count, int n) {
+                                               float (&g)[NJ], float (&u)[NJ], int64_t t,
+                                               int count, int n, const float *xs,
+                                               const uint16_t *r) {
     const Epi &e = p.e;
     const bool f16 = e.f16 != 0;
-    float r[NJ];
-    if constexpr (!GATED) {
-        if (e.residual) {
-#pragma unroll
-            for (int j = 0; j < NJ; ++j)
-                if (j < count)
-                    r[j] = act::from16(e.residual[t[j] * e.residual_ld + n], f16);
-        }
-    }
     if (e.ws) {
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
-            if (j < count) {
-                const float xs = e.xs[t[j]];
-                g[j] *= xs * f.ws;
-                if constexpr (GATED) u[j] *= xs * f.ws_up;
-            }
+        for (int j = 0; j < NJ; ++j) {
+            g[j] *= xs[j] * f.ws;
+            if constexpr (GATED) u[j] *= xs[j] * f.ws_up;
+        }
     }
     if constexpr (!GATED) {
 #pragma unroll
         for (int j = 0; j < NJ; ++j) g[j] += f.bias;
     }
     if (e.preact) {
+        uint16_t *z = e.preact + t * e.preact_ld + n;
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
             if (j < count) {
-                uint16_t *z = e.preact + t[j] * e.preact_ld + n;
-                z[0] = act::to16(g[j], f16);
-                if constexpr (GATED) z[p.N] = act::to16(u[j], f16);
+                z[j * e.preact_ld] = act::to16(g[j], f16);
+                if constexpr (GATED) z[j * e.preact_ld + p.N] = act::to16(u[j], f16);
             }
     }
     act::apply_n(g, e.act);
@@ -123,15 +137,16 @@ __device__ __forceinline__ void small_epilogue(const SmallParams &p, const RowFa
         if constexpr (GATED)
             g[j] *= u[j];
         else if (e.residual)
-            g[j] += r[j];
+            g[j] += act::from16(r[j], f16);
     }
+    uint16_t *y = e.y + t * e.y_ld + n;
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
-        if (j < count) e.y[t[j] * e.y_ld + n] = act::to16(g[j], f16);
+        if (j < count) y[j * e.y_ld] = act::to16(g[j], f16);
 }
 
 template <bool GATED, bool FP8>
-__global__ void __launch_bounds__(kSmallThreads)
+__global__ void __launch_bounds__(kSmallBound, 2)
     mm_small_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx,
                     const __grid_constant__ SmallParams p) {
     extern __shared__ unsigned char smem_raw[];
@@ -144,6 +159,7 @@ __global__ void __launch_bounds__(kSmallThreads)
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + p.stages * stage_bytes);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * kMaxSmallStages + 2);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    float *xs_s = reinterpret_cast<float *>(tmem_slot + 4);  // [256] the tokens' factors
     const uint32_t ring = ptx::smem_addr(smem);
     const uint32_t bar0 = ptx::smem_addr(bars);
     auto full = [&](int s) { return bar0 + 8u * s; };
@@ -257,9 +273,6 @@ __global__ void __launch_bounds__(kSmallThreads)
             tc::mma_commit(done);
             drain_bar(done, 0, p.err);
         }
-    } else {
-        wait_bar(done, 0, abort, p.err);
-        tc::fence_after_sync();
     }
 
     const int q = warp & 3;            // TMEM subpartition of an epilogue warp
@@ -267,30 +280,56 @@ __global__ void __launch_bounds__(kSmallThreads)
     const int row = q * 32 + lane;
     const bool row_ok = n0 + row < p.N;
     const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16);
-    constexpr int NJ = 8;
+    const int n = n0 + row;
+    const bool res = !GATED && p.e.residual != nullptr;
+    const int own = p.split == 1 ? p.bn : (p.red_tokens / 4 + p.split - 1) / p.split * 4;
+    RowFactors f = {1.f, 1.f, 0.f};
+    uint16_t r_next[16];
+    if (warp >= 2) {
+        if (p.e.ws) {
+            const int j = threadIdx.x - 64;  // 256 threads, at most 256 tokens
+            if (j < nt) xs_s[j] = p.e.xs[t0 + j];
+        }
+        if (row_ok) {
+            f = row_factors<GATED>(p, n);
+            if (res) {
+                if (p.split == 1)
+                    fetch_residual(p, r_next, 16 * half, nt, 16, t0, n);
+                else
+                    fetch_residual(p, r_next, rank * own + 4 * half,
+                                   min((rank + 1) * own, min(p.red_tokens, nt)), 4, t0, n);
+            }
+        }
+        wait_bar(done, 0, abort, p.err);
+        tc::fence_after_sync();
+        asm volatile("bar.sync 1, 256;" ::: "memory");  // xs_s is complete
+    }
     if (p.split == 1) {
         if (warp >= 2) {
-            RowFactors f = {1.f, 1.f, 0.f};
-            if (row_ok) f = row_factors<GATED>(p, n0 + row);
 #pragma unroll 1
             for (int j0 = 16 * half; j0 < nt; j0 += 32) {
                 uint32_t a[16], b[16];
                 tc::tmem_ld16(tbase + j0, a);
                 if constexpr (GATED) tc::tmem_ld16(tbase + p.bn + j0, b);
+                uint16_t r[16];
+                if (res) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) r[i] = r_next[i];
+                    if (row_ok) fetch_residual(p, r_next, j0 + 32, nt, 16, t0, n);
+                }
                 tc::tmem_ld_wait();
                 if (row_ok) {
 #pragma unroll
-                    for (int h = 0; h < 16; h += NJ) {
-                        float g[NJ], u[NJ];
-                        int t[NJ];
+                    for (int h = 0; h < 16; h += 8) {
+                        float g[8], u[8];
 #pragma unroll
-                        for (int j = 0; j < NJ; ++j) {
+                        for (int j = 0; j < 8; ++j) {
                             g[j] = __uint_as_float(a[h + j]);
                             u[j] = GATED ? __uint_as_float(b[h + j]) : 0.f;
-                            t[j] = t0 + j0 + h + j;
                         }
                         if (j0 + h < nt)
-                            small_epilogue<GATED, NJ>(p, f, g, u, t, nt - j0 - h, n0 + row);
+                            small_epilogue<GATED, 8>(p, f, g, u, t0 + j0 + h, nt - j0 - h, n,
+                                                     xs_s + j0 + h, r + h);
                     }
                 }
                 __syncwarp();
@@ -301,10 +340,7 @@ __global__ void __launch_bounds__(kSmallThreads)
         // completed).  It then holds, for this CTA's run of `own` tokens of a block
         // of red_tokens, the accumulators [from][kW][token / 4][128 rows][4].
         const uint32_t part = ptx::smem_addr(smem);
-        const int own = (p.red_tokens / 4 + p.split - 1) / p.split * 4;
         const int plane = own * 128;  // floats of one accumulator of one sender
-        RowFactors f = {1.f, 1.f, 0.f};
-        if (warp >= 2 && row_ok) f = row_factors<GATED>(p, n0 + row);
 #pragma unroll 1
         for (int jb = 0; jb < nt; jb += p.red_tokens) {
             ptx::cluster_sync_any();
@@ -332,32 +368,44 @@ __global__ void __launch_bounds__(kSmallThreads)
             }
             ptx::cluster_sync_any();
             if (warp >= 2 && row_ok) {
-                const int mine = min(own, je - rank * own);
+                const int first = rank * own, end = min(first + own, je);  // of the block
                 const float *src = reinterpret_cast<const float *>(smem) + 4 * row;
+                if (res && jb > 0)
+                    fetch_residual(p, r_next, jb + first + 4 * half, jb + end, 4, t0, n);
 #pragma unroll 1
-                for (int i0 = 4 * half; i0 < mine; i0 += 8) {
-                    float g[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
-                    int t[4];
+                for (int j0 = first + 4 * half; j0 < end; j0 += 32) {
+                    uint16_t r[16];
+                    if (res) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) t[j] = t0 + jb + rank * own + i0 + j;
+                        for (int i = 0; i < 16; ++i) r[i] = r_next[i];
+                        fetch_residual(p, r_next, jb + j0 + 32, jb + end, 4, t0, n);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int j = j0 + 8 * c;
+                        if (j < end) {
+                            float g[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 2
-                    for (int r = 0; r < p.split; ++r) {
-                        const float4 v = *reinterpret_cast<const float4 *>(
-                            src + r * kW * plane + i0 * 128);
-                        g[0] += v.x;
-                        g[1] += v.y;
-                        g[2] += v.z;
-                        g[3] += v.w;
-                        if constexpr (GATED) {
-                            const float4 w = *reinterpret_cast<const float4 *>(
-                                src + (r * kW + 1) * plane + i0 * 128);
-                            u[0] += w.x;
-                            u[1] += w.y;
-                            u[2] += w.z;
-                            u[3] += w.w;
+                            for (int s = 0; s < p.split; ++s) {
+                                const float4 v = *reinterpret_cast<const float4 *>(
+                                    src + s * kW * plane + (j - first) * 128);
+                                g[0] += v.x;
+                                g[1] += v.y;
+                                g[2] += v.z;
+                                g[3] += v.w;
+                                if constexpr (GATED) {
+                                    const float4 w = *reinterpret_cast<const float4 *>(
+                                        src + (s * kW + 1) * plane + (j - first) * 128);
+                                    u[0] += w.x;
+                                    u[1] += w.y;
+                                    u[2] += w.z;
+                                    u[3] += w.w;
+                                }
+                            }
+                            small_epilogue<GATED, 4>(p, f, g, u, t0 + jb + j, end - j, n,
+                                                     xs_s + jb + j, r + 4 * c);
                         }
                     }
-                    small_epilogue<GATED, 4>(p, f, g, u, t, mine - i0, n0 + row);
                 }
             }
         }
