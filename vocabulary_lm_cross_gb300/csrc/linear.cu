@@ -18,7 +18,6 @@
 #include <cmath>
 
 #include "act.cuh"
-#include "gemm_launch.h"
 #include "host_util.h"
 #include "mm_types.h"
 #include "vlmce.h"
@@ -34,6 +33,7 @@ constexpr int kMaxRowChunks = 64;  // partial sums of db
 struct DzParams {
     const uint16_t *dy, *pre;
     uint16_t *dz;   // may be null (db only)
+    unsigned int *ctr;  // set to zero
     float *part;    // [row chunks][N] partial sums of dz's columns, may be null
     int64_t dy_ld, pre_ld, dz_ld;
     int64_t T, N;
@@ -68,6 +68,9 @@ __device__ __forceinline__ void store_v(uint16_t *p, const float (&v)[V], bool f
 template <int ACT, bool GATED, int V>
 __global__ void __launch_bounds__(32 * kDzWarps) dz_kernel(const DzParams p) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.ctr = 0;
     const int64_t col = (static_cast<int64_t>(blockIdx.x) * 32 + lane) * V;
     const int64_t r0 = blockIdx.y * p.rows_per_chunk;
     const int64_t r1 = min(p.T, r0 + p.rows_per_chunk);
@@ -128,6 +131,8 @@ __global__ void __launch_bounds__(32 * kDzWarps) dz_kernel(const DzParams p) {
 }
 
 __global__ void db_kernel(const float *part, int chunks, int64_t N, float *db, int accumulate) {
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
     const int64_t n = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
     if (n >= N) return;
     float a = 0.f;
@@ -150,6 +155,21 @@ DzKernel dz_kernel_of(int act, bool gated, bool vec) {
         case VLMCE_ACT_RELU: return dz_pick<VLMCE_ACT_RELU>(gated, vec);
         default: return dz_pick<VLMCE_ACT_NONE>(gated, vec);
     }
+}
+
+// A launch dependent on what precedes it on the stream.
+template <class... Params, class... Args>
+cudaError_t launch(void (*k)(Params...), dim3 grid, int threads, cudaStream_t s, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, args...);
 }
 
 // ------------------------------------------------------------ checks
@@ -176,12 +196,6 @@ bool fits(int64_t rows, int64_t ld, int elt) {
 bool act_ok(int32_t act, bool gated) {
     return act >= (gated ? VLMCE_ACT_SILU : VLMCE_ACT_NONE) && act <= VLMCE_ACT_RELU;
 }
-// Bytes an access to 32 consecutive 16-bit columns of a row may use.
-int vec_of(const void *p, int64_t ld) {
-    const uint64_t a = reinterpret_cast<uint64_t>(p) | static_cast<uint64_t>(2 * ld);
-    return a % 32 == 0 ? 32 : a % 16 == 0 ? 16 : 2;
-}
-
 // An operand of the tensor cores: [rows, K] K-major.
 vlmce_status check_operand(const void *p, int64_t rows, int64_t K, int64_t ld, int elt) {
     if (ld < K || ld * elt % 16 != 0) return VLMCE_ERR_INVALID_ARG;
@@ -278,10 +292,10 @@ vlmce_status forward(const FwdArgs &a, const char *where) {
     e.ws = a.weight_scale;
     e.act = a.act;
     e.f16 = a.out_dtype == VLMCE_F16;
-    e.y_vec = vec_of(a.y, a.y_stride);
-    e.preact_vec = vec_of(a.preact, a.preact_stride);
-    e.preact_up_vec = vec_of(static_cast<uint16_t *>(a.preact) + a.N, a.preact_stride);
-    e.residual_vec = vec_of(a.residual, a.residual_stride);
+    e.y_vec = mm::vec_of(a.y, a.y_stride);
+    e.preact_vec = mm::vec_of(a.preact, a.preact_stride);
+    e.preact_up_vec = mm::vec_of(static_cast<uint16_t *>(a.preact) + a.N, a.preact_stride);
+    e.residual_vec = mm::vec_of(a.residual, a.residual_stride);
     return launch_status(mm::forward(f, a.stream), where);
 }
 
@@ -381,6 +395,7 @@ vlmce_status backward(const BwdArgs &a, const char *where) {
     const bool products = a.dx || a.dweight;
     const bool as_is = !need_pre && a.dy_stride % 8 == 0 && aligned(a.dy, 16) &&
                        a.dy_stride * 2 < (int64_t(1) << 40);
+    bool dz_ran = false;  // it also clears the tile counter
     if (a.dbias || (products && !as_is)) {
         DzParams p = {};
         p.dy = static_cast<const uint16_t *>(a.dy);
@@ -401,17 +416,21 @@ vlmce_status backward(const BwdArgs &a, const char *where) {
         chunks = std::min({chunks, (a.T + kDzWarps - 1) / kDzWarps, int64_t(kMaxRowChunks)});
         p.rows_per_chunk = (a.T + chunks - 1) / chunks;
         chunks = (a.T + p.rows_per_chunk - 1) / p.rows_per_chunk;
-        dz_kernel_of(a.act, a.gated, vec)<<<dim3(static_cast<unsigned>(gx),
-                                                 static_cast<unsigned>(chunks), 1),
-                                            32 * kDzWarps, 0, a.stream>>>(p);
-        st = launch_status(cudaSuccess, where);
+        p.ctr = ctr;
+        st = launch_status(launch(dz_kernel_of(a.act, a.gated, vec),
+                                  dim3(static_cast<unsigned>(gx), static_cast<unsigned>(chunks), 1),
+                                  32 * kDzWarps, a.stream, static_cast<const DzParams>(p)),
+                           where);
         if (st != VLMCE_OK) return st;
         if (a.dbias) {
-            db_kernel<<<static_cast<unsigned>((a.N + 255) / 256), 256, 0, a.stream>>>(
-                part, static_cast<int>(chunks), a.N, a.dbias, a.accumulate);
-            st = launch_status(cudaSuccess, where);
+            st = launch_status(launch(db_kernel, dim3(static_cast<unsigned>((a.N + 255) / 256), 1, 1),
+                                      256, a.stream, static_cast<const float *>(part),
+                                      static_cast<int>(chunks), a.N, a.dbias,
+                                      static_cast<int>(a.accumulate)),
+                               where);
             if (st != VLMCE_OK) return st;
         }
+        dz_ran = true;
     }
     if (!products) return VLMCE_OK;
     const uint16_t *g = dz;
@@ -419,49 +438,29 @@ vlmce_status backward(const BwdArgs &a, const char *where) {
         g = static_cast<const uint16_t *>(a.dy);
         dz_ld = a.dy_stride;
     }
-    e = cudaMemsetAsync(ctr, 0, 4, a.stream);
-    if (e != cudaSuccess) return launch_status(e, where);
-    gemm::Maps maps;
-    gemm::Params gp = {};
-    gp.f16 = a.dtype == VLMCE_F16;
-    gp.err = a.dev_err;
-    gp.tile_ctr = ctr;
-    bool ok = true;
-    if (a.dx) {
-        gemm::Problem &q = gp.p[gp.nprob];
-        ok = ok && gemm::make_operand_map(&maps.a[gp.nprob], g, false, a.T, rows, dz_ld, gp.f16) &&
-             gemm::make_operand_map(&maps.b[gp.nprob], a.weight, true, a.K, rows, a.weight_stride,
-                                    gp.f16);
-        q.M = static_cast<int>(a.T);
-        q.N = static_cast<int>(a.K);
-        q.K = static_cast<int>(rows);
-        q.b_mn = 1;
-        q.mode = gemm::kStoreBF16;
-        q.C16 = static_cast<uint16_t *>(a.dx);
-        q.ldc16 = a.dx_stride;
-        ++gp.nprob;
+    if (!dz_ran) {
+        e = cudaMemsetAsync(ctr, 0, 4, a.stream);
+        if (e != cudaSuccess) return launch_status(e, where);
     }
-    if (a.dweight) {
-        gemm::Problem &q = gp.p[gp.nprob];
-        ok = ok && gemm::make_operand_map(&maps.a[gp.nprob], g, true, rows, a.T, dz_ld, gp.f16) &&
-             gemm::make_operand_map(&maps.b[gp.nprob], a.x, true, a.K, a.T, a.x_stride, gp.f16);
-        q.M = static_cast<int>(rows);
-        q.N = static_cast<int>(a.K);
-        q.K = static_cast<int>(a.T);
-        q.a_mn = q.b_mn = 1;
-        if (a.dweight_dtype == VLMCE_F32) {
-            q.mode = a.accumulate ? gemm::kAccF32 : gemm::kStoreF32;
-            q.C = static_cast<float *>(a.dweight);
-            q.ldc = a.K;
-        } else {
-            q.mode = gemm::kStoreBF16;
-            q.C16 = static_cast<uint16_t *>(a.dweight);
-            q.ldc16 = a.K;
-        }
-        ++gp.nprob;
-    }
-    if (!ok) return launch_status(cudaErrorInvalidValue, where);
-    return launch_status(gemm::launch_group(maps, gp, a.stream), where);
+    mm::Bwd b = {};
+    b.dz = g;
+    b.x = a.x;
+    b.w = a.weight;
+    b.dz_ld = dz_ld;
+    b.x_ld = a.x_stride;
+    b.w_ld = a.weight_stride;
+    b.T = a.T;
+    b.rows = rows;
+    b.K = a.K;
+    b.f16 = a.dtype == VLMCE_F16;
+    b.dx = a.dx;
+    b.dx_ld = a.dx_stride;
+    b.dw = a.dweight;
+    b.dw_f32 = a.dweight_dtype == VLMCE_F32;
+    b.accumulate = a.accumulate;
+    b.ctr = ctr;
+    b.err = a.dev_err;
+    return launch_status(mm::backward(b, a.stream), where);
 }
 
 }  // namespace

@@ -1,5 +1,5 @@
-// mm.cu -- host side of the linear and gated layers' forward products: tensor
-// maps, tile and split choice, launches.
+// mm.cu -- host side of the linear and gated layers' products: tensor maps,
+// tile and split choice, launches.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -9,6 +9,7 @@
 
 #include "gemm_launch.h"
 #include "host_util.h"
+#include "mm_grad.cuh"
 #include "mm_large.cuh"
 #include "mm_small.cuh"
 
@@ -97,16 +98,22 @@ cudaError_t setup(Capacity *out) {
         Capacity c;
         for (int k = 0; k < 4; ++k) {
             const LargeKernel lk = large_kernel(k & 1, k & 2);
-            e = cudaFuncSetAttribute(lk, cudaFuncAttributeMaxDynamicSharedMemorySize, kLargeSmem);
+            e = cudaFuncSetAttribute(lk, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
             if (e == cudaSuccess)
                 e = cudaFuncSetAttribute(small_kernel(k & 1, k & 2),
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          small_budget(1));
             int n = 0;
-            if (e == cudaSuccess) e = clusters_of(lk, 2, kLargeThreads, kLargeSmem, &n);
+            if (e == cudaSuccess) e = clusters_of(lk, 2, kPairThreads, kPairSmem, &n);
             if (e != cudaSuccess) return e;
             c.pairs = k == 0 ? n : std::min(c.pairs, n);
         }
+        e = cudaFuncSetAttribute(mm_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kGradSmem);
+        int n = 0;
+        if (e == cudaSuccess) e = clusters_of(mm_grad_kernel, 2, kGradThreads, kGradSmem, &n);
+        if (e != cudaSuccess) return e;
+        c.pairs = std::min(c.pairs, n);
         e = cudaFuncSetAttribute(small_shape_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  small_budget(1));
         if (e != cudaSuccess) return e;
@@ -253,8 +260,8 @@ cudaError_t forward_large(const Fwd &f, int pairs, cudaStream_t s) {
     cudaLaunchAttribute attr[2];
     launch_attributes(attr, 2);
     cfg.gridDim = dim3(2 * std::min(p.tiles, pairs), 1, 1);
-    cfg.blockDim = dim3(kLargeThreads, 1, 1);
-    cfg.dynamicSmemBytes = kLargeSmem;
+    cfg.blockDim = dim3(kPairThreads, 1, 1);
+    cfg.dynamicSmemBytes = kPairSmem;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
@@ -310,6 +317,62 @@ cudaError_t forward(const Fwd &f, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const Plan plan = plan_of(f, cap);
     return plan.large ? forward_large(f, cap.pairs, s) : forward_small(f, plan, s);
+}
+
+cudaError_t backward(const Bwd &b, cudaStream_t s) {
+    Capacity cap;
+    const cudaError_t e = setup(&cap);
+    if (e != cudaSuccess) return e;
+    GradMaps maps;
+    GradParams p = {};
+    p.f16 = b.f16;
+    p.ctr = b.ctr;
+    p.err = b.err;
+    const bool f16 = b.f16 != 0;
+    int64_t tiles = 0;
+    bool ok = true;
+    auto add = [&](const void *a, bool a_mn, int64_t a_ld, const void *w, int64_t w_ld, int64_t M,
+                   int64_t K, void *C, int64_t ld, int f32, int accumulate) {
+        GradProblem &q = p.p[p.nprob];
+        ok = ok && gemm::make_operand_map(&maps.a[p.nprob], a, a_mn, M, K, a_ld, f16) &&
+             gemm::make_operand_map(&maps.b[p.nprob], w, true, b.K, K, w_ld, f16);
+        q.M = static_cast<int>(M);
+        q.N = static_cast<int>(b.K);
+        q.chunks = static_cast<int>((K + 63) / 64);
+        q.a_mn = a_mn;
+        q.b_mn = 1;
+        q.mt = static_cast<int>((M + 255) / 256);
+        q.nt = static_cast<int>((b.K + 255) / 256);
+        q.tile0 = static_cast<int>(tiles);
+        q.f32 = f32;
+        q.accumulate = accumulate;
+        q.C = C;
+        q.ld = ld;
+        q.vec = vec_of(C, ld);
+        tiles += static_cast<int64_t>(q.mt) * q.nt;
+        ++p.nprob;
+    };
+    const bool dx_first = b.rows >= b.T;  // longer tiles first
+    for (int i = 0; i < 2; ++i) {
+        if ((i == 0) == dx_first) {
+            if (b.dx)
+                add(b.dz, false, b.dz_ld, b.w, b.w_ld, b.T, b.rows, b.dx, b.dx_ld, 0, 0);
+        } else if (b.dw) {
+            add(b.dz, true, b.dz_ld, b.x, b.x_ld, b.rows, b.T, b.dw, b.K, b.dw_f32, b.accumulate);
+        }
+    }
+    if (!ok) return cudaErrorInvalidValue;
+    p.tiles = static_cast<int>(tiles);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    launch_attributes(attr, 2);
+    cfg.gridDim = dim3(2 * std::min(p.tiles, cap.pairs), 1, 1);
+    cfg.blockDim = dim3(kGradThreads, 1, 1);
+    cfg.dynamicSmemBytes = kGradSmem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, mm_grad_kernel, maps, static_cast<const GradParams>(p));
 }
 
 }  // namespace mm

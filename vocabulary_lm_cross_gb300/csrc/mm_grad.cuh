@@ -1,0 +1,227 @@
+// mm_grad.cuh -- the two gradient products of a linear or gated layer in one
+// launch on CTA pairs (mm_pair.cuh):
+//   dx = dz W     A = dz [T, rows] K-major,       B = W: N(=K_in)-major
+//   dW = dz^T x   A = dz: M(=rows)-major,         B = x: N(=K_in)-major
+// with either operand K-major or MN-major, so nothing is transposed in memory.
+//
+// The tiles of both products are numbered one after the other, the longer
+// inner size first, and taken in order from a counter: a scheduler warp of the
+// leader fetches numbers up to kTileQ ahead of the slowest role and publishes
+// them to both CTAs.  (dx tiles can be many times as long as dW tiles: dealt out
+// in advance, T = 4096, K = 6656, 2n = 32768 would leave pairs idle for one of
+// its 138 us dx tiles.)
+#pragma once
+
+#include <cuda.h>
+
+#include "mm_pair.cuh"
+#include "mm_types.h"
+
+namespace vlmce {
+namespace mm {
+
+constexpr int kGradThreads = kPairThreads + 32;
+constexpr int kTileQ = 4;
+constexpr int kTileQConsumers = 5 + 2 * kEpiWarps;  // 4 producers, MMA issuer, epilogue warps
+constexpr int kQueueBytes = 8 * 2 * kTileQ + 4 * kTileQ;
+constexpr int kGradSmem = kPairSmem + kQueueBytes;
+
+// C[M, N] (+)= A B^T.
+struct GradProblem {
+    int M, N, chunks;
+    int a_mn, b_mn;
+    int mt, nt, tile0;
+    int f32, accumulate;   // C fp32 (added to where accumulate is set), else 16 bits
+    void *C;
+    int64_t ld;
+    int vec;               // 16-bit C: bytes an access may use
+};
+struct GradParams {
+    GradProblem p[2];
+    int nprob, tiles;
+    int f16;
+    unsigned int *ctr;     // zero before the launch
+    int *err;
+};
+struct GradMaps {
+    CUtensorMap a[2], b[2];
+};
+
+struct GradTile {
+    int p, m0, n0;
+};
+__device__ __forceinline__ GradTile grad_tile(const GradParams &a, int t) {
+    const int p = a.nprob > 1 && t >= a.p[1].tile0 ? 1 : 0;
+    const GradProblem &P = a.p[p];
+    constexpr int kGroup = 8;  // as kGroupM of the forward product
+    const int lt = t - P.tile0;
+    const int per_group = kGroup * P.nt;
+    const int g = lt / per_group, r = lt - g * per_group;
+    const int gm = min(kGroup, P.mt - g * kGroup);
+    const int n = r / gm;
+    return {p, (g * kGroup + (r - n * gm)) * 256, n * 256};
+}
+
+// 32 fp32 columns of one row, nc of which exist (C rows are 16-byte aligned).
+__device__ __forceinline__ void store_f32(float *c, const uint32_t (&r)[32], int nc,
+                                          bool accumulate) {
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+        if (j + 4 <= nc) {
+            float4 o = accumulate ? *reinterpret_cast<const float4 *>(c + j)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+            o.x += __uint_as_float(r[j]);
+            o.y += __uint_as_float(r[j + 1]);
+            o.z += __uint_as_float(r[j + 2]);
+            o.w += __uint_as_float(r[j + 3]);
+            *reinterpret_cast<float4 *>(c + j) = o;
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kGradThreads, 1)
+    mm_grad_kernel(const __grid_constant__ GradMaps maps, const __grid_constant__ GradParams a) {
+    extern __shared__ unsigned char smem_raw[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    unsigned char *queue =
+        reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                          ~static_cast<uintptr_t>(1023)) +
+        kPairSmem - 1024;
+    const uint32_t qbar = ptx::smem_addr(queue);
+    volatile int *tq = reinterpret_cast<volatile int *>(queue + 8 * 2 * kTileQ);
+    auto qfull = [&](int i) { return qbar + 8u * i; };
+    auto qempty = [&](int i) { return qbar + 8u * (kTileQ + i); };
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < a.nprob; ++i) {
+            tc::prefetch_tensormap(&maps.a[i]);
+            tc::prefetch_tensormap(&maps.b[i]);
+        }
+    }
+    const Pair q = pair_setup(smem_raw, a.err, [&] {
+        for (int i = 0; i < kTileQ; ++i) {
+            ptx::mbar_init(qfull(i), 1);                 // the scheduler's release-arrive
+            ptx::mbar_init(qempty(i), kTileQConsumers);  // used at the leader only
+        }
+    });
+
+    // The j-th tile of this pair (-1: none left, or a wait gave up).
+    auto publish = [&](int j) {  // the leader's scheduler lane
+        const int slot = j % kTileQ;
+        int t = -1;
+        if (j < kTileQ || wait_bar<true>(qempty(slot), ((j / kTileQ) - 1) & 1, q.abort, q.err)) {
+            const unsigned int u = atomicAdd(a.ctr, 1u);
+            t = u < static_cast<unsigned int>(a.tiles) ? static_cast<int>(u) : -1;
+        }
+        tq[slot] = t;
+        ptx::st_dsmem_u32(ptx::mapa(ptx::smem_addr(const_cast<int *>(tq) + slot), 1),
+                          static_cast<uint32_t>(t));
+        ptx::mbar_arrive(qfull(slot));
+        ptx::mbar_remote_arrive_release(ptx::mapa(qfull(slot), 1));
+        return t;
+    };
+    auto consume = [&](int j) {  // every other role; all active lanes of a warp call it
+        const int slot = j % kTileQ;
+        int t = -1;
+        if (wait_bar<true>(qfull(slot), (j / kTileQ) & 1, q.abort, q.err)) t = tq[slot];
+        __syncwarp(__activemask());  // every lane has read the slot
+        if (lane == 0) {
+            if (q.rank == 0)
+                ptx::mbar_arrive(qempty(slot));
+            else
+                ptx::mbar_remote_arrive_release(ptx::mapa(qempty(slot), 0));
+        }
+        return t;
+    };
+
+    if (warp == 0 || warp == kWarpB) {
+        if (lane == 0) {
+            const uint32_t full_leader = ptx::mapa(q.full(0), 0);
+            Ring r;
+            int64_t issued = 0;
+            for (int j = 0;; ++j) {
+                const int t = consume(j);
+                if (t < 0) break;
+                const GradTile tl = grad_tile(a, t);
+                const int chunks = a.p[tl.p].chunks;
+                const bool mn = warp == 0 ? a.p[tl.p].a_mn != 0 : a.p[tl.p].b_mn != 0;
+                const CUtensorMap *m = warp == 0 ? &maps.a[tl.p] : &maps.b[tl.p];
+                const int row =
+                    (warp == 0 ? tl.m0 : tl.n0) + kHalfRows * static_cast<int>(q.rank);
+                const uint32_t base = q.ring + (warp == 0 ? 0 : kOpBytes);
+                for (int c = 0; c < chunks; ++c) {
+                    if (warp == 0)
+                        stage_begin<true>(q, r);
+                    else
+                        stage_begin<false>(q, r);
+                    const uint32_t to = base + r.s * kStageBytes, fb = full_leader + 8u * r.s;
+                    if (!mn) {
+                        tc::tma_load_2d_pair(to, m, 64 * c, row, fb);
+                    } else {
+                        tc::tma_load_2d_pair(to, m, row, 64 * c, fb);
+                        tc::tma_load_2d_pair(to + 8192, m, row + 64, 64 * c, fb);
+                    }
+                    r.next();
+                }
+                issued += chunks;
+            }
+            if (warp == 0) drain_loads(q, issued);
+        }
+    } else if (warp == 1) {
+        if (q.rank == 0 && lane == 0) {
+            Ring r;
+            for (int it = 0;; ++it) {
+                const int t = consume(it);
+                if (t < 0) break;
+                const GradProblem &P = a.p[grad_tile(a, t).p];
+                mma_tile<false>(q, r, it, P.chunks,
+                                tc::idesc_bf16_f32(256, 256, P.a_mn != 0, P.b_mn != 0, a.f16 != 0),
+                                P.a_mn != 0, P.b_mn != 0);
+            }
+            mma_finish(q);
+        }
+    } else if (warp == kWarpB + 1) {
+        if (q.rank == 0 && lane == 0) {
+            for (int j = 0;; ++j)
+                if (publish(j) < 0) break;
+        }
+    } else {
+        const int half = (warp - 2) >> 2;
+        uint32_t *stage = q.stage_words(warp - 2);
+        const uint32_t tempty_leader = ptx::mapa(q.tempty(0), 0);
+        for (int it = 0;; ++it) {
+            const int t = consume(it);
+            if (t < 0) break;
+            const GradTile tl = grad_tile(a, t);
+            const GradProblem &P = a.p[tl.p];
+            const int row0 = tl.m0 + kHalfRows * static_cast<int>(q.rank) + (warp & 3) * 32;
+            const uint32_t acc = acc_wait(q, it, warp);
+#pragma unroll 1
+            for (int c = 4 * half; c < 4 * half + 4; ++c) {
+                uint32_t r[32];
+                tc::tmem_ld32(acc + 32 * c, r);
+                tc::tmem_ld_wait();
+                const int col = tl.n0 + 32 * c;
+                if (col < P.N && row0 < P.M) {
+                    const int nr = min(32, P.M - row0), nc = min(32, P.N - col);
+                    if (P.f32) {
+                        if (lane < nr)
+                            store_f32(static_cast<float *>(P.C) + (row0 + lane) * P.ld + col, r, nc,
+                                      P.accumulate != 0);
+                    } else {
+                        float v[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+                        store_seg(static_cast<uint16_t *>(P.C) + row0 * P.ld + col, P.ld, v, nr, nc,
+                                  P.vec, a.f16 != 0, stage, lane);
+                    }
+                }
+                __syncwarp();
+            }
+            acc_release(tempty_leader, it, lane);
+        }
+    }
+    pair_teardown(q);
+}
+
+}  // namespace mm
+}  // namespace vlmce

@@ -1,0 +1,265 @@
+// mm_pair.cuh -- the machinery of the kernels that run on CTA pairs: a cluster of
+// 2 CTAs computes tiles of 256 x 256 with tcgen05.mma.cta_group::2, each CTA
+// staging its own 128 rows of either operand (128 bytes of K per row, 128-byte
+// swizzle) in a ring of 32 KB stages filled by TMA.
+//
+// Accumulators: two of 256 fp32 TMEM columns, so the epilogue of one tile
+// overlaps the products of the next.  Roles: one lane of warps 0 and 10 issues the
+// TMA loads of operand A and of operand B; warp 1 allocates TMEM and, in the
+// leader, one lane issues the MMAs; warps 2-9 epilogue: TMEM subpartition warp %
+// 4 (one row per thread), two warps per subpartition, each on half of the
+// columns.
+//
+// Operand layouts of a stage (16-bit operands): K-major, 128 rows of 64 K (8-row
+// groups 1024 B apart, a K step of 16 advances 32 B); MN-major, two boxes of 64
+// K rows x 64 M or N (8-row groups 1024 B apart, the boxes 8192 B apart, a K
+// step of 16 rows advances 2048 B).  8-bit operands: K-major, 128 K per row.
+#pragma once
+
+#include <cuda.h>
+
+#include "act.cuh"
+#include "mbar_wait.cuh"
+#include "ptx.cuh"
+#include "tcgen05.cuh"
+
+namespace vlmce {
+namespace mm {
+
+constexpr int kPairM = 256;                    // tokens of a pair tile
+constexpr int kHalfRows = 128;                 // rows of x, and of W, staged by one CTA
+constexpr int kOpBytes = kHalfRows * 128;      // one operand of a stage: 16 KB
+constexpr int kStageBytes = 2 * kOpBytes;
+constexpr int kStages = 6;
+constexpr int kPairThreads = 352;
+constexpr int kEpiWarps = 8;
+constexpr int kPairTmemCols = 512;
+constexpr int kPairBars = 2 * kStages + 5;    // full, empty, tmem full x2, tmem empty x2, drain
+constexpr int kPairTail = 8 * kPairBars + 16;  // barriers, TMEM slot, abort flag
+constexpr int kStageWords = 32 * 17;             // an epilogue warp's transposing buffer
+constexpr int kPairSmem = 1024 + kStages * kStageBytes + kPairTail + kEpiWarps * kStageWords * 4;
+
+
+// A CTA's view of the pair's pipeline.
+struct Pair {
+    unsigned char *smem;  // ring, then `tail`
+    uint32_t ring, bar0;
+    volatile int *abort;
+    int *err;
+    uint32_t rank;        // 0: the pair's leader
+    uint32_t tmem;
+
+    __device__ __forceinline__ uint32_t full(int s) const { return bar0 + 8u * s; }
+    __device__ __forceinline__ uint32_t empty(int s) const { return bar0 + 8u * (kStages + s); }
+    __device__ __forceinline__ uint32_t tfull(int b) const { return bar0 + 8u * (2 * kStages + b); }
+    __device__ __forceinline__ uint32_t tempty(int b) const {
+        return bar0 + 8u * (2 * kStages + 2 + b);
+    }
+    __device__ __forceinline__ uint32_t drain() const { return bar0 + 8u * (2 * kStages + 4); }
+    __device__ __forceinline__ uint32_t *stage_words(int epi_warp) const {
+        return reinterpret_cast<uint32_t *>(smem + kStages * kStageBytes + kPairTail) +
+               epi_warp * kStageWords;
+    }
+};
+
+// Position in the ring.
+struct Ring {
+    int s = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next() {
+        if (++s == kStages) {
+            s = 0;
+            ph ^= 1;
+        }
+    }
+};
+
+// All threads: barriers and TMEM; `more` initialises further barriers before the
+// cluster meets.  Then the next kernel of the stream may set itself up (TMEM is
+// held), and this one waits for its predecessor's results before it touches
+// global memory.
+template <class More>
+__device__ __forceinline__ Pair pair_setup(unsigned char *smem_raw, int *err, More more) {
+    Pair q;
+    q.smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    uint64_t *bars = reinterpret_cast<uint64_t *>(q.smem + kStages * kStageBytes);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kPairBars);
+    q.abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    q.ring = ptx::smem_addr(q.smem);
+    q.bar0 = ptx::smem_addr(bars);
+    q.err = err;
+    q.rank = ptx::cluster_ctarank();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            ptx::mbar_init(q.full(s), 1);   // leader: its producer + the bytes of both CTAs
+            ptx::mbar_init(q.empty(s), 1);  // one commit from the leader's MMA issuer
+        }
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(q.tfull(b), 1);
+            ptx::mbar_init(q.tempty(b), 2 * kEpiWarps);  // leader: both CTAs' epilogue warps
+        }
+        ptx::mbar_init(q.drain(), 1);
+        *q.abort = 0;
+        more();
+        ptx::fence_mbar_init_cluster();
+    }
+    if (threadIdx.x >> 5 == 1) {
+        tc::tmem_alloc_pair(ptx::smem_addr(tmem_slot), kPairTmemCols);
+        tc::tmem_relinquish_pair();
+    }
+    tc::fence_before_sync();
+    ptx::cluster_sync_any();
+    tc::fence_after_sync();
+    q.tmem = *tmem_slot;
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    return q;
+}
+// All threads, after every MMA of the pair has completed and every copy landed:
+// the pair meets before TMEM is released and either CTA exits.
+__device__ __forceinline__ void pair_teardown(const Pair &q) {
+    tc::fence_before_sync();
+    __syncthreads();
+    ptx::cluster_sync_any();
+    if (threadIdx.x >> 5 == 1) {
+        __syncwarp();
+        tc::fence_after_sync();
+        tc::tmem_dealloc_pair(q.tmem, kPairTmemCols);
+    }
+}
+
+// Producer lanes: wait for a stage's slot; operand A's lane of the leader announces
+// the stage's bytes (copies may land before that).
+constexpr int kWarpB = 10;
+template <bool A>
+__device__ __forceinline__ void stage_begin(const Pair &q, const Ring &r) {
+    wait_bar(q.empty(r.s), r.ph ^ 1, q.abort, q.err);
+    if (A && q.rank == 0) ptx::mbar_arrive_expect_tx(q.full(r.s), 2 * kStageBytes);
+}
+// Operand A's lane of the leader, at the end: every copy into the pair has landed
+// once the full phases of the last kStages loads completed.
+__device__ __forceinline__ void drain_loads(const Pair &q, int64_t issued) {
+    if (q.rank != 0) return;
+    for (int i = 0; i < kStages && i < issued; ++i) {
+        const int64_t k = issued - 1 - i;
+        drain_bar(q.full(static_cast<int>(k % kStages)), static_cast<uint32_t>((k / kStages) & 1),
+                  q.err);
+    }
+}
+// MMA lane of the leader: the products of the it-th tile.
+template <bool FP8>
+__device__ __forceinline__ void mma_tile(const Pair &q, Ring &r, int it, int chunks, uint32_t idesc,
+                                         bool a_mn, bool b_mn) {
+    const int b = it & 1;
+    wait_bar<true>(q.tempty(b), ((it >> 1) & 1) ^ 1, q.abort, q.err);
+    tc::fence_after_sync();
+    const uint32_t d = q.tmem + static_cast<uint32_t>(b * 256);
+    for (int c = 0; c < chunks; ++c) {
+        wait_bar(q.full(r.s), r.ph, q.abort, q.err);
+        tc::fence_after_sync();
+        const uint32_t sa = q.ring + r.s * kStageBytes, sb = sa + kOpBytes;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint64_t ad = a_mn ? tc::smem_desc_sw128(sa + 2048 * k, 8192, 1024)
+                                     : tc::smem_desc_sw128(sa + 32 * k, 16, 1024);
+            const uint64_t bd = b_mn ? tc::smem_desc_sw128(sb + 2048 * k, 8192, 1024)
+                                     : tc::smem_desc_sw128(sb + 32 * k, 16, 1024);
+            if constexpr (FP8)
+                tc::mma_f8_pair(d, ad, bd, idesc, (c | k) != 0);
+            else
+                tc::mma_bf16_pair(d, ad, bd, idesc, (c | k) != 0);
+        }
+        tc::mma_commit_pair(q.empty(r.s), 3u);  // the stage is free in both CTAs
+        r.next();
+    }
+    tc::mma_commit_pair(q.tfull(b), 3u);
+}
+__device__ __forceinline__ void mma_finish(const Pair &q) {
+    tc::mma_commit_pair(q.drain(), 1u);
+    drain_bar(q.drain(), 0, q.err);
+}
+// Epilogue warps: the it-th tile's accumulators (TMEM address of the warp's
+// lanes), and their release.
+__device__ __forceinline__ uint32_t acc_wait(const Pair &q, int it, int warp) {
+    wait_bar(q.tfull(it & 1), (it >> 1) & 1, q.abort, q.err);
+    tc::fence_after_sync();
+    return q.tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + (it & 1) * 256;
+}
+__device__ __forceinline__ void acc_release(uint32_t tempty_leader, int it, int lane) {
+    tc::fence_before_sync();
+    __syncwarp();
+    if (lane == 0) ptx::mbar_remote_arrive_release(tempty_leader + 8u * (it & 1));
+}
+
+// ---------------------------------------------------------- row segments
+// A warp's 32 rows x 32 consecutive 16-bit columns, one row per lane, `nr`
+// rows and `nc` columns of which exist.  vec: bytes an access may use where all
+// 32 columns exist (32, 16 or 2).  Rows without 16-byte alignment, and the last
+// columns, pass through `stage` (the warp's 32 x 17 words of shared memory),
+// so that a warp's accesses still cover consecutive addresses of a row.
+__device__ __forceinline__ void store_seg(uint16_t *base, int64_t ld, const float (&v)[32], int nr,
+                                          int nc, int vec, bool f16, uint32_t *stage, int lane) {
+    uint32_t u[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) u[j] = act::pack16x2(v[2 * j], v[2 * j + 1], f16);
+    if (nc == 32 && vec >= 16) {
+        if (lane >= nr) return;
+        uint16_t *p = base + lane * ld;
+        if (vec >= 32) {
+            ptx::st_global_v8(p, u[0], u[1], u[2], u[3], u[4], u[5], u[6], u[7]);
+            ptx::st_global_v8(p + 16, u[8], u[9], u[10], u[11], u[12], u[13], u[14], u[15]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<uint4 *>(p + 8 * j) =
+                    make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
+        }
+        return;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 16; ++j) stage[lane * 17 + j] = u[j];
+    __syncwarp();
+    const uint16_t *s16 = reinterpret_cast<const uint16_t *>(stage);
+    if (lane < nc) {
+#pragma unroll 8
+        for (int r = 0; r < nr; ++r) base[r * ld + lane] = s16[r * 34 + lane];
+    }
+}
+__device__ __forceinline__ void add_seg(const uint16_t *base, int64_t ld, float (&v)[32], int nr,
+                                        int nc, int vec, bool f16, uint32_t *stage, int lane) {
+    uint32_t u[16];
+    if (nc == 32 && vec >= 16) {
+        if (lane >= nr) return;
+        const uint16_t *p = base + lane * ld;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint4 q = *reinterpret_cast<const uint4 *>(p + 8 * j);
+            u[4 * j] = q.x;
+            u[4 * j + 1] = q.y;
+            u[4 * j + 2] = q.z;
+            u[4 * j + 3] = q.w;
+        }
+    } else {
+        uint16_t *s16 = reinterpret_cast<uint16_t *>(stage);
+        __syncwarp();
+        if (lane < nc) {
+#pragma unroll 8
+            for (int r = 0; r < nr; ++r) s16[r * 34 + lane] = base[r * ld + lane];
+        }
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) u[j] = stage[lane * 17 + j];
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        float a, b;
+        act::unpack16x2(u[j], a, b, f16);
+        v[2 * j] += a;
+        v[2 * j + 1] += b;
+    }
+}
+
+}  // namespace mm
+}  // namespace vlmce

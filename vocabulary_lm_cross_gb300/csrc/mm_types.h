@@ -47,5 +47,28 @@ struct Fwd {
 // Enqueue it (T, N, K >= 1); the kernel is chosen by the sizes.
 cudaError_t forward(const Fwd &f, cudaStream_t s);
 
+// The gradient products from dz [T, rows] (dz_ld a multiple of 8 elements, 16-bit
+// type of x and w, 16-byte aligned): dx [T, K] = dz W and dw [rows, K] = dz^T x,
+// either may be null.  ctr: a device word that is zero when the launch starts.
+struct Bwd {
+    const void *dz, *x, *w;
+    int64_t dz_ld, x_ld, w_ld;
+    int64_t T, rows, K;
+    int f16;
+    void *dx;
+    int64_t dx_ld;
+    void *dw;              // [rows, K] contiguous
+    int dw_f32, accumulate;
+    unsigned int *ctr;
+    int *err;
+};
+cudaError_t backward(const Bwd &b, cudaStream_t s);
+
+// Bytes (32, 16 or 2) an access to 32 consecutive 16-bit columns of a row may use.
+inline int vec_of(const void *p, int64_t ld) {
+    const uint64_t a = reinterpret_cast<uint64_t>(p) | static_cast<uint64_t>(2 * ld);
+    return a % 32 == 0 ? 32 : a % 16 == 0 ? 16 : 2;
+}
+
 }  // namespace mm
 }  // namespace vlmce
