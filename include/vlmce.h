@@ -390,8 +390,8 @@ vlmce_status linear_fwd(const void *x, int64_t x_stride, const float *x_scale, c
                         vlmce_stream_t stream);
 
 /* Bytes of device workspace linear_bwd / glu_bwd need (256-byte aligned): the
- * 16-bit gradient of the pre-activations, partial sums of dbias and a tile
- * counter.  0 for sizes they reject. */
+ * 16-bit gradient of the pre-activations and partial sums of dbias.  0 for sizes
+ * they reject. */
 size_t vlmce_linear_bwd_workspace_bytes(int64_t T, int64_t N, int64_t K);
 size_t vlmce_glu_bwd_workspace_bytes(int64_t T, int64_t n, int64_t K);
 

@@ -33,7 +33,6 @@ constexpr int kMaxRowChunks = 64;  // partial sums of db
 struct DzParams {
     const uint16_t *dy, *pre;
     uint16_t *dz;   // may be null (db only)
-    unsigned int *ctr;  // set to zero
     float *part;    // [row chunks][N] partial sums of dz's columns, may be null
     int64_t dy_ld, pre_ld, dz_ld;
     int64_t T, N;
@@ -70,7 +69,6 @@ __global__ void __launch_bounds__(32 * kDzWarps) dz_kernel(const DzParams p) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.ctr = 0;
     const int64_t col = (static_cast<int64_t>(blockIdx.x) * 32 + lane) * V;
     const int64_t r0 = blockIdx.y * p.rows_per_chunk;
     const int64_t r1 = min(p.T, r0 + p.rows_per_chunk);
@@ -325,19 +323,17 @@ struct BwdArgs {
     cudaStream_t stream;
 };
 
-constexpr int64_t kHead = 256;  // the GEMM launch's tile counter
-
 int64_t dz_ld_of(int64_t rows) { return round_up(rows, 8); }
 int64_t part_bytes(int64_t N) { return round_up(4 * kMaxRowChunks * N, 256); }
 bool bwd_sizes_ok(int64_t T, int64_t N, int64_t K) {
     return T >= 0 && N >= 1 && K >= 1 && T <= kMaxDim && N <= kMaxDim / 2 && K <= kMaxDim &&
            (T / 256 + 1 + N / 128 + 1) <= INT32_MAX / (K / 256 + 1);
 }
-// Head, dz [T, rows rounded to 8] and, for a linear layer, the partial sums of db.
+// dz [T, rows rounded to 8] and, for a linear layer, the partial sums of db.
 size_t bwd_workspace(int64_t T, int64_t N, int64_t K, bool gated) {
     if (!bwd_sizes_ok(T, N, K)) return 0;
     const int64_t ld = dz_ld_of(gated ? 2 * N : N);
-    return static_cast<size_t>(kHead + round_up(2 * T * ld, 256) + (gated ? 0 : part_bytes(N)));
+    return static_cast<size_t>(round_up(2 * T * ld, 256) + (gated ? 0 : part_bytes(N)));
 }
 
 vlmce_status backward(const BwdArgs &a, const char *where) {
@@ -388,14 +384,12 @@ vlmce_status backward(const BwdArgs &a, const char *where) {
     }
 
     unsigned char *ws = static_cast<unsigned char *>(a.workspace);
-    unsigned int *ctr = reinterpret_cast<unsigned int *>(ws);
-    uint16_t *dz = reinterpret_cast<uint16_t *>(ws + kHead);
+    uint16_t *dz = reinterpret_cast<uint16_t *>(ws);
     int64_t dz_ld = dz_ld_of(rows);
-    float *part = reinterpret_cast<float *>(ws + kHead + round_up(2 * a.T * dz_ld, 256));
+    float *part = reinterpret_cast<float *>(ws + round_up(2 * a.T * dz_ld, 256));
     const bool products = a.dx || a.dweight;
     const bool as_is = !need_pre && a.dy_stride % 8 == 0 && aligned(a.dy, 16) &&
                        a.dy_stride * 2 < (int64_t(1) << 40);
-    bool dz_ran = false;  // it also clears the tile counter
     if (a.dbias || (products && !as_is)) {
         DzParams p = {};
         p.dy = static_cast<const uint16_t *>(a.dy);
@@ -416,7 +410,6 @@ vlmce_status backward(const BwdArgs &a, const char *where) {
         chunks = std::min({chunks, (a.T + kDzWarps - 1) / kDzWarps, int64_t(kMaxRowChunks)});
         p.rows_per_chunk = (a.T + chunks - 1) / chunks;
         chunks = (a.T + p.rows_per_chunk - 1) / p.rows_per_chunk;
-        p.ctr = ctr;
         st = launch_status(launch(dz_kernel_of(a.act, a.gated, vec),
                                   dim3(static_cast<unsigned>(gx), static_cast<unsigned>(chunks), 1),
                                   32 * kDzWarps, a.stream, static_cast<const DzParams>(p)),
@@ -430,17 +423,12 @@ vlmce_status backward(const BwdArgs &a, const char *where) {
                                where);
             if (st != VLMCE_OK) return st;
         }
-        dz_ran = true;
     }
     if (!products) return VLMCE_OK;
     const uint16_t *g = dz;
     if (as_is) {
         g = static_cast<const uint16_t *>(a.dy);
         dz_ld = a.dy_stride;
-    }
-    if (!dz_ran) {
-        e = cudaMemsetAsync(ctr, 0, 4, a.stream);
-        if (e != cudaSuccess) return launch_status(e, where);
     }
     mm::Bwd b = {};
     b.dz = g;
@@ -458,7 +446,6 @@ vlmce_status backward(const BwdArgs &a, const char *where) {
     b.dw = a.dweight;
     b.dw_f32 = a.dweight_dtype == VLMCE_F32;
     b.accumulate = a.accumulate;
-    b.ctr = ctr;
     b.err = a.dev_err;
     return launch_status(mm::backward(b, a.stream), where);
 }

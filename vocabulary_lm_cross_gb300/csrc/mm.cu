@@ -109,9 +109,9 @@ cudaError_t setup(Capacity *out) {
             c.pairs = k == 0 ? n : std::min(c.pairs, n);
         }
         e = cudaFuncSetAttribute(mm_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kGradSmem);
+                                 kPairSmem);
         int n = 0;
-        if (e == cudaSuccess) e = clusters_of(mm_grad_kernel, 2, kGradThreads, kGradSmem, &n);
+        if (e == cudaSuccess) e = clusters_of(mm_grad_kernel, 2, kPairThreads, kPairSmem, &n);
         if (e != cudaSuccess) return e;
         c.pairs = std::min(c.pairs, n);
         e = cudaFuncSetAttribute(small_shape_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -238,7 +238,7 @@ Plan plan_of(const Fwd &f, const Capacity &cap) {
     return e.plan;
 }
 
-cudaError_t forward_large(const Fwd &f, int pairs, cudaStream_t s) {
+cudaError_t forward_large(const Fwd &f, cudaStream_t s) {
     CUtensorMap mx, mw;
     const int64_t rows = f.gated ? 2 * f.N : f.N;
     if (!operand_map(&mx, f.x, f.dtype, f.T, f.K, f.x_ld, kHalfRows) ||
@@ -253,13 +253,12 @@ cudaError_t forward_large(const Fwd &f, int pairs, cudaStream_t s) {
     p.nt = static_cast<int>(f.gated ? (f.N + 127) / 128 : (f.N + 255) / 256);
     const int64_t tiles = static_cast<int64_t>(p.mt) * p.nt;
     if (tiles * kGroupM > INT32_MAX) return cudaErrorInvalidConfiguration;
-    p.tiles = static_cast<int>(tiles);
     p.e = f.e;
     p.err = f.err;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     launch_attributes(attr, 2);
-    cfg.gridDim = dim3(2 * std::min(p.tiles, pairs), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * tiles), 1, 1);
     cfg.blockDim = dim3(kPairThreads, 1, 1);
     cfg.dynamicSmemBytes = kPairSmem;
     cfg.stream = s;
@@ -316,7 +315,7 @@ cudaError_t forward(const Fwd &f, cudaStream_t s) {
     const cudaError_t e = setup(&cap);
     if (e != cudaSuccess) return e;
     const Plan plan = plan_of(f, cap);
-    return plan.large ? forward_large(f, cap.pairs, s) : forward_small(f, plan, s);
+    return plan.large ? forward_large(f, s) : forward_small(f, plan, s);
 }
 
 cudaError_t backward(const Bwd &b, cudaStream_t s) {
@@ -326,7 +325,6 @@ cudaError_t backward(const Bwd &b, cudaStream_t s) {
     GradMaps maps;
     GradParams p = {};
     p.f16 = b.f16;
-    p.ctr = b.ctr;
     p.err = b.err;
     const bool f16 = b.f16 != 0;
     int64_t tiles = 0;
@@ -362,13 +360,12 @@ cudaError_t backward(const Bwd &b, cudaStream_t s) {
         }
     }
     if (!ok) return cudaErrorInvalidValue;
-    p.tiles = static_cast<int>(tiles);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     launch_attributes(attr, 2);
-    cfg.gridDim = dim3(2 * std::min(p.tiles, cap.pairs), 1, 1);
-    cfg.blockDim = dim3(kGradThreads, 1, 1);
-    cfg.dynamicSmemBytes = kGradSmem;
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * tiles), 1, 1);
+    cfg.blockDim = dim3(kPairThreads, 1, 1);
+    cfg.dynamicSmemBytes = kPairSmem;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;

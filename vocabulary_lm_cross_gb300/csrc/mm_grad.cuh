@@ -5,11 +5,7 @@
 // with either operand K-major or MN-major, so nothing is transposed in memory.
 //
 // The tiles of both products are numbered one after the other, the longer
-// inner size first, and taken in order from a counter: a scheduler warp of the
-// leader fetches numbers up to kTileQ ahead of the slowest role and publishes
-// them to both CTAs.  (dx tiles can be many times as long as dW tiles: dealt out
-// in advance, T = 4096, K = 6656, 2n = 32768 would leave pairs idle for one of
-// its 138 us dx tiles.)
+// inner size first.
 #pragma once
 
 #include <cuda.h>
@@ -19,12 +15,6 @@
 
 namespace vlmce {
 namespace mm {
-
-constexpr int kGradThreads = kPairThreads + 32;
-constexpr int kTileQ = 4;
-constexpr int kTileQConsumers = 5 + 2 * kEpiWarps;  // 4 producers, MMA issuer, epilogue warps
-constexpr int kQueueBytes = 8 * 2 * kTileQ + 4 * kTileQ;
-constexpr int kGradSmem = kPairSmem + kQueueBytes;
 
 // C[M, N] (+)= A B^T.
 struct GradProblem {
@@ -38,9 +28,8 @@ struct GradProblem {
 };
 struct GradParams {
     GradProblem p[2];
-    int nprob, tiles;
+    int nprob;
     int f16;
-    unsigned int *ctr;     // zero before the launch
     int *err;
 };
 struct GradMaps {
@@ -79,68 +68,25 @@ __device__ __forceinline__ void store_f32(float *c, const uint32_t (&r)[32], int
     }
 }
 
-__global__ void __launch_bounds__(kGradThreads, 1)
+__global__ void __launch_bounds__(kPairThreads, 1)
     mm_grad_kernel(const __grid_constant__ GradMaps maps, const __grid_constant__ GradParams a) {
     extern __shared__ unsigned char smem_raw[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    unsigned char *queue =
-        reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                          ~static_cast<uintptr_t>(1023)) +
-        kPairSmem - 1024;
-    const uint32_t qbar = ptx::smem_addr(queue);
-    volatile int *tq = reinterpret_cast<volatile int *>(queue + 8 * 2 * kTileQ);
-    auto qfull = [&](int i) { return qbar + 8u * i; };
-    auto qempty = [&](int i) { return qbar + 8u * (kTileQ + i); };
     if (threadIdx.x == 0) {
         for (int i = 0; i < a.nprob; ++i) {
             tc::prefetch_tensormap(&maps.a[i]);
             tc::prefetch_tensormap(&maps.b[i]);
         }
     }
-    const Pair q = pair_setup(smem_raw, a.err, [&] {
-        for (int i = 0; i < kTileQ; ++i) {
-            ptx::mbar_init(qfull(i), 1);                 // the scheduler's release-arrive
-            ptx::mbar_init(qempty(i), kTileQConsumers);  // used at the leader only
-        }
-    });
-
-    // The j-th tile of this pair (-1: none left, or a wait gave up).
-    auto publish = [&](int j) {  // the leader's scheduler lane
-        const int slot = j % kTileQ;
-        int t = -1;
-        if (j < kTileQ || wait_bar<true>(qempty(slot), ((j / kTileQ) - 1) & 1, q.abort, q.err)) {
-            const unsigned int u = atomicAdd(a.ctr, 1u);
-            t = u < static_cast<unsigned int>(a.tiles) ? static_cast<int>(u) : -1;
-        }
-        tq[slot] = t;
-        ptx::st_dsmem_u32(ptx::mapa(ptx::smem_addr(const_cast<int *>(tq) + slot), 1),
-                          static_cast<uint32_t>(t));
-        ptx::mbar_arrive(qfull(slot));
-        ptx::mbar_remote_arrive_release(ptx::mapa(qfull(slot), 1));
-        return t;
-    };
-    auto consume = [&](int j) {  // every other role; all active lanes of a warp call it
-        const int slot = j % kTileQ;
-        int t = -1;
-        if (wait_bar<true>(qfull(slot), (j / kTileQ) & 1, q.abort, q.err)) t = tq[slot];
-        __syncwarp(__activemask());  // every lane has read the slot
-        if (lane == 0) {
-            if (q.rank == 0)
-                ptx::mbar_arrive(qempty(slot));
-            else
-                ptx::mbar_remote_arrive_release(ptx::mapa(qempty(slot), 0));
-        }
-        return t;
-    };
+    const Pair q = pair_setup(smem_raw, a.err);
+    Tiles tiles;
 
     if (warp == 0 || warp == kWarpB) {
         if (lane == 0) {
             const uint32_t full_leader = ptx::mapa(q.full(0), 0);
             Ring r;
             int64_t issued = 0;
-            for (int j = 0;; ++j) {
-                const int t = consume(j);
-                if (t < 0) break;
+            for (int t; (t = tiles.next(q, lane)) >= 0;) {
                 const GradTile tl = grad_tile(a, t);
                 const int chunks = a.p[tl.p].chunks;
                 const bool mn = warp == 0 ? a.p[tl.p].a_mn != 0 : a.p[tl.p].b_mn != 0;
@@ -169,9 +115,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     } else if (warp == 1) {
         if (q.rank == 0 && lane == 0) {
             Ring r;
-            for (int it = 0;; ++it) {
-                const int t = consume(it);
-                if (t < 0) break;
+            int it = 0;
+            for (int t; (t = tiles.next(q, lane)) >= 0; ++it) {
                 const GradProblem &P = a.p[grad_tile(a, t).p];
                 mma_tile<false>(q, r, it, P.chunks,
                                 tc::idesc_bf16_f32(256, 256, P.a_mn != 0, P.b_mn != 0, a.f16 != 0),
@@ -179,18 +124,14 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             }
             mma_finish(q);
         }
-    } else if (warp == kWarpB + 1) {
-        if (q.rank == 0 && lane == 0) {
-            for (int j = 0;; ++j)
-                if (publish(j) < 0) break;
-        }
+    } else if (warp == kWarpTiles) {
+        if (q.rank == 0 && lane == 0) fetch_tiles(q);
     } else {
         const int half = (warp - 2) >> 2;
         uint32_t *stage = q.stage_words(warp - 2);
         const uint32_t tempty_leader = ptx::mapa(q.tempty(0), 0);
-        for (int it = 0;; ++it) {
-            const int t = consume(it);
-            if (t < 0) break;
+        int it = 0;
+        for (int t; (t = tiles.next(q, lane)) >= 0; ++it) {
             const GradTile tl = grad_tile(a, t);
             const GradProblem &P = a.p[tl.p];
             const int row0 = tl.m0 + kHalfRows * static_cast<int>(q.rank) + (warp & 3) * 32;

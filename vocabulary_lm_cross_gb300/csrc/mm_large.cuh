@@ -4,9 +4,8 @@
 // A tile is 256 tokens x 256 weight rows (mm_pair.cuh).  A gated layer's tile
 // takes 128 gate rows (staged by the pair's leader) and the 128 up rows of the
 // same outputs (staged by its peer), so gate and up of an output meet in one
-// thread.  Persistent grid of co-resident pairs; tile order: groups of kGroupM
-// token tiles, weight tiles outer within a group, so that the ~76 tiles in
-// flight read about 8 token and 9.5 weight tiles.
+// thread.  Tile order: groups of kGroupM token tiles, weight tiles outer within a
+// group, so that the ~76 tiles in flight read about 8 token and 9.5 weight tiles.
 #pragma once
 
 #include <cuda.h>
@@ -23,7 +22,7 @@ struct LargeParams {
     int T, N;          // tokens, outputs
     int up_row;        // gated: first up row of the weight
     int chunks;        // K in 128-byte chunks
-    int mt, nt, tiles;
+    int mt, nt;
     Epi e;
     int *err;
 };
@@ -109,9 +108,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         tc::prefetch_tensormap(&mx);
         tc::prefetch_tensormap(&mw);
     }
-    const Pair q = pair_setup(smem_raw, p.err, [] {});
-    const int first = static_cast<int>(ptx::cluster_id_x());
-    const int step = static_cast<int>(ptx::ncluster_x());
+    const Pair q = pair_setup(smem_raw, p.err);
+    Tiles tiles;
     const int rank = static_cast<int>(q.rank);
 
     if (warp == 0 || warp == kWarpB) {
@@ -120,7 +118,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const uint32_t full_leader = ptx::mapa(q.full(0), 0);
             Ring r;
             int64_t issued = 0;
-            for (int t = first; t < p.tiles; t += step) {
+            for (int t; (t = tiles.next(q, lane)) >= 0;) {
                 const LargeTile tl = large_tile<GATED>(p, t);
                 if (warp == 0) {
                     const int ar = tl.m0 + kHalfRows * rank;
@@ -149,16 +147,18 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const uint32_t idesc = tc::idesc_bf16_f32(256, 256, false, false, FP8 || p.e.f16);
             Ring r;
             int it = 0;
-            for (int t = first; t < p.tiles; t += step, ++it)
+            for (; tiles.next(q, lane) >= 0; ++it)
                 mma_tile<FP8>(q, r, it, p.chunks, idesc, false, false);
             mma_finish(q);
         }
+    } else if (warp == kWarpTiles) {
+        if (rank == 0 && lane == 0) fetch_tiles(q);
     } else {
         const int half = (warp - 2) >> 2;
         uint32_t *stage = q.stage_words(warp - 2);
         const uint32_t tempty_leader = ptx::mapa(q.tempty(0), 0);
         int it = 0;
-        for (int t = first; t < p.tiles; t += step, ++it) {
+        for (int t; (t = tiles.next(q, lane)) >= 0; ++it) {
             const LargeTile tl = large_tile<GATED>(p, t);
             const int64_t row0 = tl.m0 + kHalfRows * rank + (warp & 3) * 32;
             const float xs = p.e.xs && row0 + lane < p.T ? p.e.xs[row0 + lane] : 1.f;

@@ -8,7 +8,14 @@
 // TMA loads of operand A and of operand B; warp 1 allocates TMEM and, in the
 // leader, one lane issues the MMAs; warps 2-9 epilogue: TMEM subpartition warp %
 // 4 (one row per thread), two warps per subpartition, each on half of the
-// columns.
+// columns; warp 11 (leader) fetches the tiles.
+//
+// Tiles: one cluster is launched per tile, and the clusters that fit at once
+// stay: each takes over the work of one that has not started (cluster launch
+// control), one tile ahead of its slowest role.  So tiles are handed out in
+// order as pairs become free, without a counter in memory.  (Dealt out in
+// advance, T = 4096, K = 6656, 2n = 32768's gradient products would leave pairs
+// idle for one of its 138 us dx tiles.)
 //
 // Operand layouts of a stage (16-bit operands): K-major, 128 rows of 64 K (8-row
 // groups 1024 B apart, a K step of 16 advances 32 B); MN-major, two boxes of 64
@@ -31,11 +38,15 @@ constexpr int kHalfRows = 128;                 // rows of x, and of W, staged by
 constexpr int kOpBytes = kHalfRows * 128;      // one operand of a stage: 16 KB
 constexpr int kStageBytes = 2 * kOpBytes;
 constexpr int kStages = 6;
-constexpr int kPairThreads = 352;
+constexpr int kPairThreads = 384;
 constexpr int kEpiWarps = 8;
 constexpr int kPairTmemCols = 512;
-constexpr int kPairBars = 2 * kStages + 5;    // full, empty, tmem full x2, tmem empty x2, drain
-constexpr int kPairTail = 8 * kPairBars + 16;  // barriers, TMEM slot, abort flag
+constexpr int kWarpB = 10, kWarpTiles = 11;
+constexpr int kTileQ = 2;                      // answers about the next tile
+constexpr int kTileConsumers = 5 + 2 * kEpiWarps;  // 4 producers, MMA issuer, epilogue warps
+// full, empty, tmem full x2, tmem empty x2, drain, tile full x2, tile empty x2
+constexpr int kPairBars = 2 * kStages + 5 + 2 * kTileQ;
+constexpr int kPairTail = 16 * kTileQ + 8 * kPairBars + 16;  // answers, barriers, TMEM slot, abort flag
 constexpr int kStageWords = 32 * 17;             // an epilogue warp's transposing buffer
 constexpr int kPairSmem = 1024 + kStages * kStageBytes + kPairTail + kEpiWarps * kStageWords * 4;
 
@@ -56,6 +67,13 @@ struct Pair {
         return bar0 + 8u * (2 * kStages + 2 + b);
     }
     __device__ __forceinline__ uint32_t drain() const { return bar0 + 8u * (2 * kStages + 4); }
+    __device__ __forceinline__ uint32_t qfull(int i) const { return bar0 + 8u * (2 * kStages + 5 + i); }
+    __device__ __forceinline__ uint32_t qempty(int i) const {
+        return bar0 + 8u * (2 * kStages + 5 + kTileQ + i);
+    }
+    __device__ __forceinline__ uint32_t answer(int i) const {
+        return ring + kStages * kStageBytes + 16u * i;
+    }
     __device__ __forceinline__ uint32_t *stage_words(int epi_warp) const {
         return reinterpret_cast<uint32_t *>(smem + kStages * kStageBytes + kPairTail) +
                epi_warp * kStageWords;
@@ -74,16 +92,15 @@ struct Ring {
     }
 };
 
-// All threads: barriers and TMEM; `more` initialises further barriers before the
-// cluster meets.  Then the next kernel of the stream may set itself up (TMEM is
+// All threads: barriers and TMEM.  Then the next kernel of the stream may set itself up (TMEM is
 // held), and this one waits for its predecessor's results before it touches
 // global memory.
-template <class More>
-__device__ __forceinline__ Pair pair_setup(unsigned char *smem_raw, int *err, More more) {
+__device__ __forceinline__ Pair pair_setup(unsigned char *smem_raw, int *err) {
     Pair q;
     q.smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
-    uint64_t *bars = reinterpret_cast<uint64_t *>(q.smem + kStages * kStageBytes);
+    uint64_t *bars =
+        reinterpret_cast<uint64_t *>(q.smem + kStages * kStageBytes + 16 * kTileQ);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kPairBars);
     q.abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
     q.ring = ptx::smem_addr(q.smem);
@@ -100,8 +117,11 @@ __device__ __forceinline__ Pair pair_setup(unsigned char *smem_raw, int *err, Mo
             ptx::mbar_init(q.tempty(b), 2 * kEpiWarps);  // leader: both CTAs' epilogue warps
         }
         ptx::mbar_init(q.drain(), 1);
+        for (int i = 0; i < kTileQ; ++i) {
+            ptx::mbar_init(q.qfull(i), 1);                // the leader's fetching lane + 16 bytes
+            ptx::mbar_init(q.qempty(i), kTileConsumers);  // used at the leader only
+        }
         *q.abort = 0;
-        more();
         ptx::fence_mbar_init_cluster();
     }
     if (threadIdx.x >> 5 == 1) {
@@ -116,6 +136,45 @@ __device__ __forceinline__ Pair pair_setup(unsigned char *smem_raw, int *err, Mo
     ptx::griddep_wait();
     return q;
 }
+// The sequence of tiles of a pair, one object per role: the cluster's own, then
+// those it takes over; -1 after the last (or after a wait that gave up).  All
+// active lanes of a warp call next().
+struct Tiles {
+    int j = -1;
+    __device__ __forceinline__ int next(const Pair &q, int lane) {
+        if (++j == 0) return static_cast<int>(ptx::cluster_id_x());
+        const int i = (j - 1) % kTileQ;
+        int t = -1;
+        if (wait_bar<true>(q.qfull(i), ((j - 1) / kTileQ) & 1, q.abort, q.err)) {
+            t = ptx::clc_first_cta(q.answer(i));
+            if (t >= 0) t >>= 1;  // two CTAs per tile
+        }
+        ptx::fence_proxy_async_smem();  // the answer is read before it is overwritten
+        __syncwarp(__activemask());
+        if (lane == 0) {
+            if (q.rank == 0)
+                ptx::mbar_arrive(q.qempty(i));
+            else
+                ptx::mbar_remote_arrive_release(ptx::mapa(q.qempty(i), 0));
+        }
+        return t;
+    }
+};
+// The leader's fetching lane.
+__device__ __forceinline__ void fetch_tiles(const Pair &q) {
+    for (int n = 0;; ++n) {
+        const int i = n % kTileQ;
+        if (n >= kTileQ && !wait_bar<true>(q.qempty(i), ((n / kTileQ) - 1) & 1, q.abort, q.err))
+            return;
+        ptx::mbar_remote_arrive_expect_tx(ptx::mapa(q.qfull(i), 1), 16);
+        ptx::mbar_arrive_expect_tx(q.qfull(i), 16);
+        ptx::clc_try_cancel(q.answer(i), q.qfull(i));
+        if (!wait_bar<true>(q.qfull(i), (n / kTileQ) & 1, q.abort, q.err)) return;
+        if (ptx::clc_first_cta(q.answer(i)) < 0) return;
+        ptx::fence_proxy_async_smem();
+    }
+}
+
 // All threads, after every MMA of the pair has completed and every copy landed:
 // the pair meets before TMEM is released and either CTA exits.
 __device__ __forceinline__ void pair_teardown(const Pair &q) {
@@ -131,7 +190,6 @@ __device__ __forceinline__ void pair_teardown(const Pair &q) {
 
 // Producer lanes: wait for a stage's slot; operand A's lane of the leader announces
 // the stage's bytes (copies may land before that).
-constexpr int kWarpB = 10;
 template <bool A>
 __device__ __forceinline__ void stage_begin(const Pair &q, const Ring &r) {
     wait_bar(q.empty(r.s), r.ph ^ 1, q.abort, q.err);

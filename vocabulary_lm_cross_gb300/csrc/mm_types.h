@@ -49,7 +49,7 @@ cudaError_t forward(const Fwd &f, cudaStream_t s);
 
 // The gradient products from dz [T, rows] (dz_ld a multiple of 8 elements, 16-bit
 // type of x and w, 16-byte aligned): dx [T, K] = dz W and dw [rows, K] = dz^T x,
-// either may be null.  ctr: a device word that is zero when the launch starts.
+// either may be null.
 struct Bwd {
     const void *dz, *x, *w;
     int64_t dz_ld, x_ld, w_ld;
@@ -59,7 +59,6 @@ struct Bwd {
     int64_t dx_ld;
     void *dw;              // [rows, K] contiguous
     int dw_f32, accumulate;
-    unsigned int *ctr;
     int *err;
 };
 cudaError_t backward(const Bwd &b, cudaStream_t s);

@@ -172,6 +172,39 @@ __device__ __forceinline__ void prefetch_l2(const void *p) {
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
+// --------------------------------------------------- cluster launch control
+// Ask for a cluster of this grid that has not started yet: it will not be
+// launched, and the caller runs its work.  The 16-byte answer goes to `dst` and
+// 16 bytes are counted on `bar`, in every CTA of the cluster at these offsets.
+__device__ __forceinline__ void clc_try_cancel(uint32_t dst, uint32_t bar) {
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes"
+        ".multicast::cluster::all.b128 [%0], [%1];" ::"r"(dst),
+        "r"(bar)
+        : "memory");
+}
+// blockIdx.x of the first CTA of the cluster an answer grants, or -1: none left.
+__device__ __forceinline__ int clc_first_cta(uint32_t src) {
+    uint32_t ok, x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+        "ld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, _, _, _}, r;\n\t}"
+        : "=r"(ok), "=r"(x)
+        : "r"(src)
+        : "memory");
+    return ok ? static_cast<int>(x) : -1;
+}
+__device__ __forceinline__ void mbar_remote_arrive_expect_tx(uint32_t remote_bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(
+                     remote_bar),
+                 "r"(bytes)
+                 : "memory");
+}
+
 // ------------------------------------------------------------- arithmetic
 // 2^x on the MUFU unit (relative error about 2^-22; subnormals flushed).
 __device__ __forceinline__ float ex2(float x) {
