@@ -70,6 +70,7 @@ __device__ __forceinline__ void store_f32(float *c, const uint32_t (&r)[32], int
 
 __global__ void __launch_bounds__(kPairThreads, 1)
     mm_grad_kernel(const __grid_constant__ GradMaps maps, const __grid_constant__ GradParams a) {
+    constexpr int kPer = 1;
     extern __shared__ unsigned char smem_raw[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -78,13 +79,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             tc::prefetch_tensormap(&maps.b[i]);
         }
     }
-    const Pair q = pair_setup(smem_raw, a.err);
+    const Pair<kPer> q = pair_setup<kPer>(smem_raw, a.err);
     Tiles tiles;
 
     if (warp == 0 || warp == kWarpB) {
         if (lane == 0) {
             const uint32_t full_leader = ptx::mapa(q.full(0), 0);
-            Ring r;
+            Ring<kPer> r;
             int64_t issued = 0;
             for (int t; (t = tiles.next(q, lane)) >= 0;) {
                 const GradTile tl = grad_tile(a, t);
@@ -94,31 +95,36 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 const int row =
                     (warp == 0 ? tl.m0 : tl.n0) + kHalfRows * static_cast<int>(q.rank);
                 const uint32_t base = q.ring + (warp == 0 ? 0 : kOpBytes);
-                for (int c = 0; c < chunks; ++c) {
+                for (int c = 0; c < chunks; c += kPer) {
+                    const int n = min(kPer, chunks - c);
                     if (warp == 0)
-                        stage_begin<true>(q, r);
+                        stage_begin<true, kPer>(q, r, n);
                     else
-                        stage_begin<false>(q, r);
-                    const uint32_t to = base + r.s * kStageBytes, fb = full_leader + 8u * r.s;
-                    if (!mn) {
-                        tc::tma_load_2d_pair(to, m, 64 * c, row, fb);
-                    } else {
-                        tc::tma_load_2d_pair(to, m, row, 64 * c, fb);
-                        tc::tma_load_2d_pair(to + 8192, m, row + 64, 64 * c, fb);
+                        stage_begin<false, kPer>(q, r, n);
+                    const uint32_t fb = full_leader + 8u * r.s;
+                    for (int i = 0; i < n; ++i) {
+                        const uint32_t to = base + r.s * q.kStageBytes + i * kChunkBytes;
+                        const int k = 64 * (c + i);
+                        if (!mn) {
+                            tc::tma_load_2d_pair(to, m, k, row, fb);
+                        } else {
+                            tc::tma_load_2d_pair(to, m, row, k, fb);
+                            tc::tma_load_2d_pair(to + 8192, m, row + 64, k, fb);
+                        }
                     }
                     r.next();
                 }
-                issued += chunks;
+                issued += (chunks + kPer - 1) / kPer;
             }
             if (warp == 0) drain_loads(q, issued);
         }
     } else if (warp == 1) {
         if (q.rank == 0 && lane == 0) {
-            Ring r;
+            Ring<kPer> r;
             int it = 0;
             for (int t; (t = tiles.next(q, lane)) >= 0; ++it) {
                 const GradProblem &P = a.p[grad_tile(a, t).p];
-                mma_tile<false>(q, r, it, P.chunks,
+                mma_tile<false, kPer>(q, r, it, P.chunks,
                                 tc::idesc_bf16_f32(256, 256, P.a_mn != 0, P.b_mn != 0, a.f16 != 0),
                                 P.a_mn != 0, P.b_mn != 0);
             }

@@ -102,13 +102,14 @@ template <bool GATED, bool FP8>
 __global__ void __launch_bounds__(kPairThreads, 1)
     mm_large_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
                     const __grid_constant__ LargeParams p) {
+    constexpr int kPer = 2;
     extern __shared__ unsigned char smem_raw[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         tc::prefetch_tensormap(&mx);
         tc::prefetch_tensormap(&mw);
     }
-    const Pair q = pair_setup(smem_raw, p.err);
+    const Pair<kPer> q = pair_setup<kPer>(smem_raw, p.err);
     Tiles tiles;
     const int rank = static_cast<int>(q.rank);
 
@@ -116,39 +117,44 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         if (lane == 0) {
             constexpr int kElts = FP8 ? 128 : 64;  // K elements of a 128-byte chunk
             const uint32_t full_leader = ptx::mapa(q.full(0), 0);
-            Ring r;
+            Ring<kPer> r;
             int64_t issued = 0;
             for (int t; (t = tiles.next(q, lane)) >= 0;) {
                 const LargeTile tl = large_tile<GATED>(p, t);
                 if (warp == 0) {
                     const int ar = tl.m0 + kHalfRows * rank;
-                    for (int c = 0; c < p.chunks; ++c) {
-                        stage_begin<true>(q, r);
-                        tc::tma_load_2d_pair(q.ring + r.s * kStageBytes, &mx, c * kElts, ar,
-                                             full_leader + 8u * r.s);
+                    for (int c = 0; c < p.chunks; c += kPer) {
+                        const int n = min(kPer, p.chunks - c);
+                        stage_begin<true, kPer>(q, r, n);
+                        for (int i = 0; i < n; ++i)
+                            tc::tma_load_2d_pair(q.ring + r.s * q.kStageBytes + i * kChunkBytes, &mx,
+                                                 (c + i) * kElts, ar, full_leader + 8u * r.s);
                         r.next();
                     }
                 } else {
                     const int br = GATED ? (rank == 0 ? tl.n0 : p.up_row + tl.n0)
                                          : tl.n0 + kHalfRows * rank;
-                    for (int c = 0; c < p.chunks; ++c) {
-                        stage_begin<false>(q, r);
-                        tc::tma_load_2d_pair(q.ring + r.s * kStageBytes + kOpBytes, &mw, c * kElts,
-                                             br, full_leader + 8u * r.s);
+                    for (int c = 0; c < p.chunks; c += kPer) {
+                        const int n = min(kPer, p.chunks - c);
+                        stage_begin<false, kPer>(q, r, n);
+                        for (int i = 0; i < n; ++i)
+                            tc::tma_load_2d_pair(
+                                q.ring + r.s * q.kStageBytes + i * kChunkBytes + kOpBytes, &mw,
+                                (c + i) * kElts, br, full_leader + 8u * r.s);
                         r.next();
                     }
                 }
-                issued += p.chunks;
+                issued += (p.chunks + kPer - 1) / kPer;
             }
             if (warp == 0) drain_loads(q, issued);
         }
     } else if (warp == 1) {
         if (rank == 0 && lane == 0) {
             const uint32_t idesc = tc::idesc_bf16_f32(256, 256, false, false, FP8 || p.e.f16);
-            Ring r;
+            Ring<kPer> r;
             int it = 0;
             for (; tiles.next(q, lane) >= 0; ++it)
-                mma_tile<FP8>(q, r, it, p.chunks, idesc, false, false);
+                mma_tile<FP8, kPer>(q, r, it, p.chunks, idesc, false, false);
             mma_finish(q);
         }
     } else if (warp == kWarpTiles) {

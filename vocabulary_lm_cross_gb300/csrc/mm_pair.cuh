@@ -1,7 +1,7 @@
 // mm_pair.cuh -- the machinery of the kernels that run on CTA pairs: a cluster of
 // 2 CTAs computes tiles of 256 x 256 with tcgen05.mma.cta_group::2, each CTA
 // staging its own 128 rows of either operand (128 bytes of K per row, 128-byte
-// swizzle) in a ring of 32 KB stages filled by TMA.
+// swizzle) in a ring filled by TMA.
 //
 // Accumulators: two of 256 fp32 TMEM columns, so the epilogue of one tile
 // overlaps the products of the next.  Roles: one lane of warps 0 and 10 issues the
@@ -35,9 +35,10 @@ namespace mm {
 
 constexpr int kPairM = 256;                    // tokens of a pair tile
 constexpr int kHalfRows = 128;                 // rows of x, and of W, staged by one CTA
-constexpr int kOpBytes = kHalfRows * 128;      // one operand of a stage: 16 KB
-constexpr int kStageBytes = 2 * kOpBytes;
-constexpr int kStages = 6;
+constexpr int kOpBytes = kHalfRows * 128;      // one operand of a chunk (128 bytes of K): 16 KB
+constexpr int kChunkBytes = 2 * kOpBytes;
+constexpr int kRingChunks = 6;                 // 192 KB
+constexpr int kRingBytes = kRingChunks * kChunkBytes;
 constexpr int kPairThreads = 384;
 constexpr int kEpiWarps = 8;
 constexpr int kPairTmemCols = 512;
@@ -45,14 +46,20 @@ constexpr int kWarpB = 10, kWarpTiles = 11;
 constexpr int kTileQ = 2;                      // answers about the next tile
 constexpr int kTileConsumers = 5 + 2 * kEpiWarps;  // 4 producers, MMA issuer, epilogue warps
 // full, empty, tmem full x2, tmem empty x2, drain, tile full x2, tile empty x2
-constexpr int kPairBars = 2 * kStages + 5 + 2 * kTileQ;
+constexpr int kPairBars = 2 * kRingChunks + 5 + 2 * kTileQ;
 constexpr int kPairTail = 16 * kTileQ + 8 * kPairBars + 16;  // answers, barriers, TMEM slot, abort flag
 constexpr int kStageWords = 32 * 17;             // an epilogue warp's transposing buffer
-constexpr int kPairSmem = 1024 + kStages * kStageBytes + kPairTail + kEpiWarps * kStageWords * 4;
+constexpr int kPairSmem = 1024 + kRingBytes + kPairTail + kEpiWarps * kStageWords * 4;
 
 
-// A CTA's view of the pair's pipeline.
+// A CTA's view of the pair's pipeline; PER chunks make a stage (one barrier round
+// trip).  Two are faster where both operands are K-major (T 4096, K 6656, 2n 32768
+// forward 1065 -> 1048 us: 256 contiguous bytes of a row are fetched together), one
+// where an operand is MN-major (its gradient products 2158 against 2166 us).
+template <int PER>
 struct Pair {
+    static constexpr int kStages = kRingChunks / PER;
+    static constexpr int kStageBytes = PER * kChunkBytes;
     unsigned char *smem;  // ring, then `tail`
     uint32_t ring, bar0;
     volatile int *abort;
@@ -72,20 +79,21 @@ struct Pair {
         return bar0 + 8u * (2 * kStages + 5 + kTileQ + i);
     }
     __device__ __forceinline__ uint32_t answer(int i) const {
-        return ring + kStages * kStageBytes + 16u * i;
+        return ring + kRingBytes + 16u * i;
     }
     __device__ __forceinline__ uint32_t *stage_words(int epi_warp) const {
-        return reinterpret_cast<uint32_t *>(smem + kStages * kStageBytes + kPairTail) +
+        return reinterpret_cast<uint32_t *>(smem + kRingBytes + kPairTail) +
                epi_warp * kStageWords;
     }
 };
 
 // Position in the ring.
+template <int PER>
 struct Ring {
     int s = 0;
     uint32_t ph = 0;
     __device__ __forceinline__ void next() {
-        if (++s == kStages) {
+        if (++s == kRingChunks / PER) {
             s = 0;
             ph ^= 1;
         }
@@ -95,12 +103,13 @@ struct Ring {
 // All threads: barriers and TMEM.  Then the next kernel of the stream may set itself up (TMEM is
 // held), and this one waits for its predecessor's results before it touches
 // global memory.
-__device__ __forceinline__ Pair pair_setup(unsigned char *smem_raw, int *err) {
-    Pair q;
+template <int PER>
+__device__ __forceinline__ Pair<PER> pair_setup(unsigned char *smem_raw, int *err) {
+    Pair<PER> q;
     q.smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     uint64_t *bars =
-        reinterpret_cast<uint64_t *>(q.smem + kStages * kStageBytes + 16 * kTileQ);
+        reinterpret_cast<uint64_t *>(q.smem + kRingBytes + 16 * kTileQ);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kPairBars);
     q.abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
     q.ring = ptx::smem_addr(q.smem);
@@ -108,7 +117,7 @@ __device__ __forceinline__ Pair pair_setup(unsigned char *smem_raw, int *err) {
     q.err = err;
     q.rank = ptx::cluster_ctarank();
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < q.kStages; ++s) {
             ptx::mbar_init(q.full(s), 1);   // leader: its producer + the bytes of both CTAs
             ptx::mbar_init(q.empty(s), 1);  // one commit from the leader's MMA issuer
         }
@@ -141,7 +150,8 @@ __device__ __forceinline__ Pair pair_setup(unsigned char *smem_raw, int *err) {
 // active lanes of a warp call next().
 struct Tiles {
     int j = -1;
-    __device__ __forceinline__ int next(const Pair &q, int lane) {
+    template <int PER>
+    __device__ __forceinline__ int next(const Pair<PER> &q, int lane) {
         if (++j == 0) return static_cast<int>(ptx::cluster_id_x());
         const int i = (j - 1) % kTileQ;
         int t = -1;
@@ -161,7 +171,8 @@ struct Tiles {
     }
 };
 // The leader's fetching lane.
-__device__ __forceinline__ void fetch_tiles(const Pair &q) {
+template <int PER>
+__device__ __forceinline__ void fetch_tiles(const Pair<PER> &q) {
     for (int n = 0;; ++n) {
         const int i = n % kTileQ;
         if (n >= kTileQ && !wait_bar<true>(q.qempty(i), ((n / kTileQ) - 1) & 1, q.abort, q.err))
@@ -177,7 +188,8 @@ __device__ __forceinline__ void fetch_tiles(const Pair &q) {
 
 // All threads, after every MMA of the pair has completed and every copy landed:
 // the pair meets before TMEM is released and either CTA exits.
-__device__ __forceinline__ void pair_teardown(const Pair &q) {
+template <int PER>
+__device__ __forceinline__ void pair_teardown(const Pair<PER> &q) {
     tc::fence_before_sync();
     __syncthreads();
     ptx::cluster_sync_any();
@@ -188,16 +200,19 @@ __device__ __forceinline__ void pair_teardown(const Pair &q) {
     }
 }
 
-// Producer lanes: wait for a stage's slot; operand A's lane of the leader announces
+// Producer lanes: wait for a stage's slot, for n chunks; operand A's lane of the leader announces
 // the stage's bytes (copies may land before that).
-template <bool A>
-__device__ __forceinline__ void stage_begin(const Pair &q, const Ring &r) {
+template <bool A, int PER>
+__device__ __forceinline__ void stage_begin(const Pair<PER> &q, const Ring<PER> &r, int n) {
     wait_bar(q.empty(r.s), r.ph ^ 1, q.abort, q.err);
-    if (A && q.rank == 0) ptx::mbar_arrive_expect_tx(q.full(r.s), 2 * kStageBytes);
+    if (A && q.rank == 0)
+        ptx::mbar_arrive_expect_tx(q.full(r.s), static_cast<uint32_t>(n * 2 * kChunkBytes));
 }
 // Operand A's lane of the leader, at the end: every copy into the pair has landed
 // once the full phases of the last kStages loads completed.
-__device__ __forceinline__ void drain_loads(const Pair &q, int64_t issued) {
+template <int PER>
+__device__ __forceinline__ void drain_loads(const Pair<PER> &q, int64_t issued) {
+    constexpr int kStages = Pair<PER>::kStages;
     if (q.rank != 0) return;
     for (int i = 0; i < kStages && i < issued; ++i) {
         const int64_t k = issued - 1 - i;
@@ -206,40 +221,49 @@ __device__ __forceinline__ void drain_loads(const Pair &q, int64_t issued) {
     }
 }
 // MMA lane of the leader: the products of the it-th tile.
-template <bool FP8>
-__device__ __forceinline__ void mma_tile(const Pair &q, Ring &r, int it, int chunks, uint32_t idesc,
+template <bool FP8, int PER>
+__device__ __forceinline__ void mma_tile(const Pair<PER> &q, Ring<PER> &r, int it, int chunks, uint32_t idesc,
                                          bool a_mn, bool b_mn) {
     const int b = it & 1;
     wait_bar<true>(q.tempty(b), ((it >> 1) & 1) ^ 1, q.abort, q.err);
     tc::fence_after_sync();
     const uint32_t d = q.tmem + static_cast<uint32_t>(b * 256);
-    for (int c = 0; c < chunks; ++c) {
+    for (int c = 0; c < chunks; c += PER) {
         wait_bar(q.full(r.s), r.ph, q.abort, q.err);
         tc::fence_after_sync();
-        const uint32_t sa = q.ring + r.s * kStageBytes, sb = sa + kOpBytes;
+        const int n = min(PER, chunks - c);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint64_t ad = a_mn ? tc::smem_desc_sw128(sa + 2048 * k, 8192, 1024)
-                                     : tc::smem_desc_sw128(sa + 32 * k, 16, 1024);
-            const uint64_t bd = b_mn ? tc::smem_desc_sw128(sb + 2048 * k, 8192, 1024)
-                                     : tc::smem_desc_sw128(sb + 32 * k, 16, 1024);
-            if constexpr (FP8)
-                tc::mma_f8_pair(d, ad, bd, idesc, (c | k) != 0);
-            else
-                tc::mma_bf16_pair(d, ad, bd, idesc, (c | k) != 0);
+        for (int i = 0; i < PER; ++i) {
+            if (i < n) {
+                const uint32_t sa = q.ring + r.s * q.kStageBytes + i * kChunkBytes;
+                const uint32_t sb = sa + kOpBytes;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint64_t ad = a_mn ? tc::smem_desc_sw128(sa + 2048 * k, 8192, 1024)
+                                             : tc::smem_desc_sw128(sa + 32 * k, 16, 1024);
+                    const uint64_t bd = b_mn ? tc::smem_desc_sw128(sb + 2048 * k, 8192, 1024)
+                                             : tc::smem_desc_sw128(sb + 32 * k, 16, 1024);
+                    if constexpr (FP8)
+                        tc::mma_f8_pair(d, ad, bd, idesc, (c + i | k) != 0);
+                    else
+                        tc::mma_bf16_pair(d, ad, bd, idesc, (c + i | k) != 0);
+                }
+            }
         }
         tc::mma_commit_pair(q.empty(r.s), 3u);  // the stage is free in both CTAs
         r.next();
     }
     tc::mma_commit_pair(q.tfull(b), 3u);
 }
-__device__ __forceinline__ void mma_finish(const Pair &q) {
+template <int PER>
+__device__ __forceinline__ void mma_finish(const Pair<PER> &q) {
     tc::mma_commit_pair(q.drain(), 1u);
     drain_bar(q.drain(), 0, q.err);
 }
 // Epilogue warps: the it-th tile's accumulators (TMEM address of the warp's
 // lanes), and their release.
-__device__ __forceinline__ uint32_t acc_wait(const Pair &q, int it, int warp) {
+template <int PER>
+__device__ __forceinline__ uint32_t acc_wait(const Pair<PER> &q, int it, int warp) {
     wait_bar(q.tfull(it & 1), (it >> 1) & 1, q.abort, q.err);
     tc::fence_after_sync();
     return q.tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + (it & 1) * 256;
