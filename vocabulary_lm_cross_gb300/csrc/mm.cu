@@ -28,12 +28,20 @@ bool operand_map(CUtensorMap *m, const void *base, int32_t dtype, int64_t rows, 
     return gemm::make_tile_map(m, base, type, elt, K, rows, ld, 128 / elt, box_rows);
 }
 
+// A 16-bit (or fp32) output [rows, cols], stored in boxes of 128 bytes x 32 rows.
+bool output_map(CUtensorMap *m, const void *base, bool f32, int64_t rows, int64_t cols,
+                int64_t ld) {
+    return gemm::make_tile_map(
+        m, base, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+        f32 ? 4 : 2, cols, rows, ld, f32 ? 32 : 64, 32);
+}
+
 int chunks_of(const Fwd &f) {
     const int64_t bytes = f.K * (f.dtype == VLMCE_E4M3 ? 1 : 2);
     return static_cast<int>((bytes + 127) / 128);
 }
 
-using LargeKernel = void (*)(const CUtensorMap, const CUtensorMap, const LargeParams);
+using LargeKernel = void (*)(const LargeMaps, const LargeParams);
 using SmallKernel = void (*)(const CUtensorMap, const CUtensorMap, const SmallParams);
 
 LargeKernel large_kernel(bool gated, bool fp8) {
@@ -239,11 +247,17 @@ Plan plan_of(const Fwd &f, const Capacity &cap) {
 }
 
 cudaError_t forward_large(const Fwd &f, cudaStream_t s) {
-    CUtensorMap mx, mw;
+    LargeMaps maps = {};
     const int64_t rows = f.gated ? 2 * f.N : f.N;
-    if (!operand_map(&mx, f.x, f.dtype, f.T, f.K, f.x_ld, kHalfRows) ||
-        !operand_map(&mw, f.w, f.dtype, rows, f.K, f.w_ld, kHalfRows))
-        return cudaErrorInvalidValue;
+    const Epi &e = f.e;
+    bool ok = operand_map(&maps.x, f.x, f.dtype, f.T, f.K, f.x_ld, kHalfRows) &&
+              operand_map(&maps.w, f.w, f.dtype, rows, f.K, f.w_ld, kHalfRows);
+    if (e.y_vec >= 16) ok = ok && output_map(&maps.y, e.y, false, f.T, f.N, e.y_ld);
+    if (e.preact && e.preact_vec >= 16)
+        ok = ok && output_map(&maps.z, e.preact, false, f.T, f.N, e.preact_ld);
+    if (f.gated && e.preact && e.preact_up_vec >= 16)
+        ok = ok && output_map(&maps.z_up, e.preact + f.N, false, f.T, f.N, e.preact_ld);
+    if (!ok) return cudaErrorInvalidValue;
     LargeParams p = {};
     p.T = static_cast<int>(f.T);
     p.N = static_cast<int>(f.N);
@@ -264,7 +278,7 @@ cudaError_t forward_large(const Fwd &f, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, large_kernel(f.gated != 0, f.dtype == VLMCE_E4M3), mx, mw,
+    return cudaLaunchKernelEx(&cfg, large_kernel(f.gated != 0, f.dtype == VLMCE_E4M3), maps,
                               static_cast<const LargeParams>(p));
 }
 
@@ -333,7 +347,8 @@ cudaError_t backward(const Bwd &b, cudaStream_t s) {
                    int64_t K, void *C, int64_t ld, int f32, int accumulate) {
         GradProblem &q = p.p[p.nprob];
         ok = ok && gemm::make_operand_map(&maps.a[p.nprob], a, a_mn, M, K, a_ld, f16) &&
-             gemm::make_operand_map(&maps.b[p.nprob], w, true, b.K, K, w_ld, f16);
+             gemm::make_operand_map(&maps.b[p.nprob], w, true, b.K, K, w_ld, f16) &&
+             output_map(&maps.c[p.nprob], C, f32 != 0, M, b.K, ld);
         q.M = static_cast<int>(M);
         q.N = static_cast<int>(b.K);
         q.chunks = static_cast<int>((K + 63) / 64);
@@ -346,7 +361,6 @@ cudaError_t backward(const Bwd &b, cudaStream_t s) {
         q.accumulate = accumulate;
         q.C = C;
         q.ld = ld;
-        q.vec = vec_of(C, ld);
         tiles += static_cast<int64_t>(q.mt) * q.nt;
         ++p.nprob;
     };

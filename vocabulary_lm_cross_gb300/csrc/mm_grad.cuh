@@ -22,9 +22,8 @@ struct GradProblem {
     int a_mn, b_mn;
     int mt, nt, tile0;
     int f32, accumulate;   // C fp32 (added to where accumulate is set), else 16 bits
-    void *C;
+    void *C;               // rows 16-byte aligned
     int64_t ld;
-    int vec;               // 16-bit C: bytes an access may use
 };
 struct GradParams {
     GradProblem p[2];
@@ -33,7 +32,7 @@ struct GradParams {
     int *err;
 };
 struct GradMaps {
-    CUtensorMap a[2], b[2];
+    CUtensorMap a[2], b[2], c[2];
 };
 
 struct GradTile {
@@ -49,23 +48,6 @@ __device__ __forceinline__ GradTile grad_tile(const GradParams &a, int t) {
     const int gm = min(kGroup, P.mt - g * kGroup);
     const int n = r / gm;
     return {p, (g * kGroup + (r - n * gm)) * 256, n * 256};
-}
-
-// 32 fp32 columns of one row, nc of which exist (C rows are 16-byte aligned).
-__device__ __forceinline__ void store_f32(float *c, const uint32_t (&r)[32], int nc,
-                                          bool accumulate) {
-#pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-        if (j + 4 <= nc) {
-            float4 o = accumulate ? *reinterpret_cast<const float4 *>(c + j)
-                                  : make_float4(0.f, 0.f, 0.f, 0.f);
-            o.x += __uint_as_float(r[j]);
-            o.y += __uint_as_float(r[j + 1]);
-            o.z += __uint_as_float(r[j + 2]);
-            o.w += __uint_as_float(r[j + 3]);
-            *reinterpret_cast<float4 *>(c + j) = o;
-        }
-    }
 }
 
 __global__ void __launch_bounds__(kPairThreads, 1)
@@ -134,13 +116,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         if (q.rank == 0 && lane == 0) fetch_tiles(q);
     } else {
         const int half = (warp - 2) >> 2;
-        uint32_t *stage = q.stage_words(warp - 2);
+        uint32_t *buf = q.out_buffer(warp - 2);
         const uint32_t tempty_leader = ptx::mapa(q.tempty(0), 0);
         int it = 0;
         for (int t; (t = tiles.next(q, lane)) >= 0; ++it) {
             const GradTile tl = grad_tile(a, t);
             const GradProblem &P = a.p[tl.p];
-            const int row0 = tl.m0 + kHalfRows * static_cast<int>(q.rank) + (warp & 3) * 32;
+            const CUtensorMap *map = &maps.c[tl.p];
+            const int64_t row0 = tl.m0 + kHalfRows * static_cast<int>(q.rank) + (warp & 3) * 32;
+            const Out o = {static_cast<uint16_t *>(P.C), P.ld, 16, map};
             const uint32_t acc = acc_wait(q, it, warp);
 #pragma unroll 1
             for (int c = 4 * half; c < 4 * half + 4; ++c) {
@@ -148,24 +132,22 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 tc::tmem_ld32(acc + 32 * c, r);
                 tc::tmem_ld_wait();
                 const int col = tl.n0 + 32 * c;
-                if (col < P.N && row0 < P.M) {
-                    const int nr = min(32, P.M - row0), nc = min(32, P.N - col);
+                if (row0 < P.M) {
                     if (P.f32) {
-                        if (lane < nr)
-                            store_f32(static_cast<float *>(P.C) + (row0 + lane) * P.ld + col, r, nc,
-                                      P.accumulate != 0);
-                    } else {
+                        if (col < P.N) put_f32(map, row0, col, r, P.accumulate != 0, buf, lane);
+                    } else if (tl.n0 + 64 * (c >> 1) < P.N) {
                         float v[32];
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-                        store_seg(static_cast<uint16_t *>(P.C) + row0 * P.ld + col, P.ld, v, nr, nc,
-                                  P.vec, a.f16 != 0, stage, lane);
+                        put_seg(o, row0, tl.n0 + 64 * (c >> 1), c & 1, v, P.M, P.N, a.f16 != 0, buf,
+                                lane);
                     }
                 }
                 __syncwarp();
             }
             acc_release(tempty_leader, it, lane);
         }
+        if (lane == 0) tc::bulk_wait();
     }
     pair_teardown(q);
 }

@@ -39,75 +39,41 @@ __device__ __forceinline__ LargeTile large_tile(const LargeParams &p, int t) {
     return {(g * kGroupM + (r - n * gm)) * kPairM, n * (GATED ? 128 : 256)};
 }
 
-__device__ __forceinline__ void scale32(float (&v)[32], float xs, const float *ws, int nc) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-        if (j < nc) v[j] *= xs * ws[j];
-}
+struct LargeMaps {
+    CUtensorMap x, w;          // operands
+    CUtensorMap y, z, z_up;    // outputs with 16-byte aligned rows
+};
 
-// Epilogue of a warp's 32 tokens from row0 x 32 outputs from col (Epi in
-// mm_types.h), one token per lane.
-__device__ __forceinline__ void linear_seg(const LargeParams &p, const uint32_t (&r)[32], int64_t row0,
-                                           int col, float xs, uint32_t *stage, int lane) {
-    const Epi &e = p.e;
-    const bool f16 = e.f16 != 0;
-    const int nr = static_cast<int>(min(int64_t{32}, p.T - row0)), nc = min(32, p.N - col);
-    float v[32];
+// A warp's accumulators of 32 tokens (one per lane) x 32 outputs from `col`, as z:
+// scaled, the bias added.
+__device__ __forceinline__ void acc_seg(uint32_t acc, const Epi &e, int col, int scale_col, int N,
+                                        float xs, bool bias, float (&v)[32]) {
+    uint32_t r[32];
+    tc::tmem_ld32(acc, r);
+    tc::tmem_ld_wait();
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-    if (e.ws) scale32(v, xs, e.ws + col, nc);
-    if (e.bias) {
+    if (e.ws) {
 #pragma unroll
         for (int j = 0; j < 32; ++j)
-            if (j < nc) v[j] += act::from16(e.bias[col + j], f16);
+            if (col + j < N) v[j] *= xs * e.ws[scale_col + j];
     }
-    if (e.preact)
-        store_seg(e.preact + row0 * e.preact_ld + col, e.preact_ld, v, nr, nc, e.preact_vec, f16,
-                  stage, lane);
-    act::apply_n(v, e.act);
-    if (e.residual)
-        add_seg(e.residual + row0 * e.residual_ld + col, e.residual_ld, v, nr, nc, e.residual_vec,
-                f16, stage, lane);
-    store_seg(e.y + row0 * e.y_ld + col, e.y_ld, v, nr, nc, e.y_vec, f16, stage, lane);
-}
-__device__ __forceinline__ void gated_seg(const LargeParams &p, const uint32_t (&rg)[32],
-                                          const uint32_t (&ru)[32], int64_t row0, int col,
-                                          float xs,
-                                          uint32_t *stage, int lane) {
-    const Epi &e = p.e;
-    const bool f16 = e.f16 != 0;
-    const int nr = static_cast<int>(min(int64_t{32}, p.T - row0)), nc = min(32, p.N - col);
-    float g[32], u[32];
+    if (bias && e.bias) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-        g[j] = __uint_as_float(rg[j]);
-        u[j] = __uint_as_float(ru[j]);
+        for (int j = 0; j < 32; ++j)
+            if (col + j < N) v[j] += act::from16(e.bias[col + j], e.f16 != 0);
     }
-    if (e.ws) {
-        scale32(g, xs, e.ws + col, nc);
-        scale32(u, xs, e.ws + p.up_row + col, nc);
-    }
-    if (e.preact) {
-        uint16_t *z = e.preact + row0 * e.preact_ld + col;
-        store_seg(z, e.preact_ld, g, nr, nc, e.preact_vec, f16, stage, lane);
-        store_seg(z + p.N, e.preact_ld, u, nr, nc, e.preact_up_vec, f16, stage, lane);
-    }
-    act::apply_n(g, e.act);
-#pragma unroll
-    for (int j = 0; j < 32; ++j) g[j] *= u[j];
-    store_seg(e.y + row0 * e.y_ld + col, e.y_ld, g, nr, nc, e.y_vec, f16, stage, lane);
 }
 
 template <bool GATED, bool FP8>
 __global__ void __launch_bounds__(kPairThreads, 1)
-    mm_large_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
-                    const __grid_constant__ LargeParams p) {
+    mm_large_kernel(const __grid_constant__ LargeMaps maps, const __grid_constant__ LargeParams p) {
     constexpr int kPer = 2;
     extern __shared__ unsigned char smem_raw[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        tc::prefetch_tensormap(&mx);
-        tc::prefetch_tensormap(&mw);
+        tc::prefetch_tensormap(&maps.x);
+        tc::prefetch_tensormap(&maps.w);
     }
     const Pair<kPer> q = pair_setup<kPer>(smem_raw, p.err);
     Tiles tiles;
@@ -127,7 +93,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         const int n = min(kPer, p.chunks - c);
                         stage_begin<true, kPer>(q, r, n);
                         for (int i = 0; i < n; ++i)
-                            tc::tma_load_2d_pair(q.ring + r.s * q.kStageBytes + i * kChunkBytes, &mx,
+                            tc::tma_load_2d_pair(q.ring + r.s * q.kStageBytes + i * kChunkBytes, &maps.x,
                                                  (c + i) * kElts, ar, full_leader + 8u * r.s);
                         r.next();
                     }
@@ -139,7 +105,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         stage_begin<false, kPer>(q, r, n);
                         for (int i = 0; i < n; ++i)
                             tc::tma_load_2d_pair(
-                                q.ring + r.s * q.kStageBytes + i * kChunkBytes + kOpBytes, &mw,
+                                q.ring + r.s * q.kStageBytes + i * kChunkBytes + kOpBytes, &maps.w,
                                 (c + i) * kElts, br, full_leader + 8u * r.s);
                         r.next();
                     }
@@ -161,39 +127,68 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         if (rank == 0 && lane == 0) fetch_tiles(q);
     } else {
         const int half = (warp - 2) >> 2;
-        uint32_t *stage = q.stage_words(warp - 2);
+        uint32_t *buf = q.out_buffer(warp - 2);
         const uint32_t tempty_leader = ptx::mapa(q.tempty(0), 0);
+        const Epi &e = p.e;
+        const bool f16 = e.f16 != 0;
+        const Out y = {e.y, e.y_ld, e.y_vec, &maps.y};
+        const Out z = {e.preact, e.preact_ld, e.preact_vec, &maps.z};
+        const Out z_up = {e.preact + p.N, e.preact_ld, e.preact_up_vec, &maps.z_up};
+        const bool staged = y.vec < 16;  // y's segments leave the buffer empty
         int it = 0;
         for (int t; (t = tiles.next(q, lane)) >= 0; ++it) {
             const LargeTile tl = large_tile<GATED>(p, t);
             const int64_t row0 = tl.m0 + kHalfRows * rank + (warp & 3) * 32;
-            const float xs = p.e.xs && row0 + lane < p.T ? p.e.xs[row0 + lane] : 1.f;
+            const float xs = e.xs && row0 + lane < p.T ? e.xs[row0 + lane] : 1.f;
             const uint32_t acc = acc_wait(q, it, warp);
-            if constexpr (GATED) {
+            // 64 columns at a time: one group of a gated tile's 128 outputs per
+            // half, two of a linear tile's 256
+            constexpr int kGroups = GATED ? 1 : 2;
 #pragma unroll 1
-                for (int c = 2 * half; c < 2 * half + 2; ++c) {
-                    uint32_t rg[32], ru[32];
-                    tc::tmem_ld32(acc + 32 * c, rg);
-                    tc::tmem_ld32(acc + 128 + 32 * c, ru);
-                    tc::tmem_ld_wait();
-                    const int col = tl.n0 + 32 * c;
-                    if (col < p.N && row0 < p.T)
-                        gated_seg(p, rg, ru, row0, col, xs, stage, lane);
-                    __syncwarp();
+            for (int g = kGroups * half; g < kGroups * (half + 1); ++g) {
+                const int col = tl.n0 + 64 * g;
+                if (col >= p.N || row0 >= p.T) continue;
+                if (e.preact) {
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        float v[32];
+                        const int c = col + 32 * h;
+                        acc_seg(acc + 64 * g + 32 * h, e, c, c, p.N, xs, !GATED, v);
+                        put_seg(z, row0, col, h, v, p.T, p.N, f16, buf, lane);
+                    }
+                    if constexpr (GATED) {
+#pragma unroll 1
+                        for (int h = 0; h < 2; ++h) {
+                            float v[32];
+                            const int c = col + 32 * h;
+                            acc_seg(acc + 128 + 64 * g + 32 * h, e, c, p.up_row + c, p.N, xs,
+                                    false, v);
+                            put_seg(z_up, row0, col, h, v, p.T, p.N, f16, buf, lane);
+                        }
+                    }
                 }
-            } else {
 #pragma unroll 1
-                for (int c = 4 * half; c < 4 * half + 4; ++c) {
-                    uint32_t r[32];
-                    tc::tmem_ld32(acc + 32 * c, r);
-                    tc::tmem_ld_wait();
-                    const int col = tl.n0 + 32 * c;
-                    if (col < p.N && row0 < p.T) linear_seg(p, r, row0, col, xs, stage, lane);
+                for (int h = 0; h < 2; ++h) {
+                    float v[32];
+                    const int c = col + 32 * h;
+                    acc_seg(acc + 64 * g + 32 * h, e, c, c, p.N, xs, !GATED, v);
+                    act::apply_n(v, e.act);
+                    if constexpr (GATED) {
+                        float u[32];
+                        acc_seg(acc + 128 + 64 * g + 32 * h, e, c, p.up_row + c, p.N, xs, false, u);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] *= u[j];
+                    } else if (e.residual) {
+                        add_seg(e.residual, e.residual_ld, e.residual_vec, row0, c, v, p.T, p.N,
+                                f16, staged, buf, lane);
+                    }
                     __syncwarp();
+                    put_seg(y, row0, col, h, v, p.T, p.N, f16, buf, lane);
                 }
             }
             acc_release(tempty_leader, it, lane);
         }
+        if (lane == 0) tc::bulk_wait();
     }
     pair_teardown(q);
 }

@@ -48,8 +48,8 @@ constexpr int kTileConsumers = 5 + 2 * kEpiWarps;  // 4 producers, MMA issuer, e
 // full, empty, tmem full x2, tmem empty x2, drain, tile full x2, tile empty x2
 constexpr int kPairBars = 2 * kRingChunks + 5 + 2 * kTileQ;
 constexpr int kPairTail = 16 * kTileQ + 8 * kPairBars + 16;  // answers, barriers, TMEM slot, abort flag
-constexpr int kStageWords = 32 * 17;             // an epilogue warp's transposing buffer
-constexpr int kPairSmem = 1024 + kRingBytes + kPairTail + kEpiWarps * kStageWords * 4;
+constexpr int kOutBytes = 32 * 128;              // an epilogue warp's output buffer: 32 rows x 128 bytes
+constexpr int kPairSmem = 1024 + kRingBytes + kEpiWarps * kOutBytes + kPairTail;
 
 
 // A CTA's view of the pair's pipeline; PER chunks make a stage (one barrier round
@@ -60,7 +60,7 @@ template <int PER>
 struct Pair {
     static constexpr int kStages = kRingChunks / PER;
     static constexpr int kStageBytes = PER * kChunkBytes;
-    unsigned char *smem;  // ring, then `tail`
+    unsigned char *smem;  // ring, output buffers, tail
     uint32_t ring, bar0;
     volatile int *abort;
     int *err;
@@ -79,11 +79,10 @@ struct Pair {
         return bar0 + 8u * (2 * kStages + 5 + kTileQ + i);
     }
     __device__ __forceinline__ uint32_t answer(int i) const {
-        return ring + kRingBytes + 16u * i;
+        return ring + kRingBytes + kEpiWarps * kOutBytes + 16u * i;
     }
-    __device__ __forceinline__ uint32_t *stage_words(int epi_warp) const {
-        return reinterpret_cast<uint32_t *>(smem + kRingBytes + kPairTail) +
-               epi_warp * kStageWords;
+    __device__ __forceinline__ uint32_t *out_buffer(int epi_warp) const {
+        return reinterpret_cast<uint32_t *>(smem + kRingBytes + epi_warp * kOutBytes);
     }
 };
 
@@ -109,7 +108,7 @@ __device__ __forceinline__ Pair<PER> pair_setup(unsigned char *smem_raw, int *er
     q.smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     uint64_t *bars =
-        reinterpret_cast<uint64_t *>(q.smem + kRingBytes + 16 * kTileQ);
+        reinterpret_cast<uint64_t *>(q.smem + kRingBytes + kEpiWarps * kOutBytes + 16 * kTileQ);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kPairBars);
     q.abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
     q.ring = ptx::smem_addr(q.smem);
@@ -274,47 +273,71 @@ __device__ __forceinline__ void acc_release(uint32_t tempty_leader, int it, int 
     if (lane == 0) ptx::mbar_remote_arrive_release(tempty_leader + 8u * (it & 1));
 }
 
-// ---------------------------------------------------------- row segments
-// A warp's 32 rows x 32 consecutive 16-bit columns, one row per lane, `nr`
-// rows and `nc` columns of which exist.  vec: bytes an access may use where all
-// 32 columns exist (32, 16 or 2).  Rows without 16-byte alignment, and the last
-// columns, pass through `stage` (the warp's 32 x 17 words of shared memory),
-// so that a warp's accesses still cover consecutive addresses of a row.
-__device__ __forceinline__ void store_seg(uint16_t *base, int64_t ld, const float (&v)[32], int nr,
-                                          int nc, int vec, bool f16, uint32_t *stage, int lane) {
+// ---------------------------------------------------------- outputs
+// A warp's 32 rows x 64 consecutive columns of a 16-bit output come as two
+// segments of 32 columns, one row per lane.  Where the output's rows are 16-byte
+// aligned both are put into the warp's buffer (128-byte swizzle) and one TMA store
+// takes it to memory as whole 128-byte lines, leaving out what is not there; else
+// (`vec` = 2) a segment passes through the buffer on its own, so that a warp's
+// 2-byte accesses cover consecutive addresses of a row.
+struct Out {
+    uint16_t *base;
+    int64_t ld;
+    int vec;                 // bytes an access may use: >= 16, or 2
+    const CUtensorMap *map;  // boxes of 64 columns x 32 rows
+};
+
+// The warp's buffer may be written: its TMA stores have read it.
+__device__ __forceinline__ void buffer_free(int lane) {
+    if (lane == 0) tc::bulk_wait_read();
+    __syncwarp();
+}
+// Segment h (0 or 1) of the 64 columns from `col`.
+__device__ __forceinline__ void put_seg(const Out &o, int64_t row0, int col, int h,
+                                        const float (&v)[32], int64_t rows, int cols, bool f16,
+                                        uint32_t *buf, int lane) {
     uint32_t u[16];
 #pragma unroll
     for (int j = 0; j < 16; ++j) u[j] = act::pack16x2(v[2 * j], v[2 * j + 1], f16);
-    if (nc == 32 && vec >= 16) {
-        if (lane >= nr) return;
-        uint16_t *p = base + lane * ld;
-        if (vec >= 32) {
-            ptx::st_global_v8(p, u[0], u[1], u[2], u[3], u[4], u[5], u[6], u[7]);
-            ptx::st_global_v8(p + 16, u[8], u[9], u[10], u[11], u[12], u[13], u[14], u[15]);
-        } else {
+    if (o.vec >= 16) {
+        if (h == 0) buffer_free(lane);
+        unsigned char *row = reinterpret_cast<unsigned char *>(buf) + lane * 128;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<uint4 *>(p + 8 * j) =
-                    make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
+        for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4 *>(row + (((4 * h + j) ^ (lane & 7)) << 4)) =
+                make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
+        if (h == 1) {
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                tc::tma_store_2d(o.map, ptx::smem_addr(buf), col, static_cast<int>(row0));
+                tc::bulk_commit();
+            }
         }
         return;
     }
-    __syncwarp();
+    buffer_free(lane);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) stage[lane * 17 + j] = u[j];
+    for (int j = 0; j < 16; ++j) buf[lane * 17 + j] = u[j];
     __syncwarp();
-    const uint16_t *s16 = reinterpret_cast<const uint16_t *>(stage);
-    if (lane < nc) {
+    const int nr = static_cast<int>(min(int64_t{32}, rows - row0));
+    const uint16_t *s16 = reinterpret_cast<const uint16_t *>(buf);
+    uint16_t *p = o.base + row0 * o.ld + col + 32 * h + lane;
+    if (col + 32 * h + lane < cols) {
 #pragma unroll 8
-        for (int r = 0; r < nr; ++r) base[r * ld + lane] = s16[r * 34 + lane];
+        for (int r = 0; r < nr; ++r) p[r * o.ld] = s16[r * 34 + lane];
     }
 }
-__device__ __forceinline__ void add_seg(const uint16_t *base, int64_t ld, float (&v)[32], int nr,
-                                        int nc, int vec, bool f16, uint32_t *stage, int lane) {
+// v += the 32 columns from `col` of a 16-bit tensor; with `staged` unaligned rows
+// pass through the warp's buffer, which must hold nothing.
+__device__ __forceinline__ void add_seg(const uint16_t *base, int64_t ld, int vec, int64_t row0,
+                                        int col, float (&v)[32], int64_t rows, int cols, bool f16,
+                                        bool staged, uint32_t *buf, int lane) {
     uint32_t u[16];
-    if (nc == 32 && vec >= 16) {
-        if (lane >= nr) return;
-        const uint16_t *p = base + lane * ld;
+    const uint16_t *p = base + (row0 + lane) * ld + col;
+    const bool row_ok = row0 + lane < rows;
+    if (vec >= 16 && col + 32 <= cols) {
+        if (!row_ok) return;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const uint4 q = *reinterpret_cast<const uint4 *>(p + 8 * j);
@@ -323,16 +346,23 @@ __device__ __forceinline__ void add_seg(const uint16_t *base, int64_t ld, float 
             u[4 * j + 2] = q.z;
             u[4 * j + 3] = q.w;
         }
-    } else {
-        uint16_t *s16 = reinterpret_cast<uint16_t *>(stage);
-        __syncwarp();
-        if (lane < nc) {
+    } else if (staged) {
+        const int nr = static_cast<int>(min(int64_t{32}, rows - row0));
+        uint16_t *s16 = reinterpret_cast<uint16_t *>(buf);
+        const uint16_t *q = base + row0 * ld + col + lane;
+        buffer_free(lane);
+        if (col + lane < cols) {
 #pragma unroll 8
-            for (int r = 0; r < nr; ++r) s16[r * 34 + lane] = base[r * ld + lane];
+            for (int r = 0; r < nr; ++r) s16[r * 34 + lane] = q[r * ld];
         }
         __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) u[j] = stage[lane * 17 + j];
+        for (int j = 0; j < 16; ++j) u[j] = buf[lane * 17 + j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (row_ok && col + j < cols) v[j] += act::from16(p[j], f16);
+        return;
     }
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
@@ -340,6 +370,26 @@ __device__ __forceinline__ void add_seg(const uint16_t *base, int64_t ld, float 
         act::unpack16x2(u[j], a, b, f16);
         v[2 * j] += a;
         v[2 * j + 1] += b;
+    }
+}
+// 32 fp32 columns from `col` (boxes of 32 columns x 32 rows): stored, or added.
+__device__ __forceinline__ void put_f32(const CUtensorMap *map, int64_t row0, int col,
+                                        const uint32_t (&r)[32], bool add, uint32_t *buf,
+                                        int lane) {
+    buffer_free(lane);
+    unsigned char *row = reinterpret_cast<unsigned char *>(buf) + lane * 128;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        *reinterpret_cast<uint4 *>(row + ((j ^ (lane & 7)) << 4)) =
+            make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        if (add)
+            tc::tma_add_2d(map, ptx::smem_addr(buf), col, static_cast<int>(row0));
+        else
+            tc::tma_store_2d(map, ptx::smem_addr(buf), col, static_cast<int>(row0));
+        tc::bulk_commit();
     }
 }
 

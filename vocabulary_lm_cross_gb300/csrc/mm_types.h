@@ -29,7 +29,7 @@ struct Epi {
     int64_t residual_ld;
     const float *xs, *ws;
     int act, f16;
-    // bytes (32, 16 or 2) that accesses of whole 32-column groups may use
+    // vec_of() of the tensors
     int y_vec, preact_vec, preact_up_vec, residual_vec;
 };
 
@@ -63,10 +63,11 @@ struct Bwd {
 };
 cudaError_t backward(const Bwd &b, cudaStream_t s);
 
-// Bytes (32, 16 or 2) an access to 32 consecutive 16-bit columns of a row may use.
+// Bytes (16 or 2) an access to 32 consecutive 16-bit columns of a row may use; 16
+// also means that a tensor map can describe the rows.
 inline int vec_of(const void *p, int64_t ld) {
     const uint64_t a = reinterpret_cast<uint64_t>(p) | static_cast<uint64_t>(2 * ld);
-    return a % 32 == 0 ? 32 : a % 16 == 0 ? 16 : 2;
+    return a % 16 == 0 && ld < (int64_t{1} << 39) ? 16 : 2;
 }
 
 }  // namespace mm
