@@ -2,11 +2,17 @@
 // derivatives in fp32, and 16-bit element access (bf16 or fp16 at run time).
 //
 //   silu       a s(a)                       s(a) = 1 / (1 + e^-a)
-//   gelu       a P(a)                       P(a) = erfc(-a / sqrt 2) / 2, the normal CDF
+//   gelu       a P(a)                       P: the normal CDF
 //   gelu_tanh  a s(2 c0 (a + c1 a^3))       (1 + tanh v) / 2 = s(2 v); c0 = sqrt(2/pi), c1 = 0.044715
 //   relu       max(a, 0), NaN kept
 //
-// erfc keeps the relative accuracy of P for negative a, where 1 + erf cancels.
+// P(-x) = e^(-x^2/2) R(x) / 2 for x >= 0, with the scaled complementary error
+// function R(x) = e^(x^2/2) erfc(x / sqrt 2) as t p(t), t = 1 / (1 + 0.3 x / sqrt 2)
+// and p of degree 8: a least-squares fit, reweighted towards the smallest largest
+// relative error (2e-8 for x <= 13.4, beyond which e^(-x^2/2) is 0 in fp32).  So
+// the relative accuracy holds for negative a too (1 + erf would cancel; 9e-7 for
+// a > -4, 8e-6 for a > -13 in fp32), one exponential serves P and its derivative,
+// and there is no branch (T 1007, K 1000, N 777 with erfcf: 15.1 us, so: 13.9 us).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -29,12 +35,30 @@ constexpr float kC1 = 0.044715f;
 __device__ __forceinline__ float sigmoid(float a) {
     return ptx::rcp(1.f + ptx::ex2(-a * kLog2e));
 }
-__device__ __forceinline__ float cdf(float a) { return 0.5f * erfcf(-0.70710678f * a); }
+// P(a) and e^(-a^2/2).
+__device__ __forceinline__ float cdf(float a, float &e) {
+    e = ptx::ex2(-0.5f * kLog2e * a * a);
+    const float t = ptx::rcp(fmaf(0.3f * 0.70710678f, fabsf(a), 1.f));
+    float p = -0.12943436f;
+    p = fmaf(p, t, 0.48509780f);
+    p = fmaf(p, t, -0.51122928f);
+    p = fmaf(p, t, 0.54639840f);
+    p = fmaf(p, t, -0.09363360f);
+    p = fmaf(p, t, 0.21443731f);
+    p = fmaf(p, t, 0.14848216f);
+    p = fmaf(p, t, 0.17069197f);
+    p = fmaf(p, t, 0.16918962f);
+    const float q = 0.5f * t * p * e;
+    return a < 0.f ? q : 1.f - q;
+}
 
 template <int ACT>
 __device__ __forceinline__ float fwd(float a) {
     if constexpr (ACT == VLMCE_ACT_SILU) return a * sigmoid(a);
-    if constexpr (ACT == VLMCE_ACT_GELU) return a * cdf(a);
+    if constexpr (ACT == VLMCE_ACT_GELU) {
+        float e;
+        return a * cdf(a, e);
+    }
     if constexpr (ACT == VLMCE_ACT_GELU_TANH)
         return a * sigmoid(kC0x2 * fmaf(kC1 * a * a, a, a));
     if constexpr (ACT == VLMCE_ACT_RELU) return a < 0.f ? 0.f : a;
@@ -52,9 +76,10 @@ __device__ __forceinline__ void fwd_bwd(float a, float &f, float &d) {
         f = a * s;
         d = fmaf(c * s, 1.f - s, s);
     } else if constexpr (ACT == VLMCE_ACT_GELU) {
-        const float p = cdf(a);
+        float e;
+        const float p = cdf(a, e);
         f = a * p;
-        d = fmaf(c, 0.3989422804f * ptx::ex2(-0.5f * kLog2e * c * c), p);
+        d = fmaf(c, 0.3989422804f * e, p);
     } else if constexpr (ACT == VLMCE_ACT_GELU_TANH) {
         const float s = sigmoid(kC0x2 * fmaf(kC1 * a * a, a, a));
         f = a * s;

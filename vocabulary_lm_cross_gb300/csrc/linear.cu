@@ -18,6 +18,7 @@
 #include <cmath>
 
 #include "act.cuh"
+#include "colsum.cuh"
 #include "host_util.h"
 #include "mm_types.h"
 #include "vlmce.h"
@@ -126,16 +127,6 @@ __global__ void __launch_bounds__(32 * kDzWarps) dz_kernel(const DzParams p) {
             }
         }
     }
-}
-
-__global__ void db_kernel(const float *part, int chunks, int64_t N, float *db, int accumulate) {
-    ptx::griddep_launch_dependents();
-    ptx::griddep_wait();
-    const int64_t n = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-    if (n >= N) return;
-    float a = 0.f;
-    for (int c = 0; c < chunks; ++c) a += part[c * N + n];
-    db[n] = accumulate ? db[n] + a : a;
 }
 
 using DzKernel = void (*)(const DzParams);
@@ -416,10 +407,10 @@ vlmce_status backward(const BwdArgs &a, const char *where) {
                            where);
         if (st != VLMCE_OK) return st;
         if (a.dbias) {
-            st = launch_status(launch(db_kernel, dim3(static_cast<unsigned>((a.N + 255) / 256), 1, 1),
-                                      256, a.stream, static_cast<const float *>(part),
-                                      static_cast<int>(chunks), a.N, a.dbias,
-                                      static_cast<int>(a.accumulate)),
+            const colsum::Params d = {part, a.dbias, a.N, static_cast<int>(chunks), a.accumulate};
+            st = launch_status(launch(colsum::kernel<colsum::kWarps>,
+                                      dim3(colsum::blocks(a.N), 1, 1), 32 * colsum::kWarps,
+                                      a.stream, d),
                                where);
             if (st != VLMCE_OK) return st;
         }

@@ -20,6 +20,7 @@
 #include <cmath>
 
 #include "act.cuh"
+#include "colsum.cuh"
 #include "host_util.h"
 #include "ptx.cuh"
 #include "vlmce.h"
@@ -559,34 +560,6 @@ __global__ void __launch_bounds__(512) segment_kernel(const BwdParams p) {
     }
 }
 
-constexpr int kDwWarps = 32;
-struct DwParams {
-    const float *part;
-    float *dw;
-    int64_t H;
-    int parts, accumulate;
-};
-__global__ void __launch_bounds__(32 * kDwWarps) dw_kernel(const DwParams p) {
-    __shared__ float sh[kDwWarps][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 32 + lane;
-    ptx::griddep_launch_dependents();
-    ptx::griddep_wait();
-    float a = 0.f;
-    if (i < p.H) {
-#pragma unroll 8
-        for (int q = warp; q < p.parts; q += kDwWarps) a += p.part[q * p.H + i];
-    }
-    sh[warp][lane] = a;
-    __syncthreads();
-    if (warp == 0 && i < p.H) {
-        a = 0.f;
-#pragma unroll
-        for (int w = 0; w < kDwWarps; ++w) a += sh[w][lane];
-        p.dw[i] = p.accumulate ? p.dw[i] + a : a;
-    }
-}
-
 // ------------------------------------------------------------ host side
 constexpr int64_t kMaxH = INT64_C(1) << 30;
 // CTAs whose partial dw the workspace holds (SMs x CTAs of one SM).
@@ -931,8 +904,8 @@ extern "C" vlmce_status rmsnorm_bwd(const void *dy, int64_t dy_stride, const voi
     }
     st = launch_status(e, "rmsnorm_bwd");
     if (st != VLMCE_OK || !dweight) return st;
-    DwParams d = {p.part, dweight, H, static_cast<int>(parts), accumulate_dweight};
-    return launch_status(launch(dw_kernel, dim3(static_cast<unsigned>((H + 31) / 32), 1, 1),
-                                32 * kDwWarps, 0, s, d),
+    const colsum::Params d = {p.part, dweight, H, static_cast<int>(parts), accumulate_dweight};
+    return launch_status(launch(colsum::kernel<colsum::kWarps>, dim3(colsum::blocks(H), 1, 1),
+                                32 * colsum::kWarps, 0, s, d),
                          "rmsnorm_bwd");
 }
