@@ -37,7 +37,7 @@ struct Elt {
 
 // E consecutive elements at element index i of a row (E = 16 bytes' worth, or 1).
 template <int DT, int E>
-__device__ __forceinline__ void load_e(const void *row, int64_t i, float (&v)[E]) {
+__device__ __forceinline__ void load_e(const void *row, int i, float (&v)[E]) {
     if constexpr (E == 1) {
         if constexpr (DT == VLMCE_F32)
             v[0] = static_cast<const float *>(row)[i];
@@ -58,7 +58,7 @@ __device__ __forceinline__ void load_e(const void *row, int64_t i, float (&v)[E]
     }
 }
 template <int DT, int E>
-__device__ __forceinline__ void store_e(void *row, int64_t i, const float (&v)[E]) {
+__device__ __forceinline__ void store_e(void *row, int i, const float (&v)[E]) {
     if constexpr (E == 1) {
         if constexpr (DT == VLMCE_F32)
             static_cast<float *>(row)[i] = v[0];
@@ -75,7 +75,7 @@ __device__ __forceinline__ void store_e(void *row, int64_t i, const float (&v)[E
     }
 }
 template <int E>
-__device__ __forceinline__ void store_e4m3(unsigned char *row, int64_t i, const float (&v)[E]) {
+__device__ __forceinline__ void store_e4m3(unsigned char *row, int i, const float (&v)[E]) {
     if constexpr (E == 1) {
         row[i] = __nv_cvt_float_to_fp8(v[0], __NV_SATFINITE, __NV_E4M3);
     } else {
@@ -95,7 +95,7 @@ __device__ __forceinline__ void store_e4m3(unsigned char *row, int64_t i, const 
 }
 // The weight has the rows' type or fp32.
 template <int DT, int E>
-__device__ __forceinline__ void load_w(const void *w, bool f32, int64_t i, float offset,
+__device__ __forceinline__ void load_w(const void *w, bool f32, int i, float offset,
                                        float (&v)[E]) {
     if (DT == VLMCE_F32 || !f32) {
         load_e<DT, E>(w, i, v);
@@ -147,7 +147,8 @@ struct FwdParams {
     const void *weight;
     unsigned char *y, *sum;
     float *rstd, *scale;
-    int64_t T, H;
+    int64_t T;
+    int H;
     int64_t x_ld, residual_ld, y_ld, sum_ld;  // bytes
     float eps, offset;
     int w_f32;
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(1024) fwd_kernel(const FwdParams p) {
     constexpr int kHold = NG > 0 ? NG : 1;
     float v[kHold][E];
     float ss = 0.f, mx = 0.f;
-    auto sum_at = [&](int64_t i, float (&s)[E]) {
+    auto sum_at = [&](int i, float (&s)[E]) {
         load_e<DT, E>(x, i, s);
         if (res) {
             float r[E];
@@ -178,7 +179,7 @@ __global__ void __launch_bounds__(1024) fwd_kernel(const FwdParams p) {
             for (int j = 0; j < E; ++j) s[j] += r[j];
         }
     };
-    auto fold = [&](int64_t i, const float (&s)[E]) {
+    auto fold = [&](int i, const float (&s)[E]) {
 #pragma unroll
         for (int j = 0; j < E; ++j) ss = fmaf(s[j], s[j], ss);
         if constexpr (QUANT) {
@@ -188,8 +189,8 @@ __global__ void __launch_bounds__(1024) fwd_kernel(const FwdParams p) {
             for (int j = 0; j < E; ++j) mx = fmaxf(mx, fabsf(s[j] * w[j]));
         }
     };
-    const int64_t step = static_cast<int64_t>(blockDim.x) * E;
-    const int64_t i0 = static_cast<int64_t>(threadIdx.x) * E;
+    const int step = static_cast<int>(blockDim.x) * E;
+    const int i0 = static_cast<int>(threadIdx.x) * E;
     if constexpr (NG > 0) {
 #pragma unroll
         for (int k = 0; k < NG; ++k)
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(1024) fwd_kernel(const FwdParams p) {
                 if (sum) store_e<DT, E>(sum, i0 + k * step, v[k]);
             }
     } else {
-        for (int64_t i = i0; i < p.H; i += step) {
+        for (int i = i0; i < p.H; i += step) {
             sum_at(i, v[0]);
             fold(i, v[0]);
         }
@@ -214,7 +215,7 @@ __global__ void __launch_bounds__(1024) fwd_kernel(const FwdParams p) {
         if constexpr (QUANT) p.scale[row] = rstd * mx / 448.f;
     }
     const float mul = QUANT ? 448.f / mx : rstd;
-    auto emit = [&](int64_t i, const float (&s)[E]) {
+    auto emit = [&](int i, const float (&s)[E]) {
         float w[E], o[E];
         load_w<DT, E>(p.weight, p.w_f32 != 0, i, p.offset, w);
         if constexpr (QUANT) {
@@ -232,7 +233,7 @@ __global__ void __launch_bounds__(1024) fwd_kernel(const FwdParams p) {
         for (int k = 0; k < NG; ++k)
             if (i0 + k * step < p.H) emit(i0 + k * step, v[k]);
     } else {
-        for (int64_t i = i0; i < p.H; i += step) {
+        for (int i = i0; i < p.H; i += step) {
             sum_at(i, v[0]);
             if (sum) store_e<DT, E>(sum, i, v[0]);
             emit(i, v[0]);
@@ -247,21 +248,21 @@ __global__ void __launch_bounds__(1024) fwd_kernel(const FwdParams p) {
 // least two CTAs share an SM: one works while the other meets at its barrier.
 constexpr int kOwn = 2;
 constexpr int kRingThreads = 512;  // most threads of a CTA
-constexpr int kFwdAhead = 3, kBwdAhead = 2;
+constexpr int kBwdAhead = 2;
 
-template <int DT, bool QUANT>
+template <int DT, bool QUANT, int kFwdAhead>
 __global__ void __launch_bounds__(kRingThreads, 2) fwd_ring_kernel(const FwdParams p) {
     constexpr int E = Elt<DT>::kPer16;
     extern __shared__ __align__(16) unsigned char ring[];  // [kFwdAhead][2][kOwn][threads][16]
     __shared__ float sh[2][2][32];
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
-    int64_t at[kOwn];
+    int at[kOwn];
     bool in[kOwn];
     float w[kOwn][E];
 #pragma unroll
     for (int k = 0; k < kOwn; ++k) {
-        at[k] = static_cast<int64_t>(k * blockDim.x + threadIdx.x) * E;
+        at[k] = static_cast<int>(k * blockDim.x + threadIdx.x) * E;
         in[k] = at[k] < p.H;
         if (in[k]) load_w<DT, E>(p.weight, p.w_f32 != 0, at[k], p.offset, w[k]);
     }
@@ -338,10 +339,12 @@ struct BwdParams {
     unsigned char *dx;
     float *part;       // [CTAs][H] partial dw, or null
     float *dot;        // wide rows: [T] mean_j(a_j xhat_j)
-    int64_t T, H;
+    int64_t T;
+    int H;
     int64_t dy_ld, x_ld, dres_ld, dx_ld;  // bytes
     float offset;
     int w_f32;
+    int groups;        // ring kernel: rows a CTA works on at once
 };
 
 // Each CTA takes rows blockIdx.x, + gridDim.x, ...; a thread owns the same
@@ -351,8 +354,8 @@ __global__ void __launch_bounds__(1024) bwd_kernel(const BwdParams p) {
     __shared__ float sh[2][2][32];
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
-    const int64_t step = static_cast<int64_t>(blockDim.x) * E;
-    const int64_t i0 = static_cast<int64_t>(threadIdx.x) * E;
+    const int step = static_cast<int>(blockDim.x) * E;
+    const int i0 = static_cast<int>(threadIdx.x) * E;
     float dw[NG][E];
 #pragma unroll
     for (int k = 0; k < NG; ++k)
@@ -366,7 +369,7 @@ __global__ void __launch_bounds__(1024) bwd_kernel(const BwdParams p) {
         float c = 0.f, unused = 0.f;
 #pragma unroll
         for (int k = 0; k < NG; ++k) {
-            const int64_t i = i0 + k * step;
+            const int i = i0 + k * step;
             if (i < p.H) {
                 load_e<DT, E>(dy, i, a[k]);
                 load_e<DT, E>(x, i, h[k]);
@@ -374,7 +377,7 @@ __global__ void __launch_bounds__(1024) bwd_kernel(const BwdParams p) {
         }
 #pragma unroll
         for (int k = 0; k < NG; ++k) {
-            const int64_t i = i0 + k * step;
+            const int i = i0 + k * step;
             if (i < p.H) {
                 float w[E];
                 load_w<DT, E>(p.weight, p.w_f32 != 0, i, p.offset, w);
@@ -391,7 +394,7 @@ __global__ void __launch_bounds__(1024) bwd_kernel(const BwdParams p) {
         c /= static_cast<float>(p.H);
 #pragma unroll
         for (int k = 0; k < NG; ++k) {
-            const int64_t i = i0 + k * step;
+            const int i = i0 + k * step;
             if (i < p.H) {
                 float r[E];
 #pragma unroll
@@ -414,22 +417,31 @@ __global__ void __launch_bounds__(1024) bwd_kernel(const BwdParams p) {
 }
 
 // The same with the ring of fwd_ring_kernel, read a second time after a row's
-// reduction instead of held in registers.
-template <int DT>
+// reduction instead of held in registers.  With MULTI a CTA works on `groups` short
+// rows at once, each with its own threads and named barrier, and adds up their dw at
+// the end, so that two CTAs per SM leave few partial rows (its weights are read again
+// for every row: in registers they would spill).
+template <int DT, bool MULTI>
 __global__ void __launch_bounds__(kRingThreads, 2) bwd_ring_kernel(const BwdParams p) {
     constexpr int E = Elt<DT>::kPer16;
     extern __shared__ __align__(16) unsigned char ring[];  // [kBwdAhead][3][kOwn][threads][16]
-    __shared__ float sh[2][2][32];
+    __shared__ float sh[2][kRingThreads / 32];
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
-    int64_t at[kOwn];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int groups = MULTI ? p.groups : 1;
+    const int gt = MULTI ? static_cast<int>(blockDim.x) / groups : static_cast<int>(blockDim.x);
+    const int gw = gt >> 5;
+    const int group = MULTI ? static_cast<int>(threadIdx.x) / gt : 0;
+    const int tg = static_cast<int>(threadIdx.x) - group * gt;
+    int at[kOwn];
     bool in[kOwn];
     float w[kOwn][E], dw[kOwn][E];
 #pragma unroll
     for (int k = 0; k < kOwn; ++k) {
-        at[k] = static_cast<int64_t>(k * blockDim.x + threadIdx.x) * E;
+        at[k] = (k * gt + tg) * E;
         in[k] = at[k] < p.H;
-        if (in[k]) load_w<DT, E>(p.weight, p.w_f32 != 0, at[k], p.offset, w[k]);
+        if (!MULTI && in[k]) load_w<DT, E>(p.weight, p.w_f32 != 0, at[k], p.offset, w[k]);
 #pragma unroll
         for (int j = 0; j < E; ++j) dw[k][j] = 0.f;
     }
@@ -451,12 +463,13 @@ __global__ void __launch_bounds__(kRingThreads, 2) bwd_ring_kernel(const BwdPara
         }
         ptx::cp_async_commit();
     };
-    const int64_t step = gridDim.x;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * groups + group;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
     const float inv_h = 1.f / static_cast<float>(p.H);
-    for (int n = 0; n < kBwdAhead - 1; ++n) fetch(blockIdx.x + n * step, n);
-    float rstd = 0.f, next = blockIdx.x < p.T ? p.rstd[blockIdx.x] : 0.f;
+    for (int n = 0; n < kBwdAhead - 1; ++n) fetch(first + n * step, n);
+    float rstd = 0.f, next = first < p.T ? p.rstd[first] : 0.f;
     int s = 0, flip = 0;
-    for (int64_t row = blockIdx.x; row < p.T; row += step, flip ^= 1) {
+    for (int64_t row = first; row < p.T; row += step, flip ^= 1) {
         rstd = next;
         if (row + step < p.T) next = p.rstd[row + step];
         fetch(row + (kBwdAhead - 1) * step, s == 0 ? kBwdAhead - 1 : s - 1);
@@ -468,6 +481,7 @@ __global__ void __launch_bounds__(kRingThreads, 2) bwd_ring_kernel(const BwdPara
                 float d[E], h[E];
                 load_e<DT, E>(slot(s, 0, k), 0, d);
                 load_e<DT, E>(slot(s, 1, k), 0, h);
+                if (MULTI) load_w<DT, E>(p.weight, p.w_f32 != 0, at[k], p.offset, w[k]);
 #pragma unroll
                 for (int j = 0; j < E; ++j) {
                     const float g = d[j] * (h[j] * rstd);
@@ -475,7 +489,17 @@ __global__ void __launch_bounds__(kRingThreads, 2) bwd_ring_kernel(const BwdPara
                     c = fmaf(g, w[k][j], c);
                 }
             }
-        block_sum_max<false>(c, unused, sh[flip]);
+        // sum over the group's warps; two buffers, so one barrier a row
+        warp_sum_max<false>(c, unused);
+        if (gw > 1) {
+            if (lane == 0) sh[flip][warp] = c;
+            if (MULTI)
+                asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(gt) : "memory");
+            else
+                __syncthreads();
+            c = lane < gw ? sh[flip][group * gw + lane] : 0.f;
+            warp_sum_max<false>(c, unused);
+        }
         c *= inv_h;
 #pragma unroll
         for (int k = 0; k < kOwn; ++k)
@@ -483,6 +507,7 @@ __global__ void __launch_bounds__(kRingThreads, 2) bwd_ring_kernel(const BwdPara
                 float d[E], h[E], r[E];
                 load_e<DT, E>(slot(s, 0, k), 0, d);
                 load_e<DT, E>(slot(s, 1, k), 0, h);
+                if (MULTI) load_w<DT, E>(p.weight, p.w_f32 != 0, at[k], p.offset, w[k]);
 #pragma unroll
                 for (int j = 0; j < E; ++j) r[j] = 0.f;
                 if (p.dres) load_e<DT, E>(slot(s, 2, k), 0, r);
@@ -493,8 +518,9 @@ __global__ void __launch_bounds__(kRingThreads, 2) bwd_ring_kernel(const BwdPara
             }
         if (++s == kBwdAhead) s = 0;
     }
-    if (p.part) {
-        float *part = p.part + static_cast<int64_t>(blockIdx.x) * p.H;
+    if (!p.part) return;
+    float *part = p.part + static_cast<int64_t>(blockIdx.x) * p.H;
+    if constexpr (!MULTI) {
 #pragma unroll
         for (int k = 0; k < kOwn; ++k)
             if (in[k]) {
@@ -503,6 +529,31 @@ __global__ void __launch_bounds__(kRingThreads, 2) bwd_ring_kernel(const BwdPara
                     *reinterpret_cast<float4 *>(part + at[k] + j) =
                         make_float4(dw[k][j], dw[k][j + 1], dw[k][j + 2], dw[k][j + 3]);
             }
+    } else {
+        // [groups][kOwn gt E] floats in the ring, which no copy writes any more
+        float *sum = reinterpret_cast<float *>(ring);
+        const int width = kOwn * gt * E;
+        ptx::cp_async_wait<0>();
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k)
+#pragma unroll
+            for (int j = 0; j < E; j += 4)
+                *reinterpret_cast<float4 *>(sum + group * width + at[k] + j) =
+                    make_float4(dw[k][j], dw[k][j + 1], dw[k][j + 2], dw[k][j + 3]);
+        __syncthreads();
+        for (int i = 4 * static_cast<int>(threadIdx.x); i < p.H;
+             i += 4 * static_cast<int>(blockDim.x)) {
+            float4 a = *reinterpret_cast<const float4 *>(sum + i);
+            for (int g = 1; g < groups; ++g) {
+                const float4 o = *reinterpret_cast<const float4 *>(sum + g * width + i);
+                a.x += o.x;
+                a.y += o.y;
+                a.z += o.z;
+                a.w += o.w;
+            }
+            *reinterpret_cast<float4 *>(part + i) = a;
+        }
     }
 }
 
@@ -516,8 +567,7 @@ __global__ void __launch_bounds__(512) dot_kernel(const BwdParams p) {
     const int64_t row = blockIdx.x;
     const float rstd = p.rstd[row];
     float c = 0.f, unused = 0.f;
-    for (int64_t i = static_cast<int64_t>(threadIdx.x) * E; i < p.H;
-         i += static_cast<int64_t>(blockDim.x) * E) {
+    for (int i = static_cast<int>(threadIdx.x) * E; i < p.H; i += static_cast<int>(blockDim.x) * E) {
         float d[E], h[E], w[E];
         load_e<DT, E>(p.dy + row * p.dy_ld, i, d);
         load_e<DT, E>(p.x + row * p.x_ld, i, h);
@@ -532,7 +582,7 @@ template <int DT, int E>
 __global__ void __launch_bounds__(512) segment_kernel(const BwdParams p) {
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
-    const int64_t i = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) * E;
+    const int i = static_cast<int>(blockIdx.x * blockDim.x + threadIdx.x) * E;
     if (i >= p.H) return;
     float dw[E], w[E];
     load_w<DT, E>(p.weight, p.w_f32 != 0, i, p.offset, w);
@@ -556,15 +606,15 @@ __global__ void __launch_bounds__(512) segment_kernel(const BwdParams p) {
     }
     if (p.part) {
 #pragma unroll
-        for (int j = 0; j < E; ++j) p.part[blockIdx.y * p.H + i + j] = dw[j];
+        for (int j = 0; j < E; ++j) p.part[static_cast<int64_t>(blockIdx.y) * p.H + i + j] = dw[j];
     }
 }
 
 // ------------------------------------------------------------ host side
-constexpr int64_t kMaxH = INT64_C(1) << 30;
+constexpr int64_t kMaxH = INT64_C(1) << 30;  // columns and the kernels' strides over them fit 32 bits
 // CTAs whose partial dw the workspace holds (SMs x CTAs of one SM).
 int64_t max_parts(int64_t T, int64_t H) {
-    const int64_t n = 160 * std::min<int64_t>(8, std::max<int64_t>(2, 8192 / H));
+    const int64_t n = 160 * std::min<int64_t>(8, std::max<int64_t>(2, 16384 / H));
     return std::min(std::max<int64_t>(T, 1), n);
 }
 // CTAs of `threads` threads on one SM, for about 1024 threads.
@@ -649,20 +699,21 @@ int ring_threads(int64_t H, int32_t dtype) {
                ? static_cast<int>(round_up((granules + kOwn - 1) / kOwn, 32))
                : 0;
 }
-template <bool Q>
+template <bool Q, int A>
 FwdKernel fwd_ring_of(int32_t dtype) {
     switch (dtype) {
-        case VLMCE_F32: return fwd_ring_kernel<VLMCE_F32, Q>;
-        case VLMCE_BF16: return fwd_ring_kernel<VLMCE_BF16, Q>;
-        default: return fwd_ring_kernel<VLMCE_F16, Q>;
+        case VLMCE_F32: return fwd_ring_kernel<VLMCE_F32, Q, A>;
+        case VLMCE_BF16: return fwd_ring_kernel<VLMCE_BF16, Q, A>;
+        default: return fwd_ring_kernel<VLMCE_F16, Q, A>;
     }
 }
 using BwdKernel = void (*)(const BwdParams);
+template <bool MULTI>
 BwdKernel bwd_ring_of(int32_t dtype) {
     switch (dtype) {
-        case VLMCE_F32: return bwd_ring_kernel<VLMCE_F32>;
-        case VLMCE_BF16: return bwd_ring_kernel<VLMCE_BF16>;
-        default: return bwd_ring_kernel<VLMCE_F16>;
+        case VLMCE_F32: return bwd_ring_kernel<VLMCE_F32, MULTI>;
+        case VLMCE_BF16: return bwd_ring_kernel<VLMCE_BF16, MULTI>;
+        default: return bwd_ring_kernel<VLMCE_F16, MULTI>;
     }
 }
 template <int DT>
@@ -772,7 +823,7 @@ extern "C" vlmce_status rmsnorm_fwd(const void *x, int64_t x_stride, const void 
     p.rstd = rstd;
     p.scale = scale;
     p.T = T;
-    p.H = H;
+    p.H = static_cast<int>(H);
     p.x_ld = x_stride * elt;
     p.residual_ld = residual_stride * elt;
     p.y_ld = y_stride * yelt;
@@ -783,13 +834,21 @@ extern "C" vlmce_status rmsnorm_fwd(const void *x, int64_t x_stride, const void 
     cudaStream_t st_ = reinterpret_cast<cudaStream_t>(stream);
     const int rt = vec ? ring_threads(H, dtype) : 0;
     if (rt > 0) {
-        const int64_t ctas = static_cast<int64_t>(dev.sm_count) * per_sm_of(rt);
-        if (T >= 3 * ctas)  // rows enough to run ahead
-            return launch_status(
-                launch(quant ? fwd_ring_of<true>(dtype) : fwd_ring_of<false>(dtype),
-                       dim3(static_cast<unsigned>(ctas), 1, 1), rt,
-                       static_cast<size_t>(kFwdAhead) * 2 * kOwn * 16 * rt, st_, p),
-                "rmsnorm_fwd");
+        const int per_sm = per_sm_of(rt);
+        const int64_t ctas = static_cast<int64_t>(dev.sm_count) * per_sm;
+        // rows in flight: long 16-bit rows fill the memory system with one row ahead
+        // (8192 x 6656 bf16 to e4m3: 59 us, two rows ahead 65), others need two
+        // (8192 x 1024 bf16: 11.7 against 15.7; 4096 x 4096 fp32: 45.8 against 48)
+        const int ahead = elt == 2 && H >= 4096 ? 2 : 3;
+        if (T >= 3 * ctas) {  // rows enough to run ahead
+            const FwdKernel k = ahead == 2 ? quant ? fwd_ring_of<true, 2>(dtype)
+                                                   : fwd_ring_of<false, 2>(dtype)
+                                : quant ? fwd_ring_of<true, 3>(dtype)
+                                        : fwd_ring_of<false, 3>(dtype);
+            return launch_status(launch(k, dim3(static_cast<unsigned>(ctas), 1, 1), rt,
+                                        static_cast<size_t>(ahead) * 2 * kOwn * 16 * rt, st_, p),
+                                 "rmsnorm_fwd");
+        }
     }
     return launch_status(launch(fwd_kernel_of(dtype, quant, vec, sh.ng),
                                 dim3(static_cast<unsigned>(T), 1, 1), sh.threads, 0, st_, p),
@@ -864,7 +923,7 @@ extern "C" vlmce_status rmsnorm_bwd(const void *dy, int64_t dy_stride, const voi
     p.dot = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) +
                                       round_up(4 * H * parts_max, 256));
     p.T = T;
-    p.H = H;
+    p.H = static_cast<int>(H);
     p.dy_ld = dy_stride * elt;
     p.x_ld = x_stride * elt;
     p.dres_ld = dresidual_stride * elt;
@@ -873,12 +932,17 @@ extern "C" vlmce_status rmsnorm_bwd(const void *dy, int64_t dy_stride, const voi
     p.w_f32 = weight_dtype == VLMCE_F32;
     int64_t parts;
     const int rt = vec ? ring_threads(H, dtype) : 0;
-    const int64_t ring_ctas = rt > 0 ? static_cast<int64_t>(dev.sm_count) * per_sm_of(rt) : 0;
+    // rows of up to 128 threads share a CTA, two CTAs per SM; longer ones have their
+    // own, 1024 threads per SM
+    p.groups = rt > 0 && rt <= 128 ? std::min(15, kRingThreads / rt) : 1;
+    const int64_t ring_ctas =
+        static_cast<int64_t>(dev.sm_count) * (rt > 128 ? per_sm_of(rt) : 2);
     cudaError_t e;
-    if (rt > 0 && T >= 3 * ring_ctas && ring_ctas <= parts_max) {
+    if (rt > 0 && T >= 2 * ring_ctas * p.groups && ring_ctas <= parts_max) {
         parts = ring_ctas;
-        e = launch(bwd_ring_of(dtype), dim3(static_cast<unsigned>(parts), 1, 1), rt,
-                   static_cast<size_t>(kBwdAhead) * 3 * kOwn * 16 * rt, s, p);
+        const int threads = p.groups * rt;
+        e = launch(p.groups > 1 ? bwd_ring_of<true>(dtype) : bwd_ring_of<false>(dtype), dim3(static_cast<unsigned>(parts), 1, 1), threads,
+                   static_cast<size_t>(kBwdAhead) * 3 * kOwn * 16 * threads, s, p);
     } else if (sh.ng > 0) {
         parts = std::min<int64_t>(parts_max, static_cast<int64_t>(dev.sm_count) *
                                                  std::max(2, per_sm_of(sh.threads)));
