@@ -48,9 +48,10 @@ LargeKernel large_kernel(bool gated, bool fp8) {
     if (gated) return fp8 ? mm_large_kernel<true, true> : mm_large_kernel<true, false>;
     return fp8 ? mm_large_kernel<false, true> : mm_large_kernel<false, false>;
 }
-SmallKernel small_kernel(bool gated, bool fp8) {
-    if (gated) return fp8 ? mm_small_kernel<true, true> : mm_small_kernel<true, false>;
-    return fp8 ? mm_small_kernel<false, true> : mm_small_kernel<false, false>;
+SmallKernel small_kernel(bool gated, bool fp8, bool w_mn) {
+    if (w_mn) return mm_small_kernel<false, false, true>;
+    if (gated) return fp8 ? mm_small_kernel<true, true, false> : mm_small_kernel<true, false, false>;
+    return fp8 ? mm_small_kernel<false, true, false> : mm_small_kernel<false, false, false>;
 }
 
 // Clusters of `csize` CTAs, launched dependent on what precedes them.
@@ -104,13 +105,14 @@ cudaError_t setup(Capacity *out) {
     std::lock_guard<std::mutex> lock(mu);
     if (cached[device].pairs == 0) {
         Capacity c;
+        for (int k = 0; k < 5; ++k) {
+            e = cudaFuncSetAttribute(small_kernel(k & 1, k & 2, k & 4),
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, small_budget(1));
+            if (e != cudaSuccess) return e;
+        }
         for (int k = 0; k < 4; ++k) {
             const LargeKernel lk = large_kernel(k & 1, k & 2);
             e = cudaFuncSetAttribute(lk, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
-            if (e == cudaSuccess)
-                e = cudaFuncSetAttribute(small_kernel(k & 1, k & 2),
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         small_budget(1));
             int n = 0;
             if (e == cudaSuccess) e = clusters_of(lk, 2, kPairThreads, kPairSmem, &n);
             if (e != cudaSuccess) return e;
@@ -246,7 +248,15 @@ Plan plan_of(const Fwd &f, const Capacity &cap) {
     return e.plan;
 }
 
-cudaError_t forward_large(const Fwd &f, cudaStream_t s) {
+// Pair kernels: CTAs to launch, and how the pairs share the tiles (Tiles in
+// mm_pair.cuh).  Dealt out, T = 16, K = 4096, N = 16384's dW takes 38.7 us (45.6 by
+// launch control); T = 4096, K = 6656, 2n = 32768 forward is 4 % slower that way.
+unsigned pair_grid(int64_t tiles, int chunks, const Capacity &cap, int *dealt) {
+    *dealt = chunks < 32 ? static_cast<int>(tiles) : 0;
+    return static_cast<unsigned>(2 * (*dealt > 0 ? std::min<int64_t>(tiles, cap.pairs) : tiles));
+}
+
+cudaError_t forward_large(const Fwd &f, const Capacity &cap, cudaStream_t s) {
     LargeMaps maps = {};
     const int64_t rows = f.gated ? 2 * f.N : f.N;
     const Epi &e = f.e;
@@ -267,12 +277,13 @@ cudaError_t forward_large(const Fwd &f, cudaStream_t s) {
     p.nt = static_cast<int>(f.gated ? (f.N + 127) / 128 : (f.N + 255) / 256);
     const int64_t tiles = static_cast<int64_t>(p.mt) * p.nt;
     if (tiles * kGroupM > INT32_MAX) return cudaErrorInvalidConfiguration;
+    const unsigned grid = pair_grid(tiles, p.chunks, cap, &p.dealt);
     p.e = f.e;
     p.err = f.err;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     launch_attributes(attr, 2);
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * tiles), 1, 1);
+    cfg.gridDim = dim3(grid, 1, 1);
     cfg.blockDim = dim3(kPairThreads, 1, 1);
     cfg.dynamicSmemBytes = kPairSmem;
     cfg.stream = s;
@@ -306,8 +317,10 @@ cudaError_t forward_small(const Fwd &f, const Plan &plan, cudaStream_t s) {
 
     CUtensorMap mx, mw;
     const int64_t rows = f.gated ? 2 * f.N : f.N;
-    if (!operand_map(&mx, f.x, f.dtype, f.T, f.K, f.x_ld, p.bn) ||
-        !operand_map(&mw, f.w, f.dtype, rows, f.K, f.w_ld, 128))
+    const bool w_ok =
+        f.w_mn ? gemm::make_operand_map(&mw, f.w, true, f.N, f.K, f.w_ld, f.dtype == VLMCE_F16)
+               : operand_map(&mw, f.w, f.dtype, rows, f.K, f.w_ld, 128);
+    if (!w_ok || !operand_map(&mx, f.x, f.dtype, f.T, f.K, f.x_ld, p.bn))
         return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
@@ -318,7 +331,7 @@ cudaError_t forward_small(const Fwd &f, const Plan &plan, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, small_kernel(f.gated != 0, f.dtype == VLMCE_E4M3), mw, mx,
+    return cudaLaunchKernelEx(&cfg, small_kernel(f.gated != 0, f.dtype == VLMCE_E4M3, f.w_mn != 0), mw, mx,
                               static_cast<const SmallParams>(p));
 }
 
@@ -329,13 +342,64 @@ cudaError_t forward(const Fwd &f, cudaStream_t s) {
     const cudaError_t e = setup(&cap);
     if (e != cudaSuccess) return e;
     const Plan plan = plan_of(f, cap);
-    return plan.large ? forward_large(f, s) : forward_small(f, plan, s);
+    return plan.large ? forward_large(f, cap, s) : forward_small(f, plan, s);
 }
+
+namespace {
+
+// Estimates of backward()'s launches in SM clocks (fitted to the times above): dW
+// after dx, and both in one launch.  A dW tile of few chunks takes its epilogue's time.
+double dw_tile_clocks(const Bwd &b) {
+    const double chunks = static_cast<double>((b.T + 63) / 64);
+    return std::max(kPairChunk * chunks, 5000. + 285. * chunks);
+}
+double dw_tiles(const Bwd &b) {
+    return static_cast<double>((b.rows + 255) / 256) * static_cast<double>((b.K + 255) / 256);
+}
+double dw_clocks(const Bwd &b, const Capacity &cap) {
+    return std::ceil(dw_tiles(b) / cap.pairs) * dw_tile_clocks(b) + 5700. + 17000.;
+}
+double joint_clocks(const Bwd &b, const Capacity &cap) {
+    const double tile = kPairChunk * static_cast<double>((b.rows + 63) / 64);
+    const double tiles =
+        static_cast<double>((b.T + 255) / 256) * static_cast<double>((b.K + 255) / 256);
+    return std::max(tile, (tiles * tile + dw_tiles(b) * dw_tile_clocks(b)) / cap.pairs) + 11400.;
+}
+
+}  // namespace
 
 cudaError_t backward(const Bwd &b, cudaStream_t s) {
     Capacity cap;
     const cudaError_t e = setup(&cap);
     if (e != cudaSuccess) return e;
+    // dx alone for few tokens takes the small kernel (W's rows are its K), which
+    // spreads the weight over all SMs: T = 16, K = 4096, N = 16384 24 us (73 us in pair
+    // tiles).  Beside dW that costs a launch; it pays where one pair tile's walk along
+    // W's rows would last longer (the same sizes: 71 against 83 us; T = 256: 100
+    // against 87).
+    bool dx = b.dx != nullptr;
+    if (dx) {
+        Fwd f = {};
+        f.x = b.dz;
+        f.w = b.w;
+        f.x_ld = b.dz_ld;
+        f.w_ld = b.w_ld;
+        f.T = b.T;
+        f.N = b.K;
+        f.K = b.rows;
+        f.w_mn = 1;
+        f.dtype = b.f16 ? VLMCE_F16 : VLMCE_BF16;
+        f.e.y = static_cast<uint16_t *>(b.dx);
+        f.e.y_ld = b.dx_ld;
+        f.e.f16 = b.f16;
+        f.err = b.err;
+        const Plan plan = plan_of(f, cap);
+        if (!plan.large && (!b.dw || plan.clocks < joint_clocks(b, cap) - dw_clocks(b, cap))) {
+            const cudaError_t es = forward_small(f, plan, s);
+            if (es != cudaSuccess || !b.dw) return es;
+            dx = false;
+        }
+    }
     GradMaps maps;
     GradParams p = {};
     p.f16 = b.f16;
@@ -367,17 +431,18 @@ cudaError_t backward(const Bwd &b, cudaStream_t s) {
     const bool dx_first = b.rows >= b.T;  // longer tiles first
     for (int i = 0; i < 2; ++i) {
         if ((i == 0) == dx_first) {
-            if (b.dx)
+            if (dx)
                 add(b.dz, false, b.dz_ld, b.w, b.w_ld, b.T, b.rows, b.dx, b.dx_ld, 0, 0);
         } else if (b.dw) {
             add(b.dz, true, b.dz_ld, b.x, b.x_ld, b.rows, b.T, b.dw, b.K, b.dw_f32, b.accumulate);
         }
     }
     if (!ok) return cudaErrorInvalidValue;
+    const unsigned grid = pair_grid(tiles, p.p[0].chunks, cap, &p.dealt);  // the longest
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     launch_attributes(attr, 2);
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * tiles), 1, 1);
+    cfg.gridDim = dim3(grid, 1, 1);
     cfg.blockDim = dim3(kPairThreads, 1, 1);
     cfg.dynamicSmemBytes = kPairSmem;
     cfg.stream = s;

@@ -29,6 +29,7 @@ struct GradParams {
     GradProblem p[2];
     int nprob;
     int f16;
+    int dealt;
     int *err;
 };
 struct GradMaps {
@@ -61,7 +62,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             tc::prefetch_tensormap(&maps.b[i]);
         }
     }
-    const Pair<kPer> q = pair_setup<kPer>(smem_raw, a.err);
+    const Pair<kPer> q = pair_setup<kPer>(smem_raw, a.err, a.dealt);
     Tiles tiles;
 
     if (warp == 0 || warp == kWarpB) {
@@ -134,7 +135,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 const int col = tl.n0 + 32 * c;
                 if (row0 < P.M) {
                     if (P.f32) {
-                        if (col < P.N) put_f32(map, row0, col, r, P.accumulate != 0, buf, lane);
+                        if (col < P.N)
+                            put_f32(map, row0, col, r, P.accumulate != 0, buf, lane);
                     } else if (tl.n0 + 64 * (c >> 1) < P.N) {
                         float v[32];
 #pragma unroll

@@ -23,6 +23,7 @@ struct LargeParams {
     int up_row;        // gated: first up row of the weight
     int chunks;        // K in 128-byte chunks
     int mt, nt;
+    int dealt;
     Epi e;
     int *err;
 };
@@ -75,7 +76,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         tc::prefetch_tensormap(&maps.x);
         tc::prefetch_tensormap(&maps.w);
     }
-    const Pair<kPer> q = pair_setup<kPer>(smem_raw, p.err);
+    const Pair<kPer> q = pair_setup<kPer>(smem_raw, p.err, p.dealt);
     Tiles tiles;
     const int rank = static_cast<int>(q.rank);
 

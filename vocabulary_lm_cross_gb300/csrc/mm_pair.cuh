@@ -10,12 +10,12 @@
 // 4 (one row per thread), two warps per subpartition, each on half of the
 // columns; warp 11 (leader) fetches the tiles.
 //
-// Tiles: one cluster is launched per tile, and the clusters that fit at once
-// stay: each takes over the work of one that has not started (cluster launch
-// control), one tile ahead of its slowest role.  So tiles are handed out in
-// order as pairs become free, without a counter in memory.  (Dealt out in
-// advance, T = 4096, K = 6656, 2n = 32768's gradient products would leave pairs
-// idle for one of its 138 us dx tiles.)
+// Tiles: of long tiles one cluster each is launched, and the clusters that fit at
+// once stay: each takes over the work of one that has not started (cluster launch
+// control), one tile ahead of its slowest role.  So they are handed out in order as
+// pairs become free, without a counter in memory.  (Dealt out in advance, T = 4096,
+// K = 6656, 2n = 32768's gradient products would leave pairs idle for one of its 138
+// us dx tiles.)  Short tiles are dealt out: their answers would not keep up.
 //
 // Operand layouts of a stage (16-bit operands): K-major, 128 rows of 64 K (8-row
 // groups 1024 B apart, a K step of 16 advances 32 B); MN-major, two boxes of 64
@@ -66,6 +66,7 @@ struct Pair {
     int *err;
     uint32_t rank;        // 0: the pair's leader
     uint32_t tmem;
+    int dealt;            // > 0: so many tiles are dealt out to the clusters in turn
 
     __device__ __forceinline__ uint32_t full(int s) const { return bar0 + 8u * s; }
     __device__ __forceinline__ uint32_t empty(int s) const { return bar0 + 8u * (kStages + s); }
@@ -103,8 +104,10 @@ struct Ring {
 // held), and this one waits for its predecessor's results before it touches
 // global memory.
 template <int PER>
-__device__ __forceinline__ Pair<PER> pair_setup(unsigned char *smem_raw, int *err) {
+__device__ __forceinline__ Pair<PER> pair_setup(unsigned char *smem_raw, int *err,
+                                                      int dealt) {
     Pair<PER> q;
+    q.dealt = dealt;
     q.smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     uint64_t *bars =
@@ -144,14 +147,18 @@ __device__ __forceinline__ Pair<PER> pair_setup(unsigned char *smem_raw, int *er
     ptx::griddep_wait();
     return q;
 }
-// The sequence of tiles of a pair, one object per role: the cluster's own, then
-// those it takes over; -1 after the last (or after a wait that gave up).  All
-// active lanes of a warp call next().
+// The sequence of tiles of a pair, one object per role; -1 after the last (or after a
+// wait that gave up).  All active lanes of a warp call next().
 struct Tiles {
     int j = -1;
     template <int PER>
     __device__ __forceinline__ int next(const Pair<PER> &q, int lane) {
-        if (++j == 0) return static_cast<int>(ptx::cluster_id_x());
+        const int own = static_cast<int>(ptx::cluster_id_x());
+        if (++j == 0) return own;
+        if (q.dealt > 0) {
+            const int64_t t = own + static_cast<int64_t>(j) * ptx::ncluster_x();
+            return t < q.dealt ? static_cast<int>(t) : -1;
+        }
         const int i = (j - 1) % kTileQ;
         int t = -1;
         if (wait_bar<true>(q.qfull(i), ((j - 1) / kTileQ) & 1, q.abort, q.err)) {
@@ -172,6 +179,7 @@ struct Tiles {
 // The leader's fetching lane.
 template <int PER>
 __device__ __forceinline__ void fetch_tiles(const Pair<PER> &q) {
+    if (q.dealt > 0) return;
     for (int n = 0;; ++n) {
         const int i = n % kTileQ;
         if (n >= kTileQ && !wait_bar<true>(q.qempty(i), ((n / kTileQ) - 1) & 1, q.abort, q.err))
@@ -287,7 +295,8 @@ struct Out {
     const CUtensorMap *map;  // boxes of 64 columns x 32 rows
 };
 
-// The warp's buffer may be written: its TMA stores have read it.
+// The warp's buffer may be written: its TMA stores have read it.  (A second buffer,
+// for a ring of five chunks, measured the same.)
 __device__ __forceinline__ void buffer_free(int lane) {
     if (lane == 0) tc::bulk_wait_read();
     __syncwarp();

@@ -145,7 +145,9 @@ __device__ __forceinline__ void small_epilogue(const SmallParams &p, const RowFa
         if (j < count) y[j * e.y_ld] = act::to16(g[j], f16);
 }
 
-template <bool GATED, bool FP8>
+// W_MN: the weight is stored with its outputs contiguous ([K, N], as the gradient
+// dx = dz W reads W): 128 outputs x 64 of K come as two boxes of 64 x 64, MN-major.
+template <bool GATED, bool FP8, bool W_MN>
 __global__ void __launch_bounds__(kSmallBound, 2)
     mm_small_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx,
                     const __grid_constant__ SmallParams p) {
@@ -202,7 +204,12 @@ __global__ void __launch_bounds__(kSmallBound, 2)
     if (warp == 0 && lane == 0) {
         const int ahead = min(c1, c0 + p.stages * p.per_stage);
         for (int c = c0; c < ahead; ++c) {
-            tc::tma_prefetch_2d(&mw, c * kElts, n0);
+            if constexpr (W_MN) {
+                tc::tma_prefetch_2d(&mw, n0, c * kElts);
+                tc::tma_prefetch_2d(&mw, n0 + 64, c * kElts);
+            } else {
+                tc::tma_prefetch_2d(&mw, c * kElts, n0);
+            }
             if constexpr (GATED) tc::tma_prefetch_2d(&mw, c * kElts, p.up_row + n0);
         }
     }
@@ -219,7 +226,12 @@ __global__ void __launch_bounds__(kSmallBound, 2)
                 for (int i = 0; i < n; ++i) {
                     const uint32_t sa = ring + s * stage_bytes + i * chunk_bytes;
                     const int k = (c + i) * kElts;
-                    tc::tma_load_2d(sa, &mw, k, n0, full(s));
+                    if constexpr (W_MN) {
+                        tc::tma_load_2d(sa, &mw, n0, k, full(s));
+                        tc::tma_load_2d(sa + kWTileBytes / 2, &mw, n0 + 64, k, full(s));
+                    } else {
+                        tc::tma_load_2d(sa, &mw, k, n0, full(s));
+                    }
                     if constexpr (GATED)
                         tc::tma_load_2d(sa + kWTileBytes, &mw, k, p.up_row + n0, full(s));
                     tc::tma_load_2d(sa + kW * kWTileBytes, &mx, k, t0, full(s));
@@ -238,7 +250,7 @@ __global__ void __launch_bounds__(kSmallBound, 2)
         }
     } else if (warp == 1) {
         if (lane == 0) {
-            const uint32_t idesc = tc::idesc_bf16_f32(128, p.bn, false, false, FP8 || p.e.f16);
+            const uint32_t idesc = tc::idesc_bf16_f32(128, p.bn, W_MN, false, FP8 || p.e.f16);
             int s = 0;
             uint32_t ph = 0;
             for (int c = c0; c < c1; c += p.per_stage) {
@@ -254,7 +266,8 @@ __global__ void __launch_bounds__(kSmallBound, 2)
 #pragma unroll
                         for (int w = 0; w < kW; ++w) {
                             const uint64_t wd =
-                                tc::smem_desc_sw128(sa + w * kWTileBytes + 32 * k, 16, 1024);
+                                W_MN ? tc::smem_desc_sw128(sa + 2048 * k, kWTileBytes / 2, 1024)
+                                     : tc::smem_desc_sw128(sa + w * kWTileBytes + 32 * k, 16, 1024);
                             const uint32_t d = tmem + static_cast<uint32_t>(w * p.bn);
                             const uint32_t add = c + i > c0 || k != 0;
                             if constexpr (FP8)

@@ -39,6 +39,7 @@ struct Fwd {
     int64_t x_ld, w_ld;
     int64_t T, N, K;
     int gated;
+    int w_mn;       // the weight is stored [K, N] (small kernel, 16 bits, not gated)
     int32_t dtype;  // VLMCE_BF16, VLMCE_F16 or VLMCE_E4M3
     Epi e;
     int *err;

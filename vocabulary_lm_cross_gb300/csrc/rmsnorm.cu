@@ -192,9 +192,10 @@ __global__ void __launch_bounds__(1024) fwd_kernel(const FwdParams p) {
     const int step = static_cast<int>(blockDim.x) * E;
     const int i0 = static_cast<int>(threadIdx.x) * E;
     if constexpr (NG > 0) {
+        // (a thread without a k-th element loads the row's last one, so that no
+        // branch keeps the loads apart)
 #pragma unroll
-        for (int k = 0; k < NG; ++k)
-            if (i0 + k * step < p.H) sum_at(i0 + k * step, v[k]);
+        for (int k = 0; k < NG; ++k) sum_at(min(i0 + k * step, p.H - E), v[k]);
 #pragma unroll
         for (int k = 0; k < NG; ++k)
             if (i0 + k * step < p.H) {
@@ -368,12 +369,10 @@ __global__ void __launch_bounds__(1024) bwd_kernel(const BwdParams p) {
         float a[NG][E], h[NG][E];
         float c = 0.f, unused = 0.f;
 #pragma unroll
-        for (int k = 0; k < NG; ++k) {
-            const int i = i0 + k * step;
-            if (i < p.H) {
-                load_e<DT, E>(dy, i, a[k]);
-                load_e<DT, E>(x, i, h[k]);
-            }
+        for (int k = 0; k < NG; ++k) {  // (as in fwd_kernel)
+            const int i = min(i0 + k * step, p.H - E);
+            load_e<DT, E>(dy, i, a[k]);
+            load_e<DT, E>(x, i, h[k]);
         }
 #pragma unroll
         for (int k = 0; k < NG; ++k) {
@@ -557,8 +556,9 @@ __global__ void __launch_bounds__(kRingThreads, 2) bwd_ring_kernel(const BwdPara
     }
 }
 
-// Rows too wide for one CTA's registers: the rows' mean(a xhat), then dx and
-// the partial dw by column segments.
+// Rows too wide for one CTA's registers (unaligned ones from 4097 elements on: 16
+// elements of four arrays per thread spill, 4096 x 6661 bf16 167 us, so: 117): the
+// rows' mean(a xhat), then dx and the partial dw by column segments.
 template <int DT, int E>
 __global__ void __launch_bounds__(512) dot_kernel(const BwdParams p) {
     __shared__ float sh[2][32];
@@ -588,21 +588,33 @@ __global__ void __launch_bounds__(512) segment_kernel(const BwdParams p) {
     load_w<DT, E>(p.weight, p.w_f32 != 0, i, p.offset, w);
 #pragma unroll
     for (int j = 0; j < E; ++j) dw[j] = 0.f;
-    for (int64_t row = blockIdx.y; row < p.T; row += gridDim.y) {
-        const float rstd = p.rstd[row], c = p.dot[row];
-        float d[E], h[E], r[E];
-        load_e<DT, E>(p.dy + row * p.dy_ld, i, d);
-        load_e<DT, E>(p.x + row * p.x_ld, i, h);
+    constexpr int R = E == 1 ? 4 : 1;  // rows in flight
+    for (int64_t row0 = static_cast<int64_t>(blockIdx.y) * R; row0 < p.T;
+         row0 += static_cast<int64_t>(gridDim.y) * R) {
+        float d[R][E], h[R][E], r[R][E], rstd[R], c[R];
 #pragma unroll
-        for (int j = 0; j < E; ++j) r[j] = 0.f;
-        if (p.dres) load_e<DT, E>(p.dres + row * p.dres_ld, i, r);
+        for (int q = 0; q < R; ++q) {  // (rows past the end: the last one again)
+            const int64_t row = min(row0 + q, p.T - 1);
+            rstd[q] = p.rstd[row];
+            c[q] = p.dot[row];
+            load_e<DT, E>(p.dy + row * p.dy_ld, i, d[q]);
+            load_e<DT, E>(p.x + row * p.x_ld, i, h[q]);
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-            h[j] *= rstd;
-            dw[j] = fmaf(d[j], h[j], dw[j]);
-            r[j] = fmaf(rstd, d[j] * w[j] - h[j] * c, r[j]);
+            for (int j = 0; j < E; ++j) r[q][j] = 0.f;
+            if (p.dres) load_e<DT, E>(p.dres + row * p.dres_ld, i, r[q]);
         }
-        store_e<DT, E>(p.dx + row * p.dx_ld, i, r);
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            if (row0 + q < p.T) {
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    h[q][j] *= rstd[q];
+                    dw[j] = fmaf(d[q][j], h[q][j], dw[j]);
+                    r[q][j] = fmaf(rstd[q], d[q][j] * w[j] - h[q][j] * c[q], r[q][j]);
+                }
+                store_e<DT, E>(p.dx + (row0 + q) * p.dx_ld, i, r[q]);
+            }
+        }
     }
     if (p.part) {
 #pragma unroll
@@ -943,7 +955,7 @@ extern "C" vlmce_status rmsnorm_bwd(const void *dy, int64_t dy_stride, const voi
         const int threads = p.groups * rt;
         e = launch(p.groups > 1 ? bwd_ring_of<true>(dtype) : bwd_ring_of<false>(dtype), dim3(static_cast<unsigned>(parts), 1, 1), threads,
                    static_cast<size_t>(kBwdAhead) * 3 * kOwn * 16 * threads, s, p);
-    } else if (sh.ng > 0) {
+    } else if (sh.ng > 0 && sh.ng < 16) {
         parts = std::min<int64_t>(parts_max, static_cast<int64_t>(dev.sm_count) *
                                                  std::max(2, per_sm_of(sh.threads)));
         e = launch(bwd_kernel_of(dtype, vec, sh.ng), dim3(static_cast<unsigned>(parts), 1, 1),
