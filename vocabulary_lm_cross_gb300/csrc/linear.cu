@@ -282,9 +282,11 @@ vlmce_status forward(const FwdArgs &a, const char *where) {
     e.act = a.act;
     e.f16 = a.out_dtype == VLMCE_F16;
     e.y_vec = mm::vec_of(a.y, a.y_stride);
-    e.preact_vec = mm::vec_of(a.preact, a.preact_stride);
-    e.preact_up_vec = mm::vec_of(static_cast<uint16_t *>(a.preact) + a.N, a.preact_stride);
-    e.residual_vec = mm::vec_of(a.residual, a.residual_stride);
+    if (e.preact) {
+        e.preact_vec = mm::vec_of(e.preact, a.preact_stride);
+        e.preact_up_vec = mm::vec_of(e.preact + a.N, a.preact_stride);
+    }
+    if (e.residual) e.residual_vec = mm::vec_of(e.residual, a.residual_stride);
     return launch_status(mm::forward(f, a.stream), where);
 }
 
@@ -318,7 +320,7 @@ int64_t dz_ld_of(int64_t rows) { return round_up(rows, 8); }
 int64_t part_bytes(int64_t N) { return round_up(4 * kMaxRowChunks * N, 256); }
 bool bwd_sizes_ok(int64_t T, int64_t N, int64_t K) {
     return T >= 0 && N >= 1 && K >= 1 && T <= kMaxDim && N <= kMaxDim / 2 && K <= kMaxDim &&
-           (T / 256 + 1 + N / 128 + 1) <= INT32_MAX / (K / 256 + 1);
+           (T / 256 + 1 + N / 128 + 1) <= INT32_MAX / 32 / (K / 256 + 1);
 }
 // dz [T, rows rounded to 8] and, for a linear layer, the partial sums of db.
 size_t bwd_workspace(int64_t T, int64_t N, int64_t K, bool gated) {

@@ -8,7 +8,8 @@ from typing import NamedTuple
 import torch
 
 from . import capi
-from .rows import ACTS, DTYPES, call, matrix, rows, vector, workspace_of
+from .rows import (ACTS, DTYPES, current_device, matrix, raw_stream, rows, vector,
+                   workspace_of)
 
 _FP8 = torch.float8_e4m3fn
 
@@ -44,6 +45,10 @@ def _forward(gated, x, weight, bias, residual, act, preact, x_scale, weight_scal
              dev_err):
     dt, xs, ws = _operands(x, weight)
     dev = x.device
+    if dev.index != current_device():
+        with torch.cuda.device(dev):
+            return _forward(gated, x, weight, bias, residual, act, preact, x_scale, weight_scale,
+                            out_dtype, out, dev_err)
     T, K = x.shape
     R = weight.shape[0]
     a = _act(act, gated)
@@ -81,16 +86,22 @@ def _forward(gated, x, weight, bias, residual, act, preact, x_scale, weight_scal
     if dev_err is not None:
         err = vector(dev_err, "dev_err", 1, (torch.int32,), dev)
     if gated:
-        call(capi.lib().glu_fwd, "glu_fwd", dev, x.data_ptr(), xs, xsc, weight.data_ptr(), ws, wsc,
-             DTYPES[dt], DTYPES[odt], T, N, K, a, out.data_ptr(), ys, zp, zs, err)
+        st = capi.lib().glu_fwd(x.data_ptr(), xs, xsc, weight.data_ptr(), ws, wsc, DTYPES[dt],
+                                DTYPES[odt], T, N, K, a, out.data_ptr(), ys, zp, zs, err,
+                                raw_stream(dev.index))
+        if st:
+            capi.check(st, "glu_fwd")
         return LinearResult(out, z)
     b = vector(bias, "bias", N, (odt,), dev) if bias is not None else None
     r, rs = None, N
     if residual is not None:
         rs = rows(residual, "residual", shape, odt, dev)
         r = residual.data_ptr()
-    call(capi.lib().linear_fwd, "linear_fwd", dev, x.data_ptr(), xs, xsc, weight.data_ptr(), ws,
-         wsc, DTYPES[dt], b, r, rs, DTYPES[odt], T, N, K, a, out.data_ptr(), ys, zp, zs, err)
+    st = capi.lib().linear_fwd(x.data_ptr(), xs, xsc, weight.data_ptr(), ws, wsc, DTYPES[dt], b, r,
+                               rs, DTYPES[odt], T, N, K, a, out.data_ptr(), ys, zp, zs, err,
+                               raw_stream(dev.index))
+    if st:
+        capi.check(st, "linear_fwd")
     return LinearResult(out, z)
 
 
@@ -130,6 +141,10 @@ def _backward(gated, dy, x, weight, preact, act, bias_grad, want_dx, want_dweigh
     if dt == _FP8:
         raise TypeError("the backward pass takes bf16 or fp16")
     dev = x.device
+    if dev.index != current_device():
+        with torch.cuda.device(dev):
+            return _backward(gated, dy, x, weight, preact, act, bias_grad, want_dx, want_dweight,
+                             out, dweight, dweight_dtype, dbias, accumulate, workspace, dev_err)
     T, K = x.shape
     R = weight.shape[0]
     a = _act(act, gated)
@@ -182,11 +197,12 @@ def _backward(gated, dy, x, weight, preact, act, bias_grad, want_dx, want_dweigh
     dwt = DTYPES[dweight.dtype] if dweight is not None else capi.F32
     head = (dy.data_ptr(), ds, x.data_ptr(), xs, weight.data_ptr(), ws, z, zs, DTYPES[dt], T, N, K,
             a, out.data_ptr() if out is not None else None, dxs, dw, dwt)
-    tail = (int(accumulate), err, w.data_ptr(), w.numel() * w.element_size())
+    tail = (int(accumulate), err, w.data_ptr(), w.numel() * w.element_size(),
+            raw_stream(dev.index))
     if gated:
-        call(lib.glu_bwd, "glu_bwd", dev, *head, *tail)
+        capi.check(lib.glu_bwd(*head, *tail), "glu_bwd")
     else:
-        call(lib.linear_bwd, "linear_bwd", dev, *head, b, *tail)
+        capi.check(lib.linear_bwd(*head, b, *tail), "linear_bwd")
     return LinearGrads(out, dweight, dbias)
 
 

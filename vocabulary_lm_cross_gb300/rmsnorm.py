@@ -7,7 +7,8 @@ from typing import NamedTuple
 import torch
 
 from . import capi
-from .rows import DTYPES, call, matrix, rows, vector, workspace_of
+from .rows import (DTYPES, current_device, matrix, raw_stream, rows, vector,
+                   workspace_of)
 
 
 class RMSNormResult(NamedTuple):
@@ -41,8 +42,12 @@ def rmsnorm_fwd(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | 
     ``residual`` or ``x`` itself), only with a residual.
     """
     dt, w = _checked(x, weight)
-    T, H = shape = x.shape
     dev = x.device
+    if dev.index != current_device():
+        with torch.cuda.device(dev):
+            return rmsnorm_fwd(x, weight, residual, eps=eps, weight_offset=weight_offset, fp8=fp8,
+                               out=out, residual_out=residual_out)
+    T, H = shape = x.shape
     xs = rows(x, "x", shape, dt, dev)
     r = ro = None
     rs = ros = H
@@ -64,9 +69,12 @@ def rmsnorm_fwd(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | 
         ys = rows(out, "out", shape, ydt, dev)
     rstd = torch.empty(T, dtype=torch.float32, device=dev)
     scale = torch.empty(T, dtype=torch.float32, device=dev) if fp8 else None
-    call(capi.lib().rmsnorm_fwd, "rmsnorm_fwd", dev, x.data_ptr(), xs, r, rs, w,
-         DTYPES[weight.dtype], DTYPES[dt], T, H, eps, weight_offset, out.data_ptr(), ys,
-         DTYPES[ydt], ro, ros, rstd.data_ptr(), scale.data_ptr() if fp8 else None)
+    st = capi.lib().rmsnorm_fwd(x.data_ptr(), xs, r, rs, w, DTYPES[weight.dtype], DTYPES[dt], T, H,
+                                eps, weight_offset, out.data_ptr(), ys, DTYPES[ydt], ro, ros,
+                                rstd.data_ptr(), scale.data_ptr() if fp8 else None,
+                                raw_stream(dev.index))
+    if st:
+        capi.check(st, "rmsnorm_fwd")
     return RMSNormResult(out, residual_out, rstd, scale)
 
 
@@ -79,8 +87,13 @@ def rmsnorm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, rstd: t
     or x where there was no residual); dresidual: the gradient reaching them along
     the residual stream.  out: dx (may be ``dy`` or ``dresidual`` itself)."""
     dt, w = _checked(x, weight)
-    T, H = shape = x.shape
     dev = x.device
+    if dev.index != current_device():
+        with torch.cuda.device(dev):
+            return rmsnorm_bwd(dy, x, weight, rstd, dresidual=dresidual,
+                               weight_offset=weight_offset, out=out, dweight=dweight,
+                               accumulate_dweight=accumulate_dweight, workspace=workspace)
+    T, H = shape = x.shape
     xs = rows(x, "x", shape, dt, dev)
     ds = rows(dy, "dy", shape, dt, dev)
     rp = vector(rstd, "rstd", T, (torch.float32,), dev)
@@ -100,7 +113,11 @@ def rmsnorm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, rstd: t
     dw = vector(dweight, "dweight", H, (torch.float32,), dev)
     lib = capi.lib()
     ws = workspace_of(workspace, lib.vlmce_rmsnorm_bwd_workspace_bytes(T, H), dev)
-    call(lib.rmsnorm_bwd, "rmsnorm_bwd", dev, dy.data_ptr(), ds, x.data_ptr(), xs, w,
-         DTYPES[weight.dtype], rp, dr, drs, DTYPES[dt], T, H, weight_offset, out.data_ptr(), os_,
-         dw, int(accumulate_dweight), ws.data_ptr(), ws.numel())
+    st = lib.rmsnorm_bwd(dy.data_ptr(), ds, x.data_ptr(), xs, w, DTYPES[weight.dtype], rp, dr, drs,
+                         DTYPES[dt], T, H, weight_offset, out.data_ptr(), os_, dw,
+                         int(accumulate_dweight), ws.data_ptr(),
+                         ws.numel() * ws.element_size(),
+                         raw_stream(dev.index))
+    if st:
+        capi.check(st, "rmsnorm_bwd")
     return RMSNormGrads(out, dweight)

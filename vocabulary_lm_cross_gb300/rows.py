@@ -43,24 +43,14 @@ def matrix(t: torch.Tensor, name: str) -> None:
         raise TypeError(f"{name} must be a CUDA tensor")
 
 
-# The handle of a device's current stream: torch.cuda.current_stream builds a
-# Stream object for it, which costs 2 us a call on the host.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-if _raw_stream is None:  # a CPU-only torch
-    def _raw_stream(index):
+# The current device and the handle of its current stream.  torch.cuda's functions
+# for these check for lazy initialisation (a CUDA tensor exists here) and build a
+# Stream object, 2 us a call on the host.
+current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+if raw_stream is None:  # a CPU-only torch
+    def raw_stream(index):
         return torch.cuda.current_stream(index).cuda_stream
-
-
-def call(fn, name: str, device, *args) -> None:
-    """Enqueue on the device's current stream; raises on a non-zero status."""
-    index = device.index
-    if index == torch.cuda.current_device():
-        st = fn(*args, _raw_stream(index))
-    else:
-        with torch.cuda.device(index):
-            st = fn(*args, _raw_stream(index))
-    if st != capi.OK:
-        capi.check(st, name)
 
 
 def workspace_of(workspace, need: int, device) -> torch.Tensor:
