@@ -144,6 +144,7 @@ cudaError_t setup(Capacity *out) {
 struct Plan {
     bool large;
     int bn, split, stages, per_stage, tmem_cols, smem;
+    int part_offset;  // SmallParams
     double clocks;  // estimate
 };
 
@@ -182,10 +183,15 @@ bool small_plan(const Fwd &f, const Capacity &cap, int64_t ty, int split, int pe
     const double rounds = per_sm == 1 ? std::ceil(waves) : waves > 1. ? waves + 0.3 : 1.;
     const int stage = per_stage * (kw * kWTileBytes + p.bn * 128);
     const int steps = ((chunks + split - 1) / split + per_stage - 1) / per_stage;
-    p.stages =
-        std::min({(small_budget(per_sm) - 1024 - kSmallTail) / stage, kMaxSmallStages, steps});
+    // the split's exchange: up to 16 KB of its own (T = 8, K = N = 1024 5.3 -> 4.6 us;
+    // more would cost the ring: T = 64, K = 16384 24.8 -> 25.9)
+    int part = split > 1 ? static_cast<int>(round_up(p.bn / 4, split)) * 4 * kw * 512 : 0;
+    if (part > 16384) part = 0;
+    p.stages = std::min(
+        {(small_budget(per_sm) - 1040 - kSmallTail - part) / stage, kMaxSmallStages, steps});
     if (p.stages < 1) return false;
-    p.smem = std::max({1024 + p.stages * stage + kSmallTail,
+    p.part_offset = part > 0 ? static_cast<int>(round_up(p.stages * stage + kSmallTail, 16)) : 0;
+    p.smem = std::max({1024 + p.stages * stage + kSmallTail + (part > 0 ? part + 16 : 0),
                        p.tmem_cols * kSmemPerTmemCol - kSmemReserved, kSmallSmemMin});
     const double mma = per_stage * kw * 4 * std::max(p.bn / 2., 32. + p.bn / 4.);
     const double load = stage / kL2BytesPerClock;
@@ -309,7 +315,9 @@ cudaError_t forward_small(const Fwd &f, const Plan &plan, cudaStream_t s) {
     const int64_t mt = (f.N + 127) / 128;
     const int ring = p.stages * p.per_stage * (kw * kWTileBytes + p.bn * 128);
     p.red_tokens = p.bn;
-    while ((p.red_tokens / 4 + p.split - 1) / p.split * 4 * p.split * kw * 512 > ring)
+    p.part_offset = plan.part_offset;
+    while (p.part_offset == 0 &&
+           (p.red_tokens / 4 + p.split - 1) / p.split * 4 * p.split * kw * 512 > ring)
         p.red_tokens -= 16;
     p.e = f.e;
     p.err = f.err;

@@ -88,6 +88,13 @@ __device__ __forceinline__ void cluster_sync_any() {
     asm volatile("barrier.cluster.arrive.release;\n\t"
                  "barrier.cluster.wait.acquire;" ::: "memory");
 }
+// Its two halves: the arrival, and the wait for every thread's.
+__device__ __forceinline__ void cluster_arrive_any() {
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait_any() {
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
 // Address of the same shared-memory variable in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t mapa(uint32_t local, uint32_t rank) {
     uint32_t r;
