@@ -413,7 +413,8 @@ size_t vlmce_glu_bwd_workspace_bytes(int64_t T, int64_t n, int64_t K);
  * accumulate      != 0: dweight (then fp32) and dbias are added to instead of
  *                 overwritten.
  * workspace       >= vlmce_linear_bwd_workspace_bytes(T, N, K) bytes, 256-byte
- *                 aligned.
+ *                 aligned; not used, and may be NULL, without an activation
+ *                 when dbias is NULL and dy's rows are 16-byte aligned.
  * At least one of dx, dweight, dbias is given (T > 0).  Outputs overlap
  * nothing.  dev_err as linear_fwd.  Deterministic.
  */

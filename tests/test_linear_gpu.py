@@ -290,3 +290,27 @@ def test_binding_refuses():
                      w.to(torch.float8_e4m3fn))
     with pytest.raises(capi.VlmceError):
         v.linear_bwd(dy, x, w, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+def test_workspace_may_be_missing_where_dy_is_read_as_it_is():
+    T, K, N = 40, 64, 72
+    g, x, w = linear_case(T, K, N, "bf16", 30)
+    dy, z = randn(g, (T, N), DT["bf16"]), randn(g, (T, N), DT["bf16"])
+    lib, s = capi.lib(), torch.cuda.current_stream().cuda_stream
+    dx, db = torch.empty_like(x), torch.empty(N, device="cuda")
+
+    def call(act, db_ptr, ws):
+        return lib.linear_bwd(dy.data_ptr(), N, x.data_ptr(), K, w.data_ptr(), K, z.data_ptr(), N,
+                              capi.BF16, T, N, K, act, dx.data_ptr(), K, None, capi.F32, db_ptr, 0,
+                              None, ws.data_ptr() if ws is not None else None,
+                              ws.numel() if ws is not None else 0, s)
+
+    assert call(capi.ACT_NONE, None, None) == capi.OK
+    full = torch.empty(lib.vlmce_linear_bwd_workspace_bytes(T, N, K), dtype=torch.uint8,
+                       device="cuda")
+    got = dx.clone()
+    assert call(capi.ACT_NONE, None, full) == capi.OK
+    assert torch.equal(got, dx)
+    assert call(capi.ACT_NONE, db.data_ptr(), None) == capi.ERR_WORKSPACE_TOO_SMALL
+    assert call(capi.ACT_SILU, None, None) == capi.ERR_WORKSPACE_TOO_SMALL
+    assert call(capi.ACT_NONE, None, full[:256]) == capi.ERR_WORKSPACE_TOO_SMALL

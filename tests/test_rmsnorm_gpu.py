@@ -197,3 +197,22 @@ def test_binding_refuses():
         v.rmsnorm_bwd(x, x, w, rstd, accumulate_dweight=True)
     with pytest.raises(capi.VlmceError):
         v.rmsnorm_bwd(r, x, w, rstd, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("T,H", [(1, 40), (333, 1001), (512, 264), (512, 4100), (513, 264)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_weight_gradient_added_to_and_in_place(T, H, dtype):
+    x, r, w = make(T, H, dtype, 21)
+    res = v.rmsnorm_fwd(x, w, r)
+    dy = randn(gen(22), (T, H), DT[dtype])
+    a = v.rmsnorm_bwd(dy, res.residual, w, res.rstd)
+    acc = a.dweight.clone()
+    v.rmsnorm_bwd(dy, res.residual, w, res.rstd, dweight=acc, accumulate_dweight=True)
+    d = dy.clone()
+    b = v.rmsnorm_bwd(d, res.residual, w, res.rstd, out=d)
+    s64, rs64 = f64(res.residual), f64(res.rstd)
+    dw = ol.rmsnorm_backward(f64(dy), s64, f64(w), rs64)[1]
+    e = (T + 32) * E24 * (np.abs(f64(dy)) * np.abs(s64 * rs64[:, None])).sum(0)
+    close(a.dweight, dw, "f32", e, "dweight")
+    assert torch.equal(acc, a.dweight + a.dweight)
+    assert torch.equal(a.dx, d) and torch.equal(a.dweight, b.dweight)

@@ -21,6 +21,11 @@
 // allocates TMEM takes at least the same share of the SM's shared memory
 // (kSmemPerTmemCol per column), so that TMEM never runs out first.
 //
+// Measured on GB300 (a call among others): T = 1, K = 4096, 2n = 24576 bf16 34.5 us
+// (201 MB of weight: 5.8 TB/s with the launch's 4 us), T = 64, K = 16384, N = 6656
+// e4m3 24.8 us (4.5 TB/s), T = 300, K = 4096, 2n = 20480 e4m3 32.7 us (1.54 PFLOP/s:
+// bound by the operands' way from L2, 53 of 64 bytes a clock on the SMs with two CTAs).
+//
 // CTA = 10 warps: warp 0 TMA producer, warp 1 TMEM and MMA issuer, warps 2-9
 // epilogue (one weight row per thread, two threads on alternate groups of
 // tokens).

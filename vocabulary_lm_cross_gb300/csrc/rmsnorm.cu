@@ -154,7 +154,8 @@ struct FwdParams {
     int w_f32;
 };
 
-// One CTA per row; thread i holds the row's elements (i + k blockDim) E .. + E
+// One CTA per row (few rows: latency-bound, 1.9 us for one row of 4096 bf16 in a
+// stream of such calls); thread i holds the row's elements (i + k blockDim) E .. + E
 // for k < NG in registers (fp32 sums), so memory is read once.  NG = 0: rows
 // too wide for that; the sums are read again for the second pass.
 template <int DT, int E, int NG, bool QUANT>
@@ -247,6 +248,8 @@ __global__ void __launch_bounds__(1024) fwd_kernel(const FwdParams p) {
 // keeps the granules of the next kAhead - 1 rows on their way into its own slots
 // of shared memory, so loads never wait for a row's reduction and stores.  At
 // least two CTAs share an SM: one works while the other meets at its barrier.
+// HBM-bound: 8192 x 6656 bf16 to e4m3 60.5 us = 6.3 TB/s (93 % of the measured copy
+// rate; 74 us with one CTA per row), 8192 x 8192 bf16 88 us (90 %).
 constexpr int kOwn = 2;
 constexpr int kRingThreads = 512;  // most threads of a CTA
 constexpr int kBwdAhead = 2;
@@ -419,7 +422,10 @@ __global__ void __launch_bounds__(1024) bwd_kernel(const BwdParams p) {
 // reduction instead of held in registers.  With MULTI a CTA works on `groups` short
 // rows at once, each with its own threads and named barrier, and adds up their dw at
 // the end, so that two CTAs per SM leave few partial rows (its weights are read again
-// for every row: in registers they would spill).
+// for every row: in registers they would spill).  HBM-bound for long rows: 8192 x
+// 6656 bf16 67 us (70 with the sum of the partial rows; 118 with one row per CTA
+// loaded at a time), 8192 x 8192 83 us (95 %); short rows are bound by a row's chain
+// of reduction and stores (8192 x 2048 32 us, 62 %).
 template <int DT, bool MULTI>
 __global__ void __launch_bounds__(kRingThreads, 2) bwd_ring_kernel(const BwdParams p) {
     constexpr int E = Elt<DT>::kPer16;

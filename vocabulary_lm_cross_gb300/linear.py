@@ -192,13 +192,17 @@ def _backward(gated, dy, x, weight, preact, act, bias_grad, want_dx, want_dweigh
     lib = capi.lib()
     need = (lib.vlmce_glu_bwd_workspace_bytes if gated else lib.vlmce_linear_bwd_workspace_bytes)(
         T, N, K)
-    w = workspace_of(workspace, need, dev)
+    # (without an activation and dbias the products read dy itself)
+    w = None
+    if workspace is not None or a != capi.ACT_NONE or b is not None or ds % 8 or \
+            dy.data_ptr() % 16:
+        w = workspace_of(workspace, need, dev)
     dw = dweight.data_ptr() if dweight is not None else None
     dwt = DTYPES[dweight.dtype] if dweight is not None else capi.F32
     head = (dy.data_ptr(), ds, x.data_ptr(), xs, weight.data_ptr(), ws, z, zs, DTYPES[dt], T, N, K,
             a, out.data_ptr() if out is not None else None, dxs, dw, dwt)
-    tail = (int(accumulate), err, w.data_ptr(), w.numel() * w.element_size(),
-            raw_stream(dev.index))
+    tail = (int(accumulate), err, w.data_ptr() if w is not None else None,
+            w.numel() * w.element_size() if w is not None else 0, raw_stream(dev.index))
     if gated:
         capi.check(lib.glu_bwd(*head, *tail), "glu_bwd")
     else:
