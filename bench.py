@@ -92,7 +92,7 @@ KERNEL_SOURCES = {
     "ce_split_kernel": ["ce_split.cuh", "ce_split_bf16.cu", "ce_split_f32.cu", "ce_common.cuh",
                         "ce_census.cuh", "ptx.cuh", "host_util.h", "ce.cu"],
     "vlmce_gemm_kernel": ["gemm.cuh", "gemm_types.h", "gemm_launch.h", "gemm.cu", "tcgen05.cuh",
-                          "ce_common.cuh", "ptx.cuh", "host_util.h", "flce.cu"],
+                          "mbar_wait.cuh", "ce_common.cuh", "ptx.cuh", "host_util.h", "flce.cu"],
 }
 
 

@@ -27,7 +27,7 @@
 
 #include "act.cuh"
 #include "mbar_wait.cuh"
-#include "ptx.cuh"
+#include "ptx_async.cuh"
 #include "tcgen05.cuh"
 
 namespace vlmce {

@@ -36,7 +36,7 @@
 #include "act.cuh"
 #include "mbar_wait.cuh"
 #include "mm_types.h"
-#include "ptx.cuh"
+#include "ptx_async.cuh"
 #include "tcgen05.cuh"
 
 namespace vlmce {

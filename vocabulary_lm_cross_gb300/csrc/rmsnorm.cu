@@ -22,7 +22,7 @@
 #include "act.cuh"
 #include "colsum.cuh"
 #include "host_util.h"
-#include "ptx.cuh"
+#include "ptx_async.cuh"
 #include "vlmce.h"
 
 namespace vlmce {
