@@ -216,3 +216,80 @@ def test_weight_gradient_added_to_and_in_place(T, H, dtype):
     close(a.dweight, dw, "f32", e, "dweight")
     assert torch.equal(acc, a.dweight + a.dweight)
     assert torch.equal(a.dx, d) and torch.equal(a.dweight, b.dweight)
+
+
+# rows that start at any alignment, enough of them for the kernels that keep rows in
+# flight; pad: elements between rows (every stride of a case has the same remainder)
+SHIFTED = [(4000, 1, 0), (4001, 9, 0), (3700, 501, 0), (3651, 263, 24), (1300, 2051, 8),
+           (2000, 1002, 6), (950, 4085, 0), (2000, 1004, 4), (1250, 3333, 0), (920, 8185, 0)]
+
+
+def strided(t, pad):
+    store = torch.full((t.shape[0], t.shape[1] + pad), float("nan"), dtype=t.dtype, device="cuda")
+    store[:, :t.shape[1]] = t
+    return store, store[:, :t.shape[1]]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("T,H,pad", SHIFTED)
+def test_rows_at_any_alignment(T, H, pad, dtype):
+    x, r, w = make(T, H, dtype, 7 * T + H)
+    e = (H + 32) * E24
+    y, s, rstd = ol.rmsnorm(f64(x), f64(w), f64(r), 1e-5)
+    (xs, xv), (rs, rv) = strided(x, pad), strided(r, pad)
+    (ys, yv), (ss, sv) = strided(torch.zeros_like(x), pad), strided(torch.zeros_like(x), pad)
+    res = v.rmsnorm_fwd(xv, w, rv, eps=1e-5, out=yv, residual_out=sv)
+    close(yv, y, dtype, e * np.abs(y), "y")
+    close(sv, s, dtype, E24 * np.abs(s), "residual")
+    close(res.rstd, rstd, "f32", e * rstd, "rstd")
+    assert torch.isnan(ys[:, H:]).all() and torch.isnan(ss[:, H:]).all()
+
+    q8 = v.rmsnorm_fwd(x, w, r, eps=1e-5, fp8=True)
+    scale = rstd * np.maximum(np.abs(s * f64(w)).max(axis=1), 1e-30) / 448.0
+    close(q8.scale, scale, "f32", e * scale, "scale")
+    q = y / scale[:, None]
+    bound = np.maximum(np.abs(q) * 2.0 ** -4, 2.0 ** -10) * (1 + 1e-5) + e * np.abs(q)
+    assert (np.abs(f64(q8.y.float()) - q) <= bound).all()
+    close(q8.residual, s, dtype, E24 * np.abs(s), "residual")
+
+    g = gen(T + H + 1)
+    dy, dr = randn(g, (T, H), DT[dtype], 0.1), randn(g, (T, H), DT[dtype], 0.1)
+    (_, dyv), (_, drv), (dxs, dxv) = strided(dy, pad), strided(dr, pad), strided(dy, pad)
+    grads = v.rmsnorm_bwd(dyv, sv, w, res.rstd, dresidual=drv, out=dxv)
+    s64, rs64 = f64(sv), f64(res.rstd)
+    dx, dw = ol.rmsnorm_backward(f64(dy), s64, f64(w), rs64, f64(dr))
+    a, xhat = np.abs(f64(dy) * f64(w)), np.abs(s64 * rs64[:, None])
+    terms = rs64[:, None] * (a + xhat * np.mean(a * xhat, axis=1, keepdims=True)) + np.abs(f64(dr))
+    close(dxv, dx, dtype, e * terms, "dx")
+    close(grads.dweight, dw, "f32", (T + 32) * E24 * (np.abs(f64(dy)) * xhat).sum(0), "dweight")
+    assert torch.isnan(dxs[:, H:]).all()
+    # over dy, and over dresidual
+    for buf in (dyv, drv):
+        got = v.rmsnorm_bwd(dyv, sv, w, res.rstd, dresidual=drv, out=buf)
+        assert torch.equal(buf, dxv) and torch.equal(got.dweight, grads.dweight)
+        buf.copy_(dy if buf is dyv else dr)
+    # the sum over x
+    got = v.rmsnorm_fwd(xv, w, rv, eps=1e-5, out=yv, residual_out=xv)
+    assert torch.equal(xv, sv) and torch.equal(got.rstd, res.rstd)
+
+
+@pytest.mark.parametrize("wdtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,H", [(4000, 501), (1000, 4085)])
+def test_rows_at_any_alignment_keep_non_finite_values_to_themselves(T, H, wdtype):
+    x, r, w = make(T, H, "bf16", 31, wdtype=wdtype)
+    clean = v.rmsnorm_fwd(x, w, r, weight_offset=1.0)
+    dy = randn(gen(32), (T, H), DT["bf16"])
+    ref = v.rmsnorm_bwd(dy, clean.residual, w, clean.rstd, weight_offset=1.0)
+    bad = torch.arange(1, T, 3, device="cuda")
+    x2, dy2 = x.clone(), dy.clone()
+    x2[bad] = float("nan")
+    x2[bad[::2]] = float("inf")
+    dy2[bad] = float("nan")
+    good = torch.ones(T, dtype=torch.bool, device="cuda")
+    good[bad] = False
+    got = v.rmsnorm_fwd(x2, w, r, weight_offset=1.0)
+    assert torch.equal(got.y[good], clean.y[good])
+    assert torch.equal(got.residual[good], clean.residual[good])
+    assert not torch.isfinite(got.y[bad]).all(dim=1).any()
+    grads = v.rmsnorm_bwd(dy2, clean.residual, w, clean.rstd, weight_offset=1.0)
+    assert torch.equal(grads.dx[good], ref.dx[good]) and torch.isnan(grads.dx[bad]).all()

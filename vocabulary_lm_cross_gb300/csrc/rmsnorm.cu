@@ -115,6 +115,52 @@ __device__ __forceinline__ void load_w(const void *w, bool f32, int i, float off
     for (int j = 0; j < E; ++j) v[j] += offset;
 }
 
+// Granules at a row's ends (the ring kernels' SHIFT): elements i .. i + E of which
+// only those in [0, H) belong to the row.
+template <int E>
+__device__ __forceinline__ bool at_end(int i, int H) {
+    return i < 0 || i + E > H;
+}
+template <int E>
+__device__ __forceinline__ void clear_outside(int i, int H, float (&v)[E]) {
+    if (at_end<E>(i, H)) {
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+            if (i + j < 0 || i + j >= H) v[j] = 0.f;
+    }
+}
+template <int DT, int E, bool E4M3>
+__device__ __forceinline__ void store_inside(unsigned char *row, int i, int H,
+                                             const float (&v)[E]) {
+    if (!at_end<E>(i, H)) {
+        if constexpr (E4M3)
+            store_e4m3<E>(row, i, v);
+        else
+            store_e<DT, E>(row, i, v);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+        if (i + j >= 0 && i + j < H) {
+            const float one[1] = {v[j]};
+            if constexpr (E4M3)
+                store_e4m3<1>(row, i + j, one);
+            else
+                store_e<DT, 1>(row, i + j, one);
+        }
+}
+// Weights i .. i + E at any alignment, zeros outside the row.
+template <int DT, int E>
+__device__ __forceinline__ void load_w_inside(const void *w, bool f32, int i, int H, float offset,
+                                              float (&v)[E]) {
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+        float one[1] = {0.f};
+        if (i + j >= 0 && i + j < H) load_w<DT, 1>(w, f32, i + j, offset, one);
+        v[j] = one[0];
+    }
+}
+
 // Sum of a (and, with MAX, the maximum of m >= 0) over the block, in every
 // thread.  sh: [2][32].
 template <bool MAX>
@@ -254,7 +300,13 @@ constexpr int kOwn = 2;
 constexpr int kRingThreads = 512;  // most threads of a CTA
 constexpr int kBwdAhead = 2;
 
-template <int DT, bool QUANT, int kFwdAhead>
+// SHIFT: rows whose first element is not on a 16-byte boundary.  Granules are those
+// of the memory, so the row's first element is element `shift` of its first granule;
+// all arrays have the same shift in a row, and the grid's size is a multiple of E, so a
+// CTA's rows all have it too (its weights stay where they are).  A granule at a row's
+// start also reads the end of the row before, which is left out of everything.
+// 8192 x 6661 bf16 77 us (147 element by element), to e4m3 66 us (131).
+template <int DT, bool QUANT, int kFwdAhead, bool SHIFT>
 __global__ void __launch_bounds__(kRingThreads, 2) fwd_ring_kernel(const FwdParams p) {
     constexpr int E = Elt<DT>::kPer16;
     extern __shared__ __align__(16) unsigned char ring[];  // [kFwdAhead][2][kOwn][threads][16]
@@ -264,12 +316,24 @@ __global__ void __launch_bounds__(kRingThreads, 2) fwd_ring_kernel(const FwdPara
     int at[kOwn];
     bool in[kOwn];
     float w[kOwn][E];
+    const int shift =
+        SHIFT ? static_cast<int>(blockIdx.x * (p.x_ld / Elt<DT>::kBytes) % E) : 0;
 #pragma unroll
     for (int k = 0; k < kOwn; ++k) {
-        at[k] = static_cast<int>(k * blockDim.x + threadIdx.x) * E;
+        at[k] = static_cast<int>(k * blockDim.x + threadIdx.x) * E - shift;
         in[k] = at[k] < p.H;
-        if (in[k]) load_w<DT, E>(p.weight, p.w_f32 != 0, at[k], p.offset, w[k]);
+        if constexpr (SHIFT)
+            load_w_inside<DT, E>(p.weight, p.w_f32 != 0, at[k], p.H, p.offset, w[k]);
+        else if (in[k])
+            load_w<DT, E>(p.weight, p.w_f32 != 0, at[k], p.offset, w[k]);
     }
+    auto copy = [&](unsigned char *dst, const unsigned char *row, int i) {
+        const unsigned char *src = row + i * Elt<DT>::kBytes;
+        if constexpr (SHIFT)
+            ptx::cp_async16_first(ptx::smem_addr(dst), src, min(E, p.H - i) * Elt<DT>::kBytes);
+        else
+            ptx::cp_async16(ptx::smem_addr(dst), src);
+    };
     auto slot = [&](int s, int which, int k) {
         return ring + 16 * (((s * 2 + which) * kOwn + k) * blockDim.x + threadIdx.x);
     };
@@ -278,11 +342,8 @@ __global__ void __launch_bounds__(kRingThreads, 2) fwd_ring_kernel(const FwdPara
 #pragma unroll
             for (int k = 0; k < kOwn; ++k)
                 if (in[k]) {
-                    const int64_t off = at[k] * Elt<DT>::kBytes;
-                    ptx::cp_async16(ptx::smem_addr(slot(s, 0, k)), p.x + row * p.x_ld + off);
-                    if (p.residual)
-                        ptx::cp_async16(ptx::smem_addr(slot(s, 1, k)),
-                                        p.residual + row * p.residual_ld + off);
+                    copy(slot(s, 0, k), p.x + row * p.x_ld, at[k]);
+                    if (p.residual) copy(slot(s, 1, k), p.residual + row * p.residual_ld, at[k]);
                 }
         }
         ptx::cp_async_commit();
@@ -305,12 +366,18 @@ __global__ void __launch_bounds__(kRingThreads, 2) fwd_ring_kernel(const FwdPara
 #pragma unroll
                     for (int j = 0; j < E; ++j) v[k][j] += r[j];
                 }
+                if constexpr (SHIFT) clear_outside<E>(at[k], p.H, v[k]);
 #pragma unroll
                 for (int j = 0; j < E; ++j) {
                     ss = fmaf(v[k][j], v[k][j], ss);
                     if constexpr (QUANT) mx = fmaxf(mx, fabsf(v[k][j] * w[k][j]));
                 }
-                if (p.sum) store_e<DT, E>(p.sum + row * p.sum_ld, at[k], v[k]);
+                if (p.sum) {
+                    if constexpr (SHIFT)
+                        store_inside<DT, E, false>(p.sum + row * p.sum_ld, at[k], p.H, v[k]);
+                    else
+                        store_e<DT, E>(p.sum + row * p.sum_ld, at[k], v[k]);
+                }
             }
         block_sum_max<QUANT>(ss, mx, sh[flip]);  // two buffers: one barrier a row
         const float rstd = __frsqrt_rn(ss / static_cast<float>(p.H) + p.eps);
@@ -326,7 +393,9 @@ __global__ void __launch_bounds__(kRingThreads, 2) fwd_ring_kernel(const FwdPara
 #pragma unroll
                 for (int j = 0; j < E; ++j)
                     v[k][j] = QUANT ? v[k][j] * w[k][j] * mul : v[k][j] * mul * w[k][j];
-                if constexpr (QUANT)
+                if constexpr (SHIFT)
+                    store_inside<DT, E, QUANT>(p.y + row * p.y_ld, at[k], p.H, v[k]);
+                else if constexpr (QUANT)
                     store_e4m3<E>(p.y + row * p.y_ld, at[k], v[k]);
                 else
                     store_e<DT, E>(p.y + row * p.y_ld, at[k], v[k]);
@@ -336,6 +405,20 @@ __global__ void __launch_bounds__(kRingThreads, 2) fwd_ring_kernel(const FwdPara
 }
 
 // ------------------------------------------------------------ backward
+// A thread's columns i .. i + E of a CTA's partial dw, in whole 16 bytes (in single
+// floats, 8 apart in a warp, they took 600 x 4096 bf16 from 9.1 to 16.7 us).
+template <int E>
+__device__ __forceinline__ void store_part(float *part, int i, const float (&dw)[E]) {
+    if constexpr (E == 1) {
+        part[i] = dw[0];
+    } else {
+#pragma unroll
+        for (int j = 0; j < E; j += 4)
+            *reinterpret_cast<float4 *>(part + i + j) =
+                make_float4(dw[j], dw[j + 1], dw[j + 2], dw[j + 3]);
+    }
+}
+
 struct BwdParams {
     const unsigned char *dy, *x, *dres;
     const void *weight;
@@ -412,21 +495,20 @@ __global__ void __launch_bounds__(1024) bwd_kernel(const BwdParams p) {
         float *part = p.part + static_cast<int64_t>(blockIdx.x) * p.H;
 #pragma unroll
         for (int k = 0; k < NG; ++k)
-#pragma unroll
-            for (int j = 0; j < E; ++j)
-                if (i0 + k * step < p.H) part[i0 + k * step + j] = dw[k][j];
+            if (i0 + k * step < p.H) store_part<E>(part, i0 + k * step, dw[k]);
     }
 }
 
 // The same with the ring of fwd_ring_kernel, read a second time after a row's
 // reduction instead of held in registers.  With MULTI a CTA works on `groups` short
 // rows at once, each with its own threads and named barrier, and adds up their dw at
-// the end, so that two CTAs per SM leave few partial rows (its weights are read again
-// for every row: in registers they would spill).  HBM-bound for long rows: 8192 x
+// the end, so that two CTAs per SM leave few partial rows (its weights are in shared
+// memory: in registers they would spill).  HBM-bound for long rows: 8192 x
 // 6656 bf16 67 us (70 with the sum of the partial rows; 118 with one row per CTA
 // loaded at a time), 8192 x 8192 83 us (95 %); short rows are bound by a row's chain
-// of reduction and stores (8192 x 2048 32 us, 62 %).
-template <int DT, bool MULTI>
+// of reduction and stores (8192 x 2048 30 us, 67 %).  SHIFT as above: 8192 x 6661 83 us
+// (225 element by element).
+template <int DT, bool MULTI, bool SHIFT>
 __global__ void __launch_bounds__(kRingThreads, 2) bwd_ring_kernel(const BwdParams p) {
     constexpr int E = Elt<DT>::kPer16;
     extern __shared__ __align__(16) unsigned char ring[];  // [kBwdAhead][3][kOwn][threads][16]
@@ -439,37 +521,63 @@ __global__ void __launch_bounds__(kRingThreads, 2) bwd_ring_kernel(const BwdPara
     const int gw = gt >> 5;
     const int group = MULTI ? static_cast<int>(threadIdx.x) / gt : 0;
     const int tg = static_cast<int>(threadIdx.x) - group * gt;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * groups + group;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
     int at[kOwn];
     bool in[kOwn];
     float w[kOwn][E], dw[kOwn][E];
+    const int shift = SHIFT ? static_cast<int>(first * (p.x_ld / Elt<DT>::kBytes) % E) : 0;
+    auto load = [&](int i, float offset, float (&v)[E]) {
+        if constexpr (SHIFT)
+            load_w_inside<DT, E>(p.weight, p.w_f32 != 0, i, p.H, offset, v);
+        else
+            load_w<DT, E>(p.weight, p.w_f32 != 0, i, offset, v);
+    };
+    auto w_slot = [&](int k) {  // MULTI: weights of the rows' type
+        return ring + 16 * ((kBwdAhead * 3 * kOwn + k) * blockDim.x + threadIdx.x);
+    };
+    auto weights = [&](int k, float (&v)[E]) {
+        if (DT != VLMCE_F32 && p.w_f32 != 0) {
+            load(at[k], p.offset, v);
+        } else {
+            load_e<DT, E>(w_slot(k), 0, v);
+#pragma unroll
+            for (int j = 0; j < E; ++j) v[j] += p.offset;
+        }
+    };
 #pragma unroll
     for (int k = 0; k < kOwn; ++k) {
-        at[k] = (k * gt + tg) * E;
+        at[k] = (k * gt + tg) * E - shift;
         in[k] = at[k] < p.H;
-        if (!MULTI && in[k]) load_w<DT, E>(p.weight, p.w_f32 != 0, at[k], p.offset, w[k]);
+        if (in[k]) {
+            load(at[k], MULTI ? 0.f : p.offset, w[k]);
+            if constexpr (MULTI) store_e<DT, E>(w_slot(k), 0, w[k]);
+        }
 #pragma unroll
         for (int j = 0; j < E; ++j) dw[k][j] = 0.f;
     }
     auto slot = [&](int s, int which, int k) {
         return ring + 16 * (((s * 3 + which) * kOwn + k) * blockDim.x + threadIdx.x);
     };
+    auto copy = [&](unsigned char *dst, const unsigned char *row, int i) {
+        const unsigned char *src = row + i * Elt<DT>::kBytes;
+        if constexpr (SHIFT)
+            ptx::cp_async16_first(ptx::smem_addr(dst), src, min(E, p.H - i) * Elt<DT>::kBytes);
+        else
+            ptx::cp_async16(ptx::smem_addr(dst), src);
+    };
     auto fetch = [&](int64_t row, int s) {
         if (row < p.T) {
 #pragma unroll
             for (int k = 0; k < kOwn; ++k)
                 if (in[k]) {
-                    const int64_t off = at[k] * Elt<DT>::kBytes;
-                    ptx::cp_async16(ptx::smem_addr(slot(s, 0, k)), p.dy + row * p.dy_ld + off);
-                    ptx::cp_async16(ptx::smem_addr(slot(s, 1, k)), p.x + row * p.x_ld + off);
-                    if (p.dres)
-                        ptx::cp_async16(ptx::smem_addr(slot(s, 2, k)),
-                                        p.dres + row * p.dres_ld + off);
+                    copy(slot(s, 0, k), p.dy + row * p.dy_ld, at[k]);
+                    copy(slot(s, 1, k), p.x + row * p.x_ld, at[k]);
+                    if (p.dres) copy(slot(s, 2, k), p.dres + row * p.dres_ld, at[k]);
                 }
         }
         ptx::cp_async_commit();
     };
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * groups + group;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
     const float inv_h = 1.f / static_cast<float>(p.H);
     for (int n = 0; n < kBwdAhead - 1; ++n) fetch(first + n * step, n);
     float rstd = 0.f, next = first < p.T ? p.rstd[first] : 0.f;
@@ -486,7 +594,11 @@ __global__ void __launch_bounds__(kRingThreads, 2) bwd_ring_kernel(const BwdPara
                 float d[E], h[E];
                 load_e<DT, E>(slot(s, 0, k), 0, d);
                 load_e<DT, E>(slot(s, 1, k), 0, h);
-                if (MULTI) load_w<DT, E>(p.weight, p.w_f32 != 0, at[k], p.offset, w[k]);
+                if constexpr (MULTI) weights(k, w[k]);
+                if constexpr (SHIFT) {
+                    clear_outside<E>(at[k], p.H, d);
+                    clear_outside<E>(at[k], p.H, h);
+                }
 #pragma unroll
                 for (int j = 0; j < E; ++j) {
                     const float g = d[j] * (h[j] * rstd);
@@ -512,40 +624,50 @@ __global__ void __launch_bounds__(kRingThreads, 2) bwd_ring_kernel(const BwdPara
                 float d[E], h[E], r[E];
                 load_e<DT, E>(slot(s, 0, k), 0, d);
                 load_e<DT, E>(slot(s, 1, k), 0, h);
-                if (MULTI) load_w<DT, E>(p.weight, p.w_f32 != 0, at[k], p.offset, w[k]);
+                if constexpr (MULTI) weights(k, w[k]);
 #pragma unroll
                 for (int j = 0; j < E; ++j) r[j] = 0.f;
                 if (p.dres) load_e<DT, E>(slot(s, 2, k), 0, r);
 #pragma unroll
                 for (int j = 0; j < E; ++j)
                     r[j] = fmaf(rstd, fmaf(d[j], w[k][j], -(h[j] * rstd) * c), r[j]);
-                store_e<DT, E>(p.dx + row * p.dx_ld, at[k], r);
+                if constexpr (SHIFT)
+                    store_inside<DT, E, false>(p.dx + row * p.dx_ld, at[k], p.H, r);
+                else
+                    store_e<DT, E>(p.dx + row * p.dx_ld, at[k], r);
             }
         if (++s == kBwdAhead) s = 0;
     }
     if (!p.part) return;
     float *part = p.part + static_cast<int64_t>(blockIdx.x) * p.H;
-    if constexpr (!MULTI) {
+    if constexpr (!MULTI && !SHIFT) {
 #pragma unroll
         for (int k = 0; k < kOwn; ++k)
-            if (in[k]) {
-#pragma unroll
-                for (int j = 0; j < E; j += 4)
-                    *reinterpret_cast<float4 *>(part + at[k] + j) =
-                        make_float4(dw[k][j], dw[k][j + 1], dw[k][j + 2], dw[k][j + 3]);
-            }
+            if (in[k]) store_part<E>(part, at[k], dw[k]);
     } else {
         // [groups][kOwn gt E] floats in the ring, which no copy writes any more
         float *sum = reinterpret_cast<float *>(ring);
         const int width = kOwn * gt * E;
         ptx::cp_async_wait<0>();
         __syncthreads();
+        if constexpr (SHIFT) {  // (each group's columns start elsewhere)
+#pragma unroll
+            for (int k = 0; k < kOwn; ++k)
+#pragma unroll
+                for (int j = 0; j < E; ++j)
+                    if (at[k] + j >= 0 && at[k] + j < p.H)
+                        sum[group * width + at[k] + j] = dw[k][j];
+            __syncthreads();
+            for (int i = static_cast<int>(threadIdx.x); i < p.H; i += static_cast<int>(blockDim.x)) {
+                float a = sum[i];
+                for (int g = 1; g < groups; ++g) a += sum[g * width + i];
+                part[i] = a;
+            }
+            return;
+        }
 #pragma unroll
         for (int k = 0; k < kOwn; ++k)
-#pragma unroll
-            for (int j = 0; j < E; j += 4)
-                *reinterpret_cast<float4 *>(sum + group * width + at[k] + j) =
-                    make_float4(dw[k][j], dw[k][j + 1], dw[k][j + 2], dw[k][j + 3]);
+            store_part<E>(sum + group * width, at[k], dw[k]);
         __syncthreads();
         for (int i = 4 * static_cast<int>(threadIdx.x); i < p.H;
              i += 4 * static_cast<int>(blockDim.x)) {
@@ -562,8 +684,8 @@ __global__ void __launch_bounds__(kRingThreads, 2) bwd_ring_kernel(const BwdPara
     }
 }
 
-// Rows too wide for one CTA's registers (unaligned ones from 4097 elements on: 16
-// elements of four arrays per thread spill, 4096 x 6661 bf16 167 us, so: 117): the
+// Rows too wide for one CTA's registers, and element by element from 4097 elements on
+// (16 elements of four arrays per thread spill: 4096 x 6661 bf16 167 us, so: 117): the
 // rows' mean(a xhat), then dx and the partial dw by column segments.
 template <int DT, int E>
 __global__ void __launch_bounds__(512) dot_kernel(const BwdParams p) {
@@ -622,10 +744,7 @@ __global__ void __launch_bounds__(512) segment_kernel(const BwdParams p) {
             }
         }
     }
-    if (p.part) {
-#pragma unroll
-        for (int j = 0; j < E; ++j) p.part[static_cast<int64_t>(blockIdx.y) * p.H + i + j] = dw[j];
-    }
+    if (p.part) store_part<E>(p.part + static_cast<int64_t>(blockIdx.y) * p.H, i, dw);
 }
 
 // ------------------------------------------------------------ host side
@@ -709,30 +828,41 @@ FwdKernel fwd_kernel_of(int32_t dtype, bool quant, bool vec, int ng) {
             return quant ? fwd_pick<VLMCE_F16, true>(vec, ng) : fwd_pick<VLMCE_F16, false>(vec, ng);
     }
 }
-// Threads of the ring kernels, kOwn granules of 16 bytes each; 0: the row is too
-// wide.
-int ring_threads(int64_t H, int32_t dtype) {
-    const int64_t granules = H * elt_of(dtype) / 16;
+// Threads of the ring kernels, kOwn granules of 16 bytes each (`shifted` rows can
+// touch one more at an end); 0: the row is too wide.
+int ring_threads(int64_t H, int32_t dtype, bool shifted) {
+    const int64_t E = 16 / elt_of(dtype);
+    const int64_t granules = shifted ? (H + 2 * E - 2) / E : H / E;
     return granules <= kOwn * kRingThreads
                ? static_cast<int>(round_up((granules + kOwn - 1) / kOwn, 32))
                : 0;
 }
-template <bool Q, int A>
-FwdKernel fwd_ring_of(int32_t dtype) {
+template <bool Q, int A, bool S>
+FwdKernel fwd_ring_typed(int32_t dtype) {
     switch (dtype) {
-        case VLMCE_F32: return fwd_ring_kernel<VLMCE_F32, Q, A>;
-        case VLMCE_BF16: return fwd_ring_kernel<VLMCE_BF16, Q, A>;
-        default: return fwd_ring_kernel<VLMCE_F16, Q, A>;
+        case VLMCE_F32: return fwd_ring_kernel<VLMCE_F32, Q, A, S>;
+        case VLMCE_BF16: return fwd_ring_kernel<VLMCE_BF16, Q, A, S>;
+        default: return fwd_ring_kernel<VLMCE_F16, Q, A, S>;
     }
 }
+template <bool S>
+FwdKernel fwd_ring_of(int32_t dtype, bool quant, int ahead) {
+    if (ahead == 2)
+        return quant ? fwd_ring_typed<true, 2, S>(dtype) : fwd_ring_typed<false, 2, S>(dtype);
+    return quant ? fwd_ring_typed<true, 3, S>(dtype) : fwd_ring_typed<false, 3, S>(dtype);
+}
 using BwdKernel = void (*)(const BwdParams);
-template <bool MULTI>
-BwdKernel bwd_ring_of(int32_t dtype) {
+template <bool MULTI, bool S>
+BwdKernel bwd_ring_typed(int32_t dtype) {
     switch (dtype) {
-        case VLMCE_F32: return bwd_ring_kernel<VLMCE_F32, MULTI>;
-        case VLMCE_BF16: return bwd_ring_kernel<VLMCE_BF16, MULTI>;
-        default: return bwd_ring_kernel<VLMCE_F16, MULTI>;
+        case VLMCE_F32: return bwd_ring_kernel<VLMCE_F32, MULTI, S>;
+        case VLMCE_BF16: return bwd_ring_kernel<VLMCE_BF16, MULTI, S>;
+        default: return bwd_ring_kernel<VLMCE_F16, MULTI, S>;
     }
+}
+BwdKernel bwd_ring_of(int32_t dtype, bool multi, bool shifted) {
+    if (shifted) return multi ? bwd_ring_typed<true, true>(dtype) : bwd_ring_typed<false, true>(dtype);
+    return multi ? bwd_ring_typed<true, false>(dtype) : bwd_ring_typed<false, false>(dtype);
 }
 template <int DT>
 BwdKernel bwd_pick(bool vec, int ng) {
@@ -850,19 +980,28 @@ extern "C" vlmce_status rmsnorm_fwd(const void *x, int64_t x_stride, const void 
     p.offset = weight_offset;
     p.w_f32 = weight_dtype == VLMCE_F32;
     cudaStream_t st_ = reinterpret_cast<cudaStream_t>(stream);
-    const int rt = vec ? ring_threads(H, dtype) : 0;
+    // rows at any alignment, the same in all arrays
+    auto like_x = [&](const void *q, int64_t ld, int bytes) {
+        return !q || (ld % E == x_stride % E && aligned(q, static_cast<uintptr_t>(bytes)));
+    };
+    const bool shifted = !vec && aligned(x, 16) && like_x(y, y_stride, E * yelt) &&
+                         like_x(residual, residual_stride, 16) &&
+                         like_x(residual_out, residual_out_stride, 16);
+    const int rt = vec || shifted ? ring_threads(H, dtype, shifted) : 0;
     if (rt > 0) {
         const int per_sm = per_sm_of(rt);
-        const int64_t ctas = static_cast<int64_t>(dev.sm_count) * per_sm;
-        // rows in flight: long 16-bit rows fill the memory system with one row ahead
+        const int64_t ctas = static_cast<int64_t>(dev.sm_count) * per_sm / (shifted ? E : 1) *
+                             (shifted ? E : 1);
+        // rows ahead: long 16-bit rows fill the memory system with one row ahead
         // (8192 x 6656 bf16 to e4m3: 59 us, two rows ahead 65), others need two
         // (8192 x 1024 bf16: 11.7 against 15.7; 4096 x 4096 fp32: 45.8 against 48)
         const int ahead = elt == 2 && H >= 4096 ? 2 : 3;
-        if (T >= 3 * ctas) {  // rows enough to run ahead
-            const FwdKernel k = ahead == 2 ? quant ? fwd_ring_of<true, 2>(dtype)
-                                                   : fwd_ring_of<false, 2>(dtype)
-                                : quant ? fwd_ring_of<true, 3>(dtype)
-                                        : fwd_ring_of<false, 3>(dtype);
+        // rows enough for that; one CTA per row has the lower latency, but goes element by
+        // element through shifted rows (1200 x 2001 bf16 5.2 us, the ring 4.8; 8192 x
+        // 1001 19.7 and 14.8; 8192 x 701 14.5 and 15.0)
+        if (ctas > 0 && (shifted ? H > 768 && 2 * T >= ctas : T >= 3 * ctas)) {
+            const FwdKernel k = shifted ? fwd_ring_of<true>(dtype, quant, ahead)
+                                        : fwd_ring_of<false>(dtype, quant, ahead);
             return launch_status(launch(k, dim3(static_cast<unsigned>(ctas), 1, 1), rt,
                                         static_cast<size_t>(ahead) * 2 * kOwn * 16 * rt, st_, p),
                                  "rmsnorm_fwd");
@@ -949,18 +1088,32 @@ extern "C" vlmce_status rmsnorm_bwd(const void *dy, int64_t dy_stride, const voi
     p.offset = weight_offset;
     p.w_f32 = weight_dtype == VLMCE_F32;
     int64_t parts;
-    const int rt = vec ? ring_threads(H, dtype) : 0;
+    auto like_x = [&](const void *q, int64_t ld) {
+        return !q || (ld % E == x_stride % E && aligned(q, 16));
+    };
+    const bool shifted = !vec && aligned(x, 16) && like_x(dy, dy_stride) && like_x(dx, dx_stride) &&
+                         like_x(dresidual, dresidual_stride);
+    const int rt = vec || shifted ? ring_threads(H, dtype, shifted) : 0;
     // rows of up to 128 threads share a CTA, two CTAs per SM; longer ones have their
     // own, 1024 threads per SM
     p.groups = rt > 0 && rt <= 128 ? std::min(15, kRingThreads / rt) : 1;
+    const int64_t full = static_cast<int64_t>(dev.sm_count) * (rt > 128 ? per_sm_of(rt) : 2);
+    const int64_t unit = shifted ? E : 1;
     const int64_t ring_ctas =
-        static_cast<int64_t>(dev.sm_count) * (rt > 128 ? per_sm_of(rt) : 2);
+        std::min(full, (T + p.groups - 1) / p.groups) / unit * unit;
+    // Rows enough to run ahead (us, the ring and bwd_kernel).  Rows that share a CTA
+    // leave fewer partial rows, so theirs may be fewer: 1200 x 1024 bf16 8.2 and 9.3,
+    // 600 x 1024 7.5 and 6.0; longer ones 600 x 6656 10.4 and 11.2, 300 x 6656 7.7 and
+    // 8.0, 1200 x 2048 8.9 and 7.8; shifted 8192 x 1001 26 and 49, 1200 x 1001 12.5
+    // and 8.6.
+    const int64_t needed = rt <= 64 && !shifted ? full * p.groups / 4 : full * p.groups;
     cudaError_t e;
-    if (rt > 0 && T >= 2 * ring_ctas * p.groups && ring_ctas <= parts_max) {
+    if (rt > 0 && ring_ctas > 0 && T >= needed && ring_ctas <= parts_max) {
         parts = ring_ctas;
         const int threads = p.groups * rt;
-        e = launch(p.groups > 1 ? bwd_ring_of<true>(dtype) : bwd_ring_of<false>(dtype), dim3(static_cast<unsigned>(parts), 1, 1), threads,
-                   static_cast<size_t>(kBwdAhead) * 3 * kOwn * 16 * threads, s, p);
+        e = launch(bwd_ring_of(dtype, p.groups > 1, shifted),
+                   dim3(static_cast<unsigned>(parts), 1, 1), threads,
+                   static_cast<size_t>(kBwdAhead * 3 + (p.groups > 1)) * kOwn * 16 * threads, s, p);
     } else if (sh.ng > 0 && sh.ng < 16) {
         parts = std::min<int64_t>(parts_max, static_cast<int64_t>(dev.sm_count) *
                                                  std::max(2, per_sm_of(sh.threads)));
