@@ -44,9 +44,10 @@ int chunks_of(const Fwd &f) {
 using LargeKernel = void (*)(const LargeMaps, const LargeParams);
 using SmallKernel = void (*)(const CUtensorMap, const CUtensorMap, const SmallParams);
 
-LargeKernel large_kernel(bool gated, bool fp8) {
-    if (gated) return fp8 ? mm_large_kernel<true, true> : mm_large_kernel<true, false>;
-    return fp8 ? mm_large_kernel<false, true> : mm_large_kernel<false, false>;
+LargeKernel large_kernel(bool gated, bool fp8, bool add) {
+    if (gated) return fp8 ? mm_large_kernel<true, true, false> : mm_large_kernel<true, false, false>;
+    if (add) return fp8 ? mm_large_kernel<false, true, true> : mm_large_kernel<false, false, true>;
+    return fp8 ? mm_large_kernel<false, true, false> : mm_large_kernel<false, false, false>;
 }
 SmallKernel small_kernel(bool gated, bool fp8, bool w_mn) {
     if (w_mn) return mm_small_kernel<false, false, true>;
@@ -110,8 +111,8 @@ cudaError_t setup(Capacity *out) {
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, small_budget(1));
             if (e != cudaSuccess) return e;
         }
-        for (int k = 0; k < 4; ++k) {
-            const LargeKernel lk = large_kernel(k & 1, k & 2);
+        for (int k = 0; k < 8; ++k) {
+            const LargeKernel lk = large_kernel(k & 1, k & 2, k & 4);
             e = cudaFuncSetAttribute(lk, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
             int n = 0;
             if (e == cudaSuccess) e = clusters_of(lk, 2, kPairThreads, kPairSmem, &n);
@@ -295,7 +296,7 @@ cudaError_t forward_large(const Fwd &f, const Capacity &cap, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, large_kernel(f.gated != 0, f.dtype == VLMCE_E4M3), maps,
+    return cudaLaunchKernelEx(&cfg, large_kernel(f.gated != 0, f.dtype == VLMCE_E4M3, f.e.residual), maps,
                               static_cast<const LargeParams>(p));
 }
 

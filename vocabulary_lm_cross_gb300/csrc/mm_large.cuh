@@ -48,28 +48,26 @@ struct LargeMaps {
     CUtensorMap y, z, z_up;    // outputs with 16-byte aligned rows
 };
 
-// A warp's accumulators of 32 tokens (one per lane) x 32 outputs from `col`, as z:
-// scaled, the bias added.
-__device__ __forceinline__ void acc_seg(uint32_t acc, const Epi &e, int col, int scale_col, int N,
-                                        float xs, bool bias, float (&v)[32]) {
+// A warp's accumulators of 32 tokens (one per lane) x 32 outputs, as z: scaled, the
+// bias added; lane j has output j's scale and bias.
+__device__ __forceinline__ void acc_seg(uint32_t acc, bool scaled, float xs, float ws, bool biased,
+                                        float bias, float (&v)[32]) {
     uint32_t r[32];
     tc::tmem_ld32(acc, r);
     tc::tmem_ld_wait();
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-    if (e.ws) {
+    if (scaled) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (col + j < N) v[j] *= xs * e.ws[scale_col + j];
+        for (int j = 0; j < 32; ++j) v[j] *= xs * __shfl_sync(0xffffffffu, ws, j);
     }
-    if (bias && e.bias) {
+    if (biased) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (col + j < N) v[j] += act::from16(e.bias[col + j], e.f16 != 0);
+        for (int j = 0; j < 32; ++j) v[j] += __shfl_sync(0xffffffffu, bias, j);
     }
 }
 
-template <bool GATED, bool FP8>
+template <bool GATED, bool FP8, bool ADD>
 __global__ void __launch_bounds__(kPairThreads, 1)
     mm_large_kernel(const __grid_constant__ LargeMaps maps, const __grid_constant__ LargeParams p) {
     constexpr int kPer = 2;
@@ -138,35 +136,59 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const Out y = {e.y, e.y_ld, e.y_vec, &maps.y};
         const Out z = {e.preact, e.preact_ld, e.preact_vec, &maps.z};
         const Out z_up = {e.preact + p.N, e.preact_ld, e.preact_up_vec, &maps.z_up};
-        const bool staged = y.vec < 16;  // y's segments leave the buffer empty
         int it = 0;
         for (int t; (t = tiles.next(q, lane)) >= 0; ++it) {
             const LargeTile tl = large_tile<GATED>(p, t);
             const int64_t row0 = tl.m0 + kHalfRows * rank + (warp & 3) * 32;
-            const float xs = e.xs && row0 + lane < p.T ? e.xs[row0 + lane] : 1.f;
-            const uint32_t acc = acc_wait(q, it, warp);
             // 64 columns at a time: one group of a gated tile's 128 outputs per
             // half, two of a linear tile's 256
             constexpr int kGroups = GATED ? 1 : 2;
+            const int col0 = tl.n0 + 64 * kGroups * half;
+            // what the outputs take from memory comes while the tile's sums do
+            const float xs = e.xs && row0 + lane < p.T ? e.xs[row0 + lane] : 1.f;
+            float ws[4], bias[4];  // of columns col0 + 32 i + lane (gated: two of gate, two of up)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int c = col0 + 32 * (GATED ? i & 1 : i) + lane;
+                const int up = GATED && i >= 2 ? p.up_row : 0;
+                ws[i] = FP8 && c < p.N ? e.ws[up + c] : 1.f;
+                bias[i] = !GATED && e.bias && c < p.N ? act::from16(e.bias[c], f16) : 0.f;
+            }
+            RowFetch next;
+            if constexpr (ADD)
+                fetch_row(e.residual, e.residual_ld, row0 + lane, col0, p.T, p.N, next);
+            const uint32_t acc = acc_wait(q, it, warp) + 64 * kGroups * half;
 #pragma unroll 1
-            for (int g = kGroups * half; g < kGroups * (half + 1); ++g) {
-                const int col = tl.n0 + 64 * g;
-                if (col >= p.N || row0 >= p.T) continue;
+            for (int g = 0; g < kGroups; ++g) {
+                const int col = col0 + 64 * g;
+                if (col >= p.N || row0 >= p.T) break;
+                uint32_t add[32];
+                bool whole = false;
+                if constexpr (ADD) {
+                    whole = next.whole;
+                    align_row(next, add);
+                    if (g + 1 < kGroups)
+                        fetch_row(e.residual, e.residual_ld, row0 + lane, col + 64, p.T, p.N, next);
+                }
+                auto z_seg = [&](int h, float (&v)[32]) {
+                    acc_seg(acc + 64 * g + 32 * h, FP8, xs, h ? ws[1] : ws[0],
+                            !GATED && e.bias, h ? bias[1] : bias[0], v);
+                };
+                auto up_seg = [&](int h, float (&v)[32]) {
+                    acc_seg(acc + 128 + 32 * h, FP8, xs, h ? ws[3] : ws[2], false, 0.f, v);
+                };
                 if (e.preact) {
 #pragma unroll 1
                     for (int h = 0; h < 2; ++h) {
                         float v[32];
-                        const int c = col + 32 * h;
-                        acc_seg(acc + 64 * g + 32 * h, e, c, c, p.N, xs, !GATED, v);
+                        z_seg(h, v);
                         put_seg(z, row0, col, h, v, p.T, p.N, f16, buf, lane);
                     }
                     if constexpr (GATED) {
 #pragma unroll 1
                         for (int h = 0; h < 2; ++h) {
                             float v[32];
-                            const int c = col + 32 * h;
-                            acc_seg(acc + 128 + 64 * g + 32 * h, e, c, p.up_row + c, p.N, xs,
-                                    false, v);
+                            up_seg(h, v);
                             put_seg(z_up, row0, col, h, v, p.T, p.N, f16, buf, lane);
                         }
                     }
@@ -174,20 +196,41 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
                     float v[32];
-                    const int c = col + 32 * h;
-                    acc_seg(acc + 64 * g + 32 * h, e, c, c, p.N, xs, !GATED, v);
+                    z_seg(h, v);
                     act::apply_n(v, e.act);
                     if constexpr (GATED) {
                         float u[32];
-                        acc_seg(acc + 128 + 64 * g + 32 * h, e, c, p.up_row + c, p.N, xs, false, u);
+                        up_seg(h, u);
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] *= u[j];
-                    } else if (e.residual) {
-                        add_seg(e.residual, e.residual_ld, e.residual_vec, row0, c, v, p.T, p.N,
-                                f16, staged, buf, lane);
                     }
-                    __syncwarp();
+                    if constexpr (ADD) {
+                        const int c = col + 32 * h;
+                        if (whole) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                float a, b;
+                                act::unpack16x2(add[j], a, b, f16);
+                                v[2 * j] += a;
+                                v[2 * j + 1] += b;
+                                add[j] = add[16 + j];
+                            }
+                        } else if (row0 + lane < p.T) {
+                            const uint16_t *at = e.residual + (row0 + lane) * e.residual_ld + c;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (c + j < p.N) v[j] += act::from16(at[j], f16);
+                        }
+                        __syncwarp();
+                    }
                     put_seg(y, row0, col, h, v, p.T, p.N, f16, buf, lane);
+                }
+                if constexpr (!GATED) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        ws[i] = ws[2 + i];
+                        bias[i] = bias[2 + i];
+                    }
                 }
             }
             acc_release(tempty_leader, it, lane);

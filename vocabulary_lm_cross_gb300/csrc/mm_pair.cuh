@@ -337,49 +337,46 @@ __device__ __forceinline__ void put_seg(const Out &o, int64_t row0, int col, int
         for (int r = 0; r < nr; ++r) p[r * o.ld] = s16[r * 34 + lane];
     }
 }
-// v += the 32 columns from `col` of a 16-bit tensor; with `staged` unaligned rows
-// pass through the warp's buffer, which must hold nothing.
-__device__ __forceinline__ void add_seg(const uint16_t *base, int64_t ld, int vec, int64_t row0,
-                                        int col, float (&v)[32], int64_t rows, int cols, bool f16,
-                                        bool staged, uint32_t *buf, int lane) {
-    uint32_t u[16];
-    const uint16_t *p = base + (row0 + lane) * ld + col;
-    const bool row_ok = row0 + lane < rows;
-    if (vec >= 16 && col + 32 <= cols) {
-        if (!row_ok) return;
+// 64 columns from `col` of row `row` of a 16-bit tensor, one row per lane, on their
+// way in registers: the 16-byte granules of the memory that hold them, at any
+// alignment.  Fetched a group of columns ahead: behind the ring's copies an answer
+// takes thousands of clocks.
+struct RowFetch {
+    uint4 q[9];
+    const uint16_t *at;
+    bool whole;  // every granule lies inside the tensor; else take the elements one by one
+};
+__device__ __forceinline__ void fetch_row(const uint16_t *base, int64_t ld, int64_t row, int col,
+                                          int64_t rows, int cols, RowFetch &f) {
+    f.at = base + row * ld + col;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(f.at);
+    const uintptr_t first = a & ~uintptr_t{15}, last = a + 2 * min(64, cols - col);
+    f.whole = row < rows && col < cols && first >= reinterpret_cast<uintptr_t>(base) &&
+              ((last + 15) & ~uintptr_t{15}) <=
+                  reinterpret_cast<uintptr_t>(base + (rows - 1) * ld + cols);
+    if (f.whole) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint4 q = *reinterpret_cast<const uint4 *>(p + 8 * j);
-            u[4 * j] = q.x;
-            u[4 * j + 1] = q.y;
-            u[4 * j + 2] = q.z;
-            u[4 * j + 3] = q.w;
-        }
-    } else if (staged) {
-        const int nr = static_cast<int>(min(int64_t{32}, rows - row0));
-        uint16_t *s16 = reinterpret_cast<uint16_t *>(buf);
-        const uint16_t *q = base + row0 * ld + col + lane;
-        buffer_free(lane);
-        if (col + lane < cols) {
-#pragma unroll 8
-            for (int r = 0; r < nr; ++r) s16[r * 34 + lane] = q[r * ld];
-        }
-        __syncwarp();
+        for (int i = 0; i < 9; ++i)
+            if (first + 16 * i < last) f.q[i] = *reinterpret_cast<const uint4 *>(first + 16 * i);
+    }
+}
+// The columns' 32 words, moved to the front.
+__device__ __forceinline__ void align_row(const RowFetch &f, uint32_t (&u)[32]) {
+    const uint32_t s = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(f.at));
+    uint32_t w[36];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) u[j] = buf[lane * 17 + j];
-    } else {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (row_ok && col + j < cols) v[j] += act::from16(p[j], f16);
-        return;
+    for (int i = 0; i < 9; ++i) {
+        w[4 * i] = f.q[i].x;
+        w[4 * i + 1] = f.q[i].y;
+        w[4 * i + 2] = f.q[i].z;
+        w[4 * i + 3] = f.q[i].w;
     }
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        float a, b;
-        act::unpack16x2(u[j], a, b, f16);
-        v[2 * j] += a;
-        v[2 * j + 1] += b;
-    }
+    for (int i = 0; i < 34; ++i) w[i] = s & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 33; ++i) w[i] = s & 4 ? w[i + 1] : w[i];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) u[i] = __funnelshift_r(w[i], w[i + 1], (s & 2) * 8);
 }
 // 32 fp32 columns from `col` (boxes of 32 columns x 32 rows): stored, or added.
 __device__ __forceinline__ void put_f32(const CUtensorMap *map, int64_t row0, int col,

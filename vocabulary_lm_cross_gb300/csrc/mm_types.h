@@ -30,7 +30,7 @@ struct Epi {
     const float *xs, *ws;
     int act, f16;
     // vec_of() of the tensors
-    int y_vec, preact_vec, preact_up_vec, residual_vec;
+    int y_vec, preact_vec, preact_up_vec;
 };
 
 // One forward product: x [T, K], weight [N, K] (gated: [2N, K]).
