@@ -314,3 +314,51 @@ def test_workspace_may_be_missing_where_dy_is_read_as_it_is():
     assert call(capi.ACT_NONE, db.data_ptr(), None) == capi.ERR_WORKSPACE_TOO_SMALL
     assert call(capi.ACT_SILU, None, None) == capi.ERR_WORKSPACE_TOO_SMALL
     assert call(capi.ACT_NONE, None, full[:256]) == capi.ERR_WORKSPACE_TOO_SMALL
+
+
+def placed(t, pad, offset):
+    """t's rows `pad` elements apart from `offset` elements on, NaN around them."""
+    rows, cols = t.shape
+    store = torch.full((offset + rows * (cols + pad) + 8,), float("nan"), dtype=t.dtype,
+                       device=t.device)
+    v_ = store.as_strided((rows, cols), (cols + pad, 1), offset)
+    v_.copy_(t)
+    return v_
+
+
+# columns around a thread's 8 and a block's 256; (pad, offset) of dy and of preact
+@pytest.mark.parametrize("N", [1, 2, 5, 7, 8, 9, 12, 255, 256, 257, 263, 511, 1031])
+@pytest.mark.parametrize("T,places", [(1, ((0, 1), (0, 0))), (9, ((0, 0), (0, 3))), (70, ((1, 2), (2, 5))),
+                                      (300, ((3, 7), (0, 0)))])
+def test_gradients_of_rows_at_any_alignment(T, N, places):
+    K = 40
+    for gated, kind in ((False, "none"), (False, "gelu"), (True, "silu")):
+        g, x, w = linear_case(T, K, N, "bf16", T + N, gated)
+        pre = None if kind == "none" else placed(randn(g, (T, 2 * N if gated else N), DT["bf16"]),
+                                                 *places[1])
+        dy = placed(randn(g, (T, N), DT["bf16"], 0.5), *places[0])
+        z64 = None if pre is None else f64(pre)
+        if gated:
+            grads = v.glu_bwd(dy, x, w, pre, act=kind, dweight_dtype=torch.float32)
+            dz = ol.glu_dz(f64(dy), z64, kind)
+            scale = np.concatenate([np.abs(f64(dy) * z64[:, N:]), np.abs(f64(dy))], axis=1)
+        else:
+            grads = v.linear_bwd(dy, x, w, pre, act=kind, bias_grad=True, dweight_dtype=torch.float32)
+            dz = f64(dy) if kind == "none" else ol.linear_dz(f64(dy), z64, kind)
+            scale = np.abs(f64(dy))
+        check_grads(grads, dz, f64(x), f64(w), "bf16", kind, scale)
+
+
+@pytest.mark.parametrize("N,pad,offset", [(1031, 0, 0), (1032, 1, 3), (1033, 3, 7), (1030, 2, 2), (1029, 0, 5),
+                                          (257, 6, 1), (65, 0, 1)])
+def test_residual_at_any_alignment(N, pad, offset):
+    T, K = 2100, 72
+    g, x, w = linear_case(T, K, N, "bf16", N)
+    b, r = randn(g, (N,), DT["bf16"]), placed(randn(g, (T, N), DT["bf16"]), pad, offset)
+    y, z = ol.linear(f64(x), f64(w), f64(b), f64(r), "silu")
+    e = fp32_bound(f64(x), f64(w), K) + E23 * np.abs(z)
+    bound = 1.2 * e + 3e-6 * (1 + np.abs(z)) + E23 * np.abs(y)
+    for out in (torch.empty_like(y_ := torch.empty((T, N), dtype=DT["bf16"], device="cuda")),
+                placed(y_, pad, offset), placed(y_, -N % 8, 0), r):
+        res = v.linear_fwd(x, w, b, r, act="silu", out=out)
+        close(res.y, y, "bf16", bound, "y")

@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(32 * kDzWarps) dz_kernel(const DzParams p) {
             float d[R][V], g[R][V], u[R][V];
 #pragma unroll
             for (int q = 0; q < R; ++q) {  // (past the end: the last row again)
-                const int64_t r = min(first + q * kDzWarps, r1 - 1);
+                const int64_t r = R == 1 ? first : min(first + q * kDzWarps, r1 - 1);
                 load_v<V>(p.dy + r * p.dy_ld + col, d[q], f16);
                 if constexpr (ACT != VLMCE_ACT_NONE)
                     load_v<V>(p.pre + r * p.pre_ld + col, g[q], f16);
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(32 * kDzWarps) dz_kernel(const DzParams p) {
 #pragma unroll
             for (int q = 0; q < R; ++q) {
                 const int64_t r = first + q * kDzWarps;
-                if (r >= r1) break;
+                if (R > 1 && r >= r1) break;
                 if constexpr (ACT != VLMCE_ACT_NONE) {
 #pragma unroll
                     for (int j = 0; j < V; ++j) {
