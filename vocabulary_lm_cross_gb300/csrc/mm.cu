@@ -144,6 +144,7 @@ cudaError_t setup(Capacity *out) {
 // with K split over `split` CTAs.
 struct Plan {
     bool large;
+    int narrow;     // large: tiles of 128 weight rows
     int bn, split, stages, per_stage, tmem_cols, smem;
     int part_offset;  // SmallParams
     double clocks;  // estimate
@@ -156,11 +157,14 @@ struct Plan {
 // larger of its MMAs (128 x bn: bn / 2 clocks each at the tensor cores' rate,
 // or the shared-memory reads of both operands) and its way from L2, shared by
 // the CTAs of an SM; it is free again a fetch latency, a transfer and its MMAs
-// later.  The weight comes from HBM at 6.8 TB/s at best.
+// later.  The weight comes from HBM at 6.8 TB/s at best.  A narrow pair tile's chunk
+// costs 3/4 of a wide one's for half the products, so narrow tiles are for few of them
+// (us, narrow and wide: T 512, K 4096, N 4096 bf16 20.9 and 24.2; T 256, K 8192, N 8192
+// 36.0 and 44.2; T 1024, K 4096, N 4096 36.0 and 25.1).
 constexpr double kHbmBytesPerClock = 3570., kL2BytesPerClock = 76.;
 constexpr double kFetch = 900., kPerStage = 260., kPerCta = 6900., kSplitSync = 1300.;
 constexpr double kOut = 25., kOutSplit = 40.;   // epilogue, per token of an accumulator
-constexpr double kPairChunk = 640., kPairCta = 7900.;
+constexpr double kPairChunk = 640., kNarrowChunk = 480., kPairCta = 7900.;
 
 double hbm_clocks(const Fwd &f) {
     return static_cast<double>(f.N) * (f.gated ? 2 : 1) * f.K *
@@ -208,12 +212,18 @@ bool small_plan(const Fwd &f, const Capacity &cap, int64_t ty, int split, int pe
 
 Plan choose(const Fwd &f, const Capacity &cap) {
     Plan best = {};
-    best.large = true;
-    const int64_t tiles =
-        ((f.T + 255) / 256) * (f.gated ? (f.N + 127) / 128 : (f.N + 255) / 256);
-    const double main =
-        static_cast<double>((tiles + cap.pairs - 1) / cap.pairs) * chunks_of(f) * kPairChunk;
-    best.clocks = std::hypot(main, 0.6 * hbm_clocks(f)) + kPairCta;
+    for (int narrow = 0; narrow < 2; ++narrow) {
+        const int64_t width = (f.gated ? 128 : 256) >> narrow;
+        const int64_t tiles = ((f.T + 255) / 256) * ((f.N + width - 1) / width);
+        const double main = static_cast<double>((tiles + cap.pairs - 1) / cap.pairs) *
+                            chunks_of(f) * (narrow ? kNarrowChunk : kPairChunk);
+        const double clocks = std::hypot(main, 0.6 * hbm_clocks(f)) + kPairCta;
+        if (narrow == 0 || clocks < best.clocks) {
+            best.large = true;
+            best.narrow = narrow;
+            best.clocks = clocks;
+        }
+    }
     const int64_t t0 = (f.T + 255) / 256;
     if (t0 > 16) return best;  // enough tokens for the pair tiles
     for (int64_t ty = t0; ty < t0 + 5; ++ty)
@@ -263,12 +273,12 @@ unsigned pair_grid(int64_t tiles, int chunks, const Capacity &cap, int *dealt) {
     return static_cast<unsigned>(2 * (*dealt > 0 ? std::min<int64_t>(tiles, cap.pairs) : tiles));
 }
 
-cudaError_t forward_large(const Fwd &f, const Capacity &cap, cudaStream_t s) {
+cudaError_t forward_large(const Fwd &f, const Capacity &cap, int narrow, cudaStream_t s) {
     LargeMaps maps = {};
     const int64_t rows = f.gated ? 2 * f.N : f.N;
     const Epi &e = f.e;
     bool ok = operand_map(&maps.x, f.x, f.dtype, f.T, f.K, f.x_ld, kHalfRows) &&
-              operand_map(&maps.w, f.w, f.dtype, rows, f.K, f.w_ld, kHalfRows);
+              operand_map(&maps.w, f.w, f.dtype, rows, f.K, f.w_ld, kHalfRows >> narrow);
     if (e.y_vec >= 16) ok = ok && output_map(&maps.y, e.y, false, f.T, f.N, e.y_ld);
     if (e.preact && e.preact_vec >= 16)
         ok = ok && output_map(&maps.z, e.preact, false, f.T, f.N, e.preact_ld);
@@ -281,7 +291,9 @@ cudaError_t forward_large(const Fwd &f, const Capacity &cap, cudaStream_t s) {
     p.up_row = static_cast<int>(f.N);
     p.chunks = chunks_of(f);
     p.mt = static_cast<int>((f.T + kPairM - 1) / kPairM);
-    p.nt = static_cast<int>(f.gated ? (f.N + 127) / 128 : (f.N + 255) / 256);
+    p.narrow = narrow;
+    const int64_t width = (f.gated ? 128 : 256) >> narrow;
+    p.nt = static_cast<int>((f.N + width - 1) / width);
     const int64_t tiles = static_cast<int64_t>(p.mt) * p.nt;
     if (tiles * kGroupM > INT32_MAX) return cudaErrorInvalidConfiguration;
     const unsigned grid = pair_grid(tiles, p.chunks, cap, &p.dealt);
@@ -351,7 +363,7 @@ cudaError_t forward(const Fwd &f, cudaStream_t s) {
     const cudaError_t e = setup(&cap);
     if (e != cudaSuccess) return e;
     const Plan plan = plan_of(f, cap);
-    return plan.large ? forward_large(f, cap, s) : forward_small(f, plan, s);
+    return plan.large ? forward_large(f, cap, plan.narrow, s) : forward_small(f, plan, s);
 }
 
 namespace {

@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 const CUtensorMap *m = warp == 0 ? &maps.a[tl.p] : &maps.b[tl.p];
                 const int row =
                     (warp == 0 ? tl.m0 : tl.n0) + kHalfRows * static_cast<int>(q.rank);
-                const uint32_t base = q.ring + (warp == 0 ? 0 : kOpBytes);
+                const uint32_t side = warp == 0 ? 0 : kOpBytes;
                 for (int c = 0; c < chunks; c += kPer) {
                     const int n = min(kPer, chunks - c);
                     if (warp == 0)
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         stage_begin<false, kPer>(q, r, n);
                     const uint32_t fb = full_leader + 8u * r.s;
                     for (int i = 0; i < n; ++i) {
-                        const uint32_t to = base + r.s * q.kStageBytes + i * kChunkBytes;
+                        const uint32_t to = q.chunk(r.s, i) + side;
                         const int k = 64 * (c + i);
                         if (!mn) {
                             tc::tma_load_2d_pair(to, m, k, row, fb);
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                             tc::tma_load_2d_pair(to + 8192, m, row + 64, k, fb);
                         }
                     }
-                    r.next();
+                    r.next(q);
                 }
                 issued += (chunks + kPer - 1) / kPer;
             }

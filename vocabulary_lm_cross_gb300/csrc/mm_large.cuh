@@ -9,6 +9,13 @@
 // to back, where the power cap sets the clock (98-100 % of the library's sustained
 // rate); tensor pipe 86 % busy before two chunks made a stage.  Tile order: groups of kGroupM token tiles, weight tiles outer within a
 // group, so that the ~76 tiles in flight read about 8 token and 9.5 weight tiles.
+// `narrow` tiles have 128 weight rows (gated: 64 + 64), and four stages of the ring.
+//
+// The epilogue asks for what it reads from memory (scales, bias, residual) before it
+// waits for a tile's accumulators, the residual's next 64 columns while it works on the
+// present ones: behind the ring's copies an answer takes thousands of clocks (T 8192,
+// K 2048, N 2048 bf16 with bias, preact and residual 60.5 us, asked for where used 89;
+// N 2049 88.6 and 260).
 #pragma once
 
 #include <cuda.h>
@@ -26,6 +33,7 @@ struct LargeParams {
     int up_row;        // gated: first up row of the weight
     int chunks;        // K in 128-byte chunks
     int mt, nt;
+    int narrow;        // tiles of 128 weight rows instead of 256
     int dealt;
     Epi e;
     int *err;
@@ -40,7 +48,7 @@ __device__ __forceinline__ LargeTile large_tile(const LargeParams &p, int t) {
     const int g = t / per_group, r = t - g * per_group;
     const int gm = min(kGroupM, p.mt - g * kGroupM);
     const int n = r / gm;
-    return {(g * kGroupM + (r - n * gm)) * kPairM, n * (GATED ? 128 : 256)};
+    return {(g * kGroupM + (r - n * gm)) * kPairM, n * ((GATED ? 128 : 256) >> p.narrow)};
 }
 
 struct LargeMaps {
@@ -77,7 +85,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         tc::prefetch_tensormap(&maps.x);
         tc::prefetch_tensormap(&maps.w);
     }
-    const Pair<kPer> q = pair_setup<kPer>(smem_raw, p.err, p.dealt);
+    const Pair<kPer> q = pair_setup<kPer>(smem_raw, p.err, p.dealt,
+                                          kOpBytes + (kOpBytes >> p.narrow));
     Tiles tiles;
     const int rank = static_cast<int>(q.rank);
 
@@ -95,21 +104,21 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         const int n = min(kPer, p.chunks - c);
                         stage_begin<true, kPer>(q, r, n);
                         for (int i = 0; i < n; ++i)
-                            tc::tma_load_2d_pair(q.ring + r.s * q.kStageBytes + i * kChunkBytes, &maps.x,
+                            tc::tma_load_2d_pair(q.chunk(r.s, i), &maps.x,
                                                  (c + i) * kElts, ar, full_leader + 8u * r.s);
-                        r.next();
+                        r.next(q);
                     }
                 } else {
                     const int br = GATED ? (rank == 0 ? tl.n0 : p.up_row + tl.n0)
-                                         : tl.n0 + kHalfRows * rank;
+                                         : tl.n0 + (kHalfRows >> p.narrow) * rank;
                     for (int c = 0; c < p.chunks; c += kPer) {
                         const int n = min(kPer, p.chunks - c);
                         stage_begin<false, kPer>(q, r, n);
                         for (int i = 0; i < n; ++i)
                             tc::tma_load_2d_pair(
-                                q.ring + r.s * q.kStageBytes + i * kChunkBytes + kOpBytes, &maps.w,
+                                q.chunk(r.s, i) + kOpBytes, &maps.w,
                                 (c + i) * kElts, br, full_leader + 8u * r.s);
-                        r.next();
+                        r.next(q);
                     }
                 }
                 issued += (p.chunks + kPer - 1) / kPer;
@@ -118,7 +127,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
     } else if (warp == 1) {
         if (rank == 0 && lane == 0) {
-            const uint32_t idesc = tc::idesc_bf16_f32(256, 256, false, false, FP8 || p.e.f16);
+            const uint32_t idesc = tc::idesc_bf16_f32(256, 256 >> p.narrow, false, false,
+                                                     FP8 || p.e.f16);
             Ring<kPer> r;
             int it = 0;
             for (; tiles.next(q, lane) >= 0; ++it)
@@ -141,9 +151,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const LargeTile tl = large_tile<GATED>(p, t);
             const int64_t row0 = tl.m0 + kHalfRows * rank + (warp & 3) * 32;
             // 64 columns at a time: one group of a gated tile's 128 outputs per
-            // half, two of a linear tile's 256
-            constexpr int kGroups = GATED ? 1 : 2;
-            const int col0 = tl.n0 + 64 * kGroups * half;
+            // half of the warps, two of a linear tile's 256; of a narrow tile one of
+            // 128, and a gated one's 64 outputs are one half's, in turn
+            const bool idle = GATED && p.narrow && (it & 1) != half;
+            const int groups = GATED || p.narrow ? 1 : 2;
+            const int part = GATED && p.narrow ? 0 : 64 * groups * half;
+            const int col0 = tl.n0 + part;
             // what the outputs take from memory comes while the tile's sums do
             const float xs = e.xs && row0 + lane < p.T ? e.xs[row0 + lane] : 1.f;
             float ws[4], bias[4];  // of columns col0 + 32 i + lane (gated: two of gate, two of up)
@@ -157,17 +170,17 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             RowFetch next;
             if constexpr (ADD)
                 fetch_row(e.residual, e.residual_ld, row0 + lane, col0, p.T, p.N, next);
-            const uint32_t acc = acc_wait(q, it, warp) + 64 * kGroups * half;
+            const uint32_t acc = acc_wait(q, it, warp) + part;
 #pragma unroll 1
-            for (int g = 0; g < kGroups; ++g) {
+            for (int g = 0; g < groups; ++g) {
                 const int col = col0 + 64 * g;
-                if (col >= p.N || row0 >= p.T) break;
+                if (col >= p.N || row0 >= p.T || idle) break;
                 uint32_t add[32];
                 bool whole = false;
                 if constexpr (ADD) {
                     whole = next.whole;
                     align_row(next, add);
-                    if (g + 1 < kGroups)
+                    if (g + 1 < groups)
                         fetch_row(e.residual, e.residual_ld, row0 + lane, col + 64, p.T, p.N, next);
                 }
                 auto z_seg = [&](int h, float (&v)[32]) {
@@ -175,7 +188,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                             !GATED && e.bias, h ? bias[1] : bias[0], v);
                 };
                 auto up_seg = [&](int h, float (&v)[32]) {
-                    acc_seg(acc + 128 + 32 * h, FP8, xs, h ? ws[3] : ws[2], false, 0.f, v);
+                    acc_seg(acc + (128 >> p.narrow) + 32 * h, FP8, xs, h ? ws[3] : ws[2], false, 0.f, v);
                 };
                 if (e.preact) {
 #pragma unroll 1

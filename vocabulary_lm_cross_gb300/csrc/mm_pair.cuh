@@ -58,8 +58,6 @@ constexpr int kPairSmem = 1024 + kRingBytes + kEpiWarps * kOutBytes + kPairTail;
 // where an operand is MN-major (its gradient products 2158 against 2166 us).
 template <int PER>
 struct Pair {
-    static constexpr int kStages = kRingChunks / PER;
-    static constexpr int kStageBytes = PER * kChunkBytes;
     unsigned char *smem;  // ring, output buffers, tail
     uint32_t ring, bar0;
     volatile int *abort;
@@ -67,17 +65,22 @@ struct Pair {
     uint32_t rank;        // 0: the pair's leader
     uint32_t tmem;
     int dealt;            // > 0: so many tiles are dealt out to the clusters in turn
+    int chunk_bytes;      // both operands' part of a chunk
+    int stages;           // of the ring
 
     __device__ __forceinline__ uint32_t full(int s) const { return bar0 + 8u * s; }
-    __device__ __forceinline__ uint32_t empty(int s) const { return bar0 + 8u * (kStages + s); }
-    __device__ __forceinline__ uint32_t tfull(int b) const { return bar0 + 8u * (2 * kStages + b); }
+    __device__ __forceinline__ uint32_t empty(int s) const { return bar0 + 8u * (kRingChunks + s); }
+    __device__ __forceinline__ uint32_t tfull(int b) const { return bar0 + 8u * (2 * kRingChunks + b); }
     __device__ __forceinline__ uint32_t tempty(int b) const {
-        return bar0 + 8u * (2 * kStages + 2 + b);
+        return bar0 + 8u * (2 * kRingChunks + 2 + b);
     }
-    __device__ __forceinline__ uint32_t drain() const { return bar0 + 8u * (2 * kStages + 4); }
-    __device__ __forceinline__ uint32_t qfull(int i) const { return bar0 + 8u * (2 * kStages + 5 + i); }
+    __device__ __forceinline__ uint32_t drain() const { return bar0 + 8u * (2 * kRingChunks + 4); }
+    __device__ __forceinline__ uint32_t qfull(int i) const { return bar0 + 8u * (2 * kRingChunks + 5 + i); }
     __device__ __forceinline__ uint32_t qempty(int i) const {
-        return bar0 + 8u * (2 * kStages + 5 + kTileQ + i);
+        return bar0 + 8u * (2 * kRingChunks + 5 + kTileQ + i);
+    }
+    __device__ __forceinline__ uint32_t chunk(int s, int i) const {
+        return ring + (s * PER + i) * chunk_bytes;
     }
     __device__ __forceinline__ uint32_t answer(int i) const {
         return ring + kRingBytes + kEpiWarps * kOutBytes + 16u * i;
@@ -92,8 +95,8 @@ template <int PER>
 struct Ring {
     int s = 0;
     uint32_t ph = 0;
-    __device__ __forceinline__ void next() {
-        if (++s == kRingChunks / PER) {
+    __device__ __forceinline__ void next(const Pair<PER> &q) {
+        if (++s == q.stages) {
             s = 0;
             ph ^= 1;
         }
@@ -104,10 +107,12 @@ struct Ring {
 // held), and this one waits for its predecessor's results before it touches
 // global memory.
 template <int PER>
-__device__ __forceinline__ Pair<PER> pair_setup(unsigned char *smem_raw, int *err,
-                                                      int dealt) {
+__device__ __forceinline__ Pair<PER> pair_setup(unsigned char *smem_raw, int *err, int dealt,
+                                                int chunk_bytes = kChunkBytes) {
     Pair<PER> q;
     q.dealt = dealt;
+    q.chunk_bytes = chunk_bytes;
+    q.stages = min(kRingChunks, kRingBytes / chunk_bytes / PER);
     q.smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     uint64_t *bars =
@@ -119,7 +124,7 @@ __device__ __forceinline__ Pair<PER> pair_setup(unsigned char *smem_raw, int *er
     q.err = err;
     q.rank = ptx::cluster_ctarank();
     if (threadIdx.x == 0) {
-        for (int s = 0; s < q.kStages; ++s) {
+        for (int s = 0; s < q.stages; ++s) {
             ptx::mbar_init(q.full(s), 1);   // leader: its producer + the bytes of both CTAs
             ptx::mbar_init(q.empty(s), 1);  // one commit from the leader's MMA issuer
         }
@@ -213,18 +218,17 @@ template <bool A, int PER>
 __device__ __forceinline__ void stage_begin(const Pair<PER> &q, const Ring<PER> &r, int n) {
     wait_bar(q.empty(r.s), r.ph ^ 1, q.abort, q.err);
     if (A && q.rank == 0)
-        ptx::mbar_arrive_expect_tx(q.full(r.s), static_cast<uint32_t>(n * 2 * kChunkBytes));
+        ptx::mbar_arrive_expect_tx(q.full(r.s), static_cast<uint32_t>(n * 2 * q.chunk_bytes));
 }
 // Operand A's lane of the leader, at the end: every copy into the pair has landed
-// once the full phases of the last kStages loads completed.
+// once the full phases of the last `stages` loads completed.
 template <int PER>
 __device__ __forceinline__ void drain_loads(const Pair<PER> &q, int64_t issued) {
-    constexpr int kStages = Pair<PER>::kStages;
     if (q.rank != 0) return;
-    for (int i = 0; i < kStages && i < issued; ++i) {
+    for (int i = 0; i < q.stages && i < issued; ++i) {
         const int64_t k = issued - 1 - i;
-        drain_bar(q.full(static_cast<int>(k % kStages)), static_cast<uint32_t>((k / kStages) & 1),
-                  q.err);
+        drain_bar(q.full(static_cast<int>(k % q.stages)),
+                  static_cast<uint32_t>((k / q.stages) & 1), q.err);
     }
 }
 // MMA lane of the leader: the products of the it-th tile.
@@ -242,7 +246,7 @@ __device__ __forceinline__ void mma_tile(const Pair<PER> &q, Ring<PER> &r, int i
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             if (i < n) {
-                const uint32_t sa = q.ring + r.s * q.kStageBytes + i * kChunkBytes;
+                const uint32_t sa = q.chunk(r.s, i);
                 const uint32_t sb = sa + kOpBytes;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -258,7 +262,7 @@ __device__ __forceinline__ void mma_tile(const Pair<PER> &q, Ring<PER> &r, int i
             }
         }
         tc::mma_commit_pair(q.empty(r.s), 3u);  // the stage is free in both CTAs
-        r.next();
+        r.next(q);
     }
     tc::mma_commit_pair(q.tfull(b), 3u);
 }
