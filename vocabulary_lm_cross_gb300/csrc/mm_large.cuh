@@ -4,11 +4,12 @@
 // A tile is 256 tokens x 256 weight rows (mm_pair.cuh).  A gated layer's tile
 // takes 128 gate rows (staged by the pair's leader) and the 128 up rows of the
 // same outputs (staged by its peer), so gate and up of an output meet in one
-// thread.  Tensor-bound: T = 4096, K = 6656, 2n = 32768 bf16 911-925 us in a burst
-// (1.93-1.96 PFLOP/s, above the measured burst rate of the library), 1043-1062 us back
-// to back, where the power cap sets the clock (98-100 % of the library's sustained
-// rate); tensor pipe 86 % busy before two chunks made a stage.  Tile order: groups of kGroupM token tiles, weight tiles outer within a
-// group, so that the ~76 tiles in flight read about 8 token and 9.5 weight tiles.
+// thread.  Tensor-bound: T = 4096, K = 6656, 2n = 32768 bf16 909-925 us in a burst
+// (1.93-1.97 PFLOP/s, above the measured burst rate of the library), 1020-1086 us back to
+// back, where the power cap sets the clock (96-102 % of the library's sustained rate);
+// tensor pipe 86 % busy before two chunks made a stage.  Tile order: groups of kGroupM
+// token tiles, weight tiles outer within a group, so that the ~76 tiles in flight read
+// about 8 token and 9.5 weight tiles.
 // `narrow` tiles have 128 weight rows (gated: 64 + 64), and four stages of the ring.
 //
 // The epilogue asks for what it reads from memory (scales, bias, residual) before it
