@@ -320,7 +320,10 @@ vlmce_status swiglu_bwd(const void *x, int64_t x_stride, const void *dy, int64_t
  * rstd            [T] fp32, or NULL.
  * scale           [T] fp32 with VLMCE_E4M3, else NULL.
  * No other two buffers may overlap.  Every pointer is aligned to its element;
- * 16-byte accesses are used when H, the strides and the bases allow it.
+ * 16-byte accesses are used when H, the strides and the bases allow it, and for
+ * many rows at any alignment when the bases are 16-byte aligned and the strides
+ * leave the same remainder (a row's first access then also reads, and ignores,
+ * the end of the memory between it and the row before).
  */
 vlmce_status rmsnorm_fwd(const void *x, int64_t x_stride, const void *residual,
                          int64_t residual_stride, const void *weight, int32_t weight_dtype,
