@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const uint32_t full_leader = ptx::mapa(q.full(0), 0);
             Ring<kPer> r;
             int64_t issued = 0;
-            for (int t; (t = tiles.next(q, lane)) >= 0;) {
+            for (int t; (t = tiles.next<false>(q, lane)) >= 0;) {
                 const GradTile tl = grad_tile(a, t);
                 const int chunks = a.p[tl.p].chunks;
                 const bool mn = warp == 0 ? a.p[tl.p].a_mn != 0 : a.p[tl.p].b_mn != 0;
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         if (q.rank == 0 && lane == 0) {
             Ring<kPer> r;
             int it = 0;
-            for (int t; (t = tiles.next(q, lane)) >= 0; ++it) {
+            for (int t; (t = tiles.next<false>(q, lane)) >= 0; ++it) {
                 const GradProblem &P = a.p[grad_tile(a, t).p];
                 mma_tile<false, kPer>(q, r, it, P.chunks,
                                 tc::idesc_bf16_f32(256, 256, P.a_mn != 0, P.b_mn != 0, a.f16 != 0),
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         uint32_t *buf = q.out_buffer(warp - 2);
         const uint32_t tempty_leader = ptx::mapa(q.tempty(0), 0);
         int it = 0;
-        for (int t; (t = tiles.next(q, lane)) >= 0; ++it) {
+        for (int t; (t = tiles.next<true>(q, lane)) >= 0; ++it) {
             const GradTile tl = grad_tile(a, t);
             const GradProblem &P = a.p[tl.p];
             const CUtensorMap *map = &maps.c[tl.p];

@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const uint32_t full_leader = ptx::mapa(q.full(0), 0);
             Ring<kPer> r;
             int64_t issued = 0;
-            for (int t; (t = tiles.next(q, lane)) >= 0;) {
+            for (int t; (t = tiles.next<false>(q, lane)) >= 0;) {
                 const LargeTile tl = large_tile<GATED>(p, t);
                 if (warp == 0) {
                     const int ar = tl.m0 + kHalfRows * rank;
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                                                      FP8 || p.e.f16);
             Ring<kPer> r;
             int it = 0;
-            for (; tiles.next(q, lane) >= 0; ++it)
+            for (; tiles.next<false>(q, lane) >= 0; ++it)
                 mma_tile<FP8, kPer>(q, r, it, p.chunks, idesc, false, false);
             mma_finish(q);
         }
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const Out z = {e.preact, e.preact_ld, e.preact_vec, &maps.z};
         const Out z_up = {e.preact + p.N, e.preact_ld, e.preact_up_vec, &maps.z_up};
         int it = 0;
-        for (int t; (t = tiles.next(q, lane)) >= 0; ++it) {
+        for (int t; (t = tiles.next<true>(q, lane)) >= 0; ++it) {
             const LargeTile tl = large_tile<GATED>(p, t);
             const int64_t row0 = tl.m0 + kHalfRows * rank + (warp & 3) * 32;
             // 64 columns at a time: one group of a gated tile's 128 outputs per

@@ -153,10 +153,12 @@ __device__ __forceinline__ Pair<PER> pair_setup(unsigned char *smem_raw, int *er
     return q;
 }
 // The sequence of tiles of a pair, one object per role; -1 after the last (or after a
-// wait that gave up).  All active lanes of a warp call next().
+// wait that gave up).  A role is one lane, or (WARP) a whole warp: its lane 0 reads the
+// answer for all 32, so no lane is behind when it gives the slot back, and all lanes
+// get the same tile.
 struct Tiles {
     int j = -1;
-    template <int PER>
+    template <bool WARP, int PER>
     __device__ __forceinline__ int next(const Pair<PER> &q, int lane) {
         const int own = static_cast<int>(ptx::cluster_id_x());
         if (++j == 0) return own;
@@ -164,21 +166,20 @@ struct Tiles {
             const int64_t t = own + static_cast<int64_t>(j) * ptx::ncluster_x();
             return t < q.dealt ? static_cast<int>(t) : -1;
         }
-        const int i = (j - 1) % kTileQ;
         int t = -1;
-        if (wait_bar<true>(q.qfull(i), ((j - 1) / kTileQ) & 1, q.abort, q.err)) {
-            t = ptx::clc_first_cta(q.answer(i));
-            if (t >= 0) t >>= 1;  // two CTAs per tile
-        }
-        ptx::fence_proxy_async_smem();  // the answer is read before it is overwritten
-        __syncwarp(__activemask());
-        if (lane == 0) {
+        if (!WARP || lane == 0) {
+            const int i = (j - 1) % kTileQ;
+            if (wait_bar<true>(q.qfull(i), ((j - 1) / kTileQ) & 1, q.abort, q.err)) {
+                t = ptx::clc_first_cta(q.answer(i));
+                if (t >= 0) t >>= 1;  // two CTAs per tile
+            }
+            ptx::fence_proxy_async_smem();  // the answer is read before it is overwritten
             if (q.rank == 0)
                 ptx::mbar_arrive(q.qempty(i));
             else
                 ptx::mbar_remote_arrive_release(ptx::mapa(q.qempty(i), 0));
         }
-        return t;
+        return WARP ? __shfl_sync(0xffffffffu, t, 0) : t;
     }
 };
 // The leader's fetching lane.
@@ -276,6 +277,7 @@ __device__ __forceinline__ void mma_finish(const Pair<PER> &q) {
 template <int PER>
 __device__ __forceinline__ uint32_t acc_wait(const Pair<PER> &q, int it, int warp) {
     wait_bar(q.tfull(it & 1), (it >> 1) & 1, q.abort, q.err);
+    __syncwarp();  // each lane left the wait by itself; TMEM loads take the whole warp
     tc::fence_after_sync();
     return q.tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + (it & 1) * 256;
 }

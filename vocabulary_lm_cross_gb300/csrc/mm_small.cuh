@@ -322,6 +322,7 @@ __global__ void __launch_bounds__(kSmallBound, 2)
             }
         }
         wait_bar(done, 0, abort, p.err);
+        __syncwarp();  // each lane left the wait by itself; what follows takes the whole warp
         tc::fence_after_sync();
         asm volatile("bar.sync 1, 256;" ::: "memory");  // xs_s is complete
     }
