@@ -12,7 +12,7 @@ def source(name):
         return f.read()
 
 
-@pytest.mark.parametrize("name", ["mm_pair.cuh", "mm_large.cuh", "mm_grad.cuh", "mm_small.cuh"])
+@pytest.mark.parametrize("name", ["gemm.cuh", "mm_pair.cuh", "mm_large.cuh", "mm_grad.cuh", "mm_small.cuh"])
 def test_no_warp_waits_only_for_the_lanes_that_happen_to_be_together(name):
     # after a wait loop the lanes of a warp may be apart: a mask of the active ones would
     # let a lane give a slot back that another has yet to read

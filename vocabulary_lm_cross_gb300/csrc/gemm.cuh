@@ -344,18 +344,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mbar_remote_arrive_release(ptx::mapa(qfull(slot), 1));
         return t;
     };
-    auto consume = [&](int j) {  // every other role; all lanes of a warp call it
+    // Every other role calls consume: one lane, or the whole warp, whose lane 0
+    // reads the slot for all 32 (no lane is behind when it is given back, and
+    // all get the same tile).
+    auto consume = [&](int j) {
         const int slot = j % kTileQ;
         int t = -1;
         if (wait_bar<true>(qfull(slot), (j / kTileQ) & 1, abort, a.err)) t = tq[slot];
-        __syncwarp(__activemask());  // every lane has read the slot
-        if (lane == 0) {
-            if (prank == 0)
-                ptx::mbar_arrive(qempty(slot));
-            else
-                ptx::mbar_remote_arrive_release(ptx::mapa(qempty(slot), 0));
-        }
+        if (prank == 0)
+            ptx::mbar_arrive(qempty(slot));
+        else
+            ptx::mbar_remote_arrive_release(ptx::mapa(qempty(slot), 0));
         return t;
+    };
+    auto consume_warp = [&](int j) {
+        int t = -1;
+        if (lane == 0) t = consume(j);
+        return __shfl_sync(0xffffffffu, t, 0);
     };
 
     if (warp == 0) {
@@ -469,12 +474,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int rl = static_cast<int>(prank) * kHalf + q * 32 + lane;
         const uint32_t tempty_leader = ptx::mapa(tempty(0), 0);
         for (int it = 0;; ++it) {
-            const int t = dyn ? consume(it) : static_tile(it);
+            const int t = dyn ? consume_warp(it) : static_tile(it);
             if (t < 0) break;
             const Tile tl = tile_of(a, t);
             const Problem &P = a.p[tl.p];
             const int b = it & 1;
             wait_bar(tfull(b), (it >> 1) & 1, abort, a.err);
+            __syncwarp();  // each lane left the wait by itself; TMEM loads take the whole warp
             tc::fence_after_sync();
             const int row = tl.m0 + rl;
             const bool row_ok = row < P.M;
