@@ -18,6 +18,9 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <mutex>
+#include <set>
+#include <utility>
 
 #include "act.cuh"
 #include "colsum.cuh"
@@ -757,15 +760,34 @@ int64_t max_parts(int64_t T, int64_t H) {
 // CTAs of `threads` threads on one SM, for about 1024 threads.
 int per_sm_of(int threads) { return std::max(1, std::min(8, 1024 / threads)); }
 
+// Dynamic shared memory of the ring kernels with `threads` threads.
+size_t fwd_ring_smem(int ahead, int threads) {
+    return static_cast<size_t>(ahead) * 2 * kOwn * 16 * threads;
+}
+size_t bwd_ring_smem(bool multi, int threads) {
+    return static_cast<size_t>(kBwdAhead * 3 + multi) * kOwn * 16 * threads;
+}
+
+// Opt a kernel in to the most dynamic shared memory it is ever launched with, once
+// per device.  The limit belongs to the function, not to a launch: set to each
+// launch's own size, it could fall below what another thread, or a node of a captured
+// graph, is about to launch with.
+template <class Params>
+cudaError_t opt_in(void (*k)(Params), size_t most, int device) {
+    static std::mutex mu;
+    static std::set<std::pair<int, void (*)(Params)>> done;
+    std::lock_guard<std::mutex> lock(mu);
+    if (done.count({device, k})) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(most));
+    if (e == cudaSuccess) done.insert({device, k});
+    return e;
+}
+
 // All kernels are launched dependent on what precedes them on the stream.
 template <class Params>
 cudaError_t launch(void (*k)(Params), dim3 grid, int threads, size_t smem, cudaStream_t s,
                    const Params &p) {
-    if (smem > 0) {
-        const cudaError_t e = cudaFuncSetAttribute(
-            k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-        if (e != cudaSuccess) return e;
-    }
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1002,9 +1024,11 @@ extern "C" vlmce_status rmsnorm_fwd(const void *x, int64_t x_stride, const void 
         if (ctas > 0 && (shifted ? H > 768 && 2 * T >= ctas : T >= 3 * ctas)) {
             const FwdKernel k = shifted ? fwd_ring_of<true>(dtype, quant, ahead)
                                         : fwd_ring_of<false>(dtype, quant, ahead);
-            return launch_status(launch(k, dim3(static_cast<unsigned>(ctas), 1, 1), rt,
-                                        static_cast<size_t>(ahead) * 2 * kOwn * 16 * rt, st_, p),
-                                 "rmsnorm_fwd");
+            cudaError_t e = opt_in(k, fwd_ring_smem(ahead, kRingThreads), dev.device);
+            if (e == cudaSuccess)
+                e = launch(k, dim3(static_cast<unsigned>(ctas), 1, 1), rt,
+                           fwd_ring_smem(ahead, rt), st_, p);
+            return launch_status(e, "rmsnorm_fwd");
         }
     }
     return launch_status(launch(fwd_kernel_of(dtype, quant, vec, sh.ng),
@@ -1111,9 +1135,12 @@ extern "C" vlmce_status rmsnorm_bwd(const void *dy, int64_t dy_stride, const voi
     if (rt > 0 && ring_ctas > 0 && T >= needed && ring_ctas <= parts_max) {
         parts = ring_ctas;
         const int threads = p.groups * rt;
-        e = launch(bwd_ring_of(dtype, p.groups > 1, shifted),
-                   dim3(static_cast<unsigned>(parts), 1, 1), threads,
-                   static_cast<size_t>(kBwdAhead * 3 + (p.groups > 1)) * kOwn * 16 * threads, s, p);
+        const bool multi = p.groups > 1;
+        const BwdKernel k = bwd_ring_of(dtype, multi, shifted);
+        e = opt_in(k, bwd_ring_smem(multi, kRingThreads), dev.device);
+        if (e == cudaSuccess)
+            e = launch(k, dim3(static_cast<unsigned>(parts), 1, 1), threads,
+                       bwd_ring_smem(multi, threads), s, p);
     } else if (sh.ng > 0 && sh.ng < 16) {
         parts = std::min<int64_t>(parts_max, static_cast<int64_t>(dev.sm_count) *
                                                  std::max(2, per_sm_of(sh.threads)));
