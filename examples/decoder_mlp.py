@@ -98,6 +98,7 @@ def main(T: int = 512, H: int = 256, n: int = 768, V: int = 1000, steps: int = 8
     batch = server.logits(x[:4].clone(), stream[:4].clone())
     single = torch.cat([server.logits(x[i:i + 1].clone(), stream[i:i + 1].clone())
                         for i in range(4)])
+    v.check_device_errors()  # a program checks where it waits for the GPU anyway
     print("top tokens:", batch.argmax(dim=1).tolist(), "labels:", labels[:4].tolist())
     return losses, batch, single
 

@@ -76,8 +76,16 @@ typedef enum {
  * out_reduced[0] is the sum of the losses.  Not accepted by flce_fwd_bwd. */
 typedef enum { VLMCE_NONE = 0, VLMCE_MEAN = 1, VLMCE_SUM = 2 } vlmce_reduction;
 
-/* Bits of out_counts[3]: errors the kernels detected on the device. */
+/* Errors the kernels detected on the device: bits of out_counts[3], of a call's
+ * dev_err, and of vlmce_take_device_errors. */
 #define VLMCE_DEVERR_TIMEOUT 1 /* an on-chip wait gave up; results are invalid */
+
+/* vlmce_take_device_errors -- the VLMCE_DEVERR_* bits left on the current device by
+ * calls without an error word of their own (linear_* and glu_* with dev_err NULL,
+ * vlmce_gemm*) since the last call of this function.  Enqueued on `stream`: *out
+ * (device int32) receives the bits, which are cleared.  Calls on other streams count
+ * once their kernels have run. */
+vlmce_status vlmce_take_device_errors(int32_t *out, vlmce_stream_t stream);
 
 /* Largest vocabulary ce_fwd_bwd accepts, in elements, for the given dtype. */
 int64_t vlmce_ce_max_vocab(int32_t dtype);
@@ -380,8 +388,10 @@ vlmce_status rmsnorm_bwd(const void *dy, int64_t dy_stride, const void *x, int64
  * y               [T, y_stride >= N] of out_dtype.
  * preact          [T, preact_stride >= N] of out_dtype receiving z (what
  *                 linear_bwd needs with an activation), or NULL.
- * dev_err         device int32, or NULL: VLMCE_DEVERR_* bits are OR-ed into it
- *                 (the caller clears it).
+ * dev_err         device int32: VLMCE_DEVERR_* bits are OR-ed into it (the caller
+ *                 clears it); or NULL: into the device's own word, which
+ *                 vlmce_take_device_errors reads.  The call has returned by then, so
+ *                 a program that never reads either takes invalid results for good.
  * T >= 0, N >= 1, K >= 1.  Outputs overlap nothing but what is said above.
  * Deterministic: the same arguments give the same bits.
  */

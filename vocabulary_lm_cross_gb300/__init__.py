@@ -7,6 +7,7 @@ ctypes/PyTorch binding and the seeded synthetic workloads.
 """
 from .ce import (CEResult, ce_fwd_bwd, ce_fwd_bwd_host, describe_plan, host_workspace_bytes,  # noqa: F401
                  max_vocab, workspace_bytes)
+from .errors import check_device_errors, take_device_errors  # noqa: F401
 from .flce import FLCEResult, flce_fwd_bwd  # noqa: F401
 from .linear import (LinearGrads, LinearResult, glu_bwd, glu_fwd, linear_bwd,  # noqa: F401
                      linear_fwd)

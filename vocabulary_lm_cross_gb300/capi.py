@@ -48,6 +48,7 @@ _sz = ctypes.c_size_t
 SIGNATURES = {
     "vlmce_status_string": (ctypes.c_char_p, [_i32]),
     "vlmce_last_error": (ctypes.c_char_p, []),
+    "vlmce_take_device_errors": (_i32, [_vp, _vp]),
     "vlmce_ce_max_vocab": (_i64, [_i32]),
     "vlmce_profile_events": (None, [_vp, _vp]),
     "vlmce_ce_workspace_bytes": (_sz, [_i64, _i64, _i32]),

@@ -34,6 +34,7 @@
 #include <cstring>
 
 #include "ce_common.cuh"
+#include "device_errors.h"
 #include "gemm_launch.h"
 #include "host_util.h"
 #include "ptx.cuh"
@@ -447,9 +448,10 @@ extern "C" vlmce_status vlmce_gemm(const void *A, int32_t a_mn, const void *B, i
     p.b_mn = b_mn != 0;
     p.C = C;
     p.ldc = ldc;
-    g.err = nullptr;  // no device error word: a wait that gives up only ends the kernel
-    return launch_status(gemm::launch_group(maps, g, reinterpret_cast<cudaStream_t>(stream)),
-                         "vlmce_gemm_kernel");
+    cudaError_t e = device_error_word(&g.err);
+    if (e == cudaSuccess)
+        e = gemm::launch_group(maps, g, reinterpret_cast<cudaStream_t>(stream));
+    return launch_status(e, "vlmce_gemm_kernel");
 }
 
 extern "C" vlmce_status vlmce_gemm_bf16(const void *A, int32_t a_mn, const void *B, int32_t b_mn,

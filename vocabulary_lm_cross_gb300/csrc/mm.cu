@@ -7,6 +7,7 @@
 #include <cmath>
 #include <mutex>
 
+#include "device_errors.h"
 #include "gemm_launch.h"
 #include "host_util.h"
 #include "mm_grad.cuh"
@@ -67,10 +68,12 @@ void launch_attributes(cudaLaunchAttribute (&attr)[2], unsigned csize) {
 
 // Per device: the CTA pairs of the large kernels, and the clusters of 1 ..
 // kMaxSplit small CTAs with one (or two) CTAs' shared memory per SM, that fit
-// at once (SMs of a GPC that cannot complete a cluster stay idle).
+// at once (SMs of a GPC that cannot complete a cluster stay idle); and the word that
+// takes the errors of calls without one of their own.
 struct Capacity {
     int pairs = 0;
     int small[2][kMaxSplit];
+    int *errors = nullptr;
 };
 constexpr int kSmSmem = 233472;  // 228 KB
 constexpr int small_budget(int per_sm) { return kSmSmem / per_sm - kSmemReserved; }
@@ -106,6 +109,8 @@ cudaError_t setup(Capacity *out) {
     std::lock_guard<std::mutex> lock(mu);
     if (cached[device].pairs == 0) {
         Capacity c;
+        e = device_error_word(&c.errors);
+        if (e != cudaSuccess) return e;
         for (int k = 0; k < 5; ++k) {
             e = cudaFuncSetAttribute(small_kernel(k & 1, k & 2, k & 4),
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, small_budget(1));
@@ -298,7 +303,7 @@ cudaError_t forward_large(const Fwd &f, const Capacity &cap, int narrow, cudaStr
     if (tiles * kGroupM > INT32_MAX) return cudaErrorInvalidConfiguration;
     const unsigned grid = pair_grid(tiles, p.chunks, cap, &p.dealt);
     p.e = f.e;
-    p.err = f.err;
+    p.err = f.err ? f.err : cap.errors;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     launch_attributes(attr, 2);
@@ -312,7 +317,7 @@ cudaError_t forward_large(const Fwd &f, const Capacity &cap, int narrow, cudaStr
                               static_cast<const LargeParams>(p));
 }
 
-cudaError_t forward_small(const Fwd &f, const Plan &plan, cudaStream_t s) {
+cudaError_t forward_small(const Fwd &f, const Capacity &cap, const Plan &plan, cudaStream_t s) {
     const int kw = f.gated ? 2 : 1;
     SmallParams p = {};
     p.T = static_cast<int>(f.T);
@@ -333,7 +338,7 @@ cudaError_t forward_small(const Fwd &f, const Plan &plan, cudaStream_t s) {
            (p.red_tokens / 4 + p.split - 1) / p.split * 4 * p.split * kw * 512 > ring)
         p.red_tokens -= 16;
     p.e = f.e;
-    p.err = f.err;
+    p.err = f.err ? f.err : cap.errors;
     if (ty > 65535 || mt * p.split > INT32_MAX) return cudaErrorInvalidConfiguration;
 
     CUtensorMap mx, mw;
@@ -363,7 +368,7 @@ cudaError_t forward(const Fwd &f, cudaStream_t s) {
     const cudaError_t e = setup(&cap);
     if (e != cudaSuccess) return e;
     const Plan plan = plan_of(f, cap);
-    return plan.large ? forward_large(f, cap, plan.narrow, s) : forward_small(f, plan, s);
+    return plan.large ? forward_large(f, cap, plan.narrow, s) : forward_small(f, cap, plan, s);
 }
 
 namespace {
@@ -424,7 +429,7 @@ cudaError_t backward(const Bwd &b, cudaStream_t s) {
         f.err = b.err;
         const Plan plan = plan_of(f, cap);
         if (!plan.large && (!b.dw || plan.clocks < joint_clocks(b, cap) - dw_clocks(b, cap))) {
-            const cudaError_t es = forward_small(f, plan, s);
+            const cudaError_t es = forward_small(f, cap, plan, s);
             if (es != cudaSuccess || !b.dw) return es;
             dx = false;
         }
@@ -432,7 +437,7 @@ cudaError_t backward(const Bwd &b, cudaStream_t s) {
     GradMaps maps;
     GradParams p = {};
     p.f16 = b.f16;
-    p.err = b.err;
+    p.err = b.err ? b.err : cap.errors;
     const bool f16 = b.f16 != 0;
     int64_t tiles = 0;
     bool ok = true;

@@ -42,7 +42,7 @@ struct Fwd {
     int w_mn;       // the weight is stored [K, N] (small kernel, 16 bits, not gated)
     int32_t dtype;  // VLMCE_BF16, VLMCE_F16 or VLMCE_E4M3
     Epi e;
-    int *err;
+    int *err;       // null: the device's own word
 };
 
 // Enqueue it (T, N, K >= 1); the kernel is chosen by the sizes.
@@ -60,7 +60,7 @@ struct Bwd {
     int64_t dx_ld;
     void *dw;              // [rows, K] contiguous
     int dw_f32, accumulate;
-    int *err;
+    int *err;              // null: the device's own word
 };
 cudaError_t backward(const Bwd &b, cudaStream_t s);
 

@@ -116,7 +116,8 @@ def linear_fwd(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None 
     bf16 or fp16 operands, or float8_e4m3fn with x_scale [T] and weight_scale
     [N] (fp32).  act: none, silu, gelu, gelu_tanh or relu.  preact: True, or a
     [T, N] tensor, to keep x W^T + bias for linear_bwd.  out may be
-    ``residual`` itself.  dev_err: int32 [1] the kernels OR their error bits into.
+    ``residual`` itself.  dev_err: int32 [1] the kernels OR their error bits into;
+    without it check_device_errors() tells of them.
     """
     return _forward(False, x, weight, bias, residual, act, preact, x_scale, weight_scale,
                     out_dtype, out, dev_err)
