@@ -327,7 +327,8 @@ vlmce_status swiglu_bwd(const void *x, int64_t x_stride, const void *dy, int64_t
  *                 itself (same stride).
  * rstd            [T] fp32, or NULL.
  * scale           [T] fp32 with VLMCE_E4M3, else NULL.
- * No other two buffers may overlap.  Every pointer is aligned to its element;
+ * No other two buffers may overlap (columns side by side in one buffer, at the same
+ * stride, do not).  Every pointer is aligned to its element;
  * 16-byte accesses are used when H, the strides and the bases allow it, and for
  * many rows at any alignment when the bases are 16-byte aligned and the strides
  * leave the same remainder (a row's first access then also reads, and ignores,
@@ -392,7 +393,8 @@ vlmce_status rmsnorm_bwd(const void *dy, int64_t dy_stride, const void *x, int64
  *                 clears it); or NULL: into the device's own word, which
  *                 vlmce_take_device_errors reads.  The call has returned by then, so
  *                 a program that never reads either takes invalid results for good.
- * T >= 0, N >= 1, K >= 1.  Outputs overlap nothing but what is said above.
+ * T >= 0, N >= 1, K >= 1.  Outputs overlap nothing but what is said above
+ * (columns side by side in one buffer, at the same stride, do not overlap).
  * Deterministic: the same arguments give the same bits.
  */
 vlmce_status linear_fwd(const void *x, int64_t x_stride, const float *x_scale, const void *weight,

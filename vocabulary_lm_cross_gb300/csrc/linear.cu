@@ -21,6 +21,7 @@
 #include "colsum.cuh"
 #include "host_util.h"
 #include "mm_types.h"
+#include "rows_host.h"
 #include "vlmce.h"
 
 namespace vlmce {
@@ -175,15 +176,9 @@ struct Buf {
     const void *p;
     int64_t rows, cols, ld;
     int elt;
-    uintptr_t begin() const { return reinterpret_cast<uintptr_t>(p); }
-    uintptr_t end() const {
-        return rows < 1 ? begin()
-                        : begin() + static_cast<uintptr_t>(((rows - 1) * ld + cols) * elt);
-    }
+    RowsOf bytes() const { return {p, rows, cols * elt, ld * elt}; }
 };
-bool overlap(const Buf &a, const Buf &b) {
-    return a.p && b.p && a.begin() < b.end() && b.begin() < a.end();
-}
+bool overlap(const Buf &a, const Buf &b) { return rows_overlap(a.bytes(), b.bytes()); }
 bool same(const Buf &a, const Buf &b) { return a.p == b.p && (a.ld == b.ld || a.rows <= 1); }
 // rows * ld elements are addressable
 bool fits(int64_t rows, int64_t ld, int elt) {

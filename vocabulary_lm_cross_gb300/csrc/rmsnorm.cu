@@ -26,6 +26,7 @@
 #include "colsum.cuh"
 #include "host_util.h"
 #include "ptx_async.cuh"
+#include "rows_host.h"
 #include "vlmce.h"
 
 namespace vlmce {
@@ -926,10 +927,7 @@ vlmce_status check_rows(const void *p, int64_t T, int64_t H, int64_t ld, int elt
 }
 bool overlap(const void *a, int64_t a_ld, int a_elt, const void *b, int64_t b_ld, int b_elt,
              int64_t T, int64_t H) {
-    if (!a || !b || T < 1) return false;
-    const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
-    return pa < pb + static_cast<uintptr_t>(((T - 1) * b_ld + H) * b_elt) &&
-           pb < pa + static_cast<uintptr_t>(((T - 1) * a_ld + H) * a_elt);
+    return rows_overlap({a, T, H * a_elt, a_ld * a_elt}, {b, T, H * b_elt, b_ld * b_elt});
 }
 
 }  // namespace
