@@ -369,6 +369,23 @@ vlmce_status rmsnorm_bwd(const void *dy, int64_t dy_stride, const void *x, int64
                          size_t workspace_bytes, vlmce_stream_t stream);
 
 /*
+ * vlmce_linear_describe_plan -- the kernels that linear_fwd (gated: glu_fwd, N its n)
+ * or, with `backward`, linear_bwd / glu_bwd (dx and dweight) run for these sizes on the
+ * current device:
+ *   out[0]  kernel of the forward product, or of dx: 0 CTA pairs, 1 single CTAs ("small")
+ *   out[1]  its outputs a tile (gated: as many gate and up rows each)
+ *   out[2]  its tokens a tile
+ *   out[3]  CTAs that share a tile's K (1 .. 8)
+ *   out[4]  tiles of the pair kernel's launch (backward: dweight's, and dx's where out[0]
+ *           is 0), or of the small kernel
+ *   out[5]  1: the pair kernel's tiles are dealt out, 0: taken by launch control
+ *   out[6]  small: CTAs that share an SM
+ *   out[7]  small, shared K: rounds of the exchange through the ring (0: memory of its own)
+ */
+vlmce_status vlmce_linear_describe_plan(int32_t gated, int32_t backward, int64_t T, int64_t N,
+                                        int64_t K, int32_t dtype, int32_t *out);
+
+/*
  * linear_fwd -- linear layer with its epilogue in the product:
  *   z = x W^T + bias,  y = act(z) + residual
  * on tcgen05 tensor cores with fp32 accumulators; the epilogue is in fp32 and

@@ -9,6 +9,6 @@ from .ce import (CEResult, ce_fwd_bwd, ce_fwd_bwd_host, describe_plan, host_work
                  max_vocab, workspace_bytes)
 from .errors import check_device_errors, take_device_errors  # noqa: F401
 from .flce import FLCEResult, flce_fwd_bwd  # noqa: F401
-from .linear import (LinearGrads, LinearResult, glu_bwd, glu_fwd, linear_bwd,  # noqa: F401
-                     linear_fwd)
+from .linear import (LinearGrads, LinearPlan, LinearResult, describe_linear_plan,  # noqa: F401
+                     glu_bwd, glu_fwd, linear_bwd, linear_fwd)
 from .rmsnorm import RMSNormGrads, RMSNormResult, rmsnorm_bwd, rmsnorm_fwd  # noqa: F401

@@ -93,6 +93,7 @@ SIGNATURES = {
                            _vp, _i64, _vp, _i32, _vp, _sz, _vp]),
     "linear_fwd": (_i32, [_vp, _i64, _vp, _vp, _i64, _vp, _i32, _vp, _vp, _i64, _i32, _i64, _i64,
                           _i64, _i32, _vp, _i64, _vp, _i64, _vp, _vp]),
+    "vlmce_linear_describe_plan": (_i32, [_i32, _i32, _i64, _i64, _i64, _i32, _vp]),
     "vlmce_linear_bwd_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "vlmce_glu_bwd_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "linear_bwd": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _i64, _i64, _i64, _i32,

@@ -223,6 +223,12 @@ struct FwdArgs {
     cudaStream_t stream;
 };
 
+// the products' tiles are numbered in 32 bits
+bool fwd_sizes_ok(int64_t T, int64_t N, int64_t K) {
+    return T <= kMaxDim && N <= kMaxDim / 2 && K <= kMaxDim &&
+           T / 256 + 1 <= INT32_MAX / 16 / (N / 128 + 1);
+}
+
 vlmce_status forward(const FwdArgs &a, const char *where) {
     const bool fp8 = a.dtype == VLMCE_E4M3;
     if (!fp8 && a.dtype != VLMCE_BF16 && a.dtype != VLMCE_F16) return VLMCE_ERR_UNSUPPORTED_DTYPE;
@@ -231,10 +237,7 @@ vlmce_status forward(const FwdArgs &a, const char *where) {
     const int elt = fp8 ? 1 : 2;
     if (a.T < 0 || a.N < 1 || a.K < 1 || a.K * elt % 16 != 0 || !act_ok(a.act, a.gated))
         return VLMCE_ERR_INVALID_ARG;
-    // the products' tiles are numbered in 32 bits
-    if (a.T > kMaxDim || a.N > kMaxDim / 2 || a.K > kMaxDim ||
-        a.T / 256 + 1 > INT32_MAX / 16 / (a.N / 128 + 1))
-        return VLMCE_ERR_TOO_LARGE;
+    if (!fwd_sizes_ok(a.T, a.N, a.K)) return VLMCE_ERR_TOO_LARGE;
     const int64_t rows = a.gated ? 2 * a.N : a.N;
     vlmce_status st = check_operand(a.x, a.T, a.K, a.x_stride, elt);
     if (st == VLMCE_OK) st = check_operand(a.weight, rows, a.K, a.weight_stride, elt);
@@ -510,4 +513,39 @@ extern "C" vlmce_status glu_bwd(const void *dy, int64_t dy_stride, const void *x
                                 dweight_dtype, nullptr, accumulate, dev_err, workspace,
                                 workspace_bytes, true, reinterpret_cast<cudaStream_t>(stream)};
     return vlmce::linear::backward(a, "glu_bwd");
+}
+
+extern "C" vlmce_status vlmce_linear_describe_plan(int32_t gated, int32_t backward, int64_t T,
+                                                   int64_t N, int64_t K, int32_t dtype,
+                                                   int32_t *out) {
+    using namespace vlmce;
+    const bool fp8 = dtype == VLMCE_E4M3;
+    if ((!fp8 || backward) && dtype != VLMCE_BF16 && dtype != VLMCE_F16)
+        return VLMCE_ERR_UNSUPPORTED_DTYPE;
+    if (!out || T < 1 || N < 1 || K < 1 || K % (fp8 ? 16 : 8) != 0) return VLMCE_ERR_INVALID_ARG;
+    if (!linear::fwd_sizes_ok(T, N, K) || (backward && !linear::bwd_sizes_ok(T, N, K)))
+        return VLMCE_ERR_TOO_LARGE;
+    DeviceInfo dev;
+    const vlmce_status st = current_device(&dev);
+    if (st != VLMCE_OK) return st;
+    for (int i = 0; i < 8; ++i) out[i] = 0;
+    cudaError_t e;
+    if (backward) {
+        mm::Bwd b = {};
+        b.T = T;
+        b.rows = gated ? 2 * N : N;
+        b.K = K;
+        b.f16 = dtype == VLMCE_F16;
+        b.dw = out;  // dx and dweight; nothing is written
+        e = mm::describe(b, out);
+    } else {
+        mm::Fwd f = {};
+        f.T = T;
+        f.N = N;
+        f.K = K;
+        f.gated = gated != 0;
+        f.dtype = dtype;
+        e = mm::describe(f, out);
+    }
+    return launch_status(e, "vlmce_linear_describe_plan");
 }

@@ -151,7 +151,8 @@ struct Plan {
     bool large;
     int narrow;     // large: tiles of 128 weight rows
     int bn, split, stages, per_stage, tmem_cols, smem;
-    int part_offset;  // SmallParams
+    int part_offset, red_tokens;  // SmallParams
+    int per_sm;       // small: CTAs of an SM that the estimate counts on
     double clocks;  // estimate
 };
 
@@ -189,6 +190,7 @@ bool small_plan(const Fwd &f, const Capacity &cap, int64_t ty, int split, int pe
     p.tmem_cols = 32;
     while (p.tmem_cols < kw * p.bn) p.tmem_cols *= 2;
     const int per_sm = p.tmem_cols > 256 || clusters <= cap.small[0][split - 1] ? 1 : 2;
+    p.per_sm = per_sm;
     const double waves = static_cast<double>(clusters) / cap.small[per_sm - 1][split - 1];
     const double rounds = per_sm == 1 ? std::ceil(waves) : waves > 1. ? waves + 0.3 : 1.;
     const int stage = per_stage * (kw * kWTileBytes + p.bn * 128);
@@ -201,6 +203,10 @@ bool small_plan(const Fwd &f, const Capacity &cap, int64_t ty, int split, int pe
         {(small_budget(per_sm) - 1040 - kSmallTail - part) / stage, kMaxSmallStages, steps});
     if (p.stages < 1) return false;
     p.part_offset = part > 0 ? static_cast<int>(round_up(p.stages * stage + kSmallTail, 16)) : 0;
+    p.red_tokens = p.bn;  // in the ring: as many tokens at a time as it holds
+    while (part == 0 &&
+           (p.red_tokens / 4 + split - 1) / split * 4 * split * kw * 512 > p.stages * stage)
+        p.red_tokens -= 16;
     p.smem = std::max({1024 + p.stages * stage + kSmallTail + (part > 0 ? part + 16 : 0),
                        p.tmem_cols * kSmemPerTmemCol - kSmemReserved, kSmallSmemMin});
     const double mma = per_stage * kw * 4 * std::max(p.bn / 2., 32. + p.bn / 4.);
@@ -318,7 +324,6 @@ cudaError_t forward_large(const Fwd &f, const Capacity &cap, int narrow, cudaStr
 }
 
 cudaError_t forward_small(const Fwd &f, const Capacity &cap, const Plan &plan, cudaStream_t s) {
-    const int kw = f.gated ? 2 : 1;
     SmallParams p = {};
     p.T = static_cast<int>(f.T);
     p.N = static_cast<int>(f.N);
@@ -331,12 +336,8 @@ cudaError_t forward_small(const Fwd &f, const Capacity &cap, const Plan &plan, c
     p.tmem_cols = plan.tmem_cols;
     const int64_t ty = (f.T + p.bn - 1) / p.bn;
     const int64_t mt = (f.N + 127) / 128;
-    const int ring = p.stages * p.per_stage * (kw * kWTileBytes + p.bn * 128);
-    p.red_tokens = p.bn;
+    p.red_tokens = plan.red_tokens;
     p.part_offset = plan.part_offset;
-    while (p.part_offset == 0 &&
-           (p.red_tokens / 4 + p.split - 1) / p.split * 4 * p.split * kw * 512 > ring)
-        p.red_tokens -= 16;
     p.e = f.e;
     p.err = f.err ? f.err : cap.errors;
     if (ty > 65535 || mt * p.split > INT32_MAX) return cudaErrorInvalidConfiguration;
@@ -400,35 +401,43 @@ double joint_clocks(const Bwd &b, const Capacity &cap) {
            kJointLaunch;
 }
 
+// dx = dz W as a product of the small kernel (W's rows are its K).
+Fwd dx_product(const Bwd &b) {
+    Fwd f = {};
+    f.x = b.dz;
+    f.w = b.w;
+    f.x_ld = b.dz_ld;
+    f.w_ld = b.w_ld;
+    f.T = b.T;
+    f.N = b.K;
+    f.K = b.rows;
+    f.w_mn = 1;
+    f.dtype = b.f16 ? VLMCE_F16 : VLMCE_BF16;
+    f.e.y = static_cast<uint16_t *>(b.dx);
+    f.e.y_ld = b.dx_ld;
+    f.e.f16 = b.f16;
+    f.err = b.err;
+    return f;
+}
+// dx alone for few tokens takes the small kernel, which spreads the weight over all SMs:
+// T = 16, K = 4096, N = 16384 24 us (73 us in pair tiles).  Beside dW that costs a
+// launch; it pays where one pair tile's walk along W's rows would last longer (the same
+// sizes: 71 against 83 us; T = 256: 100 against 87).
+bool dx_goes_small(const Bwd &b, const Plan &plan, const Capacity &cap) {
+    return !plan.large && (!b.dw || plan.clocks < joint_clocks(b, cap) - dw_clocks(b, cap));
+}
+
 }  // namespace
 
 cudaError_t backward(const Bwd &b, cudaStream_t s) {
     Capacity cap;
     const cudaError_t e = setup(&cap);
     if (e != cudaSuccess) return e;
-    // dx alone for few tokens takes the small kernel (W's rows are its K), which
-    // spreads the weight over all SMs: T = 16, K = 4096, N = 16384 24 us (73 us in pair
-    // tiles).  Beside dW that costs a launch; it pays where one pair tile's walk along
-    // W's rows would last longer (the same sizes: 71 against 83 us; T = 256: 100
-    // against 87).
     bool dx = b.dx != nullptr;
     if (dx) {
-        Fwd f = {};
-        f.x = b.dz;
-        f.w = b.w;
-        f.x_ld = b.dz_ld;
-        f.w_ld = b.w_ld;
-        f.T = b.T;
-        f.N = b.K;
-        f.K = b.rows;
-        f.w_mn = 1;
-        f.dtype = b.f16 ? VLMCE_F16 : VLMCE_BF16;
-        f.e.y = static_cast<uint16_t *>(b.dx);
-        f.e.y_ld = b.dx_ld;
-        f.e.f16 = b.f16;
-        f.err = b.err;
+        const Fwd f = dx_product(b);
         const Plan plan = plan_of(f, cap);
-        if (!plan.large && (!b.dw || plan.clocks < joint_clocks(b, cap) - dw_clocks(b, cap))) {
+        if (dx_goes_small(b, plan, cap)) {
             const cudaError_t es = forward_small(f, cap, plan, s);
             if (es != cudaSuccess || !b.dw) return es;
             dx = false;
@@ -483,6 +492,60 @@ cudaError_t backward(const Bwd &b, cudaStream_t s) {
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, mm_grad_kernel, maps, static_cast<const GradParams>(p));
+}
+
+namespace {
+
+// Tiles of a pair kernel's launch, and whether they are dealt out.
+void describe_pairs(int64_t tiles, int chunks, const Capacity &cap, int32_t *out) {
+    int dealt = 0;
+    pair_grid(tiles, chunks, cap, &dealt);
+    out[4] = static_cast<int32_t>(std::min<int64_t>(tiles, INT32_MAX));
+    out[5] = dealt > 0;
+}
+void describe_tile(const Plan &p, bool gated, int32_t *out) {
+    out[0] = !p.large;
+    out[1] = p.large ? (gated ? 128 : 256) >> p.narrow : 128;
+    out[2] = p.large ? kPairM : p.bn;
+    out[3] = p.large ? 1 : p.split;
+    out[6] = p.large ? 1 : p.per_sm;
+    out[7] = p.large || p.split == 1 || p.part_offset > 0 ? 0 : (p.bn + p.red_tokens - 1) / p.red_tokens;
+}
+
+}  // namespace
+
+cudaError_t describe(const Fwd &f, int32_t *out) {
+    Capacity cap;
+    const cudaError_t e = setup(&cap);
+    if (e != cudaSuccess) return e;
+    const Plan p = plan_of(f, cap);
+    describe_tile(p, f.gated != 0, out);
+    const int64_t tiles = (f.T + out[2] - 1) / out[2] * ((f.N + out[1] - 1) / out[1]);
+    if (p.large)
+        describe_pairs(tiles, chunks_of(f), cap, out);
+    else
+        out[4] = static_cast<int32_t>(std::min<int64_t>(tiles, INT32_MAX));
+    return cudaSuccess;
+}
+
+cudaError_t describe(const Bwd &b, int32_t *out) {
+    Capacity cap;
+    const cudaError_t e = setup(&cap);
+    if (e != cudaSuccess) return e;
+    const Fwd f = dx_product(b);
+    Plan p = plan_of(f, cap);
+    const bool small = dx_goes_small(b, p, cap);
+    if (!small) {  // dx in wide pair tiles, dW's launch
+        p.large = true;
+        p.narrow = 0;
+    }
+    describe_tile(p, false, out);
+    const int64_t across = (b.K + 255) / 256;
+    const int64_t dx_tiles = small ? 0 : (b.T + 255) / 256 * across;
+    const int64_t deep = small ? b.T : std::max(b.T, b.rows);
+    describe_pairs(dx_tiles + (b.rows + 255) / 256 * across, static_cast<int>((deep + 63) / 64), cap,
+                   out);
+    return cudaSuccess;
 }
 
 }  // namespace mm

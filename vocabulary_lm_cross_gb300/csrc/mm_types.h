@@ -64,6 +64,11 @@ struct Bwd {
 };
 cudaError_t backward(const Bwd &b, cudaStream_t s);
 
+// The launches that forward() and backward() (dx and dw) would make for these sizes
+// and types, in the words of vlmce_linear_describe_plan.
+cudaError_t describe(const Fwd &f, int32_t *out);
+cudaError_t describe(const Bwd &b, int32_t *out);
+
 // Bytes (16 or 2) an access to 32 consecutive 16-bit columns of a row may use; 16
 // also means that a tensor map can describe the rows.
 inline int vec_of(const void *p, int64_t ld) {

@@ -3,6 +3,7 @@
 libvlmce.so."""
 from __future__ import annotations
 
+import ctypes
 from typing import NamedTuple
 
 import torch
@@ -23,6 +24,30 @@ class LinearGrads(NamedTuple):
     dx: torch.Tensor | None
     dweight: torch.Tensor | None
     dbias: torch.Tensor | None   # fp32 [N]
+
+
+class LinearPlan(NamedTuple):
+    """vlmce_linear_describe_plan in include/vlmce.h says what the fields are."""
+    kernel: str       # "pairs" or "small"
+    outputs: int
+    tokens: int
+    split: int
+    tiles: int
+    dealt: bool
+    per_sm: int
+    exchanges: int
+
+
+def describe_linear_plan(T: int, N: int, K: int, dtype: torch.dtype, *, gated: bool = False,
+                         backward: bool = False) -> LinearPlan:
+    """The kernels that a linear (gated: glu) layer runs for these sizes on the current
+    device; backward: those of its gradients."""
+    out = (ctypes.c_int32 * 8)()
+    capi.check(capi.lib().vlmce_linear_describe_plan(int(gated), int(backward), T, N, K, DTYPES[dtype],
+                                                     ctypes.cast(out, ctypes.c_void_p)),
+               "vlmce_linear_describe_plan")
+    return LinearPlan(("pairs", "small")[out[0]], out[1], out[2], out[3], out[4], bool(out[5]), out[6],
+                      out[7])
 
 
 def _act(act: str, gated: bool) -> int:
