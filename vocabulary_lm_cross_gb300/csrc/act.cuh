@@ -94,16 +94,7 @@ __device__ __forceinline__ void fwd_bwd(float a, float &f, float &d) {
     }
 }
 
-// act(a) with the activation chosen at run time (uniform over the grid).
-__device__ __forceinline__ float apply(float a, int kind) {
-    switch (kind) {
-        case VLMCE_ACT_SILU: return fwd<VLMCE_ACT_SILU>(a);
-        case VLMCE_ACT_GELU: return fwd<VLMCE_ACT_GELU>(a);
-        case VLMCE_ACT_GELU_TANH: return fwd<VLMCE_ACT_GELU_TANH>(a);
-        case VLMCE_ACT_RELU: return fwd<VLMCE_ACT_RELU>(a);
-        default: return a;
-    }
-}
+// act(v) with the activation chosen at run time (uniform over the grid).
 template <int N>
 __device__ __forceinline__ void apply_n(float (&v)[N], int kind) {
     switch (kind) {
