@@ -9,11 +9,11 @@
 // P(-x) = e^(-x^2/2) R(x) / 2 for x >= 0, with the scaled complementary error
 // function R(x) = e^(x^2/2) erfc(x / sqrt 2) as t p(t), t = 1 / (1 + 0.3 x / sqrt 2)
 // and p of degree 8: a least-squares fit, reweighted towards the smallest largest
-// relative error (2e-8 for x <= 13.4, beyond which e^(-x^2/2) is 0 in fp32).  So
-// the relative accuracy holds for negative a too (1 + erf would cancel; 9e-7 for
-// a > -4, 8e-6 for a > -13 in fp32), one exponential serves P and its derivative,
-// and there is no branch (T 1007, K 1000, N 777 in the small kernel with erfcf 15.1 us,
-// so 13.9).
+// relative error (6e-8 with the coefficients below, for x <= 13.4, beyond which
+// e^(-x^2/2) is 0 in fp32).  So the relative accuracy holds for negative a too (1 + erf
+// would cancel; 9e-7 for a > -4, 8e-6 for a > -13 in fp32), one exponential serves P and
+// its derivative, and there is no branch (T 1007, K 1000, N 777 in the small kernel with
+// erfcf 15.1 us, so 13.9).
 #pragma once
 
 #include <cuda_bf16.h>
