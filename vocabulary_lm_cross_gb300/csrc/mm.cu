@@ -75,7 +75,9 @@ struct Capacity {
     int small[2][kMaxSplit];
     int *errors = nullptr;
 };
-constexpr int kSmSmem = 233472;  // 228 KB
+// no small CTA beside a kernel that holds all TMEM columns (mm_small.cuh)
+static_assert(gemm::kSmemBytes + kSmallSmemMin + 2 * kSmemReserved > kSmSmem, "GEMM engine");
+static_assert(kPairSmem + kSmallSmemMin + 2 * kSmemReserved > kSmSmem, "pair kernels");
 constexpr int small_budget(int per_sm) { return kSmSmem / per_sm - kSmemReserved; }
 
 // Stands for the small kernels in occupancy queries, which count a kernel that

@@ -15,11 +15,12 @@
 // not wait for the other SM), and it adds them in rank order (fixed, so the
 // result does not depend on timing).
 //
-// Two CTAs of this kernel, or one and another kernel's, may share an SM.  TMEM
-// allocation blocks while columns are short, and a blocked CTA of a cluster
-// could wait on one that waits on it; so every kernel of the library that
-// allocates TMEM takes at least the same share of the SM's shared memory
-// (kSmemPerTmemCol per column), so that TMEM never runs out first.
+// Two CTAs of this kernel may share an SM.  TMEM allocation blocks while columns are
+// short, and a blocked CTA of a cluster could wait on one that waits on it; so CTAs of
+// this kernel take at least the same share of the SM's shared memory as of its TMEM
+// (kSmemPerTmemCol per column), and TMEM never runs out first.  The library's pair
+// kernels hold all 512 columns with less than all of the shared memory (the GEMM
+// engine 198 KB): kSmallSmemMin keeps a CTA of this kernel from fitting beside one.
 //
 // Measured on GB300 (a call among others): T = 1, K = 4096, 2n = 24576 bf16 34.5 us
 // (201 MB of weight: 5.8 TB/s with the launch's 4 us), T = 64, K = 16384, N = 6656
@@ -52,11 +53,12 @@ constexpr int kMaxSplit = 8;
 // barriers, TMEM slot, abort flag, the tokens' factors
 constexpr int kSmallTail = 8 * (2 * kMaxSmallStages + 2) + 16 + 4 * 256;
 // Shared memory of an SM (228 KB, 1 KB of it reserved per resident CTA) over its
-// 512 TMEM columns; and a floor that does not fit beside a pair kernel, which
-// holds all 512 columns with 198 KB.
+// 512 TMEM columns; and the floor beside the pair kernels.
+constexpr int kSmSmem = 233472;
 constexpr int kSmemPerTmemCol = 456;
 constexpr int kSmemReserved = 1024;
 constexpr int kSmallSmemMin = 34816;
+static_assert(kSmemPerTmemCol * 512 >= kSmSmem, "TMEM would run out first");
 
 struct SmallParams {
     int T, N;
