@@ -432,6 +432,9 @@ size_t vlmce_glu_bwd_workspace_bytes(int64_t T, int64_t n, int64_t K);
  *   dz = dy act'(z),  dx = dz W,  dweight = dz^T x,  dbias = sum_t dz
  * (the residual's gradient is dy itself).  dz is formed in fp32 and rounded
  * once to `dtype` for the two products; dbias is summed from the fp32 values.
+ * So dz has the range of `dtype` too: in fp16 an element beyond 65504 becomes infinite,
+ * and with it its row of dx and of dweight, and one below 3e-8 zero.  A loss scale
+ * has to keep dy act'(z), and dy u act'(g) of a gated layer, within it.
  *
  * dtype           VLMCE_BF16 or VLMCE_F16: dy, x, weight, preact, dx.
  * dy              [T, dy_stride >= N]; preact: linear_fwd's z (not read, and may

@@ -209,6 +209,25 @@ def test_every_way_of_running_the_gradients(gated, T, K, N, want):
     check_bwd(T, K, N, gated=gated, seed=3, dtype="f16")
 
 
+@pytest.mark.parametrize("dtype,finite", [("f16", False), ("bf16", True)])
+def test_pre_activation_gradients_have_the_range_of_their_type(dtype, finite):
+    x = torch.full((2, 8), 2.0 ** -8, device="cuda").to(DT[dtype])
+    w = torch.full((16, 8), 2.0 ** -8, device="cuda").to(DT[dtype])
+    z = torch.ones((2, 16), device="cuda").to(DT[dtype])
+    z[:, 8:] = 256
+    for dy, ok in ((128.0, True), (256.0, finite)):  # dy u = 2^15, and 2^16 > 65504
+        d = torch.full((2, 8), dy, device="cuda").to(DT[dtype])
+        d[1] = 1
+        g = v.glu_bwd(d, x, w, z, act="relu")
+        assert torch.isfinite(g.dx[1]).all() and torch.isfinite(g.dweight[8:]).all()
+        assert bool(torch.isfinite(g.dx[0]).all()) == ok
+        assert bool(torch.isfinite(g.dweight[:8]).all()) == ok
+        # below the type's range: zero, without a trace in the sums
+        d.fill_(2.0 ** -24)
+        small = torch.full_like(z, 0.25)
+        assert bool((v.glu_bwd(d, x, w, small, act="relu").dweight == 0).all()) == (dtype == "f16")
+
+
 def test_plan_refuses():
     for kw in (dict(T=0), dict(N=0), dict(K=60), dict(K=72, dtype=torch.float8_e4m3fn), dict(T=1 << 31),
                dict(dtype=torch.float32), dict(dtype=torch.float8_e4m3fn, backward=True)):

@@ -7,8 +7,9 @@
 //   gated    dz = (dy u act'(g) | dy act(g))
 //   dx = dz W,  dW = dz^T x,  db = sum_t dz
 // dz is formed in fp32 by one elementwise pass and rounded once to the
-// operands' 16-bit type, which the tensor cores need; db is summed from the
-// fp32 values.  The two products run as one launch of the library's GEMM.
+// operands' 16-bit type, which the tensor cores need (its range too: fp16 ends at
+// 65504); db is summed from the fp32 values.  The two products run as one launch of
+// the pair kernel, or dx on the small kernel and dW after it (mm.cu).
 // Without an activation dz is dy itself and the pass is left out (unless dy's
 // rows are not 16-byte aligned, or db is wanted, which reads dy only).
 #include <cuda_runtime.h>

@@ -246,7 +246,8 @@ def linear_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
     """Gradients of linear_fwd (bf16 or fp16): dx, dweight (fp32 unless
     dweight_dtype, x's dtype, asks otherwise) and, with bias_grad or dbias, dbias
     (fp32).  The residual's gradient is dy.  accumulate: add to the given fp32
-    dweight and dbias."""
+    dweight and dbias.  The gradient of the pre-activations is rounded to x's dtype:
+    in fp16 it must stay within 65504."""
     return _backward(False, dy, x, weight, preact, act, bias_grad, want_dx, want_dweight, out,
                      dweight, dweight_dtype, dbias, accumulate, workspace, dev_err)
 
@@ -258,6 +259,7 @@ def glu_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, preact: tor
             workspace: torch.Tensor | None = None,
             dev_err: torch.Tensor | None = None) -> LinearGrads:
     """Gradients of glu_fwd (bf16 or fp16): dx [T, K] and dweight [2n, K] (fp32
-    unless dweight_dtype, x's dtype, asks otherwise); dbias is None."""
+    unless dweight_dtype, x's dtype, asks otherwise); dbias is None.  The range of
+    fp16 as in linear_bwd."""
     return _backward(True, dy, x, weight, preact, act, False, want_dx, want_dweight, out, dweight,
                      dweight_dtype, None, accumulate, workspace, dev_err)
