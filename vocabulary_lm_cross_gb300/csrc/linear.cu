@@ -287,10 +287,10 @@ vlmce_status forward(const FwdArgs &a, const char *where) {
     e.ws = a.weight_scale;
     e.act = a.act;
     e.f16 = a.out_dtype == VLMCE_F16;
-    e.y_vec = mm::vec_of(a.y, a.y_stride);
+    e.y_vec = mm::vec_of(a.y, a.y_stride, a.N);
     if (e.preact) {
-        e.preact_vec = mm::vec_of(e.preact, a.preact_stride);
-        e.preact_up_vec = mm::vec_of(e.preact + a.N, a.preact_stride);
+        e.preact_vec = mm::vec_of(e.preact, a.preact_stride, a.N);
+        e.preact_up_vec = mm::vec_of(e.preact + a.N, a.preact_stride, a.N);
     }
     return launch_status(mm::forward(f, a.stream), where);
 }

@@ -29,12 +29,14 @@ bool operand_map(CUtensorMap *m, const void *base, int32_t dtype, int64_t rows, 
     return gemm::make_tile_map(m, base, type, elt, K, rows, ld, 128 / elt, box_rows);
 }
 
-// A 16-bit (or fp32) output [rows, cols], stored in boxes of 128 bytes x 32 rows.
+// A 16-bit (or fp32) output [rows, cols], stored in boxes of 128 bytes x 32 rows: its
+// columns in whole granules of 16 bytes, since a store would fill the last one (Out in
+// mm_pair.cuh; the fp32 ones, a weight's K columns, are whole).
 bool output_map(CUtensorMap *m, const void *base, bool f32, int64_t rows, int64_t cols,
                 int64_t ld) {
     return gemm::make_tile_map(
         m, base, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-        f32 ? 4 : 2, cols, rows, ld, f32 ? 32 : 64, 32);
+        f32 ? 4 : 2, cols & ~int64_t{7}, rows, ld, f32 ? 32 : 64, 32);
 }
 
 int chunks_of(const Fwd &f) {

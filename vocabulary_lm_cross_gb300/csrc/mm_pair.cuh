@@ -294,11 +294,15 @@ __device__ __forceinline__ void acc_release(uint32_t tempty_leader, int it, int 
 // takes it to memory as whole 128-byte lines, leaving out what is not there; else
 // (`vec` = 2) a segment passes through the buffer on its own, so that a warp's
 // 2-byte accesses cover consecutive addresses of a row.
+//
+// A TMA store cuts a row off at 16 bytes, not at the element: measured, it writes the
+// whole last granule.  So the maps end with the last whole granule, and the up to 7
+// columns after it are stored one by one.
 struct Out {
     uint16_t *base;
     int64_t ld;
     int vec;                 // bytes an access may use: >= 16, or 2
-    const CUtensorMap *map;  // boxes of 64 columns x 32 rows
+    const CUtensorMap *map;  // boxes of 64 columns x 32 rows, of whole granules
 };
 
 // The warp's buffer may be written: its TMA stores have read it.  (A second buffer,
@@ -321,10 +325,18 @@ __device__ __forceinline__ void put_seg(const Out &o, int64_t row0, int col, int
         for (int j = 0; j < 4; ++j)
             *reinterpret_cast<uint4 *>(row + (((4 * h + j) ^ (lane & 7)) << 4)) =
                 make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
+        const int whole = cols & ~7, c0 = col + 32 * h;
+        if (c0 < cols && c0 + 32 > whole && whole < cols && row0 + lane < rows) {
+            uint16_t *p = o.base + (row0 + lane) * o.ld + c0;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (c0 + j >= whole && c0 + j < cols)
+                    p[j] = static_cast<uint16_t>(u[j / 2] >> 16 * (j & 1));
+        }
         if (h == 1) {
             ptx::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) {
+            if (lane == 0 && col < whole) {
                 tc::tma_store_2d(o.map, ptx::smem_addr(buf), col, static_cast<int>(row0));
                 tc::bulk_commit();
             }

@@ -70,10 +70,10 @@ cudaError_t describe(const Fwd &f, int32_t *out);
 cudaError_t describe(const Bwd &b, int32_t *out);
 
 // Bytes (16 or 2) an access to 32 consecutive 16-bit columns of a row may use; 16
-// also means that a tensor map can describe the rows.
-inline int vec_of(const void *p, int64_t ld) {
+// also means that a tensor map can describe the rows (their whole granules of 16 bytes).
+inline int vec_of(const void *p, int64_t ld, int64_t cols) {
     const uint64_t a = reinterpret_cast<uint64_t>(p) | static_cast<uint64_t>(2 * ld);
-    return a % 16 == 0 && ld < (int64_t{1} << 39) ? 16 : 2;
+    return a % 16 == 0 && ld < (int64_t{1} << 39) && cols >= 8 ? 16 : 2;
 }
 
 }  // namespace mm
