@@ -144,6 +144,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const uint32_t tempty_leader = ptx::mapa(q.tempty(0), 0);
         const Epi &e = p.e;
         const bool f16 = e.f16 != 0;
+        const bool ragged = (p.N & 7) != 0;  // rows end inside a granule
         const Out y = {e.y, e.y_ld, e.y_vec, &maps.y};
         const Out z = {e.preact, e.preact_ld, e.preact_vec, &maps.z};
         const Out z_up = {e.preact + p.N, e.preact_ld, e.preact_up_vec, &maps.z_up};
@@ -198,6 +199,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         z_seg(h, v);
                         put_seg(z, row0, col, h, v, p.T, p.N, f16, buf, lane);
                     }
+                    if (ragged) put_rest(z, row0, col, p.T, p.N, buf, lane);
                     if constexpr (GATED) {
 #pragma unroll 1
                         for (int h = 0; h < 2; ++h) {
@@ -239,6 +241,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     }
                     put_seg(y, row0, col, h, v, p.T, p.N, f16, buf, lane);
                 }
+                if (ragged) put_rest(y, row0, col, p.T, p.N, buf, lane);
                 if constexpr (!GATED) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {

@@ -325,18 +325,10 @@ __device__ __forceinline__ void put_seg(const Out &o, int64_t row0, int col, int
         for (int j = 0; j < 4; ++j)
             *reinterpret_cast<uint4 *>(row + (((4 * h + j) ^ (lane & 7)) << 4)) =
                 make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
-        const int whole = cols & ~7, c0 = col + 32 * h;
-        if (c0 < cols && c0 + 32 > whole && whole < cols && row0 + lane < rows) {
-            uint16_t *p = o.base + (row0 + lane) * o.ld + c0;
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (c0 + j >= whole && c0 + j < cols)
-                    p[j] = static_cast<uint16_t>(u[j / 2] >> 16 * (j & 1));
-        }
         if (h == 1) {
             ptx::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0 && col < whole) {
+            if (lane == 0 && cols - col >= 8) {
                 tc::tma_store_2d(o.map, ptx::smem_addr(buf), col, static_cast<int>(row0));
                 tc::bulk_commit();
             }
@@ -354,6 +346,19 @@ __device__ __forceinline__ void put_seg(const Out &o, int64_t row0, int col, int
 #pragma unroll 8
         for (int r = 0; r < nr; ++r) p[r * o.ld] = s16[r * 34 + lane];
     }
+}
+// The up to 7 columns after a row's last whole granule, from the warp's buffer, which
+// still holds the 64 columns from `col`.
+__device__ __forceinline__ void put_rest(const Out &o, int64_t row0, int col, int64_t rows,
+                                         int cols, const uint32_t *buf, int lane) {
+    const int left = cols - col;
+    if (o.vec < 16 || left >= 64 || row0 + lane >= rows) return;
+    const uint16_t *at = reinterpret_cast<const uint16_t *>(
+        reinterpret_cast<const unsigned char *>(buf) + lane * 128 +
+        (((left >> 3) ^ (lane & 7)) << 4));
+    uint16_t *p = o.base + (row0 + lane) * o.ld + (cols & ~7);
+#pragma unroll 1
+    for (int j = 0; j < (left & 7); ++j) p[j] = at[j];
 }
 // 64 columns from `col` of row `row` of a 16-bit tensor, one row per lane, on their
 // way in registers: the 16-byte granules of the memory that hold them, at any
