@@ -4,8 +4,9 @@
 //   dW = dz^T x   A = dz: M(=rows)-major,         B = x: N(=K_in)-major
 // with either operand K-major or MN-major, so nothing is transposed in memory.
 //
-// Tensor-bound: T = 4096, K = 6656, 2n = 32768 both products 1.83 ms in a burst (1.95
-// PFLOP/s; with the library's older GEMM 2.18), 2.05 back to back under the power cap.
+// Tensor-bound: T = 4096, K = 6656, 2n = 32768 both products 1.82-1.90 ms in a burst
+// (1.88-1.97 PFLOP/s; with the library's older GEMM 2.18), 2.09-2.14 back to back under
+// the power cap (97-100 % of the library's sustained rate).
 // For few tokens bound by dW's stores (T = 16, K = 4096, N = 16384 39 us for 134 MB; a
 // plain fill takes 34).
 //

@@ -4,10 +4,10 @@
 // A tile is 256 tokens x 256 weight rows (mm_pair.cuh).  A gated layer's tile
 // takes 128 gate rows (staged by the pair's leader) and the 128 up rows of the
 // same outputs (staged by its peer), so gate and up of an output meet in one
-// thread.  Tensor-bound: T = 4096, K = 6656, 2n = 32768 bf16 909-925 us in a burst
-// (1.93-1.97 PFLOP/s, above the measured burst rate of the library), 1020-1086 us back to
-// back, where the power cap sets the clock (96-102 % of the library's sustained rate);
-// tensor pipe 86 % busy before two chunks made a stage.  Tile order: groups of kGroupM
+// thread.  Tensor-bound: T = 4096, K = 6656, 2n = 32768 bf16 902-940 us in a burst
+// (1.90-1.98 PFLOP/s, the measured burst rate of the library), 1048-1086 us back to
+// back, where the power cap sets the clock (96-100 % of the library's sustained rate);
+// tensor pipe 93 % busy (86 % before two chunks made a stage).  Tile order: groups of kGroupM
 // token tiles, weight tiles outer within a group, so that the ~76 tiles in flight read
 // about 8 token and 9.5 weight tiles.
 // `narrow` tiles have 128 weight rows (gated: 64 + 64), and four stages of the ring.
@@ -15,8 +15,8 @@
 // The epilogue asks for what it reads from memory (scales, bias, residual) before it
 // waits for a tile's accumulators, the residual's next 64 columns while it works on the
 // present ones: behind the ring's copies an answer takes thousands of clocks (T 8192,
-// K 2048, N 2048 bf16 with bias, preact and residual 60.5 us, asked for where used 89;
-// N 2049 88.6 and 260).
+// K 2048, N 2048 bf16 with bias, preact and residual 61.3 us, asked for where used 89;
+// N 2049 88.1 and 260).
 #pragma once
 
 #include <cuda.h>

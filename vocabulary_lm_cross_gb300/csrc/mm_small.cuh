@@ -22,9 +22,9 @@
 // kernels hold all 512 columns with less than all of the shared memory (the GEMM
 // engine 198 KB): kSmallSmemMin keeps a CTA of this kernel from fitting beside one.
 //
-// Measured on GB300 (a call among others): T = 1, K = 4096, 2n = 24576 bf16 34.5 us
-// (201 MB of weight: 5.8 TB/s with the launch's 4 us), T = 64, K = 16384, N = 6656
-// e4m3 24.8 us (4.5 TB/s), T = 300, K = 4096, 2n = 20480 e4m3 32.7 us (1.54 PFLOP/s:
+// Measured on GB300 (a call among others): T = 1, K = 4096, 2n = 24576 bf16 35.4 us
+// (201 MB of weight: 5.7 TB/s with the launch's 4 us), T = 64, K = 16384, N = 6656
+// e4m3 25.5 us (4.4 TB/s), T = 300, K = 4096, 2n = 20480 e4m3 33.1 us (1.52 PFLOP/s:
 // bound by the operands' way from L2, 53 of 64 bytes a clock on the SMs with two CTAs).
 //
 // CTA = 10 warps: warp 0 TMA producer, warp 1 TMEM and MMA issuer, warps 2-9
