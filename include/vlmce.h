@@ -57,9 +57,9 @@ typedef enum {
 } vlmce_status;
 
 /* VLMCE_F16: fp16, accepted by flce_fwd_bwd_ex, vlmce_gemm, rmsnorm_*,
- * linear_* and glu_*.  VLMCE_E4M3: 8-bit floating point (4 exponent, 3
- * mantissa bits, no infinities), the output of rmsnorm_fwd and the operands of
- * linear_fwd and glu_fwd. */
+ * linear_*, glu_*, moe_* and quantize_blocks.  VLMCE_E4M3: 8-bit floating point (4
+ * exponent, 3 mantissa bits, no infinities), the output of rmsnorm_fwd, moe_gather and
+ * quantize_blocks and the operands of linear_fwd, glu_fwd and block_linear_*. */
 typedef enum { VLMCE_F32 = 0, VLMCE_BF16 = 1, VLMCE_F16 = 2, VLMCE_E4M3 = 3 } vlmce_dtype;
 /* Activations of linear_* and (but for NONE) glu_*: a s(a) with s(a) = 1 / (1 +
  * e^-a); a P(a) with the normal CDF P; its tanh form a (1 + tanh(sqrt(2/pi) (a
@@ -485,6 +485,117 @@ vlmce_status glu_bwd(const void *dy, int64_t dy_stride, const void *x, int64_t x
                      int32_t act, void *dx, int64_t dx_stride, void *dweight,
                      int32_t dweight_dtype, int32_t accumulate, int32_t *dev_err, void *workspace,
                      size_t workspace_bytes, vlmce_stream_t stream);
+
+/*
+ * Experts: k of E experts work on each of T tokens.  moe_sort says where the experts'
+ * rows are, moe_gather copies the tokens' rows there, moe_combine brings the experts'
+ * results back.
+ *
+ * position        int32 [T, k]: the row of token t's j-th expert, or -1 (none: the
+ *                 expert is not one of these E).  The calls that read it take any value
+ *                 outside [0, R) as -1; no row may stand in it twice.
+ * offsets         int32 [E + 1]: where each expert's rows start, and the end of the last's.
+ * counts          int32 [E]: its rows in use; those up to offsets[e + 1] stand between
+ *                 (where counts were rounded up).
+ * R               rows that the experts' matrices have, at least offsets[E]; what is
+ *                 behind offsets[E] is neither read nor written.
+ */
+#define VLMCE_MOE_MAX_EXPERTS 1024
+#define VLMCE_MOE_MAX_TOPK 64
+
+/* Rows that hold any choice of k of E experts by T tokens, each expert's rows rounded
+ * up to a multiple of `align`; -1 for sizes that moe_sort rejects. */
+int64_t vlmce_moe_rows(int64_t T, int64_t k, int64_t E, int64_t align);
+
+/*
+ * moe_sort -- the order of the (token, expert) pairs by expert, those of an expert in
+ * the order of the tokens (and of a token's slots):
+ *   position[t, j] = offsets[e] + #{(t', j') before (t, j): experts[t', j'] = e},
+ *   offsets[0] = 0, offsets[e + 1] = offsets[e] + counts[e] rounded up to `align`.
+ *
+ * experts         [T, experts_stride >= k] int32, or int64 with `wide` != 0: ids; one
+ *                 outside [0, E) is no expert's pair (position -1).  A token may name
+ *                 an expert twice.
+ * align           >= 1; 128 for rows that block_linear_dweight sums over.
+ * 1 <= k <= VLMCE_MOE_MAX_TOPK, 1 <= E <= VLMCE_MOE_MAX_EXPERTS, T >= 0.
+ * Deterministic.  One launch.
+ */
+vlmce_status moe_sort(const void *experts, int64_t experts_stride, int32_t wide, int64_t T,
+                      int64_t k, int64_t E, int64_t align, int32_t *position, int32_t *offsets,
+                      int32_t *counts, vlmce_stream_t stream);
+
+/*
+ * moe_gather -- rows[position[t, j]] = x[t], and zeros in the rows between an expert's
+ * last and the next one's first.
+ *
+ * x               [T, x_stride >= H] of dtype (VLMCE_F32, VLMCE_BF16 or VLMCE_F16).
+ * rows            [R, rows_stride >= H] of rows_dtype: dtype, or VLMCE_E4M3, quantised
+ *                 as quantize_blocks does along the rows.
+ * scale           with VLMCE_E4M3: fp32 [R, ceil(H / 128)]; else NULL.
+ * H <= 2^24.  Outputs overlap nothing.
+ */
+vlmce_status moe_gather(const void *x, int64_t x_stride, int32_t dtype, const int32_t *position,
+                        const int32_t *offsets, const int32_t *counts, int64_t T, int64_t k,
+                        int64_t E, int64_t R, int64_t H, void *rows, int64_t rows_stride,
+                        int32_t rows_dtype, float *scale, vlmce_stream_t stream);
+
+/*
+ * moe_combine -- y[t] = sum_j weights[t, j] rows[position[t, j]] + residual[t], summed in
+ * fp32 in the order of j and rounded once; without weights also the gradient of moe_gather.
+ *
+ * rows            [R, rows_stride >= H] of dtype (VLMCE_F32, VLMCE_BF16 or VLMCE_F16).
+ * weights         [T, weights_stride >= k] of weights_dtype (dtype or VLMCE_F32), or
+ *                 NULL: all 1.
+ * residual        [T, residual_stride >= H] of dtype, or NULL; it may be y itself.
+ * y               [T, y_stride >= H] of dtype; overlaps nothing else.
+ * Deterministic.
+ */
+vlmce_status moe_combine(const void *rows, int64_t rows_stride, int32_t dtype,
+                         const int32_t *position, const void *weights, int64_t weights_stride,
+                         int32_t weights_dtype, const void *residual, int64_t residual_stride,
+                         int64_t T, int64_t k, int64_t R, int64_t H, void *y, int64_t y_stride,
+                         vlmce_stream_t stream);
+
+/*
+ * moe_combine_bwd -- gradients of moe_combine:
+ *   drows[position[t, j]] = weights[t, j] dy[t],  dweights[t, j] = <dy[t], rows[position[t, j]]>
+ * and zeros in the rows between an expert's last and the next one's first (the residual's
+ * gradient is dy itself).
+ *
+ * dy              [T, dy_stride >= H] of dtype; rows, weights as moe_combine (rows is
+ *                 read for dweights only).
+ * drows           [R, drows_stride >= H] of dtype, or NULL.
+ * dweights        fp32 [T, k], or NULL; 0 where there is no row.
+ * One of the two is given (T > 0).  Outputs overlap nothing.  Deterministic.
+ */
+vlmce_status moe_combine_bwd(const void *dy, int64_t dy_stride, const void *rows,
+                             int64_t rows_stride, int32_t dtype, const int32_t *position,
+                             const int32_t *offsets, const int32_t *counts, const void *weights,
+                             int64_t weights_stride, int32_t weights_dtype, int64_t T, int64_t k,
+                             int64_t E, int64_t R, int64_t H, void *drows, int64_t drows_stride,
+                             float *dweights, vlmce_stream_t stream);
+
+/*
+ * quantize_blocks -- VLMCE_E4M3 with one scale per block of 128, of `batch` matrices
+ * [R, C].  A block with the largest magnitude a stands for scale q:
+ *   a' = max(a, 2^-100),  scale = a' / 448,  q = x (448 / a') rounded to nearest even.
+ * A block that holds an infinity or a NaN stands for NaNs.
+ *
+ * x               [batch, R, C] of dtype (VLMCE_F32, VLMCE_BF16 or VLMCE_F16), rows
+ *                 x_stride and matrices x_batch_stride elements apart.
+ * square          0: blocks of 128 columns of a row for q, of 128 rows of a column for
+ *                 qt; else blocks of 128 x 128 for both.
+ * q, scale        [batch, R, q_stride >= C] and fp32 [batch, R, ceil(C / 128)] (square:
+ *                 [batch, ceil(R / 128), ceil(C / 128)]); or both NULL.
+ * qt, scale_t     the transposed form: [batch, C, qt_stride >= R] and fp32 [batch, C,
+ *                 ceil(R / 128)] (square: [batch, ceil(C / 128), ceil(R / 128)]); or
+ *                 both NULL, but not all four.
+ * (block_linear_* take strides that are multiples of 16.)  Outputs overlap nothing.
+ */
+vlmce_status quantize_blocks(const void *x, int32_t dtype, int64_t batch, int64_t R, int64_t C,
+                             int64_t x_stride, int64_t x_batch_stride, int32_t square, void *q,
+                             int64_t q_stride, float *scale, void *qt, int64_t qt_stride,
+                             float *scale_t, vlmce_stream_t stream);
 
 /* Bytes of device workspace flce_fwd_bwd needs (256-byte aligned): per-row
  * statistics of every 256-column logits tile, two bf16 [N, 8192] gradient

@@ -34,6 +34,8 @@ ACT_SILU = 1
 ACT_GELU = 2
 ACT_GELU_TANH = 3
 ACT_RELU = 4
+MOE_MAX_EXPERTS = 1024
+MOE_MAX_TOPK = 64
 
 _lock = threading.Lock()
 _lib = None
@@ -102,6 +104,16 @@ SIGNATURES = {
                        _i64, _vp, _i64, _vp, _vp]),
     "glu_bwd": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _i64, _i64, _i64, _i32,
                        _vp, _i64, _vp, _i32, _i32, _vp, _vp, _sz, _vp]),
+    "vlmce_moe_rows": (_i64, [_i64, _i64, _i64, _i64]),
+    "moe_sort": (_i32, [_vp, _i64, _i32, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp]),
+    "moe_gather": (_i32, [_vp, _i64, _i32, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _vp, _i64,
+                          _i32, _vp, _vp]),
+    "moe_combine": (_i32, [_vp, _i64, _i32, _vp, _vp, _i64, _i32, _vp, _i64, _i64, _i64, _i64,
+                           _i64, _vp, _i64, _vp]),
+    "moe_combine_bwd": (_i32, [_vp, _i64, _vp, _i64, _i32, _vp, _vp, _vp, _vp, _i64, _i32, _i64,
+                               _i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp]),
+    "quantize_blocks": (_i32, [_vp, _i32, _i64, _i64, _i64, _i64, _i64, _i32, _vp, _i64, _vp, _vp,
+                               _i64, _vp, _vp]),
 }
 
 

@@ -1,0 +1,697 @@
+// moe.cu -- tokens to their experts and back: the order of the (token, slot) pairs by
+// expert, the tokens' rows in that order (as they are, or in e4m3 by blocks of 128), the
+// experts' rows brought back with weights, and the gradients of both.
+//
+//   sort      position[t, j] = offsets[e] + rank of (t, j) among the pairs of e = experts[t, j]
+//             offsets[e + 1] = offsets[e] + count[e] rounded up to `align`
+//   gather    rows[position[t, j]] = x[t]
+//   combine   y[t] = sum_j w[t, j] rows[position[t, j]] + residual[t]   (j in order)
+//   gradient  drows[position[t, j]] = w[t, j] dy[t],  dw[t, j] = <dy[t], rows[position[t, j]]>
+//
+// Everything but the sort goes token by token: a token's row is read (and quantised)
+// once, however many experts it has, and no inverse of `position` is needed.  Those
+// kernels are bound by memory; what keeps loads in flight is a token's k rows, which a
+// thread asks for together.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <mutex>
+
+#include "blocks.cuh"
+#include "host_util.h"
+#include "ptx.cuh"
+#include "rows_host.h"
+#include "vlmce.h"
+
+namespace vlmce {
+namespace moe {
+namespace {
+
+// ------------------------------------------------------------------- sort
+// One launch of one cluster.  The pairs are dealt to its warps in consecutive runs; each
+// warp counts its run by expert in shared memory, the counts are summed over the warps of
+// a CTA and then over the CTAs (through distributed shared memory), every CTA scans the
+// experts' totals, and each warp walks its run again, 32 pairs at a time: pairs of one
+// expert find their rank among themselves (match) and take it from the warp's cursor.  So
+// the order is that of the pairs, whatever the timing, and there is no atomic that
+// matters to it.
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kMaxExperts = VLMCE_MOE_MAX_EXPERTS;
+static_assert(kMaxExperts <= kSortThreads, "a thread scans an expert");
+constexpr int kMaxSortCtas = 8;
+
+struct SortParams {
+    const void *experts;
+    int64_t ld;
+    int64_t pairs;
+    int k, E, align, wide, ctas;
+    int *position, *offsets, *counts;
+};
+
+__device__ __forceinline__ int sort_load(const SortParams &p, int64_t i) {
+    const int64_t t = i / p.k;
+    const int64_t at = t * p.ld + (i - t * p.k);
+    if (p.wide) {
+        const int64_t e = static_cast<const int64_t *>(p.experts)[at];
+        return e >= 0 && e < p.E ? static_cast<int>(e) : -1;
+    }
+    const int e = static_cast<const int *>(p.experts)[at];
+    return e >= 0 && e < p.E ? e : -1;
+}
+
+__global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const SortParams p) {
+    extern __shared__ int cursor[];          // [kSortWarps][E]: a warp's counts, then its next rows
+    __shared__ int total[kMaxExperts];       // of this CTA
+    __shared__ int warp_sum[kSortWarps];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = p.ctas > 1 ? static_cast<int>(ptx::cluster_ctarank()) : 0;
+    // whole groups of 32 pairs to a warp
+    const int64_t groups = (p.pairs + 31) / 32;
+    const int64_t warps = static_cast<int64_t>(p.ctas) * kSortWarps;
+    const int64_t per = (groups + warps - 1) / warps * 32;
+    const int64_t first = min(p.pairs, (static_cast<int64_t>(rank) * kSortWarps + warp) * per);
+    const int64_t last = min(p.pairs, first + per);
+    int *mine = cursor + warp * p.E;
+
+    for (int e = lane; e < p.E; e += 32) mine[e] = 0;
+    __syncwarp();
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+#pragma unroll 4
+    for (int64_t i = first + lane; i < last; i += 32) {
+        const int e = sort_load(p, i);
+        if (e >= 0) atomicAdd(mine + e, 1);
+    }
+    __syncthreads();
+    // where each warp's pairs of an expert start among the CTA's
+    int count = 0;  // of expert `tid`: this CTA's, then the sum over all
+    if (tid < p.E) {
+#pragma unroll 8
+        for (int w = 0; w < kSortWarps; ++w) {
+            const int c = cursor[w * p.E + tid];
+            cursor[w * p.E + tid] = count;
+            count += c;
+        }
+        total[tid] = count;
+    }
+    int before = 0;  // pairs of the expert in the CTAs before this one
+    if (p.ctas > 1) {
+        ptx::cluster_sync();
+        if (tid < p.E) {
+            count = 0;
+            for (int c = 0; c < p.ctas; ++c) {
+                int v;
+                asm volatile("ld.shared::cluster.u32 %0, [%1];"
+                             : "=r"(v)
+                             : "r"(ptx::mapa(ptx::smem_addr(total + tid), c))
+                             : "memory");
+                if (c < rank) before += v;
+                count += v;
+            }
+        }
+    }
+    // exclusive sums of the rounded counts over the experts
+    const int padded = (count + p.align - 1) / p.align * p.align;
+    int sum = padded;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int v = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += v;
+    }
+    if (lane == 31) warp_sum[warp] = sum;
+    __syncthreads();
+    if (warp == 0) {
+        int s = warp_sum[lane];
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int v = __shfl_up_sync(0xffffffffu, s, d);
+            if (lane >= d) s += v;
+        }
+        warp_sum[lane] = s;
+    }
+    __syncthreads();
+    const int start = (warp > 0 ? warp_sum[warp - 1] : 0) + sum - padded;
+    if (tid < p.E) {
+        for (int w = 0; w < kSortWarps; ++w) cursor[w * p.E + tid] += start + before;
+        if (rank == 0) {
+            p.offsets[tid] = start;
+            p.counts[tid] = count;
+            if (tid == p.E - 1) p.offsets[p.E] = start + padded;
+        }
+    }
+    __syncthreads();
+    for (int64_t g = first; g < last; g += 32) {
+        const int64_t i = g + lane;
+        const int e = i < last ? sort_load(p, i) : -1;
+        const unsigned peers = __match_any_sync(0xffffffffu, e);
+        const int ahead = __popc(peers & ((1u << lane) - 1));
+        int at = 0;
+        if (e >= 0) at = mine[e] + ahead;
+        __syncwarp();
+        if (e >= 0 && ahead == 0) mine[e] += __popc(peers);
+        __syncwarp();
+        if (i < last) p.position[i] = e >= 0 ? at : -1;
+    }
+    if (p.ctas > 1) ptx::cluster_sync();  // a CTA's totals are read until here
+}
+
+// ------------------------------------------------- rows of a token's experts
+struct RowParams {
+    const unsigned char *x;        // [T]: tokens' rows (gather), dy (combine's gradient)
+    const unsigned char *rows_in;  // [R]: experts' rows (combine and its gradient)
+    unsigned char *out;            // [R]: gather, drows; [T]: combine
+    const unsigned char *residual;
+    float *scale;                  // [R, ceil(H / 128)]: gather in e4m3
+    float *dw;                     // [T, k]
+    const int *position, *offsets, *counts;
+    const void *w;
+    int64_t x_ld, in_ld, out_ld, res_ld, w_ld;  // bytes; w_ld, scale_ld: elements
+    int64_t scale_ld, T, R, H;
+    int k, E, w_f32;
+};
+
+// Blocks of `x` index T .. T + E - 1 clear the rows between an expert's last and the next
+// one's first (there are some where the counts were rounded up), so that a product over
+// them adds nothing.
+__device__ __forceinline__ void clear_rows(const RowParams &p, int e, int64_t row_bytes, float scale) {
+    const int64_t a = max(int64_t{0}, static_cast<int64_t>(p.offsets[e]) + p.counts[e]);
+    const int64_t b = min(p.R, static_cast<int64_t>(p.offsets[e + 1]));
+    const int nthreads = blockDim.x * gridDim.y, tid = blockIdx.y * blockDim.x + threadIdx.x;
+    for (int64_t r = a; r < b; ++r) {
+        unsigned char *row = p.out + r * p.out_ld;
+        // (up to 15 bytes before the first 16-byte unit and after the last one by themselves)
+        const int64_t head = min(row_bytes, static_cast<int64_t>(
+                                                (16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15));
+        const int64_t units = (row_bytes - head) / 16;
+        if (tid < head) row[tid] = 0;
+        for (int64_t i = tid; i < units; i += nthreads)
+            reinterpret_cast<uint4 *>(row + head)[i] = make_uint4(0, 0, 0, 0);
+        const int64_t done = head + 16 * units;
+        if (tid < row_bytes - done) row[done + tid] = 0;
+        if (p.scale)
+            for (int64_t i = tid; i < p.scale_ld; i += nthreads) p.scale[r * p.scale_ld + i] = scale;
+    }
+}
+
+template <int DT, bool VEC, bool FP8>
+__global__ void __launch_bounds__(256) gather_kernel(const RowParams p) {
+    using C = blocks::Cols<VEC>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    const int64_t t = blockIdx.x;
+    if (t >= p.T) {
+        float inv;
+        const float zero = blocks::scale_of(0, inv);
+        clear_rows(p, static_cast<int>(t - p.T), p.H * (FP8 ? 1 : blocks::elt_bytes<DT>), zero);
+        return;
+    }
+    const int64_t base =
+        (static_cast<int64_t>(blockIdx.y) * (blockDim.x >> 5) + warp) * C::kWarp;
+    if (base >= p.H) return;
+    const C cols(base, lane);
+    const int *pos = p.position + t * p.k;
+    float v[C::N];
+    cols.template load<DT>(p.x + t * p.x_ld, p.H, v);
+    float scale = 0.f;
+    uint32_t q[2] = {};
+    if constexpr (FP8) {
+        uint32_t a = 0;
+#pragma unroll
+        for (int i = 0; i < C::N; ++i) a = max(a, blocks::magnitude(v[i]));
+        // a block is 16 lanes of eight columns, or a warp of four
+#pragma unroll
+        for (int d = VEC ? 8 : 16; d > 0; d /= 2) a = max(a, __shfl_xor_sync(0xffffffffu, a, d));
+        float inv;
+        scale = blocks::scale_of(a, inv);
+#pragma unroll
+        for (int i = 0; i < C::N; ++i) v[i] *= inv;
+#pragma unroll
+        for (int i = 0; i < C::N; i += 4)
+            q[i / 4] = blocks::pack_e4m3x4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    }
+    for (int j = 0; j < p.k; ++j) {
+        const int64_t r = pos[j];
+        if (r < 0 || r >= p.R) continue;
+        unsigned char *row = p.out + r * p.out_ld;
+        if constexpr (FP8) {
+            if constexpr (VEC) {
+                if (cols.c < p.H) *reinterpret_cast<uint2 *>(row + cols.c) = make_uint2(q[0], q[1]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (cols.in(i, p.H)) row[cols.c + 32 * i] = static_cast<unsigned char>(q[0] >> (8 * i));
+            }
+            if ((VEC ? lane & 15 : lane) == 0 && cols.c < p.H)
+                p.scale[r * p.scale_ld + cols.c / blocks::kBlock] = scale;
+        } else {
+            cols.template store<DT>(row, p.H, v);
+        }
+    }
+}
+
+constexpr int kAtOnce = 8;  // a token's rows that a thread has on their way together
+
+template <int DT>
+__device__ __forceinline__ float weight_of(const RowParams &p, int64_t t, int j) {
+    if (!p.w) return 1.f;
+    const int64_t i = t * p.w_ld + j;
+    if (p.w_f32) return static_cast<const float *>(p.w)[i];
+    return blocks::load1<DT>(static_cast<const unsigned char *>(p.w), i);
+}
+
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(256) combine_kernel(const RowParams p) {
+    using C = blocks::Cols<VEC>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    const int64_t t = blockIdx.x;
+    const int64_t base =
+        (static_cast<int64_t>(blockIdx.y) * (blockDim.x >> 5) + warp) * C::kWarp;
+    if (base >= p.H) return;
+    const C cols(base, lane);
+    const int *pos = p.position + t * p.k;
+    float y[C::N];
+#pragma unroll
+    for (int i = 0; i < C::N; ++i) y[i] = 0.f;
+    for (int j0 = 0; j0 < p.k; j0 += kAtOnce) {
+        float v[kAtOnce][C::N], w[kAtOnce];
+        bool held[kAtOnce];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            const int64_t r = j0 + j < p.k ? pos[j0 + j] : -1;
+            held[j] = r >= 0 && r < p.R;
+            if (held[j]) {
+                w[j] = weight_of<DT>(p, t, j0 + j);
+                cols.template load<DT>(p.rows_in + r * p.in_ld, p.H, v[j]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j)
+            if (held[j]) {
+#pragma unroll
+                for (int i = 0; i < C::N; ++i) y[i] = fmaf(w[j], v[j][i], y[i]);
+            }
+    }
+    if (p.residual) {
+        float r[C::N];
+        cols.template load<DT>(p.residual + t * p.res_ld, p.H, r);
+#pragma unroll
+        for (int i = 0; i < C::N; ++i) y[i] += r[i];
+    }
+    cols.template store<DT>(p.out + t * p.out_ld, p.H, y);
+}
+
+// A CTA has the whole row of a token: dw's sums stay in it, in an order of their own.
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(256) combine_bwd_kernel(const RowParams p) {
+    using C = blocks::Cols<VEC>;
+    const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __shared__ float part[8][kAtOnce];
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    const int64_t t = blockIdx.x;
+    if (t >= p.T) {
+        if (p.out)
+            clear_rows(p, static_cast<int>(t - p.T), p.H * blocks::elt_bytes<DT>, 0.f);
+        return;
+    }
+    const int *pos = p.position + t * p.k;
+    for (int j0 = 0; j0 < p.k; j0 += kAtOnce) {
+        int64_t r[kAtOnce];
+        float w[kAtOnce], sum[kAtOnce];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            r[j] = j0 + j < p.k ? pos[j0 + j] : -1;
+            if (r[j] >= p.R) r[j] = -1;
+            w[j] = r[j] >= 0 ? weight_of<DT>(p, t, j0 + j) : 0.f;
+            sum[j] = 0.f;
+        }
+        for (int64_t base = static_cast<int64_t>(warp) * C::kWarp; base < p.H;
+             base += static_cast<int64_t>(warps) * C::kWarp) {
+            const C cols(base, lane);
+            float d[C::N];
+            cols.template load<DT>(p.x + t * p.x_ld, p.H, d);
+            if (p.dw) {
+                float v[kAtOnce][C::N];
+#pragma unroll
+                for (int j = 0; j < kAtOnce; ++j)
+                    if (r[j] >= 0) cols.template load<DT>(p.rows_in + r[j] * p.in_ld, p.H, v[j]);
+#pragma unroll
+                for (int j = 0; j < kAtOnce; ++j)
+                    if (r[j] >= 0) {
+#pragma unroll
+                        for (int i = 0; i < C::N; ++i) sum[j] = fmaf(d[i], v[j][i], sum[j]);
+                    }
+            }
+            if (p.out) {
+#pragma unroll
+                for (int j = 0; j < kAtOnce; ++j)
+                    if (r[j] >= 0) {
+                        float o[C::N];
+#pragma unroll
+                        for (int i = 0; i < C::N; ++i) o[i] = w[j] * d[i];
+                        cols.template store<DT>(p.out + r[j] * p.out_ld, p.H, o);
+                    }
+            }
+        }
+        if (p.dw) {
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+#pragma unroll
+                for (int s = 16; s > 0; s /= 2) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], s);
+                if (lane == 0) part[warp][j] = sum[j];
+            }
+            __syncthreads();
+            if (threadIdx.x < kAtOnce && j0 + static_cast<int>(threadIdx.x) < p.k) {
+                float a = 0.f;
+                for (int i = 0; i < warps; ++i) a += part[i][threadIdx.x];
+                p.dw[t * p.k + j0 + threadIdx.x] = a;
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// ------------------------------------------------------------------- host
+using RowKernel = void (*)(const RowParams);
+
+template <class P>
+cudaError_t launch(void (*k)(const P), dim3 grid, int threads, size_t smem, unsigned ctas,
+                   cudaStream_t s, const P &p) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = ctas > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, k, p);
+}
+
+template <bool VEC, bool FP8>
+RowKernel gather_of(int dt) {
+    switch (dt) {
+        case VLMCE_F32: return gather_kernel<VLMCE_F32, VEC, FP8>;
+        case VLMCE_F16: return gather_kernel<VLMCE_F16, VEC, FP8>;
+        default: return gather_kernel<VLMCE_BF16, VEC, FP8>;
+    }
+}
+template <bool VEC>
+RowKernel combine_of(int dt, bool bwd) {
+    switch (dt) {
+        case VLMCE_F32: return bwd ? combine_bwd_kernel<VLMCE_F32, VEC> : combine_kernel<VLMCE_F32, VEC>;
+        case VLMCE_F16: return bwd ? combine_bwd_kernel<VLMCE_F16, VEC> : combine_kernel<VLMCE_F16, VEC>;
+        default: return bwd ? combine_bwd_kernel<VLMCE_BF16, VEC> : combine_kernel<VLMCE_BF16, VEC>;
+    }
+}
+
+constexpr int64_t kMaxH = int64_t(1) << 24;
+
+bool dtype_ok(int32_t dt) { return dt == VLMCE_F32 || dt == VLMCE_BF16 || dt == VLMCE_F16; }
+int elt_of(int32_t dt) { return dt == VLMCE_F32 ? 4 : 2; }
+
+// T tokens of k experts of E, rounded up to `align`: whether sort takes it.
+vlmce_status order_ok(int64_t T, int64_t k, int64_t E) {
+    if (T < 0 || k < 1 || E < 1) return VLMCE_ERR_INVALID_ARG;
+    if (k > VLMCE_MOE_MAX_TOPK || E > kMaxExperts || T > INT32_MAX / k) return VLMCE_ERR_TOO_LARGE;
+    return VLMCE_OK;
+}
+int64_t capacity(int64_t T, int64_t k, int64_t E, int64_t align) {
+    return (T * k + std::min(E, T * k) * (align - 1)) / align * align;
+}
+
+// A matrix argument: rows of `bytes` bytes.
+struct Mat {
+    const void *p;
+    int64_t rows, cols, ld;
+    int elt;
+    bool aligned16() const { return aligned(p, 16) && ld * elt % 16 == 0; }
+};
+vlmce_status check(const Mat &m) {
+    if (m.ld < m.cols || (m.rows > 0 && !m.p)) return VLMCE_ERR_INVALID_ARG;
+    if (m.ld > (int64_t(1) << 60) / m.elt / std::max<int64_t>(m.rows, 1)) return VLMCE_ERR_TOO_LARGE;
+    if (!aligned(m.p, static_cast<uintptr_t>(m.elt))) return VLMCE_ERR_MISALIGNED;
+    return VLMCE_OK;
+}
+bool overlap(const Mat &a, const Mat &b) {
+    return rows_overlap({a.p, a.rows, a.cols * a.elt, a.ld * a.elt},
+                        {b.p, b.rows, b.cols * b.elt, b.ld * b.elt});
+}
+
+// Threads of a CTA and CTAs of a row: warps of `per` columns, eight of them at most.
+int threads_of(int64_t H, int per) {
+    return static_cast<int>(32 * std::min<int64_t>(8, (H + per - 1) / per));
+}
+unsigned row_ctas(int64_t H, int per, int threads) {
+    const int64_t cols = static_cast<int64_t>(threads / 32) * per;
+    return static_cast<unsigned>((H + cols - 1) / cols);
+}
+
+vlmce_status common(int64_t T, int64_t R, int64_t H, int64_t k, int64_t E, const int32_t *position,
+                    const int32_t *offsets, const int32_t *counts) {
+    const vlmce_status st = order_ok(T, k, E);
+    if (st != VLMCE_OK) return st;
+    if (R < 0 || H < 1 || (T > 0 && !position) || !offsets || !counts) return VLMCE_ERR_INVALID_ARG;
+    if (R > INT32_MAX || H > kMaxH || T + E > INT32_MAX) return VLMCE_ERR_TOO_LARGE;
+    if (!aligned(position, 4) || !aligned(offsets, 4) || !aligned(counts, 4))
+        return VLMCE_ERR_MISALIGNED;
+    return VLMCE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+}  // namespace vlmce
+
+extern "C" int64_t vlmce_moe_rows(int64_t T, int64_t k, int64_t E, int64_t align) {
+    using namespace vlmce::moe;
+    if (order_ok(T, k, E) != VLMCE_OK || align < 1 || align > INT32_MAX) return -1;
+    const int64_t used = std::min(E, T * k);
+    if (used > 0 && align > (INT32_MAX - T * k) / used) return -1;
+    return capacity(T, k, E, align);
+}
+
+extern "C" vlmce_status moe_sort(const void *experts, int64_t experts_stride, int32_t wide,
+                                 int64_t T, int64_t k, int64_t E, int64_t align, int32_t *position,
+                                 int32_t *offsets, int32_t *counts, vlmce_stream_t stream) {
+    using namespace vlmce;
+    using namespace vlmce::moe;
+    vlmce_status st = order_ok(T, k, E);
+    if (st != VLMCE_OK) return st;
+    if (align < 1 || experts_stride < k || !offsets || !counts || (T > 0 && (!experts || !position)))
+        return VLMCE_ERR_INVALID_ARG;
+    if (vlmce_moe_rows(T, k, E, align) < 0 || experts_stride > (int64_t(1) << 56) / std::max<int64_t>(T, 1))
+        return VLMCE_ERR_TOO_LARGE;
+    if (!aligned(experts, wide ? 8 : 4) || !aligned(position, 4) || !aligned(offsets, 4) ||
+        !aligned(counts, 4))
+        return VLMCE_ERR_MISALIGNED;
+    const Mat in{experts, T, k, experts_stride, wide ? 8 : 4}, pos{position, T, k, k, 4},
+        off{offsets, 1, E + 1, E + 1, 4}, cnt{counts, 1, E, E, 4};
+    if (overlap(pos, in) || overlap(off, in) || overlap(cnt, in) || overlap(pos, off) ||
+        overlap(pos, cnt) || overlap(off, cnt))
+        return VLMCE_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    st = current_device(&dev);
+    if (st != VLMCE_OK) return st;
+    static std::mutex mu;
+    static bool opted[64] = {};
+    cudaError_t e = cudaSuccess;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!opted[dev.device]) {
+            e = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kSortWarps * kMaxExperts * 4);
+            opted[dev.device] = e == cudaSuccess;
+        }
+    }
+    if (e != cudaSuccess) return launch_status(e, "moe_sort");
+    SortParams p = {};
+    p.experts = experts;
+    p.ld = experts_stride;
+    p.pairs = T * k;
+    p.k = static_cast<int>(k);
+    p.E = static_cast<int>(E);
+    p.align = static_cast<int>(align);
+    p.wide = wide != 0;
+    p.position = position;
+    p.offsets = offsets;
+    p.counts = counts;
+    p.ctas = 1;
+    while (p.ctas < kMaxSortCtas && p.pairs > p.ctas * int64_t{2 * kSortThreads}) p.ctas *= 2;
+    e = launch(sort_kernel, dim3(static_cast<unsigned>(p.ctas), 1, 1), kSortThreads,
+               static_cast<size_t>(kSortWarps * E * 4), static_cast<unsigned>(p.ctas),
+               reinterpret_cast<cudaStream_t>(stream), p);
+    return launch_status(e, "moe_sort");
+}
+
+extern "C" vlmce_status moe_gather(const void *x, int64_t x_stride, int32_t dtype,
+                                   const int32_t *position, const int32_t *offsets,
+                                   const int32_t *counts, int64_t T, int64_t k, int64_t E,
+                                   int64_t R, int64_t H, void *rows, int64_t rows_stride,
+                                   int32_t rows_dtype, float *scale, vlmce_stream_t stream) {
+    using namespace vlmce;
+    using namespace vlmce::moe;
+    if (!dtype_ok(dtype) || (rows_dtype != dtype && rows_dtype != VLMCE_E4M3))
+        return VLMCE_ERR_UNSUPPORTED_DTYPE;
+    const bool fp8 = rows_dtype == VLMCE_E4M3;
+    vlmce_status st = common(T, R, H, k, E, position, offsets, counts);
+    if (st != VLMCE_OK) return st;
+    const int64_t nb = (H + blocks::kBlock - 1) / blocks::kBlock;
+    const Mat in{x, T, H, x_stride, elt_of(dtype)}, out{rows, R, H, rows_stride, fp8 ? 1 : elt_of(dtype)},
+        sc{scale, fp8 ? R : 0, nb, nb, 4}, pos{position, T, k, k, 4};
+    if (!fp8 && scale) return VLMCE_ERR_INVALID_ARG;
+    st = check(in);
+    if (st == VLMCE_OK) st = check(out);
+    if (st == VLMCE_OK) st = check(sc);
+    if (st != VLMCE_OK) return st;
+    if (overlap(out, in) || overlap(sc, in) || overlap(out, sc) || overlap(out, pos) || overlap(sc, pos))
+        return VLMCE_ERR_INVALID_ARG;
+    if (R == 0) return VLMCE_OK;
+    DeviceInfo dev;
+    st = current_device(&dev);
+    if (st != VLMCE_OK) return st;
+    const bool vec = H % 8 == 0 && in.aligned16() && aligned(rows, fp8 ? 8 : 16) &&
+                     rows_stride * out.elt % (fp8 ? 8 : 16) == 0;
+    RowParams p = {};
+    p.x = static_cast<const unsigned char *>(x);
+    p.x_ld = x_stride * in.elt;
+    p.out = static_cast<unsigned char *>(rows);
+    p.out_ld = rows_stride * out.elt;
+    p.scale = scale;
+    p.scale_ld = nb;
+    p.position = position;
+    p.offsets = offsets;
+    p.counts = counts;
+    p.T = T;
+    p.R = R;
+    p.H = H;
+    p.k = static_cast<int>(k);
+    p.E = static_cast<int>(E);
+    const RowKernel kern = vec ? (fp8 ? gather_of<true, true>(dtype) : gather_of<true, false>(dtype))
+                               : (fp8 ? gather_of<false, true>(dtype) : gather_of<false, false>(dtype));
+    const int per = vec ? 256 : 128, threads = threads_of(H, per);
+    return launch_status(launch(kern, dim3(static_cast<unsigned>(T + E), row_ctas(H, per, threads), 1),
+                                threads, 0, 1, reinterpret_cast<cudaStream_t>(stream), p),
+                         "moe_gather");
+}
+
+extern "C" vlmce_status moe_combine(const void *rows, int64_t rows_stride, int32_t dtype,
+                                    const int32_t *position, const void *weights,
+                                    int64_t weights_stride, int32_t weights_dtype,
+                                    const void *residual, int64_t residual_stride, int64_t T,
+                                    int64_t k, int64_t R, int64_t H, void *y, int64_t y_stride,
+                                    vlmce_stream_t stream) {
+    using namespace vlmce;
+    using namespace vlmce::moe;
+    if (!dtype_ok(dtype) || (weights && weights_dtype != VLMCE_F32 && weights_dtype != dtype))
+        return VLMCE_ERR_UNSUPPORTED_DTYPE;
+    const int32_t none = 0;
+    vlmce_status st = common(T, R, H, k, 1, position, &none, &none);
+    if (st != VLMCE_OK) return st;
+    const int elt = elt_of(dtype), welt = elt_of(weights_dtype);
+    const Mat in{rows, R, H, rows_stride, elt}, out{y, T, H, y_stride, elt},
+        res{residual, residual ? T : 0, H, residual_stride, elt}, pos{position, T, k, k, 4},
+        w{weights, weights ? T : 0, k, weights_stride, welt};
+    st = check(in);
+    if (st == VLMCE_OK) st = check(out);
+    if (st == VLMCE_OK && residual) st = check(res);
+    if (st == VLMCE_OK && weights) st = check(w);
+    if (st != VLMCE_OK) return st;
+    if (overlap(out, in) || overlap(out, w) || overlap(out, pos) ||
+        (overlap(out, res) && !(y == residual && (y_stride == residual_stride || T <= 1))))
+        return VLMCE_ERR_INVALID_ARG;
+    if (T == 0) return VLMCE_OK;
+    DeviceInfo dev;
+    st = current_device(&dev);
+    if (st != VLMCE_OK) return st;
+    const bool vec = H % 8 == 0 && in.aligned16() && out.aligned16() && (!residual || res.aligned16());
+    RowParams p = {};
+    p.rows_in = static_cast<const unsigned char *>(rows);
+    p.in_ld = rows_stride * elt;
+    p.out = static_cast<unsigned char *>(y);
+    p.out_ld = y_stride * elt;
+    p.residual = static_cast<const unsigned char *>(residual);
+    p.res_ld = residual_stride * elt;
+    p.position = position;
+    p.w = weights;
+    p.w_ld = weights_stride;
+    p.w_f32 = weights_dtype == VLMCE_F32;
+    p.T = T;
+    p.R = R;
+    p.H = H;
+    p.k = static_cast<int>(k);
+    const int per = vec ? 256 : 128, threads = threads_of(H, per);
+    return launch_status(
+        launch(vec ? combine_of<true>(dtype, false) : combine_of<false>(dtype, false),
+               dim3(static_cast<unsigned>(T), row_ctas(H, per, threads), 1), threads, 0, 1,
+               reinterpret_cast<cudaStream_t>(stream), p),
+        "moe_combine");
+}
+
+extern "C" vlmce_status moe_combine_bwd(const void *dy, int64_t dy_stride, const void *rows,
+                                        int64_t rows_stride, int32_t dtype, const int32_t *position,
+                                        const int32_t *offsets, const int32_t *counts,
+                                        const void *weights, int64_t weights_stride,
+                                        int32_t weights_dtype, int64_t T, int64_t k, int64_t E,
+                                        int64_t R, int64_t H, void *drows, int64_t drows_stride,
+                                        float *dweights, vlmce_stream_t stream) {
+    using namespace vlmce;
+    using namespace vlmce::moe;
+    if (!dtype_ok(dtype) || (weights && weights_dtype != VLMCE_F32 && weights_dtype != dtype))
+        return VLMCE_ERR_UNSUPPORTED_DTYPE;
+    vlmce_status st = common(T, R, H, k, E, position, offsets, counts);
+    if (st != VLMCE_OK) return st;
+    if (!drows && !dweights && T > 0) return VLMCE_ERR_INVALID_ARG;
+    const int elt = elt_of(dtype), welt = elt_of(weights_dtype);
+    const Mat d{dy, T, H, dy_stride, elt}, in{rows, dweights ? R : 0, H, rows_stride, elt},
+        out{drows, drows ? R : 0, H, drows_stride, elt}, w{weights, weights ? T : 0, k, weights_stride, welt},
+        dw{dweights, dweights ? T : 0, k, k, 4}, pos{position, T, k, k, 4};
+    st = check(d);
+    if (st == VLMCE_OK && dweights) st = check(in);
+    if (st == VLMCE_OK && drows) st = check(out);
+    if (st == VLMCE_OK && weights) st = check(w);
+    if (st == VLMCE_OK && dweights) st = check(dw);
+    if (st != VLMCE_OK) return st;
+    if (overlap(out, d) || overlap(out, in) || overlap(out, w) || overlap(out, dw) || overlap(out, pos) ||
+        overlap(dw, d) || overlap(dw, in) || overlap(dw, w) || overlap(dw, pos))
+        return VLMCE_ERR_INVALID_ARG;
+    if (T == 0) return VLMCE_OK;
+    DeviceInfo dev;
+    st = current_device(&dev);
+    if (st != VLMCE_OK) return st;
+    const bool vec = H % 8 == 0 && d.aligned16() && (!dweights || in.aligned16()) && (!drows || out.aligned16());
+    RowParams p = {};
+    p.x = static_cast<const unsigned char *>(dy);
+    p.x_ld = dy_stride * elt;
+    p.rows_in = static_cast<const unsigned char *>(rows);
+    p.in_ld = rows_stride * elt;
+    p.out = static_cast<unsigned char *>(drows);
+    p.out_ld = drows_stride * elt;
+    p.dw = dweights;
+    p.position = position;
+    p.offsets = offsets;
+    p.counts = counts;
+    p.w = weights;
+    p.w_ld = weights_stride;
+    p.w_f32 = weights_dtype == VLMCE_F32;
+    p.T = T;
+    p.R = R;
+    p.H = H;
+    p.k = static_cast<int>(k);
+    p.E = static_cast<int>(E);
+    const int per = vec ? 256 : 128;
+    return launch_status(launch(vec ? combine_of<true>(dtype, true) : combine_of<false>(dtype, true),
+                                dim3(static_cast<unsigned>(T + E), 1, 1), threads_of(H, per), 0, 1,
+                                reinterpret_cast<cudaStream_t>(stream), p),
+                         "moe_combine_bwd");
+}

@@ -1,0 +1,273 @@
+// quant.cu -- e4m3 with one scale per block of 128 (blocks.cuh): of a row's 128
+// columns, of a column's 128 rows (the result transposed), or of 128 x 128.
+//
+// A product of block-scaled operands sums over columns, so the same matrix is wanted
+// along its rows (the forward product) and along its columns, transposed (the gradients
+// of the weights, and of the inputs by the transposed weight).  Both come from one
+// reading: a CTA has a tile of 128 x 128 in registers, a thread eight rows of eight
+// columns.  A row's maximum is found among the 16 lanes that share it, a column's in
+// shared memory (integer maxima: no order in the result).  For the transposed form a
+// thread's eight rows of a column are one 8-byte store into shared memory, the 8-byte
+// units of a column swizzled by its group of eight columns (16 lanes then meet 32
+// different banks), and leave from there as whole 128-byte lines.
+//
+// Bound by memory.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+
+#include "blocks.cuh"
+#include "host_util.h"
+#include "ptx.cuh"
+#include "rows_host.h"
+#include "vlmce.h"
+
+namespace vlmce {
+namespace quant {
+namespace {
+
+constexpr int kB = blocks::kBlock;
+constexpr int kThreads = 256;
+
+struct Params {
+    const unsigned char *x;
+    unsigned char *q, *qt;
+    float *scale, *scale_t;
+    int64_t x_ld, x_batch;        // bytes
+    int64_t q_ld, q_batch, qt_ld, qt_batch;
+    int64_t R, C;
+    int rt, ct;                   // tiles down and across
+    int square;
+};
+
+template <int DT, bool VEC, bool ROWS, bool TRANS>
+__global__ void __launch_bounds__(kThreads) quant_kernel(const Params p) {
+    constexpr int kWarps = kThreads / 32;
+    __shared__ uint32_t col_max[kB];
+    __shared__ uint32_t tile_max[kWarps];
+    __shared__ __align__(16) unsigned char tq[TRANS ? kB * kB : 16];
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int cg = tid & 15, rg = tid >> 4;  // eight columns, eight rows of the tile
+    const int64_t tile = blockIdx.x;
+    const int64_t b = tile / (static_cast<int64_t>(p.rt) * p.ct);
+    const int in_b = static_cast<int>(tile - b * p.rt * p.ct);
+    const int tr = in_b / p.ct, tc = in_b - tr * p.ct;
+    const int64_t r0 = static_cast<int64_t>(tr) * kB + 8 * rg, c0 = static_cast<int64_t>(tc) * kB + 8 * cg;
+    if (TRANS && tid < kB) col_max[tid] = 0;
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    const unsigned char *x = p.x + b * p.x_batch + r0 * p.x_ld;
+    float v[8][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const bool row = r0 + i < p.R;
+        if constexpr (VEC) {
+            if (row && c0 < p.C) {
+                blocks::load8<DT>(x + i * p.x_ld, c0, v[i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[i][j] = row && c0 + j < p.C ? blocks::load1<DT>(x + i * p.x_ld, c0 + j) : 0.f;
+        }
+    }
+    if (p.square) {
+        uint32_t a = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) a = max(a, blocks::magnitude(v[i][j]));
+        a = __reduce_max_sync(0xffffffffu, a);
+        if (lane == 0) tile_max[tid >> 5] = a;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) a = max(a, tile_max[w]);
+        float inv;
+        const float scale = blocks::scale_of(a, inv);
+        if (tid == 0) {
+            if (ROWS) p.scale[(b * p.rt + tr) * p.ct + tc] = scale;
+            if (TRANS) p.scale_t[(b * p.ct + tc) * p.rt + tr] = scale;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] *= inv;
+    } else if (TRANS) {
+        __syncthreads();  // col_max is clear
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            uint32_t a = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) a = max(a, blocks::magnitude(v[i][j]));
+            a = max(a, __shfl_xor_sync(0xffffffffu, a, 16));  // the warp's other eight rows
+            if (lane < 16) atomicMax(col_max + 8 * cg + j, a);
+        }
+    }
+    if constexpr (ROWS) {
+        unsigned char *q = p.q + b * p.q_batch + r0 * p.q_ld;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float inv = 1.f;
+            if (!p.square) {
+                uint32_t a = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) a = max(a, blocks::magnitude(v[i][j]));
+#pragma unroll
+                for (int d = 8; d > 0; d /= 2) a = max(a, __shfl_xor_sync(0xffffffffu, a, d));
+                const float scale = blocks::scale_of(a, inv);
+                if (cg == 0 && r0 + i < p.R) p.scale[(b * p.R + r0 + i) * p.ct + tc] = scale;
+            }
+            const uint32_t lo = blocks::pack_e4m3x4(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv);
+            const uint32_t hi = blocks::pack_e4m3x4(v[i][4] * inv, v[i][5] * inv, v[i][6] * inv, v[i][7] * inv);
+            if (r0 + i < p.R) {
+                unsigned char *row = q + i * p.q_ld;
+                if (VEC) {
+                    if (c0 < p.C) *reinterpret_cast<uint2 *>(row + c0) = make_uint2(lo, hi);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (c0 + j < p.C)
+                            row[c0 + j] = static_cast<unsigned char>((j < 4 ? lo : hi) >> (8 * (j & 3)));
+                }
+            }
+        }
+    }
+    if constexpr (TRANS) {
+        __syncthreads();  // col_max is complete
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float inv = 1.f;
+            if (!p.square) {
+                const float scale = blocks::scale_of(col_max[8 * cg + j], inv);
+                if (rg == 0 && c0 + j < p.C) p.scale_t[(b * p.C + c0 + j) * p.rt + tr] = scale;
+            }
+            const uint32_t lo = blocks::pack_e4m3x4(v[0][j] * inv, v[1][j] * inv, v[2][j] * inv, v[3][j] * inv);
+            const uint32_t hi = blocks::pack_e4m3x4(v[4][j] * inv, v[5][j] * inv, v[6][j] * inv, v[7][j] * inv);
+            *reinterpret_cast<uint2 *>(tq + (8 * cg + j) * kB + 8 * (rg ^ cg)) = make_uint2(lo, hi);
+        }
+        __syncthreads();
+        // 16 rows a thread, eight threads a column
+        const int64_t rows0 = static_cast<int64_t>(tr) * kB;
+#pragma unroll
+        for (int i = 0; i < kB * kB / 16 / kThreads; ++i) {
+            const int at = i * kThreads + tid, c = at >> 3, u = at & 7;
+            const int64_t col = static_cast<int64_t>(tc) * kB + c, r = rows0 + 16 * u;
+            if (col >= p.C || r >= p.R) continue;
+            const uint2 lo = *reinterpret_cast<const uint2 *>(tq + c * kB + 8 * ((2 * u) ^ (c >> 3)));
+            const uint2 hi = *reinterpret_cast<const uint2 *>(tq + c * kB + 8 * ((2 * u + 1) ^ (c >> 3)));
+            unsigned char *to = p.qt + b * p.qt_batch + col * p.qt_ld + r;
+            if (r + 16 <= p.R && (reinterpret_cast<uintptr_t>(to) & 15) == 0) {
+                *reinterpret_cast<uint4 *>(to) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            } else {
+                const uint32_t w[4] = {lo.x, lo.y, hi.x, hi.y};
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    if (r + k < p.R) to[k] = static_cast<unsigned char>(w[k / 4] >> (8 * (k & 3)));
+            }
+        }
+    }
+}
+
+using Kernel = void (*)(const Params);
+template <int DT, bool VEC>
+Kernel kernel_of(bool rows, bool trans) {
+    if (!trans) return quant_kernel<DT, VEC, true, false>;
+    return rows ? quant_kernel<DT, VEC, true, true> : quant_kernel<DT, VEC, false, true>;
+}
+Kernel kernel_of(int dt, bool vec, bool rows, bool trans) {
+    switch (dt) {
+        case VLMCE_F32:
+            return vec ? kernel_of<VLMCE_F32, true>(rows, trans) : kernel_of<VLMCE_F32, false>(rows, trans);
+        case VLMCE_F16:
+            return vec ? kernel_of<VLMCE_F16, true>(rows, trans) : kernel_of<VLMCE_F16, false>(rows, trans);
+        default:
+            return vec ? kernel_of<VLMCE_BF16, true>(rows, trans) : kernel_of<VLMCE_BF16, false>(rows, trans);
+    }
+}
+
+}  // namespace
+}  // namespace quant
+}  // namespace vlmce
+
+extern "C" vlmce_status quantize_blocks(const void *x, int32_t dtype, int64_t batch, int64_t R,
+                                        int64_t C, int64_t x_stride, int64_t x_batch_stride,
+                                        int32_t square, void *q, int64_t q_stride, float *scale,
+                                        void *qt, int64_t qt_stride, float *scale_t,
+                                        vlmce_stream_t stream) {
+    using namespace vlmce;
+    using namespace vlmce::quant;
+    if (dtype != VLMCE_F32 && dtype != VLMCE_BF16 && dtype != VLMCE_F16)
+        return VLMCE_ERR_UNSUPPORTED_DTYPE;
+    const int elt = dtype == VLMCE_F32 ? 4 : 2;
+    if (batch < 0 || R < 0 || C < 1 || x_stride < C || (!q && !qt) || (q && q_stride < C) ||
+        (qt && qt_stride < R) || (q != nullptr) != (scale != nullptr) ||
+        (qt != nullptr) != (scale_t != nullptr))
+        return VLMCE_ERR_INVALID_ARG;
+    if (batch == 0 || R == 0) return VLMCE_OK;
+    if (!x || (batch > 1 && x_batch_stride < (R - 1) * x_stride + C)) return VLMCE_ERR_INVALID_ARG;
+    constexpr int64_t kMax = int64_t(1) << 40;  // elements a stride may span
+    if (R > INT32_MAX || C > INT32_MAX || batch > INT32_MAX || x_stride > kMax / R ||
+        q_stride > kMax / R || qt_stride > kMax / C || x_batch_stride > kMax / batch ||
+        (q && R * q_stride > kMax / batch) || (qt && C * qt_stride > kMax / batch))
+        return VLMCE_ERR_TOO_LARGE;
+    const int64_t rt = (R + kB - 1) / kB, ct = (C + kB - 1) / kB;
+    if (rt * ct > INT32_MAX / batch) return VLMCE_ERR_TOO_LARGE;
+    if (!aligned(x, static_cast<uintptr_t>(elt)) || !aligned(scale, 4) || !aligned(scale_t, 4))
+        return VLMCE_ERR_MISALIGNED;
+    // the matrices as one run of memory each
+    struct Span {
+        const void *p;
+        int64_t bytes;
+    };
+    const Span in{x, ((batch - 1) * x_batch_stride + (R - 1) * x_stride + C) * elt};
+    const int64_t blocks_of = batch * (square ? rt * ct : R * ct), blocks_t = batch * (square ? rt * ct : C * rt);
+    const Span out[4] = {{q, batch * R * q_stride - (q_stride - C)}, {scale, 4 * blocks_of},
+                         {qt, batch * C * qt_stride - (qt_stride - R)}, {scale_t, 4 * blocks_t}};
+    auto meet = [](const Span &a, const Span &b) {
+        return rows_overlap({a.p, 1, a.bytes, a.bytes}, {b.p, 1, b.bytes, b.bytes});
+    };
+    for (int i = 0; i < 4; ++i) {
+        if (meet(out[i], in)) return VLMCE_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (meet(out[i], out[j])) return VLMCE_ERR_INVALID_ARG;
+    }
+    DeviceInfo dev;
+    const vlmce_status st = current_device(&dev);
+    if (st != VLMCE_OK) return st;
+    Params p = {};
+    p.x = static_cast<const unsigned char *>(x);
+    p.q = static_cast<unsigned char *>(q);
+    p.qt = static_cast<unsigned char *>(qt);
+    p.scale = scale;
+    p.scale_t = scale_t;
+    p.x_ld = x_stride * elt;
+    p.x_batch = batch > 1 ? x_batch_stride * elt : 0;
+    p.q_ld = q_stride;
+    p.q_batch = R * q_stride;
+    p.qt_ld = qt_stride;
+    p.qt_batch = C * qt_stride;
+    p.R = R;
+    p.C = C;
+    p.rt = static_cast<int>(rt);
+    p.ct = static_cast<int>(ct);
+    p.square = square != 0;
+    const bool vec = C % 8 == 0 && aligned(x, 16) && p.x_ld % 16 == 0 && p.x_batch % 16 == 0 &&
+                     (!q || (aligned(q, 8) && q_stride % 8 == 0));
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(batch * rt * ct), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return launch_status(
+        cudaLaunchKernelEx(&cfg, kernel_of(dtype, vec, q != nullptr, qt != nullptr),
+                           static_cast<const Params>(p)),
+        "quantize_blocks");
+}
