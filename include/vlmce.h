@@ -79,10 +79,11 @@ typedef enum { VLMCE_NONE = 0, VLMCE_MEAN = 1, VLMCE_SUM = 2 } vlmce_reduction;
 /* Errors the kernels detected on the device: bits of out_counts[3], of a call's
  * dev_err, and of vlmce_take_device_errors. */
 #define VLMCE_DEVERR_TIMEOUT 1 /* an on-chip wait gave up; results are invalid */
+#define VLMCE_DEVERR_OFFSETS 2 /* offsets that block_linear_* cannot take: all experts empty */
 
 /* vlmce_take_device_errors -- the VLMCE_DEVERR_* bits left on the current device by
- * calls without an error word of their own (linear_* and glu_* with dev_err NULL,
- * vlmce_gemm*) since the last call of this function.  Enqueued on `stream`: *out
+ * calls without an error word of their own (linear_*, glu_* and block_linear_* with
+ * dev_err NULL, vlmce_gemm*) since the last call of this function.  Enqueued on `stream`: *out
  * (device int32) receives the bits, which are cleared.  Calls on other streams count
  * once their kernels have run. */
 vlmce_status vlmce_take_device_errors(int32_t *out, vlmce_stream_t stream);
@@ -596,6 +597,74 @@ vlmce_status quantize_blocks(const void *x, int32_t dtype, int64_t batch, int64_
                              int64_t x_stride, int64_t x_batch_stride, int32_t square, void *q,
                              int64_t q_stride, float *scale, void *qt, int64_t qt_stride,
                              float *scale_t, vlmce_stream_t stream);
+
+/*
+ * block_linear_fwd -- product of VLMCE_E4M3 operands with one scale per block of 128 of K
+ * (quantize_blocks, moe_gather), dense or by experts:
+ *   y[t, n] = sum_b x_scale[t, b] weight_scale[n', b] sum_{k in b} x[t, k] weight[e, n, k]
+ *             + residual[t, n]
+ * on tcgen05 tensor cores; a block's sum is theirs, the scales and the sum over the blocks
+ * are in fp32, and each output is rounded once.
+ *
+ * x               [T, x_stride >= K]; x_scale fp32 [T, x_scale_stride >= ceil(K / 128)].
+ * weight          [E N, weight_stride >= K]: the rows of E matrices, one after the other.
+ *                 Strides of x and weight are multiples of 16, both 16-byte aligned.
+ * weight_block    128: one scale for 128 rows of a matrix (n' = n / 128), weight_scale
+ *                 fp32 [E ceil(N / 128), weight_scale_stride]; or 1: for each row (n' = n),
+ *                 [E N, weight_scale_stride].
+ * offsets         int32 [E + 1]: rows offsets[e] .. offsets[e + 1] - 1 of x meet matrix e,
+ *                 0 <= offsets[e] <= offsets[e + 1] <= T; rows of y before the first and
+ *                 from the last on are left as they are.  With other values nothing is
+ *                 computed, and dev_err receives VLMCE_DEVERR_OFFSETS.  NULL (E = 1): all
+ *                 rows.
+ * residual        [T, residual_stride >= N] of out_dtype, or NULL; it may be y itself.
+ * y               [T, y_stride >= N] of out_dtype (VLMCE_BF16 or VLMCE_F16).
+ * dev_err         as linear_fwd.
+ * 1 <= E <= VLMCE_MOE_MAX_EXPERTS.  The gradient of x is the same product of dy with the
+ * transposed matrices (quantize_blocks: qt of a square quantisation).
+ * Outputs overlap nothing but what is said above.  Deterministic.
+ */
+vlmce_status block_linear_fwd(const void *x, int64_t x_stride, const float *x_scale,
+                              int64_t x_scale_stride, const void *weight, int64_t weight_stride,
+                              const float *weight_scale, int64_t weight_scale_stride,
+                              int32_t weight_block, const int32_t *offsets, int64_t E,
+                              const void *residual, int64_t residual_stride, int32_t out_dtype,
+                              int64_t T, int64_t N, int64_t K, void *y, int64_t y_stride,
+                              int32_t *dev_err, vlmce_stream_t stream);
+
+/*
+ * block_linear_dweight -- gradient of block_linear_fwd's weight from the transposed
+ * operands, blocks of 128 along their rows (qt of quantize_blocks):
+ *   dweight[e, n, k] = sum_b dyt_scale[n, b] xt_scale[k, b] sum_{r in b} dyt[n, r] xt[k, r]
+ * over the blocks b of columns offsets[e] .. offsets[e + 1] - 1.
+ *
+ * dyt, xt         [N, dyt_stride >= R] and [K, xt_stride >= R], strides multiples of 16,
+ *                 16-byte aligned; dyt_scale, xt_scale fp32 [N or K, stride >= ceil(R / 128)].
+ * offsets         int32 [E + 1] as block_linear_fwd's, within R, multiples of 128 (or R):
+ *                 moe_sort with align = 128, whose rows in between moe_gather and
+ *                 moe_combine_bwd make zero.  With other values dweight is set to zero
+ *                 (accumulate: left as it is).  NULL (E = 1): all columns.
+ * dweight         [E, N, K] contiguous of dweight_dtype (VLMCE_F32, VLMCE_BF16 or VLMCE_F16).
+ * accumulate      != 0: dweight (then fp32) is added to instead of overwritten.
+ * dev_err         as linear_fwd.  Deterministic.
+ */
+vlmce_status block_linear_dweight(const void *dyt, int64_t dyt_stride, const float *dyt_scale,
+                                  int64_t dyt_scale_stride, const void *xt, int64_t xt_stride,
+                                  const float *xt_scale, int64_t xt_scale_stride,
+                                  const int32_t *offsets, int64_t E, int64_t R, int64_t N, int64_t K,
+                                  void *dweight, int32_t dweight_dtype, int32_t accumulate,
+                                  int32_t *dev_err, vlmce_stream_t stream);
+
+/*
+ * vlmce_block_linear_describe_plan -- how block_linear_fwd runs T rows (grouped != 0: of E
+ * experts) with N outputs and K inputs on the current device:
+ *   out[0]  0: CTA pairs on tiles of 256 x 256, 1: single CTAs on 128 outputs x few rows
+ *   out[1]  rows of a tile
+ *   out[2]  CTAs that share a tile's K
+ *   out[3]  blocks of K in a stage
+ */
+vlmce_status vlmce_block_linear_describe_plan(int64_t T, int64_t N, int64_t K, int64_t E,
+                                              int32_t grouped, int32_t *out);
 
 /* Bytes of device workspace flce_fwd_bwd needs (256-byte aligned): per-row
  * statistics of every 256-column logits tile, two bf16 [N, 8192] gradient

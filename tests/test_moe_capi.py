@@ -123,3 +123,49 @@ QUANT = dict(x=P, dt=capi.BF16, batch=1, R=256, C=256, xs=256, xb=0, square=0, q
 ])
 def test_quantize_blocks_refuses(lib, kw, code):
     assert lib.quantize_blocks(*args(QUANT, kw)) == code
+
+
+FWD = dict(x=P, xs=256, xsc=FAR, xss=2, w=2 * FAR, ws=256, wsc=3 * FAR, wss=2, block=128, off=None, E=1, res=None, rs=64,
+           od=capi.BF16, T=32, N=64, K=256, y=4 * FAR, ys=64, err=None, stream=None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(od=capi.F32), capi.ERR_UNSUPPORTED_DTYPE), (dict(od=capi.E4M3), capi.ERR_UNSUPPORTED_DTYPE),
+    (dict(block=64), capi.ERR_INVALID_ARG), (dict(E=2), capi.ERR_INVALID_ARG),  # experts without offsets
+    (dict(off=P, E=0), capi.ERR_INVALID_ARG), (dict(T=-1), capi.ERR_INVALID_ARG), (dict(N=0), capi.ERR_INVALID_ARG),
+    (dict(K=0), capi.ERR_INVALID_ARG), (dict(xs=240), capi.ERR_INVALID_ARG), (dict(xs=264), capi.ERR_INVALID_ARG),
+    (dict(ws=258), capi.ERR_INVALID_ARG), (dict(xss=1), capi.ERR_INVALID_ARG), (dict(wss=1), capi.ERR_INVALID_ARG),
+    (dict(ys=63), capi.ERR_INVALID_ARG), (dict(res=5 * FAR, rs=63), capi.ERR_INVALID_ARG),
+    (dict(x=None), capi.ERR_INVALID_ARG), (dict(xsc=None), capi.ERR_INVALID_ARG), (dict(w=None), capi.ERR_INVALID_ARG),
+    (dict(wsc=None), capi.ERR_INVALID_ARG), (dict(y=None), capi.ERR_INVALID_ARG), (dict(y=P), capi.ERR_INVALID_ARG),
+    (dict(y=FAR), capi.ERR_INVALID_ARG), (dict(y=2 * FAR), capi.ERR_INVALID_ARG), (dict(y=3 * FAR), capi.ERR_INVALID_ARG),
+    (dict(off=4 * FAR + 64), capi.ERR_INVALID_ARG), (dict(res=4 * FAR, rs=72), capi.ERR_INVALID_ARG),
+    (dict(x=P + 8), capi.ERR_MISALIGNED), (dict(w=2 * FAR + 1), capi.ERR_MISALIGNED),
+    (dict(xsc=FAR + 2), capi.ERR_MISALIGNED), (dict(y=4 * FAR + 1), capi.ERR_MISALIGNED),
+    (dict(off=P + 2), capi.ERR_MISALIGNED), (dict(err=P + 2), capi.ERR_MISALIGNED),
+    (dict(off=P, E=1025), capi.ERR_TOO_LARGE), (dict(T=1 << 31), capi.ERR_TOO_LARGE),
+    (dict(N=1 << 31, ys=1 << 31), capi.ERR_TOO_LARGE), (dict(off=P, E=1024, N=1 << 21, ys=1 << 21), capi.ERR_TOO_LARGE),
+    (dict(xs=1 << 40), capi.ERR_TOO_LARGE), (dict(T=1 << 30, N=1 << 20, ys=1 << 20), capi.ERR_TOO_LARGE),
+])
+def test_block_linear_fwd_refuses(lib, kw, code):
+    assert lib.block_linear_fwd(*args(FWD, kw)) == code
+
+
+DW = dict(d=P, ds=256, dsc=FAR, dss=2, x=2 * FAR, xs=256, xsc=3 * FAR, xss=2, off=None, E=1, R=256, N=64, K=32, dw=4 * FAR,
+          dt=capi.F32, acc=0, err=None, stream=None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dt=capi.E4M3), capi.ERR_UNSUPPORTED_DTYPE), (dict(E=2), capi.ERR_INVALID_ARG),
+    (dict(R=-1), capi.ERR_INVALID_ARG), (dict(N=0), capi.ERR_INVALID_ARG), (dict(K=0), capi.ERR_INVALID_ARG),
+    (dict(dt=capi.BF16, acc=1), capi.ERR_INVALID_ARG), (dict(ds=255), capi.ERR_INVALID_ARG),
+    (dict(xs=264), capi.ERR_INVALID_ARG), (dict(dss=1), capi.ERR_INVALID_ARG), (dict(xss=1), capi.ERR_INVALID_ARG),
+    (dict(d=None), capi.ERR_INVALID_ARG), (dict(x=None), capi.ERR_INVALID_ARG), (dict(dw=None), capi.ERR_INVALID_ARG),
+    (dict(dsc=None), capi.ERR_INVALID_ARG), (dict(dw=P), capi.ERR_INVALID_ARG), (dict(dw=FAR), capi.ERR_INVALID_ARG),
+    (dict(off=4 * FAR), capi.ERR_INVALID_ARG), (dict(d=P + 8), capi.ERR_MISALIGNED), (dict(dw=4 * FAR + 2), capi.ERR_MISALIGNED),
+    (dict(off=P + 1), capi.ERR_MISALIGNED), (dict(R=1 << 31, ds=1 << 31, xs=1 << 31), capi.ERR_TOO_LARGE),
+    (dict(off=P, E=1024, N=1 << 20, K=1 << 20), capi.ERR_TOO_LARGE),
+    (dict(ds=1 << 40), capi.ERR_TOO_LARGE),
+])
+def test_block_linear_dweight_refuses(lib, kw, code):
+    assert lib.block_linear_dweight(*args(DW, kw)) == code

@@ -5,6 +5,8 @@ The compute lives in ``lib/libvlmce.so`` (hand-written CUDA kernels behind the
 C ABI in ``include/vlmce.h``); this package holds the build script, a thin
 ctypes/PyTorch binding and the seeded synthetic workloads.
 """
+from .block_linear import (BlockLinearPlan, block_linear_dweight, block_linear_fwd,  # noqa: F401
+                           describe_block_linear_plan)
 from .ce import (CEResult, ce_fwd_bwd, ce_fwd_bwd_host, describe_plan, host_workspace_bytes,  # noqa: F401
                  max_vocab, workspace_bytes)
 from .errors import check_device_errors, take_device_errors  # noqa: F401

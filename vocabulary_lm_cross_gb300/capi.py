@@ -29,6 +29,7 @@ NONE = 0
 MEAN = 1
 SUM = 2
 DEVERR_TIMEOUT = 1
+DEVERR_OFFSETS = 2
 ACT_NONE = 0
 ACT_SILU = 1
 ACT_GELU = 2
@@ -112,6 +113,11 @@ SIGNATURES = {
                            _i64, _vp, _i64, _vp]),
     "moe_combine_bwd": (_i32, [_vp, _i64, _vp, _i64, _i32, _vp, _vp, _vp, _vp, _i64, _i32, _i64,
                                _i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp]),
+    "block_linear_fwd": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _i64, _vp,
+                                _i64, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _vp]),
+    "block_linear_dweight": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i64,
+                                    _i64, _i64, _vp, _i32, _i32, _vp, _vp]),
+    "vlmce_block_linear_describe_plan": (_i32, [_i64, _i64, _i64, _i64, _i32, _vp]),
     "quantize_blocks": (_i32, [_vp, _i32, _i64, _i64, _i64, _i64, _i64, _i32, _vp, _i64, _vp, _vp,
                                _i64, _vp, _vp]),
 }

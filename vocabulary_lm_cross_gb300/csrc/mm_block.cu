@@ -1,0 +1,311 @@
+// mm_block.cu -- host side of the products with block scales: tensor maps, the choice of
+// kernel and tiles, launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <mutex>
+
+#include "device_errors.h"
+#include "gemm_launch.h"
+#include "host_util.h"
+#include "mm_block_pair.cuh"
+#include "mm_block_small.cuh"
+#include "mm_types.h"
+
+namespace vlmce {
+namespace mmb {
+namespace {
+
+constexpr int kMaxDevices = 64;
+// Shared memory of an SM (228 KB, 1 KB of it reserved per resident CTA) and, so that a
+// CTA that waits for TMEM columns never waits on one that waits for it, the least a CTA of
+// single-CTA kernels takes for its columns (mm_small.cuh) and beside the pair kernels.
+constexpr int kSmSmem = 233472, kSmemReserved = 1024, kSmemPerTmemCol = 456;
+constexpr int kSmallSmemMax = kSmSmem - kSmemReserved;
+
+using SmallKernel = void (*)(const CUtensorMap, const CUtensorMap, const SmallParams);
+using PairKernel = void (*)(const PairMaps, const PairParams);
+
+SmallKernel small_kernel(int bn, bool residual) {
+    switch (bn) {
+        case 16: return residual ? mm_block_small_kernel<8, true> : mm_block_small_kernel<8, false>;
+        case 32: return residual ? mm_block_small_kernel<16, true> : mm_block_small_kernel<16, false>;
+        case 64: return residual ? mm_block_small_kernel<32, true> : mm_block_small_kernel<32, false>;
+        default: return residual ? mm_block_small_kernel<64, true> : mm_block_small_kernel<64, false>;
+    }
+}
+PairKernel pair_kernel(bool dw, bool b_rows) {
+    if (dw) return mm_block_pair_kernel<true, true>;
+    return b_rows ? mm_block_pair_kernel<false, true> : mm_block_pair_kernel<false, false>;
+}
+
+void launch_attributes(cudaLaunchAttribute (&attr)[2], unsigned csize) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = csize;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+}
+
+// Per device: the kernels' shared memory is opted in to, the CTA pairs that fit at once,
+// the SMs, and the word for errors of calls without one of their own.
+struct Capacity {
+    int pairs = 0, sms = 0;
+    int *errors = nullptr;
+};
+cudaError_t setup(Capacity *out) {
+    static std::mutex mu;
+    static Capacity cached[kMaxDevices];
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    if (device < 0 || device >= kMaxDevices) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    if (cached[device].pairs == 0) {
+        Capacity c;
+        e = device_error_word(&c.errors);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&c.sms, cudaDevAttrMultiProcessorCount, device);
+        if (e != cudaSuccess) return e;
+        for (int bn = 16; bn <= 128; bn *= 2)
+            for (int res = 0; res < 2; ++res) {
+                e = cudaFuncSetAttribute(small_kernel(bn, res), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kSmallSmemMax);
+                if (e != cudaSuccess) return e;
+            }
+        for (int k = 0; k < 3; ++k) {
+            const PairKernel pk = pair_kernel(k == 2, k == 1);
+            e = cudaFuncSetAttribute(pk, cudaFuncAttributeMaxDynamicSharedMemorySize, mm::kPairSmem);
+            if (e != cudaSuccess) return e;
+            cudaLaunchConfig_t cfg = {};
+            cudaLaunchAttribute attr[2];
+            launch_attributes(attr, 2);
+            cfg.gridDim = dim3(2, 1, 1);
+            cfg.blockDim = dim3(mm::kPairThreads, 1, 1);
+            cfg.dynamicSmemBytes = mm::kPairSmem;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            e = cudaOccupancyMaxActiveClusters(&n, pk, &cfg);
+            if (e == cudaSuccess && n < 1) e = cudaErrorInvalidConfiguration;
+            if (e != cudaSuccess) return e;
+            c.pairs = k == 0 ? n : std::min(c.pairs, n);
+        }
+        cached[device] = c;
+    }
+    *out = cached[device];
+    return cudaSuccess;
+}
+
+bool e4m3_map(CUtensorMap *m, const void *p, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+    return gemm::make_tile_map(m, p, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, cols, rows, ld, 128, box_rows);
+}
+
+// How a forward product is run.
+struct Plan {
+    bool pair;
+    int bn, split, per_stage, stages;
+    int part, scale, table, bar, smem;  // small: where its shared memory's parts start, and its size
+};
+
+bool small_layout(const Fwd &f, int bn, int split, int per_stage, Plan *p) {
+    const int chunk = kSmallWBytes + bn * 128;
+    const int part = split > 1 ? bn * 512 : 0, scale = 8 * bn * 4;  // 8 warps x 2 x bn / 2
+    const int table = static_cast<int>(round_up(table_bytes(static_cast<int>(f.groups)), 16));
+    const int fixed = 1024 + part + scale + table + kSmallTail;
+    const int64_t chunks = (f.K + 127) / 128;
+    const int steps = static_cast<int>((chunks + split - 1) / split);
+    p->pair = false;
+    p->bn = bn;
+    p->split = split;
+    p->per_stage = per_stage;
+    p->stages = std::min((kSmallSmemMax - fixed) / (per_stage * chunk), kMaxStages);
+    if (p->stages < 2 || split > chunks) return false;
+    (void)steps;
+    p->part = p->stages * per_stage * chunk;
+    p->scale = p->part + part;
+    p->table = p->scale + scale;
+    p->bar = p->table + table;
+    p->smem = std::max(p->bar + kSmallTail + 1024, kSmallBufs * bn * kSmemPerTmemCol - kSmemReserved);
+    // one CTA per SM
+    p->smem = std::max(p->smem, kSmSmem / 2 - kSmemReserved + 1);
+    return true;
+}
+
+int64_t groups_used(const Fwd &f) { return f.offsets ? std::min(f.groups, f.T) : 1; }
+
+Plan choose(const Fwd &f, const Capacity &cap) {
+    Plan p = {};
+    const int64_t used = groups_used(f);
+    const double rows = static_cast<double>(f.T) / static_cast<double>(used);  // of a group, on average
+    if (rows > 192) {
+        p.pair = true;
+        return p;
+    }
+    int bn = 16;
+    while (bn < 128 && bn < rows * 1.25) bn *= 2;
+    const int64_t nt = (f.N + 127) / 128;
+    const int64_t tiles = nt * (f.offsets ? used + f.T / bn : (f.T + bn - 1) / bn);
+    const int64_t chunks = (f.K + 127) / 128;
+    int split = 1;
+    while (split < kMaxSplit && tiles * split * 2 <= cap.sms && chunks >= split * 4) split *= 2;
+    if (!small_layout(f, bn, split, chunks / split >= 2 ? 2 : 1, &p)) p.pair = true;
+    return p;
+}
+
+cudaError_t forward_small(const Fwd &f, const Capacity &cap, const Plan &plan, cudaStream_t s) {
+    CUtensorMap mw, mx;
+    if (!e4m3_map(&mw, f.w, f.groups * f.N, f.K, f.w_ld, 128) ||
+        !e4m3_map(&mx, f.x, f.T, f.K, f.x_ld, plan.bn))
+        return cudaErrorInvalidValue;
+    SmallParams p = {};
+    p.offsets = f.offsets;
+    p.xs = f.xs;
+    p.ws = f.ws;
+    p.xs_ld = f.xs_ld;
+    p.ws_ld = f.ws_ld;
+    p.residual = f.residual;
+    p.residual_ld = f.residual_ld;
+    p.y = f.y;
+    p.y_ld = f.y_ld;
+    p.T = static_cast<int>(f.T);
+    p.N = static_cast<int>(f.N);
+    p.groups = static_cast<int>(f.groups);
+    p.block = f.block;
+    p.scale_rows = static_cast<int>((f.N + f.block - 1) / f.block);
+    p.nt = static_cast<int>((f.N + 127) / 128);
+    p.chunks = static_cast<int>((f.K + 127) / 128);
+    p.split = plan.split;
+    p.stages = plan.stages;
+    p.per_stage = plan.per_stage;
+    p.part_offset = plan.part;
+    p.scale_offset = plan.scale;
+    p.table_offset = plan.table;
+    p.bar_offset = plan.bar;
+    p.f16 = f.f16;
+    p.err = f.err ? f.err : cap.errors;
+    const int64_t most = p.nt * (f.offsets ? f.T / plan.bn + groups_used(f) : (f.T + plan.bn - 1) / plan.bn);
+    if (most * plan.split > INT32_MAX) return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    launch_attributes(attr, static_cast<unsigned>(plan.split));
+    cfg.gridDim = dim3(static_cast<unsigned>(plan.split > 1 ? most * plan.split : std::min<int64_t>(most, cap.sms)),
+                       1, 1);
+    cfg.blockDim = dim3(kSmallThreads, 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(plan.smem);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, small_kernel(plan.bn, f.residual != nullptr), static_cast<const CUtensorMap>(mw),
+                              static_cast<const CUtensorMap>(mx), static_cast<const SmallParams>(p));
+}
+
+cudaError_t launch_pair(PairKernel k, const PairMaps &maps, const PairParams &p, int64_t tiles,
+                        const Capacity &cap, cudaStream_t s) {
+    if (tiles > INT32_MAX / kPairGroupM) return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    launch_attributes(attr, 2);
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(tiles, cap.pairs)), 1, 1);
+    cfg.blockDim = dim3(mm::kPairThreads, 1, 1);
+    cfg.dynamicSmemBytes = mm::kPairSmem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, k, maps, p);
+}
+
+// (A TMA store fills a row's last 16 bytes, so the map ends with the last whole ones.)
+bool output_map(CUtensorMap *m, const void *p, bool f32, int64_t rows, int64_t cols, int64_t ld) {
+    return gemm::make_tile_map(
+        m, p, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, f32 ? 4 : 2,
+        cols & ~int64_t{f32 ? 3 : 7}, rows, ld, f32 ? 32 : 64, 32);
+}
+
+cudaError_t forward_pair(const Fwd &f, const Capacity &cap, cudaStream_t s) {
+    PairMaps maps = {};
+    PairParams p = {};
+    p.vec = mm::vec_of(f.y, f.y_ld, f.N);
+    if (!e4m3_map(&maps.a, f.x, f.T, f.K, f.x_ld, mm::kHalfRows) ||
+        !e4m3_map(&maps.b, f.w, f.groups * f.N, f.K, f.w_ld, mm::kHalfRows) ||
+        (p.vec >= 16 && !output_map(&maps.y, f.y, false, f.T, f.N, f.y_ld)))
+        return cudaErrorInvalidValue;
+    p.offsets = f.offsets;
+    p.as = f.xs;
+    p.bs = f.ws;
+    p.as_ld = f.xs_ld;
+    p.bs_ld = f.ws_ld;
+    p.residual = f.residual;
+    p.residual_ld = f.residual_ld;
+    p.y = f.y;
+    p.y_ld = f.y_ld;
+    p.T = static_cast<int>(f.T);
+    p.N = static_cast<int>(f.N);
+    p.groups = static_cast<int>(f.groups);
+    p.scale_rows = static_cast<int>((f.N + f.block - 1) / f.block);
+    p.nt = static_cast<int>((f.N + 255) / 256);
+    p.chunks = static_cast<int>((f.K + 127) / 128);
+    p.out = f.f16 ? VLMCE_F16 : VLMCE_BF16;
+    p.err = f.err ? f.err : cap.errors;
+    const int64_t most = p.nt * (f.offsets ? f.T / 256 + groups_used(f) : (f.T + 255) / 256);
+    return launch_pair(pair_kernel(false, f.block == 1), maps, p, most, cap, s);
+}
+
+}  // namespace
+
+cudaError_t forward(const Fwd &f, cudaStream_t s) {
+    Capacity cap;
+    const cudaError_t e = setup(&cap);
+    if (e != cudaSuccess) return e;
+    const Plan plan = choose(f, cap);
+    return plan.pair ? forward_pair(f, cap, s) : forward_small(f, cap, plan, s);
+}
+
+cudaError_t describe(const Fwd &f, int32_t *out) {
+    Capacity cap;
+    const cudaError_t e = setup(&cap);
+    if (e != cudaSuccess) return e;
+    const Plan plan = choose(f, cap);
+    out[0] = plan.pair ? 0 : 1;
+    out[1] = plan.pair ? 256 : plan.bn;
+    out[2] = plan.pair ? 1 : plan.split;
+    out[3] = plan.pair ? 1 : plan.per_stage;
+    return cudaSuccess;
+}
+
+cudaError_t dweight(const Dw &d, cudaStream_t s) {
+    Capacity cap;
+    const cudaError_t e = setup(&cap);
+    if (e != cudaSuccess) return e;
+    PairMaps maps = {};
+    PairParams p = {};
+    const bool f32 = d.dtype == VLMCE_F32;
+    p.vec = f32 ? (aligned(d.dw, 16) && d.K % 4 == 0 ? 16 : 2) : mm::vec_of(d.dw, d.K, d.K);
+    if (!e4m3_map(&maps.a, d.dyt, d.N, d.R, d.dyt_ld, mm::kHalfRows) ||
+        !e4m3_map(&maps.b, d.xt, d.K, d.R, d.xt_ld, mm::kHalfRows) ||
+        (p.vec >= 16 && !output_map(&maps.y, d.dw, f32, d.groups * d.N, d.K, d.K)))
+        return cudaErrorInvalidValue;
+    p.offsets = d.offsets;
+    p.as = d.dyts;
+    p.bs = d.xts;
+    p.as_ld = d.dyts_ld;
+    p.bs_ld = d.xts_ld;
+    p.y = d.dw;
+    p.y_ld = d.K;
+    p.T = static_cast<int>(d.R);
+    p.N = static_cast<int>(d.N);
+    p.groups = static_cast<int>(d.groups);
+    p.K = static_cast<int>(d.K);
+    p.nt = static_cast<int>((d.K + 255) / 256);
+    p.mt = static_cast<int>((d.N + 255) / 256);
+    p.out = d.dtype;
+    p.add = d.accumulate;
+    p.err = d.err ? d.err : cap.errors;
+    const int64_t tiles = d.groups * p.mt * static_cast<int64_t>(p.nt);
+    return launch_pair(pair_kernel(true, true), maps, p, tiles, cap, s);
+}
+
+}  // namespace mmb
+}  // namespace vlmce

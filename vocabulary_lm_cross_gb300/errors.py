@@ -7,8 +7,8 @@ from . import capi
 
 
 def take_device_errors(device=None) -> int:
-    """The DEVERR_* bits (capi.py) that linear and gated layers called without dev_err
-    have left on `device` since the last call; they are cleared.  Waits for the current
+    """The DEVERR_* bits (capi.py) that linear, gated and block-scaled layers called
+    without dev_err have left on `device` since the last call; they are cleared.  Waits for the current
     stream; layers on other streams count once they have run."""
     dev = torch.device("cuda" if device is None else device)
     with torch.cuda.device(dev):
@@ -23,5 +23,8 @@ def check_device_errors(device=None) -> None:
     bits = take_device_errors(device)
     if bits & capi.DEVERR_TIMEOUT:
         raise RuntimeError("a kernel's wait gave up: results since the last check are invalid")
+    if bits & capi.DEVERR_OFFSETS:
+        raise RuntimeError("offsets that block_linear_fwd or block_linear_dweight cannot take: "
+                           "its experts counted as empty")
     if bits:
         raise RuntimeError(f"device error bits {bits:#x}")
