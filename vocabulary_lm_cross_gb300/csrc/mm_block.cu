@@ -83,7 +83,7 @@ cudaError_t setup(Capacity *out) {
             cudaLaunchAttribute attr[2];
             launch_attributes(attr, 2);
             cfg.gridDim = dim3(2, 1, 1);
-            cfg.blockDim = dim3(mm::kPairThreads, 1, 1);
+            cfg.blockDim = dim3(kPairThreads, 1, 1);
             cfg.dynamicSmemBytes = mm::kPairSmem;
             cfg.attrs = attr;
             cfg.numAttrs = 1;
@@ -107,14 +107,14 @@ bool e4m3_map(CUtensorMap *m, const void *p, int64_t rows, int64_t cols, int64_t
 struct Plan {
     bool pair;
     int bn, split, per_stage, stages;
-    int part, scale, table, bar, smem;  // small: where its shared memory's parts start, and its size
+    int part, factors, table, bar, smem;  // small: where its shared memory's parts start, and its size
 };
 
 bool small_layout(const Fwd &f, int bn, int split, int per_stage, Plan *p) {
     const int chunk = kSmallWBytes + bn * 128;
-    const int part = split > 1 ? bn * 512 : 0, scale = 8 * bn * 4;  // 8 warps x 2 x bn / 2
+    const int part = split > 1 ? bn * 512 : 0, factors = kSmallFactors + kFactorBarBytes;
     const int table = static_cast<int>(round_up(table_bytes(static_cast<int>(f.groups)), 16));
-    const int fixed = 1024 + part + scale + table + kSmallTail;
+    const int fixed = 1024 + part + factors + table + kSmallTail;
     const int64_t chunks = (f.K + 127) / 128;
     const int steps = static_cast<int>((chunks + split - 1) / split);
     p->pair = false;
@@ -125,8 +125,8 @@ bool small_layout(const Fwd &f, int bn, int split, int per_stage, Plan *p) {
     if (p->stages < 2 || split > chunks) return false;
     (void)steps;
     p->part = p->stages * per_stage * chunk;
-    p->scale = p->part + part;
-    p->table = p->scale + scale;
+    p->factors = p->part + part;
+    p->table = p->factors + factors;
     p->bar = p->table + table;
     p->smem = std::max(p->bar + kSmallTail + 1024, kSmallBufs * bn * kSmemPerTmemCol - kSmemReserved);
     // one CTA per SM
@@ -181,7 +181,7 @@ cudaError_t forward_small(const Fwd &f, const Capacity &cap, const Plan &plan, c
     p.stages = plan.stages;
     p.per_stage = plan.per_stage;
     p.part_offset = plan.part;
-    p.scale_offset = plan.scale;
+    p.factor_offset = plan.factors;
     p.table_offset = plan.table;
     p.bar_offset = plan.bar;
     p.f16 = f.f16;
@@ -209,7 +209,7 @@ cudaError_t launch_pair(PairKernel k, const PairMaps &maps, const PairParams &p,
     cudaLaunchAttribute attr[2];
     launch_attributes(attr, 2);
     cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(tiles, cap.pairs)), 1, 1);
-    cfg.blockDim = dim3(mm::kPairThreads, 1, 1);
+    cfg.blockDim = dim3(kPairThreads, 1, 1);
     cfg.dynamicSmemBytes = mm::kPairSmem;
     cfg.stream = s;
     cfg.attrs = attr;
@@ -229,7 +229,7 @@ cudaError_t forward_pair(const Fwd &f, const Capacity &cap, cudaStream_t s) {
     PairParams p = {};
     p.vec = mm::vec_of(f.y, f.y_ld, f.N);
     if (!e4m3_map(&maps.a, f.x, f.T, f.K, f.x_ld, mm::kHalfRows) ||
-        !e4m3_map(&maps.b, f.w, f.groups * f.N, f.K, f.w_ld, mm::kHalfRows) ||
+        !e4m3_map(&maps.b, f.w, f.groups * f.N, f.K, f.w_ld, kPairN / 2) ||
         (p.vec >= 16 && !output_map(&maps.y, f.y, false, f.T, f.N, f.y_ld)))
         return cudaErrorInvalidValue;
     p.offsets = f.offsets;
@@ -245,7 +245,7 @@ cudaError_t forward_pair(const Fwd &f, const Capacity &cap, cudaStream_t s) {
     p.N = static_cast<int>(f.N);
     p.groups = static_cast<int>(f.groups);
     p.scale_rows = static_cast<int>((f.N + f.block - 1) / f.block);
-    p.nt = static_cast<int>((f.N + 255) / 256);
+    p.nt = static_cast<int>((f.N + kPairN - 1) / kPairN);
     p.chunks = static_cast<int>((f.K + 127) / 128);
     p.out = f.f16 ? VLMCE_F16 : VLMCE_BF16;
     p.err = f.err ? f.err : cap.errors;
@@ -284,7 +284,7 @@ cudaError_t dweight(const Dw &d, cudaStream_t s) {
     const bool f32 = d.dtype == VLMCE_F32;
     p.vec = f32 ? (aligned(d.dw, 16) && d.K % 4 == 0 ? 16 : 2) : mm::vec_of(d.dw, d.K, d.K);
     if (!e4m3_map(&maps.a, d.dyt, d.N, d.R, d.dyt_ld, mm::kHalfRows) ||
-        !e4m3_map(&maps.b, d.xt, d.K, d.R, d.xt_ld, mm::kHalfRows) ||
+        !e4m3_map(&maps.b, d.xt, d.K, d.R, d.xt_ld, kPairN / 2) ||
         (p.vec >= 16 && !output_map(&maps.y, d.dw, f32, d.groups * d.N, d.K, d.K)))
         return cudaErrorInvalidValue;
     p.offsets = d.offsets;
@@ -298,7 +298,7 @@ cudaError_t dweight(const Dw &d, cudaStream_t s) {
     p.N = static_cast<int>(d.N);
     p.groups = static_cast<int>(d.groups);
     p.K = static_cast<int>(d.K);
-    p.nt = static_cast<int>((d.K + 255) / 256);
+    p.nt = static_cast<int>((d.K + kPairN - 1) / kPairN);
     p.mt = static_cast<int>((d.N + 255) / 256);
     p.out = d.dtype;
     p.add = d.accumulate;

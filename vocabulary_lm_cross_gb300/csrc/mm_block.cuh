@@ -24,18 +24,43 @@
 namespace vlmce {
 namespace mmb {
 
+// ------------------------------------------------------------ packed fp32
+__device__ __forceinline__ uint64_t pack2(uint32_t a, uint32_t b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) {
+    uint32_t x, y;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(x), "=r"(y) : "l"(v));
+    a = __uint_as_float(x);
+    b = __uint_as_float(y);
+}
+__device__ __forceinline__ uint64_t both(float a) {
+    return pack2(__float_as_uint(a), __float_as_uint(a));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 // ------------------------------------------------------------ the groups' tiles
 // In shared memory: for each group its rows and the tiles of `step` rows before it.
 struct Table {
     int *tile0;  // [groups + 1]
-    int *row0, *row1;
+    int *row;    // [groups + 1]: a group's rows end where the next one's start
 };
-constexpr int table_bytes(int groups) { return 4 * (3 * groups + 1); }
+constexpr int table_bytes(int groups) { return 8 * (groups + 1); }
 __device__ __forceinline__ Table table_at(unsigned char *p, int groups) {
     Table t;
     t.tile0 = reinterpret_cast<int *>(p);
-    t.row0 = t.tile0 + groups + 1;
-    t.row1 = t.row0 + groups;
+    t.row = t.tile0 + groups + 1;
     return t;
 }
 // All threads.  Offsets outside [0, rows] or descending, or (`whole` > 1) not its multiples
@@ -44,8 +69,8 @@ __device__ __forceinline__ void table_fill(const Table &t, const int *offsets, i
                                            int step, int whole, int *err) {
     if (!offsets) {
         if (threadIdx.x == 0) {
-            t.row0[0] = 0;
-            t.row1[0] = rows;
+            t.row[0] = 0;
+            t.row[1] = rows;
             t.tile0[0] = 0;
             t.tile0[1] = (rows + step - 1) / step;
         }
@@ -53,15 +78,14 @@ __device__ __forceinline__ void table_fill(const Table &t, const int *offsets, i
         return;
     }
     bool bad = false;
-    for (int e = threadIdx.x; e < groups; e += blockDim.x) {
-        const int a = offsets[e], b = offsets[e + 1];
-        bad |= a < 0 || b < a || b > rows || a % whole != 0 || (b % whole != 0 && b != rows);
-        t.row0[e] = a;
-        t.row1[e] = b;
+    for (int e = threadIdx.x; e <= groups; e += blockDim.x) {
+        const int b = offsets[e], a = e > 0 ? offsets[e - 1] : 0;
+        bad |= a < 0 || b < a || b > rows || (b % whole != 0 && (e == 0 || b != rows));
+        t.row[e] = b;
     }
     if (__syncthreads_or(bad)) {
         if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(err, VLMCE_DEVERR_OFFSETS);
-        for (int e = threadIdx.x; e < groups; e += blockDim.x) t.row0[e] = t.row1[e] = 0;
+        for (int e = threadIdx.x; e <= groups; e += blockDim.x) t.row[e] = 0;
         __syncthreads();
     }
     if (threadIdx.x < 32) {
@@ -69,7 +93,7 @@ __device__ __forceinline__ void table_fill(const Table &t, const int *offsets, i
         int before = 0;
         for (int e0 = 0; e0 < groups; e0 += 32) {
             const int e = e0 + lane;
-            const int n = e < groups ? (t.row1[e] - t.row0[e] + step - 1) / step : 0;
+            const int n = e < groups ? (t.row[e + 1] - t.row[e] + step - 1) / step : 0;
             int sum = n;
 #pragma unroll
             for (int d = 1; d < 32; d *= 2) {
@@ -94,6 +118,67 @@ __device__ __forceinline__ int group_of(const Table &t, int groups, int at) {
             hi = mid;
     }
     return lo;
+}
+
+// ------------------------------------------------------------ factors
+// A warp of its own brings the factors into shared memory, four blocks at a time and up to
+// eight ahead: behind the operands' copies an answer takes thousands of clocks (fetched into
+// registers two blocks ahead, T 4096, K 4096, N 4096 took 151 us).  Its lanes take four
+// blocks of eight rows, so that an access covers eight lines of memory (with 32 rows of one
+// block, 32 lines kept the load unit busy for 60 clocks), and rows of the ring are 8 words
+// apart from a multiple of 32, so that they write to 32 banks.
+constexpr int kFactorBatch = 4;
+constexpr int kFactorSlots = 3;  // batches
+constexpr int kFactorBarBytes = 16 * kFactorSlots;
+// Words of a block's factors: n of them.
+constexpr int factor_words(int n) { return (n + 31) / 32 * 32 + 8; }
+
+struct Factors {
+    uint32_t slots, bars;  // shared-memory addresses
+    int words;             // of a block
+    __device__ __forceinline__ uint32_t full(int s) const { return bars + 8u * s; }
+    __device__ __forceinline__ uint32_t empty(int s) const { return bars + 8u * (kFactorSlots + s); }
+    __device__ __forceinline__ uint32_t at(int s) const {
+        return slots + static_cast<uint32_t>(4 * kFactorBatch * s * words);
+    }
+    // one thread, before the CTA's barrier
+    __device__ __forceinline__ void init(int readers) const {
+        for (int s = 0; s < kFactorSlots; ++s) {
+            ptx::mbar_init(full(s), 32);        // every lane's copies
+            ptx::mbar_init(empty(s), readers);  // warps
+        }
+    }
+};
+// Position in the ring of batches.
+struct Slot {
+    int s = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next() {
+        if (++s == kFactorSlots) {
+            s = 0;
+            ph ^= 1;
+        }
+    }
+};
+// Four blocks' (those of the first `blocks`) factors of N (a multiple of 8) rows from `first`
+// of base [.., ld], the rows from `count` on as 0; `dst`: where the first block's go.
+template <int N>
+__device__ __forceinline__ void factors_copy(uint32_t dst, int words, const float *base, int64_t first, int64_t ld,
+                                             int count, int blocks, int lane) {
+    const int k = lane & 3, r = lane >> 2;
+    const float *src = base + (first + r) * ld + k;
+    const uint32_t to = dst + 4u * (k * words + r);
+    const int64_t step = 8 * ld;
+#pragma unroll 4
+    for (int j = 0; j < N; j += 8, src += step) {
+        const bool in = k < blocks && j + r < count;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + 4u * j), "l"(in ? src : base),
+                     "r"(in ? 4 : 0)
+                     : "memory");
+    }
+}
+__device__ __forceinline__ void factors_done(const Factors &f, int s) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(f.full(s)) : "memory");
 }
 
 }  // namespace mmb

@@ -1,21 +1,23 @@
 // mm_block_pair.cuh -- products with block scales on CTA pairs (mm_pair.cuh): tiles of
-// 256 x 256, each CTA with 128 rows of operand A and all 256 of B in its accumulators.
+// 256 x 192, each CTA with 128 rows of operand A and all 192 of B in its accumulators.
 //
 //   forward   A = x (rows of one group), B = the group's weight
 //   dweight   A = dyt, B = xt, over a group's part of their common columns
 //
-// A pair's products of one block (128 of K) take about 540 clocks at the tensor cores'
-// rate, and so long the other TMEM buffer has to be emptied: 8 epilogue warps, each with 32
-// rows x 128 columns of sums in registers (128 a thread, 224 with what else it needs: the
-// control warps give theirs up), 64 columns a load.  A's factor is a thread's own.  B's is
-// one for the 128 columns (a weight's blocks of 128 x 128: acc += (a b) d, one packed
-// multiply-add), or one for each column (B_ROWS), put into shared memory by the lanes that
-// fetched them.  Factors are fetched some blocks ahead.
+// The sums of a block are in one of two TMEM buffers while the next block's form in the
+// other; 12 epilogue warps, each with 32 rows x 64 columns of running sums in registers,
+// empty it.  A's factor is a thread's own.  B's is one for the 64 columns (a weight's
+// blocks of 128 x 128: acc += (a b) d), or one for each column (B_ROWS).  192 columns, since
+// the running sums of 256 leave no registers to work with (128 of a thread's 168; with
+// setmaxnreg's 224 the loop's multiply-adds took ten clocks each).
+//
+// One commit per block: "the stage is free" and "the block's sums are there" are the same
+// event, and both CTAs' epilogue warps wait on the stage's barrier, as the copies do.
 //
 // The tiles are dealt out in order; a group's tiles go down 8 tiles of rows before they go
 // across, so those in flight share operands.
 //
-// Warps: 0 and 2 fetch A and B, 1 TMEM and MMA issuer, 3 idle, 4-11 epilogue.
+// Warps: 0 and 2 fetch A and B, 1 TMEM and MMA issuer, 3 fetches the factors, 4-15 epilogue.
 #pragma once
 
 #include <cuda.h>
@@ -26,14 +28,26 @@
 namespace vlmce {
 namespace mmb {
 
-constexpr int kPairStages = 5;  // of mm_pair.cuh's ring; its last chunk's memory is the
-                                // groups' table and the columns' factors
-constexpr int kPairFactors = 8 * 2 * 128 * 4;
-constexpr int kPairGroupM = 8;
+constexpr int kPairThreads = 384;
+constexpr int kPairN = 256;
+constexpr int kPairEpiWarps = 8;
+constexpr int kPairCols = 4 * kPairN / kPairEpiWarps;  // columns of a warp
 constexpr int kControlRegs = 56, kEpilogueRegs = 224;
-static_assert((kControlRegs + 2 * kEpilogueRegs) * 128 <= 65536 / mm::kPairThreads / 8 * 8 * mm::kPairThreads,
+static_assert((kControlRegs + 2 * kEpilogueRegs) * 128 <= 65536 / kPairThreads / 8 * 8 * kPairThreads,
               "more registers than a launch has");
-static_assert(kPairFactors + table_bytes(VLMCE_MOE_MAX_EXPERTS) <= mm::kChunkBytes, "in one chunk");
+constexpr int kPairBBytes = kPairN / 2 * 128;  // a CTA's part of B, of a block
+constexpr int kPairChunk = mm::kOpBytes + kPairBBytes;
+constexpr int kPairGroupM = 8;
+// Shared memory: mm_pair.cuh's, whose ring and output buffers are these instead.
+constexpr int kPairStages = 5;
+constexpr int kPairWords = factor_words(128 + kPairN);  // a block's factors: the CTA's rows of A, the columns
+constexpr int kPairOutAt = kPairStages * kPairChunk;
+constexpr int kPairFactorsAt = kPairOutAt + kPairEpiWarps * mm::kOutBytes;
+constexpr int kPairBarsAt = kPairFactorsAt + 4 * kFactorSlots * kFactorBatch * kPairWords + kFactorBarBytes;
+constexpr int kPairTableAt = kPairBarsAt + 16;
+static_assert(kPairTableAt + table_bytes(VLMCE_MOE_MAX_EXPERTS) <= mm::kRingBytes + mm::kEpiWarps * mm::kOutBytes,
+              "in mm_pair.cuh's ring and output buffers");
+static_assert(kPairOutAt % 1024 == 0, "the output buffers' swizzle");
 
 struct PairMaps {
     CUtensorMap a, b, y;
@@ -47,14 +61,14 @@ template <bool DW>
 __device__ __forceinline__ PairTile pair_tile(const PairParams &p, const Table &t, int i) {
     if constexpr (DW) {
         const int per = p.mt * p.nt, g = i / per, l = i - g * per, n = l / p.mt;
-        const int r0 = t.row0[g], rows = t.row1[g] - r0;
-        return {g, (l - n * p.mt) * 256, p.N, n * 256, r0 / 128, (rows + 127) / 128};
+        const int r0 = t.row[g], rows = t.row[g + 1] - r0;
+        return {g, (l - n * p.mt) * 256, p.N, n * kPairN, r0 / 128, (rows + 127) / 128};
     } else {
         const int g = group_of(t, p.groups, i / p.nt);
         const int l = i - t.tile0[g] * p.nt, mt = t.tile0[g + 1] - t.tile0[g];
         const int per = kPairGroupM * p.nt, q = l / per, r = l - q * per;
         const int gm = min(kPairGroupM, mt - q * kPairGroupM), n = r / gm;
-        return {g, t.row0[g] + (q * kPairGroupM + r - n * gm) * 256, t.row1[g], n * 256, 0, p.chunks};
+        return {g, t.row[g] + (q * kPairGroupM + r - n * gm) * 256, t.row[g + 1], n * kPairN, 0, p.chunks};
     }
 }
 
@@ -78,15 +92,8 @@ __device__ __forceinline__ void put_f32_rows(float *base, int64_t ld, int64_t ro
     }
 }
 
-// G blocks' factors: of a thread's row of A, and of B's columns lane, lane + 32, .. (B_ROWS)
-// or of its rows' block.
-template <bool B_ROWS, int G>
-struct PairScales {
-    float a[G], b[B_ROWS ? 4 : 1][G];
-};
-
 template <bool DW, bool B_ROWS>
-__global__ void __launch_bounds__(mm::kPairThreads, 1)
+__global__ void __launch_bounds__(kPairThreads, 1)
     mm_block_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ PairParams p) {
     extern __shared__ unsigned char smem_raw[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -94,10 +101,18 @@ __global__ void __launch_bounds__(mm::kPairThreads, 1)
         tc::prefetch_tensormap(&maps.a);
         tc::prefetch_tensormap(&maps.b);
     }
-    mm::Pair<1> q = mm::pair_setup<1>(smem_raw, p.err, 1);
+    unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                            ~static_cast<uintptr_t>(1023));
+    const uint32_t smem_at = ptx::smem_addr(smem);
+    const Factors factors = {smem_at + kPairFactorsAt, smem_at + kPairFactorsAt + 4 * kFactorSlots * kFactorBatch * kPairWords, kPairWords};
+    const uint32_t buf_empty = smem_at + kPairBarsAt;  // [2], the leader's
+    if (threadIdx.x == 0) {
+        factors.init(kPairEpiWarps);
+        for (int b = 0; b < 2; ++b) ptx::mbar_init(buf_empty + 8u * b, 2 * kPairEpiWarps);  // of both CTAs
+    }
+    mm::Pair<1> q = mm::pair_setup<1>(smem_raw, p.err, 1, kPairChunk);
     q.stages = kPairStages;
-    unsigned char *rest = q.smem + kPairStages * mm::kChunkBytes;
-    const Table table = table_at(rest + kPairFactors, p.groups);
+    const Table table = table_at(smem + kPairTableAt, p.groups);
     table_fill(table, p.offsets, p.groups, p.T, DW ? 1 : 256, DW ? 128 : 1, p.err);
     const int rank = static_cast<int>(q.rank);
     const int first = static_cast<int>(ptx::cluster_id_x()), step = static_cast<int>(ptx::ncluster_x());
@@ -112,7 +127,8 @@ __global__ void __launch_bounds__(mm::kPairThreads, 1)
                 int64_t issued = 0;
                 for (int i = first; i < total; i += step) {
                     const PairTile t = pair_tile<DW>(p, table, i);
-                    const int row = (warp == 0 ? t.row : DW ? t.col : t.g * p.N + t.col) + mm::kHalfRows * rank;
+                    const int row = warp == 0 ? t.row + mm::kHalfRows * rank
+                                              : (DW ? t.col : t.g * p.N + t.col) + kPairN / 2 * rank;
                     for (int c = 0; c < t.chunks; ++c) {
                         if (warp == 0) {
                             mm::stage_begin<true, 1>(q, r, 1);
@@ -131,114 +147,138 @@ __global__ void __launch_bounds__(mm::kPairThreads, 1)
             }
         } else if (warp == 1) {
             if (rank == 0 && lane == 0) {
-                const uint32_t idesc = tc::idesc_bf16_f32(256, 256, false, false, true);
+                const uint32_t idesc = tc::idesc_bf16_f32(256, kPairN, false, false, true);
                 mm::Ring<1> r;
                 int it = 0;
                 for (int i = first; i < total; i += step) {
                     const int chunks = pair_tile<DW>(p, table, i).chunks;
-                    for (int c = 0; c < chunks; ++c) mm::mma_tile<true, 1>(q, r, it++, 1, idesc, false, false);
+                    for (int c = 0; c < chunks; ++c, ++it) {
+                        const int b = it & 1;
+                        const uint32_t d = q.tmem + static_cast<uint32_t>(b * 256);
+                        wait_bar(q.full(r.s), r.ph, q.abort, q.err);
+                        const uint64_t ad = tc::smem_desc_sw128(q.chunk(r.s, 0), 16, 1024);
+                        const uint64_t bd = tc::smem_desc_sw128(q.chunk(r.s, 0) + mm::kOpBytes, 16, 1024);
+                        wait_bar(buf_empty + 8u * b, ((it >> 1) & 1) ^ 1, q.abort, q.err);
+                        tc::fence_after_sync();
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)  // (32 bytes on: 2 in a descriptor)
+                            tc::mma_f8_pair(d, ad + 2 * k, bd + 2 * k, idesc, k != 0);
+                        // in both CTAs: the stage is free, and its block's sums are there
+                        tc::mma_commit_pair(q.empty(r.s), 3u);
+                        r.next(q);
+                    }
                 }
                 mm::mma_finish(q);
             }
+        } else {
+            Slot at;
+            for (int i = first; i < total; i += step) {
+                const PairTile t = pair_tile<DW>(p, table, i);
+                const int row = t.row + mm::kHalfRows * rank;
+                for (int c = 0; c < t.chunks; c += kFactorBatch) {
+                    wait_bar(factors.empty(at.s), at.ph ^ 1, q.abort, q.err);
+                    const uint32_t to = factors.at(at.s);
+                    const int n = t.chunks - c;
+                    factors_copy<128>(to, kPairWords, p.as + t.c0 + c, row, p.as_ld, t.end - row, n, lane);
+                    if constexpr (B_ROWS) {
+                        factors_copy<kPairN>(to + 512, kPairWords, p.bs + t.c0 + c,
+                                             DW ? t.col : static_cast<int64_t>(t.g) * p.N + t.col, p.bs_ld,
+                                             (DW ? p.K : p.N) - t.col, n, lane);
+                    } else {
+                        // of the columns' two blocks
+                        factors_copy<8>(to + 512, kPairWords, p.bs + c,
+                                        static_cast<int64_t>(t.g) * p.scale_rows + t.col / 128, p.bs_ld,
+                                        min(2, p.scale_rows - t.col / 128), n, lane);
+                    }
+                    factors_done(factors, at.s);
+                    at.next();
+                }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpilogueRegs));
-        constexpr int G = 2;
-        using Scales = PairScales<B_ROWS, G>;
-        const int half = (warp - 4) >> 2;
-        uint32_t *buf = q.out_buffer(warp - 4);
-        float *bf = reinterpret_cast<float *>(rest) + (warp - 4) * 256;  // [2][128]
-        const uint32_t tempty_leader = ptx::mapa(q.tempty(0), 0);
+        const int part = kPairCols * ((warp - 4) >> 2);  // the warp's first column of the tile
+        uint32_t *buf = reinterpret_cast<uint32_t *>(smem + kPairOutAt + (warp - 4) * mm::kOutBytes);
+        const float *slots = reinterpret_cast<const float *>(smem + kPairFactorsAt);
+        const uint32_t empty_leader = ptx::mapa(buf_empty, 0);
         const int in_tile = mm::kHalfRows * rank + (warp & 3) * 32;  // the warp's first row
         const int cols = DW ? p.K : p.N;
-        auto fetch = [&](Scales &f, const PairTile &t, int c) {
-            const int row = t.row + in_tile + lane;
-            const float *pa = p.as + static_cast<int64_t>(row) * p.as_ld + t.c0 + c;
-#pragma unroll
-            for (int k = 0; k < G; ++k) f.a[k] = row < t.end && c + k < t.chunks ? pa[k] : 0.f;
-            if constexpr (B_ROWS) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int col = t.col + 128 * half + 32 * j + lane;
-                    const int64_t at = DW ? col : static_cast<int64_t>(t.g) * p.N + col;
-                    const float *pb = p.bs + at * p.bs_ld + t.c0 + c;
-#pragma unroll
-                    for (int k = 0; k < G; ++k) f.b[j][k] = col < cols && c + k < t.chunks ? pb[k] : 0.f;
-                }
-            } else {
-                const int block = t.col / 128 + half;
-                const float *pb = p.bs + (static_cast<int64_t>(t.g) * p.scale_rows + block) * p.bs_ld + c;
-#pragma unroll
-                for (int k = 0; k < G; ++k) f.b[0][k] = block < p.scale_rows && c + k < t.chunks ? pb[k] : 0.f;
-            }
-        };
-        PairTile t = {};
-        Scales next = {};
-        if (first < total) {
-            t = pair_tile<DW>(p, table, first);
-            fetch(next, t, 0);
-        }
+        Slot at;
+        mm::Ring<1> r;
         int it = 0;
         for (int i = first; i < total; i += step) {
-            float acc[128];
+            const PairTile t = pair_tile<DW>(p, table, i);
+            const int block = 128 + (DW ? 0 : ((t.col + part) >> 7) - (t.col >> 7));  // B's factor in a slot
+            uint64_t acc[kPairCols / 2];  // two columns each
 #pragma unroll
-            for (int j = 0; j < 128; ++j) acc[j] = 0.f;
-            if (t.chunks == 0 && i + step < total) fetch(next, pair_tile<DW>(p, table, i + step), 0);
+            for (int j = 0; j < kPairCols / 2; ++j) acc[j] = 0;
+            const float *f = nullptr;
 #pragma unroll 1
-            for (int c = 0; c < t.chunks; c += G) {
-                const Scales f = next;
-                if (c + G < t.chunks)
-                    fetch(next, t, c + G);
-                else if (i + step < total)
-                    fetch(next, pair_tile<DW>(p, table, i + step), 0);
-#pragma unroll
-                for (int k = 0; k < G; ++k) {
-                    if (c + k >= t.chunks) break;
-                    float *slot = bf + (it & 1) * 128;
-                    if constexpr (B_ROWS) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) slot[32 * j + lane] = f.b[j][k];
+            for (int c = 0; c < t.chunks; ++c, ++it) {
+                if (c % kFactorBatch == 0) {
+                    if (c > 0) {
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(factors.empty(at.s));
+                        at.next();
                     }
-                    const float a = B_ROWS ? f.a[k] : f.a[k] * f.b[0][k];
-                    const uint32_t d0 = mm::acc_wait(q, it, warp) + 128 * half;
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        uint32_t d[32];
-                        tc::tmem_ld32(d0 + 32 * h, d);
-                        tc::tmem_ld_wait();
-                        if (h == 3) mm::acc_release(tempty_leader, it, lane);
-                        if constexpr (B_ROWS) {
-#pragma unroll
-                            for (int j = 0; j < 32; j += 4) {
-                                const float4 b = *reinterpret_cast<const float4 *>(slot + 32 * h + j);
-                                float *to = acc + 32 * h + j;
-                                to[0] = fmaf(__uint_as_float(d[j]), b.x * a, to[0]);
-                                to[1] = fmaf(__uint_as_float(d[j + 1]), b.y * a, to[1]);
-                                to[2] = fmaf(__uint_as_float(d[j + 2]), b.z * a, to[2]);
-                                to[3] = fmaf(__uint_as_float(d[j + 3]), b.w * a, to[3]);
-                            }
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                acc[32 * h + j] = fmaf(__uint_as_float(d[j]), a, acc[32 * h + j]);
-                        }
-                    }
-                    ++it;
+                    wait_bar(factors.full(at.s), at.ph, q.abort, q.err);
+                    f = slots + at.s * (kFactorBatch * kPairWords);
+                } else {
+                    f += kPairWords;
                 }
+                float a = f[(warp & 3) * 32 + lane];
+                if constexpr (!B_ROWS) a *= f[block];
+                wait_bar(q.empty(r.s), r.ph, q.abort, q.err);
+                r.next(q);
+                __syncwarp();  // each lane left the wait by itself; TMEM loads take the whole warp
+                tc::fence_after_sync();
+                const uint32_t d0 = q.tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 256 * (it & 1) + part;
+                const uint64_t a2 = both(a);
+#pragma unroll
+                for (int h = 0; h < kPairCols; h += 16) {
+                    uint32_t d[16];
+                    tc::tmem_ld16(d0 + h, d);
+                    tc::tmem_ld_wait();
+                    if (h + 16 == kPairCols) {
+                        tc::fence_before_sync();
+                        __syncwarp();
+                        // (TMEM was read, nothing written: no release at the cluster's scope,
+                        // whose fence took longer than the sums)
+                        if (lane == 0) ptx::mbar_remote_arrive(empty_leader + 8u * (it & 1));
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4) {
+                        uint64_t *to = acc + (h + j) / 2;
+                        uint64_t f0 = a2, f1 = a2;
+                        if constexpr (B_ROWS) {
+                            const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(f + 128 + part + h + j);
+                            f0 = mul2(b.x, a2);
+                            f1 = mul2(b.y, a2);
+                        }
+                        to[0] = fma2(pack2(d[j], d[j + 1]), f0, to[0]);
+                        to[1] = fma2(pack2(d[j + 2], d[j + 3]), f1, to[1]);
+                    }
+                }
+            }
+            if (t.chunks > 0) {
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(factors.empty(at.s));
+                at.next();
             }
             const int64_t out0 = DW ? static_cast<int64_t>(t.g) * p.N : 0;  // dweight: a group's first row of y
             const int64_t row0 = out0 + t.row + in_tile, end = out0 + t.end;
-            const int col0 = t.col + 128 * half;
+            const int col0 = t.col + part;
             if (row0 < end && col0 < cols && !(p.add && t.chunks == 0)) {
                 const bool whole = p.vec >= 16 && row0 + 32 <= end;
                 const bool f16 = p.out == VLMCE_F16;
                 const mm::Out y = {static_cast<uint16_t *>(p.y), p.y_ld, whole ? 16 : 2, &maps.y};
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
+                for (int s = 0; s < kPairCols / 32; ++s) {
                     const int col = col0 + 32 * s;
                     float v[32];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = acc[32 * s + j];
+                    for (int j = 0; j < 16; ++j) unpack2(acc[16 * s + j], v[2 * j], v[2 * j + 1]);
                     if constexpr (DW) {
                         if (p.out == VLMCE_F32) {
                             if (col < cols) {
@@ -274,14 +314,13 @@ __global__ void __launch_bounds__(mm::kPairThreads, 1)
                         }
                     }
                     __syncwarp();
-                    const int pair = col0 + 64 * (s / 2);  // the 64 columns of this store
+                    const int pair = col0 + 64 * (s / 2);  // the 64 columns of a store
                     if (pair < cols) {
                         mm::put_seg(y, row0, pair, s & 1, v, end, cols, f16, buf, lane);
                         if (s & 1) mm::put_rest(y, row0, pair, end, cols, buf, lane);
                     }
                 }
             }
-            if (i + step < total) t = pair_tile<DW>(p, table, i + step);
         }
         if (lane == 0) tc::bulk_wait();
     }

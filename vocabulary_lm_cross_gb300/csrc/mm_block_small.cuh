@@ -7,15 +7,14 @@
 // one's sums leave.  Four TMEM buffers of bn columns hold the sums of the last four blocks.
 //
 // Each of the eight epilogue warps has 32 weight rows (a lane each) x bn / 2 rows of x:
-// the weight's factor is a lane's own, x's are put into shared memory by the lanes that
-// fetched them and read by all.  Factors are fetched for four blocks at a time, four to
-// eight blocks ahead (behind the ring's copies an answer takes thousands of clocks).
+// the weight's factor is a lane's own, x's are read by all.
 //
 // Where there are too few tiles for the SMs, `split` CTAs of a cluster share a tile's K;
 // each owns bn / split of the rows, the others push their sums of those into its shared
 // memory, and it adds them in rank order (so the result does not depend on timing).
 //
-// CTA = 10 warps: warp 0 TMA producer, warp 1 TMEM and MMA issuer, warps 2-9 epilogue.
+// CTA = 11 warps: warp 0 TMA producer, warp 1 TMEM and MMA issuer, warps 2-9 epilogue, warp
+// 10 the factors.
 #pragma once
 
 #include <cuda.h>
@@ -26,7 +25,9 @@
 namespace vlmce {
 namespace mmb {
 
-constexpr int kSmallThreads = 320;
+constexpr int kSmallThreads = 352;
+constexpr int kSmallWords = factor_words(128 + 128);  // a block's factors: the weight's rows, rows of x
+constexpr int kSmallFactors = 4 * kFactorSlots * kFactorBatch * kSmallWords;
 constexpr int kSmallBufs = 4;             // TMEM buffers
 constexpr int kSmallWBytes = 128 * 128;   // 128 weight rows x a block of K
 constexpr int kMaxStages = 12;
@@ -43,15 +44,8 @@ __device__ __forceinline__ SmallTile small_tile(const SmallParams &p, const Tabl
     const int l = i - t.tile0[g] * p.nt;
     const int mt = t.tile0[g + 1] - t.tile0[g];
     const int n = l / mt;
-    return {g, t.row0[g] + (l - n * mt) * bn, t.row1[g], n * 128};
+    return {g, t.row[g] + (l - n * mt) * bn, t.row[g + 1], n * 128};
 }
-
-// The factors of four blocks: of a lane's weight row, and of its rows of x (lane, lane +
-// 32).
-template <int NS>
-struct SmallScales {
-    float w[4], x[NS][4];
-};
 
 template <int NC, bool RES>
 __global__ void __launch_bounds__(kSmallThreads, 1)
@@ -76,6 +70,9 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     auto tempty = [&](int b) { return bar0 + 8u * (2 * kMaxStages + kSmallBufs + b); };
     const uint32_t done = bar0 + 8u * (2 * kMaxStages + 2 * kSmallBufs);
 
+    const Factors factors = {ptx::smem_addr(smem + p.factor_offset),
+                             ptx::smem_addr(smem + p.factor_offset) + kSmallFactors, kSmallWords};
+
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = p.split > 1 ? static_cast<int>(ptx::cluster_ctarank()) : 0;
 
@@ -89,6 +86,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
             ptx::mbar_init(tempty(b), 8);
         }
         ptx::mbar_init(done, 1);
+        factors.init(8);
         *abort = 0;
         ptx::fence_mbar_init_cluster();
     }
@@ -180,38 +178,35 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
             tc::mma_commit(done);
             drain_bar(done, 0, p.err);
         }
+    } else if (warp == 10) {
+        Slot at;
+        for (int i = first; i < total; i += step) {
+            const SmallTile t = small_tile(p, table, i, bn);
+            const int64_t w0 = static_cast<int64_t>(t.g) * p.scale_rows;
+            for (int c = c0; c < c1; c += kFactorBatch) {
+                wait_bar(factors.empty(at.s), at.ph ^ 1, abort, p.err);
+                const uint32_t to = factors.at(at.s);
+                if (p.block == 1)
+                    factors_copy<128>(to, kSmallWords, p.ws + c, w0 + t.n, p.ws_ld, p.N - t.n, c1 - c, lane);
+                else
+                    factors_copy<8>(to, kSmallWords, p.ws + c, w0 + t.n / 128, p.ws_ld, 1, c1 - c, lane);
+                factors_copy<bn>(to + 512, kSmallWords, p.xs + c, t.row, p.xs_ld, t.end - t.row, c1 - c, lane);
+                factors_done(factors, at.s);
+                at.next();
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
-        constexpr int NS = (NC + 31) / 32;
         const int half = (warp - 2) >> 2;
         const int wrow = (warp & 3) * 32 + lane;  // weight row of the tile
         const uint32_t tbase = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + half * NC;
-        // [2][NC] factors of x's rows
-        float *xf = reinterpret_cast<float *>(smem + p.scale_offset) + (warp - 2) * 2 * NC;
+        const float *slots = reinterpret_cast<const float *>(smem + p.factor_offset);
+        const int wf = p.block == 1 ? wrow : 0;
         float *part = reinterpret_cast<float *>(smem + p.part_offset);
-        auto fetch = [&](SmallScales<NS> &f, const SmallTile &t, int c) {
-            const int n = t.n + wrow;
-            const float *pw = p.ws + (static_cast<int64_t>(t.g) * p.scale_rows + n / p.block) * p.ws_ld;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) f.w[k] = n < p.N && c + k < c1 ? pw[c + k] : 0.f;
-#pragma unroll
-            for (int q = 0; q < NS; ++q) {
-                const int j = 32 * q + lane, r = t.row + half * NC + j;
-                const float *px = p.xs + static_cast<int64_t>(r) * p.xs_ld;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    f.x[q][k] = j < NC && r < t.end && c + k < c1 ? px[c + k] : 0.f;
-            }
-        };
-        SmallTile t = {};
-        SmallScales<NS> next = {};
-        if (first < total) {
-            t = small_tile(p, table, first, bn);
-            fetch(next, t, c0);
-        }
+        Slot at;
         int it = 0;
         for (int i = first; i < total; i += step) {
-            SmallTile after = {};
-            if (i + step < total) after = small_tile(p, table, i + step, bn);
+            const SmallTile t = small_tile(p, table, i, bn);
             const int n = t.n + wrow;
             const int row = t.row + half * NC;  // of x: this thread's first
             // rows of x whose sums this thread stores, from `row` (split: below)
@@ -228,54 +223,55 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
             float acc[NC];
 #pragma unroll
             for (int j = 0; j < NC; ++j) acc[j] = 0.f;
+            const float *f = nullptr;
 #pragma unroll 1
-            for (int c = c0; c < c1; c += 4) {
-                const SmallScales<NS> f = next;
-                if (c + 4 < c1)
-                    fetch(next, t, c + 4);
-                else if (i + step < total)
-                    fetch(next, after, c0);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (c + k >= c1) break;
-                    float *slot = xf + (it & 1) * NC;
-#pragma unroll
-                    for (int q = 0; q < NS; ++q)
-                        if (32 * q + lane < NC) slot[32 * q + lane] = f.x[q][k];
-                    const int b = it % kSmallBufs;
-                    wait_bar(tfull(b), (it / kSmallBufs) & 1, abort, p.err);
-                    __syncwarp();  // the slot is written; what follows takes the whole warp
-                    tc::fence_after_sync();
-                    const float w = f.w[k];
-                    constexpr int kPiece = NC < 32 ? NC : 32;
-#pragma unroll
-                    for (int h = 0; h < NC; h += kPiece) {
-                        uint32_t d[kPiece];
-                        if constexpr (NC == 8)
-                            tc::tmem_ld8(tbase + b * bn, d);
-                        else if constexpr (NC == 16)
-                            tc::tmem_ld16(tbase + b * bn, d);
-                        else
-                            tc::tmem_ld32(tbase + b * bn + h, d);
-                        tc::tmem_ld_wait();
-                        if (h + kPiece == NC) {
-                            tc::fence_before_sync();
-                            __syncwarp();
-                            if (lane == 0) ptx::mbar_arrive(tempty(b));
-                        }
-#pragma unroll
-                        for (int j = 0; j < kPiece; j += 4) {
-                            const float4 x4 = *reinterpret_cast<const float4 *>(slot + h + j);
-                            float *to = acc + h + j;
-                            to[0] = fmaf(__uint_as_float(d[j]), x4.x * w, to[0]);
-                            to[1] = fmaf(__uint_as_float(d[j + 1]), x4.y * w, to[1]);
-                            to[2] = fmaf(__uint_as_float(d[j + 2]), x4.z * w, to[2]);
-                            to[3] = fmaf(__uint_as_float(d[j + 3]), x4.w * w, to[3]);
-                        }
+            for (int c = c0; c < c1; ++c, ++it) {
+                if ((c - c0) % kFactorBatch == 0) {
+                    if (c > c0) {
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(factors.empty(at.s));
+                        at.next();
                     }
-                    ++it;
+                    wait_bar(factors.full(at.s), at.ph, abort, p.err);
+                    f = slots + at.s * (kFactorBatch * kSmallWords);
+                } else {
+                    f += kSmallWords;
+                }
+                const float w = f[wf];
+                const int b = it % kSmallBufs;
+                wait_bar(tfull(b), (it / kSmallBufs) & 1, abort, p.err);
+                __syncwarp();  // what follows takes the whole warp
+                tc::fence_after_sync();
+                constexpr int kPiece = NC < 32 ? NC : 32;
+#pragma unroll
+                for (int h = 0; h < NC; h += kPiece) {
+                    uint32_t d[kPiece];
+                    if constexpr (NC == 8)
+                        tc::tmem_ld8(tbase + b * bn, d);
+                    else if constexpr (NC == 16)
+                        tc::tmem_ld16(tbase + b * bn, d);
+                    else
+                        tc::tmem_ld32(tbase + b * bn + h, d);
+                    tc::tmem_ld_wait();
+                    if (h + kPiece == NC) {
+                        tc::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(tempty(b));
+                    }
+#pragma unroll
+                    for (int j = 0; j < kPiece; j += 4) {
+                        const float4 x4 = *reinterpret_cast<const float4 *>(f + 128 + half * NC + h + j);
+                        float *to = acc + h + j;
+                        to[0] = fmaf(__uint_as_float(d[j]), x4.x * w, to[0]);
+                        to[1] = fmaf(__uint_as_float(d[j + 1]), x4.y * w, to[1]);
+                        to[2] = fmaf(__uint_as_float(d[j + 2]), x4.z * w, to[2]);
+                        to[3] = fmaf(__uint_as_float(d[j + 3]), x4.w * w, to[3]);
+                    }
                 }
             }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(factors.empty(at.s));
+            at.next();
             if (p.split == 1) {
                 uint16_t *y = p.y + static_cast<int64_t>(row) * p.y_ld + n;
 #pragma unroll
@@ -305,10 +301,9 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
                     p.y[to * p.y_ld + n] = act::to16(v, p.f16);
                 }
             }
-            t = after;
         }
     }
-    if (p.split > 1 && (warp < 2 || first >= total)) {
+    if (p.split > 1 && (warp < 2 || warp == 10 || first >= total)) {
         ptx::cluster_wait_any();
         if (first < total) ptx::cluster_sync_any();  // as the epilogue warps, once
     }

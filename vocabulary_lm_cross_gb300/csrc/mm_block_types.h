@@ -64,7 +64,7 @@ struct SmallParams {
     int chunks;             // K in blocks
     int split;              // CTAs of a cluster that share a tile's K
     int stages, per_stage;
-    int part_offset, scale_offset, table_offset, bar_offset;
+    int part_offset, factor_offset, table_offset, bar_offset;
     int f16;
     int *err;
 };

@@ -18,6 +18,11 @@ __device__ __forceinline__ void cluster_wait_any() {
     asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
+// Arrive (release at this CTA's scope) on a barrier of another CTA of the cluster.
+__device__ __forceinline__ void mbar_remote_arrive(uint32_t remote_bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(remote_bar) : "memory");
+}
+
 // 16 bytes from global to shared memory without a register in between; each
 // thread's copies complete in groups (cp_async_wait<N>: all but the last N).
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
