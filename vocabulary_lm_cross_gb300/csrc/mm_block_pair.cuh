@@ -1,23 +1,30 @@
 // mm_block_pair.cuh -- products with block scales on CTA pairs (mm_pair.cuh): tiles of
-// 256 x 192, each CTA with 128 rows of operand A and all 192 of B in its accumulators.
+// 256 x 256, each CTA with 128 rows of operand A and all 256 of B in its accumulators.
 //
 //   forward   A = x (rows of one group), B = the group's weight
 //   dweight   A = dyt, B = xt, over a group's part of their common columns
 //
-// The sums of a block are in one of two TMEM buffers while the next block's form in the
-// other; 12 epilogue warps, each with 32 rows x 64 columns of running sums in registers,
-// empty it.  A's factor is a thread's own.  B's is one for the 64 columns (a weight's
-// blocks of 128 x 128: acc += (a b) d), or one for each column (B_ROWS).  192 columns, since
-// the running sums of 256 leave no registers to work with (128 of a thread's 168; with
-// setmaxnreg's 224 the loop's multiply-adds took ten clocks each).
+// A block's sums are in one of two TMEM buffers while the next block's form in the other;
+// eight epilogue warps, each with 32 rows x 128 columns of running sums in registers (128 a
+// thread; the control warps give theirs up), empty it, 16 columns a load.  A's factor is a
+// thread's own.  B's is one for the 128 columns (a weight's blocks of 128 x 128: acc += (a
+// b) d), or one for each column (B_ROWS), read from shared memory: twice the arithmetic,
+// and as many bytes through the load unit as come from TMEM.
 //
-// One commit per block: "the stage is free" and "the block's sums are there" are the same
-// event, and both CTAs' epilogue warps wait on the stage's barrier, as the copies do.
+// What bounds it: the epilogue warps' own instructions, about 920 clocks a block, where the
+// products take 512 and their hand-over 400 (two buffers: (512 + 400 + the time a buffer is
+// being read) / 2).  8192 x 8192 x 4096 242 us = 2.27 PFLOP/s (a scale for each row, without
+// this epilogue: 174 us), with a factor for each column 428 us.  Tried: loads of 32 columns
+// (255 us), a load ahead of its sums (273), single instead of packed multiply-adds (254),
+// four buffers of 128 columns (330), 256 x 192 tiles on twelve warps without a change of
+// registers (292).  One commit per block: "the stage is free" and "the block's sums are
+// there" are the same event, and both CTAs' epilogue warps wait on the stage's barrier, as
+// the copies do (a commit for each 267 us).
 //
 // The tiles are dealt out in order; a group's tiles go down 8 tiles of rows before they go
 // across, so those in flight share operands.
 //
-// Warps: 0 and 2 fetch A and B, 1 TMEM and MMA issuer, 3 fetches the factors, 4-15 epilogue.
+// Warps: 0 and 2 fetch A and B, 1 TMEM and MMA issuer, 3 fetches the factors, 4-11 epilogue.
 #pragma once
 
 #include <cuda.h>
@@ -96,7 +103,7 @@ template <bool DW, bool B_ROWS>
 __global__ void __launch_bounds__(kPairThreads, 1)
     mm_block_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ PairParams p) {
     extern __shared__ unsigned char smem_raw[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         tc::prefetch_tensormap(&maps.a);
         tc::prefetch_tensormap(&maps.b);
@@ -114,6 +121,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     q.stages = kPairStages;
     const Table table = table_at(smem + kPairTableAt, p.groups);
     table_fill(table, p.offsets, p.groups, p.T, DW ? 1 : 256, DW ? 128 : 1, p.err);
+    const uint32_t tmem = __shfl_sync(0xffffffffu, q.tmem, 0);
     const int rank = static_cast<int>(q.rank);
     const int first = static_cast<int>(ptx::cluster_id_x()), step = static_cast<int>(ptx::ncluster_x());
     const int total = DW ? p.groups * p.mt * p.nt : table.tile0[p.groups] * p.nt;
@@ -146,29 +154,35 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 if (warp == 0) mm::drain_loads(q, issued);
             }
         } else if (warp == 1) {
-            if (rank == 0 && lane == 0) {
+            if (rank == 0) {
+                // The whole warp walks, so that descriptors and addresses are uniform values
+                // (in a branch of one lane each product waited about 100 clocks for them).
                 const uint32_t idesc = tc::idesc_bf16_f32(256, kPairN, false, false, true);
                 mm::Ring<1> r;
                 int it = 0;
                 for (int i = first; i < total; i += step) {
-                    const int chunks = pair_tile<DW>(p, table, i).chunks;
+                    const int chunks = __shfl_sync(0xffffffffu, pair_tile<DW>(p, table, i).chunks, 0);
                     for (int c = 0; c < chunks; ++c, ++it) {
                         const int b = it & 1;
-                        const uint32_t d = q.tmem + static_cast<uint32_t>(b * 256);
+                        const uint32_t d = tmem + static_cast<uint32_t>(b * 256);
                         wait_bar(q.full(r.s), r.ph, q.abort, q.err);
                         const uint64_t ad = tc::smem_desc_sw128(q.chunk(r.s, 0), 16, 1024);
                         const uint64_t bd = tc::smem_desc_sw128(q.chunk(r.s, 0) + mm::kOpBytes, 16, 1024);
                         wait_bar(buf_empty + 8u * b, ((it >> 1) & 1) ^ 1, q.abort, q.err);
+                        __syncwarp();
                         tc::fence_after_sync();
+                        if (lane == 0) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)  // (32 bytes on: 2 in a descriptor)
-                            tc::mma_f8_pair(d, ad + 2 * k, bd + 2 * k, idesc, k != 0);
-                        // in both CTAs: the stage is free, and its block's sums are there
-                        tc::mma_commit_pair(q.empty(r.s), 3u);
+                            for (int k = 0; k < 4; ++k)  // (32 bytes on: 2 in a descriptor)
+                                tc::mma_f8_pair(d, ad + 2 * k, bd + 2 * k, idesc, k != 0);
+                            // in both CTAs: the stage is free, and its block's sums are there
+                            tc::mma_commit_pair(q.empty(r.s), 3u);
+                        }
+                        __syncwarp();
                         r.next(q);
                     }
                 }
-                mm::mma_finish(q);
+                if (lane == 0) mm::mma_finish(q);
             }
         } else {
             Slot at;
@@ -213,9 +227,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             uint64_t acc[kPairCols / 2];  // two columns each
 #pragma unroll
             for (int j = 0; j < kPairCols / 2; ++j) acc[j] = 0;
-            const float *f = nullptr;
-#pragma unroll 1
-            for (int c = 0; c < t.chunks; ++c, ++it) {
+            const float *f = slots;
+            auto factor = [&](int c) {  // of block c, in order
                 if (c % kFactorBatch == 0) {
                     if (c > 0) {
                         __syncwarp();
@@ -227,18 +240,26 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 } else {
                     f += kPairWords;
                 }
-                float a = f[(warp & 3) * 32 + lane];
-                if constexpr (!B_ROWS) a *= f[block];
+                const float a = f[(warp & 3) * 32 + lane];
+                return B_ROWS ? a : a * f[block];
+            };
+            const uint32_t d0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + part;
+            float next = B_ROWS && t.chunks > 0 ? factor(0) : 0.f;
+#pragma unroll 1
+            for (int c = 0; c < t.chunks; ++c, ++it) {
+                // (fetched ahead where the columns' factors take registers too: 8192 x 8192 x 4096
+                // 468 -> 428 us; else it costs, 242 -> 267)
+                if (!B_ROWS) next = factor(c);
+                const uint64_t a = both(next);
+                const float *fb = f + 128 + part;
                 wait_bar(q.empty(r.s), r.ph, q.abort, q.err);
                 r.next(q);
                 __syncwarp();  // each lane left the wait by itself; TMEM loads take the whole warp
                 tc::fence_after_sync();
-                const uint32_t d0 = q.tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 256 * (it & 1) + part;
-                const uint64_t a2 = both(a);
 #pragma unroll
                 for (int h = 0; h < kPairCols; h += 16) {
                     uint32_t d[16];
-                    tc::tmem_ld16(d0 + h, d);
+                    tc::tmem_ld16(d0 + 256 * (it & 1) + h, d);
                     tc::tmem_ld_wait();
                     if (h + 16 == kPairCols) {
                         tc::fence_before_sync();
@@ -250,16 +271,17 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 16; j += 4) {
                         uint64_t *to = acc + (h + j) / 2;
-                        uint64_t f0 = a2, f1 = a2;
+                        uint64_t f0 = a, f1 = a;
                         if constexpr (B_ROWS) {
-                            const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(f + 128 + part + h + j);
-                            f0 = mul2(b.x, a2);
-                            f1 = mul2(b.y, a2);
+                            const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(fb + h + j);
+                            f0 = mul2(b.x, a);
+                            f1 = mul2(b.y, a);
                         }
                         to[0] = fma2(pack2(d[j], d[j + 1]), f0, to[0]);
                         to[1] = fma2(pack2(d[j + 2], d[j + 3]), f1, to[1]);
                     }
                 }
+                if (B_ROWS && c + 1 < t.chunks) next = factor(c + 1);
             }
             if (t.chunks > 0) {
                 __syncwarp();
