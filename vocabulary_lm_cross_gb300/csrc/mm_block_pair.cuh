@@ -47,6 +47,9 @@ constexpr int kPairChunk = mm::kOpBytes + kPairBBytes;
 constexpr int kPairGroupM = 8;
 // Shared memory: mm_pair.cuh's, whose ring and output buffers are these instead.
 constexpr int kPairStages = 5;
+// with a factor for each column, the last stage's memory is where sums change their layout
+constexpr int kPairStagesRows = 4;
+static_assert(kPairEpiWarps * mm::kOutBytes <= kPairChunk, "32 x 32 sums of each warp");
 constexpr int kPairWords = factor_words(128 + kPairN);  // a block's factors: the CTA's rows of A, the columns
 constexpr int kPairOutAt = kPairStages * kPairChunk;
 constexpr int kPairFactorsAt = kPairOutAt + kPairEpiWarps * mm::kOutBytes;
@@ -79,6 +82,27 @@ __device__ __forceinline__ PairTile pair_tile(const PairParams &p, const Table &
     }
 }
 
+// 32 x 32 sums as tmem_ld_16x32 lays them out (v[16 i + 4 g + 2 r + e]: row 16 i + 8 r +
+// lane / 4, column 8 g + 2 (lane % 4) + e) to a row per lane, through the warp's `buf`.
+__device__ __forceinline__ void to_rows(float (&v)[32], unsigned char *buf, int lane) {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = 8 * i + (lane >> 2);
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int unit = 2 * g + ((lane & 3) >> 1);  // of 16 bytes
+            *reinterpret_cast<float2 *>(buf + row * 128 + ((unit ^ (row & 7)) << 4) + 8 * (lane & 1)) =
+                make_float2(v[16 * (i >> 1) + 4 * g + 2 * (i & 1)], v[16 * (i >> 1) + 4 * g + 2 * (i & 1) + 1]);
+        }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float4 u = *reinterpret_cast<const float4 *>(buf + lane * 128 + ((j ^ (lane & 7)) << 4));
+        v[4 * j] = u.x, v[4 * j + 1] = u.y, v[4 * j + 2] = u.z, v[4 * j + 3] = u.w;
+    }
+}
 // 32 rows x 32 columns of fp32 whose rows TMA cannot take: through the warp's buffer, so
 // that its accesses cover consecutive addresses.
 __device__ __forceinline__ void put_f32_rows(float *base, int64_t ld, int64_t row0, int col, const float (&v)[32],
@@ -118,7 +142,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         for (int b = 0; b < 2; ++b) ptx::mbar_init(buf_empty + 8u * b, 2 * kPairEpiWarps);  // of both CTAs
     }
     mm::Pair<1> q = mm::pair_setup<1>(smem_raw, p.err, 1, kPairChunk);
-    q.stages = kPairStages;
+    q.stages = B_ROWS ? kPairStagesRows : kPairStages;
     const Table table = table_at(smem + kPairTableAt, p.groups);
     table_fill(table, p.offsets, p.groups, p.T, DW ? 1 : 256, DW ? 128 : 1, p.err);
     const uint32_t tmem = __shfl_sync(0xffffffffu, q.tmem, 0);
@@ -228,7 +252,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
             for (int j = 0; j < kPairCols / 2; ++j) acc[j] = 0;
             const float *f = slots;
-            auto factor = [&](int c) {  // of block c, in order
+            auto advance = [&](int c) {  // f: block c's factors, in order
                 if (c % kFactorBatch == 0) {
                     if (c > 0) {
                         __syncwarp();
@@ -240,48 +264,64 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 } else {
                     f += kPairWords;
                 }
-                const float a = f[(warp & 3) * 32 + lane];
-                return B_ROWS ? a : a * f[block];
             };
             const uint32_t d0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + part;
-            float next = B_ROWS && t.chunks > 0 ? factor(0) : 0.f;
 #pragma unroll 1
             for (int c = 0; c < t.chunks; ++c, ++it) {
-                // (fetched ahead where the columns' factors take registers too: 8192 x 8192 x 4096
-                // 468 -> 428 us; else it costs, 242 -> 267)
-                if (!B_ROWS) next = factor(c);
-                const uint64_t a = both(next);
-                const float *fb = f + 128 + part;
+                advance(c);
+                // (fetching it a block ahead costs: 242 -> 267 us)
+                float af[B_ROWS ? 4 : 1];
+#pragma unroll
+                for (int i = 0; i < (B_ROWS ? 4 : 1); ++i)
+                    af[i] = f[(warp & 3) * 32 + (B_ROWS ? 8 * i + (lane >> 2) : lane)];
+                if constexpr (!B_ROWS) af[0] *= f[block];
                 wait_bar(q.empty(r.s), r.ph, q.abort, q.err);
                 r.next(q);
                 __syncwarp();  // each lane left the wait by itself; TMEM loads take the whole warp
                 tc::fence_after_sync();
+                const uint32_t from = d0 + 256 * (it & 1);
+                auto release = [&] {
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    // (TMEM was read, nothing written: no release at the cluster's scope,
+                    // whose fence took longer than the sums)
+                    if (lane == 0) ptx::mbar_remote_arrive(empty_leader + 8u * (it & 1));
+                };
+                if constexpr (B_ROWS) {
 #pragma unroll
-                for (int h = 0; h < kPairCols; h += 16) {
-                    uint32_t d[16];
-                    tc::tmem_ld16(d0 + 256 * (it & 1) + h, d);
-                    tc::tmem_ld_wait();
-                    if (h + 16 == kPairCols) {
-                        tc::fence_before_sync();
-                        __syncwarp();
-                        // (TMEM was read, nothing written: no release at the cluster's scope,
-                        // whose fence took longer than the sums)
-                        if (lane == 0) ptx::mbar_remote_arrive(empty_leader + 8u * (it & 1));
-                    }
+                    for (int h = 0; h < kPairCols; h += 32) {
+                        uint64_t b[4];
 #pragma unroll
-                    for (int j = 0; j < 16; j += 4) {
-                        uint64_t *to = acc + (h + j) / 2;
-                        uint64_t f0 = a, f1 = a;
-                        if constexpr (B_ROWS) {
-                            const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(fb + h + j);
-                            f0 = mul2(b.x, a);
-                            f1 = mul2(b.y, a);
+                        for (int g = 0; g < 4; ++g)
+                            b[g] = *reinterpret_cast<const uint64_t *>(f + 128 + part + h + 8 * g + 2 * (lane & 3));
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {  // 16 rows each
+                            uint32_t d[16];
+                            tc::tmem_ld_16x32(from + (static_cast<uint32_t>(16 * i) << 16) + h, d);
+                            tc::tmem_ld_wait();
+                            if (h + 32 == kPairCols && i == 1) release();
+                            uint64_t *to = acc + h / 2 + 8 * i;
+#pragma unroll
+                            for (int g = 0; g < 4; ++g) {
+                                to[2 * g] = fma2(pack2(d[4 * g], d[4 * g + 1]), mul2(b[g], both(af[2 * i])), to[2 * g]);
+                                to[2 * g + 1] = fma2(pack2(d[4 * g + 2], d[4 * g + 3]), mul2(b[g], both(af[2 * i + 1])),
+                                                     to[2 * g + 1]);
+                            }
                         }
-                        to[0] = fma2(pack2(d[j], d[j + 1]), f0, to[0]);
-                        to[1] = fma2(pack2(d[j + 2], d[j + 3]), f1, to[1]);
+                    }
+                } else {
+                    const uint64_t a = both(af[0]);
+#pragma unroll
+                    for (int h = 0; h < kPairCols; h += 16) {
+                        uint32_t d[16];
+                        tc::tmem_ld16(from + h, d);
+                        tc::tmem_ld_wait();
+                        if (h + 16 == kPairCols) release();
+                        uint64_t *to = acc + h / 2;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) to[j] = fma2(pack2(d[2 * j], d[2 * j + 1]), a, to[j]);
                     }
                 }
-                if (B_ROWS && c + 1 < t.chunks) next = factor(c + 1);
             }
             if (t.chunks > 0) {
                 __syncwarp();
@@ -301,6 +341,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     float v[32];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) unpack2(acc[16 * s + j], v[2 * j], v[2 * j + 1]);
+                    if constexpr (B_ROWS) to_rows(v, smem + kPairStagesRows * kPairChunk + (warp - 4) * mm::kOutBytes, lane);
                     if constexpr (DW) {
                         if (p.out == VLMCE_F32) {
                             if (col < cols) {

@@ -118,6 +118,18 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
           "=r"(r[7])
         : "r"(taddr));
 }
+// 16 lanes x 32 consecutive fp32 columns of TMEM into 16 registers per thread: of each
+// eight columns 8 g .., thread i gets columns 2 (i % 4) and the next of lane i / 4 (r[4 g],
+// r[4 g + 1]) and of lane i / 4 + 8 (r[4 g + 2], r[4 g + 3]).
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
 // 32 lanes x 16 consecutive fp32 columns of TMEM into 16 registers per thread.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
