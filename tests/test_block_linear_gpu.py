@@ -89,9 +89,13 @@ def check_dense(T, N, K, dtype="bf16", by_row=False, residual=False, pad=0, seed
 
 SMALL = [(1, 1, 1), (1, 128, 128), (1, 4096, 2048), (1, 100, 16), (2, 300, 640), (3, 129, 200), (16, 256, 4096),
          (17, 257, 1000), (40, 1000, 136), (64, 136, 16384), (100, 512, 512), (128, 8, 100), (129, 96, 1664),
-         (8, 20000, 256)]
+         (8, 20000, 256),
+         # K shared by clusters of two to eight, with each tile
+         (1, 12000, 2048), (1, 7500, 1024), (5, 3000, 2048), (20, 7500, 2048), (33, 5000, 2048), (130, 1500, 2048),
+         (100, 7500, 2048), (200, 1500, 2048), (200, 500, 2048)]
 PAIRS = [(193, 8, 16), (256, 256, 128), (257, 264, 640), (300, 1001, 200), (512, 128, 4096), (700, 777, 1000),
-         (1024, 100, 136), (2000, 520, 256)]
+         (1024, 100, 136), (2000, 520, 256),
+         (2000, 2600, 264), (513, 9000, 136), (130, 12000, 512)]
 
 
 @pytest.mark.parametrize("by_row", [False, True])
@@ -125,7 +129,8 @@ def group_rows(g, E, most, align=1):
 
 
 EXPERTS = [(4, 3, 96, 128), (7, 20, 300, 256), (33, 9, 136, 640), (64, 1, 512, 384), (5, 100, 264, 1000),
-           (16, 50, 1000, 200), (3, 700, 264, 512), (2, 1000, 100, 136), (1000, 1, 64, 128)]
+           (16, 50, 1000, 200), (3, 700, 264, 512), (2, 1000, 100, 136), (1000, 1, 64, 128), (3, 1400, 1000, 600), (40, 60, 1000, 384),
+           (6, 150, 2000, 384), (10, 130, 1200, 256)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])

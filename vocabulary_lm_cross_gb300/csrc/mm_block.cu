@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <cmath>
 #include <mutex>
 
 #include "device_errors.h"
@@ -106,53 +107,88 @@ bool e4m3_map(CUtensorMap *m, const void *p, int64_t rows, int64_t cols, int64_t
 // How a forward product is run.
 struct Plan {
     bool pair;
-    int bn, split, per_stage, stages;
+    int bn, split, per_sm, per_stage, stages;
     int part, factors, table, bar, smem;  // small: where its shared memory's parts start, and its size
+    double clocks;                        // estimate
 };
 
-bool small_layout(const Fwd &f, int bn, int split, int per_stage, Plan *p) {
+bool small_layout(const Fwd &f, int bn, int split, int per_sm, int per_stage, Plan *p) {
     const int chunk = kSmallWBytes + bn * 128;
-    const int part = split > 1 ? bn * 512 : 0, factors = kSmallFactors + kFactorBarBytes;
+    const int part = split > 1 ? (bn + split - 1) / split * split * 512 : 0;
+    const int factors = kSmallFactors + kFactorBarBytes;
     const int table = static_cast<int>(round_up(table_bytes(static_cast<int>(f.groups)), 16));
+    const int budget = kSmSmem / per_sm - kSmemReserved;
     const int fixed = 1024 + part + factors + table + kSmallTail;
     const int64_t chunks = (f.K + 127) / 128;
-    const int steps = static_cast<int>((chunks + split - 1) / split);
     p->pair = false;
     p->bn = bn;
     p->split = split;
+    p->per_sm = per_sm;
     p->per_stage = per_stage;
-    p->stages = std::min((kSmallSmemMax - fixed) / (per_stage * chunk), kMaxStages);
-    if (p->stages < 2 || split > chunks) return false;
-    (void)steps;
+    p->stages = std::min((budget - fixed) / (per_stage * chunk), kMaxStages);
+    if (p->stages < 2 || split > chunks || (per_sm > 1 && bn > 2 * kSmallTwoNc)) return false;
     p->part = p->stages * per_stage * chunk;
     p->factors = p->part + part;
     p->table = p->factors + factors;
     p->bar = p->table + table;
     p->smem = std::max(p->bar + kSmallTail + 1024, kSmallBufs * bn * kSmemPerTmemCol - kSmemReserved);
-    // one CTA per SM
-    p->smem = std::max(p->smem, kSmSmem / 2 - kSmemReserved + 1);
+    // no more CTAs per SM than that
+    p->smem = std::max(p->smem, kSmSmem / (per_sm + 1) - kSmemReserved + 16);
     return true;
 }
 
 int64_t groups_used(const Fwd &f) { return f.offsets ? std::min(f.groups, f.T) : 1; }
 
+// Estimates in SM clocks at 1.9 GHz, from a sweep on GB300 of every bn, split, per_sm and
+// per_stage over 22 products (T = 1 .. 8192, dense and of 8 .. 128 experts): the chosen plan
+// is the fastest or within 8 % of it.  A block costs an SM kSmallBlock[bn] clocks (of a pair
+// tile kPairBlock) and the weights come from HBM at 6.8 TB/s at best.  Where a group's rows
+// are known on the device only, a group takes half a tile more than its average.  Two CTAs
+// per SM are for tiles of 16 rows (T 512, 32 experts, K 4096, N 4096 95.8 us, one CTA 107),
+// two blocks a stage wherever there are two (32 rows 100.9 us, one block 115.5).
+constexpr double kHbmBytesPerClock = 3570.;
+constexpr int kBns[4] = {16, 32, 64, 128};
+constexpr double kSmallBlock[4] = {480., 800., 900., 1100.}, kPairBlock = 1100.;
+constexpr double kLoneCta = 1.25;  // one CTA on an SM that could take two
+constexpr double kSmallCta = 6000., kPairCta = 7500., kSplitSync = 1500.;
+
 Plan choose(const Fwd &f, const Capacity &cap) {
-    Plan p = {};
     const int64_t used = groups_used(f);
-    const double rows = static_cast<double>(f.T) / static_cast<double>(used);  // of a group, on average
-    if (rows > 192) {
-        p.pair = true;
-        return p;
-    }
-    int bn = 16;
-    while (bn < 128 && bn < rows * 1.25) bn *= 2;
-    const int64_t nt = (f.N + 127) / 128;
-    const int64_t tiles = nt * (f.offsets ? used + f.T / bn : (f.T + bn - 1) / bn);
+    const double rows = static_cast<double>(f.T) / static_cast<double>(used);  // of a group
     const int64_t chunks = (f.K + 127) / 128;
-    int split = 1;
-    while (split < kMaxSplit && tiles * split * 2 <= cap.sms && chunks >= split * 4) split *= 2;
-    if (!small_layout(f, bn, split, chunks / split >= 2 ? 2 : 1, &p)) p.pair = true;
-    return p;
+    const double hbm = static_cast<double>(used) * f.N * f.K / kHbmBytesPerClock;
+    auto tiles_of = [&](int step, int64_t across) {
+        const double down = f.offsets ? std::max(1., rows / step + 0.5) * used
+                                      : static_cast<double>((f.T + step - 1) / step);
+        return down * static_cast<double>(across);
+    };
+    auto joined = [&](double own) { return std::sqrt(std::hypot(own * own, hbm * hbm)); };
+    Plan best = {};
+    best.pair = true;
+    best.clocks = joined(std::ceil(tiles_of(256, (f.N + kPairN - 1) / kPairN) / cap.pairs) *
+                         chunks * kPairBlock) + kPairCta;
+    for (int i = 0; i < 4; ++i) {
+        const int bn = kBns[i], per_sm = bn <= 2 * kSmallTwoNc ? 2 : 1;
+        const double tiles = tiles_of(bn, (f.N + 127) / 128);
+        if (tiles > 1e6) continue;  // pair tiles
+        for (int split = 1; split <= kMaxSplit && split <= chunks; ++split) {
+            const double ctas = tiles * split;
+            // A shared tile is a cluster's only one, so a second wave starts from nothing (T
+            // 128, K 4096, N 12288 in three parts 49.6 us, whole 23.4).
+            if (split > 1 && ctas > per_sm * cap.sms) break;
+            const int64_t each = (chunks + split - 1) / split;
+            const int at_once = ctas <= cap.sms ? 1 : per_sm;
+            const double own = std::ceil(ctas / (cap.sms * at_once)) * at_once * each * kSmallBlock[i] *
+                               (at_once < per_sm ? kLoneCta : 1.);
+            const double clocks = joined(own) + kSmallCta + (split > 1 ? kSplitSync + 30. * bn : 0.);
+            Plan p = {};
+            if (clocks < best.clocks && small_layout(f, bn, split, per_sm, each >= 2 ? 2 : 1, &p)) {
+                best = p;
+                best.clocks = clocks;
+            }
+        }
+    }
+    return best;
 }
 
 cudaError_t forward_small(const Fwd &f, const Capacity &cap, const Plan &plan, cudaStream_t s) {
@@ -191,7 +227,7 @@ cudaError_t forward_small(const Fwd &f, const Capacity &cap, const Plan &plan, c
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     launch_attributes(attr, static_cast<unsigned>(plan.split));
-    cfg.gridDim = dim3(static_cast<unsigned>(plan.split > 1 ? most * plan.split : std::min<int64_t>(most, cap.sms)),
+    cfg.gridDim = dim3(static_cast<unsigned>(plan.split > 1 ? most * plan.split : std::min<int64_t>(most, cap.sms * plan.per_sm)),
                        1, 1);
     cfg.blockDim = dim3(kSmallThreads, 1, 1);
     cfg.dynamicSmemBytes = static_cast<size_t>(plan.smem);

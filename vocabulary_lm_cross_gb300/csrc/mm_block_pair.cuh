@@ -275,6 +275,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 for (int i = 0; i < (B_ROWS ? 4 : 1); ++i)
                     af[i] = f[(warp & 3) * 32 + (B_ROWS ? 8 * i + (lane >> 2) : lane)];
                 if constexpr (!B_ROWS) af[0] *= f[block];
+                uint64_t b[B_ROWS ? 16 : 1];
+                if constexpr (B_ROWS) {
+#pragma unroll
+                    for (int g = 0; g < 16; ++g)
+                        b[g] = *reinterpret_cast<const uint64_t *>(f + 128 + part + 8 * g + 2 * (lane & 3));
+                }
                 wait_bar(q.empty(r.s), r.ph, q.abort, q.err);
                 r.next(q);
                 __syncwarp();  // each lane left the wait by itself; TMEM loads take the whole warp
@@ -290,10 +296,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 if constexpr (B_ROWS) {
 #pragma unroll
                     for (int h = 0; h < kPairCols; h += 32) {
-                        uint64_t b[4];
-#pragma unroll
-                        for (int g = 0; g < 4; ++g)
-                            b[g] = *reinterpret_cast<const uint64_t *>(f + 128 + part + h + 8 * g + 2 * (lane & 3));
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {  // 16 rows each
                             uint32_t d[16];
@@ -303,8 +305,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                             uint64_t *to = acc + h / 2 + 8 * i;
 #pragma unroll
                             for (int g = 0; g < 4; ++g) {
-                                to[2 * g] = fma2(pack2(d[4 * g], d[4 * g + 1]), mul2(b[g], both(af[2 * i])), to[2 * g]);
-                                to[2 * g + 1] = fma2(pack2(d[4 * g + 2], d[4 * g + 3]), mul2(b[g], both(af[2 * i + 1])),
+                                to[2 * g] = fma2(pack2(d[4 * g], d[4 * g + 1]), mul2(b[h / 8 + g], both(af[2 * i])), to[2 * g]);
+                                to[2 * g + 1] = fma2(pack2(d[4 * g + 2], d[4 * g + 3]), mul2(b[h / 8 + g], both(af[2 * i + 1])),
                                                      to[2 * g + 1]);
                             }
                         }

@@ -10,7 +10,7 @@
 // the weight's factor is a lane's own, x's are read by all.
 //
 // Where there are too few tiles for the SMs, `split` CTAs of a cluster share a tile's K;
-// each owns bn / split of the rows, the others push their sums of those into its shared
+// each owns as many of the rows, the others push their sums of those into its shared
 // memory, and it adds them in rank order (so the result does not depend on timing).
 //
 // CTA = 11 warps: warp 0 TMA producer, warp 1 TMEM and MMA issuer, warps 2-9 epilogue, warp
@@ -36,6 +36,9 @@ constexpr int kMaxSplit = 8;
 constexpr int kSmallBars = 2 * kMaxStages + 2 * kSmallBufs + 1;
 constexpr int kSmallTail = 8 * kSmallBars + 16;
 
+// Two CTAs may share an SM where a thread has few sums.
+constexpr int kSmallTwoNc = 8;
+
 struct SmallTile {
     int g, row, end, n;  // group, first row of x and the group's end, first weight row of the group
 };
@@ -48,7 +51,7 @@ __device__ __forceinline__ SmallTile small_tile(const SmallParams &p, const Tabl
 }
 
 template <int NC, bool RES>
-__global__ void __launch_bounds__(kSmallThreads, 1)
+__global__ void __launch_bounds__(kSmallThreads, NC <= kSmallTwoNc ? 2 : 1)
     mm_block_small_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx,
                           const __grid_constant__ SmallParams p) {
     constexpr int bn = 2 * NC;
@@ -73,7 +76,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     const Factors factors = {ptx::smem_addr(smem + p.factor_offset),
                              ptx::smem_addr(smem + p.factor_offset) + kSmallFactors, kSmallWords};
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
     const int rank = p.split > 1 ? static_cast<int>(ptx::cluster_ctarank()) : 0;
 
     if (threadIdx.x == 0) {
@@ -101,7 +104,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     ptx::griddep_launch_dependents();
     if (p.split > 1) ptx::cluster_arrive_any();  // this CTA has started
     ptx::griddep_wait();
@@ -146,38 +149,43 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = tc::idesc_bf16_f32(128, bn, false, false, true);
-            int s = 0;
-            uint32_t ph = 0;
-            int it = 0;
-            for (int i = first; i < total; i += step) {
-                for (int c = c0; c < c1; c += p.per_stage) {
-                    wait_bar(full(s), ph, abort, p.err);
-                    const int n = min(p.per_stage, c1 - c);
-                    for (int j = 0; j < n; ++j, ++it) {
-                        const int b = it % kSmallBufs;
-                        wait_bar(tempty(b), ((it / kSmallBufs) & 1) ^ 1, abort, p.err);
-                        tc::fence_after_sync();
-                        const uint32_t sa = ring + s * stage_bytes + j * chunk_bytes;
-                        const uint32_t d = tmem + static_cast<uint32_t>(b * bn);
+        // the whole warp walks, so that descriptors are uniform values (mm_block_pair.cuh)
+        const uint32_t idesc = tc::idesc_bf16_f32(128, bn, false, false, true);
+        int s = 0;
+        uint32_t ph = 0;
+        int it = 0;
+        for (int i = first; i < total; i += step) {
+            for (int c = c0; c < c1; c += p.per_stage) {
+                wait_bar(full(s), ph, abort, p.err);
+                const int n = min(p.per_stage, c1 - c);
+                for (int j = 0; j < n; ++j, ++it) {
+                    const int b = it % kSmallBufs;
+                    const uint32_t sa = ring + s * stage_bytes + j * chunk_bytes;
+                    const uint64_t wd = tc::smem_desc_sw128(sa, 16, 1024);
+                    const uint64_t xd = tc::smem_desc_sw128(sa + kSmallWBytes, 16, 1024);
+                    wait_bar(tempty(b), ((it / kSmallBufs) & 1) ^ 1, abort, p.err);
+                    __syncwarp();
+                    tc::fence_after_sync();
+                    if (lane == 0) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            tc::mma_f8(d, tc::smem_desc_sw128(sa + 32 * k, 16, 1024),
-                                       tc::smem_desc_sw128(sa + kSmallWBytes + 32 * k, 16, 1024), idesc,
-                                       k != 0);
+                        for (int k = 0; k < 4; ++k)  // (32 bytes on: 2 in a descriptor)
+                            tc::mma_f8(tmem + static_cast<uint32_t>(b * bn), wd + 2 * k, xd + 2 * k, idesc, k != 0);
                         tc::mma_commit(tfull(b));
                     }
-                    tc::mma_commit(empty(s));
-                    if (++s == p.stages) {
-                        s = 0;
-                        ph ^= 1;
-                    }
+                    __syncwarp();
+                }
+                if (lane == 0) tc::mma_commit(empty(s));
+                if (++s == p.stages) {
+                    s = 0;
+                    ph ^= 1;
                 }
             }
+        }
+        if (lane == 0) {
             tc::mma_commit(done);
             drain_bar(done, 0, p.err);
         }
+        __syncwarp();
     } else if (warp == 10) {
         Slot at;
         for (int i = first; i < total; i += step) {
@@ -210,8 +218,9 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
             const int n = t.n + wrow;
             const int row = t.row + half * NC;  // of x: this thread's first
             // rows of x whose sums this thread stores, from `row` (split: below)
-            uint16_t res[RES ? NC : 1];
-            if constexpr (RES) {
+            constexpr bool kAhead = RES && NC <= 16;  // (more would take the sums' registers)
+            uint16_t res[kAhead ? NC : 1];
+            if constexpr (kAhead) {
                 if (p.split == 1) {
 #pragma unroll
                     for (int j = 0; j < NC; ++j)
@@ -278,12 +287,15 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
                 for (int j = 0; j < NC; ++j)
                     if (n < p.N && row + j < t.end) {
                         float v = acc[j];
-                        if constexpr (RES) v += act::from16(res[j], p.f16);
+                        if constexpr (kAhead)
+                            v += act::from16(res[j], p.f16);
+                        else if constexpr (RES)
+                            v += act::from16(p.residual[static_cast<int64_t>(row + j) * p.residual_ld + n], p.f16);
                         y[static_cast<int64_t>(j) * p.y_ld] = act::to16(v, p.f16);
                     }
             } else {
-                // [from][bn / split rows of x][128 weight rows]
-                const int own = bn / p.split;
+                // [from][own rows of x][128 weight rows]
+                const int own = (bn + p.split - 1) / p.split;
                 ptx::cluster_wait_any();
                 const uint32_t at = ptx::smem_addr(part) + 4u * (rank * own * 128 + wrow);
 #pragma unroll
@@ -294,7 +306,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
                 ptx::cluster_sync_any();
                 for (int r = half; r < own; r += 2) {
                     const int64_t to = t.row + rank * own + r;
-                    if (n >= p.N || to >= t.end) continue;
+                    if (n >= p.N || to >= t.end || rank * own + r >= bn) continue;
                     float v = 0.f;
                     for (int from = 0; from < p.split; ++from) v += part[(from * own + r) * 128 + wrow];
                     if constexpr (RES) v += act::from16(p.residual[to * p.residual_ld + n], p.f16);
