@@ -105,6 +105,50 @@ struct Cols {
     __device__ __forceinline__ Cols(int64_t base, int lane) : c(base + (VEC ? 8 * lane : lane)) {}
     __device__ __forceinline__ bool in(int i, int64_t H) const { return VEC ? c < H : c + 32 * i < H; }
 
+    // The values as they are in memory, to have many on their way in few registers.
+    template <int DT>
+    struct Raw {
+        static constexpr int kWords = VEC ? 2 * elt_bytes<DT> : 4;
+        uint32_t u[kWords];
+    };
+    template <int DT>
+    __device__ __forceinline__ void fetch(const unsigned char *row, int64_t H, Raw<DT> &r) const {
+        if constexpr (VEC) {
+            if (c < H) {
+                const uint4 *p = reinterpret_cast<const uint4 *>(row + c * elt_bytes<DT>);
+#pragma unroll
+                for (int i = 0; i < elt_bytes<DT> / 2; ++i) {
+                    const uint4 q = p[i];
+                    r.u[4 * i] = q.x, r.u[4 * i + 1] = q.y, r.u[4 * i + 2] = q.z, r.u[4 * i + 3] = q.w;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < Raw<DT>::kWords; ++i) r.u[i] = 0;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (DT == VLMCE_F32)
+                    r.u[i] = in(i, H) ? reinterpret_cast<const uint32_t *>(row)[c + 32 * i] : 0;
+                else
+                    r.u[i] = in(i, H) ? reinterpret_cast<const uint16_t *>(row)[c + 32 * i] : 0;
+            }
+        }
+    }
+    // Value i of them.
+    template <int DT>
+    static __device__ __forceinline__ float value(const Raw<DT> &r, int i) {
+        if constexpr (DT == VLMCE_F32) {
+            return __uint_as_float(r.u[i]);
+        } else if constexpr (VEC) {
+            float a, b;
+            act::unpack16x2(r.u[i / 2], a, b, DT == VLMCE_F16);
+            return i & 1 ? b : a;
+        } else {
+            return act::from16(static_cast<uint16_t>(r.u[i]), DT == VLMCE_F16);
+        }
+    }
+
     // values outside the row are 0
     template <int DT>
     __device__ __forceinline__ void load(const unsigned char *row, int64_t H, float (&v)[N]) const {

@@ -83,9 +83,9 @@ __device__ __forceinline__ PairTile pair_tile(const PairParams &p, const Table &
 }
 
 // 32 x 32 sums as tmem_ld_16x32 lays them out (v[16 i + 4 g + 2 r + e]: row 16 i + 8 r +
-// lane / 4, column 8 g + 2 (lane % 4) + e) to a row per lane, through the warp's `buf`.
-__device__ __forceinline__ void to_rows(float (&v)[32], unsigned char *buf, int lane) {
-    __syncwarp();
+// lane / 4, column 8 g + 2 (lane % 4) + e) into a buffer of 32 rows of 128 bytes, as a TMA
+// store takes them.
+__device__ __forceinline__ void put_fragment(const float (&v)[32], unsigned char *buf, int lane) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int row = 8 * i + (lane >> 2);
@@ -96,6 +96,12 @@ __device__ __forceinline__ void to_rows(float (&v)[32], unsigned char *buf, int 
                 make_float2(v[16 * (i >> 1) + 4 * g + 2 * (i & 1)], v[16 * (i >> 1) + 4 * g + 2 * (i & 1) + 1]);
         }
     }
+}
+// The same, to a row per lane.
+__device__ __forceinline__ void to_rows(float (&v)[32], unsigned char *buf, int lane) {
+    if (lane == 0) tc::bulk_wait_read();
+    __syncwarp();
+    put_fragment(v, buf, lane);
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -238,6 +244,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpilogueRegs));
         const int part = kPairCols * ((warp - 4) >> 2);  // the warp's first column of the tile
         uint32_t *buf = reinterpret_cast<uint32_t *>(smem + kPairOutAt + (warp - 4) * mm::kOutBytes);
+        unsigned char *scratch = smem + kPairStagesRows * kPairChunk + (warp - 4) * mm::kOutBytes;  // B_ROWS
         const float *slots = reinterpret_cast<const float *>(smem + kPairFactorsAt);
         const uint32_t empty_leader = ptx::mapa(buf_empty, 0);
         const int in_tile = mm::kHalfRows * rank + (warp & 3) * 32;  // the warp's first row
@@ -343,18 +350,32 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     float v[32];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) unpack2(acc[16 * s + j], v[2 * j], v[2 * j + 1]);
-                    if constexpr (B_ROWS) to_rows(v, smem + kPairStagesRows * kPairChunk + (warp - 4) * mm::kOutBytes, lane);
+                    if constexpr (DW) {
+                        if (p.out == VLMCE_F32 && whole) {
+                            // from two buffers in turn: the store before this one may still read
+                            unsigned char *from = s & 1 ? scratch : reinterpret_cast<unsigned char *>(buf);
+                            if (col >= cols) continue;
+                            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                            __syncwarp();
+                            put_fragment(v, from, lane);
+                            ptx::fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) {
+                                if (p.add)
+                                    tc::tma_add_2d(&maps.y, ptx::smem_addr(from), col, static_cast<int>(row0));
+                                else
+                                    tc::tma_store_2d(&maps.y, ptx::smem_addr(from), col, static_cast<int>(row0));
+                                tc::bulk_commit();
+                            }
+                            continue;
+                        }
+                    }
+                    if constexpr (B_ROWS) to_rows(v, scratch, lane);
                     if constexpr (DW) {
                         if (p.out == VLMCE_F32) {
-                            if (col < cols) {
-                                if (whole) {
-                                    mm::put_f32(&maps.y, row0, col, reinterpret_cast<uint32_t(&)[32]>(v),
-                                                p.add != 0, buf, lane);
-                                } else {
-                                    put_f32_rows(static_cast<float *>(p.y), p.y_ld, row0, col, v, end, cols,
-                                                 p.add != 0, buf, lane);
-                                }
-                            }
+                            if (col < cols)
+                                put_f32_rows(static_cast<float *>(p.y), p.y_ld, row0, col, v, end, cols, p.add != 0,
+                                             buf, lane);
                             continue;
                         }
                     } else if (p.residual && row0 + lane < end && col < cols) {

@@ -41,18 +41,21 @@ constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxExperts = VLMCE_MOE_MAX_EXPERTS;
 static_assert(kMaxExperts <= kSortThreads, "a thread scans an expert");
 constexpr int kMaxSortCtas = 8;
+constexpr int kSortAtOnce = 4;  // groups of 32 pairs that a warp has on their way
 
 struct SortParams {
     const void *experts;
     int64_t ld;
-    int64_t pairs;
-    int k, E, align, wide, ctas;
+    int pairs, k, E, align, wide, ctas;
     int *position, *offsets, *counts;
 };
 
-__device__ __forceinline__ int sort_load(const SortParams &p, int64_t i) {
-    const int64_t t = i / p.k;
-    const int64_t at = t * p.ld + (i - t * p.k);
+__device__ __forceinline__ int sort_load(const SortParams &p, int i) {
+    int64_t at = i;
+    if (p.ld != p.k) {
+        const int t = i / p.k;
+        at = t * p.ld + (i - t * p.k);
+    }
     if (p.wide) {
         const int64_t e = static_cast<const int64_t *>(p.experts)[at];
         return e >= 0 && e < p.E ? static_cast<int>(e) : -1;
@@ -68,21 +71,26 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const SortParams 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = p.ctas > 1 ? static_cast<int>(ptx::cluster_ctarank()) : 0;
     // whole groups of 32 pairs to a warp
-    const int64_t groups = (p.pairs + 31) / 32;
-    const int64_t warps = static_cast<int64_t>(p.ctas) * kSortWarps;
-    const int64_t per = (groups + warps - 1) / warps * 32;
-    const int64_t first = min(p.pairs, (static_cast<int64_t>(rank) * kSortWarps + warp) * per);
-    const int64_t last = min(p.pairs, first + per);
+    const int groups = (p.pairs + 31) / 32, warps = p.ctas * kSortWarps;
+    const int per = (groups + warps - 1) / warps;
+    const int first = min(groups, (rank * kSortWarps + warp) * per) * 32;
+    const int last = min(p.pairs, min(groups, (rank * kSortWarps + warp + 1) * per) * 32);
     int *mine = cursor + warp * p.E;
 
     for (int e = lane; e < p.E; e += 32) mine[e] = 0;
     __syncwarp();
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
-#pragma unroll 4
-    for (int64_t i = first + lane; i < last; i += 32) {
-        const int e = sort_load(p, i);
-        if (e >= 0) atomicAdd(mine + e, 1);
+    for (int g = first; g < last; g += 32 * kSortAtOnce) {
+        int e[kSortAtOnce];
+#pragma unroll
+        for (int j = 0; j < kSortAtOnce; ++j) {
+            const int i = g + 32 * j + lane;
+            e[j] = i < last ? sort_load(p, i) : -1;
+        }
+#pragma unroll
+        for (int j = 0; j < kSortAtOnce; ++j)
+            if (e[j] >= 0) atomicAdd(mine + e[j], 1);
     }
     __syncthreads();
     // where each warp's pairs of an expert start among the CTA's
@@ -142,17 +150,27 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const SortParams 
         }
     }
     __syncthreads();
-    for (int64_t g = first; g < last; g += 32) {
-        const int64_t i = g + lane;
-        const int e = i < last ? sort_load(p, i) : -1;
-        const unsigned peers = __match_any_sync(0xffffffffu, e);
-        const int ahead = __popc(peers & ((1u << lane) - 1));
-        int at = 0;
-        if (e >= 0) at = mine[e] + ahead;
-        __syncwarp();
-        if (e >= 0 && ahead == 0) mine[e] += __popc(peers);
-        __syncwarp();
-        if (i < last) p.position[i] = e >= 0 ? at : -1;
+    for (int g = first; g < last; g += 32 * kSortAtOnce) {
+        int e[kSortAtOnce];
+        unsigned peers[kSortAtOnce];
+#pragma unroll
+        for (int j = 0; j < kSortAtOnce; ++j) {
+            const int i = g + 32 * j + lane;
+            e[j] = i < last ? sort_load(p, i) : -1;
+        }
+#pragma unroll
+        for (int j = 0; j < kSortAtOnce; ++j) peers[j] = __match_any_sync(0xffffffffu, e[j]);
+#pragma unroll
+        for (int j = 0; j < kSortAtOnce; ++j) {
+            const int i = g + 32 * j + lane;
+            const int ahead = __popc(peers[j] & ((1u << lane) - 1));
+            int at = -1;
+            if (e[j] >= 0) at = mine[e[j]] + ahead;
+            __syncwarp();
+            if (e[j] >= 0 && ahead == 0) mine[e[j]] = at + __popc(peers[j]);
+            __syncwarp();
+            if (i < last) p.position[i] = at;
+        }
     }
     if (p.ctas > 1) ptx::cluster_sync();  // a CTA's totals are read until here
 }
@@ -252,8 +270,6 @@ __global__ void __launch_bounds__(256) gather_kernel(const RowParams p) {
     }
 }
 
-constexpr int kAtOnce = 8;  // a token's rows that a thread has on their way together
-
 template <int DT>
 __device__ __forceinline__ float weight_of(const RowParams &p, int64_t t, int j) {
     if (!p.w) return 1.f;
@@ -262,8 +278,8 @@ __device__ __forceinline__ float weight_of(const RowParams &p, int64_t t, int j)
     return blocks::load1<DT>(static_cast<const unsigned char *>(p.w), i);
 }
 
-template <int DT, bool VEC>
-__global__ void __launch_bounds__(256) combine_kernel(const RowParams p) {
+template <int DT, bool VEC, int AT_ONCE>
+__global__ void __launch_bounds__(256, AT_ONCE > 4 && DT == VLMCE_F32 ? 2 : 3) combine_kernel(const RowParams p) {
     using C = blocks::Cols<VEC>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     ptx::griddep_launch_dependents();
@@ -274,43 +290,44 @@ __global__ void __launch_bounds__(256) combine_kernel(const RowParams p) {
     if (base >= p.H) return;
     const C cols(base, lane);
     const int *pos = p.position + t * p.k;
+    typename C::template Raw<DT> res;
+    if (p.residual) cols.template fetch<DT>(p.residual + t * p.res_ld, p.H, res);
     float y[C::N];
 #pragma unroll
     for (int i = 0; i < C::N; ++i) y[i] = 0.f;
-    for (int j0 = 0; j0 < p.k; j0 += kAtOnce) {
-        float v[kAtOnce][C::N], w[kAtOnce];
-        bool held[kAtOnce];
+    for (int j0 = 0; j0 < p.k; j0 += AT_ONCE) {
+        typename C::template Raw<DT> v[AT_ONCE];
+        float w[AT_ONCE];
+        int r[AT_ONCE];
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
-            const int64_t r = j0 + j < p.k ? pos[j0 + j] : -1;
-            held[j] = r >= 0 && r < p.R;
-            if (held[j]) {
-                w[j] = weight_of<DT>(p, t, j0 + j);
-                cols.template load<DT>(p.rows_in + r * p.in_ld, p.H, v[j]);
-            }
+        for (int j = 0; j < AT_ONCE; ++j) {
+            r[j] = j0 + j < p.k ? pos[j0 + j] : -1;
+            w[j] = j0 + j < p.k ? weight_of<DT>(p, t, j0 + j) : 0.f;
+            if (r[j] >= p.R) r[j] = -1;
         }
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j)
-            if (held[j]) {
+        for (int j = 0; j < AT_ONCE; ++j)
+            if (r[j] >= 0) cols.template fetch<DT>(p.rows_in + r[j] * p.in_ld, p.H, v[j]);
 #pragma unroll
-                for (int i = 0; i < C::N; ++i) y[i] = fmaf(w[j], v[j][i], y[i]);
+        for (int j = 0; j < AT_ONCE; ++j)
+            if (r[j] >= 0) {
+#pragma unroll
+                for (int i = 0; i < C::N; ++i) y[i] = fmaf(w[j], C::template value<DT>(v[j], i), y[i]);
             }
     }
     if (p.residual) {
-        float r[C::N];
-        cols.template load<DT>(p.residual + t * p.res_ld, p.H, r);
 #pragma unroll
-        for (int i = 0; i < C::N; ++i) y[i] += r[i];
+        for (int i = 0; i < C::N; ++i) y[i] += C::template value<DT>(res, i);
     }
     cols.template store<DT>(p.out + t * p.out_ld, p.H, y);
 }
 
 // A CTA has the whole row of a token: dw's sums stay in it, in an order of their own.
-template <int DT, bool VEC>
-__global__ void __launch_bounds__(256) combine_bwd_kernel(const RowParams p) {
+template <int DT, bool VEC, int AT_ONCE>
+__global__ void __launch_bounds__(256, AT_ONCE > 4 || DT == VLMCE_F32 ? 2 : 3) combine_bwd_kernel(const RowParams p) {
     using C = blocks::Cols<VEC>;
     const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    __shared__ float part[8][kAtOnce];
+    __shared__ float part[8][AT_ONCE];
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
     const int64_t t = blockIdx.x;
@@ -320,53 +337,53 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const RowParams p) {
         return;
     }
     const int *pos = p.position + t * p.k;
-    for (int j0 = 0; j0 < p.k; j0 += kAtOnce) {
-        int64_t r[kAtOnce];
-        float w[kAtOnce], sum[kAtOnce];
+    for (int j0 = 0; j0 < p.k; j0 += AT_ONCE) {
+        int r[AT_ONCE];
+        float w[AT_ONCE], sum[AT_ONCE];
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
+        for (int j = 0; j < AT_ONCE; ++j) {
             r[j] = j0 + j < p.k ? pos[j0 + j] : -1;
+            w[j] = j0 + j < p.k ? weight_of<DT>(p, t, j0 + j) : 0.f;
             if (r[j] >= p.R) r[j] = -1;
-            w[j] = r[j] >= 0 ? weight_of<DT>(p, t, j0 + j) : 0.f;
             sum[j] = 0.f;
         }
         for (int64_t base = static_cast<int64_t>(warp) * C::kWarp; base < p.H;
              base += static_cast<int64_t>(warps) * C::kWarp) {
             const C cols(base, lane);
-            float d[C::N];
-            cols.template load<DT>(p.x + t * p.x_ld, p.H, d);
+            typename C::template Raw<DT> d, v[AT_ONCE];
+            cols.template fetch<DT>(p.x + t * p.x_ld, p.H, d);
             if (p.dw) {
-                float v[kAtOnce][C::N];
 #pragma unroll
-                for (int j = 0; j < kAtOnce; ++j)
-                    if (r[j] >= 0) cols.template load<DT>(p.rows_in + r[j] * p.in_ld, p.H, v[j]);
+                for (int j = 0; j < AT_ONCE; ++j)
+                    if (r[j] >= 0) cols.template fetch<DT>(p.rows_in + r[j] * p.in_ld, p.H, v[j]);
 #pragma unroll
-                for (int j = 0; j < kAtOnce; ++j)
+                for (int j = 0; j < AT_ONCE; ++j)
                     if (r[j] >= 0) {
 #pragma unroll
-                        for (int i = 0; i < C::N; ++i) sum[j] = fmaf(d[i], v[j][i], sum[j]);
+                        for (int i = 0; i < C::N; ++i)
+                            sum[j] = fmaf(C::template value<DT>(d, i), C::template value<DT>(v[j], i), sum[j]);
                     }
             }
             if (p.out) {
 #pragma unroll
-                for (int j = 0; j < kAtOnce; ++j)
+                for (int j = 0; j < AT_ONCE; ++j)
                     if (r[j] >= 0) {
                         float o[C::N];
 #pragma unroll
-                        for (int i = 0; i < C::N; ++i) o[i] = w[j] * d[i];
+                        for (int i = 0; i < C::N; ++i) o[i] = w[j] * C::template value<DT>(d, i);
                         cols.template store<DT>(p.out + r[j] * p.out_ld, p.H, o);
                     }
             }
         }
         if (p.dw) {
 #pragma unroll
-            for (int j = 0; j < kAtOnce; ++j) {
+            for (int j = 0; j < AT_ONCE; ++j) {
 #pragma unroll
                 for (int s = 16; s > 0; s /= 2) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], s);
                 if (lane == 0) part[warp][j] = sum[j];
             }
             __syncthreads();
-            if (threadIdx.x < kAtOnce && j0 + static_cast<int>(threadIdx.x) < p.k) {
+            if (threadIdx.x < AT_ONCE && j0 + static_cast<int>(threadIdx.x) < p.k) {
                 float a = 0.f;
                 for (int i = 0; i < warps; ++i) a += part[i][threadIdx.x];
                 p.dw[t * p.k + j0 + threadIdx.x] = a;
@@ -407,13 +424,21 @@ RowKernel gather_of(int dt) {
         default: return gather_kernel<VLMCE_BF16, VEC, FP8>;
     }
 }
-template <bool VEC>
+template <bool VEC, int AT_ONCE>
 RowKernel combine_of(int dt, bool bwd) {
     switch (dt) {
-        case VLMCE_F32: return bwd ? combine_bwd_kernel<VLMCE_F32, VEC> : combine_kernel<VLMCE_F32, VEC>;
-        case VLMCE_F16: return bwd ? combine_bwd_kernel<VLMCE_F16, VEC> : combine_kernel<VLMCE_F16, VEC>;
-        default: return bwd ? combine_bwd_kernel<VLMCE_BF16, VEC> : combine_kernel<VLMCE_BF16, VEC>;
+        case VLMCE_F32:
+            return bwd ? combine_bwd_kernel<VLMCE_F32, VEC, AT_ONCE> : combine_kernel<VLMCE_F32, VEC, AT_ONCE>;
+        case VLMCE_F16:
+            return bwd ? combine_bwd_kernel<VLMCE_F16, VEC, AT_ONCE> : combine_kernel<VLMCE_F16, VEC, AT_ONCE>;
+        default:
+            return bwd ? combine_bwd_kernel<VLMCE_BF16, VEC, AT_ONCE> : combine_kernel<VLMCE_BF16, VEC, AT_ONCE>;
     }
+}
+// (unused places of eight cost registers: up to four rows of a token at a time, or eight)
+RowKernel combine_of(int dt, bool bwd, bool vec, int64_t k) {
+    if (k <= 4) return vec ? combine_of<true, 4>(dt, bwd) : combine_of<false, 4>(dt, bwd);
+    return vec ? combine_of<true, 8>(dt, bwd) : combine_of<false, 8>(dt, bwd);
 }
 
 constexpr int64_t kMaxH = int64_t(1) << 24;
@@ -518,7 +543,7 @@ extern "C" vlmce_status moe_sort(const void *experts, int64_t experts_stride, in
     SortParams p = {};
     p.experts = experts;
     p.ld = experts_stride;
-    p.pairs = T * k;
+    p.pairs = static_cast<int>(T * k);
     p.k = static_cast<int>(k);
     p.E = static_cast<int>(E);
     p.align = static_cast<int>(align);
@@ -527,7 +552,7 @@ extern "C" vlmce_status moe_sort(const void *experts, int64_t experts_stride, in
     p.offsets = offsets;
     p.counts = counts;
     p.ctas = 1;
-    while (p.ctas < kMaxSortCtas && p.pairs > p.ctas * int64_t{2 * kSortThreads}) p.ctas *= 2;
+    while (p.ctas < kMaxSortCtas && p.pairs > p.ctas * kSortThreads) p.ctas *= 2;
     e = launch(sort_kernel, dim3(static_cast<unsigned>(p.ctas), 1, 1), kSortThreads,
                static_cast<size_t>(kSortWarps * E * 4), static_cast<unsigned>(p.ctas),
                reinterpret_cast<cudaStream_t>(stream), p);
@@ -632,7 +657,7 @@ extern "C" vlmce_status moe_combine(const void *rows, int64_t rows_stride, int32
     p.k = static_cast<int>(k);
     const int per = vec ? 256 : 128, threads = threads_of(H, per);
     return launch_status(
-        launch(vec ? combine_of<true>(dtype, false) : combine_of<false>(dtype, false),
+        launch(combine_of(dtype, false, vec, k),
                dim3(static_cast<unsigned>(T), row_ctas(H, per, threads), 1), threads, 0, 1,
                reinterpret_cast<cudaStream_t>(stream), p),
         "moe_combine");
@@ -690,7 +715,7 @@ extern "C" vlmce_status moe_combine_bwd(const void *dy, int64_t dy_stride, const
     p.k = static_cast<int>(k);
     p.E = static_cast<int>(E);
     const int per = vec ? 256 : 128;
-    return launch_status(launch(vec ? combine_of<true>(dtype, true) : combine_of<false>(dtype, true),
+    return launch_status(launch(combine_of(dtype, true, vec, k),
                                 dim3(static_cast<unsigned>(T + E), 1, 1), threads_of(H, per), 0, 1,
                                 reinterpret_cast<cudaStream_t>(stream), p),
                          "moe_combine_bwd");

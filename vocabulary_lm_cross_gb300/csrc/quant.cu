@@ -5,8 +5,8 @@
 // along its rows (the forward product) and along its columns, transposed (the gradients
 // of the weights, and of the inputs by the transposed weight).  Both come from one
 // reading: a CTA has a tile of 128 x 128 in registers, a thread eight rows of eight
-// columns.  A row's maximum is found among the 16 lanes that share it, a column's in
-// shared memory (integer maxima: no order in the result).  For the transposed form a
+// columns, as they are in memory.  A row's maximum is found among the 16 lanes that share
+// it, a column's among the warps in shared memory (integer maxima: no order in the result).  For the transposed form a
 // thread's eight rows of a column are one 8-byte store into shared memory, the 8-byte
 // units of a column swizzled by its group of eight columns (16 lanes then meet 32
 // different banks), and leave from there as whole 128-byte lines.
@@ -41,11 +41,42 @@ struct Params {
     int square;
 };
 
+// A thread's eight rows of eight columns, as they are in memory: 16-bit ones two to a
+// word.  Magnitudes are compared as they are, too (16-bit ones two at a time).
+template <int DT>
+struct Tile {
+    static constexpr bool k16 = DT != VLMCE_F32;
+    static constexpr int kWords = k16 ? 4 : 8;  // of a row
+    uint32_t u[8][kWords];
+
+    static __device__ __forceinline__ uint32_t magnitudes(uint32_t w) { return w & (k16 ? 0x7fff7fffu : 0x7fffffffu); }
+    static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return k16 ? __vmaxu2(a, b) : max(a, b); }
+    // The larger magnitude of a word, as an fp32 number's bits.
+    static __device__ __forceinline__ uint32_t widest(uint32_t w) {
+        if constexpr (k16) {
+            const uint16_t m = static_cast<uint16_t>(max(w & 0xffffu, w >> 16));
+            return __float_as_uint(act::from16(m, DT == VLMCE_F16));
+        } else {
+            return w;
+        }
+    }
+    __device__ __forceinline__ float at(int i, int j) const {
+        if constexpr (k16) {
+            float a, b;
+            act::unpack16x2(u[i][j / 2], a, b, DT == VLMCE_F16);
+            return j & 1 ? b : a;
+        } else {
+            return __uint_as_float(u[i][j]);
+        }
+    }
+};
+
 template <int DT, bool VEC, bool ROWS, bool TRANS>
-__global__ void __launch_bounds__(kThreads) quant_kernel(const Params p) {
-    constexpr int kWarps = kThreads / 32;
-    __shared__ uint32_t col_max[kB];
+__global__ void __launch_bounds__(kThreads, DT == VLMCE_F32 ? 2 : 3) quant_kernel(const Params p) {
+    using T = Tile<DT>;
+    constexpr int kWarps = kThreads / 32, kW = T::kWords;
     __shared__ uint32_t tile_max[kWarps];
+    __shared__ __align__(16) uint32_t col_max[TRANS ? kWarps : 1][16 * kW];
     __shared__ __align__(16) unsigned char tq[TRANS ? kB * kB : 16];
     const int tid = threadIdx.x, lane = tid & 31;
     const int cg = tid & 15, rg = tid >> 4;  // eight columns, eight rows of the tile
@@ -54,75 +85,79 @@ __global__ void __launch_bounds__(kThreads) quant_kernel(const Params p) {
     const int in_b = static_cast<int>(tile - b * p.rt * p.ct);
     const int tr = in_b / p.ct, tc = in_b - tr * p.ct;
     const int64_t r0 = static_cast<int64_t>(tr) * kB + 8 * rg, c0 = static_cast<int64_t>(tc) * kB + 8 * cg;
-    if (TRANS && tid < kB) col_max[tid] = 0;
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
     const unsigned char *x = p.x + b * p.x_batch + r0 * p.x_ld;
-    float v[8][8];
+    T v;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const bool row = r0 + i < p.R;
         if constexpr (VEC) {
-            if (row && c0 < p.C) {
-                blocks::load8<DT>(x + i * p.x_ld, c0, v[i]);
-            } else {
+            const uint4 *from = reinterpret_cast<const uint4 *>(x + i * p.x_ld + c0 * blocks::elt_bytes<DT>);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+            for (int k = 0; k < kW / 4; ++k) {
+                const uint4 q = row && c0 < p.C ? from[k] : make_uint4(0, 0, 0, 0);
+                v.u[i][4 * k] = q.x, v.u[i][4 * k + 1] = q.y, v.u[i][4 * k + 2] = q.z, v.u[i][4 * k + 3] = q.w;
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[i][j] = row && c0 + j < p.C ? blocks::load1<DT>(x + i * p.x_ld, c0 + j) : 0.f;
+            for (int j = 0; j < 8; ++j) {
+                const bool in = row && c0 + j < p.C;
+                if constexpr (T::k16) {
+                    const uint32_t e = in ? reinterpret_cast<const uint16_t *>(x + i * p.x_ld)[c0 + j] : 0;
+                    v.u[i][j / 2] = j & 1 ? v.u[i][j / 2] | e << 16 : e;
+                } else {
+                    v.u[i][j] = in ? reinterpret_cast<const uint32_t *>(x + i * p.x_ld)[c0 + j] : 0;
+                }
+            }
         }
     }
+    float tile_inv = 1.f;
     if (p.square) {
         uint32_t a = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) a = max(a, blocks::magnitude(v[i][j]));
-        a = __reduce_max_sync(0xffffffffu, a);
+            for (int k = 0; k < kW; ++k) a = T::larger(a, T::magnitudes(v.u[i][k]));
+        a = __reduce_max_sync(0xffffffffu, T::widest(a));
         if (lane == 0) tile_max[tid >> 5] = a;
         __syncthreads();
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) a = max(a, tile_max[w]);
-        float inv;
-        const float scale = blocks::scale_of(a, inv);
+        const float scale = blocks::scale_of(a, tile_inv);
         if (tid == 0) {
             if (ROWS) p.scale[(b * p.rt + tr) * p.ct + tc] = scale;
             if (TRANS) p.scale_t[(b * p.ct + tc) * p.rt + tr] = scale;
         }
+    } else if constexpr (TRANS) {
+        uint32_t *mine = col_max[tid >> 5] + kW * cg;  // of the warp's 16 rows
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] *= inv;
-    } else if (TRANS) {
-        __syncthreads();  // col_max is clear
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int k = 0; k < kW; ++k) {
             uint32_t a = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) a = max(a, blocks::magnitude(v[i][j]));
-            a = max(a, __shfl_xor_sync(0xffffffffu, a, 16));  // the warp's other eight rows
-            if (lane < 16) atomicMax(col_max + 8 * cg + j, a);
+            for (int i = 0; i < 8; ++i) a = T::larger(a, T::magnitudes(v.u[i][k]));
+            a = T::larger(a, __shfl_xor_sync(0xffffffffu, a, 16));
+            if (lane < 16) mine[k] = a;
         }
     }
     if constexpr (ROWS) {
         unsigned char *q = p.q + b * p.q_batch + r0 * p.q_ld;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            float inv = 1.f;
+            float inv = tile_inv;
             if (!p.square) {
                 uint32_t a = 0;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) a = max(a, blocks::magnitude(v[i][j]));
+                for (int k = 0; k < kW; ++k) a = T::larger(a, T::magnitudes(v.u[i][k]));
 #pragma unroll
-                for (int d = 8; d > 0; d /= 2) a = max(a, __shfl_xor_sync(0xffffffffu, a, d));
-                const float scale = blocks::scale_of(a, inv);
+                for (int d = 8; d > 0; d /= 2) a = T::larger(a, __shfl_xor_sync(0xffffffffu, a, d));
+                const float scale = blocks::scale_of(T::widest(a), inv);
                 if (cg == 0 && r0 + i < p.R) p.scale[(b * p.R + r0 + i) * p.ct + tc] = scale;
             }
-            const uint32_t lo = blocks::pack_e4m3x4(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv);
-            const uint32_t hi = blocks::pack_e4m3x4(v[i][4] * inv, v[i][5] * inv, v[i][6] * inv, v[i][7] * inv);
+            const uint32_t lo =
+                blocks::pack_e4m3x4(v.at(i, 0) * inv, v.at(i, 1) * inv, v.at(i, 2) * inv, v.at(i, 3) * inv);
+            const uint32_t hi =
+                blocks::pack_e4m3x4(v.at(i, 4) * inv, v.at(i, 5) * inv, v.at(i, 6) * inv, v.at(i, 7) * inv);
             if (r0 + i < p.R) {
                 unsigned char *row = q + i * p.q_ld;
                 if (VEC) {
@@ -138,15 +173,32 @@ __global__ void __launch_bounds__(kThreads) quant_kernel(const Params p) {
     }
     if constexpr (TRANS) {
         __syncthreads();  // col_max is complete
+        uint32_t m[kW];
+        if (!p.square) {
+#pragma unroll
+            for (int k = 0; k < kW; ++k) m[k] = 0;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w)
+#pragma unroll
+                for (int k = 0; k < kW; k += 4) {
+                    const uint4 q = *reinterpret_cast<const uint4 *>(col_max[w] + kW * cg + k);
+                    m[k] = T::larger(m[k], q.x), m[k + 1] = T::larger(m[k + 1], q.y);
+                    m[k + 2] = T::larger(m[k + 2], q.z), m[k + 3] = T::larger(m[k + 3], q.w);
+                }
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            float inv = 1.f;
+            float inv = tile_inv;
             if (!p.square) {
-                const float scale = blocks::scale_of(col_max[8 * cg + j], inv);
+                // (the other half of a word is another column)
+                const uint32_t a = T::k16 ? (j & 1 ? m[j / 2] >> 16 : m[j / 2] & 0xffffu) : m[j % kW];
+                const float scale = blocks::scale_of(T::widest(a), inv);
                 if (rg == 0 && c0 + j < p.C) p.scale_t[(b * p.C + c0 + j) * p.rt + tr] = scale;
             }
-            const uint32_t lo = blocks::pack_e4m3x4(v[0][j] * inv, v[1][j] * inv, v[2][j] * inv, v[3][j] * inv);
-            const uint32_t hi = blocks::pack_e4m3x4(v[4][j] * inv, v[5][j] * inv, v[6][j] * inv, v[7][j] * inv);
+            const uint32_t lo =
+                blocks::pack_e4m3x4(v.at(0, j) * inv, v.at(1, j) * inv, v.at(2, j) * inv, v.at(3, j) * inv);
+            const uint32_t hi =
+                blocks::pack_e4m3x4(v.at(4, j) * inv, v.at(5, j) * inv, v.at(6, j) * inv, v.at(7, j) * inv);
             *reinterpret_cast<uint2 *>(tq + (8 * cg + j) * kB + 8 * (rg ^ cg)) = make_uint2(lo, hi);
         }
         __syncthreads();

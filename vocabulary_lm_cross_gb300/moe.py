@@ -43,17 +43,17 @@ def moe_sort(experts: torch.Tensor, num_experts: int, *, align: int = 1) -> MoEO
             return moe_sort(experts, num_experts, align=align)
     T, k = experts.shape
     stride = rows(experts, "experts", experts.shape, experts.dtype, dev)
-    lib = capi.lib()
-    n = lib.vlmce_moe_rows(T, k, num_experts, align)
     E = num_experts if 0 < num_experts <= capi.MOE_MAX_EXPERTS else 1
     position = torch.empty((T, k), dtype=torch.int32, device=dev)
-    ends = torch.empty(2 * E + 1, dtype=torch.int32, device=dev)  # offsets and counts
-    offsets, counts = ends[:E + 1], ends[E + 1:]
-    st = lib.moe_sort(experts.data_ptr(), stride, int(experts.dtype == torch.int64), T, k,
+    offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+    counts = torch.empty(E, dtype=torch.int32, device=dev)
+    st = capi.lib().moe_sort(experts.data_ptr(), stride, int(experts.dtype == torch.int64), T, k,
                       num_experts, align, position.data_ptr(), offsets.data_ptr(),
                       counts.data_ptr(), raw_stream(dev.index))
     if st:
         capi.check(st, "moe_sort")
+    # vlmce_moe_rows
+    n = (T * k + min(num_experts, T * k) * (align - 1)) // align * align
     return MoEOrder(position, offsets, counts, n)
 
 
@@ -95,6 +95,14 @@ def padded(n: int) -> int:
     return (n + 15) // 16 * 16
 
 
+def empty_fp8(shape, device) -> torch.Tensor:
+    """An 8-bit tensor of such rows."""
+    n = shape[-1]
+    if n % 16 == 0:
+        return torch.empty(shape, dtype=_FP8, device=device)
+    return torch.empty((*shape[:-1], padded(n)), dtype=_FP8, device=device)[..., :n]
+
+
 def moe_gather(x: torch.Tensor, order: MoEOrder, *, fp8: bool = False,
                out: torch.Tensor | None = None) -> MoEGather:
     """rows[order.position[t, j]] = x[t], x [T, H].  fp8: in float8_e4m3fn with a scale
@@ -111,8 +119,7 @@ def moe_gather(x: torch.Tensor, order: MoEOrder, *, fp8: bool = False,
     R = order.rows
     odt = _FP8 if fp8 else dt
     if out is None:
-        out = torch.empty((R, padded(H)), dtype=odt, device=dev)[:, :H] if fp8 else \
-            torch.empty((R, H), dtype=odt, device=dev)
+        out = empty_fp8((R, H), dev) if fp8 else torch.empty((R, H), dtype=odt, device=dev)
     os_ = rows(out, "out", (R, H), odt, dev)
     if R <= 1:
         os_ = max(os_, H)

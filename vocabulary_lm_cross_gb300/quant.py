@@ -7,7 +7,7 @@ from typing import NamedTuple
 import torch
 
 from . import capi
-from .moe import padded
+from .moe import empty_fp8, padded
 from .rows import DTYPES, current_device, raw_stream
 
 _FP8 = torch.float8_e4m3fn
@@ -51,10 +51,10 @@ def quantize_blocks(x: torch.Tensor, *, square: bool = False, rows: bool = True,
     rb, cb = (R + 127) // 128, (C + 127) // 128
     q = s = qt = st_ = None
     if rows:
-        q = torch.empty((*b, R, padded(C)), dtype=_FP8, device=dev)[..., :C]
+        q = empty_fp8((*b, R, C), dev)
         s = torch.empty((*b, rb if square else R, cb), dtype=torch.float32, device=dev)
     if transposed:
-        qt = torch.empty((*b, C, padded(R)), dtype=_FP8, device=dev)[..., :R]
+        qt = empty_fp8((*b, C, R), dev)
         st_ = torch.empty((*b, cb if square else C, rb), dtype=torch.float32, device=dev)
     if x.numel() == 0:
         return BlockQuant(q, s, qt, st_)
