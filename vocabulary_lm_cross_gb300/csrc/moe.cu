@@ -29,19 +29,20 @@ namespace moe {
 namespace {
 
 // ------------------------------------------------------------------- sort
-// One launch of one cluster.  The pairs are dealt to its warps in consecutive runs; each
-// warp counts its run by expert in shared memory, the counts are summed over the warps of
-// a CTA and then over the CTAs (through distributed shared memory), every CTA scans the
-// experts' totals, and each warp walks its run again, 32 pairs at a time: pairs of one
-// expert find their rank among themselves (match) and take it from the warp's cursor.  So
-// the order is that of the pairs, whatever the timing, and there is no atomic that
-// matters to it.
+// One launch of one cluster.  The pairs are dealt to its warps in consecutive runs, which a
+// warp walks 32 pairs at a time: pairs of one expert find their rank among themselves
+// (match) and take it from the warp's count of that expert, in shared memory.  The counts
+// are summed over the warps of a CTA and then over the CTAs (through distributed shared
+// memory), and every CTA scans the experts' totals; then a pair's row is its rank in the
+// warp's run and where the run's pairs of the expert start.  So the order is that of the
+// pairs, whatever the timing, without an atomic.  A run of up to kSortKeep groups of 32 stays
+// in registers; a longer one is walked again.
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxExperts = VLMCE_MOE_MAX_EXPERTS;
 static_assert(kMaxExperts <= kSortThreads, "a thread scans an expert");
 constexpr int kMaxSortCtas = 8;
-constexpr int kSortAtOnce = 4;  // groups of 32 pairs that a warp has on their way
+constexpr int kSortKeep = 16;
 
 struct SortParams {
     const void *experts;
@@ -65,7 +66,7 @@ __device__ __forceinline__ int sort_load(const SortParams &p, int i) {
 }
 
 __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const SortParams p) {
-    extern __shared__ int cursor[];          // [kSortWarps][E]: a warp's counts, then its next rows
+    extern __shared__ int cursor[];          // [kSortWarps][E]: a warp's counts, then where its rows start
     __shared__ int total[kMaxExperts];       // of this CTA
     __shared__ int warp_sum[kSortWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -81,17 +82,26 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const SortParams 
     __syncwarp();
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
-    for (int g = first; g < last; g += 32 * kSortAtOnce) {
-        int e[kSortAtOnce];
+    // a pair: its expert and its rank among the run's pairs of that; -1: nobody's
+    int kept_e[kSortKeep], kept_rank[kSortKeep];
+    auto walk = [&](int from, int(&e)[kSortKeep], int(&rank_of)[kSortKeep]) {
 #pragma unroll
-        for (int j = 0; j < kSortAtOnce; ++j) {
-            const int i = g + 32 * j + lane;
+        for (int j = 0; j < kSortKeep; ++j) {
+            const int i = from + 32 * j + lane;
             e[j] = i < last ? sort_load(p, i) : -1;
         }
 #pragma unroll
-        for (int j = 0; j < kSortAtOnce; ++j)
-            if (e[j] >= 0) atomicAdd(mine + e[j], 1);
-    }
+        for (int j = 0; j < kSortKeep; ++j) {
+            if (from + 32 * j >= last) break;
+            const unsigned peers = __match_any_sync(0xffffffffu, e[j]);
+            const int ahead = __popc(peers & ((1u << lane) - 1));
+            rank_of[j] = e[j] >= 0 ? mine[e[j]] + ahead : 0;
+            __syncwarp();
+            if (e[j] >= 0 && ahead == 0) mine[e[j]] = rank_of[j] + __popc(peers);
+            __syncwarp();
+        }
+    };
+    for (int g = first; g < last; g += 32 * kSortKeep) walk(g, kept_e, kept_rank);
     __syncthreads();
     // where each warp's pairs of an expert start among the CTA's
     int count = 0;  // of expert `tid`: this CTA's, then the sum over all
@@ -150,26 +160,13 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const SortParams 
         }
     }
     __syncthreads();
-    for (int g = first; g < last; g += 32 * kSortAtOnce) {
-        int e[kSortAtOnce];
-        unsigned peers[kSortAtOnce];
+    const bool kept = last - first <= 32 * kSortKeep;
+    for (int g = first; g < last; g += 32 * kSortKeep) {
+        if (!kept) walk(g, kept_e, kept_rank);  // (the counts now start where the rows do)
 #pragma unroll
-        for (int j = 0; j < kSortAtOnce; ++j) {
-            const int i = g + 32 * j + lane;
-            e[j] = i < last ? sort_load(p, i) : -1;
-        }
-#pragma unroll
-        for (int j = 0; j < kSortAtOnce; ++j) peers[j] = __match_any_sync(0xffffffffu, e[j]);
-#pragma unroll
-        for (int j = 0; j < kSortAtOnce; ++j) {
-            const int i = g + 32 * j + lane;
-            const int ahead = __popc(peers[j] & ((1u << lane) - 1));
-            int at = -1;
-            if (e[j] >= 0) at = mine[e[j]] + ahead;
-            __syncwarp();
-            if (e[j] >= 0 && ahead == 0) mine[e[j]] = at + __popc(peers[j]);
-            __syncwarp();
-            if (i < last) p.position[i] = at;
+        for (int j = 0; j < kSortKeep; ++j) {
+            const int i = g + 32 * j + lane, e = kept_e[j];
+            if (i < last) p.position[i] = e >= 0 ? kept_rank[j] + (kept ? mine[e] : 0) : -1;
         }
     }
     if (p.ctas > 1) ptx::cluster_sync();  // a CTA's totals are read until here

@@ -77,6 +77,7 @@ __global__ void __launch_bounds__(kThreads, DT == VLMCE_F32 ? 2 : 3) quant_kerne
     constexpr int kWarps = kThreads / 32, kW = T::kWords;
     __shared__ uint32_t tile_max[kWarps];
     __shared__ __align__(16) uint32_t col_max[TRANS ? kWarps : 1][16 * kW];
+    __shared__ __align__(16) float col_inv[TRANS ? kB : 4];
     __shared__ __align__(16) unsigned char tq[TRANS ? kB * kB : 16];
     const int tid = threadIdx.x, lane = tid & 31;
     const int cg = tid & 15, rg = tid >> 4;  // eight columns, eight rows of the tile
@@ -142,18 +143,25 @@ __global__ void __launch_bounds__(kThreads, DT == VLMCE_F32 ? 2 : 3) quant_kerne
     }
     if constexpr (ROWS) {
         unsigned char *q = p.q + b * p.q_batch + r0 * p.q_ld;
+        float mine = tile_inv;  // of row lane % 8 of the eight
+        if (!p.square) {
+            uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float inv = tile_inv;
-            if (!p.square) {
+            for (int i = 0; i < 8; ++i) {
                 uint32_t a = 0;
 #pragma unroll
                 for (int k = 0; k < kW; ++k) a = T::larger(a, T::magnitudes(v.u[i][k]));
 #pragma unroll
                 for (int d = 8; d > 0; d /= 2) a = T::larger(a, __shfl_xor_sync(0xffffffffu, a, d));
-                const float scale = blocks::scale_of(T::widest(a), inv);
-                if (cg == 0 && r0 + i < p.R) p.scale[(b * p.R + r0 + i) * p.ct + tc] = scale;
+                if ((lane & 7) == i) m = a;
             }
+            // (the two divisions cost more than the values' own arithmetic: one row a lane)
+            const float scale = blocks::scale_of(T::widest(m), mine);
+            if (cg < 8 && r0 + cg < p.R) p.scale[(b * p.R + r0 + cg) * p.ct + tc] = scale;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float inv = __shfl_sync(0xffffffffu, mine, (lane & 16) + i);
             const uint32_t lo =
                 blocks::pack_e4m3x4(v.at(i, 0) * inv, v.at(i, 1) * inv, v.at(i, 2) * inv, v.at(i, 3) * inv);
             const uint32_t hi =
@@ -172,29 +180,37 @@ __global__ void __launch_bounds__(kThreads, DT == VLMCE_F32 ? 2 : 3) quant_kerne
         }
     }
     if constexpr (TRANS) {
-        __syncthreads();  // col_max is complete
-        uint32_t m[kW];
+        float invs[8];
         if (!p.square) {
+            __syncthreads();  // col_max is complete
+            if (tid < kB) {   // a column a thread
+                uint32_t a = 0;
 #pragma unroll
-            for (int k = 0; k < kW; ++k) m[k] = 0;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w)
-#pragma unroll
-                for (int k = 0; k < kW; k += 4) {
-                    const uint4 q = *reinterpret_cast<const uint4 *>(col_max[w] + kW * cg + k);
-                    m[k] = T::larger(m[k], q.x), m[k + 1] = T::larger(m[k + 1], q.y);
-                    m[k + 2] = T::larger(m[k + 2], q.z), m[k + 3] = T::larger(m[k + 3], q.w);
+                for (int w = 0; w < kWarps; ++w) {
+                    if constexpr (T::k16)
+                        a = max(a, static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(col_max[w])[tid]));
+                    else
+                        a = max(a, col_max[w][tid]);
                 }
+                float inv;
+                const float scale = blocks::scale_of(T::widest(a), inv);
+                const int64_t col = static_cast<int64_t>(tc) * kB + tid;
+                if (col < p.C) p.scale_t[(b * p.C + col) * p.rt + tr] = scale;
+                col_inv[tid] = inv;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < 8; j += 4) {
+                const float4 f = *reinterpret_cast<const float4 *>(col_inv + 8 * cg + j);
+                invs[j] = f.x, invs[j + 1] = f.y, invs[j + 2] = f.z, invs[j + 3] = f.w;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) invs[j] = tile_inv;
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            float inv = tile_inv;
-            if (!p.square) {
-                // (the other half of a word is another column)
-                const uint32_t a = T::k16 ? (j & 1 ? m[j / 2] >> 16 : m[j / 2] & 0xffffu) : m[j % kW];
-                const float scale = blocks::scale_of(T::widest(a), inv);
-                if (rg == 0 && c0 + j < p.C) p.scale_t[(b * p.C + c0 + j) * p.rt + tr] = scale;
-            }
+            const float inv = invs[j];
             const uint32_t lo =
                 blocks::pack_e4m3x4(v.at(0, j) * inv, v.at(1, j) * inv, v.at(2, j) * inv, v.at(3, j) * inv);
             const uint32_t hi =
