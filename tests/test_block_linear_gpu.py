@@ -115,7 +115,7 @@ def test_residual_at_any_alignment(T, N, K, dtype):
 def test_both_kernels_every_tile_and_split_are_reached():
     plans = [v.describe_block_linear_plan(T, N, K) for T, N, K in SMALL + PAIRS]
     assert {p.kernel for p in plans} == {"pairs", "small"}
-    assert {p.rows for p in plans if p.kernel == "small"} == {16, 64, 128}
+    assert {p.rows for p in plans if p.kernel == "small"} == {16, 32, 64, 128}
     assert {1, 2, 4, 8} <= {p.split for p in plans}
     assert {p.per_stage for p in plans if p.kernel == "small"} == {1, 2}
 

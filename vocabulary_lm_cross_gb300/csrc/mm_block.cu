@@ -20,7 +20,7 @@ namespace mmb {
 namespace {
 
 constexpr int kMaxDevices = 64;
-constexpr int kBns[3] = {16, 64, 128};  // rows of x in a small tile (32 were never the fastest)
+constexpr int kBns[4] = {16, 32, 64, 128};  // rows of x in a small tile
 // Shared memory of an SM (228 KB, 1 KB of it reserved per resident CTA) and, so that a
 // CTA that waits for TMEM columns never waits on one that waits for it, the least a CTA of
 // single-CTA kernels takes for its columns (mm_small.cuh) and beside the pair kernels.
@@ -33,6 +33,7 @@ using PairKernel = void (*)(const PairMaps, const PairParams);
 SmallKernel small_kernel(int bn, bool residual) {
     switch (bn) {
         case 16: return residual ? mm_block_small_kernel<8, true> : mm_block_small_kernel<8, false>;
+        case 32: return residual ? mm_block_small_kernel<16, true> : mm_block_small_kernel<16, false>;
         case 64: return residual ? mm_block_small_kernel<32, true> : mm_block_small_kernel<32, false>;
         default: return residual ? mm_block_small_kernel<64, true> : mm_block_small_kernel<64, false>;
     }
@@ -139,15 +140,16 @@ bool small_layout(const Fwd &f, int bn, int split, int per_sm, int per_stage, Pl
 
 int64_t groups_used(const Fwd &f) { return f.offsets ? std::min(f.groups, f.T) : 1; }
 
-// Estimates in SM clocks at 1.9 GHz, from a sweep on GB300 of every bn, split, per_sm and
-// per_stage over 22 products (T = 1 .. 8192, dense and of 8 .. 128 experts): the chosen plan
-// is the fastest or within 8 % of it.  A block costs an SM kSmallBlock[bn] clocks (of a pair
-// tile kPairBlock) and the weights come from HBM at 6.8 TB/s at best.  Where a group's rows
-// are known on the device only, a group takes half a tile more than its average.  Two CTAs
-// per SM are for tiles of 16 rows (T 512, 32 experts, K 4096, N 4096 95.8 us, one CTA 107),
-// two blocks a stage wherever there are two (64 rows 111.8 us, one block 122).
+// Estimates in SM clocks at 1.9 GHz, from sweeps on GB300 of every bn, split, per_sm and
+// per_stage over 26 products (T = 1 .. 8192, dense and of 8 .. 128 experts): the chosen plan
+// is within 10 % of the fastest. A block costs an SM kSmallBlock[bn] clocks (of a pair tile
+// kPairBlock) and the weights come from HBM at 6.8 TB/s at best.  Where a group's rows are
+// known on the device only, a group takes half a tile more than its average.  Two CTAs per
+// SM are for tiles of few rows (us with two and with one: T 512, 32 experts, K 4096, N 4096
+// in tiles of 16 96 and 107, T 2048, 64 experts, N 2048 in tiles of 32 103 and 140), two
+// blocks a stage wherever there are two (the latter 103 and 108).
 constexpr double kHbmBytesPerClock = 3570.;
-constexpr double kSmallBlock[3] = {480., 900., 1100.}, kPairBlock = 1100.;
+constexpr double kSmallBlock[4] = {480., 600., 1000., 1100.}, kPairBlock = 1100.;
 constexpr double kLoneCta = 1.25;  // one CTA on an SM that could take two
 constexpr double kSmallCta = 6000., kPairCta = 7500., kSplitSync = 1500.;
 
@@ -166,7 +168,7 @@ Plan choose(const Fwd &f, const Capacity &cap) {
     best.pair = true;
     best.clocks = joined(std::ceil(tiles_of(256, (f.N + kPairN - 1) / kPairN) / cap.pairs) *
                          chunks * kPairBlock) + kPairCta;
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < 4; ++i) {
         const int bn = kBns[i], per_sm = bn <= 2 * kSmallTwoNc ? 2 : 1;
         const double tiles = tiles_of(bn, (f.N + 127) / 128);
         if (tiles > 1e6) continue;  // pair tiles

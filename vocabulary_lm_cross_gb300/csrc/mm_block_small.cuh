@@ -2,7 +2,7 @@
 // acc[n, t] = W x^T on 128 weight rows x bn rows of x, one CTA per SM.
 //
 // With few rows the product is bound by streaming the weights, so these take the tensor
-// core's M side and x's rows its N side (bn = 16, 64 or 128).  A ring of stages is filled by
+// core's M side and x's rows its N side (bn = 16 .. 128).  A ring of stages is filled by
 // TMA; a CTA walks over tiles, so the next tile's weights are on their way while the last
 // one's sums leave.  Four TMEM buffers of bn columns hold the sums of the last four blocks.
 //
@@ -37,7 +37,7 @@ constexpr int kSmallBars = 2 * kMaxStages + 2 * kSmallBufs + 1;
 constexpr int kSmallTail = 8 * kSmallBars + 16;
 
 // Two CTAs may share an SM where a thread has few sums.
-constexpr int kSmallTwoNc = 8;
+constexpr int kSmallTwoNc = 16;
 
 struct SmallTile {
     int g, row, end, n;  // group, first row of x and the group's end, first weight row of the group
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kSmallThreads, NC <= kSmallTwoNc ? 2 : 1)
             const int n = t.n + wrow;
             const int row = t.row + half * NC;  // of x: this thread's first
             // rows of x whose sums this thread stores, from `row` (split: below)
-            constexpr bool kAhead = RES && NC <= kSmallTwoNc;  // (more would take the sums' registers)
+            constexpr bool kAhead = RES && NC <= 8;  // (more would take the sums' registers)
             uint16_t res[kAhead ? NC : 1];
             if constexpr (kAhead) {
                 if (p.split == 1) {
@@ -257,6 +257,8 @@ __global__ void __launch_bounds__(kSmallThreads, NC <= kSmallTwoNc ? 2 : 1)
                     uint32_t d[kPiece];
                     if constexpr (NC == 8)
                         tc::tmem_ld8(tbase + b * bn, d);
+                    else if constexpr (NC == 16)
+                        tc::tmem_ld16(tbase + b * bn, d);
                     else
                         tc::tmem_ld32(tbase + b * bn + h, d);
                     tc::tmem_ld_wait();

@@ -39,6 +39,8 @@ struct Params {
     int64_t R, C;
     int rt, ct;                   // tiles down and across
     int square;
+    int q_vec;                    // q's rows take 8-byte stores
+    uintptr_t first, last;        // x's memory
 };
 
 // A thread's eight rows of eight columns, as they are in memory: 16-bit ones two to a
@@ -60,6 +62,58 @@ struct Tile {
             return w;
         }
     }
+    // Row i from `from`, its first n values (n may be 0, or less); 16-byte aligned, n whole.
+    __device__ __forceinline__ void load16(int i, const unsigned char *from, int64_t n) {
+#pragma unroll
+        for (int k = 0; k < kWords / 4; ++k) {
+            const uint4 q = n > 0 ? reinterpret_cast<const uint4 *>(from)[k] : make_uint4(0, 0, 0, 0);
+            u[i][4 * k] = q.x, u[i][4 * k + 1] = q.y, u[i][4 * k + 2] = q.z, u[i][4 * k + 3] = q.w;
+        }
+    }
+    // At any alignment: the 16-byte units that hold them, moved into place, where those lie
+    // between `first` and `last`; else one by one.
+    __device__ __forceinline__ void load(int i, const unsigned char *from, int64_t n, uintptr_t first,
+                                         uintptr_t last) {
+        constexpr int kElt = k16 ? 2 : 4;
+        const uintptr_t a = reinterpret_cast<uintptr_t>(from), unit = a & ~uintptr_t{15};
+        const uint32_t off = static_cast<uint32_t>(a & 15);
+        const int64_t take = n < 8 ? n : 8;
+        if (take > 0 && unit >= first && ((a + take * kElt + 15) & ~uintptr_t{15}) <= last) {
+            uint32_t w[kWords + 4];
+#pragma unroll
+            for (int k = 0; k <= kWords / 4; ++k) {
+                uint4 q = make_uint4(0, 0, 0, 0);
+                if (16u * k < off + take * kElt) q = *reinterpret_cast<const uint4 *>(unit + 16 * k);
+                w[4 * k] = q.x, w[4 * k + 1] = q.y, w[4 * k + 2] = q.z, w[4 * k + 3] = q.w;
+            }
+#pragma unroll
+            for (int k = 0; k < kWords + 2; ++k) w[k] = off & 8 ? w[k + 2] : w[k];
+#pragma unroll
+            for (int k = 0; k < kWords + 1; ++k) w[k] = off & 4 ? w[k + 1] : w[k];
+#pragma unroll
+            for (int k = 0; k < kWords; ++k) u[i][k] = k16 ? __funnelshift_r(w[k], w[k + 1], (off & 2) * 8) : w[k];
+            if (take < 8) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (j >= take) {
+                        if constexpr (k16)
+                            u[i][j / 2] &= j & 1 ? 0xffffu : 0xffff0000u;
+                        else
+                            u[i][j] = 0;
+                    }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if constexpr (k16) {
+                    const uint32_t e = j < take ? reinterpret_cast<const uint16_t *>(from)[j] : 0;
+                    u[i][j / 2] = j & 1 ? u[i][j / 2] | e << 16 : e;
+                } else {
+                    u[i][j] = j < take ? reinterpret_cast<const uint32_t *>(from)[j] : 0;
+                }
+            }
+        }
+    }
     __device__ __forceinline__ float at(int i, int j) const {
         if constexpr (k16) {
             float a, b;
@@ -71,7 +125,7 @@ struct Tile {
     }
 };
 
-template <int DT, bool VEC, bool ROWS, bool TRANS>
+template <int DT, bool ALIGNED, bool ROWS, bool TRANS>
 __global__ void __launch_bounds__(kThreads, DT == VLMCE_F32 ? 2 : 3) quant_kernel(const Params p) {
     using T = Tile<DT>;
     constexpr int kWarps = kThreads / 32, kW = T::kWords;
@@ -92,26 +146,11 @@ __global__ void __launch_bounds__(kThreads, DT == VLMCE_F32 ? 2 : 3) quant_kerne
     T v;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const bool row = r0 + i < p.R;
-        if constexpr (VEC) {
-            const uint4 *from = reinterpret_cast<const uint4 *>(x + i * p.x_ld + c0 * blocks::elt_bytes<DT>);
-#pragma unroll
-            for (int k = 0; k < kW / 4; ++k) {
-                const uint4 q = row && c0 < p.C ? from[k] : make_uint4(0, 0, 0, 0);
-                v.u[i][4 * k] = q.x, v.u[i][4 * k + 1] = q.y, v.u[i][4 * k + 2] = q.z, v.u[i][4 * k + 3] = q.w;
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const bool in = row && c0 + j < p.C;
-                if constexpr (T::k16) {
-                    const uint32_t e = in ? reinterpret_cast<const uint16_t *>(x + i * p.x_ld)[c0 + j] : 0;
-                    v.u[i][j / 2] = j & 1 ? v.u[i][j / 2] | e << 16 : e;
-                } else {
-                    v.u[i][j] = in ? reinterpret_cast<const uint32_t *>(x + i * p.x_ld)[c0 + j] : 0;
-                }
-            }
-        }
+        const int64_t n = r0 + i < p.R ? p.C - c0 : 0;  // of the eight columns, those there are
+        if (ALIGNED)
+            v.load16(i, x + i * p.x_ld + c0 * blocks::elt_bytes<DT>, n);
+        else
+            v.load(i, x + i * p.x_ld + c0 * blocks::elt_bytes<DT>, n, p.first, p.last);
     }
     float tile_inv = 1.f;
     if (p.square) {
@@ -168,8 +207,8 @@ __global__ void __launch_bounds__(kThreads, DT == VLMCE_F32 ? 2 : 3) quant_kerne
                 blocks::pack_e4m3x4(v.at(i, 4) * inv, v.at(i, 5) * inv, v.at(i, 6) * inv, v.at(i, 7) * inv);
             if (r0 + i < p.R) {
                 unsigned char *row = q + i * p.q_ld;
-                if (VEC) {
-                    if (c0 < p.C) *reinterpret_cast<uint2 *>(row + c0) = make_uint2(lo, hi);
+                if (p.q_vec && c0 + 8 <= p.C) {
+                    *reinterpret_cast<uint2 *>(row + c0) = make_uint2(lo, hi);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
@@ -241,10 +280,10 @@ __global__ void __launch_bounds__(kThreads, DT == VLMCE_F32 ? 2 : 3) quant_kerne
 }
 
 using Kernel = void (*)(const Params);
-template <int DT, bool VEC>
+template <int DT, bool ALIGNED>
 Kernel kernel_of(bool rows, bool trans) {
-    if (!trans) return quant_kernel<DT, VEC, true, false>;
-    return rows ? quant_kernel<DT, VEC, true, true> : quant_kernel<DT, VEC, false, true>;
+    if (!trans) return quant_kernel<DT, ALIGNED, true, false>;
+    return rows ? quant_kernel<DT, ALIGNED, true, true> : quant_kernel<DT, ALIGNED, false, true>;
 }
 Kernel kernel_of(int dt, bool vec, bool rows, bool trans) {
     switch (dt) {
@@ -323,8 +362,10 @@ extern "C" vlmce_status quantize_blocks(const void *x, int32_t dtype, int64_t ba
     p.rt = static_cast<int>(rt);
     p.ct = static_cast<int>(ct);
     p.square = square != 0;
-    const bool vec = C % 8 == 0 && aligned(x, 16) && p.x_ld % 16 == 0 && p.x_batch % 16 == 0 &&
-                     (!q || (aligned(q, 8) && q_stride % 8 == 0));
+    p.q_vec = aligned(q, 8) && q_stride % 8 == 0 && (batch == 1 || p.q_batch % 8 == 0);
+    p.first = reinterpret_cast<uintptr_t>(x);
+    p.last = p.first + static_cast<uintptr_t>(in.bytes);
+    const bool vec = C % 8 == 0 && aligned(x, 16) && p.x_ld % 16 == 0 && p.x_batch % 16 == 0;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
