@@ -319,3 +319,35 @@ def test_streams_and_graphs():
     torch.cuda.synchronize()
     got = [t.clone() for t in out]
     assert all(torch.equal(a, b) for a, b in zip(got, step()))
+
+
+def test_outputs_and_rows_beyond_2_to_the_31_elements():
+    g = gen(6)
+    N, K = 16384, 256
+    T = 2 ** 31 // N + 300
+    x, xs = e4m3(g, 300, K), scales(g, 300, 2)
+    w, ws = e4m3(g, N, K), scales(g, N // 128, 2)
+    far = torch.zeros((T, K), dtype=FP8, device="cuda")
+    fars = torch.ones((T, 2), device="cuda")
+    far[-300:], fars[-300:] = x, xs
+    want = v.block_linear_fwd(x, xs, w, ws)
+    got = v.block_linear_fwd(far, fars, w, ws)
+    # (another kernel sums the same two blocks in the same order)
+    assert torch.equal(got[-300:], want) and not got[:128].any()
+    off = torch.tensor([0, 5, T - 300, T], dtype=torch.int32, device="cuda")
+    y = torch.zeros((T, N), dtype=torch.bfloat16, device="cuda")
+    v.block_linear_fwd(far, fars, w.expand(3, N, K).contiguous(), ws.expand(3, N // 128, 2).contiguous(), offsets=off,
+                       out=y)
+    assert torch.equal(y[-300:], want)
+
+
+def test_a_gradient_beyond_2_to_the_31_elements():
+    g = gen(7)
+    N, K, E = 8192, 8192, 34
+    d, sd = e4m3(g, N, 256), scales(g, N, 2)
+    e, se = e4m3(g, K, 256), scales(g, K, 2)
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[E - 1:] = torch.tensor([128, 256], dtype=torch.int32)
+    got = v.block_linear_dweight(d, sd, e, se, offsets=off, dweight_dtype=torch.bfloat16)
+    last = v.block_linear_dweight(d[:, 128:], sd[:, 1:], e[:, 128:], se[:, 1:], dweight_dtype=torch.bfloat16)
+    assert torch.equal(got[-1], last) and not got[:E - 2].any() and got[E - 2].any()
