@@ -78,7 +78,8 @@ def test_sort_of_nothing_of_nobodys_and_of_strided_ids():
 
 
 SHAPES = [(1, 1, 1, 1, 1), (1, 8, 8, 4096, 1), (5, 3, 4, 100, 16), (37, 2, 6, 1001, 128), (64, 8, 16, 264, 1),
-          (130, 12, 12, 2056, 16), (300, 4, 64, 640, 128)]
+          (130, 12, 12, 2056, 16), (300, 4, 64, 640, 128),
+          (9, 3, 5, 4112, 16), (70, 2, 3, 48, 1), (33, 2, 4, 8200, 1)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
