@@ -199,6 +199,19 @@ def test_no_tokens():
     assert r.drows.shape == (0, 64) and r.dweights.shape == (0, 2)
 
 
+def test_rows_between_are_cleared_without_any_tokens():
+    """An order of no tokens whose experts still hold rows: those become zero."""
+    empty = v.moe_sort(torch.empty((0, 2), dtype=torch.int32, device="cuda"), 2)
+    order = empty._replace(offsets=torch.tensor([0, 3, 4], dtype=torch.int32, device="cuda"), rows=5)
+    x = torch.empty((0, 40), device="cuda")
+    data = randn(gen(3), (5, 40), torch.float32)
+    for call in (lambda out: v.moe_gather(x, order, out=out),
+                 lambda out: v.moe_combine_bwd(x, data, order, out=out)):
+        out = torch.full((5, 40), 7.0, device="cuda")
+        call(out)
+        assert torch.equal(out[:4], torch.zeros_like(out[:4])) and bool((out[4] == 7.0).all())
+
+
 def test_rows_beyond_2_to_the_31_elements():
     H, T = 8192, 4
     R = 2 ** 31 // H + 40

@@ -786,7 +786,7 @@ extern "C" vlmce_status moe_combine_bwd(const void *dy, int64_t dy_stride, const
     if (overlap(out, d) || overlap(out, in) || overlap(out, w) || overlap(out, dw) || overlap(out, pos) ||
         overlap(dw, d) || overlap(dw, in) || overlap(dw, w) || overlap(dw, pos))
         return VLMCE_ERR_INVALID_ARG;
-    if (T == 0) return VLMCE_OK;
+    if (T == 0 && out.rows == 0) return VLMCE_OK;
     DeviceInfo dev;
     st = current_device(&dev);
     if (st != VLMCE_OK) return st;
