@@ -100,7 +100,9 @@ def empty_fp8(shape, device) -> torch.Tensor:
     n = shape[-1]
     if n % 16 == 0:
         return torch.empty(shape, dtype=_FP8, device=device)
-    return torch.empty((*shape[:-1], padded(n)), dtype=_FP8, device=device)[..., :n]
+    ld = padded(n)
+    return torch.empty_strided(shape, (ld, 1) if len(shape) == 2 else (shape[1] * ld, ld, 1),
+                               dtype=_FP8, device=device)
 
 
 def moe_gather(x: torch.Tensor, order: MoEOrder, *, fp8: bool = False,
@@ -121,8 +123,6 @@ def moe_gather(x: torch.Tensor, order: MoEOrder, *, fp8: bool = False,
     if out is None:
         out = empty_fp8((R, H), dev) if fp8 else torch.empty((R, H), dtype=odt, device=dev)
     os_ = rows(out, "out", (R, H), odt, dev)
-    if R <= 1:
-        os_ = max(os_, H)
     scale = torch.empty((R, (H + 127) // 128), dtype=torch.float32, device=dev) if fp8 else None
     st = capi.lib().moe_gather(x.data_ptr(), xs, DTYPES[dt], pos, off, cnt, T, k, E, R, H,
                                out.data_ptr(), os_, DTYPES[odt],
