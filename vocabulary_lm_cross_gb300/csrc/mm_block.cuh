@@ -16,6 +16,7 @@
 
 #include <cuda.h>
 
+#include "f32x2.cuh"
 #include "mbar_wait.cuh"
 #include "mm_block_types.h"
 #include "ptx_async.cuh"
@@ -23,32 +24,6 @@
 
 namespace vlmce {
 namespace mmb {
-
-// ------------------------------------------------------------ packed fp32
-__device__ __forceinline__ uint64_t pack2(uint32_t a, uint32_t b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) {
-    uint32_t x, y;
-    asm("mov.b64 {%0, %1}, %2;" : "=r"(x), "=r"(y) : "l"(v));
-    a = __uint_as_float(x);
-    b = __uint_as_float(y);
-}
-__device__ __forceinline__ uint64_t both(float a) {
-    return pack2(__float_as_uint(a), __float_as_uint(a));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 
 // ------------------------------------------------------------ the groups' tiles
 // In shared memory: for each group its rows and the tiles of `step` rows before it.

@@ -18,6 +18,7 @@
 #include <climits>
 
 #include "blocks.cuh"
+#include "f32x2.cuh"
 #include "host_util.h"
 #include "ptx.cuh"
 #include "rows_host.h"
@@ -39,7 +40,7 @@ struct Params {
     int64_t R, C;
     int rt, ct;                   // tiles down and across
     int square;
-    int q_vec;                    // q's rows take 8-byte stores
+    int q_vec, qt_vec;            // q's rows take 8-byte stores, qt's 16-byte ones
     uintptr_t first, last;        // x's memory
 };
 
@@ -51,8 +52,31 @@ struct Tile {
     static constexpr int kWords = k16 ? 4 : 8;  // of a row
     uint32_t u[8][kWords];
 
+    // The larger magnitudes of two words, signs aside (any sign in the result).
+    static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+        uint32_t r;
+        if constexpr (DT == VLMCE_BF16)
+            asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        else if constexpr (DT == VLMCE_F16)
+            asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        else {
+            float m;
+            asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(m) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
+            r = __float_as_uint(m);
+        }
+        return r;
+    }
     static __device__ __forceinline__ uint32_t magnitudes(uint32_t w) { return w & (k16 ? 0x7fff7fffu : 0x7fffffffu); }
-    static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return k16 ? __vmaxu2(a, b) : max(a, b); }
+    // Columns 2 k and 2 k + 1 of row i.
+    __device__ __forceinline__ uint64_t pair(int i, int k) const {
+        if constexpr (k16) {
+            float a, b;
+            act::unpack16x2(u[i][k], a, b, DT == VLMCE_F16);
+            return pack2(__float_as_uint(a), __float_as_uint(b));
+        } else {
+            return pack2(u[i][2 * k], u[i][2 * k + 1]);
+        }
+    }
     // The larger magnitude of a word, as an fp32 number's bits.
     static __device__ __forceinline__ uint32_t widest(uint32_t w) {
         if constexpr (k16) {
@@ -62,11 +86,11 @@ struct Tile {
             return w;
         }
     }
-    // Row i from `from`, its first n values (n may be 0, or less); 16-byte aligned, n whole.
-    __device__ __forceinline__ void load16(int i, const unsigned char *from, int64_t n) {
+    // Row i from `from`, 16-byte aligned, or zeros.
+    __device__ __forceinline__ void load16(int i, const unsigned char *from, bool in) {
 #pragma unroll
         for (int k = 0; k < kWords / 4; ++k) {
-            const uint4 q = n > 0 ? reinterpret_cast<const uint4 *>(from)[k] : make_uint4(0, 0, 0, 0);
+            const uint4 q = in ? reinterpret_cast<const uint4 *>(from)[k] : make_uint4(0, 0, 0, 0);
             u[i][4 * k] = q.x, u[i][4 * k + 1] = q.y, u[i][4 * k + 2] = q.z, u[i][4 * k + 3] = q.w;
         }
     }
@@ -114,15 +138,6 @@ struct Tile {
             }
         }
     }
-    __device__ __forceinline__ float at(int i, int j) const {
-        if constexpr (k16) {
-            float a, b;
-            act::unpack16x2(u[i][j / 2], a, b, DT == VLMCE_F16);
-            return j & 1 ? b : a;
-        } else {
-            return __uint_as_float(u[i][j]);
-        }
-    }
 };
 
 template <int DT, bool ALIGNED, bool ROWS, bool TRANS>
@@ -143,23 +158,30 @@ __global__ void __launch_bounds__(kThreads, DT == VLMCE_F32 ? 2 : 3) quant_kerne
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
     const unsigned char *x = p.x + b * p.x_batch + r0 * p.x_ld;
+    const int rows_in = static_cast<int>(min(int64_t{8}, p.R - r0));  // of the eight (may be less than 0)
+    const int64_t cols_in = p.C - c0;
     T v;
+    if (ALIGNED && (tr + 1) * int64_t{kB} <= p.R && (tc + 1) * int64_t{kB} <= p.C) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int64_t n = r0 + i < p.R ? p.C - c0 : 0;  // of the eight columns, those there are
-        if (ALIGNED)
-            v.load16(i, x + i * p.x_ld + c0 * blocks::elt_bytes<DT>, n);
-        else
-            v.load(i, x + i * p.x_ld + c0 * blocks::elt_bytes<DT>, n, p.first, p.last);
+        for (int i = 0; i < 8; ++i) v.load16(i, x + i * p.x_ld + c0 * blocks::elt_bytes<DT>, true);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const unsigned char *from = x + i * p.x_ld + c0 * blocks::elt_bytes<DT>;
+            if (ALIGNED)
+                v.load16(i, from, i < rows_in && cols_in > 0);
+            else
+                v.load(i, from, i < rows_in ? cols_in : 0, p.first, p.last);
+        }
     }
     float tile_inv = 1.f;
     if (p.square) {
-        uint32_t a = 0;
+        uint32_t a = v.u[0][0];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int k = 0; k < kW; ++k) a = T::larger(a, T::magnitudes(v.u[i][k]));
-        a = __reduce_max_sync(0xffffffffu, T::widest(a));
+            for (int k = 0; k < kW; ++k) a = T::larger(a, v.u[i][k]);
+        a = __reduce_max_sync(0xffffffffu, T::widest(T::magnitudes(a)));
         if (lane == 0) tile_max[tid >> 5] = a;
         __syncthreads();
 #pragma unroll
@@ -173,53 +195,62 @@ __global__ void __launch_bounds__(kThreads, DT == VLMCE_F32 ? 2 : 3) quant_kerne
         uint32_t *mine = col_max[tid >> 5] + kW * cg;  // of the warp's 16 rows
 #pragma unroll
         for (int k = 0; k < kW; ++k) {
-            uint32_t a = 0;
+            uint32_t a = v.u[0][k];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) a = T::larger(a, T::magnitudes(v.u[i][k]));
+            for (int i = 1; i < 8; ++i) a = T::larger(a, v.u[i][k]);
             a = T::larger(a, __shfl_xor_sync(0xffffffffu, a, 16));
-            if (lane < 16) mine[k] = a;
+            if (lane < 16) mine[k] = T::magnitudes(a);
         }
     }
     if constexpr (ROWS) {
         unsigned char *q = p.q + b * p.q_batch + r0 * p.q_ld;
         float mine = tile_inv;  // of row lane % 8 of the eight
         if (!p.square) {
-            uint32_t m = 0;
+            // the eight rows' maxima over the 16 lanes: each step, a lane gives away half of
+            // its rows and takes the other half's values (8 exchanges instead of 32)
+            uint32_t m[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                uint32_t a = 0;
+                m[i] = v.u[i][0];
 #pragma unroll
-                for (int k = 0; k < kW; ++k) a = T::larger(a, T::magnitudes(v.u[i][k]));
-#pragma unroll
-                for (int d = 8; d > 0; d /= 2) a = T::larger(a, __shfl_xor_sync(0xffffffffu, a, d));
-                if ((lane & 7) == i) m = a;
+                for (int k = 1; k < kW; ++k) m[i] = T::larger(m[i], v.u[i][k]);
             }
+#pragma unroll
+            for (int d = 4; d > 0; d /= 2)
+#pragma unroll
+                for (int i = 0; i < d; ++i) {
+                    const bool upper = lane & d;
+                    const uint32_t keep = upper ? m[i + d] : m[i], give = upper ? m[i] : m[i + d];
+                    m[i] = T::larger(keep, __shfl_xor_sync(0xffffffffu, give, d));
+                }
+            m[0] = T::magnitudes(T::larger(m[0], __shfl_xor_sync(0xffffffffu, m[0], 8)));
             // (the two divisions cost more than the values' own arithmetic: one row a lane)
-            const float scale = blocks::scale_of(T::widest(m), mine);
+            const float scale = blocks::scale_of(T::widest(m[0]), mine);
             if (cg < 8 && r0 + cg < p.R) p.scale[(b * p.R + r0 + cg) * p.ct + tc] = scale;
         }
+        const bool wide = p.q_vec && cols_in >= 8;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float inv = __shfl_sync(0xffffffffu, mine, (lane & 16) + i);
-            const uint32_t lo =
-                blocks::pack_e4m3x4(v.at(i, 0) * inv, v.at(i, 1) * inv, v.at(i, 2) * inv, v.at(i, 3) * inv);
-            const uint32_t hi =
-                blocks::pack_e4m3x4(v.at(i, 4) * inv, v.at(i, 5) * inv, v.at(i, 6) * inv, v.at(i, 7) * inv);
-            if (r0 + i < p.R) {
-                unsigned char *row = q + i * p.q_ld;
-                if (p.q_vec && c0 + 8 <= p.C) {
-                    *reinterpret_cast<uint2 *>(row + c0) = make_uint2(lo, hi);
+            const uint64_t inv = both(__shfl_sync(0xffffffffu, mine, (lane & 16) + i));
+            float f[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) unpack2(mul2(v.pair(i, k), inv), f[2 * k], f[2 * k + 1]);
+            const uint32_t lo = blocks::pack_e4m3x4(f[0], f[1], f[2], f[3]);
+            const uint32_t hi = blocks::pack_e4m3x4(f[4], f[5], f[6], f[7]);
+            if (i < rows_in) {
+                unsigned char *row = q + i * p.q_ld + c0;
+                if (wide) {
+                    *reinterpret_cast<uint2 *>(row) = make_uint2(lo, hi);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        if (c0 + j < p.C)
-                            row[c0 + j] = static_cast<unsigned char>((j < 4 ? lo : hi) >> (8 * (j & 3)));
+                        if (j < cols_in) row[j] = static_cast<unsigned char>((j < 4 ? lo : hi) >> (8 * (j & 3)));
                 }
             }
         }
     }
     if constexpr (TRANS) {
-        float invs[8];
+        uint64_t invs[4];  // of the eight columns
         if (!p.square) {
             __syncthreads();  // col_max is complete
             if (tid < kB) {   // a column a thread
@@ -239,42 +270,49 @@ __global__ void __launch_bounds__(kThreads, DT == VLMCE_F32 ? 2 : 3) quant_kerne
             }
             __syncthreads();
 #pragma unroll
-            for (int j = 0; j < 8; j += 4) {
-                const float4 f = *reinterpret_cast<const float4 *>(col_inv + 8 * cg + j);
-                invs[j] = f.x, invs[j + 1] = f.y, invs[j + 2] = f.z, invs[j + 3] = f.w;
+            for (int k = 0; k < 4; k += 2) {
+                const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(col_inv + 8 * cg + 2 * k);
+                invs[k] = f.x, invs[k + 1] = f.y;
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) invs[j] = tile_inv;
+            for (int k = 0; k < 4; ++k) invs[k] = both(tile_inv);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float inv = invs[j];
-            const uint32_t lo =
-                blocks::pack_e4m3x4(v.at(0, j) * inv, v.at(1, j) * inv, v.at(2, j) * inv, v.at(3, j) * inv);
-            const uint32_t hi =
-                blocks::pack_e4m3x4(v.at(4, j) * inv, v.at(5, j) * inv, v.at(6, j) * inv, v.at(7, j) * inv);
-            *reinterpret_cast<uint2 *>(tq + (8 * cg + j) * kB + 8 * (rg ^ cg)) = make_uint2(lo, hi);
+        for (int k = 0; k < 4; ++k) {
+            float e[8], o[8];  // columns 2 k and 2 k + 1
+#pragma unroll
+            for (int i = 0; i < 8; ++i) unpack2(mul2(v.pair(i, k), invs[k]), e[i], o[i]);
+            unsigned char *to = tq + (8 * cg + 2 * k) * kB + 8 * (rg ^ cg);
+            *reinterpret_cast<uint2 *>(to) =
+                make_uint2(blocks::pack_e4m3x4(e[0], e[1], e[2], e[3]), blocks::pack_e4m3x4(e[4], e[5], e[6], e[7]));
+            *reinterpret_cast<uint2 *>(to + kB) =
+                make_uint2(blocks::pack_e4m3x4(o[0], o[1], o[2], o[3]), blocks::pack_e4m3x4(o[4], o[5], o[6], o[7]));
         }
         __syncthreads();
-        // 16 rows a thread, eight threads a column
-        const int64_t rows0 = static_cast<int64_t>(tr) * kB;
+        // 16 rows a thread, eight threads a column, every 32nd column
+        const int c = tid >> 3, u = tid & 7;
+        const int64_t r = static_cast<int64_t>(tr) * kB + 16 * u, col = static_cast<int64_t>(tc) * kB + c;
+        const int left = static_cast<int>(min(int64_t{16}, p.R - r));
+        if (left <= 0) return;
+        unsigned char *to = p.qt + b * p.qt_batch + col * p.qt_ld + r;
+        const bool wide = p.qt_vec && left == 16;
 #pragma unroll
         for (int i = 0; i < kB * kB / 16 / kThreads; ++i) {
-            const int at = i * kThreads + tid, c = at >> 3, u = at & 7;
-            const int64_t col = static_cast<int64_t>(tc) * kB + c, r = rows0 + 16 * u;
-            if (col >= p.C || r >= p.R) continue;
-            const uint2 lo = *reinterpret_cast<const uint2 *>(tq + c * kB + 8 * ((2 * u) ^ (c >> 3)));
-            const uint2 hi = *reinterpret_cast<const uint2 *>(tq + c * kB + 8 * ((2 * u + 1) ^ (c >> 3)));
-            unsigned char *to = p.qt + b * p.qt_batch + col * p.qt_ld + r;
-            if (r + 16 <= p.R && (reinterpret_cast<uintptr_t>(to) & 15) == 0) {
+            if (col + 32 * i >= p.C) break;
+            const unsigned char *from = tq + (c + 32 * i) * kB;
+            const int swizzle = (c >> 3) + 4 * i;
+            const uint2 lo = *reinterpret_cast<const uint2 *>(from + 8 * ((2 * u) ^ swizzle));
+            const uint2 hi = *reinterpret_cast<const uint2 *>(from + 8 * ((2 * u + 1) ^ swizzle));
+            if (wide) {
                 *reinterpret_cast<uint4 *>(to) = make_uint4(lo.x, lo.y, hi.x, hi.y);
             } else {
                 const uint32_t w[4] = {lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
                 for (int k = 0; k < 16; ++k)
-                    if (r + k < p.R) to[k] = static_cast<unsigned char>(w[k / 4] >> (8 * (k & 3)));
+                    if (k < left) to[k] = static_cast<unsigned char>(w[k / 4] >> (8 * (k & 3)));
             }
+            to += 32 * p.qt_ld;
         }
     }
 }
@@ -363,6 +401,7 @@ extern "C" vlmce_status quantize_blocks(const void *x, int32_t dtype, int64_t ba
     p.ct = static_cast<int>(ct);
     p.square = square != 0;
     p.q_vec = aligned(q, 8) && q_stride % 8 == 0 && (batch == 1 || p.q_batch % 8 == 0);
+    p.qt_vec = aligned(qt, 16) && qt_stride % 16 == 0;
     p.first = reinterpret_cast<uintptr_t>(x);
     p.last = p.first + static_cast<uintptr_t>(in.bytes);
     const bool vec = C % 8 == 0 && aligned(x, 16) && p.x_ld % 16 == 0 && p.x_batch % 16 == 0;
