@@ -93,6 +93,27 @@ def test_a_batch_is_its_matrices(R, C):
                 assert torch.equal(raw(a[e]), raw(b))
 
 
+@pytest.mark.parametrize("square", [False, True])
+@pytest.mark.parametrize("R,C,dtype", [(3001, 4104, "bf16"), (8200, 4096, "f16"), (3001, 4104, "f32"),
+                                       (3001, 4101, "bf16")])
+def test_more_tiles_than_run_at_once(R, C, dtype, square):
+    """The whole is its parts of 256 rows, which the tests above hold against the oracle."""
+    x = randn(gen(C), (R, C), DT[dtype])
+    x *= torch.exp2(torch.arange(R, device="cuda") % 7 - 3)[:, None].to(x.dtype)
+    for rows, transposed in ((True, True), (True, False), (False, True)):
+        r = v.quantize_blocks(x, square=square, rows=rows, transposed=transposed)
+        for at in range(0, R, 256):
+            part = v.quantize_blocks(x[at:at + 256], square=square, rows=rows, transposed=transposed)
+            n, b = min(256, R - at), at // 128
+            if rows:
+                s = r.scale[b:b + part.scale.shape[0]] if square else r.scale[at:at + n]
+                assert torch.equal(r.q[at:at + n].view(torch.uint8), part.q.view(torch.uint8))
+                assert torch.equal(s, part.scale)
+            if transposed:
+                assert torch.equal(r.qt[:, at:at + n].view(torch.uint8), part.qt.view(torch.uint8))
+                assert torch.equal(r.scale_t[:, b:b + part.scale_t.shape[1]], part.scale_t)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_zeros_tiny_values_infinities_and_nans(dtype):
     x = torch.zeros((130, 640), dtype=DT[dtype])

@@ -6,21 +6,26 @@
 // of the weights, and of the inputs by the transposed weight).  Both come from one
 // reading: a CTA has a tile of 128 x 128 in registers, a thread eight rows of eight
 // columns, as they are in memory.  A row's maximum is found among the 16 lanes that share
-// it, a column's among the warps in shared memory (integer maxima: no order in the result).  For the transposed form a
-// thread's eight rows of a column are one 8-byte store into shared memory, the 8-byte
-// units of a column swizzled by its group of eight columns (16 lanes then meet 32
-// different banks), and leave from there as whole 128-byte lines.
+// it, a column's among the warps in shared memory (maxima: no order in the result).  For
+// the transposed form a thread's eight rows of a column are one 8-byte store into shared
+// memory, the 8-byte units of a column swizzled by its group of eight columns (16 lanes then
+// meet 32 different banks), and leave from there as whole 128-byte lines.
 //
-// Bound by memory.
+// Bound by memory and, both ways at once, by the instructions and barriers between reading a
+// tile and writing it (8192 x 6656 bf16: 26.4 us along rows, 164 MB, 6.2 TB/s; both ways 39.8
+// us, 222 MB, 5.6 TB/s, 60 % of the issue slots).  Four CTAs per SM of 64 registers: 51.8 us.
+// Dealing out the tiles in blocks of 2 .. 16 rows of tiles changed nothing.
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <climits>
+#include <mutex>
 
 #include "blocks.cuh"
 #include "f32x2.cuh"
 #include "host_util.h"
 #include "ptx.cuh"
+#include "ptx_async.cuh"
 #include "rows_host.h"
 #include "vlmce.h"
 
@@ -38,11 +43,23 @@ struct Params {
     int64_t x_ld, x_batch;        // bytes
     int64_t q_ld, q_batch, qt_ld, qt_batch;
     int64_t R, C;
-    int rt, ct;                   // tiles down and across
+    int batch, rt, ct;            // matrices, tiles down and across
     int square;
     int q_vec, qt_vec;            // q's rows take 8-byte stores, qt's 16-byte ones
     uintptr_t first, last;        // x's memory
 };
+
+// Whether a CTA goes on to other tiles, staged: aligned ones of 16-bit values (an fp32
+// thread's 32 bytes are two copies, half a sector each: 4096 x 6656 both ways 45 us, a tile a
+// CTA from registers 30; bf16, 8192 x 6656: along rows, transposed, both 26.4, 26.4 and 39.8 us
+// so, 26.7, 29.5 and 41.4 a tile a CTA).  Squares go on for kSquareRun tiles, so that the
+// last ones are dealt out as CTAs end (both ways 35.7, to the end 39.7, a tile a CTA 36.4).
+template <int DT, bool ALIGNED>
+constexpr bool kStaged = ALIGNED && DT != VLMCE_F32;
+constexpr int kSquareRun = 4;
+constexpr int kStage = kB * kB * 2;
+template <int DT>
+constexpr int kCtas = DT == VLMCE_F32 ? 2 : 3;
 
 // A thread's eight rows of eight columns, as they are in memory: 16-bit ones two to a
 // word.  Magnitudes are compared as they are, too (16-bit ones two at a time).
@@ -140,179 +157,212 @@ struct Tile {
     }
 };
 
+// Where a tile is: its matrix, and its place down and across.
+struct Where {
+    int b, tr, tc;
+    __device__ __forceinline__ Where(const Params &p, unsigned at) {
+        int tile = static_cast<int>(at);
+        b = tile / (p.rt * p.ct);
+        tile -= b * (p.rt * p.ct);
+        tr = tile / p.ct;
+        tc = tile - tr * p.ct;
+    }
+};
+
 template <int DT, bool ALIGNED, bool ROWS, bool TRANS>
-__global__ void __launch_bounds__(kThreads, DT == VLMCE_F32 ? 2 : 3) quant_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, kCtas<DT>) quant_kernel(const Params p) {
     using T = Tile<DT>;
     constexpr int kWarps = kThreads / 32, kW = T::kWords;
-    __shared__ uint32_t tile_max[kWarps];
+    extern __shared__ __align__(16) unsigned char staged[];  // kStaged: kStage bytes
+    __shared__ uint32_t tile_max[2][kWarps];
     __shared__ __align__(16) uint32_t col_max[TRANS ? kWarps : 1][16 * kW];
     __shared__ __align__(16) float col_inv[TRANS ? kB : 4];
     __shared__ __align__(16) unsigned char tq[TRANS ? kB * kB : 16];
     const int tid = threadIdx.x, lane = tid & 31;
     const int cg = tid & 15, rg = tid >> 4;  // eight columns, eight rows of the tile
-    const int64_t tile = blockIdx.x;
-    const int64_t b = tile / (static_cast<int64_t>(p.rt) * p.ct);
-    const int in_b = static_cast<int>(tile - b * p.rt * p.ct);
-    const int tr = in_b / p.ct, tc = in_b - tr * p.ct;
-    const int64_t r0 = static_cast<int64_t>(tr) * kB + 8 * rg, c0 = static_cast<int64_t>(tc) * kB + 8 * cg;
+    const unsigned tiles = static_cast<unsigned>(p.batch * p.rt * p.ct), step = gridDim.x;
+    // Each thread's own part of a tile on its way to its own slots: no barrier, and the next
+    // tile's loads are in flight while this one is worked on.
+    const uint32_t slot = ptx::smem_addr(staged) + 16u * tid;
+    auto fetch = [&](unsigned tile) {  // (16-bit values)
+        const Where at(p, tile);
+        const int64_t r0 = static_cast<int64_t>(at.tr) * kB + 8 * rg, c0 = static_cast<int64_t>(at.tc) * kB + 8 * cg;
+        const unsigned char *from = p.x + at.b * p.x_batch + r0 * p.x_ld + c0 * blocks::elt_bytes<DT>;
+        const bool in = c0 < p.C;
+        const int rows_in = static_cast<int>(min(int64_t{8}, p.R - r0));
+#pragma unroll
+        for (int i = 0; i < 8; ++i, from += p.x_ld) {
+            const bool have = in && i < rows_in;
+            ptx::cp_async16_first(slot + i * (16 * kThreads), have ? from : p.x, have ? 16 : 0);
+        }
+        ptx::cp_async_commit();
+    };
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
-    const unsigned char *x = p.x + b * p.x_batch + r0 * p.x_ld;
-    const int rows_in = static_cast<int>(min(int64_t{8}, p.R - r0));  // of the eight (may be less than 0)
-    const int64_t cols_in = p.C - c0;
-    T v;
-    if (ALIGNED && (tr + 1) * int64_t{kB} <= p.R && (tc + 1) * int64_t{kB} <= p.C) {
+    if constexpr (kStaged<DT, ALIGNED>) fetch(blockIdx.x);
+    int parity = 0;
+    for (unsigned tile = blockIdx.x; tile < tiles; tile += step, parity ^= 1) {
+        const Where at(p, tile);
+        const int64_t b = at.b;
+        const int tr = at.tr, tc = at.tc;
+        const int64_t r0 = static_cast<int64_t>(tr) * kB + 8 * rg, c0 = static_cast<int64_t>(tc) * kB + 8 * cg;
+        const int rows_in = static_cast<int>(min(int64_t{8}, p.R - r0));  // of the eight (may be less than 0)
+        const int64_t cols_in = p.C - c0;
+        T v;
+        if constexpr (kStaged<DT, ALIGNED>) {
+            ptx::cp_async_wait<0>();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v.load16(i, x + i * p.x_ld + c0 * blocks::elt_bytes<DT>, true);
-    } else {
+            for (int i = 0; i < 8; ++i) v.load16(i, staged + 16 * (i * kThreads + tid), true);
+            if (tile + step < tiles) fetch(tile + step);
+        } else {
+            const unsigned char *x = p.x + b * p.x_batch + r0 * p.x_ld + c0 * blocks::elt_bytes<DT>;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const unsigned char *from = x + i * p.x_ld + c0 * blocks::elt_bytes<DT>;
-            if (ALIGNED)
-                v.load16(i, from, i < rows_in && cols_in > 0);
-            else
-                v.load(i, from, i < rows_in ? cols_in : 0, p.first, p.last);
+            for (int i = 0; i < 8; ++i)
+                if constexpr (ALIGNED)
+                    v.load16(i, x + i * p.x_ld, i < rows_in && cols_in > 0);
+                else
+                    v.load(i, x + i * p.x_ld, i < rows_in ? cols_in : 0, p.first, p.last);
         }
-    }
-    float tile_inv = 1.f;
-    if (p.square) {
-        uint32_t a = v.u[0][0];
+        float tile_inv = 1.f;
+        if (p.square) {
+            uint32_t a = v.u[0][0];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int k = 0; k < kW; ++k) a = T::larger(a, v.u[i][k]);
-        a = __reduce_max_sync(0xffffffffu, T::widest(T::magnitudes(a)));
-        if (lane == 0) tile_max[tid >> 5] = a;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) a = max(a, tile_max[w]);
-        const float scale = blocks::scale_of(a, tile_inv);
-        if (tid == 0) {
-            if (ROWS) p.scale[(b * p.rt + tr) * p.ct + tc] = scale;
-            if (TRANS) p.scale_t[(b * p.ct + tc) * p.rt + tr] = scale;
-        }
-    } else if constexpr (TRANS) {
-        uint32_t *mine = col_max[tid >> 5] + kW * cg;  // of the warp's 16 rows
-#pragma unroll
-        for (int k = 0; k < kW; ++k) {
-            uint32_t a = v.u[0][k];
-#pragma unroll
-            for (int i = 1; i < 8; ++i) a = T::larger(a, v.u[i][k]);
-            a = T::larger(a, __shfl_xor_sync(0xffffffffu, a, 16));
-            if (lane < 16) mine[k] = T::magnitudes(a);
-        }
-    }
-    if constexpr (ROWS) {
-        unsigned char *q = p.q + b * p.q_batch + r0 * p.q_ld;
-        float mine = tile_inv;  // of row lane % 8 of the eight
-        if (!p.square) {
-            // the eight rows' maxima over the 16 lanes: each step, a lane gives away half of
-            // its rows and takes the other half's values (8 exchanges instead of 32)
-            uint32_t m[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                m[i] = v.u[i][0];
-#pragma unroll
-                for (int k = 1; k < kW; ++k) m[i] = T::larger(m[i], v.u[i][k]);
-            }
-#pragma unroll
-            for (int d = 4; d > 0; d /= 2)
-#pragma unroll
-                for (int i = 0; i < d; ++i) {
-                    const bool upper = lane & d;
-                    const uint32_t keep = upper ? m[i + d] : m[i], give = upper ? m[i] : m[i + d];
-                    m[i] = T::larger(keep, __shfl_xor_sync(0xffffffffu, give, d));
-                }
-            m[0] = T::magnitudes(T::larger(m[0], __shfl_xor_sync(0xffffffffu, m[0], 8)));
-            // (the two divisions cost more than the values' own arithmetic: one row a lane)
-            const float scale = blocks::scale_of(T::widest(m[0]), mine);
-            if (cg < 8 && r0 + cg < p.R) p.scale[(b * p.R + r0 + cg) * p.ct + tc] = scale;
-        }
-        const bool wide = p.q_vec && cols_in >= 8;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint64_t inv = both(__shfl_sync(0xffffffffu, mine, (lane & 16) + i));
-            float f[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) unpack2(mul2(v.pair(i, k), inv), f[2 * k], f[2 * k + 1]);
-            const uint32_t lo = blocks::pack_e4m3x4(f[0], f[1], f[2], f[3]);
-            const uint32_t hi = blocks::pack_e4m3x4(f[4], f[5], f[6], f[7]);
-            if (i < rows_in) {
-                unsigned char *row = q + i * p.q_ld + c0;
-                if (wide) {
-                    *reinterpret_cast<uint2 *>(row) = make_uint2(lo, hi);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (j < cols_in) row[j] = static_cast<unsigned char>((j < 4 ? lo : hi) >> (8 * (j & 3)));
-                }
-            }
-        }
-    }
-    if constexpr (TRANS) {
-        uint64_t invs[4];  // of the eight columns
-        if (!p.square) {
-            __syncthreads();  // col_max is complete
-            if (tid < kB) {   // a column a thread
-                uint32_t a = 0;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    if constexpr (T::k16)
-                        a = max(a, static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(col_max[w])[tid]));
-                    else
-                        a = max(a, col_max[w][tid]);
-                }
-                float inv;
-                const float scale = blocks::scale_of(T::widest(a), inv);
-                const int64_t col = static_cast<int64_t>(tc) * kB + tid;
-                if (col < p.C) p.scale_t[(b * p.C + col) * p.rt + tr] = scale;
-                col_inv[tid] = inv;
-            }
+                for (int k = 0; k < kW; ++k) a = T::larger(a, v.u[i][k]);
+            a = __reduce_max_sync(0xffffffffu, T::widest(T::magnitudes(a)));
+            if (lane == 0) tile_max[parity][tid >> 5] = a;  // (the other may still be read)
             __syncthreads();
 #pragma unroll
-            for (int k = 0; k < 4; k += 2) {
-                const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(col_inv + 8 * cg + 2 * k);
-                invs[k] = f.x, invs[k + 1] = f.y;
+            for (int w = 0; w < kWarps; ++w) a = max(a, tile_max[parity][w]);
+            const float scale = blocks::scale_of(a, tile_inv);
+            if (tid == 0) {
+                if (ROWS) p.scale[(b * p.rt + tr) * p.ct + tc] = scale;
+                if (TRANS) p.scale_t[(b * p.ct + tc) * p.rt + tr] = scale;
             }
-        } else {
+        } else if constexpr (TRANS) {
+            uint32_t *mine = col_max[tid >> 5] + kW * cg;  // of the warp's 16 rows
 #pragma unroll
-            for (int k = 0; k < 4; ++k) invs[k] = both(tile_inv);
+            for (int k = 0; k < kW; ++k) {
+                uint32_t a = v.u[0][k];
+#pragma unroll
+                for (int i = 1; i < 8; ++i) a = T::larger(a, v.u[i][k]);
+                a = T::larger(a, __shfl_xor_sync(0xffffffffu, a, 16));
+                if (lane < 16) mine[k] = T::magnitudes(a);
+            }
         }
+        if constexpr (ROWS) {
+            unsigned char *q = p.q + b * p.q_batch + r0 * p.q_ld;
+            float mine = tile_inv;  // of row lane % 8 of the eight
+            if (!p.square) {
+                // the eight rows' maxima over the 16 lanes: each step, a lane gives away half of
+                // its rows and takes the other half's values (8 exchanges instead of 32)
+                uint32_t m[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            float e[8], o[8];  // columns 2 k and 2 k + 1
+                for (int i = 0; i < 8; ++i) {
+                    m[i] = v.u[i][0];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) unpack2(mul2(v.pair(i, k), invs[k]), e[i], o[i]);
-            unsigned char *to = tq + (8 * cg + 2 * k) * kB + 8 * (rg ^ cg);
-            *reinterpret_cast<uint2 *>(to) =
-                make_uint2(blocks::pack_e4m3x4(e[0], e[1], e[2], e[3]), blocks::pack_e4m3x4(e[4], e[5], e[6], e[7]));
-            *reinterpret_cast<uint2 *>(to + kB) =
-                make_uint2(blocks::pack_e4m3x4(o[0], o[1], o[2], o[3]), blocks::pack_e4m3x4(o[4], o[5], o[6], o[7]));
+                    for (int k = 1; k < kW; ++k) m[i] = T::larger(m[i], v.u[i][k]);
+                }
+#pragma unroll
+                for (int d = 4; d > 0; d /= 2)
+#pragma unroll
+                    for (int i = 0; i < d; ++i) {
+                        const bool upper = lane & d;
+                        const uint32_t keep = upper ? m[i + d] : m[i], give = upper ? m[i] : m[i + d];
+                        m[i] = T::larger(keep, __shfl_xor_sync(0xffffffffu, give, d));
+                    }
+                m[0] = T::magnitudes(T::larger(m[0], __shfl_xor_sync(0xffffffffu, m[0], 8)));
+                // (the two divisions cost more than the values' own arithmetic: one row a lane)
+                const float scale = blocks::scale_of(T::widest(m[0]), mine);
+                if (cg < 8 && r0 + cg < p.R) p.scale[(b * p.R + r0 + cg) * p.ct + tc] = scale;
+            }
+            const bool wide = p.q_vec && cols_in >= 8;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint64_t inv = both(__shfl_sync(0xffffffffu, mine, (lane & 16) + i));
+                float f[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) unpack2(mul2(v.pair(i, k), inv), f[2 * k], f[2 * k + 1]);
+                const uint32_t lo = blocks::pack_e4m3x4(f[0], f[1], f[2], f[3]);
+                const uint32_t hi = blocks::pack_e4m3x4(f[4], f[5], f[6], f[7]);
+                if (i < rows_in) {
+                    unsigned char *row = q + i * p.q_ld + c0;
+                    if (wide) {
+                        *reinterpret_cast<uint2 *>(row) = make_uint2(lo, hi);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (j < cols_in) row[j] = static_cast<unsigned char>((j < 4 ? lo : hi) >> (8 * (j & 3)));
+                    }
+                }
+            }
         }
-        __syncthreads();
-        // 16 rows a thread, eight threads a column, every 32nd column
-        const int c = tid >> 3, u = tid & 7;
-        const int64_t r = static_cast<int64_t>(tr) * kB + 16 * u, col = static_cast<int64_t>(tc) * kB + c;
-        const int left = static_cast<int>(min(int64_t{16}, p.R - r));
-        if (left <= 0) return;
-        unsigned char *to = p.qt + b * p.qt_batch + col * p.qt_ld + r;
-        const bool wide = p.qt_vec && left == 16;
+        if constexpr (TRANS) {
+            uint64_t invs[4];  // of the eight columns
+            if (!p.square) {
+                __syncthreads();  // col_max is complete
+                if (tid < kB) {   // a column a thread
+                    uint32_t a = 0;
 #pragma unroll
-        for (int i = 0; i < kB * kB / 16 / kThreads; ++i) {
-            if (col + 32 * i >= p.C) break;
-            const unsigned char *from = tq + (c + 32 * i) * kB;
-            const int swizzle = (c >> 3) + 4 * i;
-            const uint2 lo = *reinterpret_cast<const uint2 *>(from + 8 * ((2 * u) ^ swizzle));
-            const uint2 hi = *reinterpret_cast<const uint2 *>(from + 8 * ((2 * u + 1) ^ swizzle));
-            if (wide) {
-                *reinterpret_cast<uint4 *>(to) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                    for (int w = 0; w < kWarps; ++w) {
+                        if constexpr (T::k16)
+                            a = max(a, static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(col_max[w])[tid]));
+                        else
+                            a = max(a, col_max[w][tid]);
+                    }
+                    float inv;
+                    const float scale = blocks::scale_of(T::widest(a), inv);
+                    const int64_t col = static_cast<int64_t>(tc) * kB + tid;
+                    if (col < p.C) p.scale_t[(b * p.C + col) * p.rt + tr] = scale;
+                    col_inv[tid] = inv;
+                }
+                __syncthreads();
+#pragma unroll
+                for (int k = 0; k < 4; k += 2) {
+                    const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(col_inv + 8 * cg + 2 * k);
+                    invs[k] = f.x, invs[k + 1] = f.y;
+                }
             } else {
-                const uint32_t w[4] = {lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    if (k < left) to[k] = static_cast<unsigned char>(w[k / 4] >> (8 * (k & 3)));
+                for (int k = 0; k < 4; ++k) invs[k] = both(tile_inv);
             }
-            to += 32 * p.qt_ld;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float e[8], o[8];  // columns 2 k and 2 k + 1
+#pragma unroll
+                for (int i = 0; i < 8; ++i) unpack2(mul2(v.pair(i, k), invs[k]), e[i], o[i]);
+                unsigned char *to = tq + (8 * cg + 2 * k) * kB + 8 * (rg ^ cg);
+                *reinterpret_cast<uint2 *>(to) =
+                    make_uint2(blocks::pack_e4m3x4(e[0], e[1], e[2], e[3]), blocks::pack_e4m3x4(e[4], e[5], e[6], e[7]));
+                *reinterpret_cast<uint2 *>(to + kB) =
+                    make_uint2(blocks::pack_e4m3x4(o[0], o[1], o[2], o[3]), blocks::pack_e4m3x4(o[4], o[5], o[6], o[7]));
+            }
+            __syncthreads();
+            // 16 rows a thread, eight threads a column, every 32nd column
+            const int c = tid >> 3, u = tid & 7;
+            const int64_t r = static_cast<int64_t>(tr) * kB + 16 * u, col = static_cast<int64_t>(tc) * kB + c;
+            const int left = static_cast<int>(min(int64_t{16}, p.R - r));
+            if (left <= 0) continue;
+            unsigned char *to = p.qt + b * p.qt_batch + col * p.qt_ld + r;
+            const bool wide = p.qt_vec && left == 16;
+#pragma unroll
+            for (int i = 0; i < kB * kB / 16 / kThreads; ++i) {
+                if (col + 32 * i >= p.C) break;
+                const unsigned char *from = tq + (c + 32 * i) * kB;
+                const int swizzle = (c >> 3) + 4 * i;
+                const uint2 lo = *reinterpret_cast<const uint2 *>(from + 8 * ((2 * u) ^ swizzle));
+                const uint2 hi = *reinterpret_cast<const uint2 *>(from + 8 * ((2 * u + 1) ^ swizzle));
+                if (wide) {
+                    *reinterpret_cast<uint4 *>(to) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                } else {
+                    const uint32_t w[4] = {lo.x, lo.y, hi.x, hi.y};
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        if (k < left) to[k] = static_cast<unsigned char>(w[k / 4] >> (8 * (k & 3)));
+                }
+                to += 32 * p.qt_ld;
+            }
         }
     }
 }
@@ -332,6 +382,23 @@ Kernel kernel_of(int dt, bool vec, bool rows, bool trans) {
         default:
             return vec ? kernel_of<VLMCE_BF16, true>(rows, trans) : kernel_of<VLMCE_BF16, false>(rows, trans);
     }
+}
+
+// The kernels that stage tiles, their shared memory, once per device.
+cudaError_t opt_in(int device) {
+    static std::mutex mu;
+    static bool done[64] = {};
+    std::lock_guard<std::mutex> lock(mu);
+    cudaError_t e = cudaSuccess;
+    if (!done[device]) {
+        for (const int dt : {VLMCE_BF16, VLMCE_F16})
+            for (const int out : {1, 2, 3})
+                if (e == cudaSuccess)
+                    e = cudaFuncSetAttribute(kernel_of(dt, true, out & 1, out & 2),
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kStage);
+        done[device] = e == cudaSuccess;
+    }
+    return e;
 }
 
 }  // namespace
@@ -397,6 +464,7 @@ extern "C" vlmce_status quantize_blocks(const void *x, int32_t dtype, int64_t ba
     p.qt_batch = C * qt_stride;
     p.R = R;
     p.C = C;
+    p.batch = static_cast<int>(batch);
     p.rt = static_cast<int>(rt);
     p.ct = static_cast<int>(ct);
     p.square = square != 0;
@@ -409,13 +477,21 @@ extern "C" vlmce_status quantize_blocks(const void *x, int32_t dtype, int64_t ba
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(batch * rt * ct), 1, 1);
+    const Kernel kernel = kernel_of(dtype, vec, q != nullptr, qt != nullptr);
+    const int64_t tiles = batch * rt * ct;
+    const bool staged = vec && dtype != VLMCE_F32;
+    const int64_t at_once = std::min<int64_t>(tiles, kCtas<VLMCE_BF16> * dev.sm_count);
+    const int64_t ctas = !staged ? tiles : square ? std::max(at_once, (tiles + kSquareRun - 1) / kSquareRun) : at_once;
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+    cfg.dynamicSmemBytes = staged ? kStage : 0;
+    if (staged) {
+        const cudaError_t e = opt_in(dev.device);
+        if (e != cudaSuccess) return launch_status(e, "quantize_blocks");
+    }
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return launch_status(
-        cudaLaunchKernelEx(&cfg, kernel_of(dtype, vec, q != nullptr, qt != nullptr),
-                           static_cast<const Params>(p)),
-        "quantize_blocks");
+        cudaLaunchKernelEx(&cfg, kernel, static_cast<const Params>(p)), "quantize_blocks");
 }
