@@ -6,20 +6,27 @@
 //
 // A block's sums are in one of two TMEM buffers while the next block's form in the other;
 // eight epilogue warps, each with 32 rows x 128 columns of running sums in registers (128 a
-// thread; the control warps give theirs up), empty it, 16 columns a load.  A's factor is a
-// thread's own.  B's is one for the 128 columns (a weight's blocks of 128 x 128: acc += (a
-// b) d), or one for each column (B_ROWS), read from shared memory: twice the arithmetic,
-// and as many bytes through the load unit as come from TMEM.
+// thread; the control warps give theirs up), empty it.  A's factor is a thread's own.  B's is
+// one for the 128 columns (a weight's blocks of 128 x 128: acc += (a b) d, a row a lane, 16
+// columns a load), or one for each column (B_ROWS: twice the arithmetic).  For those the sums
+// come 16 rows x 32 columns a load, two columns of a group of eight in each lane, so that a
+// lane has 32 of the columns' factors and keeps them in registers for all its rows (each of
+// them read from shared memory by all lanes, 428 us instead of 349 at the size below).
 //
-// What bounds it: the epilogue warps' own instructions, about 920 clocks a block, where the
-// products take 512 and their hand-over 400 (two buffers: (512 + 400 + the time a buffer is
-// being read) / 2).  8192 x 8192 x 4096 242 us = 2.27 PFLOP/s (a scale for each row, without
-// this epilogue: 174 us), with a factor for each column 428 us.  Tried: loads of 32 columns
-// (255 us), a load ahead of its sums (273), single instead of packed multiply-adds (254),
-// four buffers of 128 columns (330), 256 x 192 tiles on twelve warps without a change of
-// registers (292).  One commit per block: "the stage is free" and "the block's sums are
-// there" are the same event, and both CTAs' epilogue warps wait on the stage's barrier, as
-// the copies do (a commit for each 267 us).
+// What bounds it: the epilogue warps' own instructions, about 920 clocks a block (B_ROWS
+// 1310), where the products take 512 and their hand-over 400 (two buffers: (512 + 400 + the
+// time a buffer is being read) / 2).  8192 x 8192 x 4096 237 us = 2.31 PFLOP/s (a scale for
+// each row, without this epilogue: 174 us), with a factor for each column 349 us into fp32.
+// Tried: loads of 32 columns (255 us) and of 8 (247), a load ahead of its sums (273), two
+// blocks an iteration (357), single instead of packed multiply-adds (254), four buffers of 128
+// columns (330), 256 x 192 tiles on twelve warps without a change of registers (292), other
+// splits of the registers (268).  One commit per block: "the stage is free" and "the block's
+// sums are there" are the same event, and both CTAs' epilogue warps wait on the stage's
+// barrier, as the copies do (a commit for each 267 us).
+//
+// A tile of dweight is stored in 32 x 32 pieces from two buffers a warp; it costs the
+// epilogue about 2900 clocks (4096 x 4096, 1024 rows: 36.0 us, without the stores 29.8).  Three
+// buffers, or several pieces handed over at once, were not faster (36.8, 37.3).
 //
 // The tiles are dealt out in order; a group's tiles go down 8 tiles of rows before they go
 // across, so those in flight share operands.
@@ -276,7 +283,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll 1
             for (int c = 0; c < t.chunks; ++c, ++it) {
                 advance(c);
-                // (fetching it a block ahead costs: 242 -> 267 us)
+                // (fetching it a block ahead costs: 237 -> 267 us)
                 float af[B_ROWS ? 4 : 1];
 #pragma unroll
                 for (int i = 0; i < (B_ROWS ? 4 : 1); ++i)

@@ -11,7 +11,10 @@
 // Everything but the sort goes token by token: a token's row is read (and quantised)
 // once, however many experts it has, and no inverse of `position` is needed.  Those
 // kernels are bound by memory; what keeps loads in flight is a token's k rows, which a
-// thread asks for together.
+// thread asks for together.  8192 tokens, k = 4, H = 4096 bf16: gather to e4m3 31.8 us (206
+// MB, 6.5 TB/s), the gradient of combine 90.3 us (604 MB, 6.7 TB/s).  Few tokens are bound by
+// the launch and two trips to memory one after the other (a position, then its row): combine
+// of 16 tokens, k = 8, H = 4096 2.3 us, sort of 64 x 8 pairs 3.8 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>
