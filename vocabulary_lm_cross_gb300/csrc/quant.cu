@@ -111,7 +111,38 @@ struct Tile {
             u[i][4 * k] = q.x, u[i][4 * k + 1] = q.y, u[i][4 * k + 2] = q.z, u[i][4 * k + 3] = q.w;
         }
     }
-    // At any alignment: the 16-byte units that hold them, moved into place, where those lie
+    // Row i out of the 16-byte units that hold it, of which it starts `off` bytes in.
+    __device__ __forceinline__ void place(int i, uint32_t (&w)[kWords + 4], uint32_t off) {
+#pragma unroll
+        for (int k = 0; k < kWords + 2; ++k) w[k] = off & 8 ? w[k + 2] : w[k];
+#pragma unroll
+        for (int k = 0; k < kWords + 1; ++k) w[k] = off & 4 ? w[k + 1] : w[k];
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) u[i][k] = k16 ? __funnelshift_r(w[k], w[k + 1], (off & 2) * 8) : w[k];
+    }
+    // At any alignment, eight rows `ld` bytes apart whose units lie within x's memory: four
+    // rows' loads at a time (in a branch for each row they wait for one another: 7042 x 6722
+    // bf16 along rows 54 us).
+    __device__ __forceinline__ void load_units(const unsigned char *from, int64_t ld) {
+#pragma unroll
+        for (int h = 0; h < 8; h += 4) {
+            uint32_t w[4][kWords + 4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uintptr_t unit = reinterpret_cast<uintptr_t>(from + (h + i) * ld) & ~uintptr_t{15};
+#pragma unroll
+                for (int k = 0; k <= kWords / 4; ++k) {
+                    const uint4 q = *reinterpret_cast<const uint4 *>(unit + 16 * k);
+                    w[i][4 * k] = q.x, w[i][4 * k + 1] = q.y, w[i][4 * k + 2] = q.z, w[i][4 * k + 3] = q.w;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                place(h + i, w[i], static_cast<uint32_t>(reinterpret_cast<uintptr_t>(from + (h + i) * ld) & 15));
+        }
+    }
+    static constexpr int kUnitBytes = 4 * kWords + 16;  // of a row's units
+    // At any alignment, the first n values (n may be 0, or less): the units, where those lie
     // between `first` and `last`; else one by one.
     __device__ __forceinline__ void load(int i, const unsigned char *from, int64_t n, uintptr_t first,
                                          uintptr_t last) {
@@ -127,12 +158,7 @@ struct Tile {
                 if (16u * k < off + take * kElt) q = *reinterpret_cast<const uint4 *>(unit + 16 * k);
                 w[4 * k] = q.x, w[4 * k + 1] = q.y, w[4 * k + 2] = q.z, w[4 * k + 3] = q.w;
             }
-#pragma unroll
-            for (int k = 0; k < kWords + 2; ++k) w[k] = off & 8 ? w[k + 2] : w[k];
-#pragma unroll
-            for (int k = 0; k < kWords + 1; ++k) w[k] = off & 4 ? w[k + 1] : w[k];
-#pragma unroll
-            for (int k = 0; k < kWords; ++k) u[i][k] = k16 ? __funnelshift_r(w[k], w[k + 1], (off & 2) * 8) : w[k];
+            place(i, w, off);
             if (take < 8) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
@@ -216,12 +242,18 @@ __global__ void __launch_bounds__(kThreads, kCtas<DT>) quant_kernel(const Params
             if (tile + step < tiles) fetch(tile + step);
         } else {
             const unsigned char *x = p.x + b * p.x_batch + r0 * p.x_ld + c0 * blocks::elt_bytes<DT>;
+            const uintptr_t end = (reinterpret_cast<uintptr_t>(x + 7 * p.x_ld) & ~uintptr_t{15}) + T::kUnitBytes;
+            if (!ALIGNED && rows_in >= 8 && cols_in >= 8 &&
+                (reinterpret_cast<uintptr_t>(x) & ~uintptr_t{15}) >= p.first && end <= p.last) {
+                v.load_units(x, p.x_ld);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if constexpr (ALIGNED)
-                    v.load16(i, x + i * p.x_ld, i < rows_in && cols_in > 0);
-                else
-                    v.load(i, x + i * p.x_ld, i < rows_in ? cols_in : 0, p.first, p.last);
+                for (int i = 0; i < 8; ++i)
+                    if constexpr (ALIGNED)
+                        v.load16(i, x + i * p.x_ld, i < rows_in && cols_in > 0);
+                    else
+                        v.load(i, x + i * p.x_ld, i < rows_in ? cols_in : 0, p.first, p.last);
+            }
         }
         float tile_inv = 1.f;
         if (p.square) {
