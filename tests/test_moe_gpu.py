@@ -79,7 +79,8 @@ def test_sort_of_nothing_of_nobodys_and_of_strided_ids():
 
 SHAPES = [(1, 1, 1, 1, 1), (1, 8, 8, 4096, 1), (5, 3, 4, 100, 16), (37, 2, 6, 1001, 128), (64, 8, 16, 264, 1),
           (130, 12, 12, 2056, 16), (300, 4, 64, 640, 128),
-          (9, 3, 5, 4112, 16), (70, 2, 3, 48, 1), (33, 2, 4, 8200, 1)]
+          (9, 3, 5, 4112, 16), (70, 2, 3, 48, 1), (33, 2, 4, 8200, 1), (20, 8, 16, 100, 1), (20, 6, 16, 1001, 16),
+          (11, 5, 9, 30, 1)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
@@ -156,6 +157,31 @@ def test_combine_and_its_gradients(T, k, E, H, align, dtype, wide):
     assert rows.dweights is None
     used = torch.from_numpy(np.unique(pos[pos >= 0])).cuda()
     assert torch.equal(rows.drows[used], r.drows[used])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("H", [16, 30, 100, 264, 1001])
+def test_rows_at_any_alignment(H, dtype):
+    """x at the end and the start of its memory, 8-bit rows anywhere: as from and to aligned
+    rows."""
+    T, k, E = 23, 3, 5
+    order = v.moe_sort(routing(H, T, k, E).cuda(), E, align=4)
+    R = int(order.offsets[-1])
+    flat = randn(gen(H), (T * H + 3,), DT[dtype])
+    aligned = flat[3:].view(T, H).clone()
+    want8, want = v.moe_gather(aligned, order, fp8=True), v.moe_gather(aligned, order).rows
+    for x in (flat[3:].view(T, H), torch.cat([flat[3:], flat[:1]])[:-1].view(T, H)):
+        got = v.moe_gather(x, order, fp8=True)
+        assert torch.equal(got.rows[:R].view(torch.uint8), want8.rows[:R].view(torch.uint8))
+        assert torch.equal(got.scale[:R], want8.scale[:R])
+        assert torch.equal(v.moe_gather(x, order).rows[:R], want[:R])
+        for pad, skip in ((1, 0), (5, 0), (16, 3)):
+            store = torch.full((order.rows, H + pad), 77, dtype=torch.uint8, device="cuda")
+            out = store[:, skip:skip + H].view(torch.float8_e4m3fn)
+            got = v.moe_gather(x, order, fp8=True, out=out)
+            assert torch.equal(out[:R].view(torch.uint8), want8.rows[:R].view(torch.uint8))
+            assert torch.equal(got.scale[:R], want8.scale[:R])
+            assert (store[:, :skip] == 77).all() and (store[:, skip + H:] == 77).all() and (store[R:] == 77).all()
 
 
 def test_combine_in_place_of_the_residual_and_without_weights():

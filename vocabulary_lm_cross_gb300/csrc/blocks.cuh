@@ -46,10 +46,6 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float
         : "f"(a), "f"(b), "f"(c), "f"(d));
     return r;
 }
-__device__ __forceinline__ uint8_t to_e4m3(float a) {
-    return __nv_cvt_float_to_fp8(a, __NV_SATFINITE, __NV_E4M3);
-}
-
 template <int DT>
 constexpr int elt_bytes = DT == VLMCE_F32 ? 4 : 2;
 
@@ -60,122 +56,86 @@ __device__ __forceinline__ float load1(const unsigned char *row, int64_t c) {
     else
         return act::from16(reinterpret_cast<const uint16_t *>(row)[c], DT == VLMCE_F16);
 }
-template <int DT>
-__device__ __forceinline__ void store1(unsigned char *row, int64_t c, float v) {
-    if constexpr (DT == VLMCE_F32)
-        reinterpret_cast<float *>(row)[c] = v;
-    else
-        reinterpret_cast<uint16_t *>(row)[c] = act::to16(v, DT == VLMCE_F16);
-}
-// Eight consecutive values, 16-byte aligned.
-template <int DT>
-__device__ __forceinline__ void load8(const unsigned char *row, int64_t c, float (&v)[8]) {
-    if constexpr (DT == VLMCE_F32) {
-        const float4 *p = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(row) + c);
-        const float4 a = p[0], b = p[1];
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-        const uint4 u =
-            *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(row) + c);
-        act::unpack16x2(u.x, v[0], v[1], DT == VLMCE_F16);
-        act::unpack16x2(u.y, v[2], v[3], DT == VLMCE_F16);
-        act::unpack16x2(u.z, v[4], v[5], DT == VLMCE_F16);
-        act::unpack16x2(u.w, v[6], v[7], DT == VLMCE_F16);
-    }
-}
-template <int DT>
-__device__ __forceinline__ void store8(unsigned char *row, int64_t c, const float (&v)[8]) {
-    if constexpr (DT == VLMCE_F32) {
-        float4 *p = reinterpret_cast<float4 *>(reinterpret_cast<float *>(row) + c);
-        p[0] = make_float4(v[0], v[1], v[2], v[3]);
-        p[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-        constexpr bool f16 = DT == VLMCE_F16;
-        *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(row) + c) =
-            make_uint4(act::pack16x2(v[0], v[1], f16), act::pack16x2(v[2], v[3], f16),
-                       act::pack16x2(v[4], v[5], f16), act::pack16x2(v[6], v[7], f16));
+// W words that start `off` (of 16, a multiple of their elements' size) bytes into these.
+template <int W, bool HALVES>
+__device__ __forceinline__ void move_into_place(uint32_t (&w)[W + 4], uint32_t off) {
+#pragma unroll
+    for (int k = 0; k < W + 2; ++k) w[k] = off & 8 ? w[k + 2] : w[k];
+#pragma unroll
+    for (int k = 0; k < W + 1; ++k) w[k] = off & 4 ? w[k + 1] : w[k];
+    if constexpr (HALVES) {
+#pragma unroll
+        for (int k = 0; k < W; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], (off & 2) * 8);
     }
 }
 
-// A thread's columns of a row, of the 256 (VEC) or 128 that its warp takes from `base`:
-// eight in a row, in 16-byte accesses; or four that are 32 apart, at any alignment (a
-// warp's accesses cover consecutive elements).
-template <bool VEC>
+// A thread's eight columns of a row, of the 256 that its warp takes from `base`, in accesses
+// of U bytes (16, 4, or 2 of 16-bit values) that divide the row's length and addresses: a
+// warp's access covers 32 U consecutive bytes.
+template <int DT, int U>
 struct Cols {
-    static constexpr int N = VEC ? 8 : 4;
-    static constexpr int kWarp = 32 * N;
+    static constexpr int kElt = elt_bytes<DT>, P = U / kElt;  // columns of an access
+    static constexpr int N = 8, kWarp = 32 * N;
+    static constexpr bool kF16 = DT == VLMCE_F16;
     int64_t c;
-    __device__ __forceinline__ Cols(int64_t base, int lane) : c(base + (VEC ? 8 * lane : lane)) {}
-    __device__ __forceinline__ bool in(int i, int64_t H) const { return VEC ? c < H : c + 32 * i < H; }
+    __device__ __forceinline__ Cols(int64_t base, int lane) : c(base + P * lane) {}
+    __device__ __forceinline__ bool in(int i, int64_t H) const { return c + i / P * (32 * P) < H; }
+    __device__ __forceinline__ int64_t at(int i) const { return (c + i / P * (32 * P)) * kElt; }
 
     // The values as they are in memory, to have many on their way in few registers.
-    template <int DT>
     struct Raw {
-        static constexpr int kWords = VEC ? 2 * elt_bytes<DT> : 4;
-        uint32_t u[kWords];
+        uint32_t u[U > 2 ? N * kElt / 4 : N];
     };
-    template <int DT>
-    __device__ __forceinline__ void fetch(const unsigned char *row, int64_t H, Raw<DT> &r) const {
-        if constexpr (VEC) {
-            if (c < H) {
-                const uint4 *p = reinterpret_cast<const uint4 *>(row + c * elt_bytes<DT>);
+    __device__ __forceinline__ void fetch(const unsigned char *row, int64_t H, Raw &r) const {
 #pragma unroll
-                for (int i = 0; i < elt_bytes<DT> / 2; ++i) {
-                    const uint4 q = p[i];
-                    r.u[4 * i] = q.x, r.u[4 * i + 1] = q.y, r.u[4 * i + 2] = q.z, r.u[4 * i + 3] = q.w;
+        for (int i = 0; i < N; i += P) {
+            if constexpr (U == 16) {
+                uint32_t *to = r.u + i * kElt / 4;
+                if (in(i, H)) {
+                    const uint4 q = *reinterpret_cast<const uint4 *>(row + at(i));
+                    to[0] = q.x, to[1] = q.y, to[2] = q.z, to[3] = q.w;
+                } else {
+                    to[0] = to[1] = to[2] = to[3] = 0;
                 }
+            } else if constexpr (U == 4) {
+                r.u[i * kElt / 4] = in(i, H) ? *reinterpret_cast<const uint32_t *>(row + at(i)) : 0;
             } else {
-#pragma unroll
-                for (int i = 0; i < Raw<DT>::kWords; ++i) r.u[i] = 0;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (DT == VLMCE_F32)
-                    r.u[i] = in(i, H) ? reinterpret_cast<const uint32_t *>(row)[c + 32 * i] : 0;
-                else
-                    r.u[i] = in(i, H) ? reinterpret_cast<const uint16_t *>(row)[c + 32 * i] : 0;
+                r.u[i] = in(i, H) ? *reinterpret_cast<const uint16_t *>(row + at(i)) : 0;
             }
         }
     }
     // Value i of them.
-    template <int DT>
-    static __device__ __forceinline__ float value(const Raw<DT> &r, int i) {
+    static __device__ __forceinline__ float value(const Raw &r, int i) {
         if constexpr (DT == VLMCE_F32) {
             return __uint_as_float(r.u[i]);
-        } else if constexpr (VEC) {
+        } else if constexpr (U > 2) {
             float a, b;
-            act::unpack16x2(r.u[i / 2], a, b, DT == VLMCE_F16);
+            act::unpack16x2(r.u[i / 2], a, b, kF16);
             return i & 1 ? b : a;
         } else {
-            return act::from16(static_cast<uint16_t>(r.u[i]), DT == VLMCE_F16);
+            return act::from16(static_cast<uint16_t>(r.u[i]), kF16);
         }
     }
-
-    // values outside the row are 0
-    template <int DT>
-    __device__ __forceinline__ void load(const unsigned char *row, int64_t H, float (&v)[N]) const {
-        if constexpr (VEC) {
-            if (c < H) {
-                load8<DT>(row, c, v);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = 0.f;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = in(i, H) ? load1<DT>(row, c + 32 * i) : 0.f;
-        }
-    }
-    template <int DT>
     __device__ __forceinline__ void store(unsigned char *row, int64_t H, const float (&v)[N]) const {
-        if constexpr (VEC) {
-            if (c < H) store8<DT>(row, c, v);
-        } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (in(i, H)) store1<DT>(row, c + 32 * i, v[i]);
+        for (int i = 0; i < N; i += P) {
+            if (!in(i, H)) continue;
+            uint32_t w[U > 4 ? U / 4 : 1];
+            if constexpr (DT == VLMCE_F32) {
+#pragma unroll
+                for (int k = 0; k < P; ++k) w[k] = __float_as_uint(v[i + k]);
+            } else if constexpr (U > 2) {
+#pragma unroll
+                for (int k = 0; k < P; k += 2) w[k / 2] = act::pack16x2(v[i + k], v[i + k + 1], kF16);
+            } else {
+                w[0] = act::to16(v[i], kF16);
+            }
+            if constexpr (U == 16)
+                *reinterpret_cast<uint4 *>(row + at(i)) = make_uint4(w[0], w[1], w[2], w[3]);
+            else if constexpr (U == 4)
+                *reinterpret_cast<uint32_t *>(row + at(i)) = w[0];
+            else
+                *reinterpret_cast<uint16_t *>(row + at(i)) = static_cast<uint16_t>(w[0]);
         }
     }
 };

@@ -19,7 +19,9 @@
 
 #include <algorithm>
 #include <climits>
+#include <initializer_list>
 #include <mutex>
+#include <type_traits>
 
 #include "blocks.cuh"
 #include "host_util.h"
@@ -216,8 +218,9 @@ struct RowParams {
     const int *position, *offsets, *counts;
     const void *w;
     int64_t x_ld, in_ld, out_ld, res_ld, w_ld;  // bytes; w_ld, scale_ld: elements
-    int64_t scale_ld, T, R, H;
+    int64_t scale_ld, T, R, H, row_bytes;  // row_bytes: of out
     int k, E, w_f32;
+    uintptr_t first, last;         // x's memory
 };
 
 // Blocks of `x` index T .. T + E - 1 clear the rows between an expert's last and the next
@@ -243,67 +246,47 @@ __device__ __forceinline__ void clear_rows(const RowParams &p, int e, int64_t ro
     }
 }
 
-template <int DT, bool VEC, bool FP8>
-__global__ void __launch_bounds__(256) gather_kernel(const RowParams p) {
-    using C = blocks::Cols<VEC>;
+// Rows as they are, in units of U bytes; kCopyUnits<U> a thread, 32 apart (twice as many: 512
+// rows of 4096 bf16 5.3 us instead of 4.4, 8192 rows 51.1 and 50.2).
+template <int U>
+constexpr int kCopyUnits = U == 16 ? 2 : 4;
+template <int U>
+__global__ void __launch_bounds__(256) gather_copy_kernel(const RowParams p) {
+    using Unit = std::conditional_t<U == 16, uint4, std::conditional_t<U == 4, uint32_t, uint16_t>>;
+    constexpr int N = kCopyUnits<U>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
     const int64_t t = blockIdx.x;
     if (t >= p.T) {
-        float inv;
-        const float zero = blocks::scale_of(0, inv);
-        clear_rows(p, static_cast<int>(t - p.T), p.H * (FP8 ? 1 : blocks::elt_bytes<DT>), zero);
+        clear_rows(p, static_cast<int>(t - p.T), p.row_bytes, 0.f);
         return;
     }
-    const int64_t base =
-        (static_cast<int64_t>(blockIdx.y) * (blockDim.x >> 5) + warp) * C::kWarp;
-    if (base >= p.H) return;
-    const C cols(base, lane);
+    const int first = (static_cast<int>(blockIdx.y) * (blockDim.x >> 5) + warp) * (32 * N) + lane;
+    const int left = static_cast<int>(p.row_bytes / U) - first;  // units of the row from there
+    if (left <= 0) return;
     const int *pos = p.position + t * p.k;
-    float v[C::N];
-    cols.template load<DT>(p.x + t * p.x_ld, p.H, v);
-    float scale = 0.f;
-    uint32_t q[2] = {};
-    if constexpr (FP8) {
-        uint32_t a = 0;
+    const Unit *from = reinterpret_cast<const Unit *>(p.x + t * p.x_ld) + first;
+    Unit v[N];
 #pragma unroll
-        for (int i = 0; i < C::N; ++i) a = max(a, blocks::magnitude(v[i]));
-        // a block is 16 lanes of eight columns, or a warp of four
-#pragma unroll
-        for (int d = VEC ? 8 : 16; d > 0; d /= 2) a = max(a, __shfl_xor_sync(0xffffffffu, a, d));
-        float inv;
-        scale = blocks::scale_of(a, inv);
-#pragma unroll
-        for (int i = 0; i < C::N; ++i) v[i] *= inv;
-#pragma unroll
-        for (int i = 0; i < C::N; i += 4)
-            q[i / 4] = blocks::pack_e4m3x4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-    }
+    for (int i = 0; i < N; ++i)
+        if (32 * i < left) v[i] = from[32 * i];
     for (int j = 0; j < p.k; ++j) {
-        const int64_t r = pos[j];
+        const int r = pos[j];
         if (r < 0 || r >= p.R) continue;
-        unsigned char *row = p.out + r * p.out_ld;
-        if constexpr (FP8) {
-            if constexpr (VEC) {
-                if (cols.c < p.H) *reinterpret_cast<uint2 *>(row + cols.c) = make_uint2(q[0], q[1]);
-            } else {
+        Unit *to = reinterpret_cast<Unit *>(p.out + r * p.out_ld) + first;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (cols.in(i, p.H)) row[cols.c + 32 * i] = static_cast<unsigned char>(q[0] >> (8 * i));
-            }
-            if ((VEC ? lane & 15 : lane) == 0 && cols.c < p.H)
-                p.scale[r * p.scale_ld + cols.c / blocks::kBlock] = scale;
-        } else {
-            cols.template store<DT>(row, p.H, v);
-        }
+        for (int i = 0; i < N; ++i)
+            if (32 * i < left) to[32 * i] = v[i];
     }
 }
 
-// In e4m3 with 16 columns a thread, for rows of whole 16-byte units: bound by instructions
+// In e4m3 with 16 columns a thread, to rows of whole 16-byte units: bound by instructions
 // with eight (8192 tokens to 4 rows of 4096 each 40 us, 77 % of the issue slots), of which the
 // two divisions of a block and a row's address are a thread's, however many columns it has.
-template <int DT>
+// ALIGNED: x's rows are whole units, too, and 16 divides H.  Else the units that hold a
+// thread's columns are moved into place (8192 tokens to 4 rows of 4097 42.6 us, by elements 83).
+template <int DT, bool ALIGNED>
 __global__ void __launch_bounds__(256) gather_wide_kernel(const RowParams p) {
     constexpr bool k16 = DT != VLMCE_F32;
     constexpr int kWords = k16 ? 8 : 16;
@@ -314,17 +297,40 @@ __global__ void __launch_bounds__(256) gather_wide_kernel(const RowParams p) {
     if (t >= p.T) {
         float inv;
         const float zero = blocks::scale_of(0, inv);
-        clear_rows(p, static_cast<int>(t - p.T), p.H, zero);
+        clear_rows(p, static_cast<int>(t - p.T), p.row_bytes, zero);
         return;
     }
     const int64_t c = (static_cast<int64_t>(blockIdx.y) * (blockDim.x >> 5) + warp) * 512 + 16 * lane;
+    const int n = static_cast<int>(min(int64_t{16}, p.H - c));  // columns of the 16 there are
     const int *pos = p.position + t * p.k;
-    uint32_t u[kWords];
-    const uint4 *from = reinterpret_cast<const uint4 *>(p.x + t * p.x_ld + c * blocks::elt_bytes<DT>);
+    const unsigned char *from = p.x + t * p.x_ld + c * blocks::elt_bytes<DT>;
+    uint32_t u[kWords + 4];
+    if constexpr (ALIGNED) {
 #pragma unroll
-    for (int i = 0; i < kWords / 4; ++i) {
-        const uint4 q = c < p.H ? from[i] : make_uint4(0, 0, 0, 0);
-        u[4 * i] = q.x, u[4 * i + 1] = q.y, u[4 * i + 2] = q.z, u[4 * i + 3] = q.w;
+        for (int i = 0; i < kWords; i += 4) {
+            const uint4 q = n > 0 ? *reinterpret_cast<const uint4 *>(from + 4 * i) : make_uint4(0, 0, 0, 0);
+            u[i] = q.x, u[i + 1] = q.y, u[i + 2] = q.z, u[i + 3] = q.w;
+        }
+    } else {
+        const uintptr_t unit = reinterpret_cast<uintptr_t>(from) & ~uintptr_t{15};
+        if (n == 16 && unit >= p.first && unit + 4 * kWords + 16 <= p.last) {
+#pragma unroll
+            for (int i = 0; i < kWords + 4; i += 4) {
+                const uint4 q = *reinterpret_cast<const uint4 *>(unit + 4 * i);
+                u[i] = q.x, u[i + 1] = q.y, u[i + 2] = q.z, u[i + 3] = q.w;
+            }
+            blocks::move_into_place<kWords, k16>(u, static_cast<uint32_t>(reinterpret_cast<uintptr_t>(from) & 15));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                if constexpr (k16) {
+                    const uint32_t e = i < n ? reinterpret_cast<const uint16_t *>(from)[i] : 0;
+                    u[i / 2] = i & 1 ? u[i / 2] | e << 16 : e;
+                } else {
+                    u[i] = i < n ? reinterpret_cast<const uint32_t *>(from)[i] : 0;
+                }
+            }
+        }
     }
     uint32_t a = 0;  // magnitudes, 16-bit ones two at a time
 #pragma unroll
@@ -351,12 +357,57 @@ __global__ void __launch_bounds__(256) gather_wide_kernel(const RowParams p) {
         }
         q[i] = blocks::pack_e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
     }
-    if (c >= p.H) return;
+    if (n <= 0) return;
     for (int j = 0; j < p.k; ++j) {
         const int r = pos[j];
         if (r < 0 || r >= p.R) continue;
-        *reinterpret_cast<uint4 *>(p.out + r * p.out_ld + c) = make_uint4(q[0], q[1], q[2], q[3]);
+        unsigned char *to = p.out + r * p.out_ld + c;
+        if (ALIGNED || n == 16) {
+            *reinterpret_cast<uint4 *>(to) = make_uint4(q[0], q[1], q[2], q[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (i < n) to[i] = static_cast<unsigned char>(q[i / 4] >> (8 * (i & 3)));
+        }
         if ((lane & 7) == 0) p.scale[r * p.scale_ld + c / blocks::kBlock] = scale;
+    }
+}
+
+// In e4m3 to rows at any alignment: a warp a block, a lane four columns 32 apart.
+template <int DT>
+__global__ void __launch_bounds__(256) gather_bytes_kernel(const RowParams p) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    const int64_t t = blockIdx.x;
+    if (t >= p.T) {
+        float inv;
+        const float zero = blocks::scale_of(0, inv);
+        clear_rows(p, static_cast<int>(t - p.T), p.row_bytes, zero);
+        return;
+    }
+    const int64_t base = (static_cast<int64_t>(blockIdx.y) * (blockDim.x >> 5) + warp) * blocks::kBlock, c = base + lane;
+    if (base >= p.H) return;
+    const int *pos = p.position + t * p.k;
+    const unsigned char *x = p.x + t * p.x_ld;
+    float v[4];
+    uint32_t a = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] = c + 32 * i < p.H ? blocks::load1<DT>(x, c + 32 * i) : 0.f;
+        a = max(a, blocks::magnitude(v[i]));
+    }
+    float inv;
+    const float scale = blocks::scale_of(__reduce_max_sync(0xffffffffu, a), inv);
+    const uint32_t q = blocks::pack_e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+    for (int j = 0; j < p.k; ++j) {
+        const int r = pos[j];
+        if (r < 0 || r >= p.R) continue;
+        unsigned char *row = p.out + r * p.out_ld;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (c + 32 * i < p.H) row[c + 32 * i] = static_cast<unsigned char>(q >> (8 * i));
+        if (lane == 0) p.scale[r * p.scale_ld + base / blocks::kBlock] = scale;
     }
 }
 
@@ -368,9 +419,13 @@ __device__ __forceinline__ float weight_of(const RowParams &p, int64_t t, int j)
     return blocks::load1<DT>(static_cast<const unsigned char *>(p.w), i);
 }
 
-template <int DT, bool VEC, int AT_ONCE>
-__global__ void __launch_bounds__(256, AT_ONCE > 4 && DT == VLMCE_F32 ? 2 : 3) combine_kernel(const RowParams p) {
-    using C = blocks::Cols<VEC>;
+// (Five CTAs per SM of up to 51 registers where a thread has four rows of 16-bit values:
+// 8192 x 4 rows of 4096 68 us, as the compiler likes 72.  The gradient needs four of 64: 91
+// us, with three 100.)
+template <int DT, int U, int AT_ONCE>
+__global__ void __launch_bounds__(256, AT_ONCE > 4 ? (DT == VLMCE_F32 || U == 2 ? 2 : 3) : DT == VLMCE_F32 || U == 2 ? 3 : 5)
+    combine_kernel(const RowParams p) {
+    using C = blocks::Cols<DT, U>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
@@ -380,13 +435,13 @@ __global__ void __launch_bounds__(256, AT_ONCE > 4 && DT == VLMCE_F32 ? 2 : 3) c
     if (base >= p.H) return;
     const C cols(base, lane);
     const int *pos = p.position + t * p.k;
-    typename C::template Raw<DT> res;
-    if (p.residual) cols.template fetch<DT>(p.residual + t * p.res_ld, p.H, res);
+    typename C::Raw res;
+    if (p.residual) cols.fetch(p.residual + t * p.res_ld, p.H, res);
     float y[C::N];
 #pragma unroll
     for (int i = 0; i < C::N; ++i) y[i] = 0.f;
     for (int j0 = 0; j0 < p.k; j0 += AT_ONCE) {
-        typename C::template Raw<DT> v[AT_ONCE];
+        typename C::Raw v[AT_ONCE];
         float w[AT_ONCE];
         int r[AT_ONCE];
 #pragma unroll
@@ -397,25 +452,26 @@ __global__ void __launch_bounds__(256, AT_ONCE > 4 && DT == VLMCE_F32 ? 2 : 3) c
         }
 #pragma unroll
         for (int j = 0; j < AT_ONCE; ++j)
-            if (r[j] >= 0) cols.template fetch<DT>(p.rows_in + r[j] * p.in_ld, p.H, v[j]);
+            if (r[j] >= 0) cols.fetch(p.rows_in + r[j] * p.in_ld, p.H, v[j]);
 #pragma unroll
         for (int j = 0; j < AT_ONCE; ++j)
             if (r[j] >= 0) {
 #pragma unroll
-                for (int i = 0; i < C::N; ++i) y[i] = fmaf(w[j], C::template value<DT>(v[j], i), y[i]);
+                for (int i = 0; i < C::N; ++i) y[i] = fmaf(w[j], C::value(v[j], i), y[i]);
             }
     }
     if (p.residual) {
 #pragma unroll
-        for (int i = 0; i < C::N; ++i) y[i] += C::template value<DT>(res, i);
+        for (int i = 0; i < C::N; ++i) y[i] += C::value(res, i);
     }
-    cols.template store<DT>(p.out + t * p.out_ld, p.H, y);
+    cols.store(p.out + t * p.out_ld, p.H, y);
 }
 
 // A CTA has the whole row of a token: dw's sums stay in it, in an order of their own.
-template <int DT, bool VEC, int AT_ONCE>
-__global__ void __launch_bounds__(256, AT_ONCE > 4 || DT == VLMCE_F32 ? 2 : 3) combine_bwd_kernel(const RowParams p) {
-    using C = blocks::Cols<VEC>;
+template <int DT, int U, int AT_ONCE>
+__global__ void __launch_bounds__(256, AT_ONCE > 4 || DT == VLMCE_F32 ? 2 : U == 2 ? 3 : 4)
+    combine_bwd_kernel(const RowParams p) {
+    using C = blocks::Cols<DT, U>;
     const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     __shared__ float part[8][AT_ONCE];
     ptx::griddep_launch_dependents();
@@ -423,7 +479,7 @@ __global__ void __launch_bounds__(256, AT_ONCE > 4 || DT == VLMCE_F32 ? 2 : 3) c
     const int64_t t = blockIdx.x;
     if (t >= p.T) {
         if (p.out)
-            clear_rows(p, static_cast<int>(t - p.T), p.H * blocks::elt_bytes<DT>, 0.f);
+            clear_rows(p, static_cast<int>(t - p.T), p.row_bytes, 0.f);
         return;
     }
     const int *pos = p.position + t * p.k;
@@ -440,18 +496,18 @@ __global__ void __launch_bounds__(256, AT_ONCE > 4 || DT == VLMCE_F32 ? 2 : 3) c
         for (int64_t base = static_cast<int64_t>(warp) * C::kWarp; base < p.H;
              base += static_cast<int64_t>(warps) * C::kWarp) {
             const C cols(base, lane);
-            typename C::template Raw<DT> d, v[AT_ONCE];
-            cols.template fetch<DT>(p.x + t * p.x_ld, p.H, d);
+            typename C::Raw d, v[AT_ONCE];
+            cols.fetch(p.x + t * p.x_ld, p.H, d);
             if (p.dw) {
 #pragma unroll
                 for (int j = 0; j < AT_ONCE; ++j)
-                    if (r[j] >= 0) cols.template fetch<DT>(p.rows_in + r[j] * p.in_ld, p.H, v[j]);
+                    if (r[j] >= 0) cols.fetch(p.rows_in + r[j] * p.in_ld, p.H, v[j]);
 #pragma unroll
                 for (int j = 0; j < AT_ONCE; ++j)
                     if (r[j] >= 0) {
 #pragma unroll
                         for (int i = 0; i < C::N; ++i)
-                            sum[j] = fmaf(C::template value<DT>(d, i), C::template value<DT>(v[j], i), sum[j]);
+                            sum[j] = fmaf(C::value(d, i), C::value(v[j], i), sum[j]);
                     }
             }
             if (p.out) {
@@ -460,8 +516,8 @@ __global__ void __launch_bounds__(256, AT_ONCE > 4 || DT == VLMCE_F32 ? 2 : 3) c
                     if (r[j] >= 0) {
                         float o[C::N];
 #pragma unroll
-                        for (int i = 0; i < C::N; ++i) o[i] = w[j] * C::template value<DT>(d, i);
-                        cols.template store<DT>(p.out + r[j] * p.out_ld, p.H, o);
+                        for (int i = 0; i < C::N; ++i) o[i] = w[j] * C::value(d, i);
+                        cols.store(p.out + r[j] * p.out_ld, p.H, o);
                     }
             }
         }
@@ -506,36 +562,40 @@ cudaError_t launch(void (*k)(const P), dim3 grid, int threads, size_t smem, unsi
     return cudaLaunchKernelEx(&cfg, k, p);
 }
 
-template <bool VEC, bool FP8>
-RowKernel gather_of(int dt) {
-    switch (dt) {
-        case VLMCE_F32: return gather_kernel<VLMCE_F32, VEC, FP8>;
-        case VLMCE_F16: return gather_kernel<VLMCE_F16, VEC, FP8>;
-        default: return gather_kernel<VLMCE_BF16, VEC, FP8>;
-    }
+RowKernel gather_copy_of(int unit) {
+    return unit == 16 ? gather_copy_kernel<16> : unit == 4 ? gather_copy_kernel<4> : gather_copy_kernel<2>;
 }
+template <bool ALIGNED>
 RowKernel gather_wide_of(int dt) {
     switch (dt) {
-        case VLMCE_F32: return gather_wide_kernel<VLMCE_F32>;
-        case VLMCE_F16: return gather_wide_kernel<VLMCE_F16>;
-        default: return gather_wide_kernel<VLMCE_BF16>;
+        case VLMCE_F32: return gather_wide_kernel<VLMCE_F32, ALIGNED>;
+        case VLMCE_F16: return gather_wide_kernel<VLMCE_F16, ALIGNED>;
+        default: return gather_wide_kernel<VLMCE_BF16, ALIGNED>;
     }
 }
-template <bool VEC, int AT_ONCE>
-RowKernel combine_of(int dt, bool bwd) {
+RowKernel gather_bytes_of(int dt) {
     switch (dt) {
-        case VLMCE_F32:
-            return bwd ? combine_bwd_kernel<VLMCE_F32, VEC, AT_ONCE> : combine_kernel<VLMCE_F32, VEC, AT_ONCE>;
-        case VLMCE_F16:
-            return bwd ? combine_bwd_kernel<VLMCE_F16, VEC, AT_ONCE> : combine_kernel<VLMCE_F16, VEC, AT_ONCE>;
-        default:
-            return bwd ? combine_bwd_kernel<VLMCE_BF16, VEC, AT_ONCE> : combine_kernel<VLMCE_BF16, VEC, AT_ONCE>;
+        case VLMCE_F32: return gather_bytes_kernel<VLMCE_F32>;
+        case VLMCE_F16: return gather_bytes_kernel<VLMCE_F16>;
+        default: return gather_bytes_kernel<VLMCE_BF16>;
     }
 }
-// (unused places of eight cost registers: up to four rows of a token at a time, or eight)
-RowKernel combine_of(int dt, bool bwd, bool vec, int64_t k) {
-    if (k <= 4) return vec ? combine_of<true, 4>(dt, bwd) : combine_of<false, 4>(dt, bwd);
-    return vec ? combine_of<true, 8>(dt, bwd) : combine_of<false, 8>(dt, bwd);
+template <int DT, int U>
+RowKernel combine_of(bool bwd, int64_t k) {
+    // (unused places of eight cost registers: up to four rows of a token at a time, or eight)
+    if (k <= 4) return bwd ? combine_bwd_kernel<DT, U, 4> : combine_kernel<DT, U, 4>;
+    return bwd ? combine_bwd_kernel<DT, U, 8> : combine_kernel<DT, U, 8>;
+}
+template <int DT>
+RowKernel combine_of16(int unit, bool bwd, int64_t k) {
+    return unit == 16 ? combine_of<DT, 16>(bwd, k) : unit == 4 ? combine_of<DT, 4>(bwd, k) : combine_of<DT, 2>(bwd, k);
+}
+RowKernel combine_of(int dt, int unit, bool bwd, int64_t k) {
+    switch (dt) {
+        case VLMCE_F32: return unit == 16 ? combine_of<VLMCE_F32, 16>(bwd, k) : combine_of<VLMCE_F32, 4>(bwd, k);
+        case VLMCE_F16: return combine_of16<VLMCE_F16>(unit, bwd, k);
+        default: return combine_of16<VLMCE_BF16>(unit, bwd, k);
+    }
 }
 
 constexpr int64_t kMaxH = int64_t(1) << 24;
@@ -558,7 +618,9 @@ struct Mat {
     const void *p;
     int64_t rows, cols, ld;
     int elt;
-    bool aligned16() const { return aligned(p, 16) && ld * elt % 16 == 0; }
+    bool in_units(int u) const {
+        return aligned(p, static_cast<uintptr_t>(u)) && ld * elt % u == 0 && cols * elt % u == 0;
+    }
 };
 vlmce_status check(const Mat &m) {
     if (m.ld < m.cols || (m.rows > 0 && !m.p)) return VLMCE_ERR_INVALID_ARG;
@@ -569,6 +631,15 @@ vlmce_status check(const Mat &m) {
 bool overlap(const Mat &a, const Mat &b) {
     return rows_overlap({a.p, a.rows, a.cols * a.elt, a.ld * a.elt},
                         {b.p, b.rows, b.cols * b.elt, b.ld * b.elt});
+}
+
+// The largest accesses that all of them take (an absent one takes any).  8192 tokens, k = 4,
+// bf16, H 4096 in 16 bytes, 4100 in 4 and 4097 in 2: gather 50, 60 and 70 us, combine 68, 76
+// and 112, its gradient 91, 97 and 132 (all in single elements, four a thread: 73, 130, 135).
+int unit_of(std::initializer_list<const Mat *> mats, int elt) {
+    for (const int u : {16, 4})
+        if (std::all_of(mats.begin(), mats.end(), [u](const Mat *m) { return !m->p || m->in_units(u); })) return u;
+    return elt;
 }
 
 // Threads of a CTA and CTAs of a row: warps of `per` columns, eight of them at most.
@@ -682,13 +753,14 @@ extern "C" vlmce_status moe_gather(const void *x, int64_t x_stride, int32_t dtyp
     DeviceInfo dev;
     st = current_device(&dev);
     if (st != VLMCE_OK) return st;
-    const bool vec = H % 8 == 0 && in.aligned16() && aligned(rows, fp8 ? 8 : 16) &&
-                     rows_stride * out.elt % (fp8 ? 8 : 16) == 0;
     RowParams p = {};
     p.x = static_cast<const unsigned char *>(x);
     p.x_ld = x_stride * in.elt;
     p.out = static_cast<unsigned char *>(rows);
     p.out_ld = rows_stride * out.elt;
+    p.row_bytes = H * out.elt;
+    p.first = reinterpret_cast<uintptr_t>(x);
+    p.last = p.first + (T > 0 ? static_cast<uintptr_t>(((T - 1) * x_stride + H) * in.elt) : 0);
     p.scale = scale;
     p.scale_ld = nb;
     p.position = position;
@@ -699,11 +771,13 @@ extern "C" vlmce_status moe_gather(const void *x, int64_t x_stride, int32_t dtyp
     p.H = H;
     p.k = static_cast<int>(k);
     p.E = static_cast<int>(E);
-    const bool wide = fp8 && H % 16 == 0 && in.aligned16() && out.aligned16();
-    const RowKernel kern = wide  ? gather_wide_of(dtype)
-                           : vec ? (fp8 ? gather_of<true, true>(dtype) : gather_of<true, false>(dtype))
-                                 : (fp8 ? gather_of<false, true>(dtype) : gather_of<false, false>(dtype));
-    const int per = wide ? 512 : vec ? 256 : 128, threads = threads_of(H, per);
+    const int unit = unit_of({&in, &out}, in.elt);
+    const bool wide = aligned(rows, 16) && rows_stride % 16 == 0;  // e4m3
+    const RowKernel kern = !fp8   ? gather_copy_of(unit)
+                           : wide ? (H % 16 == 0 && in.in_units(16) ? gather_wide_of<true>(dtype) : gather_wide_of<false>(dtype))
+                                  : gather_bytes_of(dtype);
+    const int per = !fp8 ? 32 * unit / in.elt * (unit == 16 ? kCopyUnits<16> : kCopyUnits<4>) : wide ? 512 : blocks::kBlock;
+    const int threads = threads_of(H, per);
     return launch_status(launch(kern, dim3(static_cast<unsigned>(T + E), row_ctas(H, per, threads), 1),
                                 threads, 0, 1, reinterpret_cast<cudaStream_t>(stream), p),
                          "moe_gather");
@@ -738,7 +812,7 @@ extern "C" vlmce_status moe_combine(const void *rows, int64_t rows_stride, int32
     DeviceInfo dev;
     st = current_device(&dev);
     if (st != VLMCE_OK) return st;
-    const bool vec = H % 8 == 0 && in.aligned16() && out.aligned16() && (!residual || res.aligned16());
+    const int unit = unit_of({&in, &out, &res}, elt);
     RowParams p = {};
     p.rows_in = static_cast<const unsigned char *>(rows);
     p.in_ld = rows_stride * elt;
@@ -754,9 +828,10 @@ extern "C" vlmce_status moe_combine(const void *rows, int64_t rows_stride, int32
     p.R = R;
     p.H = H;
     p.k = static_cast<int>(k);
-    const int per = vec ? 256 : 128, threads = threads_of(H, per);
+    constexpr int per = blocks::Cols<VLMCE_F32, 16>::kWarp;
+    const int threads = threads_of(H, per);
     return launch_status(
-        launch(combine_of(dtype, false, vec, k),
+        launch(combine_of(dtype, unit, false, k),
                dim3(static_cast<unsigned>(T), row_ctas(H, per, threads), 1), threads, 0, 1,
                reinterpret_cast<cudaStream_t>(stream), p),
         "moe_combine");
@@ -793,7 +868,8 @@ extern "C" vlmce_status moe_combine_bwd(const void *dy, int64_t dy_stride, const
     DeviceInfo dev;
     st = current_device(&dev);
     if (st != VLMCE_OK) return st;
-    const bool vec = H % 8 == 0 && d.aligned16() && (!dweights || in.aligned16()) && (!drows || out.aligned16());
+    // (rows that are not read do not count)
+    const int unit = dweights ? unit_of({&d, &in, &out}, elt) : unit_of({&d, &out}, elt);
     RowParams p = {};
     p.x = static_cast<const unsigned char *>(dy);
     p.x_ld = dy_stride * elt;
@@ -801,6 +877,7 @@ extern "C" vlmce_status moe_combine_bwd(const void *dy, int64_t dy_stride, const
     p.in_ld = rows_stride * elt;
     p.out = static_cast<unsigned char *>(drows);
     p.out_ld = drows_stride * elt;
+    p.row_bytes = H * elt;
     p.dw = dweights;
     p.position = position;
     p.offsets = offsets;
@@ -813,8 +890,8 @@ extern "C" vlmce_status moe_combine_bwd(const void *dy, int64_t dy_stride, const
     p.H = H;
     p.k = static_cast<int>(k);
     p.E = static_cast<int>(E);
-    const int per = vec ? 256 : 128;
-    return launch_status(launch(combine_of(dtype, true, vec, k),
+    constexpr int per = blocks::Cols<VLMCE_F32, 16>::kWarp;
+    return launch_status(launch(combine_of(dtype, unit, true, k),
                                 dim3(static_cast<unsigned>(T + E), 1, 1), threads_of(H, per), 0, 1,
                                 reinterpret_cast<cudaStream_t>(stream), p),
                          "moe_combine_bwd");

@@ -113,12 +113,9 @@ struct Tile {
     }
     // Row i out of the 16-byte units that hold it, of which it starts `off` bytes in.
     __device__ __forceinline__ void place(int i, uint32_t (&w)[kWords + 4], uint32_t off) {
+        blocks::move_into_place<kWords, k16>(w, off);
 #pragma unroll
-        for (int k = 0; k < kWords + 2; ++k) w[k] = off & 8 ? w[k + 2] : w[k];
-#pragma unroll
-        for (int k = 0; k < kWords + 1; ++k) w[k] = off & 4 ? w[k + 1] : w[k];
-#pragma unroll
-        for (int k = 0; k < kWords; ++k) u[i][k] = k16 ? __funnelshift_r(w[k], w[k + 1], (off & 2) * 8) : w[k];
+        for (int k = 0; k < kWords; ++k) u[i][k] = w[k];
     }
     // At any alignment, eight rows `ld` bytes apart whose units lie within x's memory: four
     // rows' loads at a time (in a branch for each row they wait for one another: 7042 x 6722
