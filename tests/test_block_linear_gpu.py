@@ -92,10 +92,13 @@ SMALL = [(1, 1, 1), (1, 128, 128), (1, 4096, 2048), (1, 100, 16), (2, 300, 640),
          (8, 20000, 256),
          # K shared by clusters of two to eight, with each tile
          (1, 12000, 2048), (1, 7500, 1024), (5, 3000, 2048), (20, 7500, 2048), (33, 5000, 2048), (130, 1500, 2048),
-         (100, 7500, 2048), (200, 1500, 2048), (200, 500, 2048)]
+         (100, 7500, 2048), (200, 1500, 2048), (200, 500, 2048),
+         (40, 5000, 4096), (100, 2000, 2048), (900, 300, 4096), (200, 2000, 4096), (900, 96, 4096), (20, 3000, 4096)]
 PAIRS = [(193, 8, 16), (256, 256, 128), (257, 264, 640), (300, 1001, 200), (512, 128, 4096), (700, 777, 1000),
          (1024, 100, 136), (2000, 520, 256),
-         (2000, 2600, 264), (513, 9000, 136), (130, 12000, 512)]
+         (2000, 2600, 264), (513, 9000, 136), (130, 12000, 512),
+         (2000, 7777, 16), (1000, 2600, 264), (2600, 1001, 264), (300, 9000, 264), (257, 9000, 400), (4100, 520, 264),
+         (3100, 777, 264)]
 
 
 @pytest.mark.parametrize("by_row", [False, True])
@@ -105,7 +108,7 @@ def test_dense(T, N, K, by_row):
 
 
 @pytest.mark.parametrize("T,N,K", [(1, 256, 512), (5, 1000, 4096), (30, 128, 1024), (60, 300, 300), (130, 130, 130),
-                                   (300, 1000, 264), (333, 77, 300)])
+                                   (300, 1000, 264), (333, 77, 300), (1000, 2600, 264)])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_residual_at_any_alignment(T, N, K, dtype):
     for pad in (0, 1, 8):
@@ -130,7 +133,8 @@ def group_rows(g, E, most, align=1):
 
 EXPERTS = [(4, 3, 96, 128), (7, 20, 300, 256), (33, 9, 136, 640), (64, 1, 512, 384), (5, 100, 264, 1000),
            (16, 50, 1000, 200), (3, 700, 264, 512), (2, 1000, 100, 136), (1000, 1, 64, 128), (3, 1400, 1000, 600), (40, 60, 1000, 384),
-           (6, 150, 2000, 384), (10, 130, 1200, 256)]
+           (6, 150, 2000, 384), (10, 130, 1200, 256), (6, 60, 2000, 1000), (8, 130, 1000, 1000), (5, 900, 777, 512),
+           (4, 900, 2100, 264)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])

@@ -52,10 +52,12 @@ void launch_attributes(cudaLaunchAttribute (&attr)[2], unsigned csize) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
 }
 
-// Per device: the kernels' shared memory is opted in to, the CTA pairs that fit at once,
-// the SMs, and the word for errors of calls without one of their own.
+// Per device: the kernels' shared memory is opted in to, the CTA pairs that fit at once, the
+// clusters of single CTAs (one or two of them on an SM), the SMs, and the word for errors of
+// calls without one of their own.
 struct Capacity {
     int pairs = 0, sms = 0;
+    int clusters[2][kMaxSplit + 1] = {};
     int *errors = nullptr;
 };
 cudaError_t setup(Capacity *out) {
@@ -94,6 +96,26 @@ cudaError_t setup(Capacity *out) {
             if (e == cudaSuccess && n < 1) e = cudaErrorInvalidConfiguration;
             if (e != cudaSuccess) return e;
             c.pairs = k == 0 ? n : std::min(c.pairs, n);
+        }
+        int *one = c.clusters[0], *two = c.clusters[1];
+        one[1] = c.sms;
+        for (int split = 2; split <= kMaxSplit; ++split) {
+            cudaLaunchConfig_t cfg = {};
+            cudaLaunchAttribute attr[2];
+            launch_attributes(attr, static_cast<unsigned>(split));
+            cfg.gridDim = dim3(static_cast<unsigned>(split), 1, 1);
+            cfg.blockDim = dim3(kSmallThreads, 1, 1);
+            cfg.dynamicSmemBytes = kSmallSmemMax;
+            cfg.attrs = attr;
+            cfg.numAttrs = 2;
+            e = cudaOccupancyMaxActiveClusters(&one[split], small_kernel(128, false), &cfg);
+            if (e != cudaSuccess) return e;
+        }
+        // Two CTAs on an SM: as half as many alone (the runtime's answer counts one for kernels
+        // with tensor memory).
+        for (int split = 2; split <= kMaxSplit; ++split) {
+            const int half = (split + 1) / 2;
+            two[split] = one[half] * 2 * half / split;
         }
         cached[device] = c;
     }
@@ -141,17 +163,17 @@ bool small_layout(const Fwd &f, int bn, int split, int per_sm, int per_stage, Pl
 int64_t groups_used(const Fwd &f) { return f.offsets ? std::min(f.groups, f.T) : 1; }
 
 // Estimates in SM clocks at 1.9 GHz, from sweeps on GB300 of every bn, split, per_sm and
-// per_stage over 26 products (T = 1 .. 8192, dense and of 8 .. 128 experts): the chosen plan
-// is within 10 % of the fastest. A block costs an SM kSmallBlock[bn] clocks (of a pair tile
-// kPairBlock) and the weights come from HBM at 6.8 TB/s at best.  Where a group's rows are
-// known on the device only, a group takes half a tile more than its average.  Two CTAs per
-// SM are for tiles of few rows (us with two and with one: T 512, 32 experts, K 4096, N 4096
-// in tiles of 16 96 and 107, T 2048, 64 experts, N 2048 in tiles of 32 103 and 140), two
-// blocks a stage wherever there are two (the latter 103 and 108).
+// per_stage over 49 products (T = 1 .. 22252, dense and of 4 .. 128 experts): the chosen plan
+// is within 10 % of the fastest, 1.5 % on average.  A block costs an SM kSmallBlock[bn] clocks
+// (of a pair tile kPairBlock) and the weights come from HBM at 6.8 TB/s at best.  Where a
+// group's rows are known on the device only, a group takes kGroupTail tiles more than its
+// average.  Two CTAs per SM are for tiles of few rows (us with two and with one: T 512, 32
+// experts, K 4096, N 4096 in tiles of 16 93 and 107, T 2048, 64 experts, N 2048 in tiles of 32
+// 102 and 140), two blocks a stage wherever there are two (the latter 102 and 107).
 constexpr double kHbmBytesPerClock = 3570.;
-constexpr double kSmallBlock[4] = {480., 600., 1000., 1100.}, kPairBlock = 1100.;
-constexpr double kLoneCta = 1.25;  // one CTA on an SM that could take two
-constexpr double kSmallCta = 6000., kPairCta = 7500., kSplitSync = 1500.;
+constexpr double kSmallBlock[4] = {315., 490., 820., 1270.}, kPairBlock = 1140.;
+constexpr double kLoneCta = 1.35;  // one CTA on an SM that could take two
+constexpr double kSmallCta = 5700., kPairCta = 9300., kSplitSync = 1240., kSplitRow = 40., kGroupTail = 0.45;
 
 Plan choose(const Fwd &f, const Capacity &cap) {
     const int64_t used = groups_used(f);
@@ -159,7 +181,7 @@ Plan choose(const Fwd &f, const Capacity &cap) {
     const int64_t chunks = (f.K + 127) / 128;
     const double hbm = static_cast<double>(used) * f.N * f.K / kHbmBytesPerClock;
     auto tiles_of = [&](int step, int64_t across) {
-        const double down = f.offsets ? std::max(1., rows / step + 0.5) * used
+        const double down = f.offsets ? std::max(1., rows / step + kGroupTail) * used
                                       : static_cast<double>((f.T + step - 1) / step);
         return down * static_cast<double>(across);
     };
@@ -175,13 +197,15 @@ Plan choose(const Fwd &f, const Capacity &cap) {
         for (int split = 1; split <= kMaxSplit && split <= chunks; ++split) {
             const double ctas = tiles * split;
             // A shared tile is a cluster's only one, so a second wave starts from nothing (T
-            // 128, K 4096, N 12288 in three parts 49.6 us, whole 23.4).
-            if (split > 1 && ctas > per_sm * cap.sms) break;
+            // 128, K 4096, N 12288 in three parts 49.6 us, whole 23.4), and fewer clusters of
+            // eight fit than eighths of the SMs (T 1017, K 7664, N 108: 16 clusters of eight
+            // 19.0 us, of six 11.6).
+            if (split > 1 && tiles > cap.clusters[per_sm - 1][split]) continue;
             const int64_t each = (chunks + split - 1) / split;
             const int at_once = ctas <= cap.sms ? 1 : per_sm;
             const double own = std::ceil(ctas / (cap.sms * at_once)) * at_once * each * kSmallBlock[i] *
                                (at_once < per_sm ? kLoneCta : 1.);
-            const double clocks = joined(own) + kSmallCta + (split > 1 ? kSplitSync + 30. * bn : 0.);
+            const double clocks = joined(own) + kSmallCta + (split > 1 ? kSplitSync + kSplitRow * bn : 0.);
             Plan p = {};
             if (clocks < best.clocks && small_layout(f, bn, split, per_sm, each >= 2 ? 2 : 1, &p)) {
                 best = p;
