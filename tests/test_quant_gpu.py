@@ -143,6 +143,30 @@ def test_zeros_tiny_values_infinities_and_nans(dtype):
     assert torch.isnan(vs[:128, 256:512]).all() and not torch.isnan(vs[:, :256]).any()
 
 
+@pytest.mark.parametrize("shape", [(256, 256), (130, 261)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_one_bad_value_spoils_its_block_only(dtype, shape):
+    """Of either sign, beside larger patterns of the other, aligned rows or not."""
+    x = randn(gen(7), shape, DT[dtype])
+    spots = {(1, 3): float("inf"), (70, 130): float("-inf"), (129, 5): float("nan"), (128, 200): -float("nan")}
+    for at, value in spots.items():
+        x[at] = value
+    clean = torch.where(torch.isfinite(x), x, torch.zeros_like(x))
+    for square in (False, True):
+        r, c = (v.quantize_blocks(t, square=square, transposed=True) for t in (x, clean))
+        for q, s, qc, sc, flip in ((r.q, r.scale, c.q, c.scale, False), (r.qt, r.scale_t, c.qt, c.scale_t, True)):
+            R, C = q.shape
+            down = 128 if square else 1
+            bad = torch.zeros((R, C), dtype=torch.bool, device="cuda")
+            for i, j in spots:
+                i, j = (j, i) if flip else (i, j)
+                i0, j0 = i // down * down, j // 128 * 128
+                bad[i0:i0 + down, j0:j0 + 128] = True
+            val = q.float() * s.repeat_interleave(down, 0)[:R].repeat_interleave(128, 1)[:, :C]
+            assert torch.equal(torch.isnan(val), bad)
+            assert torch.equal(q.view(torch.uint8)[~bad], qc.view(torch.uint8)[~bad])
+
+
 def test_empty_and_a_stream():
     r = v.quantize_blocks(torch.empty((0, 256), device="cuda"), transposed=True)
     assert r.q.shape == (0, 256) and r.qt.shape == (256, 0) and r.scale.shape == (0, 2)

@@ -14,7 +14,7 @@
 // memory, and it adds them in rank order (so the result does not depend on timing).
 //
 // Bound by the weights' way from HBM where rows are few (T 64, 8 of 32 experts, K 4096, N
-// 4096: 93 us, 560 MB, 6.0 TB/s; T 1, K 4096, N 12288: 13.5 us, 50 MB, of which 4-5 us are the
+// 4096: 95 us, 560 MB, 5.9 TB/s; T 1, K 4096, N 12288: 13.5 us, 50 MB, of which 4-5 us are the
 // launch, the first fetch and the last block's way out), and by the epilogue's instructions
 // from 64 rows a tile on (64 rows an expert of 4096 x 4096 132 us; each thread with four weight
 // rows, so that x's factors are read a quarter as often, 136).
