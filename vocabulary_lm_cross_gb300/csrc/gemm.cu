@@ -90,6 +90,22 @@ bool make_tile_map(CUtensorMap *m, const void *base, CUtensorMapDataType type, i
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_stack_map(CUtensorMap *m, const void *base, CUtensorMapDataType type, int elt, int64_t inner,
+                    int64_t rows, int64_t matrices, int64_t stride, int box_inner, int box_rows) {
+    EncodeTiled enc = encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows),
+                                static_cast<cuuint64_t>(matrices)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(stride * elt),
+                                   static_cast<cuuint64_t>(rows * stride * elt)};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_inner), static_cast<cuuint32_t>(box_rows), 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, type, 3, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool make_operand_map(CUtensorMap *m, const void *base, bool mn, int64_t rows, int64_t K,
                       int64_t ld, bool f16) {
     const CUtensorMapDataType type =

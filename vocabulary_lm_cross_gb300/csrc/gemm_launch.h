@@ -19,6 +19,10 @@ namespace gemm {
 bool make_tile_map(CUtensorMap *m, const void *base, CUtensorMapDataType type, int elt,
                    int64_t inner, int64_t outer, int64_t stride, int box_inner, int box_outer);
 
+// The same of `matrices` that follow each other: a box's rows end with its matrix's.
+bool make_stack_map(CUtensorMap *m, const void *base, CUtensorMapDataType type, int elt, int64_t inner,
+                    int64_t rows, int64_t matrices, int64_t stride, int box_inner, int box_rows);
+
 // Tensor map of operand A (rows = M) or B (rows = N) of C = A B^T, bf16
 // (fp16 with f16): K-major ([rows, ld], K contiguous; boxes of 64 K x 128
 // rows) or MN-major ([K, ld], rows contiguous; boxes of 64 x 64).

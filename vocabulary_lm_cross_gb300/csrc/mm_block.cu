@@ -279,10 +279,8 @@ cudaError_t launch_pair(PairKernel k, const PairMaps &maps, const PairParams &p,
 }
 
 // (A TMA store fills a row's last 16 bytes, so the map ends with the last whole ones.)
-bool output_map(CUtensorMap *m, const void *p, bool f32, int64_t rows, int64_t cols, int64_t ld) {
-    return gemm::make_tile_map(
-        m, p, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, f32 ? 4 : 2,
-        cols & ~int64_t{f32 ? 3 : 7}, rows, ld, f32 ? 32 : 64, 32);
+bool output_map(CUtensorMap *m, const void *p, int64_t rows, int64_t cols, int64_t ld) {
+    return gemm::make_tile_map(m, p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, cols & ~int64_t{7}, rows, ld, 64, 32);
 }
 
 cudaError_t forward_pair(const Fwd &f, const Capacity &cap, cudaStream_t s) {
@@ -291,7 +289,7 @@ cudaError_t forward_pair(const Fwd &f, const Capacity &cap, cudaStream_t s) {
     p.vec = mm::vec_of(f.y, f.y_ld, f.N);
     if (!e4m3_map(&maps.a, f.x, f.T, f.K, f.x_ld, mm::kHalfRows) ||
         !e4m3_map(&maps.b, f.w, f.groups * f.N, f.K, f.w_ld, kPairN / 2) ||
-        (p.vec >= 16 && !output_map(&maps.y, f.y, false, f.T, f.N, f.y_ld)))
+        (p.vec >= 16 && !output_map(&maps.y, f.y, f.T, f.N, f.y_ld)))
         return cudaErrorInvalidValue;
     p.offsets = f.offsets;
     p.as = f.xs;
@@ -346,7 +344,9 @@ cudaError_t dweight(const Dw &d, cudaStream_t s) {
     p.vec = f32 ? (aligned(d.dw, 16) && d.K % 4 == 0 ? 16 : 2) : mm::vec_of(d.dw, d.K, d.K);
     if (!e4m3_map(&maps.a, d.dyt, d.N, d.R, d.dyt_ld, mm::kHalfRows) ||
         !e4m3_map(&maps.b, d.xt, d.K, d.R, d.xt_ld, kPairN / 2) ||
-        (p.vec >= 16 && !output_map(&maps.y, d.dw, f32, d.groups * d.N, d.K, d.K)))
+        (p.vec >= 16 && !(f32 ? gemm::make_stack_map(&maps.y, d.dw, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, d.K, d.N,
+                                                     d.groups, d.K, 32, 32)
+                              : output_map(&maps.y, d.dw, d.groups * d.N, d.K, d.K))))
         return cudaErrorInvalidValue;
     p.offsets = d.offsets;
     p.as = d.dyts;

@@ -26,7 +26,9 @@
 //
 // A tile of dweight is stored in 32 x 32 pieces from two buffers a warp; it costs the
 // epilogue about 2900 clocks (4096 x 4096, 1024 rows: 36.0 us, without the stores 29.8).  Three
-// buffers, or several pieces handed over at once, were not faster (36.8, 37.3).
+// buffers, or several pieces handed over at once, were not faster (36.8, 37.3).  Its fp32 map
+// has the matrices as a third dimension, so that a matrix's last rows leave like any others
+// (34 of 223 x 3568 46 -> 22 us).
 //
 // The tiles are dealt out in order; a group's tiles go down 8 tiles of rows before they go
 // across, so those in flight share operands.
@@ -358,7 +360,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) unpack2(acc[16 * s + j], v[2 * j], v[2 * j + 1]);
                     if constexpr (DW) {
-                        if (p.out == VLMCE_F32 && whole) {
+                        if (p.out == VLMCE_F32 && p.vec >= 16) {
                             // from two buffers in turn: the store before this one may still read
                             unsigned char *from = s & 1 ? scratch : reinterpret_cast<unsigned char *>(buf);
                             if (col >= cols) continue;
@@ -368,10 +370,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                             ptx::fence_proxy_async_smem();
                             __syncwarp();
                             if (lane == 0) {
+                                // (rows behind the matrix's last are not stored)
                                 if (p.add)
-                                    tc::tma_add_2d(&maps.y, ptx::smem_addr(from), col, static_cast<int>(row0));
+                                    tc::tma_add_3d(&maps.y, ptx::smem_addr(from), col, t.row + in_tile, t.g);
                                 else
-                                    tc::tma_store_2d(&maps.y, ptx::smem_addr(from), col, static_cast<int>(row0));
+                                    tc::tma_store_3d(&maps.y, ptx::smem_addr(from), col, t.row + in_tile, t.g);
                                 tc::bulk_commit();
                             }
                             continue;
