@@ -57,7 +57,7 @@ constexpr int kPairGroupM = 8;
 // Shared memory: mm_pair.cuh's, whose ring and output buffers are these instead.
 constexpr int kPairStages = 5;
 // with a factor for each column, the last stage's memory is where sums change their layout
-constexpr int kPairStagesRows = 4;
+constexpr int kPairStagesUsed = 4;
 static_assert(kPairEpiWarps * mm::kOutBytes <= kPairChunk, "32 x 32 sums of each warp");
 constexpr int kPairWords = factor_words(128 + kPairN);  // a block's factors: the CTA's rows of A, the columns
 constexpr int kPairOutAt = kPairStages * kPairChunk;
@@ -138,6 +138,31 @@ __device__ __forceinline__ void put_f32_rows(float *base, int64_t ld, int64_t ro
     }
 }
 
+// Half `h` of 64 columns of 32 rows, all there, on their way by a TMA store; the columns after
+// a row's last whole 16 bytes singly.
+__device__ __forceinline__ void put_half(const mm::Out &y, int64_t row0, int col, int h, const float (&v)[32], int cols,
+                                         bool f16, unsigned char *buf, int lane) {
+    if (h == 0) {
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        __syncwarp();
+    }
+    unsigned char *row = buf + lane * 128;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint4 *>(row + (((4 * h + j) ^ (lane & 7)) << 4)) =
+            make_uint4(act::pack16x2(v[8 * j], v[8 * j + 1], f16), act::pack16x2(v[8 * j + 2], v[8 * j + 3], f16),
+                       act::pack16x2(v[8 * j + 4], v[8 * j + 5], f16), act::pack16x2(v[8 * j + 6], v[8 * j + 7], f16));
+    if (h == 1) {
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            if (cols - col >= 8) tc::tma_store_2d(y.map, ptx::smem_addr(buf), col, static_cast<int>(row0));
+            tc::bulk_commit();
+        }
+        mm::put_rest(y, row0, col, row0 + 32, cols, reinterpret_cast<const uint32_t *>(buf), lane);
+    }
+}
+
 template <bool DW, bool B_ROWS>
 __global__ void __launch_bounds__(kPairThreads, 1)
     mm_block_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ PairParams p) {
@@ -157,7 +182,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         for (int b = 0; b < 2; ++b) ptx::mbar_init(buf_empty + 8u * b, 2 * kPairEpiWarps);  // of both CTAs
     }
     mm::Pair<1> q = mm::pair_setup<1>(smem_raw, p.err, 1, kPairChunk);
-    q.stages = B_ROWS ? kPairStagesRows : kPairStages;
+    q.stages = kPairStagesUsed;
     const Table table = table_at(smem + kPairTableAt, p.groups);
     table_fill(table, p.offsets, p.groups, p.T, DW ? 1 : 256, DW ? 128 : 1, p.err);
     const uint32_t tmem = __shfl_sync(0xffffffffu, q.tmem, 0);
@@ -253,7 +278,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpilogueRegs));
         const int part = kPairCols * ((warp - 4) >> 2);  // the warp's first column of the tile
         uint32_t *buf = reinterpret_cast<uint32_t *>(smem + kPairOutAt + (warp - 4) * mm::kOutBytes);
-        unsigned char *scratch = smem + kPairStagesRows * kPairChunk + (warp - 4) * mm::kOutBytes;  // B_ROWS
+        unsigned char *scratch = smem + kPairStagesUsed * kPairChunk + (warp - 4) * mm::kOutBytes;  // B_ROWS
         const float *slots = reinterpret_cast<const float *>(smem + kPairFactorsAt);
         const uint32_t empty_leader = ptx::mapa(buf_empty, 0);
         const int in_tile = mm::kHalfRows * rank + (warp & 3) * 32;  // the warp's first row
@@ -411,7 +436,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     }
                     __syncwarp();
                     const int pair = col0 + 64 * (s / 2);  // the 64 columns of a store
-                    if (pair < cols) {
+                    if (!B_ROWS && whole) {
+                        // from two buffers in turn: the store before this one may still read
+                        unsigned char *from = s < 2 ? reinterpret_cast<unsigned char *>(buf) : scratch;
+                        if (pair < cols) put_half(y, row0, pair, s & 1, v, cols, f16, from, lane);
+                    } else if (pair < cols) {
                         mm::put_seg(y, row0, pair, s & 1, v, end, cols, f16, buf, lane);
                         if (s & 1) mm::put_rest(y, row0, pair, end, cols, buf, lane);
                     }
