@@ -138,29 +138,44 @@ __device__ __forceinline__ void put_f32_rows(float *base, int64_t ld, int64_t ro
     }
 }
 
-// Half `h` of 64 columns of 32 rows, all there, on their way by a TMA store; the columns after
-// a row's last whole 16 bytes singly.
-__device__ __forceinline__ void put_half(const mm::Out &y, int64_t row0, int col, int h, const float (&v)[32], int cols,
-                                         bool f16, unsigned char *buf, int lane) {
-    if (h == 0) {
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-        __syncwarp();
-    }
+// 64 columns of 32 rows (a row a lane) of an output whose rows are whole 16-byte units apart,
+// on their way by a TMA store; where the group ends before the last row, the rows there are in
+// such units.  The columns after a row's last whole unit singly.
+template <bool F16>
+__device__ __forceinline__ void put_units(const mm::Out &y, int64_t row0, int64_t end, int col, const uint64_t *acc,
+                                          int cols, unsigned char *buf, int lane) {
+    // (of two buffers in turn: the store before this one may still read the other)
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+    __syncwarp();
     unsigned char *row = buf + lane * 128;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<uint4 *>(row + (((4 * h + j) ^ (lane & 7)) << 4)) =
-            make_uint4(act::pack16x2(v[8 * j], v[8 * j + 1], f16), act::pack16x2(v[8 * j + 2], v[8 * j + 3], f16),
-                       act::pack16x2(v[8 * j + 4], v[8 * j + 5], f16), act::pack16x2(v[8 * j + 6], v[8 * j + 7], f16));
-    if (h == 1) {
+    for (int j = 0; j < 8; ++j) {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float a, b;
+            unpack2(acc[4 * j + k], a, b);
+            w[k] = act::pack16x2(a, b, F16);
+        }
+        *reinterpret_cast<uint4 *>(row + ((j ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    if (row0 + 32 <= end) {
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-            if (cols - col >= 8) tc::tma_store_2d(y.map, ptx::smem_addr(buf), col, static_cast<int>(row0));
-            tc::bulk_commit();
+        if (lane == 0 && cols - col >= 8) tc::tma_store_2d(y.map, ptx::smem_addr(buf), col, static_cast<int>(row0));
+    } else {
+        __syncwarp();
+        const int unit = lane & 7, rows = static_cast<int>(end - row0);
+        if (col + 8 * unit + 8 <= cols) {
+            uint16_t *to = y.base + row0 * y.ld + col + 8 * unit;
+#pragma unroll 1
+            for (int r = lane >> 3; r < rows; r += 4)
+                *reinterpret_cast<uint4 *>(to + r * y.ld) =
+                    *reinterpret_cast<const uint4 *>(buf + r * 128 + ((unit ^ (r & 7)) << 4));
         }
-        mm::put_rest(y, row0, col, row0 + 32, cols, reinterpret_cast<const uint32_t *>(buf), lane);
     }
+    if (lane == 0) tc::bulk_commit();
+    mm::put_rest(y, row0, col, end, cols, reinterpret_cast<const uint32_t *>(buf), lane);
 }
 
 template <bool DW, bool B_ROWS>
@@ -378,17 +393,21 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 const bool whole = p.vec >= 16 && row0 + 32 <= end;
                 const bool f16 = p.out == VLMCE_F16;
                 const mm::Out y = {static_cast<uint16_t *>(p.y), p.y_ld, whole ? 16 : 2, &maps.y};
+                // What most tiles take stands by itself: among the other ways out, unrolled with
+                // them, its instructions came from afar.
+                bool done = false;
+                if constexpr (DW) {
+                    if (p.out == VLMCE_F32 && p.vec >= 16) {
+                        done = true;
 #pragma unroll
-                for (int s = 0; s < kPairCols / 32; ++s) {
-                    const int col = col0 + 32 * s;
-                    float v[32];
+                        for (int s = 0; s < kPairCols / 32; ++s) {
+                            const int col = col0 + 32 * s;
+                            if (col >= cols) break;
+                            float v[32];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) unpack2(acc[16 * s + j], v[2 * j], v[2 * j + 1]);
-                    if constexpr (DW) {
-                        if (p.out == VLMCE_F32 && p.vec >= 16) {
+                            for (int j = 0; j < 16; ++j) unpack2(acc[16 * s + j], v[2 * j], v[2 * j + 1]);
                             // from two buffers in turn: the store before this one may still read
                             unsigned char *from = s & 1 ? scratch : reinterpret_cast<unsigned char *>(buf);
-                            if (col >= cols) continue;
                             if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
                             __syncwarp();
                             put_fragment(v, from, lane);
@@ -402,9 +421,31 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                                     tc::tma_store_3d(&maps.y, ptx::smem_addr(from), col, t.row + in_tile, t.g);
                                 tc::bulk_commit();
                             }
-                            continue;
                         }
                     }
+                } else if constexpr (!B_ROWS) {
+                    if (p.vec >= 16 && !p.residual) {
+                        done = true;
+                        const mm::Out units = {static_cast<uint16_t *>(p.y), p.y_ld, 16, &maps.y};
+#pragma unroll
+                        for (int s = 0; s < kPairCols / 64; ++s) {
+                            const int col = col0 + 64 * s;
+                            if (col >= cols) break;
+                            unsigned char *from = s ? scratch : reinterpret_cast<unsigned char *>(buf);
+                            if (f16)
+                                put_units<true>(units, row0, end, col, acc + 32 * s, cols, from, lane);
+                            else
+                                put_units<false>(units, row0, end, col, acc + 32 * s, cols, from, lane);
+                        }
+                    }
+                }
+                if (!done) {
+#pragma unroll
+                for (int s = 0; s < kPairCols / 32; ++s) {
+                    const int col = col0 + 32 * s;
+                    float v[32];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) unpack2(acc[16 * s + j], v[2 * j], v[2 * j + 1]);
                     if constexpr (B_ROWS) to_rows(v, scratch, lane);
                     if constexpr (DW) {
                         if (p.out == VLMCE_F32) {
@@ -436,14 +477,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     }
                     __syncwarp();
                     const int pair = col0 + 64 * (s / 2);  // the 64 columns of a store
-                    if (!B_ROWS && whole) {
-                        // from two buffers in turn: the store before this one may still read
-                        unsigned char *from = s < 2 ? reinterpret_cast<unsigned char *>(buf) : scratch;
-                        if (pair < cols) put_half(y, row0, pair, s & 1, v, cols, f16, from, lane);
-                    } else if (pair < cols) {
+                    if (pair < cols) {
                         mm::put_seg(y, row0, pair, s & 1, v, end, cols, f16, buf, lane);
                         if (s & 1) mm::put_rest(y, row0, pair, end, cols, buf, lane);
                     }
+                }
                 }
             }
         }
