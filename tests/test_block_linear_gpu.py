@@ -246,6 +246,14 @@ def test_dweight_of_experts(N, K, n, accumulate):
     check_dweight(N, K, n, accumulate=accumulate, pad=N % 2)
 
 
+@pytest.mark.parametrize("K", [288, 352, 416])
+def test_dweight_of_experts_without_rows_after_others(K):
+    """A warp's last store of a tile still reads its buffer when a tile without any products
+    follows at once, also where a tile has an odd number of stores."""
+    for N in (256, 200):
+        check_dweight(N, K, [128] * 38 + [0] * 38 + [128] * 38 + [0] * 38)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("N,K,n", SIZES)
 def test_dweight_in_16_bits(N, K, n, dtype):

@@ -24,6 +24,11 @@
 // sums are there" are the same event, and both CTAs' epilogue warps wait on the stage's
 // barrier, as the copies do (a commit for each 267 us).
 //
+// What most tiles take to memory stands apart from the other ways out: unrolled among them, its
+// instructions came from afar, and a tile's output took 4000 clocks (8192 rows of 16 experts, K
+// 4096, N 4096 293 us, now 274; 9728 x 8192, K 256 50 and 46; one rolled loop for all the others
+// is slower, N 16241 86 us instead of 48).
+//
 // A tile of dweight is stored in 32 x 32 pieces from two buffers a warp; it costs the
 // epilogue about 2900 clocks (4096 x 4096, 1024 rows: 36.0 us, without the stores 29.8).  Three
 // buffers, or several pieces handed over at once, were not faster (36.8, 37.3).  Its fp32 map
@@ -55,8 +60,9 @@ constexpr int kPairBBytes = kPairN / 2 * 128;  // a CTA's part of B, of a block
 constexpr int kPairChunk = mm::kOpBytes + kPairBBytes;
 constexpr int kPairGroupM = 8;
 // Shared memory: mm_pair.cuh's, whose ring and output buffers are these instead.
+// Five stages' room, of which the ring takes four; the last one's memory is a second output
+// buffer of each warp, and with a factor for each column where sums change their layout.
 constexpr int kPairStages = 5;
-// with a factor for each column, the last stage's memory is where sums change their layout
 constexpr int kPairStagesUsed = 4;
 static_assert(kPairEpiWarps * mm::kOutBytes <= kPairChunk, "32 x 32 sums of each warp");
 constexpr int kPairWords = factor_words(128 + kPairN);  // a block's factors: the CTA's rows of A, the columns
@@ -293,14 +299,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpilogueRegs));
         const int part = kPairCols * ((warp - 4) >> 2);  // the warp's first column of the tile
         uint32_t *buf = reinterpret_cast<uint32_t *>(smem + kPairOutAt + (warp - 4) * mm::kOutBytes);
-        unsigned char *scratch = smem + kPairStagesUsed * kPairChunk + (warp - 4) * mm::kOutBytes;  // B_ROWS
+        unsigned char *scratch = smem + kPairStagesUsed * kPairChunk + (warp - 4) * mm::kOutBytes;
         const float *slots = reinterpret_cast<const float *>(smem + kPairFactorsAt);
         const uint32_t empty_leader = ptx::mapa(buf_empty, 0);
         const int in_tile = mm::kHalfRows * rank + (warp & 3) * 32;  // the warp's first row
         const int cols = DW ? p.K : p.N;
         Slot at;
         mm::Ring<1> r;
-        int it = 0;
+        int it = 0, turn = 0;  // turn: of the output buffers, over all tiles
         for (int i = first; i < total; i += step) {
             const PairTile t = pair_tile<DW>(p, table, i);
             const int block = 128 + (DW ? 0 : ((t.col + part) >> 7) - (t.col >> 7));  // B's factor in a slot
@@ -407,7 +413,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
                             for (int j = 0; j < 16; ++j) unpack2(acc[16 * s + j], v[2 * j], v[2 * j + 1]);
                             // from two buffers in turn: the store before this one may still read
-                            unsigned char *from = s & 1 ? scratch : reinterpret_cast<unsigned char *>(buf);
+                            unsigned char *from = turn ? scratch : reinterpret_cast<unsigned char *>(buf);
+                            turn ^= 1;
                             if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
                             __syncwarp();
                             put_fragment(v, from, lane);
@@ -431,7 +438,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         for (int s = 0; s < kPairCols / 64; ++s) {
                             const int col = col0 + 64 * s;
                             if (col >= cols) break;
-                            unsigned char *from = s ? scratch : reinterpret_cast<unsigned char *>(buf);
+                            unsigned char *from = turn ? scratch : reinterpret_cast<unsigned char *>(buf);
+                            turn ^= 1;
                             if (f16)
                                 put_units<true>(units, row0, end, col, acc + 32 * s, cols, from, lane);
                             else
