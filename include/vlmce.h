@@ -518,7 +518,8 @@ int64_t vlmce_moe_rows(int64_t T, int64_t k, int64_t E, int64_t align);
  *                 outside [0, E) is no expert's pair (position -1).  A token may name
  *                 an expert twice.
  * align           >= 1; 128 for rows that block_linear_dweight sums over.
- * 1 <= k <= VLMCE_MOE_MAX_TOPK, 1 <= E <= VLMCE_MOE_MAX_EXPERTS, T >= 0.
+ * 1 <= k <= VLMCE_MOE_MAX_TOPK, 1 <= E <= VLMCE_MOE_MAX_EXPERTS, T >= 0,
+ * T k <= 2^31 - 512.
  * Deterministic.  One launch.
  */
 vlmce_status moe_sort(const void *experts, int64_t experts_stride, int32_t wide, int64_t T,

@@ -50,6 +50,10 @@ constexpr int kMaxExperts = VLMCE_MOE_MAX_EXPERTS;
 static_assert(kMaxExperts <= kSortThreads, "a thread scans an expert");
 constexpr int kMaxSortCtas = 8;
 constexpr int kSortKeep = 16;
+// The pairs are numbered in 32 bits, also where a warp's last step begins before the last
+// pair and ends 32 kSortKeep after it: a step begins at a multiple of 32 below kMaxPairs.
+constexpr int64_t kMaxPairs = (int64_t(1) << 31) - 32 * kSortKeep;
+static_assert(kMaxPairs % 32 == 0 && kMaxPairs - 32 + 32 * kSortKeep <= INT32_MAX, "a step's end is a number");
 
 struct SortParams {
     const void *experts;
@@ -603,11 +607,15 @@ constexpr int64_t kMaxH = int64_t(1) << 24;
 bool dtype_ok(int32_t dt) { return dt == VLMCE_F32 || dt == VLMCE_BF16 || dt == VLMCE_F16; }
 int elt_of(int32_t dt) { return dt == VLMCE_F32 ? 4 : 2; }
 
-// T tokens of k experts of E, rounded up to `align`: whether sort takes it.
+// T tokens of k experts of E: whether the calls that read positions take them, and sort.
 vlmce_status order_ok(int64_t T, int64_t k, int64_t E) {
     if (T < 0 || k < 1 || E < 1) return VLMCE_ERR_INVALID_ARG;
     if (k > VLMCE_MOE_MAX_TOPK || E > kMaxExperts || T > INT32_MAX / k) return VLMCE_ERR_TOO_LARGE;
     return VLMCE_OK;
+}
+vlmce_status sort_ok(int64_t T, int64_t k, int64_t E) {
+    const vlmce_status st = order_ok(T, k, E);
+    return st == VLMCE_OK && T * k > kMaxPairs ? VLMCE_ERR_TOO_LARGE : st;
 }
 int64_t capacity(int64_t T, int64_t k, int64_t E, int64_t align) {
     return (T * k + std::min(E, T * k) * (align - 1)) / align * align;
@@ -668,7 +676,7 @@ vlmce_status common(int64_t T, int64_t R, int64_t H, int64_t k, int64_t E, const
 
 extern "C" int64_t vlmce_moe_rows(int64_t T, int64_t k, int64_t E, int64_t align) {
     using namespace vlmce::moe;
-    if (order_ok(T, k, E) != VLMCE_OK || align < 1 || align > INT32_MAX) return -1;
+    if (sort_ok(T, k, E) != VLMCE_OK || align < 1 || align > INT32_MAX) return -1;
     const int64_t used = std::min(E, T * k);
     if (used > 0 && align > (INT32_MAX - T * k) / used) return -1;
     return capacity(T, k, E, align);
@@ -679,7 +687,7 @@ extern "C" vlmce_status moe_sort(const void *experts, int64_t experts_stride, in
                                  int32_t *offsets, int32_t *counts, vlmce_stream_t stream) {
     using namespace vlmce;
     using namespace vlmce::moe;
-    vlmce_status st = order_ok(T, k, E);
+    vlmce_status st = sort_ok(T, k, E);
     if (st != VLMCE_OK) return st;
     if (align < 1 || experts_stride < k || !offsets || !counts || (T > 0 && (!experts || !position)))
         return VLMCE_ERR_INVALID_ARG;
