@@ -749,13 +749,15 @@ extern "C" vlmce_status moe_gather(const void *x, int64_t x_stride, int32_t dtyp
     if (st != VLMCE_OK) return st;
     const int64_t nb = (H + blocks::kBlock - 1) / blocks::kBlock;
     const Mat in{x, T, H, x_stride, elt_of(dtype)}, out{rows, R, H, rows_stride, fp8 ? 1 : elt_of(dtype)},
-        sc{scale, fp8 ? R : 0, nb, nb, 4}, pos{position, T, k, k, 4};
+        sc{scale, fp8 ? R : 0, nb, nb, 4}, pos{position, T, k, k, 4}, off{offsets, 1, E + 1, E + 1, 4},
+        cnt{counts, 1, E, E, 4};
     if (!fp8 && scale) return VLMCE_ERR_INVALID_ARG;
     st = check(in);
     if (st == VLMCE_OK) st = check(out);
     if (st == VLMCE_OK) st = check(sc);
     if (st != VLMCE_OK) return st;
-    if (overlap(out, in) || overlap(sc, in) || overlap(out, sc) || overlap(out, pos) || overlap(sc, pos))
+    if (overlap(out, in) || overlap(sc, in) || overlap(out, sc) || overlap(out, pos) || overlap(sc, pos) ||
+        overlap(out, off) || overlap(sc, off) || overlap(out, cnt) || overlap(sc, cnt))
         return VLMCE_ERR_INVALID_ARG;
     if (R == 0) return VLMCE_OK;
     DeviceInfo dev;
@@ -862,7 +864,8 @@ extern "C" vlmce_status moe_combine_bwd(const void *dy, int64_t dy_stride, const
     const int elt = elt_of(dtype), welt = elt_of(weights_dtype);
     const Mat d{dy, T, H, dy_stride, elt}, in{rows, dweights ? R : 0, H, rows_stride, elt},
         out{drows, drows ? R : 0, H, drows_stride, elt}, w{weights, weights ? T : 0, k, weights_stride, welt},
-        dw{dweights, dweights ? T : 0, k, k, 4}, pos{position, T, k, k, 4};
+        dw{dweights, dweights ? T : 0, k, k, 4}, pos{position, T, k, k, 4}, off{offsets, 1, E + 1, E + 1, 4},
+        cnt{counts, 1, E, E, 4};
     st = check(d);
     if (st == VLMCE_OK && dweights) st = check(in);
     if (st == VLMCE_OK && drows) st = check(out);
@@ -870,7 +873,8 @@ extern "C" vlmce_status moe_combine_bwd(const void *dy, int64_t dy_stride, const
     if (st == VLMCE_OK && dweights) st = check(dw);
     if (st != VLMCE_OK) return st;
     if (overlap(out, d) || overlap(out, in) || overlap(out, w) || overlap(out, dw) || overlap(out, pos) ||
-        overlap(dw, d) || overlap(dw, in) || overlap(dw, w) || overlap(dw, pos))
+        overlap(dw, d) || overlap(dw, in) || overlap(dw, w) || overlap(dw, pos) || overlap(out, off) ||
+        overlap(out, cnt) || overlap(dw, off) || overlap(dw, cnt))
         return VLMCE_ERR_INVALID_ARG;
     if (T == 0 && out.rows == 0) return VLMCE_OK;
     DeviceInfo dev;
