@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         wait_bar(q.full(r.s), r.ph, q.abort, q.err);
                         const uint64_t ad = tc::smem_desc_sw128(q.chunk(r.s, 0), 16, 1024);
                         const uint64_t bd = tc::smem_desc_sw128(q.chunk(r.s, 0) + mm::kOpBytes, 16, 1024);
-                        wait_bar(buf_empty + 8u * b, ((it >> 1) & 1) ^ 1, q.abort, q.err);
+                        wait_bar<true>(buf_empty + 8u * b, ((it >> 1) & 1) ^ 1, q.abort, q.err);
                         __syncwarp();
                         tc::fence_after_sync();
                         if (lane == 0) {
@@ -351,9 +351,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 auto release = [&] {
                     tc::fence_before_sync();
                     __syncwarp();
-                    // (TMEM was read, nothing written: no release at the cluster's scope,
-                    // whose fence took longer than the sums)
-                    if (lane == 0) ptx::mbar_remote_arrive(empty_leader + 8u * (it & 1));
+                    // (TMEM was read, nothing written: the fences of tcgen05 order it across the
+                    // cluster, and a release's fence took longer than the sums)
+                    if (lane == 0) ptx::mbar_remote_arrive_relaxed(empty_leader + 8u * (it & 1));
                 };
                 if constexpr (B_ROWS) {
 #pragma unroll

@@ -18,9 +18,10 @@ __device__ __forceinline__ void cluster_wait_any() {
     asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
-// Arrive (release at this CTA's scope) on a barrier of another CTA of the cluster.
-__device__ __forceinline__ void mbar_remote_arrive(uint32_t remote_bar) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(remote_bar) : "memory");
+// Arrive on a barrier of another CTA of the cluster without a release: for what is ordered
+// otherwise, TMEM loads by tcgen05.wait::ld and tcgen05.fence::before_thread_sync.
+__device__ __forceinline__ void mbar_remote_arrive_relaxed(uint32_t remote_bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_bar) : "memory");
 }
 
 // 16 bytes from global to shared memory without a register in between; each
