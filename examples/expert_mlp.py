@@ -84,6 +84,7 @@ def main(T: int = 512, E: int = 8, k: int = 2, H: int = 256, n: int = 384):
     y, grads = train_step(m, x, experts, weights, torch.ones_like(x))
     for name in m.master:
         m.master[name].add_(grads[name], alpha=-1e-3)
+    m.sync()
     print("tokens of each expert:", torch.bincount(experts.flatten(), minlength=E).tolist())
     print("gradient norms:", {name: round(float(t.float().norm()), 3) for name, t in grads.items()})
     few = serve(m, x[:4].clone(), experts[:4], weights[:4])
