@@ -7,6 +7,7 @@ import vocabulary_lm_cross_gb300 as v
 from examples import expert_mlp as ex
 
 pytestmark = pytest.mark.gpu
+FP8 = torch.float8_e4m3fn
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -31,3 +32,15 @@ def test_the_example_serves_with_the_weights_that_it_has_trained():
     after = ex.serve(m, x[:4].clone(), experts[:4], weights[:4])
     assert not torch.equal(before, after)
     assert torch.equal(few, after)
+
+
+@pytest.mark.parametrize("R", [100, 128, 300])
+def test_dweight_of_experts_that_all_start_at_the_end(R):
+    a, sa = torch.ones((40, 304), device="cuda").to(FP8)[:, :R], torch.ones((40, -(-R // 128)), device="cuda")
+    off = torch.full((4,), R, dtype=torch.int32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = v.block_linear_dweight(a, sa, a, sa, offsets=off, dev_err=err)
+    assert int(err) == 0 and got.shape == (3, 40, 40) and not got.any()
+    keep = torch.ones((3, 40, 40), device="cuda")
+    v.block_linear_dweight(a, sa, a, sa, offsets=off, dev_err=err, dweight=keep, accumulate=True)
+    assert int(err) == 0 and (keep == 1).all()

@@ -55,7 +55,7 @@ __device__ __forceinline__ void table_fill(const Table &t, const int *offsets, i
     bool bad = false;
     for (int e = threadIdx.x; e <= groups; e += blockDim.x) {
         const int b = offsets[e], a = e > 0 ? offsets[e - 1] : 0;
-        bad |= a < 0 || b < a || b > rows || (b % whole != 0 && (e == 0 || b != rows));
+        bad |= a < 0 || b < a || b > rows || (b % whole != 0 && b != rows);
         t.row[e] = b;
     }
     if (__syncthreads_or(bad)) {
