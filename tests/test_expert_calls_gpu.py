@@ -44,3 +44,9 @@ def test_dweight_of_experts_that_all_start_at_the_end(R):
     keep = torch.ones((3, 40, 40), device="cuda")
     v.block_linear_dweight(a, sa, a, sa, offsets=off, dev_err=err, dweight=keep, accumulate=True)
     assert int(err) == 0 and (keep == 1).all()
+
+
+def test_a_plan_of_no_experts_is_refused():
+    with pytest.raises(v.capi.VlmceError):
+        v.describe_block_linear_plan(16, 128, 128, 0)
+    assert v.describe_block_linear_plan(16, 128, 128, 1).kernel == "small"

@@ -26,7 +26,7 @@ def describe_block_linear_plan(T: int, N: int, K: int, experts: int | None = Non
     """How block_linear_fwd runs these sizes on the current device."""
     out = (ctypes.c_int32 * 4)()
     capi.check(capi.lib().vlmce_block_linear_describe_plan(
-        T, N, K, experts or 1, int(experts is not None), ctypes.cast(out, ctypes.c_void_p)),
+        T, N, K, 1 if experts is None else experts, int(experts is not None), ctypes.cast(out, ctypes.c_void_p)),
         "vlmce_block_linear_describe_plan")
     return BlockLinearPlan(("pairs", "small")[out[0]], out[1], out[2], out[3])
 
