@@ -584,7 +584,8 @@ vlmce_status moe_combine_bwd(const void *dy, int64_t dy_stride, const void *rows
  * A block that holds an infinity or a NaN stands for NaNs.
  *
  * x               [batch, R, C] of dtype (VLMCE_F32, VLMCE_BF16 or VLMCE_F16), rows
- *                 x_stride and matrices x_batch_stride elements apart.
+ *                 x_stride and matrices x_batch_stride elements apart, one behind the
+ *                 other: x_batch_stride >= (R - 1) x_stride + C.
  * square          0: blocks of 128 columns of a row for q, of 128 rows of a column for
  *                 qt; else blocks of 128 x 128 for both.
  * q, scale        [batch, R, q_stride >= C] and fp32 [batch, R, ceil(C / 128)] (square:
@@ -605,7 +606,8 @@ vlmce_status quantize_blocks(const void *x, int32_t dtype, int64_t batch, int64_
  *   y[t, n] = sum_b x_scale[t, b] weight_scale[n', b] sum_{k in b} x[t, k] weight[e, n, k]
  *             + residual[t, n]
  * on tcgen05 tensor cores; a block's sum is theirs, the scales and the sum over the blocks
- * are in fp32, and each output is rounded once.
+ * are in fp32, and each output is rounded once.  The two scales are multiplied first: a
+ * product of theirs beyond fp32's range is 0 or an infinity.
  *
  * x               [T, x_stride >= K]; x_scale fp32 [T, x_scale_stride >= ceil(K / 128)].
  * weight          [E N, weight_stride >= K]: the rows of E matrices, one after the other.
@@ -637,7 +639,8 @@ vlmce_status block_linear_fwd(const void *x, int64_t x_stride, const float *x_sc
  * block_linear_dweight -- gradient of block_linear_fwd's weight from the transposed
  * operands, blocks of 128 along their rows (qt of quantize_blocks):
  *   dweight[e, n, k] = sum_b dyt_scale[n, b] xt_scale[k, b] sum_{r in b} dyt[n, r] xt[k, r]
- * over the blocks b of columns offsets[e] .. offsets[e + 1] - 1.
+ * over the blocks b of columns offsets[e] .. offsets[e + 1] - 1, the two scales multiplied
+ * first, as there.
  *
  * dyt, xt         [N, dyt_stride >= R] and [K, xt_stride >= R], strides multiples of 16,
  *                 16-byte aligned; dyt_scale, xt_scale fp32 [N or K, stride >= ceil(R / 128)].

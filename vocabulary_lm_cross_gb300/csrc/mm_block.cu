@@ -164,7 +164,9 @@ int64_t groups_used(const Fwd &f) { return f.offsets ? std::min(f.groups, f.T) :
 
 // Estimates in SM clocks at 1.9 GHz, from sweeps on GB300 of every bn, split, per_sm and
 // per_stage over 49 products (T = 1 .. 22252, dense and of 4 .. 128 experts): the chosen plan
-// is within 10 % of the fastest, 1.5 % on average.  A block costs an SM kSmallBlock[bn] clocks
+// is within 10 % of the fastest, 1.5 % on average.  All of them had weights with a scale for
+// 128 rows: a pair tile's block takes half as long again with one for each row
+// (mm_block_pair.cuh), which the estimate does not know.  A block costs an SM kSmallBlock[bn] clocks
 // (of a pair tile kPairBlock) and the weights come from HBM at 6.8 TB/s at best.  Where a
 // group's rows are known on the device only, a group takes kGroupTail tiles more than its
 // average.  Two CTAs per SM are for tiles of few rows (us with two and with one: T 512, 32

@@ -13,10 +13,16 @@
 // lane has 32 of the columns' factors and keeps them in registers for all its rows (each of
 // them read from shared memory by all lanes, 428 us instead of 349 at the size below).
 //
-// What bounds it: the epilogue warps' own instructions, about 920 clocks a block (B_ROWS
-// 1310), where the products take 512 and their hand-over 400 (two buffers: (512 + 400 + the
-// time a buffer is being read) / 2).  8192 x 8192 x 4096 237 us = 2.31 PFLOP/s (a scale for
-// each row, without this epilogue: 174 us), with a factor for each column 349 us into fp32.
+// What bounds it: the time that the epilogue warps need to take a block's sums out, about 910
+// clocks (dweight 1375; forward with a scale for each weight row 1490, 28 bytes spilled), where
+// the products take 512 and their hand-over 400 (two buffers: (512 + 400 + the time a buffer is
+// being read) / 2).  No unit is near its rate meanwhile (ncu, 4864 x 4096 x 4096 with a scale
+// for 128 weight rows, for each, and a dweight: issue slots 44, 41 and 36 %, FMA pipe 32, 35 and
+// 30 %, tensor pipe 49, 29 and 25 %): each warp goes from a load through its wait to the
+// multiply-adds in a line, and two of them a scheduler do not cover the latencies.  Beside its
+// blocks a tile takes 1.7 us (dweight into fp32 2.5, 16 bits 2.9, scale for each row 3.0).
+// 8192 x 8192 x 4096 233 us = 2.36 PFLOP/s (one scale for a whole row, without this
+// epilogue: linear_fwd 159 us), with a scale for each weight row 389 us, dweight into fp32 354 us.
 // Tried: loads of 32 columns (255 us) and of 8 (247), a load ahead of its sums (273), two
 // blocks an iteration (357), single instead of packed multiply-adds (254), four buffers of 128
 // columns (330), 256 x 192 tiles on twelve warps without a change of registers (292), other

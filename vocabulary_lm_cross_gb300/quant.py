@@ -24,7 +24,8 @@ class BlockQuant(NamedTuple):
 
 def quantize_blocks(x: torch.Tensor, *, square: bool = False, rows: bool = True,
                     transposed: bool = False) -> BlockQuant:
-    """x [R, C] or [E, R, C] (fp32, bf16 or fp16) in float8_e4m3fn by blocks of 128.
+    """x [R, C] or [E, R, C] (fp32, bf16 or fp16; matrices one behind the other) in
+    float8_e4m3fn by blocks of 128.
 
     rows: q, blocks of 128 columns of a row (what block_linear_fwd takes as x);
     transposed: qt, blocks of 128 rows of a column, transposed (what
