@@ -26,6 +26,12 @@ constexpr int kBns[4] = {16, 32, 64, 128};  // rows of x in a small tile
 // single-CTA kernels takes for its columns (mm_small.cuh) and beside the pair kernels.
 constexpr int kSmSmem = 233472, kSmemReserved = 1024, kSmemPerTmemCol = 456;
 constexpr int kSmallSmemMax = kSmSmem - kSmemReserved;
+constexpr int kMaxPerSm = 2;  // CTAs of single-CTA kernels
+// The least shared memory of a CTA where so many are to share an SM, and one more is not.
+constexpr int least_smem(int per_sm) { return kSmSmem / (per_sm + 1) - kSmemReserved + 16; }
+static_assert(gemm::kSmemBytes + least_smem(kMaxPerSm) + 2 * kSmemReserved > kSmSmem, "GEMM engine");
+static_assert(mm::kPairSmem + least_smem(kMaxPerSm) + 2 * kSmemReserved > kSmSmem, "pair kernels");
+static_assert(kSmemPerTmemCol * 512 >= kSmSmem, "TMEM would run out first");
 
 using SmallKernel = void (*)(const CUtensorMap, const CUtensorMap, const SmallParams);
 using PairKernel = void (*)(const PairMaps, const PairParams);
@@ -155,8 +161,7 @@ bool small_layout(const Fwd &f, int bn, int split, int per_sm, int per_stage, Pl
     p->table = p->factors + factors;
     p->bar = p->table + table;
     p->smem = std::max(p->bar + kSmallTail + 1024, kSmallBufs * bn * kSmemPerTmemCol - kSmemReserved);
-    // no more CTAs per SM than that
-    p->smem = std::max(p->smem, kSmSmem / (per_sm + 1) - kSmemReserved + 16);
+    p->smem = std::max(p->smem, least_smem(per_sm));
     return true;
 }
 
@@ -193,7 +198,7 @@ Plan choose(const Fwd &f, const Capacity &cap) {
     best.clocks = joined(std::ceil(tiles_of(256, (f.N + kPairN - 1) / kPairN) / cap.pairs) *
                          chunks * kPairBlock) + kPairCta;
     for (int i = 0; i < 4; ++i) {
-        const int bn = kBns[i], per_sm = bn <= 2 * kSmallTwoNc ? 2 : 1;
+        const int bn = kBns[i], per_sm = bn <= 2 * kSmallTwoNc ? kMaxPerSm : 1;
         const double tiles = tiles_of(bn, (f.N + 127) / 128);
         if (tiles > 1e6) continue;  // pair tiles
         for (int split = 1; split <= kMaxSplit && split <= chunks; ++split) {
